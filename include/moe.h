@@ -54,7 +54,8 @@ typedef enum {
     MOE_ERR_WORKSPACE = 4,     /* ws_bytes < moe_workspace_size(cfg) */
     MOE_ERR_NONFINITE = 5,     /* device: a score was NaN */
     MOE_ERR_TIMEOUT = 6,       /* device: a bounded wait ran out */
-    MOE_ERR_CUDA = 7           /* a CUDA runtime call failed */
+    MOE_ERR_CUDA = 7,          /* a CUDA runtime call failed */
+    MOE_ERR_INDEX = 8          /* device: a page, sequence, length or token index is out of range */
 } moe_status_t;
 
 /* moe_config_t.flags: size the workspace for the FP8 entry points too (adds
@@ -460,6 +461,155 @@ moe_status_t moe_dispatch_static(const moe_config_t* cfg, const float* scores_de
                                  int32_t* counts_dev, int32_t* offsets_dev, int32_t* perm_dev,
                                  float* combine_w_dev, int32_t* n_rerouted_dev,
                                  int32_t* n_dropped_dev, int32_t* status_dev, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Around the layer in a decoding step: the paged key-value cache, attention of
+ * one new token per sequence over it, and the log probabilities read off the
+ * logits.  These calls use no moe_config_t and no workspace of the layer.
+ * Sequences, pages, positions and tokens are int32; strides count elements.
+ * Indices that a kernel reads on the device (page table entries, sequence
+ * numbers, lengths, tokens) are checked there: one out of range records
+ * MOE_ERR_INDEX in the status word and the access is skipped.
+ * ------------------------------------------------------------------------ */
+
+/* moe_kv_cache_t.type */
+#define MOE_KV_BF16 0u
+#define MOE_KV_E4M3 1u  /* e4m3 codes; one exponent byte per (token, head) row of k and of v */
+
+/* A paged key-value cache: stores k and v, [n_pages, page_size, n_kv_heads,
+ * head_dim] by shape, with any strides (the same for k and v) whose last one is
+ * 1: token-major and head-major pages are both fine.  head_dim is 64, 128 or 256.
+ * k and v are 16-byte aligned and their strides multiples of 16 bytes.
+ * MOE_KV_E4M3: a row's values are e4m3(code) * 2^(byte - 127); the exponent bytes
+ * k_exp, v_exp are [n_pages, page_size, n_kv_heads] by shape with strides of their
+ * own.  A power of two leaves every stored value exact in bf16 and costs no
+ * precision against an fp32 scale (the codes are floating point themselves). */
+typedef struct {
+    void* k;
+    void* v;
+    void* k_exp;          /* NULL for MOE_KV_BF16 */
+    void* v_exp;
+    uint32_t type;        /* MOE_KV_* */
+    int32_t n_pages;
+    int32_t page_size;    /* tokens per page, at least 1 (no power of two needed) */
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int64_t page_stride, token_stride, head_stride;
+    int64_t exp_page_stride, exp_token_stride, exp_head_stride;
+} moe_kv_cache_t;
+
+/* moe_append_t.flags: rotated pairs are (2i, 2i + 1) instead of (i, i + rot_dim/2). */
+#define MOE_ROTATE_INTERLEAVED 1u
+
+/* New tokens for moe_kv_append.  q, k and v may be views of one projection's
+ * output: strides are multiples of 8 elements, pointers 16-byte aligned, the
+ * head_dim values of one head contiguous. */
+typedef struct {
+    int32_t T;                   /* tokens */
+    int32_t n_seqs, max_pages;   /* page table [n_seqs, max_pages], rows table_stride apart */
+    int32_t n_heads;             /* query heads (0, with q = NULL: append only) */
+    int32_t rot_dim;             /* leading dimensions rotated: a multiple of 16 up to head_dim, 0 = none */
+    uint32_t flags;              /* MOE_ROTATE_INTERLEAVED or 0 */
+    const int32_t* pos;          /* [T] position in the sequence; < 0: a padding token */
+    const int32_t* seq;          /* [T] page table row of each token, or NULL: token t is row t */
+    const int32_t* page_table;   /* entry j of a row: the page of positions j*page_size ... */
+    int64_t table_stride;
+    const uint64_t* phase;       /* [rot_dim / 2] from moe_rope_phase (NULL when rot_dim = 0) */
+    const void* q;               /* [T, n_heads, head_dim] bf16 */
+    const void* k;               /* [T, n_kv_heads, head_dim] bf16 */
+    const void* v;
+    void* q_out;                 /* [T, n_heads, head_dim] bf16: the rotated q; may be q itself */
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    int64_t q_out_token_stride, q_out_head_stride;
+} moe_append_t;
+
+/* Rotation frequencies for moe_kv_append (host call, host arrays): inv_freq[i] in
+ * radians per position, any finite values (scaled variants of the frequencies need
+ * nothing else); phase[i] is the same in units of 2^-64 turns.  The kernel's angle
+ * is the low 64 bits of pos * phase[i]: exact modulo a turn, so far positions are
+ * as accurate as near ones. */
+moe_status_t moe_rope_phase(int32_t n, const double* inv_freq, uint64_t* phase);
+
+/* Rotates q and k by their positions and writes k and v into the cache, one
+ * launch.  For pair (a, b) of a row at position p with angle th = p * inv_freq[i]:
+ * (a cos th - b sin th, a sin th + b cos th) in fp32, rounded once, to bf16 (q_out,
+ * MOE_KV_BF16) or to the row's e4m3 code (MOE_KV_E4M3: the smallest exponent with
+ * max|x| <= 448 * 2^e, at least -126; 0 for an all-zero row; a value that is not
+ * finite is stored as NaN and does not count in the maximum).  A padding token
+ * (pos < 0) writes nothing to the cache and zeros to q_out.  Two tokens at one
+ * position of one sequence race.  status_dev: NULL, or the int32 status word. */
+moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const moe_append_t* a, int32_t* status_dev,
+                           void* stream);
+
+/* One new token per sequence for moe_paged_attention. */
+typedef struct {
+    int32_t B;                   /* sequences */
+    int32_t n_heads;             /* query heads, a multiple of n_kv_heads: head h reads key head
+                                    h / (n_heads / n_kv_heads) */
+    int32_t max_pages;           /* page table [B, max_pages], rows table_stride apart */
+    int32_t window;              /* > 0: only the last `window` cached tokens; 0: all */
+    float scale;                 /* of the scores, finite */
+    const int32_t* seq_len;      /* [B] cached tokens (the new one included); 0: an empty row */
+    const int32_t* page_table;
+    int64_t table_stride;
+    const void* q;               /* [B, n_heads, head_dim] bf16 */
+    void* out;                   /* [B, n_heads, head_dim] bf16 */
+    float* lse;                  /* [B, n_heads] fp32 or NULL */
+    int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+} moe_attention_t;
+
+/* Bytes of the workspace for moe_paged_attention at this head_dim (any batch,
+ * lengths and heads; 0 for an unsupported head_dim), and its set-up, enqueued on
+ * `stream` once after allocating it (256-byte aligned).  The first word is a status
+ * word for moe_get_device_status.  Calls that share a workspace must not overlap. */
+size_t moe_paged_attention_workspace_size(int32_t head_dim);
+moe_status_t moe_paged_attention_workspace_init(void* ws_dev, size_t ws_bytes, void* stream);
+
+/* Attention of one new token per sequence over the cache:
+ *   s_j = scale * q . k_j over the live positions j (max(0, seq_len - window) <= j <
+ *   seq_len), out = sum_j softmax(s)_j v_j, lse = ln sum_j e^(s_j)
+ * with fp32 scores, statistics and sums.  A row with no live position, or no score above
+ * -inf, gets zeros and lse = -inf.  What the cache holds in other places (NaN included) has no effect.
+ * Lengths are read on the device: a captured graph replays at other lengths.  A
+ * length outside [0, max_pages * page_size] is brought to its nearer end, and keys
+ * of a page outside [0, n_pages) are left out; both record MOE_ERR_INDEX. */
+moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_attention_t* a, void* ws_dev,
+                                 size_t ws_bytes, void* stream);
+
+/* moe_token_logprobs type */
+#define MOE_LOGITS_F32 0u
+#define MOE_LOGITS_BF16 1u
+#define MOE_MAX_TOP 32
+
+/* Log probabilities read off logits [rows, vocab] (rows row_stride elements apart,
+ * any alignment of the type; 0 repeats one row), each row read once:
+ *   lse = ln sum_i e^(x_i), logprob = x[token] - lse, entropy = lse - sum_i p_i x_i
+ *   (the last two taken from the row's maximum, so that a large lse costs them nothing),
+ *   top_ids, top_logprobs [rows, n_top]: the n_top largest x, ties to the lowest index
+ * all in fp32.  token_dev [rows]: < 0 means none (logprob 0); >= vocab records
+ * MOE_ERR_INDEX and counts as none.  n_top <= MOE_MAX_TOP; past vocab entries are id -1,
+ * -inf.  A masked logit (-inf, or the type's lowest value) has probability 0, and
+ * logprob -inf where it is -inf; a row of -inf alone has lse -inf, entropy 0.  NaN or
+ * +inf makes the row's lse, logprob and entropy NaN, records MOE_ERR_NONFINITE for NaN,
+ * and NaN ranks last.  Each output may be NULL (token_dev with logprob_dev; top_*
+ * with n_top = 0).  status_dev: NULL, or the int32 status word. */
+moe_status_t moe_token_logprobs(int64_t rows, int32_t vocab, uint32_t type, const void* logits_dev,
+                                int64_t row_stride, const int32_t* token_dev, int32_t n_top,
+                                float* logprob_dev, float* entropy_dev, float* lse_dev,
+                                int32_t* top_ids_dev, float* top_logprobs_dev, int32_t* status_dev,
+                                void* stream);
+
+/* Gradient of logprob and entropy with respect to the logits, from the forward's
+ * lse and entropy:  dx_i = g (1[i = token] - p_i) - h p_i (ln p_i + entropy),
+ * g = dlogprob (0 for a row without a token), h = dentropy; either may be NULL (0).
+ * dlogits_dev [rows, vocab] of the logits' type, rows drow_stride apart; it may be the
+ * logits themselves. */
+moe_status_t moe_token_logprobs_backward(int64_t rows, int32_t vocab, uint32_t type,
+                                         const void* logits_dev, int64_t row_stride,
+                                         const int32_t* token_dev, const float* lse_dev,
+                                         const float* entropy_dev, const float* dlogprob_dev,
+                                         const float* dentropy_dev, void* dlogits_dev,
+                                         int64_t drow_stride, int32_t* status_dev, void* stream);
 
 #ifdef __cplusplus
 }

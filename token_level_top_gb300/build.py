@@ -21,7 +21,7 @@ OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libmoe.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "moe.h")
 UNITS = ["api.cu", "route.cu", "dispatch.cu", "gemm.cu", "bwd_gemm.cu", "nvfp4.cu", "misc.cu", "router.cu",
-         "backward.cu", "noalloc.cu"]
+         "backward.cu", "noalloc.cu", "kv_append.cu", "attention.cu", "logprobs.cu", "decode_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills"]

@@ -680,6 +680,7 @@ const char* moe_status_string(moe_status_t st)
         case MOE_ERR_NONFINITE: return "non-finite (NaN) score";
         case MOE_ERR_TIMEOUT: return "bounded device wait timed out";
         case MOE_ERR_CUDA: return "CUDA runtime error";
+        case MOE_ERR_INDEX: return "index out of range";
     }
     return "unknown status";
 }

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -267,6 +268,79 @@ size_t backward_bytes(long long T, int d, int E, int k, int F, long long R);
 // R for backward_bytes: at most sum over experts of (kept rows rounded up to 128).
 long long backward_block_rows(long long T, int E, int k, long long C);
 cudaError_t run_backward(const BackwardArgs& a, cudaStream_t s);
+
+// The paged cache (kv_append.cu, attention.cu).  Strides count elements.
+struct AppendArgs {
+    int T, n_seqs, max_pages, n_heads, n_kv_heads, rot_dim, n_pages, page_size;
+    bool interleaved;
+    const int32_t* pos;
+    const int32_t* seq;          // or NULL: token t is row t of the table
+    const int32_t* page_table;
+    long long table_stride;
+    const uint64_t* phase;       // [rot_dim / 2], 2^-64 turns per position
+    const __nv_bfloat16 *q, *k, *v;
+    __nv_bfloat16* q_out;
+    long long q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    long long q_out_token_stride, q_out_head_stride;
+    void *cache_k, *cache_v;
+    uint8_t *k_exp, *v_exp;      // e4m3 cache only
+    long long page_stride, token_stride, head_stride;
+    long long exp_page_stride, exp_token_stride, exp_head_stride;
+    int* status;
+    int parts;                   // warps per token (set by the launcher)
+};
+cudaError_t launch_kv_append(AppendArgs a, int head_dim, bool e4m3, cudaStream_t s);
+
+struct AttentionArgs {
+    int B, n_heads, n_kv_heads, max_pages, window, n_pages, page_size;
+    float scale;
+    const int32_t* seq_len;
+    const int32_t* page_table;
+    long long table_stride;
+    const __nv_bfloat16* q;
+    __nv_bfloat16* out;
+    float* lse;                  // or NULL
+    long long q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+    const void *k, *v;
+    const uint8_t *k_exp, *v_exp;   // e4m3 cache only
+    long long page_stride, token_stride, head_stride;
+    long long exp_page_stride, exp_token_stride, exp_head_stride;
+    void* ws;
+    int* status;
+};
+// The attention workspace starts with the status word and the counters of the join.
+constexpr size_t kAttentionCtrlBytes = 256;
+size_t paged_attention_ws_bytes(int head_dim);   // 0: unsupported head_dim
+cudaError_t launch_paged_attention(const AttentionArgs& a, int head_dim, bool e4m3, cudaStream_t s);
+
+// Log probabilities read off logits (logprobs.cu).
+struct LogprobArgs {
+    long long rows;
+    int vocab;
+    bool bf16;
+    const void* logits;
+    long long row_stride;
+    const int32_t* token;    // or NULL
+    int n_top;
+    float *logprob, *entropy, *lse;   // each or NULL
+    int32_t* top_ids;        // or NULL
+    float* top_logprobs;
+    int* status;
+};
+cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t s);
+struct LogprobGradArgs {
+    long long rows;
+    int vocab;
+    bool bf16;
+    const void* logits;
+    long long row_stride;
+    const int32_t* token;    // or NULL
+    const float *lse, *entropy, *dlogprob, *dentropy;
+    void* dlogits;
+    long long drow_stride;
+    int* status;
+};
+cudaError_t launch_token_logprobs_backward(const LogprobGradArgs& a, cudaStream_t s);
 
 cudaError_t launch_timeout_probe(int* status, long long budget, cudaStream_t s);
 

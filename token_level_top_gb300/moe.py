@@ -22,7 +22,7 @@ STAGE_NAMES = ["route", "dispatch", "prep", "gate_up", "down", "combine"]
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "misaligned pointer",
           4: "workspace too small", 5: "non-finite (NaN) score", 6: "bounded device wait timed out",
-          7: "CUDA runtime error"}
+          7: "CUDA runtime error", 8: "index out of range"}
 
 
 class MoEError(RuntimeError):
@@ -42,6 +42,31 @@ class MoEConfig(ctypes.Structure):
 class MoERouter(ctypes.Structure):
     _fields_ = [("w", ctypes.c_void_p), ("w2", ctypes.c_void_p), ("bias", ctypes.c_void_p),
                 ("norm_gamma", ctypes.c_void_p), ("norm_beta", ctypes.c_void_p)]
+
+
+class MoEKVCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("type", ctypes.c_uint32), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)] + [
+                    (n, ctypes.c_int64) for n in ("page_stride", "token_stride", "head_stride", "exp_page_stride",
+                                                  "exp_token_stride", "exp_head_stride")]
+
+
+class MoEAppend(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("pos", ctypes.c_void_p), ("seq", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64)] + [
+                    (n, ctypes.c_void_p) for n in ("phase", "q", "k", "v", "q_out")] + [
+                    (n + s, ctypes.c_int64) for n in ("q", "k", "v", "q_out") for s in ("_token_stride", "_head_stride")]
+
+
+class MoEAttention(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("seq_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("q", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p)] + [
+                    (n + s, ctypes.c_int64) for n in ("q", "out") for s in ("_token_stride", "_head_stride")]
 
 
 @dataclass
@@ -99,7 +124,9 @@ _lib = None
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
 SZ = ctypes.c_size_t
+I64 = ctypes.c_int64
 CFG = ctypes.POINTER(MoEConfig)
+KVC = ctypes.POINTER(MoEKVCache)
 RTR = ctypes.POINTER(MoERouter)
 
 _SIGS = {
@@ -129,6 +156,13 @@ _SIGS = {
     "moe_router_logits": (I32, [CFG, P, RTR, P, P, SZ, P]),
     "moe_layer_backward": (I32, [CFG] + [P] * 12 + [SZ, P]),
     "moe_layer_forward_router": (I32, [CFG, P, RTR] + [P] * 15 + [SZ, P]),
+    "moe_rope_phase": (I32, [I32, P, P]),
+    "moe_kv_append": (I32, [KVC, ctypes.POINTER(MoEAppend), P, P]),
+    "moe_paged_attention_workspace_size": (SZ, [I32]),
+    "moe_paged_attention_workspace_init": (I32, [P, SZ, P]),
+    "moe_paged_attention": (I32, [KVC, ctypes.POINTER(MoEAttention), P, SZ, P]),
+    "moe_token_logprobs": (I32, [I64, I32, ctypes.c_uint32, P, I64, P, I32] + [P] * 7),
+    "moe_token_logprobs_backward": (I32, [I64, I32, ctypes.c_uint32, P, I64] + [P] * 6 + [I64, P, P]),
 }
 
 
@@ -454,4 +488,207 @@ def dispatch_static(cfg: Config, scores, device="cuda"):
                                    _p(out["perm"]), _p(out["cw"]), _p(out["n_rerouted"]),
                                    _p(out["n_dropped"]), _p(out["status"]), _stream())
     _check(st, "moe_dispatch_static")
+    return out
+
+
+# ------------------------------------------------------------ around the layer in a decoding step
+
+KV_BF16, KV_E4M3 = 0, 1            # MOE_KV_*
+LOGITS = {torch.float32: 0, torch.bfloat16: 1}   # MOE_LOGITS_*
+ROTATE_INTERLEAVED = 1             # MOE_ROTATE_INTERLEAVED
+
+
+def _want(t: torch.Tensor, name: str, dtype, ndim: int):
+    """Raises ValueError unless t is a CUDA tensor of this type and rank whose last dimension is contiguous."""
+    if t.dtype is not dtype or t.dim() != ndim or not t.is_cuda or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{name}: want a CUDA tensor of {ndim} dimensions, {dtype}, last one contiguous; "
+                         f"got {tuple(t.shape)} {t.dtype}, strides {t.stride()}, {t.device}")
+
+
+def _rows(t: torch.Tensor, name: str, n: int):
+    """_want for an int32 or fp32 array of n values (int32 unless the name says otherwise)."""
+    _want(t, name, torch.float32 if name in ("lse", "entropy", "dlogprob", "dentropy") else torch.int32, 1)
+    if t.shape[0] != n:
+        raise ValueError(f"{name}: want {n} values, got {t.shape[0]}")
+
+
+def _strides(t: torch.Tensor):
+    """t's strides, 0 for a dimension of one element (torch leaves those arbitrary)."""
+    return [st if n > 1 else 0 for st, n in zip(t.stride(), t.shape)]
+
+
+def status_word(device="cuda") -> torch.Tensor:
+    """A cleared status word for the calls that take one (read it with device_status / check_device)."""
+    return torch.zeros(64, dtype=torch.int32, device=device)
+
+
+class KVCache:
+    """A paged key-value cache (moe_kv_cache_t).  k, v: [n_pages, page_size, n_kv_heads, head_dim] by shape,
+    bf16, or uint8 e4m3 codes with the exponent bytes k_exp, v_exp [n_pages, page_size, n_kv_heads]; any
+    strides (k and v alike) whose last one is 1."""
+
+    def __init__(self, k, v, k_exp=None, v_exp=None):
+        e4m3 = k_exp is not None
+        for t, name in ((k, "k"), (v, "v")):
+            _want(t, name, torch.uint8 if e4m3 else torch.bfloat16, 4)
+        if k.shape != v.shape or _strides(k) != _strides(v) or e4m3 != (v_exp is not None):
+            raise ValueError("k and v (and k_exp and v_exp) must have the same shape and strides")
+        exp = (0, 0, 0)
+        if e4m3:
+            for t in (k_exp, v_exp):
+                if t.dtype is not torch.uint8 or t.shape != k.shape[:3] or not t.is_cuda:
+                    raise ValueError("k_exp, v_exp: want uint8 CUDA tensors [n_pages, page_size, n_kv_heads]")
+            if _strides(k_exp) != _strides(v_exp):
+                raise ValueError("k_exp and v_exp must have the same strides")
+            exp = _strides(k_exp)
+        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        n, page, heads, dim = k.shape
+        self.c = MoEKVCache(k.data_ptr(), v.data_ptr(), k_exp.data_ptr() if e4m3 else None,
+                            v_exp.data_ptr() if e4m3 else None, KV_E4M3 if e4m3 else KV_BF16, n, page, heads, dim,
+                            *_strides(k)[:3], *exp)
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, e4m3=False, device="cuda"):
+        """A zeroed cache whose pages keep each head's rows together (the faster order to read)."""
+        def store(*tail, dtype, fill):
+            return torch.full((n_pages, n_kv_heads, page_size, *tail), fill, dtype=dtype, device=device).transpose(1, 2)
+        if not e4m3:
+            return cls(*[store(head_dim, dtype=torch.bfloat16, fill=0) for _ in range(2)])
+        return cls(*[store(head_dim, dtype=torch.uint8, fill=0) for _ in range(2)],
+                   *[store(dtype=torch.uint8, fill=127) for _ in range(2)])
+
+
+def rope_phase(inv_freq) -> torch.Tensor:
+    """moe_rope_phase: rotation frequencies in radians per position (fp64, host) to int64 phases for kv_append
+    (host; move them to the device once)."""
+    f = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").contiguous()
+    out = torch.empty(f.numel(), dtype=torch.int64)
+    _check(lib().moe_rope_phase(f.numel(), _p(f), _p(out)), "moe_rope_phase")
+    return out
+
+
+def kv_append(cache: KVCache, k, v, pos, page_table, q=None, phase=None, seq=None, interleaved=False, q_out=None,
+              status=None):
+    """Rotates q and k by their positions and writes k, v into the cache (moe_kv_append).  k, v [T, n_kv_heads,
+    head_dim] and q [T, n_heads, head_dim] bf16 (views of one projection's output are fine); pos [T], seq [T]
+    (None: token t belongs to row t of page_table [n_seqs, max_pages]) int32; phase from rope_phase on the device
+    (None: no rotation).  Returns the rotated q (q_out when given, which may be q), or None without q.  status: a
+    status_word or workspace that records indices out of range."""
+    _want(k, "k", torch.bfloat16, 3)
+    _want(v, "v", torch.bfloat16, 3)
+    _want(page_table, "page_table", torch.int32, 2)
+    T, c = k.shape[0], cache.c
+    _rows(pos, "pos", T)
+    if seq is not None:
+        _rows(seq, "seq", T)
+    if k.shape[1:] != (c.n_kv_heads, c.head_dim) or v.shape != k.shape:
+        raise ValueError(f"k, v: want [T, {c.n_kv_heads}, {c.head_dim}], got {tuple(k.shape)}, {tuple(v.shape)}")
+    heads, qp, qs, op, os_ = 0, None, (0, 0), None, (0, 0)
+    if q is not None:
+        _want(q, "q", torch.bfloat16, 3)
+        if q.shape[0] != T or q.shape[2] != c.head_dim:
+            raise ValueError(f"q: want [{T}, n_heads, {c.head_dim}], got {tuple(q.shape)}")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        else:
+            _want(q_out, "q_out", torch.bfloat16, 3)
+            if q_out.shape != q.shape:
+                raise ValueError(f"q_out: want {tuple(q.shape)}, got {tuple(q_out.shape)}")
+        heads, qp, qs, op, os_ = q.shape[1], q.data_ptr(), _strides(q), q_out.data_ptr(), _strides(q_out)
+    ks, vs = _strides(k), _strides(v)
+    rot, pp = 0, None
+    if phase is not None:
+        _want(phase, "phase", torch.int64, 1)
+        rot, pp = 2 * phase.shape[0], phase.data_ptr()
+    a = MoEAppend(T, page_table.shape[0], page_table.shape[1], heads, rot, ROTATE_INTERLEAVED if interleaved else 0,
+                  pos.data_ptr(), None if seq is None else seq.data_ptr(), page_table.data_ptr(), _strides(page_table)[0],
+                  pp, qp, k.data_ptr(), v.data_ptr(), op, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1])
+    _check(lib().moe_kv_append(ctypes.byref(c), ctypes.byref(a), _p(status), _stream()), "moe_kv_append")
+    return q_out if q is not None else None
+
+
+def attention_workspace(head_dim: int, device="cuda") -> torch.Tensor:
+    """A workspace for paged_attention at this head_dim (any batch), initialised."""
+    n = int(lib().moe_paged_attention_workspace_size(head_dim))
+    if n == 0:
+        raise MoEError(2, "moe_paged_attention_workspace_size")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    _check(lib().moe_paged_attention_workspace_init(_p(ws), n, _stream()), "moe_paged_attention_workspace_init")
+    return ws
+
+
+def paged_attention(cache: KVCache, ws, q, seq_len, page_table, scale=None, window=0, out=None, return_lse=False):
+    """Attention of one new token per sequence over the cache (moe_paged_attention): q [B, n_heads, head_dim] bf16,
+    seq_len [B] and page_table [B, max_pages] int32, scale (None: head_dim ** -0.5), window (0: all cached tokens).
+    Returns out [B, n_heads, head_dim] bf16, and lse [B, n_heads] fp32 with return_lse."""
+    _want(q, "q", torch.bfloat16, 3)
+    _want(page_table, "page_table", torch.int32, 2)
+    B, heads, dim = q.shape
+    c = cache.c
+    _rows(seq_len, "seq_len", B)
+    if dim != c.head_dim or page_table.shape[0] != B:
+        raise ValueError(f"q, page_table: want [B, n_heads, {c.head_dim}] and [B, max_pages], got {tuple(q.shape)}, "
+                         f"{tuple(page_table.shape)}")
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    else:
+        _want(out, "out", torch.bfloat16, 3)
+        if out.shape != q.shape:
+            raise ValueError(f"out: want {tuple(q.shape)}, got {tuple(out.shape)}")
+    lse = torch.empty(B, heads, dtype=torch.float32, device=q.device) if return_lse else None
+    qs, os_ = _strides(q), _strides(out)
+    if not 0 <= window < 2 ** 31:
+        raise ValueError(f"window: want 0 .. 2^31 - 1, got {window}")
+    a = MoEAttention(B, heads, page_table.shape[1], window, dim ** -0.5 if scale is None else scale, seq_len.data_ptr(),
+                     page_table.data_ptr(), _strides(page_table)[0], q.data_ptr(), out.data_ptr(),
+                     lse.data_ptr() if return_lse else None, qs[0], qs[1], os_[0], os_[1])
+    _check(lib().moe_paged_attention(ctypes.byref(c), ctypes.byref(a), _p(ws), ws.numel() * ws.element_size(), _stream()),
+           "moe_paged_attention")
+    return (out, lse) if return_lse else out
+
+
+def token_logprobs(logits, token=None, top=0, status=None):
+    """Log probabilities read off logits [rows, vocab] (fp32 or bf16, moe_token_logprobs): dict(lse, entropy [rows],
+    with token [rows] int32 (negative: none) logprob [rows], with top > 0 top_ids int32 and top_logprobs
+    [rows, top])."""
+    if logits.dtype not in LOGITS:
+        raise ValueError(f"logits: want float32 or bfloat16, got {logits.dtype}")
+    _want(logits, "logits", logits.dtype, 2)
+    n, v = logits.shape
+    dev = logits.device
+    out = dict(lse=torch.empty(n, dtype=torch.float32, device=dev), entropy=torch.empty(n, dtype=torch.float32, device=dev))
+    if token is not None:
+        _rows(token, "token", n)
+        out["logprob"] = torch.empty(n, dtype=torch.float32, device=dev)
+    if top > 0:
+        out["top_ids"] = torch.empty(n, top, dtype=torch.int32, device=dev)
+        out["top_logprobs"] = torch.empty(n, top, dtype=torch.float32, device=dev)
+    g = out.get
+    st = lib().moe_token_logprobs(n, v, LOGITS[logits.dtype], _p(logits), _strides(logits)[0], _p(token), top,
+                                  _p(g("logprob")), _p(out["entropy"]), _p(out["lse"]), _p(g("top_ids")),
+                                  _p(g("top_logprobs")), _p(status), _stream())
+    _check(st, "moe_token_logprobs")
+    return out
+
+
+def token_logprobs_backward(logits, token, lse, entropy=None, dlogprob=None, dentropy=None, out=None, status=None):
+    """Gradient of token_logprobs' logprob and entropy with respect to the logits (moe_token_logprobs_backward), from
+    its lse and entropy.  Returns dlogits [rows, vocab] of the logits' type (out when given, which may be logits)."""
+    if logits.dtype not in LOGITS:
+        raise ValueError(f"logits: want float32 or bfloat16, got {logits.dtype}")
+    _want(logits, "logits", logits.dtype, 2)
+    n, v = logits.shape
+    for t, name in ((token, "token"), (lse, "lse"), (entropy, "entropy"), (dlogprob, "dlogprob"), (dentropy, "dentropy")):
+        if t is not None:
+            _rows(t, name, n)
+    if out is None:
+        out = torch.empty(n, v, dtype=logits.dtype, device=logits.device)
+    else:
+        _want(out, "out", logits.dtype, 2)
+        if out.shape != logits.shape:
+            raise ValueError(f"out: want {tuple(logits.shape)}, got {tuple(out.shape)}")
+    st = lib().moe_token_logprobs_backward(n, v, LOGITS[logits.dtype], _p(logits), _strides(logits)[0], _p(token), _p(lse),
+                                           _p(entropy), _p(dlogprob), _p(dentropy), _p(out), _strides(out)[0], _p(status),
+                                           _stream())
+    _check(st, "moe_token_logprobs_backward")
     return out
