@@ -31,7 +31,8 @@ BAD_CACHES = [(dict(k=None), 1), (dict(v=None), 1), (dict(type=2), 1), (dict(n_p
               (dict(n_kv_heads=0), 1), (dict(type=1), 1), (dict(k_exp=FAKE), 1), (dict(type=1, k_exp=FAKE), 1),
               (dict(head_dim=96), 2), (dict(n_kv_heads=5000), 2), (dict(k=FAKE + 8), 3), (dict(v=FAKE + 2), 3),
               (dict(token_stride=132), 3), (dict(page_stride=4), 3), (dict(head_stride=2049), 3),
-              (dict(type=1, k_exp=FAKE, v_exp=FAKE, token_stride=136), 3)]
+              (dict(type=1, k_exp=FAKE, v_exp=FAKE, token_stride=136), 3),
+              (dict(type=1, k_exp=FAKE + 2, v_exp=FAKE), 3)]
 
 
 def _append(**kw):
