@@ -13,34 +13,41 @@
 // unnormalised output) go to the workspace and the block that finishes last
 // joins them, always in the same order.
 //
-// A warp's tile is 16 keys.  Every lane copies exactly the 16-byte pieces that
-// it will feed to the matrix instructions (cp.async into its own place of a
-// ring in shared memory), so the ring needs no barrier and no bank is hit
-// twice, and some 100 to 190 KB per SM are in flight whatever the arithmetic does.
-//   scores: C[head][key] = Q K^T, m16n8k16.  The inner dimension may be taken in
-//   any order if both sides agree: a lane's 16 bytes of a key row are its B
-//   fragments of consecutive steps, and the same 16 bytes of Q its A fragments.
-//   values: C[head][d] += P V.  The C layout of the scores is the A layout of
-//   the weights; a lane holds pieces of four keys' rows, which byte permutes
-//   pair up into B fragments.
+// A warp's tile is 16 keys, copied (cp.async) into the warp's own ring of key
+// and value tiles in shared memory, which needs no barrier of the block.  All
+// products are m16n8k16 with the cache as the 16-row side; the fragments are
+// 16-byte pieces of its rows when the free orders are chosen to fit:
+//   scores: C[key][head] = K Q^T.  The inner dimension may come in any order if
+//   both sides agree: a lane's 16 bytes of a key row are its A fragments of
+//   consecutive steps, and the same 16 bytes of a row of Q its B fragments.
+//   values: C[d][head] += V^T P.  A lane holds pieces of four keys' rows, which
+//   byte permutes pair up over the keys; the order of d is free.  The weights
+//   get from the layout of C to that of B by a matrix transpose across the warp.
 // The weights go in as the sum of two 16-bit parts (their own rounding would
-// cost more than the output's): with at most 8 query heads the low parts use
-// the other 8 rows of the same instruction.
+// cost more than the output's); with at most 4 query heads the columns 4..7
+// carry the low parts, so both take one product.
+//
+// The running maximum is raised only when a score passes it by 2^kSlack: the
+// weights stay below 2^kSlack, sums are fp32, and the usual tile needs neither
+// an exchange between lanes nor a pass over the output registers.
 //
 // e4m3 rows become f16 in one conversion per two codes (exact), so that path
 // multiplies in f16: Q is scaled by a power of two per head, and the value rows'
 // exponents enter as 2^(s + e) in the weights, whose running maximum is taken
 // over s + e; the sum of the softmax uses 2^s against the same maximum.
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
 namespace moe {
 namespace {
 
-constexpr int kAttentionCtas = 152;   // most blocks of a launch (one per SM)
+constexpr int kAttentionCtas = 4 * 152;   // most blocks of a launch
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// e4m3 path: weights are held times 2^14, so that f16 keeps those 2^-38 of the largest
-constexpr float kShift = 14.0f;
+constexpr float kSlack = 8.0f;
+// e4m3 path: weights are held times 2^6 (at most 2^14), so that f16 keeps those 2^-30 of the maximum's
+constexpr float kShift = 6.0f;
 
 __device__ __forceinline__ float exp2_fast(float x)
 {
@@ -64,15 +71,10 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Copies N bytes, or writes N zeros when !live (src is then not read).
-template <int N>
+// Copies 16 bytes, or writes 16 zeros when !live (src is then not read).
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool live)
 {
-    const int n = live ? N : 0;
-    if (N == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
 // The first n bytes of the 4 at src (4-byte aligned), zeros behind them.
@@ -122,6 +124,14 @@ __device__ __forceinline__ float pow2_of_byte(uint32_t b)
     return __uint_as_float(b ? b << 23 : 0x00400000u);
 }
 
+// Transposes an 8 x 8 matrix of 16-bit values held as one pair (row lane / 4, columns 2 (lane % 4) ..) per lane.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 // (a, b) as the sum of two pairs of 16-bit values.
 template <bool kF16>
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo)
@@ -137,69 +147,88 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint3
     }
 }
 
-template <int D, bool kE4m3>
+template <int D, bool kE4m3, int kHeads>
 struct Shape {
     static constexpr int kRow = D * (kE4m3 ? 1 : 2);          // bytes of a row
-    static constexpr int kWarps = D == 256 ? 4 : 8;          // at D = 256 a warp needs 255 registers
+    static constexpr int kCols = kHeads <= 8 ? 1 : 2;         // column tiles of 8
+    static constexpr int kOut = D / 16 * 4 * kCols;           // output registers
+    static constexpr int kWarps = 4;
+    // blocks per SM, as the registers of outputs and queries allow: 128, 168 or 255 a thread
+    static constexpr int kCtas = kOut + D / 8 * kCols <= 24 ? 4 : (kOut + D / 8 * kCols <= 48 ? 3 : 2);
     static constexpr int kTile = 16 * kRow;                   // bytes of a warp's key (or value) tile
     static constexpr int kGranule = 16 * kWarps;              // keys
-    static constexpr int kMerge = kWarps * 8 * D * 4;         // the block's join of 8 heads
+    static constexpr int kMerge = kWarps * 4 * D * 4;         // the block's join of 4 heads
     // beside a tile: which of its keys are live, and e4m3 32 exponent words and where their bytes are
-    static constexpr int kMeta = kE4m3 ? 192 : 16, kMask = kE4m3 ? 128 : 0, kByte = 132;
-    // as many stages as 227 KB hold beside the join, at most 8
-    static constexpr int kFit = (232448 - 512 - kMerge - kWarps * 128) / (kWarps * (2 * kTile + kMeta));
-    static constexpr int kStages = kFit < 8 ? kFit : 8;
-    static constexpr int kRing = kWarps * kStages * 2 * kTile;
-    static constexpr int kSmem = kRing + kMerge + kWarps * (kStages * kMeta + 128);
+    static constexpr int kMeta = kE4m3 ? 192 : 4, kMask = kE4m3 ? 128 : 0, kByte = 132;
+    // as many slots (key or value tiles) as the block's share of 228 KB holds beside the join, at most 16
+    static constexpr int kShare = 233472 / kCtas - 1024 - 256;
+    static constexpr int kRoom = kShare - kMerge - kWarps * 128;
+    static constexpr int kFit = (2 * kRoom / kWarps - 2 * kMeta) / (2 * kTile + kMeta);
+    static constexpr int kSlots = kFit < 16 ? kFit : 16;
+    static constexpr int kMetas = (kSlots + 3) / 2;           // tiles begun and not finished
+    static constexpr int kRing = kWarps * kSlots * kTile;
+    static constexpr int kSmem = kRing + kMerge + kWarps * (kMetas * kMeta + 128);
+    static_assert(kSlots >= 3 && kSmem <= kShare, "the ring");
+    static constexpr int kCopyRows = kRow >= 128 ? 4 : 2;     // rows that a lane copies from, 16 bytes of each
+    static constexpr int kCopySegs = kRow >= 128 ? kRow / 128 : 1;   // ... per 128-byte segment
     static constexpr int kKeySegs = kRow / 64;                // 16-byte pieces of a key row per lane
     static constexpr int kValBytes = kRow / 8 < 16 ? kRow / 8 : 16;
     static constexpr int kValSegs = kRow / (8 * kValBytes);
     static constexpr int kValElts = kValBytes / (kE4m3 ? 1 : 2);
     static constexpr int kSteps = kE4m3 ? 4 : 2;              // inner steps per 16-byte piece
-    static constexpr int kQ = D / 8;                          // A registers of one half of the heads
-    static constexpr int kTiles = D / 8;                      // output column tiles
+    static constexpr int kQ = D / 8;                          // B registers of 8 heads
+    static constexpr int kTiles = D / 16;                     // output row tiles
 };
 
 // One item of the work list while it is walked granule by granule.
 struct Walk {
-    int b, h;            // sequence; key head * head blocks + head block
-    int len, first, n;   // its live keys [first, len) and its granules (per h)
+    int b, hk, block;    // sequence, key head, block of query heads
+    int len, first, n;   // its live keys [first, len) and its granules (per key head and block)
     int g;               // granule within the item
     long long off;       // the item's first granule in the whole list
+    // Tiles start at multiples of 16, so that with pages of 16 k tokens a tile lies in one page.
+    __device__ __forceinline__ int base() const { return first & ~15; }
 };
 
 __device__ __forceinline__ int clamped_len(const AttentionArgs& a, int b, bool record)
 {
-    const long long most = static_cast<long long>(a.max_pages) * a.page_size;
+    // (a tile's keys past the end still have to be int)
+    const long long most = min(static_cast<long long>(a.max_pages) * a.page_size, 0x7fff0000LL);
     const int n = a.seq_len[b];
     if (n >= 0 && n <= most) return n;
     if (record) record_error(a.status, MOE_ERR_INDEX);
     return n < 0 ? 0 : static_cast<int>(most);
 }
 
-__device__ __forceinline__ int live_keys(const AttentionArgs& a, int len)
+__device__ __forceinline__ int first_key(const AttentionArgs& a, int len)
 {
-    return a.window > 0 && len > a.window ? a.window : len;
+    return a.window > 0 && len > a.window ? len - a.window : 0;
+}
+
+template <int kGranule>
+__device__ __forceinline__ int granules_of(const AttentionArgs& a, int len)
+{
+    return static_cast<int>((static_cast<unsigned>(len - (first_key(a, len) & ~15)) + kGranule - 1) / kGranule);
 }
 
 template <int kGranule>
 __device__ __forceinline__ void load_item(const AttentionArgs& a, Walk& w)
 {
     w.len = clamped_len(a, w.b, false);
-    const int live = live_keys(a, w.len);
-    w.first = w.len - live;
-    w.n = (live + kGranule - 1) / kGranule;
+    w.first = first_key(a, w.len);
+    w.n = granules_of<kGranule>(a, w.len);
 }
 
-// The next granule; past the end of the batch the walk stays on its last item.
+// To the next item; past the end of the batch the walk stays behind its last one (n = 0).
 template <int kGranule>
-__device__ __forceinline__ void advance(const AttentionArgs& a, Walk& w, int heads)
+__device__ __forceinline__ void next_item(const AttentionArgs& a, Walk& w, int blocks)
 {
-    if (++w.g < w.n) return;
     w.off += w.n;
     w.g = 0;
-    if (++w.h < heads) return;
-    w.h = 0;
+    if (++w.block < blocks) return;
+    w.block = 0;
+    if (++w.hk < a.n_kv_heads) return;
+    w.hk = 0;
     do {
         if (++w.b >= a.B) {
             w.n = 0;
@@ -209,20 +238,18 @@ __device__ __forceinline__ void advance(const AttentionArgs& a, Walk& w, int hea
     } while (w.n == 0);
 }
 
-// The e4m3 and bf16 paths differ in how bytes become fragments and in the weights.
 template <int D, bool kE4m3, int kHeads>
-__global__ void __launch_bounds__(32 * Shape<D, kE4m3>::kWarps, 1) paged_attention_kernel(const AttentionArgs a)
+__global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D, kE4m3, kHeads>::kCtas) paged_attention_kernel(const AttentionArgs a)
 {
-    using S = Shape<D, kE4m3>;
-    constexpr int kWarps = S::kWarps, kThreads = 32 * kWarps, kStages = S::kStages;
-    constexpr int kHalves = kHeads / 8;
+    using S = Shape<D, kE4m3, kHeads>;
+    constexpr int kWarps = S::kWarps, kThreads = 32 * kWarps, kSlots = S::kSlots, kMetas = S::kMetas, kCols = S::kCols;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long s_scan[kWarps];
     __shared__ Walk s_start;
     __shared__ int s_last;
     float* const s_merge = reinterpret_cast<float*>(smem + S::kRing);
-    unsigned char* const s_meta = smem + S::kRing + S::kMerge;              // [warp][stage]
-    float2* const s_ml = reinterpret_cast<float2*>(s_meta + kWarps * kStages * S::kMeta);   // [warp][16]
+    unsigned char* const s_meta = smem + S::kRing + S::kMerge;              // [warp][tile]
+    float2* const s_ml = reinterpret_cast<float2*>(s_meta + kWarps * kMetas * S::kMeta);   // [warp][16]
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
@@ -235,7 +262,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3>::kWarps, 1) paged_attenti
     const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
     long long mine = 0;
     for (int b = b0; b < b1; ++b)
-        mine += (live_keys(a, clamped_len(a, b, blockIdx.x == 0)) + S::kGranule - 1) / S::kGranule;
+        mine += granules_of<S::kGranule>(a, clamped_len(a, b, blockIdx.x == 0));
     long long incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -245,7 +272,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3>::kWarps, 1) paged_attenti
     if (lane == 31) s_scan[warp] = incl;
     // sequences without live keys: zeros
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        if (live_keys(a, clamped_len(a, b, false)) > 0) continue;
+        if (clamped_len(a, b, false) > 0) continue;
         for (int i = threadIdx.x; i < a.n_heads * (D / 8); i += kThreads) {
             const int h = i / (D / 8), d = i % (D / 8);
             *reinterpret_cast<uint4*>(a.out + b * a.out_token_stride + h * a.out_head_stride + 8 * d) = make_uint4(0, 0, 0, 0);
@@ -273,105 +300,150 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3>::kWarps, 1) paged_attenti
             ++w.b;
             load_item<S::kGranule>(a, w);
         }
-        w.h = static_cast<int>((lo - w.off) / w.n);
-        w.off += static_cast<long long>(w.h) * w.n;
+        const int h = static_cast<int>((lo - w.off) / w.n);
+        w.hk = h / blocks;
+        w.block = h - w.hk * blocks;
+        w.off += static_cast<long long>(h) * w.n;
         w.g = static_cast<int>(lo - w.off);
         s_start = w;
     }
     __syncthreads();
 
-    const uint32_t ring = smem_u32(smem) + warp * kStages * 2 * S::kTile;
-    unsigned char* const meta = s_meta + warp * kStages * S::kMeta;
+    const uint32_t ring = smem_u32(smem) + warp * kSlots * S::kTile;
+    unsigned char* const meta = s_meta + warp * kMetas * S::kMeta;
     Walk iw = s_start, cw = s_start;
     const int count = static_cast<int>(hi - lo);
 
-    // ---- the copying side: key `lane & 15` of the tile belongs to this lane
-    int next_page = -1, next_at = 0;
-    bool next_live = false;
+    // ---- the copying side
+    constexpr int kElt = kE4m3 ? 1 : 2;
+    const long long token_bytes = a.token_stride * kElt;
+    // A copy instruction moves four 128-byte lines, eight lanes to a line.  A tile is stored by lines (a
+    // 128-byte segment of a row, or two 64-byte rows) whose 16-byte pieces are permuted by an XOR with f(row), so
+    // that the copies write whole lines and the fragment reads below hit every bank once: for the keys (8 lanes
+    // read 4 pieces of rows 2n, 2n + 1) f flips bit 2 with the row, for the values (2 pieces of rows 2n, 2n + 2,
+    // 2n + 4, 2n + 6) bits 1 and 2 with row / 2.
+    const int sub = lane >> 3, piece = lane & 7;
+    const char* const kb = static_cast<const char*>(a.k) + (S::kRow >= 128 ? piece : piece & 3) * 16;
+    const long long k_to_v = static_cast<const char*>(a.v) - static_cast<const char*>(a.k);
+    const int row0 = S::kRow >= 128 ? sub : 2 * sub + (piece >> 2);       // the lane's rows: row0, row0 + row_step, ..
+    constexpr int row_step = S::kRow >= 128 ? 4 : 8;
+    const long long lane_row = row0 * token_bytes;
+    const uint32_t to_k = sub * 128 + (S::kRow >= 128 ? piece ^ ((sub & 1) << 2 | sub >> 1) : piece) * 16;
+    const uint32_t to_v = sub * 128 + (S::kRow >= 128 ? piece ^ (sub >> 1) << 1 : piece ^ sub << 1) * 16;
+    const uint32_t from_k = S::kRow >= 128 ? g * 128 + (c ^ ((g & 1) << 2 | g >> 1)) * 16 : lane * 16;
+    const uint32_t from_v = S::kRow >= 128 ? c * 256 + (g ^ c << 1) * 16 : c * 128 + ((g >> 1) ^ c << 1) * 16 + (g & 1) * 8;
+    auto copy_tile = [&](uint32_t dst, uint32_t flip, long long store, bool one, long long row, uint32_t live) {
+#pragma unroll
+        for (int j = 0; j < S::kCopyRows; ++j) {
+            const int r = row0 + j * row_step;
+            const char* src = kb + store + (one ? row * (kE4m3 ? 1 : 2) + lane_row + j * row_step * token_bytes
+                                                : __shfl_sync(0xffffffffu, row, r) * (kE4m3 ? 1 : 2));
+            const bool ok = (live >> r) & 1;
+            src = ok ? src : kb;
+#pragma unroll
+            for (int u = 0; u < S::kCopySegs; ++u)
+                copy_async((dst ^ (S::kRow >= 128 && (j & 1) ? flip : 0)) + u * 2048 + j * 512, src + u * 128, ok);
+        }
+    };
+    const bool one_page = a.page_size % 16 == 0;   // a tile's keys lie in one page
+    long long head_off = 0;                        // the key head's place in a page, elements
+    int next_key = 0, next_page = -1, next_at = 0;
+    long long row = 0;                             // of the tile whose keys were copied last: its first key's place
+    uint32_t rows_live = 0;                        //   (one_page) or that of key `lane & 15`, and which keys live
+    int imeta = 0;
+    // The page of the next tile's first key (one_page) or of its key `lane & 15`, asked for one tile ahead.
     auto look_up = [&]() {
-        const int key = iw.first + iw.g * S::kGranule + warp * 16 + (lane & 15);
-        next_live = iw.n > 0 && key < iw.len;
-        if (next_live) {
-            const int j = static_cast<int>(static_cast<unsigned>(key) / static_cast<unsigned>(a.page_size));
+        next_key = iw.base() + iw.g * S::kGranule + warp * 16;
+        const int key = one_page ? next_key : next_key + (lane & 15);
+        next_page = -1;
+        if (iw.n > 0 && key < iw.len) {
+            const int j = static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(key)) * a.page_mul) >> a.page_shift);
             next_at = key - j * a.page_size;
             next_page = __ldg(a.page_table + iw.b * a.table_stride + j);
         }
     };
-    auto issue = [&](int stage) {
-        const int hk = iw.h / blocks;
-        bool live = next_live;
-        long long row = 0;
-        if (live) {
-            if (next_page >= 0 && next_page < a.n_pages)
-                row = next_page * a.page_stride + next_at * a.token_stride + hk * a.head_stride;
-            else {
-                record_error(a.status, MOE_ERR_INDEX);
-                live = false;
+    auto start_item = [&]() { head_off = iw.hk * a.head_stride; };
+    auto issue_keys = [&](int slot) {
+        // keys [first, len) of the tile's 16
+        const int lo_key = max(iw.first - next_key, 0), hi_key = min(max(iw.len - next_key, 0), 16);
+        rows_live = lo_key < hi_key ? (0xffffu >> (16 - hi_key)) & (0xffffu << lo_key) : 0u;
+        const bool ok_page = static_cast<unsigned>(next_page) < static_cast<unsigned>(a.n_pages);
+        if (one_page) {
+            if (!ok_page && rows_live) {
+                if (lane == 0) record_error(a.status, MOE_ERR_INDEX);
+                rows_live = 0;
             }
+        } else {
+            const bool mine = (rows_live >> (lane & 15)) & 1;
+            if (mine && !ok_page) record_error(a.status, MOE_ERR_INDEX);
+            rows_live = __ballot_sync(0xffffffffu, mine && ok_page) & 0xffffu;
         }
-        const uint32_t mask = __ballot_sync(0xffffffffu, live);
-        const uint32_t dst = ring + stage * 2 * S::kTile + lane * 16;
-        const char* const kb = static_cast<const char*>(a.k);
-        const char* const vb = static_cast<const char*>(a.v);
-        constexpr int kElt = kE4m3 ? 1 : 2;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const long long r = __shfl_sync(0xffffffffu, row, t * 8 + g) * kElt + c * 16;
-            const bool ok = (mask >> (t * 8 + g)) & 1;
-#pragma unroll
-            for (int u = 0; u < S::kKeySegs; ++u)
-                copy_async<16>(dst + (t * S::kKeySegs + u) * 512, kb + r + u * 64, ok);
-        }
-        const uint32_t vdst = ring + stage * 2 * S::kTile + S::kTile + lane * S::kValBytes;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int key = 2 * c + (t & 1) + (t >> 1) * 8;
-            const long long r = __shfl_sync(0xffffffffu, row, key) * kElt + g * S::kValBytes;
-            const bool ok = (mask >> key) & 1;
-#pragma unroll
-            for (int u = 0; u < S::kValSegs; ++u)
-                copy_async<S::kValBytes>(vdst + (t * S::kValSegs + u) * 32 * S::kValBytes, vb + r + u * 8 * S::kValBytes, ok);
-        }
+        row = ok_page ? next_page * a.page_stride + next_at * a.token_stride + head_off : 0;
+        copy_tile(ring + slot * S::kTile + to_k, 32, 0, one_page, row, rows_live);
+        unsigned char* const to = meta + imeta * S::kMeta;
         if (kE4m3) {
             // lanes 0..15 fetch the keys' exponent bytes, 16..31 the values': the byte is the last of the
             // `n` copied ones of its aligned word, so nothing behind it is read
             const uint8_t* e = (lane < 16 ? a.k_exp : a.v_exp);
             int n = 0;
-            if (live) {
-                e += next_page * a.exp_page_stride + next_at * a.exp_token_stride + hk * a.exp_head_stride;
+            if ((rows_live >> (lane & 15)) & 1) {
+                const int at = one_page ? next_at + (lane & 15) : next_at;
+                e += next_page * a.exp_page_stride + at * a.exp_token_stride + iw.hk * a.exp_head_stride;
                 n = static_cast<int>(reinterpret_cast<uintptr_t>(e) & 3) + 1;
                 e -= n - 1;
             }
-            copy_async_4(smem_u32(meta) + stage * S::kMeta + lane * 4, e, n);
-            meta[stage * S::kMeta + S::kByte + lane] = static_cast<unsigned char>(n);
+            copy_async_4(smem_u32(to) + lane * 4, e, n);
+            to[S::kByte + lane] = static_cast<unsigned char>(n);
         }
-        if (lane == 0) *reinterpret_cast<uint32_t*>(meta + stage * S::kMeta + S::kMask) = mask;
-        advance<S::kGranule>(a, iw, heads);
+        if (lane == 0) *reinterpret_cast<uint32_t*>(to + S::kMask) = rows_live;
+        imeta = imeta + 1 == kMetas ? 0 : imeta + 1;
+        if (++iw.g == iw.n) {
+            next_item<S::kGranule>(a, iw, blocks);
+            start_item();
+        }
         look_up();
     };
-
-    look_up();
-    for (int i = 0; i < kStages; ++i) {
-        if (i < count) issue(i);
+    auto issue_values = [&](int slot) {
+        copy_tile(ring + slot * S::kTile + to_v, 64, k_to_v, one_page, row, rows_live);
+    };
+    // The run as a sequence of 2 * count tiles (keys, values, keys, ...): number k goes to slot k % kSlots,
+    // issued when number k - kSlots has been used.
+    auto issue_number = [&](int k, bool values, int slot) {
+        if (k < 2 * count) {
+            if (values)
+                issue_values(slot);
+            else
+                issue_keys(slot);
+        }
         copy_commit();
-    }
+    };
+    constexpr bool kOdd = (kSlots & 1) != 0;
+
+    start_item();
+    look_up();
+#pragma unroll 1
+    for (int k = 0; k < kSlots; ++k) issue_number(k, (k & 1) != 0, k);
 
     // ---- the computing side
-    uint32_t q[kHalves][S::kQ];
-    float qscale[kHalves];            // scores in units of log2: accumulator * qscale (* the key's exponent)
-    float o[S::kTiles][4];
-    float m[kHalves], l[kHalves];
-    int stage = 0;
+    uint32_t q[kCols][S::kQ];
+    float qscale[kCols][2];           // scores in units of log2: accumulator * qscale (* the key's exponent)
+    float o[kCols][S::kTiles][4];
+    float m[kCols][2], l[kCols][2];   // of the heads 2c and 2c + 1 of the column tile
+    int slot = 0, cmeta = 0;
     for (int i = 0; i < count; ++i) {
-        const int hk = cw.h / blocks, block = cw.h - hk * blocks;
-        const int head0 = hk * group + block * kHeads, live_heads = min(kHeads, group - block * kHeads);
+        const int head0 = cw.hk * group + cw.block * kHeads, live_heads = min(kHeads, group - cw.block * kHeads);
         if (i == 0 || cw.g == 0) {    // a new item
 #pragma unroll
-            for (int hh = 0; hh < kHalves; ++hh) {
-                const bool ok = hh * 8 + g < live_heads;
-                const __nv_bfloat16* src = a.q + cw.b * a.q_token_stride + (head0 + hh * 8 + g) * a.q_head_stride;
-                m[hh] = -INFINITY;
-                l[hh] = 0.0f;
+            for (int hh = 0; hh < kCols; ++hh) {
+                const int h = kHeads == 4 ? g & 3 : hh * 8 + g;
+                const bool ok = h < live_heads;
+                const __nv_bfloat16* src = a.q + cw.b * a.q_token_stride + (head0 + h) * a.q_head_stride;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    m[hh][e] = -INFINITY;
+                    l[hh][e] = 0.0f;
+                    qscale[hh][e] = a.scale * kLog2e;
+                }
                 if (!kE4m3) {
 #pragma unroll
                     for (int u = 0; u < S::kKeySegs; ++u) {
@@ -381,7 +453,6 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3>::kWarps, 1) paged_attenti
                         q[hh][4 * u + 2] = v.z;
                         q[hh][4 * u + 3] = v.w;
                     }
-                    qscale[hh] = a.scale * kLog2e;
                 } else {
                     // bf16 to f16 after a power of two that puts the row's largest value near 2^13: values
                     // down to 2^-27 of it stay exact
@@ -403,7 +474,9 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3>::kWarps, 1) paged_attenti
                     int e = 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
                     e = top == 0.0f ? 0 : max(-114, min(100, e));
                     const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-                    qscale[hh] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) qscale[hh][k] *= __shfl_sync(0xffffffffu, down, (2 * c + k) * 4);
 #pragma unroll
                     for (int u = 0; u < 2 * S::kKeySegs; ++u) {
                         const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
@@ -412,104 +485,145 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3>::kWarps, 1) paged_attenti
                             q[hh][4 * u + j] = pack_f16x2(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xffff0000u) * up);
                     }
                 }
+#pragma unroll
+                for (int t = 0; t < S::kTiles; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[hh][t][j] = 0.0f;
             }
-#pragma unroll
-            for (int t = 0; t < S::kTiles; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[t][j] = 0.0f;
         }
 
-        copy_wait<kStages - 1>();
+        // ---- scores of the tile's keys g, g + 8 for the heads 2c, 2c + 1
+        copy_wait<kSlots - 1>();
         __syncwarp();
-        const uint32_t mask = *reinterpret_cast<const volatile uint32_t*>(meta + stage * S::kMeta + S::kMask);
-        if (mask & 0xffffu) {
-            const uint32_t kt = ring + stage * 2 * S::kTile + lane * 16;
-            float s[2][4];
+        unsigned char* const me = meta + cmeta * S::kMeta;
+        const uint32_t mask = *reinterpret_cast<const volatile uint32_t*>(me + S::kMask) & 0xffffu;
+        float s[kCols][4];
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+        for (int hh = 0; hh < kCols; ++hh)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[t][j] = 0.0f;
+            for (int j = 0; j < 4; ++j) s[hh][j] = 0.0f;
+        if (mask) {
+            const uint32_t kt = ring + slot * S::kTile + from_k;
 #pragma unroll
-            for (int u = 0; u < S::kKeySegs; ++u)
+            for (int u = 0; u < S::kKeySegs; ++u) {
+                const uint32_t at = S::kRow >= 128 ? (kt ^ (u & 1) * 64) + (u >> 1) * 2048 : kt;
+                const uint4 v0 = lds128(at), v1 = lds128(at + (S::kRow >= 128 ? 1024 : 512));
+                const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const uint4 v = lds128(kt + (t * S::kKeySegs + u) * 512);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int k = 0; k < S::kSteps; ++k) {
-                        const uint32_t k0 = kE4m3 ? f16_of_codes(w[k], 0) : w[2 * (k & 1)];
-                        const uint32_t k1 = kE4m3 ? f16_of_codes(w[k], 1) : w[2 * (k & 1) + 1];
-                        const int at = (u * S::kSteps + k) * 2;
-                        mma_16816(s[t], q[0][at], kHalves == 2 ? q[kHalves - 1][at] : 0u, q[0][at + 1],
-                                  kHalves == 2 ? q[kHalves - 1][at + 1] : 0u, k0, k1, kE4m3);
+                for (int k = 0; k < S::kSteps; ++k) {
+                    uint32_t f[4];
+                    if (kE4m3) {
+                        f[0] = f16_of_codes(w0[k], 0);
+                        f[1] = f16_of_codes(w1[k], 0);
+                        f[2] = f16_of_codes(w0[k], 1);
+                        f[3] = f16_of_codes(w1[k], 1);
+                    } else {
+                        f[0] = w0[2 * (k & 1)];
+                        f[1] = w1[2 * (k & 1)];
+                        f[2] = w0[2 * (k & 1) + 1];
+                        f[3] = w1[2 * (k & 1) + 1];
                     }
+                    const int step = (u * S::kSteps + k) * 2;
+#pragma unroll
+                    for (int hh = 0; hh < kCols; ++hh)
+                        mma_16816(s[hh], f[0], f[1], f[2], f[3], q[hh][step], q[hh][step + 1], kE4m3);
                 }
+            }
+        }
+        __syncwarp();
+        issue_number(2 * i + kSlots, kOdd, slot);
+        slot = slot + 1 == kSlots ? 0 : slot + 1;
 
-            // scores to log2 units; keys 2c, 2c+1 (+8) are this lane's columns
-            float kscale[4] = {1.0f, 1.0f, 1.0f, 1.0f}, vexp[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t whi[kCols][2], wlo[kCols][2];
+        if (mask) {
+            // scores to log2 units
+            float kscale[2] = {1.0f, 1.0f}, vexp[2] = {0.0f, 0.0f};
             if (kE4m3) {
-                const unsigned char* me = meta + stage * S::kMeta;
                 const uint32_t n = me[S::kByte + lane];
                 const uint32_t word = *reinterpret_cast<const volatile uint32_t*>(me + lane * 4);
                 const uint32_t byte = n ? (word >> (8 * (n - 1))) & 0xffu : 127u;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int key = 2 * c + (j & 1) + (j >> 1) * 8;
-                    kscale[j] = pow2_of_byte(__shfl_sync(0xffffffffu, byte, key));
-                    vexp[j] = static_cast<float>(static_cast<int>(__shfl_sync(0xffffffffu, byte, 16 + key)) - 127);
+                for (int r = 0; r < 2; ++r) {
+                    kscale[r] = pow2_of_byte(__shfl_sync(0xffffffffu, byte, 8 * r + g));
+                    vexp[r] = static_cast<float>(static_cast<int>(__shfl_sync(0xffffffffu, byte, 16 + 8 * r + g)) - 127);
                 }
             }
-            uint32_t whi[kHalves][2], wlo[kHalves][2];
-            float fix[kHalves];
+            float x[kCols][4], y[kCols][4];
             bool grew = false;
 #pragma unroll
-            for (int hh = 0; hh < kHalves; ++hh) {
-                float x[4], y[4];
+            for (int hh = 0; hh < kCols; ++hh)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const bool ok = (mask >> (2 * c + (j & 1) + (j >> 1) * 8)) & 1;
-                    x[j] = s[j >> 1][hh * 2 + (j & 1)] * qscale[hh];
-                    if (kE4m3) x[j] *= kscale[j];
-                    x[j] = ok ? x[j] : -INFINITY;
-                    y[j] = kE4m3 ? x[j] + vexp[j] : x[j];
+                    const bool ok = (mask >> (8 * (j >> 1) + g)) & 1;
+                    x[hh][j] = s[hh][j] * qscale[hh][j & 1];
+                    if (kE4m3) x[hh][j] *= kscale[j >> 1];
+                    x[hh][j] = ok ? x[hh][j] : -INFINITY;
+                    y[hh][j] = kE4m3 ? x[hh][j] + vexp[j >> 1] : x[hh][j];
+                    grew |= y[hh][j] > m[hh][j & 1] + kSlack;
                 }
-                float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float mn = fmaxf(m[hh], top);
-                const float ref = mn == -INFINITY ? 0.0f : (kE4m3 ? mn - kShift : mn);
-                fix[hh] = mn > m[hh] ? exp2_fast(m[hh] - mn) : 1.0f;
-                grew |= mn > m[hh];
-                m[hh] = mn;
-                float p[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) p[j] = exp2_fast(y[j] - ref);
-                float sum;
-                if (kE4m3)
-                    sum = (exp2_fast(x[0] - ref) + exp2_fast(x[1] - ref)) + (exp2_fast(x[2] - ref) + exp2_fast(x[3] - ref));
-                else
-                    sum = (p[0] + p[1]) + (p[2] + p[3]);
-                l[hh] = l[hh] * fix[hh] + sum;
-                split_pair<kE4m3>(p[0], p[1], whi[hh][0], wlo[hh][0]);
-                split_pair<kE4m3>(p[2], p[3], whi[hh][1], wlo[hh][1]);
-            }
             if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-                for (int t = 0; t < S::kTiles; ++t) {
-                    o[t][0] *= fix[0];
-                    o[t][1] *= fix[0];
-                    o[t][2] *= fix[kHalves - 1];
-                    o[t][3] *= fix[kHalves - 1];
+                for (int hh = 0; hh < kCols; ++hh)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float top = fmaxf(y[hh][e], y[hh][2 + e]);
+#pragma unroll
+                        for (int off = 4; off <= 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                        const float mn = fmaxf(m[hh][e], top);
+                        const float fix = mn > m[hh][e] ? exp2_fast(m[hh][e] - mn) : 1.0f;
+                        m[hh][e] = mn;
+                        l[hh][e] *= fix;
+#pragma unroll
+                        for (int t = 0; t < S::kTiles; ++t) {
+                            o[hh][t][e] *= fix;
+                            o[hh][t][2 + e] *= fix;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int hh = 0; hh < kCols; ++hh) {
+                float p[4];
+                float ref[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    ref[e] = m[hh][e] == -INFINITY ? 0.0f : (kE4m3 ? m[hh][e] - kShift : m[hh][e]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) p[j] = exp2_fast(y[hh][j] - ref[j & 1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (kE4m3)
+                        l[hh][e] += exp2_fast(x[hh][e] - ref[e]) + exp2_fast(x[hh][2 + e] - ref[e]);
+                    else
+                        l[hh][e] += p[e] + p[2 + e];
+                }
+                uint32_t h0, l0, h1, l1;
+                split_pair<kE4m3>(p[0], p[1], h0, l0);
+                split_pair<kE4m3>(p[2], p[3], h1, l1);
+                if (kHeads == 4) {
+                    whi[hh][0] = transpose_8x8(c < 2 ? h0 : l0);
+                    whi[hh][1] = transpose_8x8(c < 2 ? h1 : l1);
+                } else {
+                    whi[hh][0] = transpose_8x8(h0);
+                    whi[hh][1] = transpose_8x8(h1);
+                    wlo[hh][0] = transpose_8x8(l0);
+                    wlo[hh][1] = transpose_8x8(l1);
                 }
             }
+        }
+        cmeta = cmeta + 1 == kMetas ? 0 : cmeta + 1;
 
-            const uint32_t vt = ring + stage * 2 * S::kTile + S::kTile + lane * S::kValBytes;
+        // ---- the weighted values
+        copy_wait<kSlots - 1>();
+        __syncwarp();
+        if (mask) {
+            const uint32_t vt = ring + slot * S::kTile + from_v;
 #pragma unroll
             for (int u = 0; u < S::kValSegs; ++u) {
                 uint32_t v[4][4];
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    const uint32_t at = vt + (t * S::kValSegs + u) * 32 * S::kValBytes;
+                    const uint32_t at = S::kRow >= 128 ? vt + u * 2048 + (t & 1) * 128 + (t >> 1) * 1024
+                                                       : (vt ^ (t & 1) * 64) + (t >> 1) * 512;
                     if (S::kValBytes == 16) {
                         const uint4 w = lds128(at);
                         v[t][0] = w.x;
@@ -523,33 +637,37 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3>::kWarps, 1) paged_attenti
                         v[t][2] = v[t][3] = 0;
                     }
                 }
+                // rows g and g + 8 of a tile are the dimensions j and j + 1 of the lane's piece
 #pragma unroll
-                for (int j = 0; j < S::kValElts; ++j) {
-                    uint32_t v0, v1;
+                for (int j = 0; j < S::kValElts; j += 2) {
+                    uint32_t f[4];
                     if (kE4m3) {
-                        // bytes j of two keys side by side, two j at a time
+                        // bytes j, j + 1 of two keys side by side
                         const int w = j >> 2, sel = (j & 2) ? 0x7362 : 0x5140;
-                        v0 = f16_of_codes(__byte_perm(v[0][w], v[1][w], sel), j & 1);
-                        v1 = f16_of_codes(__byte_perm(v[2][w], v[3][w], sel), j & 1);
+                        const uint32_t low = __byte_perm(v[0][w], v[1][w], sel), high = __byte_perm(v[2][w], v[3][w], sel);
+                        f[0] = f16_of_codes(low, 0);
+                        f[1] = f16_of_codes(low, 1);
+                        f[2] = f16_of_codes(high, 0);
+                        f[3] = f16_of_codes(high, 1);
                     } else {
-                        const int w = j >> 1, sel = (j & 1) ? 0x7632 : 0x5410;
-                        v0 = __byte_perm(v[0][w], v[1][w], sel);
-                        v1 = __byte_perm(v[2][w], v[3][w], sel);
+                        const int w = j >> 1;
+                        f[0] = __byte_perm(v[0][w], v[1][w], 0x5410);
+                        f[1] = __byte_perm(v[0][w], v[1][w], 0x7632);
+                        f[2] = __byte_perm(v[2][w], v[3][w], 0x5410);
+                        f[3] = __byte_perm(v[2][w], v[3][w], 0x7632);
                     }
-                    float(&acc)[4] = o[u * S::kValElts + j];
-                    if (kHalves == 1) {
-                        mma_16816(acc, whi[0][0], wlo[0][0], whi[0][1], wlo[0][1], v0, v1, kE4m3);
-                    } else {
-                        mma_16816(acc, whi[0][0], whi[kHalves - 1][0], whi[0][1], whi[kHalves - 1][1], v0, v1, kE4m3);
-                        mma_16816(acc, wlo[0][0], wlo[kHalves - 1][0], wlo[0][1], wlo[kHalves - 1][1], v0, v1, kE4m3);
+                    const int t = (u * S::kValElts + j) / 2;
+#pragma unroll
+                    for (int hh = 0; hh < kCols; ++hh) {
+                        mma_16816(o[hh][t], f[0], f[1], f[2], f[3], whi[hh][0], whi[hh][1], kE4m3);
+                        if (kHeads != 4) mma_16816(o[hh][t], f[0], f[1], f[2], f[3], wlo[hh][0], wlo[hh][1], kE4m3);
                     }
                 }
             }
         }
         __syncwarp();
-        if (i + kStages < count) issue(stage);
-        copy_commit();
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+        issue_number(2 * i + 1 + kSlots, !kOdd, slot);
+        slot = slot + 1 == kSlots ? 0 : slot + 1;
 
         // ---- the end of an item, or of this block's part of it
         if (cw.g + 1 == cw.n || i + 1 == count) {
@@ -559,70 +677,72 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3>::kWarps, 1) paged_attenti
             float* const slots = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kAttentionCtrlBytes);
             float* const part = slots + (2 * static_cast<size_t>(blockIdx.x) + (c0 == blockIdx.x ? 1 : 0)) * kSlot;
 #pragma unroll
-            for (int hh = 0; hh < kHalves; ++hh) {
-                float sum = l[hh];
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                if (c == 0) s_ml[warp * 16 + hh * 8 + g] = make_float2(m[hh], sum);
+            for (int hh = 0; hh < kCols; ++hh) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float sum = l[hh][e];
+#pragma unroll
+                    for (int off = 4; off <= 16; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                    if (g == 0 && (kHeads != 4 || c < 2)) s_ml[warp * 16 + hh * 8 + 2 * c + e] = make_float2(m[hh][e], sum);
+                }
+                if (kHeads == 4) {   // the low parts' columns
+#pragma unroll
+                    for (int t = 0; t < S::kTiles; ++t)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[hh][t][j] += __shfl_xor_sync(0xffffffffu, o[hh][t][j], 2);
+                }
             }
-            // rows of 8 heads at a time through shared memory: row r of half hh is warp r's (and r + 4's)
+            // four heads at a time through shared memory
 #pragma unroll
-            for (int hh = 0; hh < kHalves; ++hh) {
-                if (hh * 8 >= live_heads) break;
-                if (hh > 0) __syncthreads();
-                float* dst = s_merge + (warp * 8 + g) * D;
+            for (int four = 0; four < kHeads / 4; ++four) {
+                if (four * 4 >= live_heads) break;
+                if (four > 0) __syncthreads();
+                if ((c >> 1) == (four & 1)) {
 #pragma unroll
-                for (int u = 0; u < S::kValSegs; ++u)
+                    for (int e = 0; e < 2; ++e) {
+                        float* dst = s_merge + (warp * 4 + (2 * c & 3) + e) * D + g * S::kValElts;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                        for (int u = 0; u < S::kValSegs; ++u)
 #pragma unroll
-                        for (int j = 0; j < S::kValElts; j += 4) {
-                            float x[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float(&acc)[4] = o[u * S::kValElts + j + k];
-                                x[k] = kHalves == 1 ? acc[e] + acc[2 + e] : acc[2 * hh + e];
+                            for (int j = 0; j < S::kValElts; j += 4) {
+                                const int t = (u * S::kValElts + j) / 2;
+                                *reinterpret_cast<float4*>(dst + u * 8 * S::kValElts + j) =
+                                    make_float4(o[four >> 1][t][e], o[four >> 1][t][2 + e], o[four >> 1][t + 1][e], o[four >> 1][t + 1][2 + e]);
                             }
-                            *reinterpret_cast<float4*>(dst + u * 8 * S::kValElts + (2 * c + e) * S::kValElts + j) =
-                                make_float4(x[0], x[1], x[2], x[3]);
-                        }
+                    }
+                }
                 __syncthreads();
-                for (int r = warp; r < 8 && hh * 8 + r < live_heads; r += kWarps) {
+                for (int at = threadIdx.x; at < D; at += kThreads) {   // D = 4 rows of D / 4 float4
+                    const int r = at / (D / 4), d = at % (D / 4) * 4;
+                    if (four * 4 + r >= live_heads) break;
                     float M = -INFINITY;
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * 16 + hh * 8 + r].x);
+                    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * 16 + four * 4 + r].x);
                     const float ref = M == -INFINITY ? 0.0f : M;
-                    float L = 0.0f, f[kWarps];
+                    float L = 0.0f;
+                    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) {
-                        const float2 ml = s_ml[w * 16 + hh * 8 + r];
-                        f[w] = exp2_fast(ml.x - ref);
-                        L += ml.y * f[w];
+                        const float2 ml = s_ml[w * 16 + four * 4 + r];
+                        const float f = exp2_fast(ml.x - ref);
+                        const float4 y = *reinterpret_cast<const float4*>(s_merge + (w * 4 + r) * D + d);
+                        L += ml.y * f;
+                        x.x += y.x * f;
+                        x.y += y.y * f;
+                        x.z += y.z * f;
+                        x.w += y.w * f;
                     }
-                    const int head = head0 + hh * 8 + r;
-                    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-                    for (int d = 4 * lane; d < D; d += 128) {
-                        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                        for (int w = 0; w < kWarps; ++w) {
-                            const float4 y = *reinterpret_cast<const float4*>(s_merge + (w * 8 + r) * D + d);
-                            x.x += y.x * f[w];
-                            x.y += y.y * f[w];
-                            x.z += y.z * f[w];
-                            x.w += y.w * f[w];
-                        }
-                        if (whole)
-                            *reinterpret_cast<uint2*>(a.out + cw.b * a.out_token_stride + head * a.out_head_stride + d) =
-                                make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-                        else
-                            *reinterpret_cast<float4*>(part + (hh * 8 + r) * D + d) = x;
-                    }
-                    if (lane == 0) {
-                        if (!whole)
-                            *reinterpret_cast<float2*>(part + 16 * D + 2 * (hh * 8 + r)) = make_float2(M, L);
-                        else if (a.lse)
+                    const int head = head0 + four * 4 + r;
+                    if (whole) {
+                        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+                        *reinterpret_cast<uint2*>(a.out + cw.b * a.out_token_stride + head * a.out_head_stride + d) =
+                            make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+                        if (d == 0 && a.lse)
                             a.lse[static_cast<long long>(cw.b) * a.n_heads + head] =
                                 L == 0.0f ? -INFINITY : ((kE4m3 ? M - kShift : M) + log2f(L)) * kLn2;
+                    } else {
+                        *reinterpret_cast<float4*>(part + (four * 4 + r) * D + d) = x;
+                        if (d == 0) *reinterpret_cast<float2*>(part + 16 * D + 2 * (four * 4 + r)) = make_float2(M, L);
                     }
                 }
             }
@@ -651,7 +771,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3>::kWarps, 1) paged_attenti
                         float4 x[(D + 127) / 128];
 #pragma unroll
                         for (int e = 0; e < (D + 127) / 128; ++e) x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
                         for (int k = 0; k < parts; ++k) {
                             const float* p = slot(k);
                             const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + 16 * D + 2 * r));
@@ -686,35 +806,44 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3>::kWarps, 1) paged_attenti
             }
             __syncthreads();   // the shared rows are free for the next item
         }
-        advance<S::kGranule>(a, cw, heads);
+        if (++cw.g == cw.n) next_item<S::kGranule>(a, cw, blocks);
     }
 }
 
 template <int D, bool kE4m3, int kHeads>
 cudaError_t launch_heads(const AttentionArgs& a, cudaStream_t s)
 {
-    using S = Shape<D, kE4m3>;
+    using S = Shape<D, kE4m3, kHeads>;
     const auto kernel = paged_attention_kernel<D, kE4m3, kHeads>;
     if (cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), S::kSmem); e != cudaSuccess) return e;
-    // one block per SM, fewer when the longest possible batch has fewer granules
+    // every resident block once, fewer when the longest possible batch has fewer granules
     const long long most = static_cast<long long>(a.max_pages) * a.page_size;
     const long long keys = a.window > 0 && a.window < most ? a.window : most;
     const int group = a.n_heads / a.n_kv_heads;
     const long long items = static_cast<long long>(a.B) * a.n_kv_heads * ((group + kHeads - 1) / kHeads);
-    const long long granules = (keys + S::kGranule - 1) / S::kGranule;
-    long long grid = num_sms() < kAttentionCtas ? num_sms() : kAttentionCtas;
+    const long long granules = (keys + 15 + S::kGranule - 1) / S::kGranule;
+    long long grid = std::min(num_sms() * S::kCtas, kAttentionCtas);
     if (items < grid && granules < grid && items * granules < grid) grid = items * granules;
-    kernel<<<static_cast<unsigned>(grid), 32 * S::kWarps, S::kSmem, s>>>(a);
+    AttentionArgs b = a;
+    // key / page_size for 0 <= key < 2^31 as a product and a shift: with 2^l the power of two at or above
+    // page_size and mul = ceil(2^(31 + l) / page_size), mul * page_size exceeds 2^(31 + l) by less than 2^l
+    int l = 0;
+    while ((1LL << l) < a.page_size) ++l;
+    b.page_shift = 31 + l;
+    b.page_mul = static_cast<uint32_t>(((1ULL << (31 + l)) + a.page_size - 1) / a.page_size);
+    kernel<<<static_cast<unsigned>(grid), 32 * S::kWarps, S::kSmem, s>>>(b);
     return cudaGetLastError();
 }
 
 template <int D, bool kE4m3>
 cudaError_t launch_d(const AttentionArgs& a, cudaStream_t s)
 {
-    // 8 query heads per block of heads leave the other half of the matrix rows to the weights' low
-    // parts; more share one read of the cache between 16 (at D = 256 the registers hold 8)
+    // up to 4 query heads per key head take both parts of the weights in one product; more than 8 share
+    // one read of the cache between 16 (at D = 256 the registers hold 8)
+    const int group = a.n_heads / a.n_kv_heads;
+    if (group <= 4) return launch_heads<D, kE4m3, 4>(a, s);
     if constexpr (D < 256)
-        if (a.n_heads / a.n_kv_heads > 8) return launch_heads<D, kE4m3, 16>(a, s);
+        if (group > 8) return launch_heads<D, kE4m3, 16>(a, s);
     return launch_heads<D, kE4m3, 8>(a, s);
 }
 

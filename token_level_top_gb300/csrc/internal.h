@@ -307,9 +307,11 @@ struct AttentionArgs {
     long long exp_page_stride, exp_token_stride, exp_head_stride;
     void* ws;
     int* status;
+    uint32_t page_mul;           // key / page_size = key * page_mul >> page_shift (set by the launcher)
+    int page_shift;
 };
 // The attention workspace starts with the status word and the counters of the join.
-constexpr size_t kAttentionCtrlBytes = 1024;
+constexpr size_t kAttentionCtrlBytes = 4096;
 size_t paged_attention_ws_bytes(int head_dim);   // 0: unsupported head_dim
 cudaError_t launch_paged_attention(const AttentionArgs& a, int head_dim, bool e4m3, cudaStream_t s);
 
