@@ -573,7 +573,8 @@ moe_status_t moe_paged_attention_workspace_init(void* ws_dev, size_t ws_bytes, v
  * -inf, gets zeros and lse = -inf.  What the cache holds in other places (NaN included) has no effect.
  * Lengths are read on the device: a captured graph replays at other lengths.  A
  * length outside [0, max_pages * page_size] (at most 2^31 - 65536) is brought to its nearer end, and keys
- * of a page outside [0, n_pages) are left out; both record MOE_ERR_INDEX. */
+ * of a page outside [0, n_pages) are left out; both record MOE_ERR_INDEX.  Page and token
+ * strides of 4 GB and more, or below 0, are MOE_ERR_UNSUPPORTED. */
 moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_attention_t* a, void* ws_dev,
                                  size_t ws_bytes, void* stream);
 

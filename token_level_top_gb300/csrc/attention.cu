@@ -71,8 +71,13 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // Copies 16 bytes, or writes 16 zeros when !live (src is then not read).
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool live)
+__device__ __forceinline__ void copy_async_or_zeros(uint32_t dst, const void* src, bool live)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
@@ -103,13 +108,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t a)
     return v;
 }
 
-// Two e4m3 codes (the low or high half of w) to two f16, exactly.
-__device__ __forceinline__ uint32_t f16_of_codes(uint32_t w, int half)
+// Four e4m3 codes to two pairs of f16, exactly.
+__device__ __forceinline__ void f16_of_codes(uint32_t w, uint32_t& lo, uint32_t& hi)
 {
-    uint32_t r;
-    const uint16_t two = static_cast<uint16_t>(half ? w >> 16 : w & 0xffffu);
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(two));
-    return r;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
@@ -316,61 +320,86 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
 
     // ---- the copying side
     constexpr int kElt = kE4m3 ? 1 : 2;
-    const long long token_bytes = a.token_stride * kElt;
     // A copy instruction moves four 128-byte lines, eight lanes to a line.  A tile is stored by lines (a
     // 128-byte segment of a row, or two 64-byte rows) whose 16-byte pieces are permuted by an XOR with f(row), so
     // that the copies write whole lines and the fragment reads below hit every bank once: for the keys (8 lanes
     // read 4 pieces of rows 2n, 2n + 1) f flips bit 2 with the row, for the values (2 pieces of rows 2n, 2n + 2,
     // 2n + 4, 2n + 6) bits 1 and 2 with row / 2.
     const int sub = lane >> 3, piece = lane & 7;
-    const char* const kb = static_cast<const char*>(a.k) + (S::kRow >= 128 ? piece : piece & 3) * 16;
-    const long long k_to_v = static_cast<const char*>(a.v) - static_cast<const char*>(a.k);
-    const int row0 = S::kRow >= 128 ? sub : 2 * sub + (piece >> 2);       // the lane's rows: row0, row0 + row_step, ..
-    constexpr int row_step = S::kRow >= 128 ? 4 : 8;
-    const long long lane_row = row0 * token_bytes;
-    const uint32_t to_k = sub * 128 + (S::kRow >= 128 ? piece ^ ((sub & 1) << 2 | sub >> 1) : piece) * 16;
-    const uint32_t to_v = sub * 128 + (S::kRow >= 128 ? piece ^ (sub >> 1) << 1 : piece ^ sub << 1) * 16;
-    const uint32_t from_k = S::kRow >= 128 ? g * 128 + (c ^ ((g & 1) << 2 | g >> 1)) * 16 : lane * 16;
-    const uint32_t from_v = S::kRow >= 128 ? c * 256 + (g ^ c << 1) * 16 : c * 128 + ((g >> 1) ^ c << 1) * 16 + (g & 1) * 8;
-    auto copy_tile = [&](uint32_t dst, uint32_t flip, long long store, bool one, long long row, uint32_t live) {
-#pragma unroll
-        for (int j = 0; j < S::kCopyRows; ++j) {
-            const int r = row0 + j * row_step;
-            const char* src = kb + store + (one ? row * (kE4m3 ? 1 : 2) + lane_row + j * row_step * token_bytes
-                                                : __shfl_sync(0xffffffffu, row, r) * (kE4m3 ? 1 : 2));
-            const bool ok = (live >> r) & 1;
-            src = ok ? src : kb;
-#pragma unroll
-            for (int u = 0; u < S::kCopySegs; ++u)
-                copy_async((dst ^ (S::kRow >= 128 && (j & 1) ? flip : 0)) + u * 2048 + j * 512, src + u * 128, ok);
-        }
-    };
+    const int row0 = S::kRow >= 128 ? sub : 2 * sub + (piece >> 2);       // the lane's rows: row0, row0 + kStep, ..
+    constexpr int kStep = S::kRow >= 128 ? 4 : 8;
+    const uint32_t token_bytes = static_cast<uint32_t>(a.token_stride * kElt);
+    const uint32_t page_bytes = static_cast<uint32_t>(a.page_stride * kElt);
+    const uint32_t to_k = ring + sub * 128 + (S::kRow >= 128 ? piece ^ ((sub & 1) << 2 | sub >> 1) : piece) * 16;
+    const uint32_t to_v = ring + sub * 128 + (S::kRow >= 128 ? piece ^ (sub >> 1) << 1 : piece ^ sub << 1) * 16;
+    const uint32_t from_k = ring + (S::kRow >= 128 ? g * 128 + (c ^ ((g & 1) << 2 | g >> 1)) * 16 : lane * 16);
+    const uint32_t from_v = ring + (S::kRow >= 128 ? c * 256 + (g ^ c << 1) * 16 : c * 128 + ((g >> 1) ^ c << 1) * 16 + (g & 1) * 8);
     const bool one_page = a.page_size % 16 == 0;   // a tile's keys lie in one page
-    long long head_off = 0;                        // the key head's place in a page, elements
+    // of the item whose tiles are copied: its table row, this lane's place in a page of its key head (for
+    // one_page with the lane's first row), the same in the exponents
+    const int32_t* table = nullptr;
+    const char *lane_k = nullptr, *lane_v = nullptr;
+    const uint8_t* lane_exp = nullptr;
     int next_key = 0, next_page = -1, next_at = 0;
-    long long row = 0;                             // of the tile whose keys were copied last: its first key's place
-    uint32_t rows_live = 0;                        //   (one_page) or that of key `lane & 15`, and which keys live
+    const char *row_k = nullptr, *row_v = nullptr;   // this lane's first row of the tile whose keys were copied last
+    uint32_t rows_live = 0;                          // and which of its keys live
     int imeta = 0;
+    auto start_item = [&]() {
+        table = a.page_table + iw.b * a.table_stride;
+        const long long at = iw.hk * a.head_stride * kElt + (S::kRow >= 128 ? piece : piece & 3) * 16;
+        lane_k = static_cast<const char*>(a.k) + at;
+        lane_v = static_cast<const char*>(a.v) + at;
+        if (one_page) {
+            lane_k += row0 * static_cast<long long>(token_bytes);
+            lane_v += row0 * static_cast<long long>(token_bytes);
+        }
+        if (kE4m3)
+            lane_exp = (lane < 16 ? a.k_exp : a.v_exp) + iw.hk * a.exp_head_stride +
+                       (one_page ? (lane & 15) * a.exp_token_stride : 0);
+        next_key = iw.base() + iw.g * S::kGranule + warp * 16;
+    };
     // The page of the next tile's first key (one_page) or of its key `lane & 15`, asked for one tile ahead.
     auto look_up = [&]() {
-        next_key = iw.base() + iw.g * S::kGranule + warp * 16;
         const int key = one_page ? next_key : next_key + (lane & 15);
         next_page = -1;
-        if (iw.n > 0 && key < iw.len) {
-            const int j = static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(key)) * a.page_mul) >> a.page_shift);
-            next_at = key - j * a.page_size;
-            next_page = __ldg(a.page_table + iw.b * a.table_stride + j);
+        if (key < iw.len) {
+            const uint32_t j = static_cast<uint32_t>((static_cast<uint64_t>(static_cast<uint32_t>(key)) * a.page_mul) >> a.page_shift);
+            next_at = key - static_cast<int>(j * static_cast<uint32_t>(a.page_size));
+            next_page = __ldg(table + j);
         }
     };
-    auto start_item = [&]() { head_off = iw.hk * a.head_stride; };
+    auto copy_tile = [&](uint32_t dst, uint32_t flip, const char* row, const char* idle) {
+        if (one_page && rows_live == 0xffffu) {
+#pragma unroll
+            for (int j = 0; j < S::kCopyRows; ++j) {
+                const char* src = row + static_cast<uint64_t>(token_bytes) * (j * kStep);
+#pragma unroll
+                for (int u = 0; u < S::kCopySegs; ++u)
+                    copy_async((S::kRow >= 128 && (j & 1) ? dst ^ flip : dst) + u * 2048 + j * 512, src + u * 128);
+            }
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < S::kCopyRows; ++j) {
+                const int r = row0 + j * kStep;
+                const char* src = one_page ? row + static_cast<uint64_t>(token_bytes) * (j * kStep)
+                                           : reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r)) +
+                                                 (S::kRow >= 128 ? piece : piece & 3) * 16;
+                const bool ok = (rows_live >> r) & 1;
+                src = ok ? src : idle;
+#pragma unroll
+                for (int u = 0; u < S::kCopySegs; ++u)
+                    copy_async_or_zeros((S::kRow >= 128 && (j & 1) ? dst ^ flip : dst) + u * 2048 + j * 512, src + u * 128, ok);
+            }
+        }
+    };
     auto issue_keys = [&](int slot) {
         // keys [first, len) of the tile's 16
         const int lo_key = max(iw.first - next_key, 0), hi_key = min(max(iw.len - next_key, 0), 16);
         rows_live = lo_key < hi_key ? (0xffffu >> (16 - hi_key)) & (0xffffu << lo_key) : 0u;
         const bool ok_page = static_cast<unsigned>(next_page) < static_cast<unsigned>(a.n_pages);
         if (one_page) {
-            if (!ok_page && rows_live) {
-                if (lane == 0) record_error(a.status, MOE_ERR_INDEX);
+            if (!ok_page) {
+                if (rows_live && lane == 0) record_error(a.status, MOE_ERR_INDEX);
                 rows_live = 0;
             }
         } else {
@@ -378,17 +407,23 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
             if (mine && !ok_page) record_error(a.status, MOE_ERR_INDEX);
             rows_live = __ballot_sync(0xffffffffu, mine && ok_page) & 0xffffu;
         }
-        row = ok_page ? next_page * a.page_stride + next_at * a.token_stride + head_off : 0;
-        copy_tile(ring + slot * S::kTile + to_k, 32, 0, one_page, row, rows_live);
+        const uint64_t place = static_cast<uint64_t>(static_cast<uint32_t>(next_page)) * page_bytes +
+                               static_cast<uint64_t>(static_cast<uint32_t>(next_at)) * token_bytes;
+        row_k = lane_k + place;
+        row_v = lane_v + place;
+        if (!one_page) {   // the rows are handed around: without the lane's piece
+            row_k -= (S::kRow >= 128 ? piece : piece & 3) * 16;
+            row_v -= (S::kRow >= 128 ? piece : piece & 3) * 16;
+        }
+        copy_tile(to_k + slot * S::kTile, 32, row_k, static_cast<const char*>(a.k));
         unsigned char* const to = meta + imeta * S::kMeta;
         if (kE4m3) {
             // lanes 0..15 fetch the keys' exponent bytes, 16..31 the values': the byte is the last of the
             // `n` copied ones of its aligned word, so nothing behind it is read
-            const uint8_t* e = (lane < 16 ? a.k_exp : a.v_exp);
+            const uint8_t* e = lane < 16 ? a.k_exp : a.v_exp;
             int n = 0;
             if ((rows_live >> (lane & 15)) & 1) {
-                const int at = one_page ? next_at + (lane & 15) : next_at;
-                e += next_page * a.exp_page_stride + at * a.exp_token_stride + iw.hk * a.exp_head_stride;
+                e = lane_exp + next_page * a.exp_page_stride + next_at * a.exp_token_stride;
                 n = static_cast<int>(reinterpret_cast<uintptr_t>(e) & 3) + 1;
                 e -= n - 1;
             }
@@ -397,15 +432,14 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
         }
         if (lane == 0) *reinterpret_cast<uint32_t*>(to + S::kMask) = rows_live;
         imeta = imeta + 1 == kMetas ? 0 : imeta + 1;
+        next_key += S::kGranule;
         if (++iw.g == iw.n) {
             next_item<S::kGranule>(a, iw, blocks);
-            start_item();
+            if (iw.n > 0) start_item();
         }
         look_up();
     };
-    auto issue_values = [&](int slot) {
-        copy_tile(ring + slot * S::kTile + to_v, 64, k_to_v, one_page, row, rows_live);
-    };
+    auto issue_values = [&](int slot) { copy_tile(to_v + slot * S::kTile, 64, row_v, static_cast<const char*>(a.v)); };
     // The run as a sequence of 2 * count tiles (keys, values, keys, ...): number k goes to slot k % kSlots,
     // issued when number k - kSlots has been used.
     auto issue_number = [&](int k, bool values, int slot) {
@@ -429,6 +463,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
     float qscale[kCols][2];           // scores in units of log2: accumulator * qscale (* the key's exponent)
     float o[kCols][S::kTiles][4];
     float m[kCols][2], l[kCols][2];   // of the heads 2c and 2c + 1 of the column tile
+    float ref[kCols][2], limit[kCols][2];   // what the exponents are taken against, and the score that raises m
     int slot = 0, cmeta = 0;
     for (int i = 0; i < count; ++i) {
         const int head0 = cw.hk * group + cw.block * kHeads, live_heads = min(kHeads, group - cw.block * kHeads);
@@ -440,7 +475,8 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                 const __nv_bfloat16* src = a.q + cw.b * a.q_token_stride + (head0 + h) * a.q_head_stride;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    m[hh][e] = -INFINITY;
+                    m[hh][e] = limit[hh][e] = -INFINITY;
+                    ref[hh][e] = 0.0f;
                     l[hh][e] = 0.0f;
                     qscale[hh][e] = a.scale * kLog2e;
                 }
@@ -503,7 +539,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[hh][j] = 0.0f;
         if (mask) {
-            const uint32_t kt = ring + slot * S::kTile + from_k;
+            const uint32_t kt = from_k + slot * S::kTile;
 #pragma unroll
             for (int u = 0; u < S::kKeySegs; ++u) {
                 const uint32_t at = S::kRow >= 128 ? (kt ^ (u & 1) * 64) + (u >> 1) * 2048 : kt;
@@ -513,10 +549,8 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                 for (int k = 0; k < S::kSteps; ++k) {
                     uint32_t f[4];
                     if (kE4m3) {
-                        f[0] = f16_of_codes(w0[k], 0);
-                        f[1] = f16_of_codes(w1[k], 0);
-                        f[2] = f16_of_codes(w0[k], 1);
-                        f[3] = f16_of_codes(w1[k], 1);
+                        f16_of_codes(w0[k], f[0], f[2]);
+                        f16_of_codes(w1[k], f[1], f[3]);
                     } else {
                         f[0] = w0[2 * (k & 1)];
                         f[1] = w1[2 * (k & 1)];
@@ -554,12 +588,22 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
             for (int hh = 0; hh < kCols; ++hh)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const bool ok = (mask >> (8 * (j >> 1) + g)) & 1;
                     x[hh][j] = s[hh][j] * qscale[hh][j & 1];
                     if (kE4m3) x[hh][j] *= kscale[j >> 1];
-                    x[hh][j] = ok ? x[hh][j] : -INFINITY;
+                }
+            if (mask != 0xffffu) {
+                const bool ok0 = (mask >> g) & 1, ok1 = (mask >> (8 + g)) & 1;
+#pragma unroll
+                for (int hh = 0; hh < kCols; ++hh)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[hh][j] = (j < 2 ? ok0 : ok1) ? x[hh][j] : -INFINITY;
+            }
+#pragma unroll
+            for (int hh = 0; hh < kCols; ++hh)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
                     y[hh][j] = kE4m3 ? x[hh][j] + vexp[j >> 1] : x[hh][j];
-                    grew |= y[hh][j] > m[hh][j & 1] + kSlack;
+                    grew |= y[hh][j] > limit[hh][j & 1];
                 }
             if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -572,6 +616,8 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                         const float mn = fmaxf(m[hh][e], top);
                         const float fix = mn > m[hh][e] ? exp2_fast(m[hh][e] - mn) : 1.0f;
                         m[hh][e] = mn;
+                        limit[hh][e] = mn + kSlack;
+                        ref[hh][e] = mn == -INFINITY ? 0.0f : (kE4m3 ? mn - kShift : mn);
                         l[hh][e] *= fix;
 #pragma unroll
                         for (int t = 0; t < S::kTiles; ++t) {
@@ -583,16 +629,12 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
 #pragma unroll
             for (int hh = 0; hh < kCols; ++hh) {
                 float p[4];
-                float ref[2];
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    ref[e] = m[hh][e] == -INFINITY ? 0.0f : (kE4m3 ? m[hh][e] - kShift : m[hh][e]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) p[j] = exp2_fast(y[hh][j] - ref[j & 1]);
+                for (int j = 0; j < 4; ++j) p[j] = exp2_fast(y[hh][j] - ref[hh][j & 1]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if (kE4m3)
-                        l[hh][e] += exp2_fast(x[hh][e] - ref[e]) + exp2_fast(x[hh][2 + e] - ref[e]);
+                        l[hh][e] += exp2_fast(x[hh][e] - ref[hh][e]) + exp2_fast(x[hh][2 + e] - ref[hh][e]);
                     else
                         l[hh][e] += p[e] + p[2 + e];
                 }
@@ -616,7 +658,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
         copy_wait<kSlots - 1>();
         __syncwarp();
         if (mask) {
-            const uint32_t vt = ring + slot * S::kTile + from_v;
+            const uint32_t vt = from_v + slot * S::kTile;
 #pragma unroll
             for (int u = 0; u < S::kValSegs; ++u) {
                 uint32_t v[4][4];
@@ -644,11 +686,8 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                     if (kE4m3) {
                         // bytes j, j + 1 of two keys side by side
                         const int w = j >> 2, sel = (j & 2) ? 0x7362 : 0x5140;
-                        const uint32_t low = __byte_perm(v[0][w], v[1][w], sel), high = __byte_perm(v[2][w], v[3][w], sel);
-                        f[0] = f16_of_codes(low, 0);
-                        f[1] = f16_of_codes(low, 1);
-                        f[2] = f16_of_codes(high, 0);
-                        f[3] = f16_of_codes(high, 1);
+                        f16_of_codes(__byte_perm(v[0][w], v[1][w], sel), f[0], f[1]);
+                        f16_of_codes(__byte_perm(v[2][w], v[3][w], sel), f[2], f[3]);
                     } else {
                         const int w = j >> 1;
                         f[0] = __byte_perm(v[0][w], v[1][w], 0x5410);

@@ -127,7 +127,11 @@ moe_status_t moe_paged_attention(const moe_kv_cache_t* c, const moe_attention_t*
     if (!p || p->B < 0 || p->n_heads <= 0 || p->n_heads % c->n_kv_heads != 0 || p->max_pages <= 0 || p->window < 0 ||
         p->table_stride < 0 || !isfinite(p->scale))
         return MOE_ERR_INVALID_ARG;
-    if (p->n_heads > kMaxHeads) return MOE_ERR_UNSUPPORTED;
+    // the kernel's place of a row in a page is a 32-bit byte offset
+    const int64_t elt = c->type == MOE_KV_E4M3 ? 1 : 2, far = int64_t{1} << 32;
+    if (p->n_heads > kMaxHeads || c->page_stride < 0 || c->token_stride < 0 || c->page_stride >= far / elt ||
+        c->token_stride >= far / elt)
+        return MOE_ERR_UNSUPPORTED;
     if (!ws) return MOE_ERR_INVALID_ARG;
     if (!aligned(ws, 256)) return MOE_ERR_MISALIGNED;
     if (ws_bytes < paged_attention_ws_bytes(c->head_dim)) return MOE_ERR_WORKSPACE;
