@@ -479,8 +479,7 @@ moe_status_t moe_dispatch_static(const moe_config_t* cfg, const float* scores_de
 /* A paged key-value cache: stores k and v, [n_pages, page_size, n_kv_heads,
  * head_dim] by shape, with any strides (the same for k and v) whose last one is
  * 1: token-major and head-major pages are both fine.  head_dim is 64, 128 or 256.
- * k and v are 16-byte aligned, their strides multiples of 16 bytes; k_exp and v_exp
- * are 4-byte aligned.
+ * k and v are 16-byte aligned, their strides multiples of 16 bytes.
  * MOE_KV_E4M3: a row's values are e4m3(code) * 2^(byte - 127); the exponent bytes
  * k_exp, v_exp are [n_pages, page_size, n_kv_heads] by shape with strides of their
  * own.  A power of two leaves every stored value exact in bf16 and costs no

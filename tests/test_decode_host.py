@@ -31,8 +31,7 @@ BAD_CACHES = [(dict(k=None), 1), (dict(v=None), 1), (dict(type=2), 1), (dict(n_p
               (dict(n_kv_heads=0), 1), (dict(type=1), 1), (dict(k_exp=FAKE), 1), (dict(type=1, k_exp=FAKE), 1),
               (dict(head_dim=96), 2), (dict(n_kv_heads=5000), 2), (dict(k=FAKE + 8), 3), (dict(v=FAKE + 2), 3),
               (dict(token_stride=132), 3), (dict(page_stride=4), 3), (dict(head_stride=2049), 3),
-              (dict(type=1, k_exp=FAKE, v_exp=FAKE, token_stride=136), 3),
-              (dict(type=1, k_exp=FAKE + 2, v_exp=FAKE), 3)]
+              (dict(type=1, k_exp=FAKE, v_exp=FAKE, token_stride=136), 3)]
 
 
 def _append(**kw):
@@ -85,6 +84,8 @@ def test_attention_refusals(L):
                    (dict(page_table=None), 1), (dict(q=None), 1), (dict(out=None), 1), (dict(q=FAKE + 2), 3),
                    (dict(out=FAKE + 8), 3), (dict(q_token_stride=4), 3), (dict(out_head_stride=100), 3)]:
         assert call(_cache(), att(**kw)) == st, kw
+    for kw in (dict(page_stride=2 ** 31), dict(token_stride=2 ** 31), dict(page_stride=-8), dict(token_stride=-8)):
+        assert call(_cache(**kw), att()) == 2, kw
     assert call(_cache(), att(), ws=None) == 1
     assert call(_cache(), att(), ws=FAKE + 16) == 3
     assert call(_cache(), att(), nb=n - 1) == 4

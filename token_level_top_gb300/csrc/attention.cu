@@ -60,12 +60,12 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
                                           uint32_t b1, bool f16)
 {
     if (f16)
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -80,12 +80,6 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src)
 __device__ __forceinline__ void copy_async_or_zeros(uint32_t dst, const void* src, bool live)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-
-// The first n bytes of the 4 at src (4-byte aligned), zeros behind them.
-__device__ __forceinline__ void copy_async_4(uint32_t dst, const void* src, int n)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -159,21 +153,25 @@ struct Shape {
     static constexpr int kWarps = 4;
     // blocks per SM, as the registers of outputs and queries allow: 128, 168 or 255 a thread
     static constexpr int kCtas = kOut + D / 8 * kCols <= 24 ? 4 : (kOut + D / 8 * kCols <= 48 ? 3 : 2);
-    static constexpr int kTile = 16 * kRow;                   // bytes of a warp's key (or value) tile
-    static constexpr int kGranule = 16 * kWarps;              // keys
+    // 16-key parts of a tile: two where a row is short, so that a pass of the loop does twice the work
+    static constexpr int kParts = kRow <= 128 ? 2 : 1;
+    static constexpr int kPart = 16 * kRow;                   // bytes of 16 keys
+    static constexpr int kTile = kParts * kPart;              // bytes of a warp's key (or value) tile
+    static constexpr int kTileKeys = 16 * kParts;
+    static constexpr int kGranule = kTileKeys * kWarps;       // keys
     static constexpr int kMerge = kWarps * 4 * D * 4;         // the block's join of 4 heads
-    // beside a tile: which of its keys are live, and e4m3 32 exponent words and where their bytes are
-    static constexpr int kMeta = kE4m3 ? 192 : 4, kMask = kE4m3 ? 128 : 0, kByte = 132;
+    // beside a tile: which of its keys are live, and the exponent bytes of its e4m3 keys and values
+    static constexpr int kMask = kE4m3 ? 2 * kTileKeys : 0, kMeta = kMask + 4;
     // as many slots (key or value tiles) as the block's share of 228 KB holds beside the join, at most 16
-    static constexpr int kShare = 233472 / kCtas - 1024 - 256;
+    static constexpr int kShare = 233472 / kCtas - 1024 - 384;
     static constexpr int kRoom = kShare - kMerge - kWarps * 128;
     static constexpr int kFit = (2 * kRoom / kWarps - 2 * kMeta) / (2 * kTile + kMeta);
     static constexpr int kSlots = kFit < 16 ? kFit : 16;
     static constexpr int kMetas = (kSlots + 3) / 2;           // tiles begun and not finished
     static constexpr int kRing = kWarps * kSlots * kTile;
     static constexpr int kSmem = kRing + kMerge + kWarps * (kMetas * kMeta + 128);
-    static_assert(kSlots >= 3 && kSmem <= kShare, "the ring");
-    static constexpr int kCopyRows = kRow >= 128 ? 4 : 2;     // rows that a lane copies from, 16 bytes of each
+    static_assert(kSlots >= 3 && kSmem <= kShare && kWarps * kMetas * kMeta % 8 == 0, "the ring");
+    static constexpr int kCopyRows = kRow >= 128 ? 4 : 2;     // rows of a part that a lane copies from, 16 bytes of each
     static constexpr int kCopySegs = kRow >= 128 ? kRow / 128 : 1;   // ... per 128-byte segment
     static constexpr int kKeySegs = kRow / 64;                // 16-byte pieces of a key row per lane
     static constexpr int kValBytes = kRow / 8 < 16 ? kRow / 8 : 16;
@@ -190,7 +188,7 @@ struct Walk {
     int len, first, n;   // its live keys [first, len) and its granules (per key head and block)
     int g;               // granule within the item
     long long off;       // the item's first granule in the whole list
-    // Tiles start at multiples of 16, so that with pages of 16 k tokens a tile lies in one page.
+    // Tiles start at multiples of 16, so that with pages of 16 k tokens the 16 keys of a part lie in one page.
     __device__ __forceinline__ int base() const { return first & ~15; }
 };
 
@@ -334,42 +332,50 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
     const uint32_t to_v = ring + sub * 128 + (S::kRow >= 128 ? piece ^ (sub >> 1) << 1 : piece ^ sub << 1) * 16;
     const uint32_t from_k = ring + (S::kRow >= 128 ? g * 128 + (c ^ ((g & 1) << 2 | g >> 1)) * 16 : lane * 16);
     const uint32_t from_v = ring + (S::kRow >= 128 ? c * 256 + (g ^ c << 1) * 16 : c * 128 + ((g >> 1) ^ c << 1) * 16 + (g & 1) * 8);
-    const bool one_page = a.page_size % 16 == 0;   // a tile's keys lie in one page
+    const bool one_page = a.page_size % 16 == 0;   // a part's keys lie in one page
     // of the item whose tiles are copied: its table row, this lane's place in a page of its key head (for
     // one_page with the lane's first row), the same in the exponents
     const int32_t* table = nullptr;
     const char *lane_k = nullptr, *lane_v = nullptr;
-    const uint8_t* lane_exp = nullptr;
-    int next_key = 0, next_page = -1, next_at = 0;
-    const char *row_k = nullptr, *row_v = nullptr;   // this lane's first row of the tile whose keys were copied last
-    uint32_t rows_live = 0;                          // and which of its keys live
+    long long lane_exp = 0;
+    int next_key = 0, next_page[S::kParts], next_at[S::kParts];
+    const char* row_v[S::kParts];     // this lane's first row of the parts whose keys were copied last
+    uint32_t rows_live = 0;           // and which of their keys live
     int imeta = 0;
+    // e4m3: the exponent bytes of key `lane` of that tile, stored beside it when the next one is issued
+    uint32_t exp_k = 0, exp_v = 0;
+    unsigned char* exp_to = nullptr;
+    auto store_exponents = [&]() {
+        if (kE4m3 && exp_to && lane < S::kTileKeys) {
+            exp_to[lane] = static_cast<unsigned char>(exp_k);
+            exp_to[S::kTileKeys + lane] = static_cast<unsigned char>(exp_v);
+        }
+        exp_to = nullptr;
+    };
     auto start_item = [&]() {
         table = a.page_table + iw.b * a.table_stride;
-        const long long at = iw.hk * a.head_stride * kElt + (S::kRow >= 128 ? piece : piece & 3) * 16;
+        long long at = iw.hk * a.head_stride * kElt + (S::kRow >= 128 ? piece : piece & 3) * 16;
+        if (one_page) at += row0 * static_cast<long long>(token_bytes);
         lane_k = static_cast<const char*>(a.k) + at;
         lane_v = static_cast<const char*>(a.v) + at;
-        if (one_page) {
-            lane_k += row0 * static_cast<long long>(token_bytes);
-            lane_v += row0 * static_cast<long long>(token_bytes);
-        }
-        if (kE4m3)
-            lane_exp = (lane < 16 ? a.k_exp : a.v_exp) + iw.hk * a.exp_head_stride +
-                       (one_page ? (lane & 15) * a.exp_token_stride : 0);
-        next_key = iw.base() + iw.g * S::kGranule + warp * 16;
+        if (kE4m3) lane_exp = iw.hk * a.exp_head_stride + (one_page ? (lane & 15) * a.exp_token_stride : 0);
+        next_key = iw.base() + iw.g * S::kGranule + warp * S::kTileKeys;
     };
-    // The page of the next tile's first key (one_page) or of its key `lane & 15`, asked for one tile ahead.
+    // The page of the next parts' first key (one_page) or of their key `lane & 15`, asked for one tile ahead.
     auto look_up = [&]() {
-        const int key = one_page ? next_key : next_key + (lane & 15);
-        next_page = -1;
-        if (key < iw.len) {
-            const uint32_t j = static_cast<uint32_t>((static_cast<uint64_t>(static_cast<uint32_t>(key)) * a.page_mul) >> a.page_shift);
-            next_at = key - static_cast<int>(j * static_cast<uint32_t>(a.page_size));
-            next_page = __ldg(table + j);
+#pragma unroll
+        for (int h = 0; h < S::kParts; ++h) {
+            const int key = next_key + 16 * h + (one_page ? 0 : lane & 15);
+            next_page[h] = -1;
+            if (key < iw.len) {
+                const uint32_t j = static_cast<uint32_t>((static_cast<uint64_t>(static_cast<uint32_t>(key)) * a.page_mul) >> a.page_shift);
+                next_at[h] = key - static_cast<int>(j * static_cast<uint32_t>(a.page_size));
+                next_page[h] = __ldg(table + j);
+            }
         }
     };
-    auto copy_tile = [&](uint32_t dst, uint32_t flip, const char* row, const char* idle) {
-        if (one_page && rows_live == 0xffffu) {
+    auto copy_part = [&](uint32_t dst, uint32_t flip, const char* row, uint32_t live, const char* idle) {
+        if (one_page && live == 0xffffu) {
 #pragma unroll
             for (int j = 0; j < S::kCopyRows; ++j) {
                 const char* src = row + static_cast<uint64_t>(token_bytes) * (j * kStep);
@@ -384,7 +390,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                 const char* src = one_page ? row + static_cast<uint64_t>(token_bytes) * (j * kStep)
                                            : reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r)) +
                                                  (S::kRow >= 128 ? piece : piece & 3) * 16;
-                const bool ok = (rows_live >> r) & 1;
+                const bool ok = (live >> r) & 1;
                 src = ok ? src : idle;
 #pragma unroll
                 for (int u = 0; u < S::kCopySegs; ++u)
@@ -392,43 +398,42 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
             }
         }
     };
-    auto issue_keys = [&](int slot) {
-        // keys [first, len) of the tile's 16
-        const int lo_key = max(iw.first - next_key, 0), hi_key = min(max(iw.len - next_key, 0), 16);
-        rows_live = lo_key < hi_key ? (0xffffu >> (16 - hi_key)) & (0xffffu << lo_key) : 0u;
-        const bool ok_page = static_cast<unsigned>(next_page) < static_cast<unsigned>(a.n_pages);
-        if (one_page) {
-            if (!ok_page) {
-                if (rows_live && lane == 0) record_error(a.status, MOE_ERR_INDEX);
-                rows_live = 0;
+    auto issue_keys = [&](uint32_t slot) {
+        // keys [first, len) of the tile
+        const int lo_key = max(iw.first - next_key, 0), hi_key = min(max(iw.len - next_key, 0), S::kTileKeys);
+        rows_live = lo_key < hi_key ? (0xffffffffu >> (32 - hi_key)) & (0xffffffffu << lo_key) : 0u;
+#pragma unroll
+        for (int h = 0; h < S::kParts; ++h) {
+            const bool ok_page = static_cast<unsigned>(next_page[h]) < static_cast<unsigned>(a.n_pages);
+            const uint32_t part = 0xffffu << (16 * h);
+            if (one_page) {
+                if (!ok_page) {
+                    if ((rows_live & part) && lane == 0) record_error(a.status, MOE_ERR_INDEX);
+                    rows_live &= ~part;
+                }
+            } else {
+                const bool mine = (rows_live >> (16 * h + (lane & 15))) & 1;
+                if (mine && !ok_page) record_error(a.status, MOE_ERR_INDEX);
+                rows_live = (rows_live & ~part) | (__ballot_sync(0xffffffffu, mine && ok_page) & 0xffffu) << (16 * h);
             }
-        } else {
-            const bool mine = (rows_live >> (lane & 15)) & 1;
-            if (mine && !ok_page) record_error(a.status, MOE_ERR_INDEX);
-            rows_live = __ballot_sync(0xffffffffu, mine && ok_page) & 0xffffu;
+            long long place = static_cast<uint64_t>(static_cast<uint32_t>(next_page[h])) * page_bytes +
+                              static_cast<uint64_t>(static_cast<uint32_t>(next_at[h])) * token_bytes;
+            if (!one_page) place -= (S::kRow >= 128 ? piece : piece & 3) * 16;   // handed around: without the lane's piece
+            row_v[h] = lane_v + place;
+            copy_part(to_k + slot + h * S::kPart, 32, lane_k + place, rows_live >> (16 * h) & 0xffffu, static_cast<const char*>(a.k));
         }
-        const uint64_t place = static_cast<uint64_t>(static_cast<uint32_t>(next_page)) * page_bytes +
-                               static_cast<uint64_t>(static_cast<uint32_t>(next_at)) * token_bytes;
-        row_k = lane_k + place;
-        row_v = lane_v + place;
-        if (!one_page) {   // the rows are handed around: without the lane's piece
-            row_k -= (S::kRow >= 128 ? piece : piece & 3) * 16;
-            row_v -= (S::kRow >= 128 ? piece : piece & 3) * 16;
-        }
-        copy_tile(to_k + slot * S::kTile, 32, row_k, static_cast<const char*>(a.k));
         unsigned char* const to = meta + imeta * S::kMeta;
         if (kE4m3) {
-            // lanes 0..15 fetch the keys' exponent bytes, 16..31 the values': the byte is the last of the
-            // `n` copied ones of its aligned word, so nothing behind it is read
-            const uint8_t* e = lane < 16 ? a.k_exp : a.v_exp;
-            int n = 0;
-            if ((rows_live >> (lane & 15)) & 1) {
-                e = lane_exp + next_page * a.exp_page_stride + next_at * a.exp_token_stride;
-                n = static_cast<int>(reinterpret_cast<uintptr_t>(e) & 3) + 1;
-                e -= n - 1;
+            const int h = S::kParts == 2 ? lane >> 4 : 0;
+            const int page = S::kParts == 2 && h ? next_page[S::kParts - 1] : next_page[0];
+            const int at = S::kParts == 2 && h ? next_at[S::kParts - 1] : next_at[0];
+            exp_k = exp_v = 127;
+            if (lane < S::kTileKeys && ((rows_live >> lane) & 1)) {
+                const long long e = lane_exp + page * a.exp_page_stride + at * a.exp_token_stride;
+                exp_k = __ldg(a.k_exp + e);
+                exp_v = __ldg(a.v_exp + e);
             }
-            copy_async_4(smem_u32(to) + lane * 4, e, n);
-            to[S::kByte + lane] = static_cast<unsigned char>(n);
+            exp_to = to;
         }
         if (lane == 0) *reinterpret_cast<uint32_t*>(to + S::kMask) = rows_live;
         imeta = imeta + 1 == kMetas ? 0 : imeta + 1;
@@ -439,10 +444,15 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
         }
         look_up();
     };
-    auto issue_values = [&](int slot) { copy_tile(to_v + slot * S::kTile, 64, row_v, static_cast<const char*>(a.v)); };
+    auto issue_values = [&](uint32_t slot) {
+#pragma unroll
+        for (int h = 0; h < S::kParts; ++h)
+            copy_part(to_v + slot + h * S::kPart, 64, row_v[h], rows_live >> (16 * h) & 0xffffu, static_cast<const char*>(a.v));
+    };
     // The run as a sequence of 2 * count tiles (keys, values, keys, ...): number k goes to slot k % kSlots,
     // issued when number k - kSlots has been used.
-    auto issue_number = [&](int k, bool values, int slot) {
+    auto issue_number = [&](int k, bool values, uint32_t slot) {
+        if (!values) store_exponents();
         if (k < 2 * count) {
             if (values)
                 issue_values(slot);
@@ -456,7 +466,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
     start_item();
     look_up();
 #pragma unroll 1
-    for (int k = 0; k < kSlots; ++k) issue_number(k, (k & 1) != 0, k);
+    for (int k = 0; k < kSlots; ++k) issue_number(k, (k & 1) != 0, k * S::kTile);
 
     // ---- the computing side
     uint32_t q[kCols][S::kQ];
@@ -464,7 +474,8 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
     float o[kCols][S::kTiles][4];
     float m[kCols][2], l[kCols][2];   // of the heads 2c and 2c + 1 of the column tile
     float ref[kCols][2], limit[kCols][2];   // what the exponents are taken against, and the score that raises m
-    int slot = 0, cmeta = 0;
+    uint32_t slot = 0;                // byte offset in the ring
+    int cmeta = 0;
     for (int i = 0; i < count; ++i) {
         const int head0 = cw.hk * group + cw.block * kHeads, live_heads = min(kHeads, group - cw.block * kHeads);
         if (i == 0 || cw.g == 0) {    // a new item
@@ -528,21 +539,21 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
             }
         }
 
-        // ---- scores of the tile's keys g, g + 8 for the heads 2c, 2c + 1
+        // ---- scores of the parts' keys g, g + 8 for the heads 2c, 2c + 1
         copy_wait<kSlots - 1>();
         __syncwarp();
-        unsigned char* const me = meta + cmeta * S::kMeta;
-        const uint32_t mask = *reinterpret_cast<const volatile uint32_t*>(me + S::kMask) & 0xffffu;
-        float s[kCols][4];
+        const unsigned char* const me = meta + cmeta * S::kMeta;
+        const uint32_t mask = *reinterpret_cast<const volatile uint32_t*>(me + S::kMask);
+        float x[S::kParts][kCols][4];
 #pragma unroll
-        for (int hh = 0; hh < kCols; ++hh)
+        for (int h = 0; h < S::kParts; ++h) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[hh][j] = 0.0f;
-        if (mask) {
-            const uint32_t kt = from_k + slot * S::kTile;
+            for (int hh = 0; hh < kCols; ++hh)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[h][hh][j] = 0.0f;
 #pragma unroll
             for (int u = 0; u < S::kKeySegs; ++u) {
-                const uint32_t at = S::kRow >= 128 ? (kt ^ (u & 1) * 64) + (u >> 1) * 2048 : kt;
+                const uint32_t at = (S::kRow >= 128 ? ((from_k + slot) ^ (u & 1) * 64) + (u >> 1) * 2048 : from_k + slot) + h * S::kPart;
                 const uint4 v0 = lds128(at), v1 = lds128(at + (S::kRow >= 128 ? 1024 : 512));
                 const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
@@ -560,81 +571,90 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                     const int step = (u * S::kSteps + k) * 2;
 #pragma unroll
                     for (int hh = 0; hh < kCols; ++hh)
-                        mma_16816(s[hh], f[0], f[1], f[2], f[3], q[hh][step], q[hh][step + 1], kE4m3);
+                        mma_16816(x[h][hh], f[0], f[1], f[2], f[3], q[hh][step], q[hh][step + 1], kE4m3);
                 }
             }
         }
         __syncwarp();
         issue_number(2 * i + kSlots, kOdd, slot);
-        slot = slot + 1 == kSlots ? 0 : slot + 1;
+        slot = slot + S::kTile == kSlots * S::kTile ? 0 : slot + S::kTile;
 
-        uint32_t whi[kCols][2], wlo[kCols][2];
-        if (mask) {
-            // scores to log2 units
-            float kscale[2] = {1.0f, 1.0f}, vexp[2] = {0.0f, 0.0f};
-            if (kE4m3) {
-                const uint32_t n = me[S::kByte + lane];
-                const uint32_t word = *reinterpret_cast<const volatile uint32_t*>(me + lane * 4);
-                const uint32_t byte = n ? (word >> (8 * (n - 1))) & 0xffu : 127u;
+        // ---- their weights, scores in log2 units
+        float kscale[S::kParts][2], vexp[S::kParts][2];
+        if (kE4m3) {
+#pragma unroll
+            for (int h = 0; h < S::kParts; ++h)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    kscale[r] = pow2_of_byte(__shfl_sync(0xffffffffu, byte, 8 * r + g));
-                    vexp[r] = static_cast<float>(static_cast<int>(__shfl_sync(0xffffffffu, byte, 16 + 8 * r + g)) - 127);
+                    const int key = 16 * h + 8 * r + g;
+                    kscale[h][r] = pow2_of_byte(*static_cast<const volatile unsigned char*>(me + key));
+                    vexp[h][r] = static_cast<float>(static_cast<int>(*static_cast<const volatile unsigned char*>(me + S::kTileKeys + key)) - 127);
                 }
-            }
-            float x[kCols][4], y[kCols][4];
-            bool grew = false;
+        }
+        cmeta = cmeta + 1 == kMetas ? 0 : cmeta + 1;
+#pragma unroll
+        for (int h = 0; h < S::kParts; ++h)
 #pragma unroll
             for (int hh = 0; hh < kCols; ++hh)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    x[hh][j] = s[hh][j] * qscale[hh][j & 1];
-                    if (kE4m3) x[hh][j] *= kscale[j >> 1];
+                    x[h][hh][j] *= qscale[hh][j & 1];
+                    if (kE4m3) x[h][hh][j] *= kscale[h][j >> 1];
                 }
-            if (mask != 0xffffu) {
-                const bool ok0 = (mask >> g) & 1, ok1 = (mask >> (8 + g)) & 1;
+        if (mask != (S::kParts == 2 ? 0xffffffffu : 0xffffu)) {
+#pragma unroll
+            for (int h = 0; h < S::kParts; ++h) {
+                const bool ok0 = (mask >> (16 * h + g)) & 1, ok1 = (mask >> (16 * h + 8 + g)) & 1;
 #pragma unroll
                 for (int hh = 0; hh < kCols; ++hh)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[hh][j] = (j < 2 ? ok0 : ok1) ? x[hh][j] : -INFINITY;
+                    for (int j = 0; j < 4; ++j) x[h][hh][j] = (j < 2 ? ok0 : ok1) ? x[h][hh][j] : -INFINITY;
             }
+        }
+        auto y = [&](int h, int hh, int j) { return kE4m3 ? x[h][hh][j] + vexp[h][j >> 1] : x[h][hh][j]; };
+        bool grew = false;
+#pragma unroll
+        for (int hh = 0; hh < kCols; ++hh)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float top = fmaxf(y(0, hh, e), y(0, hh, 2 + e));
+                if (S::kParts == 2) top = fmaxf(top, fmaxf(y(S::kParts - 1, hh, e), y(S::kParts - 1, hh, 2 + e)));
+                grew |= top > limit[hh][e];
+            }
+        if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
             for (int hh = 0; hh < kCols; ++hh)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    y[hh][j] = kE4m3 ? x[hh][j] + vexp[j >> 1] : x[hh][j];
-                    grew |= y[hh][j] > limit[hh][j & 1];
-                }
-            if (__any_sync(0xffffffffu, grew)) {
+                for (int e = 0; e < 2; ++e) {
+                    float top = fmaxf(y(0, hh, e), y(0, hh, 2 + e));
+                    if (S::kParts == 2) top = fmaxf(top, fmaxf(y(S::kParts - 1, hh, e), y(S::kParts - 1, hh, 2 + e)));
 #pragma unroll
-                for (int hh = 0; hh < kCols; ++hh)
+                    for (int off = 4; off <= 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                    const float mn = fmaxf(m[hh][e], top);
+                    const float fix = mn > m[hh][e] ? exp2_fast(m[hh][e] - mn) : 1.0f;
+                    m[hh][e] = mn;
+                    limit[hh][e] = mn + kSlack;
+                    ref[hh][e] = mn == -INFINITY ? 0.0f : (kE4m3 ? mn - kShift : mn);
+                    l[hh][e] *= fix;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float top = fmaxf(y[hh][e], y[hh][2 + e]);
-#pragma unroll
-                        for (int off = 4; off <= 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                        const float mn = fmaxf(m[hh][e], top);
-                        const float fix = mn > m[hh][e] ? exp2_fast(m[hh][e] - mn) : 1.0f;
-                        m[hh][e] = mn;
-                        limit[hh][e] = mn + kSlack;
-                        ref[hh][e] = mn == -INFINITY ? 0.0f : (kE4m3 ? mn - kShift : mn);
-                        l[hh][e] *= fix;
-#pragma unroll
-                        for (int t = 0; t < S::kTiles; ++t) {
-                            o[hh][t][e] *= fix;
-                            o[hh][t][2 + e] *= fix;
-                        }
+                    for (int t = 0; t < S::kTiles; ++t) {
+                        o[hh][t][e] *= fix;
+                        o[hh][t][2 + e] *= fix;
                     }
-            }
+                }
+        }
+        uint32_t whi[S::kParts][kCols][2], wlo[S::kParts][kCols][2];
+#pragma unroll
+        for (int h = 0; h < S::kParts; ++h)
 #pragma unroll
             for (int hh = 0; hh < kCols; ++hh) {
                 float p[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) p[j] = exp2_fast(y[hh][j] - ref[hh][j & 1]);
+                for (int j = 0; j < 4; ++j) p[j] = exp2_fast(y(h, hh, j) - ref[hh][j & 1]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if (kE4m3)
-                        l[hh][e] += exp2_fast(x[hh][e] - ref[hh][e]) + exp2_fast(x[hh][2 + e] - ref[hh][e]);
+                        l[hh][e] += exp2_fast(x[h][hh][e] - ref[hh][e]) + exp2_fast(x[h][hh][2 + e] - ref[hh][e]);
                     else
                         l[hh][e] += p[e] + p[2 + e];
                 }
@@ -642,30 +662,28 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                 split_pair<kE4m3>(p[0], p[1], h0, l0);
                 split_pair<kE4m3>(p[2], p[3], h1, l1);
                 if (kHeads == 4) {
-                    whi[hh][0] = transpose_8x8(c < 2 ? h0 : l0);
-                    whi[hh][1] = transpose_8x8(c < 2 ? h1 : l1);
+                    whi[h][hh][0] = transpose_8x8(c < 2 ? h0 : l0);
+                    whi[h][hh][1] = transpose_8x8(c < 2 ? h1 : l1);
                 } else {
-                    whi[hh][0] = transpose_8x8(h0);
-                    whi[hh][1] = transpose_8x8(h1);
-                    wlo[hh][0] = transpose_8x8(l0);
-                    wlo[hh][1] = transpose_8x8(l1);
+                    whi[h][hh][0] = transpose_8x8(h0);
+                    whi[h][hh][1] = transpose_8x8(h1);
+                    wlo[h][hh][0] = transpose_8x8(l0);
+                    wlo[h][hh][1] = transpose_8x8(l1);
                 }
             }
-        }
-        cmeta = cmeta + 1 == kMetas ? 0 : cmeta + 1;
 
         // ---- the weighted values
         copy_wait<kSlots - 1>();
         __syncwarp();
-        if (mask) {
-            const uint32_t vt = from_v + slot * S::kTile;
+#pragma unroll
+        for (int h = 0; h < S::kParts; ++h)
 #pragma unroll
             for (int u = 0; u < S::kValSegs; ++u) {
                 uint32_t v[4][4];
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    const uint32_t at = S::kRow >= 128 ? vt + u * 2048 + (t & 1) * 128 + (t >> 1) * 1024
-                                                       : (vt ^ (t & 1) * 64) + (t >> 1) * 512;
+                    const uint32_t at = (S::kRow >= 128 ? from_v + slot + u * 2048 + (t & 1) * 128 + (t >> 1) * 1024
+                                                        : ((from_v + slot) ^ (t & 1) * 64) + (t >> 1) * 512) + h * S::kPart;
                     if (S::kValBytes == 16) {
                         const uint4 w = lds128(at);
                         v[t][0] = w.x;
@@ -679,7 +697,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                         v[t][2] = v[t][3] = 0;
                     }
                 }
-                // rows g and g + 8 of a tile are the dimensions j and j + 1 of the lane's piece
+                // rows g and g + 8 of an output tile are the dimensions j and j + 1 of the lane's piece
 #pragma unroll
                 for (int j = 0; j < S::kValElts; j += 2) {
                     uint32_t f[4];
@@ -698,23 +716,21 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                     const int t = (u * S::kValElts + j) / 2;
 #pragma unroll
                     for (int hh = 0; hh < kCols; ++hh) {
-                        mma_16816(o[hh][t], f[0], f[1], f[2], f[3], whi[hh][0], whi[hh][1], kE4m3);
-                        if (kHeads != 4) mma_16816(o[hh][t], f[0], f[1], f[2], f[3], wlo[hh][0], wlo[hh][1], kE4m3);
+                        mma_16816(o[hh][t], f[0], f[1], f[2], f[3], whi[h][hh][0], whi[h][hh][1], kE4m3);
+                        if (kHeads != 4) mma_16816(o[hh][t], f[0], f[1], f[2], f[3], wlo[h][hh][0], wlo[h][hh][1], kE4m3);
                     }
                 }
             }
-        }
         __syncwarp();
         issue_number(2 * i + 1 + kSlots, !kOdd, slot);
-        slot = slot + 1 == kSlots ? 0 : slot + 1;
+        slot = slot + S::kTile == kSlots * S::kTile ? 0 : slot + S::kTile;
 
         // ---- the end of an item, or of this block's part of it
         if (cw.g + 1 == cw.n || i + 1 == count) {
-            const long long c0 = cw.off / run, c1 = (cw.off + cw.n - 1) / run;   // the item's blocks
-            const bool whole = c0 == c1;
+            const bool starts = cw.off >= lo, ends = cw.off + cw.n <= hi, whole = starts && ends;
             constexpr int kSlot = 16 * D + 32;                                   // floats per part
             float* const slots = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kAttentionCtrlBytes);
-            float* const part = slots + (2 * static_cast<size_t>(blockIdx.x) + (c0 == blockIdx.x ? 1 : 0)) * kSlot;
+            float* const part = slots + (2 * static_cast<size_t>(blockIdx.x) + (starts ? 1 : 0)) * kSlot;
 #pragma unroll
             for (int hh = 0; hh < kCols; ++hh) {
 #pragma unroll
@@ -786,60 +802,60 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                 }
             }
             if (!whole) {
-                // the last of the item's blocks joins the parts, in the order of the blocks
+                // the last of the item's blocks (first .. first + parts - 1) joins the parts, in their order
                 __threadfence();
                 __syncthreads();
-                const int parts = static_cast<int>(c1 - c0) + 1;
+                const unsigned first = starts ? blockIdx.x : static_cast<unsigned>(cw.off / run);
+                const int parts = static_cast<int>((ends ? blockIdx.x : static_cast<unsigned>((cw.off + cw.n - 1) / run)) - first) + 1;
                 if (threadIdx.x == 0) {
-                    unsigned* counter = reinterpret_cast<unsigned*>(static_cast<char*>(a.ws) + 256) + c0;
+                    unsigned* counter = reinterpret_cast<unsigned*>(static_cast<char*>(a.ws) + 256) + first;
                     s_last = atomicInc(counter, parts - 1) == static_cast<unsigned>(parts - 1);   // back to 0 by itself
                     __threadfence();
                 }
                 __syncthreads();
                 if (s_last) {
+                    const float* base = slots + 2 * static_cast<size_t>(first) * kSlot;
+                    auto slot_of = [&](int k) { return base + (2 * static_cast<size_t>(k) + (k == 0 ? 1 : 0)) * kSlot; };
+                    float2* const s_row = s_ml;   // per head: maximum, 1 / sum
                     for (int r = warp; r < live_heads; r += kWarps) {
-                        const float* base = slots + 2 * static_cast<size_t>(c0) * kSlot;
-                        auto slot = [&](int k) { return base + (2 * static_cast<size_t>(k) + (k == 0 ? 1 : 0)) * kSlot; };
-                        float M = -INFINITY;
-                        for (int k = lane; k < parts; k += 32)
-                            M = fmaxf(M, __ldcg(slot(k) + 16 * D + 2 * r));
+                        float M = -INFINITY, L = 0.0f;
+                        for (int k = lane; k < parts; k += 32) {
+                            const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot_of(k) + 16 * D + 2 * r));
+                            const float mn = fmaxf(M, ml.x), at = mn == -INFINITY ? 0.0f : mn;
+                            L = L * exp2_fast(M - at) + ml.y * exp2_fast(ml.x - at);
+                            M = mn;
+                        }
 #pragma unroll
-                        for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-                        const float ref = M == -INFINITY ? 0.0f : M;
-                        float L = 0.0f;
-                        float4 x[(D + 127) / 128];
-#pragma unroll
-                        for (int e = 0; e < (D + 127) / 128; ++e) x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        for (int off = 16; off >= 1; off >>= 1) {
+                            const float M2 = __shfl_xor_sync(0xffffffffu, M, off), L2 = __shfl_xor_sync(0xffffffffu, L, off);
+                            const float mn = fmaxf(M, M2), at = mn == -INFINITY ? 0.0f : mn;
+                            L = L * exp2_fast(M - at) + L2 * exp2_fast(M2 - at);
+                            M = mn;
+                        }
+                        if (lane == 0) {
+                            s_row[r] = make_float2(M == -INFINITY ? 0.0f : M, L == 0.0f ? 0.0f : 1.0f / L);
+                            if (a.lse)
+                                a.lse[static_cast<long long>(cw.b) * a.n_heads + head0 + r] =
+                                    L == 0.0f ? -INFINITY : ((kE4m3 ? M - kShift : M) + log2f(L)) * kLn2;
+                        }
+                    }
+                    __syncthreads();
+                    for (int at = threadIdx.x; at < live_heads * (D / 4); at += kThreads) {
+                        const int r = at / (D / 4), d = at % (D / 4) * 4;
+                        const float2 row = s_row[r];
+                        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
                         for (int k = 0; k < parts; ++k) {
-                            const float* p = slot(k);
-                            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + 16 * D + 2 * r));
-                            const float f = exp2_fast(ml.x - ref);
-                            L += ml.y * f;
-#pragma unroll
-                            for (int e = 0; e < (D + 127) / 128; ++e) {
-                                const int d = 4 * lane + 128 * e;
-                                if (d < D) {
-                                    const float4 y = __ldcg(reinterpret_cast<const float4*>(p + r * D + d));
-                                    x[e].x += y.x * f;
-                                    x[e].y += y.y * f;
-                                    x[e].z += y.z * f;
-                                    x[e].w += y.w * f;
-                                }
-                            }
+                            const float* p = slot_of(k);
+                            const float f = exp2_fast(__ldcg(p + 16 * D + 2 * r) - row.x);
+                            const float4 y = __ldcg(reinterpret_cast<const float4*>(p + r * D + d));
+                            x.x += y.x * f;
+                            x.y += y.y * f;
+                            x.z += y.z * f;
+                            x.w += y.w * f;
                         }
-                        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-                        const int head = head0 + r;
-#pragma unroll
-                        for (int e = 0; e < (D + 127) / 128; ++e) {
-                            const int d = 4 * lane + 128 * e;
-                            if (d < D)
-                                *reinterpret_cast<uint2*>(a.out + cw.b * a.out_token_stride + head * a.out_head_stride + d) =
-                                    make_uint2(pack_bf16x2(x[e].x * inv, x[e].y * inv), pack_bf16x2(x[e].z * inv, x[e].w * inv));
-                        }
-                        if (lane == 0 && a.lse)
-                            a.lse[static_cast<long long>(cw.b) * a.n_heads + head] =
-                                L == 0.0f ? -INFINITY : ((kE4m3 ? M - kShift : M) + log2f(L)) * kLn2;
+                        *reinterpret_cast<uint2*>(a.out + cw.b * a.out_token_stride + (head0 + r) * a.out_head_stride + d) =
+                            make_uint2(pack_bf16x2(x.x * row.y, x.y * row.y), pack_bf16x2(x.z * row.y, x.w * row.y));
                     }
                 }
             }
