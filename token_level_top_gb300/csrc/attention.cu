@@ -145,6 +145,22 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint3
     }
 }
 
+// *counter == last ? 0 : *counter + 1, and the value before: the block's writes so far (ordered before thread
+// 0's arrival by the block's barrier) are visible to whoever reads after a later arrival.
+__device__ __forceinline__ unsigned count_arrival(unsigned* counter, unsigned last)
+{
+    unsigned old;
+    asm volatile("atom.inc.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(last) : "memory");
+    return old;
+}
+
+// a / b for a >= 0, b > 0: nearly always both fit 32 bits, whose division is far shorter.
+__device__ __forceinline__ long long quotient(long long a, long long b)
+{
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 template <int D, bool kE4m3, int kHeads>
 struct Shape {
     static constexpr int kRow = D * (kE4m3 ? 1 : 2);          // bytes of a row
@@ -158,6 +174,7 @@ struct Shape {
     static constexpr int kPart = 16 * kRow;                   // bytes of 16 keys
     static constexpr int kTile = kParts * kPart;              // bytes of a warp's key (or value) tile
     static constexpr int kTileKeys = 16 * kParts;
+    static constexpr int kAhead = 2;                          // tiles whose pages are looked up in advance
     static constexpr int kGranule = kTileKeys * kWarps;       // keys
     static constexpr int kMerge = kWarps * 4 * D * 4;         // the block's join of 4 heads
     // beside a tile: which of its keys are live, and the exponent bytes of its e4m3 keys and values
@@ -289,7 +306,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
         total += s_scan[i];
     }
     const long long all = total * heads;
-    const long long run = (all + gridDim.x - 1) / gridDim.x;    // granules per block
+    const long long run = quotient(all + gridDim.x - 1, gridDim.x);    // granules per block
     const long long lo = run * blockIdx.x, hi = min(all, lo + run);
     if (lo >= hi) return;
     if (mine > 0 && before * heads <= lo && lo < (before + mine) * heads) {
@@ -302,7 +319,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
             ++w.b;
             load_item<S::kGranule>(a, w);
         }
-        const int h = static_cast<int>((lo - w.off) / w.n);
+        const int h = static_cast<int>(quotient(lo - w.off, w.n));
         w.hk = h / blocks;
         w.block = h - w.hk * blocks;
         w.off += static_cast<long long>(h) * w.n;
@@ -338,7 +355,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
     const int32_t* table = nullptr;
     const char *lane_k = nullptr, *lane_v = nullptr;
     long long lane_exp = 0;
-    int next_key = 0, next_page[S::kParts], next_at[S::kParts];
+    int next_key = 0, ahead_page[S::kAhead][S::kParts];   // of the next tiles of the item
     const char* row_v[S::kParts];     // this lane's first row of the parts whose keys were copied last
     uint32_t rows_live = 0;           // and which of their keys live
     int imeta = 0;
@@ -361,17 +378,16 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
         if (kE4m3) lane_exp = iw.hk * a.exp_head_stride + (one_page ? (lane & 15) * a.exp_token_stride : 0);
         next_key = iw.base() + iw.g * S::kGranule + warp * S::kTileKeys;
     };
-    // The page of the next parts' first key (one_page) or of their key `lane & 15`, asked for one tile ahead.
-    auto look_up = [&]() {
+    // The pages of the first keys of a tile's parts (one_page) or of their keys `lane & 15`, asked for one tile
+    // before the copies (two within an item, where registers allow).
+    auto page_of = [&](int key) {
+        return static_cast<uint32_t>((static_cast<uint64_t>(static_cast<uint32_t>(key)) * a.page_mul) >> a.page_shift);
+    };
+    auto look_up = [&](int tile) {
 #pragma unroll
         for (int h = 0; h < S::kParts; ++h) {
-            const int key = next_key + 16 * h + (one_page ? 0 : lane & 15);
-            next_page[h] = -1;
-            if (key < iw.len) {
-                const uint32_t j = static_cast<uint32_t>((static_cast<uint64_t>(static_cast<uint32_t>(key)) * a.page_mul) >> a.page_shift);
-                next_at[h] = key - static_cast<int>(j * static_cast<uint32_t>(a.page_size));
-                next_page[h] = __ldg(table + j);
-            }
+            const int key = next_key + tile * S::kGranule + 16 * h + (one_page ? 0 : lane & 15);
+            ahead_page[tile][h] = key < iw.len ? __ldg(table + page_of(key)) : -1;
         }
     };
     auto copy_part = [&](uint32_t dst, uint32_t flip, const char* row, uint32_t live, const char* idle) {
@@ -402,8 +418,12 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
         // keys [first, len) of the tile
         const int lo_key = max(iw.first - next_key, 0), hi_key = min(max(iw.len - next_key, 0), S::kTileKeys);
         rows_live = lo_key < hi_key ? (0xffffffffu >> (32 - hi_key)) & (0xffffffffu << lo_key) : 0u;
+        int next_page[S::kParts], next_at[S::kParts];
 #pragma unroll
         for (int h = 0; h < S::kParts; ++h) {
+            const int key = next_key + 16 * h + (one_page ? 0 : lane & 15);
+            next_page[h] = ahead_page[0][h];
+            next_at[h] = key - static_cast<int>(page_of(key) * static_cast<uint32_t>(a.page_size));
             const bool ok_page = static_cast<unsigned>(next_page[h]) < static_cast<unsigned>(a.n_pages);
             const uint32_t part = 0xffffu << (16 * h);
             if (one_page) {
@@ -440,9 +460,17 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
         next_key += S::kGranule;
         if (++iw.g == iw.n) {
             next_item<S::kGranule>(a, iw, blocks);
-            if (iw.n > 0) start_item();
+            if (iw.n > 0) {
+                start_item();
+                look_up(0);
+                if (S::kAhead == 2) look_up(S::kAhead - 1);
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < S::kParts; ++h)
+                if (S::kAhead == 2) ahead_page[0][h] = ahead_page[S::kAhead - 1][h];
+            look_up(S::kAhead - 1);
         }
-        look_up();
     };
     auto issue_values = [&](uint32_t slot) {
 #pragma unroll
@@ -464,12 +492,33 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
     constexpr bool kOdd = (kSlots & 1) != 0;
 
     start_item();
-    look_up();
+    uint32_t q[kCols][S::kQ];
+    // An item's rows of Q as bf16 (e4m3: converted when the item begins): the lane's 16 bytes of each 64 of a key
+    // row (e4m3: 32 bytes of 128).
+    auto load_q = [&](const Walk& w) {
+#pragma unroll
+        for (int hh = 0; hh < kCols; ++hh) {
+            const int h = kHeads == 4 ? g & 3 : hh * 8 + g;
+            const bool ok = h < group - w.block * kHeads;
+            const __nv_bfloat16* src = a.q + w.b * a.q_token_stride + (w.hk * group + w.block * kHeads + h) * a.q_head_stride;
+#pragma unroll
+            for (int u = 0; u < S::kQ / 4; ++u) {
+                const uint4 v = ok ? __ldg(reinterpret_cast<const uint4*>(src + (kE4m3 ? (u >> 1) * 64 + c * 16 + (u & 1) * 8 : u * 32 + c * 8)))
+                                   : make_uint4(0, 0, 0, 0);
+                q[hh][4 * u] = v.x;
+                q[hh][4 * u + 1] = v.y;
+                q[hh][4 * u + 2] = v.z;
+                q[hh][4 * u + 3] = v.w;
+            }
+        }
+    };
+    load_q(cw);
+    look_up(0);
+    if (S::kAhead == 2) look_up(S::kAhead - 1);
 #pragma unroll 1
     for (int k = 0; k < kSlots; ++k) issue_number(k, (k & 1) != 0, k * S::kTile);
 
     // ---- the computing side
-    uint32_t q[kCols][S::kQ];
     float qscale[kCols][2];           // scores in units of log2: accumulator * qscale (* the key's exponent)
     float o[kCols][S::kTiles][4];
     float m[kCols][2], l[kCols][2];   // of the heads 2c and 2c + 1 of the column tile
@@ -481,9 +530,6 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
         if (i == 0 || cw.g == 0) {    // a new item
 #pragma unroll
             for (int hh = 0; hh < kCols; ++hh) {
-                const int h = kHeads == 4 ? g & 3 : hh * 8 + g;
-                const bool ok = h < live_heads;
-                const __nv_bfloat16* src = a.q + cw.b * a.q_token_stride + (head0 + h) * a.q_head_stride;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     m[hh][e] = limit[hh][e] = -INFINITY;
@@ -491,30 +537,15 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                     l[hh][e] = 0.0f;
                     qscale[hh][e] = a.scale * kLog2e;
                 }
-                if (!kE4m3) {
-#pragma unroll
-                    for (int u = 0; u < S::kKeySegs; ++u) {
-                        const uint4 v = ok ? *reinterpret_cast<const uint4*>(src + u * 32 + c * 8) : make_uint4(0, 0, 0, 0);
-                        q[hh][4 * u] = v.x;
-                        q[hh][4 * u + 1] = v.y;
-                        q[hh][4 * u + 2] = v.z;
-                        q[hh][4 * u + 3] = v.w;
-                    }
-                } else {
+                if (kE4m3) {
                     // bf16 to f16 after a power of two that puts the row's largest value near 2^13: values
                     // down to 2^-27 of it stay exact
-                    uint4 v[2 * S::kKeySegs];
                     float top = 0.0f;
 #pragma unroll
-                    for (int u = 0; u < 2 * S::kKeySegs; ++u) {
-                        v[u] = ok ? *reinterpret_cast<const uint4*>(src + (u >> 1) * 64 + c * 16 + (u & 1) * 8) : make_uint4(0, 0, 0, 0);
-                        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float x = fabsf(__uint_as_float(w[j] << 16)), y = fabsf(__uint_as_float(w[j] & 0xffff0000u));
-                            top = fmaxf(top, x < INFINITY ? x : 0.0f);
-                            top = fmaxf(top, y < INFINITY ? y : 0.0f);
-                        }
+                    for (int j = 0; j < S::kQ; ++j) {
+                        const float x = fabsf(__uint_as_float(q[hh][j] << 16)), y = fabsf(__uint_as_float(q[hh][j] & 0xffff0000u));
+                        top = fmaxf(top, x < INFINITY ? x : 0.0f);
+                        top = fmaxf(top, y < INFINITY ? y : 0.0f);
                     }
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -525,12 +556,8 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
 #pragma unroll
                     for (int k = 0; k < 2; ++k) qscale[hh][k] *= __shfl_sync(0xffffffffu, down, (2 * c + k) * 4);
 #pragma unroll
-                    for (int u = 0; u < 2 * S::kKeySegs; ++u) {
-                        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            q[hh][4 * u + j] = pack_f16x2(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xffff0000u) * up);
-                    }
+                    for (int j = 0; j < S::kQ; ++j)
+                        q[hh][j] = pack_f16x2(__uint_as_float(q[hh][j] << 16) * up, __uint_as_float(q[hh][j] & 0xffff0000u) * up);
                 }
 #pragma unroll
                 for (int t = 0; t < S::kTiles; ++t)
@@ -578,6 +605,14 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
         __syncwarp();
         issue_number(2 * i + kSlots, kOdd, slot);
         slot = slot + S::kTile == kSlots * S::kTile ? 0 : slot + S::kTile;
+
+        // Q of the block's next item arrives while this one ends
+        const bool last = cw.g + 1 == cw.n;
+        Walk nw = cw;
+        if (last && i + 1 < count) {
+            next_item<S::kGranule>(a, nw, blocks);
+            load_q(nw);
+        }
 
         // ---- their weights, scores in log2 units
         float kscale[S::kParts][2], vexp[S::kParts][2];
@@ -726,7 +761,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
         slot = slot + S::kTile == kSlots * S::kTile ? 0 : slot + S::kTile;
 
         // ---- the end of an item, or of this block's part of it
-        if (cw.g + 1 == cw.n || i + 1 == count) {
+        if (last || i + 1 == count) {
             const bool starts = cw.off >= lo, ends = cw.off + cw.n <= hi, whole = starts && ends;
             constexpr int kSlot = 16 * D + 32;                                   // floats per part
             float* const slots = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kAttentionCtrlBytes);
@@ -803,14 +838,12 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
             }
             if (!whole) {
                 // the last of the item's blocks (first .. first + parts - 1) joins the parts, in their order
-                __threadfence();
                 __syncthreads();
-                const unsigned first = starts ? blockIdx.x : static_cast<unsigned>(cw.off / run);
-                const int parts = static_cast<int>((ends ? blockIdx.x : static_cast<unsigned>((cw.off + cw.n - 1) / run)) - first) + 1;
+                const unsigned first = starts ? blockIdx.x : static_cast<unsigned>(quotient(cw.off, run));
+                const int parts = static_cast<int>((ends ? blockIdx.x : static_cast<unsigned>(quotient(cw.off + cw.n - 1, run))) - first) + 1;
                 if (threadIdx.x == 0) {
                     unsigned* counter = reinterpret_cast<unsigned*>(static_cast<char*>(a.ws) + 256) + first;
-                    s_last = atomicInc(counter, parts - 1) == static_cast<unsigned>(parts - 1);   // back to 0 by itself
-                    __threadfence();
+                    s_last = count_arrival(counter, parts - 1) == static_cast<unsigned>(parts - 1);   // back to 0 by itself
                 }
                 __syncthreads();
                 if (s_last) {
@@ -844,15 +877,25 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                         const int r = at / (D / 4), d = at % (D / 4) * 4;
                         const float2 row = s_row[r];
                         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-                        for (int k = 0; k < parts; ++k) {
-                            const float* p = slot_of(k);
-                            const float f = exp2_fast(__ldcg(p + 16 * D + 2 * r) - row.x);
-                            const float4 y = __ldcg(reinterpret_cast<const float4*>(p + r * D + d));
-                            x.x += y.x * f;
-                            x.y += y.y * f;
-                            x.z += y.z * f;
-                            x.w += y.w * f;
+                        for (int k0 = 0; k0 < parts; k0 += 8) {   // eight parts' loads at a time
+                            float f[8];
+                            float4 y[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const float* p = slot_of(min(k0 + k, parts - 1));
+                                f[k] = __ldcg(p + 16 * D + 2 * r);
+                                y[k] = __ldcg(reinterpret_cast<const float4*>(p + r * D + d));
+                            }
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const float w = k0 + k < parts ? exp2_fast(f[k] - row.x) : 0.0f;
+                                if (k0 + k < parts) {
+                                    x.x += y[k].x * w;
+                                    x.y += y[k].y * w;
+                                    x.z += y[k].z * w;
+                                    x.w += y[k].w * w;
+                                }
+                            }
                         }
                         *reinterpret_cast<uint2*>(a.out + cw.b * a.out_token_stride + (head0 + r) * a.out_head_stride + d) =
                             make_uint2(pack_bf16x2(x.x * row.y, x.y * row.y), pack_bf16x2(x.z * row.y, x.w * row.y));
@@ -861,7 +904,10 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
             }
             __syncthreads();   // the shared rows are free for the next item
         }
-        if (++cw.g == cw.n) next_item<S::kGranule>(a, cw, blocks);
+        if (last)
+            cw = nw;
+        else
+            ++cw.g;
     }
 }
 
