@@ -591,8 +591,8 @@ moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_attentio
  * MOE_ERR_INDEX and counts as none.  n_top <= MOE_MAX_TOP; past vocab entries are id -1,
  * -inf.  A masked logit (-inf, or the type's lowest value) has probability 0, and
  * logprob -inf where it is -inf; a row of -inf alone has lse -inf, entropy 0.  NaN or
- * +inf makes the row's lse, logprob and entropy NaN, records MOE_ERR_NONFINITE for NaN,
- * and NaN ranks last.  Each output may be NULL (token_dev with logprob_dev; top_*
+ * +inf makes the row's lse, logprob and entropy NaN and records MOE_ERR_NONFINITE; NaN
+ * ranks last.  Each output may be NULL (token_dev with logprob_dev; top_*
  * with n_top = 0).  status_dev: NULL, or the int32 status word. */
 moe_status_t moe_token_logprobs(int64_t rows, int32_t vocab, uint32_t type, const void* logits_dev,
                                 int64_t row_stride, const int32_t* token_dev, int32_t n_top,

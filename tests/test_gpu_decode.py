@@ -528,6 +528,38 @@ def test_logprobs_nan_infinity_and_bad_tokens(bf16):
     assert moe.device_status(status) == 0
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+def test_logprobs_rows_mostly_nan(bf16):
+    """Fewer numbers than alternatives: the NaNs follow, lowest index first; numbers among them rank by value."""
+    dt = torch.bfloat16 if bf16 else torch.float32
+    x = torch.full((3, 9001), float("nan"))
+    x[0, 4000], x[0, 17], x[0, 8999] = 1.0, -float("inf"), 2.0
+    x[1, 9000] = 0.5
+    got = moe.token_logprobs(x.to(dt).cuda(), top=5)
+    want = ref.logprobs(x.numpy().astype(np.float64), None, 5)
+    assert np.array_equal(got["top_ids"].cpu().numpy(), want["top_ids"])
+
+
+@pytest.mark.parametrize("split_rows", [1, 700])
+def test_logprobs_many_values_above_the_threshold(split_rows):
+    """Rows laid out against the threshold: 1500 distinct large values within the reach of a few threads, which
+    leaves the others' maxima far below them; and thousands of ties at the n-th place."""
+    vocab = 60000
+    g = _gen(31)
+    x = torch.randn(2, vocab, generator=g)
+    for piece in range(0, 400):                       # 16-byte pieces of one column of threads
+        x[0, piece * 1024: piece * 1024 + 4] += 50.0 if piece * 1024 + 4 <= vocab else 0.0
+    x[0, 1024 * 3: 1024 * 3 + 2000] += 40.0
+    x[1] = torch.where(torch.rand(vocab, generator=g) < 0.5, torch.tensor(3.0), torch.tensor(2.0))
+    x[1, 59000:59005] = 4.0
+    x = x.repeat_interleave(split_rows, 0)[: 2 * split_rows].cuda()
+    got = moe.token_logprobs(x, top=32)
+    rows = [0, 2 * split_rows - 1]
+    want = ref.logprobs(ref.f64(x[rows]), None, 32)
+    assert np.array_equal(got["top_ids"][rows].cpu().numpy(), want["top_ids"])
+    assert (got["top_ids"][:split_rows] == got["top_ids"][0]).all()
+
+
 def test_logprobs_of_one_row_repeated():
     x, _ = _logits(1, 5003, True, 0, 2)
     token = torch.arange(50, dtype=torch.int32).cuda()

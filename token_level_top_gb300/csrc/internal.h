@@ -328,6 +328,7 @@ struct LogprobArgs {
     int32_t* top_ids;        // or NULL
     float* top_logprobs;
     int* status;
+    int split;               // blocks per row (set by the launcher)
 };
 cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t s);
 struct LogprobGradArgs {
@@ -341,6 +342,7 @@ struct LogprobGradArgs {
     void* dlogits;
     long long drow_stride;
     int* status;
+    int runs;                // blocks per row (set by the launcher)
 };
 cudaError_t launch_token_logprobs_backward(const LogprobGradArgs& a, cudaStream_t s);
 

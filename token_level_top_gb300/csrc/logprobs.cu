@@ -1,156 +1,537 @@
 // logprobs.cu -- log probabilities of given tokens, entropy and the most likely
 // alternatives, read off a row of logits, and their gradient.
 //
-// Forward: one block per row; the row's maximum, then the sums, then n_top
-// rounds that each take the best entry after the one before.
+// Forward.  A row is read once from memory, by one block or, when there are few
+// rows, by a cluster of up to 8 whose parts meet in distributed shared memory.
+// A thread keeps the running maximum m of what it has read and, against it,
+//   l = sum 2^z,  w = sum 2^z z,  z = (x - m) log2 e,
+// so that lse = m + ln l and entropy = ln l - ln 2 * w / l: sums of terms of one
+// sign, whatever the size of the logits.
+// Alternatives: no list is kept while streaming, only the maximum of every few
+// pieces that a thread reads.  From the threads' maxima comes a threshold that at
+// least n values reach; the pieces whose maximum reaches it -- some dozens, still
+// in L2 -- are read again, and the values found are ranked by counting how many
+// exceed each (keys of value and index are distinct, so the ranks are too).
+// Backward: element by element, from lse and entropy.
+//
+// Both are bound by memory where rows are many; the arithmetic per bf16 value
+// (unpack, fma, clamp, ex2, add, fma) fills about half of the issue slots at that
+// rate.
 #include "common.cuh"
 #include "internal.h"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kBatch = 4;          // 16-byte pieces that a thread has in flight
+constexpr int kMaxGroups = 16;     // maxima kept per thread
+constexpr int kMaxFound = 1024;    // values at or above the threshold that are ranked at once
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// exponents below this give 0, and 0 times it is 0 (an infinite one would make NaN)
+constexpr float kFloor = -200.0f;
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// max that keeps NaN
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// Ascending in the value; -0 counts as +0, NaN below everything (0).
+__device__ __forceinline__ uint32_t order_of(float x)
+{
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    if (x != x) return 0u;
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t order)
+{
+    if (order == 0u) return NAN;
+    return __uint_as_float(order & 0x80000000u ? order ^ 0x80000000u : ~order);
+}
+// Distinct keys: larger value first, then lower index.
+__device__ __forceinline__ uint64_t key_of(uint32_t order, int i)
+{
+    return (static_cast<uint64_t>(order) << 32) | static_cast<uint32_t>(~i);
+}
 
 template <class T>
-__device__ __forceinline__ float value(const T* p, long long i)
-{
-    return static_cast<float>(p[i]);
-}
-
-// Orders (value, index) pairs: larger value first, then lower index; NaN last.
-__device__ __forceinline__ uint64_t rank_key(float x, int i)
-{
-    uint32_t b = __float_as_uint(x == 0.0f ? 0.0f : x);
-    b = b & 0x80000000u ? ~b : b | 0x80000000u;
-    if (x != x) b = 0;
-    return (static_cast<uint64_t>(b) << 32) | static_cast<uint32_t>(~i);
-}
-
-__device__ float block_sum(float x, float* s)
-{
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = 0.0f;
-    for (int i = 0; i < kThreads / 32; ++i) x += s[i];
-    __syncthreads();
-    return x;
-}
-
-template <class T>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const LogprobArgs a)
-{
-    __shared__ float s_f[kThreads / 32];
-    __shared__ uint64_t s_k[kThreads / 32];
-    const long long row = blockIdx.x;
-    const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
-    float m = -INFINITY;
-    bool nan = false;
-    for (int i = threadIdx.x; i < a.vocab; i += kThreads) {
-        const float v = value(x, i);
-        nan |= v != v;
-        m = fmaxf(m, v);
+struct Piece;
+template <>
+struct Piece<float> {
+    static constexpr int kN = 4;
+    static __device__ __forceinline__ uint4 nothing() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
+    static __device__ __forceinline__ void unpack(const uint4 v, float (&x)[4])
+    {
+        x[0] = __uint_as_float(v.x);
+        x[1] = __uint_as_float(v.y);
+        x[2] = __uint_as_float(v.z);
+        x[3] = __uint_as_float(v.w);
     }
+    static __device__ __forceinline__ uint4 pack(const float (&x)[4])
+    {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
+    static __device__ __forceinline__ float top(const uint4 v)
+    {
+        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    }
+};
+template <>
+struct Piece<__nv_bfloat16> {
+    static constexpr int kN = 8;
+    static __device__ __forceinline__ uint4 nothing() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
+    static __device__ __forceinline__ void unpack(const uint4 v, float (&x)[8])
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    if ((threadIdx.x & 31) == 0) s_f[threadIdx.x >> 5] = m;
-    nan = __syncthreads_or(nan);
-    for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, s_f[i]);
-    __syncthreads();
-    if (nan && threadIdx.x == 0) record_error(a.status, MOE_ERR_NONFINITE);
-    const float ref = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, w = 0.0f;
-    for (int i = threadIdx.x; i < a.vocab; i += kThreads) {
-        const float z = value(x, i) - ref, e = expf(z);
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&x)[8])
+    {
+        return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    }
+    static __device__ __forceinline__ float top(const uint4 v)
+    {
+        const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
+        const __nv_bfloat162 t = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
+        return fmaxf(__bfloat162float(t.x), __bfloat162float(t.y));
+    }
+};
+
+// A row as whole 16-byte pieces and the few values before and behind them.
+template <class T>
+struct Row {
+    const T* x;          // value 0
+    const uint4* body;   // piece 0
+    int head, pieces;    // values before piece 0; pieces
+    __device__ __forceinline__ Row(const void* logits, long long row_stride, long long row, int vocab)
+    {
+        constexpr int kN = Piece<T>::kN;
+        x = static_cast<const T*>(logits) + row * row_stride;
+        const int off = static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(T) % kN);
+        head = min(off ? kN - off : 0, vocab);
+        body = reinterpret_cast<const uint4*>(x + head);
+        pieces = (vocab - head) / kN;
+    }
+    // the edge value of thread t (fewer than 2 kN of them), or -1
+    __device__ __forceinline__ int edge(int t, int vocab) const
+    {
+        const int i = t < head ? t : head + pieces * Piece<T>::kN + (t - head);
+        return i < vocab ? i : -1;
+    }
+};
+
+// The running statistics of one thread, warp, block or cluster.
+struct Stats {
+    float m, l, w;   // maximum, sum 2^z, sum 2^z z with z = (x - m) log2 e
+    __device__ __forceinline__ void raise(float to)   // to >= m
+    {
+        if (to > m) {
+            const float d = fmaxf((m - to) * kLog2e, -1e20f), f = exp2_fast(d);
+            w = f * (w + d * l);
+            l *= f;
+            m = to;
+        }
+    }
+    __device__ __forceinline__ void join(Stats o)
+    {
+        const float to = fmaxf(m, o.m);
+        raise(to);
+        o.raise(to);
+        l += o.l;
+        w += o.w;
+    }
+    // z = x log2 e - base in one fma, unless the base would overflow (masks of the type's lowest value)
+    __device__ __forceinline__ bool far() const { return fabsf(m) > 2e38f && fabsf(m) < INFINITY; }
+    __device__ __forceinline__ float base() const { return (m == -INFINITY ? 0.0f : m) * kLog2e; }
+    __device__ __forceinline__ void add(float z)
+    {
+        z = max_nan(z, kFloor);
+        const float e = exp2_fast(z);
         l += e;
-        if (e != 0.0f) w += e * z;
+        w = fmaf(e, z, w);
     }
-    l = block_sum(l, s_f);
-    w = block_sum(w, s_f);
-    const bool none = m == -INFINITY && !nan;
-    const float log_l = logf(l);
-    const float lse = ref + log_l;
-    if (threadIdx.x == 0) {
-        if (a.lse) a.lse[row] = lse;
-        if (a.entropy) a.entropy[row] = none ? 0.0f : log_l - w / l;
-        if (a.logprob) {
-            const int t = a.token[row];
-            float lp = 0.0f;
-            if (t >= a.vocab) record_error(a.status, MOE_ERR_INDEX);
-            if (t >= 0 && t < a.vocab) {
-                const float v = value(x, t);
-                lp = none ? -INFINITY : v - ref - log_l;
+    template <int N>
+    __device__ __forceinline__ void add(const float (&x)[N], float base, bool far)
+    {
+        if (!far) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) add(fmaf(x[i], kLog2e, -base));
+        } else {
+            for (int i = 0; i < N; ++i) add((x[i] - m) * kLog2e);
+        }
+    }
+};
+
+struct Shared {
+    Stats stats[kWarps];
+    uint64_t best[MOE_MAX_TOP];     // this block's best keys, in order
+    uint32_t least[kWarps];
+    int entries, found, before[kWarps];
+    uint64_t keys[kMaxFound];
+    uint16_t entry[kMaxGroups * kThreads];
+    float top[kMaxGroups * kThreads];
+};
+
+// The best n keys of the block's share of a row into s.best (0 where there are none), sorted.
+template <class T>
+__device__ void find_best(Shared& s, const Row<T>& row, int vocab, int n, int lo, int hi, int per_group, int groups,
+                          float thread_top, int edge, float edge_value)
+{
+    constexpr int kN = Piece<T>::kN;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    if (t < MOE_MAX_TOP) s.best[t] = 0;
+    if (t == 0) s.entries = s.found = 0;
+    // threshold: with k = ceil(n / full warps), the least of the full warps' k-th largest thread maxima is
+    // reached by at least n values (a warp is full when each of its threads has read something)
+    const int full = min((hi - lo) / 32, kWarps);
+    uint32_t mine = order_of(thread_top), kth = 0xffffffffu;
+    if (warp < full) {
+        for (int k = (n + full - 1) / full; k > 0; --k) {
+            kth = __reduce_max_sync(0xffffffffu, mine);
+            const uint32_t who = __ballot_sync(0xffffffffu, mine == kth);
+            if (lane == __ffs(who) - 1) mine = 0;
+        }
+    }
+    if (lane == 0) s.least[warp] = kth;
+    __syncthreads();
+    uint32_t level = full ? 0xffffffffu : 0u;
+    for (int w = 0; w < full; ++w) level = min(level, s.least[w]);
+    for (int g = 0; g < groups; ++g)
+        if (order_of(s.top[g * kThreads + t]) >= level) s.entry[atomicAdd(&s.entries, 1)] = static_cast<uint16_t>(g * kThreads + t);
+    __syncthreads();
+    const int entries = s.entries;
+    // (one more pass, for the values above the level alone, when those at it are too many to rank)
+    int strict = 0;
+    for (;; ++strict) {
+        auto offer = [&](uint32_t order, int i) {
+            if (order < level || (strict && order == level)) return;
+            const int at = atomicAdd(&s.found, 1);
+            if (at < kMaxFound) s.keys[at] = key_of(order, i);
+        };
+        const int values = per_group * kBatch * kN;   // of an entry
+        for (int e = warp; e < entries; e += kWarps) {
+            const int g = s.entry[e] / kThreads, who = s.entry[e] % kThreads;
+            for (int v = lane; v < values; v += 32) {
+                const int piece = lo + who + kThreads * (g * per_group * kBatch + v / kN);
+                if (piece < hi) {
+                    const int i = row.head + piece * kN + v % kN;
+                    offer(order_of(static_cast<float>(row.x[i])), i);
+                }
             }
-            a.logprob[row] = lp;
         }
+        if (edge >= 0) offer(order_of(edge_value), edge);
+        __syncthreads();
+        if (s.found <= kMaxFound || strict) break;
+        __syncthreads();
+        if (t == 0) s.found = 0;
+        __syncthreads();
     }
-    uint64_t last = ~0ull;
-    for (int n = 0; n < a.n_top; ++n) {
-        uint64_t best = 0;
-        for (int i = threadIdx.x; i < a.vocab; i += kThreads) {
-            const uint64_t k = rank_key(value(x, i), i);
-            if (k < last && k > best) best = k;
+    const int found = s.found;
+    if (found <= kMaxFound) {
+        for (int a = t; a < found; a += kThreads) {
+            const uint64_t key = s.keys[a];
+            int rank = 0;
+            for (int b = 0; b < found; ++b) rank += s.keys[b] > key;
+            if (rank < n) s.best[rank] = key;
         }
+        __syncthreads();
+        // fewer than n: the values at the level when those above it alone were ranked, then (level = that of
+        // -inf) the NaNs, each in the order of their indices
+        int have = found;
+        for (int pass = strict ? 0 : 1; pass < 2 && have < n; ++pass) {
+            const uint32_t want = pass == 0 ? level : 0u;
+            if (pass == 1 && level == 0u) break;   // they were ranked with the rest
+            const int steps = (hi - lo + kThreads - 1) / kThreads;
+            // the edge values before the body, the body, the edge values behind it
+            for (int step = -1; step <= steps && have < n; ++step) {
+                const int piece = lo + step * kThreads + t;
+                const bool side = step < 0 || step == steps;
+                int count = 0;
+                if (side)
+                    count = edge >= 0 && (edge < row.head) == (step < 0) && order_of(edge_value) == want;
+                else if (piece < hi)
+                    for (int j = 0; j < kN; ++j) count += order_of(static_cast<float>(row.x[row.head + piece * kN + j])) == want;
+                int incl = count;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, incl, off);
+                    if (lane >= off) incl += o;
+                }
+                if (lane == 31) s.before[warp] = incl;
+                __syncthreads();
+                int at = have + incl - count;
+                for (int w = 0; w < kWarps; ++w) {
+                    if (w < warp) at += s.before[w];
+                    have += s.before[w];
+                }
+                if (side && count && at < n) s.best[at] = key_of(want, edge);
+                if (!side && count)
+                    for (int j = 0; j < kN && at < n; ++j) {
+                        const int i = row.head + piece * kN + j;
+                        if (order_of(static_cast<float>(row.x[i])) == want) s.best[at++] = key_of(want, i);
+                    }
+                __syncthreads();
+            }
+        }
+        return;
+    }
+    // too many values above a loose threshold (a row laid out against it): n rounds over the share
+    uint64_t last = ~0ull;
+    for (int k = 0; k < n; ++k) {
+        uint64_t best = 0;
+        auto see = [&](float x, int i) {
+            const uint64_t key = key_of(order_of(x), i);
+            if (key < last && key > best) best = key;
+        };
+        for (int p = lo + t; p < hi; p += kThreads)
+            for (int j = 0; j < kN; ++j) see(static_cast<float>(row.x[row.head + p * kN + j]), row.head + p * kN + j);
+        if (edge >= 0) see(edge_value, edge);
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) {
             const uint64_t o = __shfl_xor_sync(0xffffffffu, best, off);
             best = o > best ? o : best;
         }
-        if ((threadIdx.x & 31) == 0) s_k[threadIdx.x >> 5] = best;
+        if (lane == 0) s.keys[warp] = best;
         __syncthreads();
-        for (int i = 0; i < kThreads / 32; ++i) best = s_k[i] > best ? s_k[i] : best;
+        for (int w = 0; w < kWarps; ++w) best = s.keys[w] > best ? s.keys[w] : best;
         __syncthreads();
-        if (threadIdx.x == 0) {
-            const int id = best ? static_cast<int>(~static_cast<uint32_t>(best)) : -1;
-            a.top_ids[row * a.n_top + n] = id;
-            a.top_logprobs[row * a.n_top + n] = id < 0 || none ? -INFINITY : value(x, id) - ref - log_l;
-        }
+        if (t == 0) s.best[k] = best;
         last = best;
     }
+    __syncthreads();
 }
 
-// dx_i = g (1[i = token] - p_i) - h p_i (ln p_i + H).
+template <class T, bool kTop>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) token_logprobs_kernel(const LogprobArgs a)
+{
+    constexpr int kN = Piece<T>::kN;
+    extern __shared__ __align__(16) unsigned char smem[];
+    Shared& s = *reinterpret_cast<Shared*>(smem);
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int rank = static_cast<int>(blockIdx.x) & (a.split - 1);
+    const long long r = blockIdx.x / static_cast<unsigned>(a.split);
+    const Row<T> row(a.logits, a.row_stride, r, a.vocab);
+    // this block's share of the pieces
+    const int share = (row.pieces + a.split - 1) / a.split;
+    const int lo = min(row.pieces, rank * share), hi = min(row.pieces, lo + share);
+    const int batches = (hi - lo + kThreads * kBatch - 1) / (kThreads * kBatch);
+    const int per_group = (batches + kMaxGroups - 1) / kMaxGroups;    // batches under one maximum
+
+    Stats st{-INFINITY, 0.0f, 0.0f};
+    float group_top = -INFINITY;
+    int group = 0, in_group = 0;
+    for (int b = 0; b < batches; ++b) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int p = lo + t + kThreads * (b * kBatch + j);
+            v[j] = p < hi ? __ldg(row.body + p) : Piece<T>::nothing();
+        }
+        float top = fmaxf(fmaxf(Piece<T>::top(v[0]), Piece<T>::top(v[1])), fmaxf(Piece<T>::top(v[2]), Piece<T>::top(v[3])));
+        st.raise(fmaxf(st.m, top));
+        const float base = st.base();
+        const bool far = st.far();
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            float x[kN];
+            Piece<T>::unpack(v[j], x);
+            st.add(x, base, far);
+        }
+        if (kTop) {
+            group_top = fmaxf(group_top, top);
+            if (++in_group == per_group || b + 1 == batches) {
+                s.top[group * kThreads + t] = group_top;
+                group_top = -INFINITY;
+                in_group = 0;
+                ++group;
+            }
+        }
+    }
+    const float thread_top = st.m;
+    // the values beside the whole pieces: rank 0's threads, one each
+    const int edge = rank == 0 ? row.edge(t, a.vocab) : -1;
+    const float edge_value = edge >= 0 ? static_cast<float>(row.x[edge]) : -INFINITY;
+    if (edge >= 0) {
+        st.raise(fmaxf(st.m, edge_value));
+        const float one[1] = {edge_value};
+        st.add(one, st.base(), st.far());
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1)
+        st.join(Stats{__shfl_xor_sync(0xffffffffu, st.m, off), __shfl_xor_sync(0xffffffffu, st.l, off),
+                      __shfl_xor_sync(0xffffffffu, st.w, off)});
+    if (lane == 0) s.stats[warp] = st;
+    if (kTop)
+        find_best<T>(s, row, a.vocab, a.n_top, lo, hi, per_group, group, thread_top, edge, edge_value);
+    if (a.split > 1)
+        cluster_sync_all();
+    else
+        __syncthreads();
+    if (rank == 0) {
+        // the row's statistics, by every warp for itself: lane i has warp i % 8 of block i / 8, then the next four
+        Stats all{-INFINITY, 0.0f, 0.0f};
+        for (int i = lane; i < a.split * kWarps; i += 32) {
+            const uint32_t at = map_to_rank(smem_u32(&s.stats[i % kWarps]), i / kWarps);
+            all.join(Stats{ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)});
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1)
+            all.join(Stats{__shfl_xor_sync(0xffffffffu, all.m, off), __shfl_xor_sync(0xffffffffu, all.l, off),
+                           __shfl_xor_sync(0xffffffffu, all.w, off)});
+        const bool none = all.m == -INFINITY && all.l == 0.0f;      // nothing but -inf
+        const float ref = all.m == -INFINITY ? 0.0f : all.m, log_l = logf(all.l);
+        if (t == 0) {
+            if (all.l != all.l) record_error(a.status, MOE_ERR_NONFINITE);
+            if (a.lse) a.lse[r] = ref + log_l;
+            if (a.entropy) a.entropy[r] = none ? 0.0f : log_l - all.w / all.l * kLn2;
+            if (a.logprob) {
+                const int token = a.token[r];
+                if (token >= a.vocab) record_error(a.status, MOE_ERR_INDEX);
+                float lp = 0.0f;
+                if (token >= 0 && token < a.vocab) lp = none ? -INFINITY : static_cast<float>(row.x[token]) - ref - log_l;
+                a.logprob[r] = lp;
+            }
+        }
+        if (kTop) {
+            // thread (block, k) ranks that block's k-th best key among all
+            const int total = a.split * MOE_MAX_TOP;
+            if (t < total) {
+                const uint32_t mine = map_to_rank(smem_u32(&s.best[t % MOE_MAX_TOP]), t / MOE_MAX_TOP);
+                s.keys[t] = static_cast<uint64_t>(static_cast<uint32_t>(ld_cluster_s32(mine + 4))) << 32 |
+                            static_cast<uint32_t>(ld_cluster_s32(mine));
+            }
+            if (t < a.n_top) {
+                a.top_ids[r * a.n_top + t] = -1;
+                a.top_logprobs[r * a.n_top + t] = -INFINITY;
+            }
+            __syncthreads();
+            if (t < total && s.keys[t]) {
+                const uint64_t key = s.keys[t];
+                int at = 0;
+                if (a.split == 1)
+                    at = t;
+                else
+                    for (int i = 0; i < total; ++i) at += s.keys[i] > key;
+                if (at < a.n_top) {
+                    a.top_ids[r * a.n_top + at] = static_cast<int>(~static_cast<uint32_t>(key));
+                    a.top_logprobs[r * a.n_top + at] = none ? -INFINITY : value_of(static_cast<uint32_t>(key >> 32)) - ref - log_l;
+                }
+            }
+        }
+    }
+    if (a.split > 1) cluster_sync_all();   // a block's shared memory stays until it has been read
+}
+
+// dx_i = g (1[i = token] - p_i) - h p_i (ln p_i + H) = g 1[i = token] - p_i (g + h (z_i + H)), z = x - lse.
+// One block per run of 1024 pieces; dst has the logits' alignment or is written value by value.
 template <class T>
 __global__ void __launch_bounds__(kThreads) token_logprobs_backward_kernel(const LogprobGradArgs a)
 {
-    const long long row = blockIdx.x;
-    const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
-    T* dx = static_cast<T*>(a.dlogits) + row * a.drow_stride;
-    int t = a.token ? a.token[row] : -1;
-    if (t >= a.vocab) {
-        if (threadIdx.x == 0) record_error(a.status, MOE_ERR_INDEX);
-        t = -1;
+    constexpr int kN = Piece<T>::kN;
+    const long long r = blockIdx.x / static_cast<unsigned>(a.runs);
+    const int run = static_cast<int>(blockIdx.x - r * a.runs);
+    const Row<T> row(a.logits, a.row_stride, r, a.vocab);
+    T* dx = static_cast<T*>(a.dlogits) + r * a.drow_stride;
+    const bool vector = (reinterpret_cast<uintptr_t>(dx + row.head) & 15) == 0;
+    uint4 v[kBatch];
+    const int p0 = run * kThreads * kBatch + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+        if (p0 + j * kThreads < row.pieces) v[j] = row.body[p0 + j * kThreads];
+    int token = a.token ? a.token[r] : -1;
+    if (token >= a.vocab) {
+        if (run == 0 && threadIdx.x == 0) record_error(a.status, MOE_ERR_INDEX);
+        token = -1;
     }
-    const float lse = a.lse[row], H = a.entropy ? a.entropy[row] : 0.0f;
-    const float g = t >= 0 && a.dlogprob ? a.dlogprob[row] : 0.0f, h = a.dentropy ? a.dentropy[row] : 0.0f;
+    const float lse = a.lse[r], H = a.entropy ? a.entropy[r] : 0.0f;
     const bool none = lse == -INFINITY;   // nothing live in the row: no probability to move
-    for (int i = threadIdx.x; i < a.vocab; i += kThreads) {
-        const float z = value(x, i) - lse, p = none ? 0.0f : expf(z);
-        float d = -g * p;
-        if (p != 0.0f) d -= h * p * (z + H);
-        if (i == t && !none) d += g;
-        dx[i] = static_cast<T>(d);
+    const float g = token >= 0 && a.dlogprob ? a.dlogprob[r] : 0.0f, h = a.dentropy ? a.dentropy[r] : 0.0f;
+    const float gh = fmaf(h, H, g);
+    auto grad = [&](float x) {
+        const float z = max_nan(x - lse, -1e4f);   // p = 0 below; -inf would make NaN of 0 * z
+        return none ? 0.0f : -exp2_fast(z * kLog2e) * fmaf(h, z, gh);
+    };
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+        const int p = p0 + j * kThreads;
+        if (p >= row.pieces) break;
+        float x[kN];
+        Piece<T>::unpack(v[j], x);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) x[i] = grad(x[i]);
+        const int first = row.head + p * kN;
+        if (token >= first && token < first + kN && !none) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+                if (first + i == token) x[i] += g;
+        }
+        if (vector) {
+            *reinterpret_cast<uint4*>(dx + first) = Piece<T>::pack(x);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) dx[first + i] = static_cast<T>(x[i]);
+        }
+    }
+    if (run == 0) {
+        const int i = row.edge(threadIdx.x, a.vocab);
+        if (i >= 0) {
+            const float x = grad(static_cast<float>(row.x[i]));
+            dx[i] = static_cast<T>(i == token && !none ? x + g : x);
+        }
     }
 }
 
 }  // namespace
 
-cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t s)
+cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t s)
 {
-    if (a.rows <= 0) return cudaSuccess;
-    const unsigned grid = static_cast<unsigned>(a.rows);
-    if (a.bf16)
-        token_logprobs_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(a);
-    else
-        token_logprobs_kernel<float><<<grid, kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    if (args.rows <= 0) return cudaSuccess;
+    LogprobArgs a = args;
+    // few rows: a cluster of blocks per row, while that leaves a block two pieces per thread at least and
+    // the rows' blocks still fit the machine at once
+    const long long pieces = static_cast<long long>(a.vocab) * (a.bf16 ? 2 : 4) / 16;
+    a.split = 1;
+    while (a.split < 8 && a.rows * a.split * 2 <= 4LL * num_sms() && pieces / (a.split * 2) >= 2 * kThreads) a.split *= 2;
+    if (a.rows * a.split > 0x7fffffffLL) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(static_cast<unsigned>(a.rows * a.split));
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = a.n_top > 0 ? sizeof(Shared) : offsetof(Shared, least);
+    c.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(a.split);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    c.attrs = &attr;
+    c.numAttrs = a.split > 1 ? 1 : 0;
+    const auto kernel = a.bf16 ? (a.n_top > 0 ? token_logprobs_kernel<__nv_bfloat16, true> : token_logprobs_kernel<__nv_bfloat16, false>)
+                               : (a.n_top > 0 ? token_logprobs_kernel<float, true> : token_logprobs_kernel<float, false>);
+    return cudaLaunchKernelEx(&c, kernel, a);
 }
 
-cudaError_t launch_token_logprobs_backward(const LogprobGradArgs& a, cudaStream_t s)
+cudaError_t launch_token_logprobs_backward(const LogprobGradArgs& args, cudaStream_t s)
 {
-    if (a.rows <= 0) return cudaSuccess;
-    const unsigned grid = static_cast<unsigned>(a.rows);
+    if (args.rows <= 0) return cudaSuccess;
+    LogprobGradArgs a = args;
+    const long long pieces = static_cast<long long>(a.vocab) * (a.bf16 ? 2 : 4) / 16;
+    a.runs = static_cast<int>((pieces + kThreads * kBatch - 1) / (kThreads * kBatch));
+    if (a.runs < 1) a.runs = 1;
+    if (a.rows * a.runs > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const unsigned grid = static_cast<unsigned>(a.rows * a.runs);
     if (a.bf16)
         token_logprobs_backward_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(a);
     else
