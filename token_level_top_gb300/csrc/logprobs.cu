@@ -25,17 +25,43 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBatch = 4;          // 16-byte pieces that a thread has in flight
-constexpr int kMaxGroups = 16;     // maxima kept per thread
+constexpr int kMaxGroups = 8;      // maxima kept per thread
 constexpr int kMaxFound = 1024;    // values at or above the threshold that are ranked at once
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// exponents below this give 0, and 0 times it is 0 (an infinite one would make NaN)
-constexpr float kFloor = -200.0f;
+// Values are raised to this: their exponentials are 0 all the same, and 0 times them is 0 (-inf would make NaN).
+constexpr float kFloor = -1e30f;
 
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Two fp32 operations in one instruction (fma.rn.f32x2 and add.rn.f32x2: each as the scalar one).
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
+    return p;
+}
+__device__ __forceinline__ float2 unpair(uint64_t p)
+{
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 // max that keeps NaN
@@ -77,6 +103,12 @@ struct Piece<float> {
         x[2] = __uint_as_float(v.z);
         x[3] = __uint_as_float(v.w);
     }
+    // each value raised to kFloor, NaN kept
+    static __device__ __forceinline__ uint4 floored(const uint4 v)
+    {
+        auto f = [](uint32_t w) { return __float_as_uint(max_nan(__uint_as_float(w), kFloor)); };
+        return make_uint4(f(v.x), f(v.y), f(v.z), f(v.w));
+    }
     static __device__ __forceinline__ uint4 pack(const float (&x)[4])
     {
         return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
@@ -98,6 +130,15 @@ struct Piece<__nv_bfloat16> {
             x[2 * i] = __uint_as_float(w[i] << 16);
             x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
+    }
+    static __device__ __forceinline__ uint4 floored(const uint4 v)
+    {
+        const __nv_bfloat162 low = __float2bfloat162_rn(kFloor);
+        auto f = [&](uint32_t w) {
+            const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&w), low);
+            return *reinterpret_cast<const uint32_t*>(&r);
+        };
+        return make_uint4(f(v.x), f(v.y), f(v.z), f(v.w));
     }
     static __device__ __forceinline__ uint4 pack(const float (&x)[8])
     {
@@ -157,34 +198,58 @@ struct Stats {
     // z = x log2 e - base in one fma, unless the base would overflow (masks of the type's lowest value)
     __device__ __forceinline__ bool far() const { return fabsf(m) > 2e38f && fabsf(m) < INFINITY; }
     __device__ __forceinline__ float base() const { return (m == -INFINITY ? 0.0f : m) * kLog2e; }
-    __device__ __forceinline__ void add(float z)
+    // one value, against any maximum
+    __device__ __forceinline__ void add(float x)
     {
-        z = max_nan(z, kFloor);
-        const float e = exp2_fast(z);
+        const float z = max_nan(far() ? (x - m) * kLog2e : fmaf(x, kLog2e, -base()), kFloor), e = exp2_fast(z);
         l += e;
         w = fmaf(e, z, w);
     }
+};
+
+// l and w of a thread as two interleaved sums.
+struct Sums {
+    uint64_t l, w;
     template <int N>
-    __device__ __forceinline__ void add(const float (&x)[N], float base, bool far)
+    __device__ __forceinline__ void add(const float (&x)[N], uint64_t scale, uint64_t minus_base)
     {
-        if (!far) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) add(fmaf(x[i], kLog2e, -base));
-        } else {
-            for (int i = 0; i < N; ++i) add((x[i] - m) * kLog2e);
+        for (int i = 0; i < N; i += 2) {
+            const uint64_t z = fma2(pair(x[i], x[i + 1]), scale, minus_base);
+            const float2 f = unpair(z);
+            const uint64_t e = pair(exp2_fast(f.x), exp2_fast(f.y));
+            l = add2(l, e);
+            w = fma2(e, z, w);
         }
     }
 };
 
+// Kept small: what shared memory leaves of the SM's 256 KB holds the loads in flight (with 33 KB a block the
+// 4096 x 131072 fp32 rows took 377 us instead of TODO).
 struct Shared {
     Stats stats[kWarps];
     uint64_t best[MOE_MAX_TOP];     // this block's best keys, in order
     uint32_t least[kWarps];
     int entries, found, before[kWarps];
-    uint64_t keys[kMaxFound];
     uint16_t entry[kMaxGroups * kThreads];
-    float top[kMaxGroups * kThreads];
+    union {
+        float top[kMaxGroups * kThreads];          // until the entries are listed
+        alignas(16) uint64_t keys[kMaxFound];      // from then on
+    };
 };
+
+// How many of keys[0, count) (16-byte aligned) exceed key.
+__device__ __forceinline__ int rank_in(const uint64_t* keys, int count, uint64_t key)
+{
+    int rank = 0, i = 0;
+#pragma unroll 4
+    for (; i + 2 <= count; i += 2) {
+        const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(keys + i);
+        rank += (k.x > key) + (k.y > key);
+    }
+    if (i < count) rank += keys[i] > key;
+    return rank;
+}
 
 // The best n keys of the block's share of a row into s.best (0 where there are none), sorted.
 template <class T>
@@ -222,15 +287,26 @@ __device__ void find_best(Shared& s, const Row<T>& row, int vocab, int n, int lo
             const int at = atomicAdd(&s.found, 1);
             if (at < kMaxFound) s.keys[at] = key_of(order, i);
         };
-        const int values = per_group * kBatch * kN;   // of an entry
-        for (int e = warp; e < entries; e += kWarps) {
-            const int g = s.entry[e] / kThreads, who = s.entry[e] % kThreads;
-            for (int v = lane; v < values; v += 32) {
-                const int piece = lo + who + kThreads * (g * per_group * kBatch + v / kN);
-                if (piece < hi) {
-                    const int i = row.head + piece * kN + v % kN;
-                    offer(order_of(static_cast<float>(row.x[i])), i);
-                }
+        // the entries' pieces, one per thread and step, two steps' loads in flight
+        const int per_entry = per_group * kBatch, all = entries * per_entry;
+        for (int q0 = t; q0 < all; q0 += 2 * kThreads) {
+            uint4 v[2];
+            int first[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int q = q0 + j * kThreads;
+                const int e = q < all ? s.entry[q / per_entry] : 0;
+                const int piece = lo + e % kThreads + kThreads * (e / kThreads * per_entry + q % per_entry);
+                first[j] = q < all && piece < hi ? row.head + piece * kN : -1;
+                v[j] = first[j] >= 0 ? __ldg(row.body + piece) : Piece<T>::nothing();
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (first[j] < 0 || (level > 0u && order_of(Piece<T>::top(v[j])) < level)) continue;
+                float x[kN];
+                Piece<T>::unpack(v[j], x);
+#pragma unroll
+                for (int i = 0; i < kN; ++i) offer(order_of(x[i]), first[j] + i);
             }
         }
         if (edge >= 0) offer(order_of(edge_value), edge);
@@ -244,8 +320,7 @@ __device__ void find_best(Shared& s, const Row<T>& row, int vocab, int n, int lo
     if (found <= kMaxFound) {
         for (int a = t; a < found; a += kThreads) {
             const uint64_t key = s.keys[a];
-            int rank = 0;
-            for (int b = 0; b < found; ++b) rank += s.keys[b] > key;
+            const int rank = rank_in(s.keys, found, key);
             if (rank < n) s.best[rank] = key;
         }
         __syncthreads();
@@ -331,6 +406,18 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) token_logpro
     const int batches = (hi - lo + kThreads * kBatch - 1) / (kThreads * kBatch);
     const int per_group = (batches + kMaxGroups - 1) / kMaxGroups;    // batches under one maximum
 
+    // asked for early: the given token and its logit
+    int token = -1;
+    float given = 0.0f;
+    if (a.logprob && rank == 0 && t == 0) {
+        token = a.token[r];
+        if (token >= a.vocab) {
+            record_error(a.status, MOE_ERR_INDEX);
+            token = -1;
+        }
+        if (token >= 0) given = static_cast<float>(row.x[token]);
+    }
+
     Stats st{-INFINITY, 0.0f, 0.0f};
     float group_top = -INFINITY;
     int group = 0, in_group = 0;
@@ -343,13 +430,25 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) token_logpro
         }
         float top = fmaxf(fmaxf(Piece<T>::top(v[0]), Piece<T>::top(v[1])), fmaxf(Piece<T>::top(v[2]), Piece<T>::top(v[3])));
         st.raise(fmaxf(st.m, top));
-        const float base = st.base();
-        const bool far = st.far();
+        if (!st.far()) {
+            const uint64_t scale = pair(kLog2e, kLog2e), minus_base = pair(-st.base(), -st.base());
+            Sums sums{pair(st.l, 0.0f), pair(st.w, 0.0f)};
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            float x[kN];
-            Piece<T>::unpack(v[j], x);
-            st.add(x, base, far);
+            for (int j = 0; j < kBatch; ++j) {
+                float x[kN];
+                Piece<T>::unpack(Piece<T>::floored(v[j]), x);
+                sums.add(x, scale, minus_base);
+            }
+            st.l = unpair(sums.l).x + unpair(sums.l).y;
+            st.w = unpair(sums.w).x + unpair(sums.w).y;
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < kBatch; ++j) {
+                float x[kN];
+                Piece<T>::unpack(j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3], x);
+#pragma unroll
+                for (int i = 0; i < kN; ++i) st.add(x[i]);
+            }
         }
         if (kTop) {
             group_top = fmaxf(group_top, top);
@@ -367,8 +466,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) token_logpro
     const float edge_value = edge >= 0 ? static_cast<float>(row.x[edge]) : -INFINITY;
     if (edge >= 0) {
         st.raise(fmaxf(st.m, edge_value));
-        const float one[1] = {edge_value};
-        st.add(one, st.base(), st.far());
+        st.add(edge_value);
     }
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1)
@@ -398,37 +496,28 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) token_logpro
             if (all.l != all.l) record_error(a.status, MOE_ERR_NONFINITE);
             if (a.lse) a.lse[r] = ref + log_l;
             if (a.entropy) a.entropy[r] = none ? 0.0f : log_l - all.w / all.l * kLn2;
-            if (a.logprob) {
-                const int token = a.token[r];
-                if (token >= a.vocab) record_error(a.status, MOE_ERR_INDEX);
-                float lp = 0.0f;
-                if (token >= 0 && token < a.vocab) lp = none ? -INFINITY : static_cast<float>(row.x[token]) - ref - log_l;
-                a.logprob[r] = lp;
-            }
+            if (a.logprob) a.logprob[r] = token < 0 ? 0.0f : (none ? -INFINITY : given - ref - log_l);
         }
         if (kTop) {
-            // thread (block, k) ranks that block's k-th best key among all
-            const int total = a.split * MOE_MAX_TOP;
+            // thread t ranks key t % n of block t / n among all blocks' best
+            const int n = a.n_top, total = a.split * n;
+            uint64_t key = 0;
             if (t < total) {
-                const uint32_t mine = map_to_rank(smem_u32(&s.best[t % MOE_MAX_TOP]), t / MOE_MAX_TOP);
-                s.keys[t] = static_cast<uint64_t>(static_cast<uint32_t>(ld_cluster_s32(mine + 4))) << 32 |
-                            static_cast<uint32_t>(ld_cluster_s32(mine));
+                const uint32_t mine = map_to_rank(smem_u32(&s.best[t % n]), t / n);
+                key = static_cast<uint64_t>(static_cast<uint32_t>(ld_cluster_s32(mine + 4))) << 32 |
+                      static_cast<uint32_t>(ld_cluster_s32(mine));
+                s.keys[t] = key;
             }
-            if (t < a.n_top) {
-                a.top_ids[r * a.n_top + t] = -1;
-                a.top_logprobs[r * a.n_top + t] = -INFINITY;
+            if (t < n && t >= a.vocab) {
+                a.top_ids[r * n + t] = -1;
+                a.top_logprobs[r * n + t] = -INFINITY;
             }
-            __syncthreads();
-            if (t < total && s.keys[t]) {
-                const uint64_t key = s.keys[t];
-                int at = 0;
-                if (a.split == 1)
-                    at = t;
-                else
-                    for (int i = 0; i < total; ++i) at += s.keys[i] > key;
-                if (at < a.n_top) {
-                    a.top_ids[r * a.n_top + at] = static_cast<int>(~static_cast<uint32_t>(key));
-                    a.top_logprobs[r * a.n_top + at] = none ? -INFINITY : value_of(static_cast<uint32_t>(key >> 32)) - ref - log_l;
+            if (a.split > 1) __syncthreads();
+            if (key) {
+                const int at = a.split == 1 ? t : rank_in(s.keys, total, key);
+                if (at < n) {
+                    a.top_ids[r * n + at] = static_cast<int>(~static_cast<uint32_t>(key));
+                    a.top_logprobs[r * n + at] = none ? -INFINITY : value_of(static_cast<uint32_t>(key >> 32)) - ref - log_l;
                 }
             }
         }
