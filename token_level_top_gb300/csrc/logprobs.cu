@@ -38,32 +38,6 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
-// Two fp32 operations in one instruction (fma.rn.f32x2 and add.rn.f32x2: each as the scalar one).
-__device__ __forceinline__ uint64_t pair(float a, float b)
-{
-    uint64_t p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
-    return p;
-}
-__device__ __forceinline__ float2 unpair(uint64_t p)
-{
-    float2 v;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // max that keeps NaN
 __device__ __forceinline__ float max_nan(float a, float b)
 {
@@ -187,13 +161,18 @@ struct Stats {
             m = to;
         }
     }
-    __device__ __forceinline__ void join(Stats o)
+    // The warp's, in every lane: the maximum first, then plain sums.
+    __device__ __forceinline__ void join_warp()
     {
-        const float to = fmaxf(m, o.m);
+        float to = m;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, off));
         raise(to);
-        o.raise(to);
-        l += o.l;
-        w += o.w;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) {
+            l += __shfl_xor_sync(0xffffffffu, l, off);
+            w += __shfl_xor_sync(0xffffffffu, w, off);
+        }
     }
     // z = x log2 e - base in one fma, unless the base would overflow (masks of the type's lowest value)
     __device__ __forceinline__ bool far() const { return fabsf(m) > 2e38f && fabsf(m) < INFINITY; }
@@ -204,23 +183,6 @@ struct Stats {
         const float z = max_nan(far() ? (x - m) * kLog2e : fmaf(x, kLog2e, -base()), kFloor), e = exp2_fast(z);
         l += e;
         w = fmaf(e, z, w);
-    }
-};
-
-// l and w of a thread as two interleaved sums.
-struct Sums {
-    uint64_t l, w;
-    template <int N>
-    __device__ __forceinline__ void add(const float (&x)[N], uint64_t scale, uint64_t minus_base)
-    {
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const uint64_t z = fma2(pair(x[i], x[i + 1]), scale, minus_base);
-            const float2 f = unpair(z);
-            const uint64_t e = pair(exp2_fast(f.x), exp2_fast(f.y));
-            l = add2(l, e);
-            w = fma2(e, z, w);
-        }
     }
 };
 
@@ -238,16 +200,16 @@ struct Shared {
     };
 };
 
-// How many of keys[0, count) (16-byte aligned) exceed key.
-__device__ __forceinline__ int rank_in(const uint64_t* keys, int count, uint64_t key)
+// How many of the pairs part, part + kParts, .. of keys[0, count) (16-byte aligned) exceed key.
+template <int kParts>
+__device__ __forceinline__ int rank_in(const uint64_t* keys, int count, uint64_t key, int part)
 {
-    int rank = 0, i = 0;
-#pragma unroll 4
-    for (; i + 2 <= count; i += 2) {
+    int rank = 0;
+#pragma unroll 8
+    for (int i = 2 * part; i < count; i += 2 * kParts) {
         const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(keys + i);
-        rank += (k.x > key) + (k.y > key);
+        rank += (k.x > key) + (i + 1 < count && k.y > key);
     }
-    if (i < count) rank += keys[i] > key;
     return rank;
 }
 
@@ -275,18 +237,24 @@ __device__ void find_best(Shared& s, const Row<T>& row, int vocab, int n, int lo
     __syncthreads();
     uint32_t level = full ? 0xffffffffu : 0u;
     for (int w = 0; w < full; ++w) level = min(level, s.least[w]);
-    for (int g = 0; g < groups; ++g)
-        if (order_of(s.top[g * kThreads + t]) >= level) s.entry[atomicAdd(&s.entries, 1)] = static_cast<uint16_t>(g * kThreads + t);
+    // compared as values: NaN never reaches the level, unless that is 0 and takes everything
+    const float level_value = value_of(level);
+    const bool any = level == 0u;
+    for (int g = 0; g < groups; ++g) {
+        const uint32_t who = __ballot_sync(0xffffffffu, any || s.top[g * kThreads + t] >= level_value);
+        if (who) {
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&s.entries, __popc(who));
+            at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & lanemask_lt());
+            if ((who >> lane) & 1) s.entry[at] = static_cast<uint16_t>(g * kThreads + t);
+        }
+    }
     __syncthreads();
     const int entries = s.entries;
     // (one more pass, for the values above the level alone, when those at it are too many to rank)
     int strict = 0;
     for (;; ++strict) {
-        auto offer = [&](uint32_t order, int i) {
-            if (order < level || (strict && order == level)) return;
-            const int at = atomicAdd(&s.found, 1);
-            if (at < kMaxFound) s.keys[at] = key_of(order, i);
-        };
+        auto reaches = [&](float x) { return any || (strict ? x > level_value : x >= level_value); };
         // the entries' pieces, one per thread and step, two steps' loads in flight
         const int per_entry = per_group * kBatch, all = entries * per_entry;
         for (int q0 = t; q0 < all; q0 += 2 * kThreads) {
@@ -302,14 +270,22 @@ __device__ void find_best(Shared& s, const Row<T>& row, int vocab, int n, int lo
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                if (first[j] < 0 || (level > 0u && order_of(Piece<T>::top(v[j])) < level)) continue;
+                if (first[j] < 0 || !reaches(Piece<T>::top(v[j]))) continue;
                 float x[kN];
                 Piece<T>::unpack(v[j], x);
+                int count = 0;
 #pragma unroll
-                for (int i = 0; i < kN; ++i) offer(order_of(x[i]), first[j] + i);
+                for (int i = 0; i < kN; ++i) count += reaches(x[i]);
+                int at = atomicAdd(&s.found, count);
+#pragma unroll
+                for (int i = 0; i < kN; ++i)
+                    if (reaches(x[i]) && at++ < kMaxFound) s.keys[at - 1] = key_of(order_of(x[i]), first[j] + i);
             }
         }
-        if (edge >= 0) offer(order_of(edge_value), edge);
+        if (edge >= 0 && reaches(edge_value)) {
+            const int at = atomicAdd(&s.found, 1);
+            if (at < kMaxFound) s.keys[at] = key_of(order_of(edge_value), edge);
+        }
         __syncthreads();
         if (s.found <= kMaxFound || strict) break;
         __syncthreads();
@@ -318,10 +294,14 @@ __device__ void find_best(Shared& s, const Row<T>& row, int vocab, int n, int lo
     }
     const int found = s.found;
     if (found <= kMaxFound) {
-        for (int a = t; a < found; a += kThreads) {
-            const uint64_t key = s.keys[a];
-            const int rank = rank_in(s.keys, found, key);
-            if (rank < n) s.best[rank] = key;
+        // four lanes to a key, each with a quarter of the comparisons
+        for (int a0 = 0; a0 < found; a0 += kThreads / 4) {
+            const int a = a0 + t / 4;
+            const uint64_t key = a < found ? s.keys[a] : ~0ull;
+            int rank = rank_in<4>(s.keys, found, key, t & 3);
+            rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+            rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+            if (a < found && (t & 3) == 0 && rank < n) s.best[rank] = key;
         }
         __syncthreads();
         // fewer than n: the values at the level when those above it alone were ranked, then (level = that of
@@ -431,16 +411,24 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) token_logpro
         float top = fmaxf(fmaxf(Piece<T>::top(v[0]), Piece<T>::top(v[1])), fmaxf(Piece<T>::top(v[2]), Piece<T>::top(v[3])));
         st.raise(fmaxf(st.m, top));
         if (!st.far()) {
-            const uint64_t scale = pair(kLog2e, kLog2e), minus_base = pair(-st.base(), -st.base());
-            Sums sums{pair(st.l, 0.0f), pair(st.w, 0.0f)};
+            const float minus_base = -st.base();
+            float l2 = 0.0f, w2 = 0.0f;   // a second pair of sums halves the chains
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 float x[kN];
                 Piece<T>::unpack(Piece<T>::floored(v[j]), x);
-                sums.add(x, scale, minus_base);
+#pragma unroll
+                for (int i = 0; i < kN; i += 2) {
+                    const float z0 = fmaf(x[i], kLog2e, minus_base), z1 = fmaf(x[i + 1], kLog2e, minus_base);
+                    const float e0 = exp2_fast(z0), e1 = exp2_fast(z1);
+                    st.l += e0;
+                    l2 += e1;
+                    st.w = fmaf(e0, z0, st.w);
+                    w2 = fmaf(e1, z1, w2);
+                }
             }
-            st.l = unpair(sums.l).x + unpair(sums.l).y;
-            st.w = unpair(sums.w).x + unpair(sums.w).y;
+            st.l += l2;
+            st.w += w2;
         } else {
 #pragma unroll 1
             for (int j = 0; j < kBatch; ++j) {
@@ -468,10 +456,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) token_logpro
         st.raise(fmaxf(st.m, edge_value));
         st.add(edge_value);
     }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1)
-        st.join(Stats{__shfl_xor_sync(0xffffffffu, st.m, off), __shfl_xor_sync(0xffffffffu, st.l, off),
-                      __shfl_xor_sync(0xffffffffu, st.w, off)});
+    st.join_warp();
     if (lane == 0) s.stats[warp] = st;
     if (kTop)
         find_best<T>(s, row, a.vocab, a.n_top, lo, hi, per_group, group, thread_top, edge, edge_value);
@@ -479,17 +464,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) token_logpro
         cluster_sync_all();
     else
         __syncthreads();
-    if (rank == 0) {
+    if (rank == 0 && (warp == 0 || a.split > 1)) {   // (without a split the first warp does the rest)
         // the row's statistics, by every warp for itself: lane i has warp i % 8 of block i / 8, then the next four
         Stats all{-INFINITY, 0.0f, 0.0f};
         for (int i = lane; i < a.split * kWarps; i += 32) {
             const uint32_t at = map_to_rank(smem_u32(&s.stats[i % kWarps]), i / kWarps);
-            all.join(Stats{ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)});
+            Stats o{ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)};
+            const float to = fmaxf(all.m, o.m);
+            all.raise(to);
+            o.raise(to);
+            all.l += o.l;
+            all.w += o.w;
         }
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1)
-            all.join(Stats{__shfl_xor_sync(0xffffffffu, all.m, off), __shfl_xor_sync(0xffffffffu, all.l, off),
-                           __shfl_xor_sync(0xffffffffu, all.w, off)});
+        all.join_warp();
         const bool none = all.m == -INFINITY && all.l == 0.0f;      // nothing but -inf
         const float ref = all.m == -INFINITY ? 0.0f : all.m, log_l = logf(all.l);
         if (t == 0) {
@@ -514,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) token_logpro
             }
             if (a.split > 1) __syncthreads();
             if (key) {
-                const int at = a.split == 1 ? t : rank_in(s.keys, total, key);
+                const int at = a.split == 1 ? t : rank_in<1>(s.keys, total, key, 0);
                 if (at < n) {
                     a.top_ids[r * n + at] = static_cast<int>(~static_cast<uint32_t>(key));
                     a.top_logprobs[r * n + at] = none ? -INFINITY : value_of(static_cast<uint32_t>(key >> 32)) - ref - log_l;
