@@ -138,6 +138,16 @@ def test_binding_refusals():
         moe.rope_phase([float("nan")])
 
 
+def test_packed_structures_match_their_fields():
+    """The binding packs a call's structure at once: the same bytes as the ctypes fields give."""
+    a = _append(T=7, n_seqs=9, seq=FAKE + 64, flags=1, q_out_head_stride=77)
+    v = [getattr(a, n) or 0 for n, _ in moe.MoEAppend._fields_]
+    assert moe._APPEND.pack(*v) == bytes(a)
+    t = moe.MoEAttention(3, 4, 5, 6, 0.25, FAKE, FAKE + 1, 8, FAKE + 2, FAKE + 3, FAKE + 4, 9, 10, 11, 12)
+    v = [getattr(t, n) for n, _ in moe.MoEAttention._fields_]
+    assert moe._ATTENTION.pack(*v) == bytes(t)
+
+
 def test_status_strings(L):
     for code, text in moe.STATUS.items():
         assert L.moe_status_string(code).decode() == text

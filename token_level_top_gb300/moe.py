@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -126,7 +127,6 @@ I32 = ctypes.c_int32
 SZ = ctypes.c_size_t
 I64 = ctypes.c_int64
 CFG = ctypes.POINTER(MoEConfig)
-KVC = ctypes.POINTER(MoEKVCache)
 RTR = ctypes.POINTER(MoERouter)
 
 _SIGS = {
@@ -157,10 +157,10 @@ _SIGS = {
     "moe_layer_backward": (I32, [CFG] + [P] * 12 + [SZ, P]),
     "moe_layer_forward_router": (I32, [CFG, P, RTR] + [P] * 15 + [SZ, P]),
     "moe_rope_phase": (I32, [I32, P, P]),
-    "moe_kv_append": (I32, [KVC, ctypes.POINTER(MoEAppend), P, P]),
+    "moe_kv_append": (I32, [P, P, P, P]),
     "moe_paged_attention_workspace_size": (SZ, [I32]),
     "moe_paged_attention_workspace_init": (I32, [P, SZ, P]),
-    "moe_paged_attention": (I32, [KVC, ctypes.POINTER(MoEAttention), P, SZ, P]),
+    "moe_paged_attention": (I32, [P, P, P, SZ, P]),
     "moe_token_logprobs": (I32, [I64, I32, ctypes.c_uint32, P, I64, P, I32] + [P] * 7),
     "moe_token_logprobs_backward": (I32, [I64, I32, ctypes.c_uint32, P, I64] + [P] * 6 + [I64, P, P]),
 }
@@ -498,6 +498,12 @@ LOGITS = {torch.float32: 0, torch.bfloat16: 1}   # MOE_LOGITS_*
 ROTATE_INTERLEAVED = 1             # MOE_ROTATE_INTERLEAVED
 
 
+# A call's structure is packed in one go (the fields of MoEAppend and MoEAttention in their order, padded as C pads
+# them): filling a ctypes structure field by field costs as much as the launch.
+_APPEND = struct.Struct("=5iI3Qq5Q8q")
+_ATTENTION = struct.Struct("=4if4x2Qq3Q4q")
+
+
 def _want(t: torch.Tensor, name: str, dtype, ndim: int):
     """Raises ValueError unless t is a CUDA tensor of this type and rank whose last dimension is contiguous."""
     if t.dtype is not dtype or t.dim() != ndim or not t.is_cuda or (t.stride(-1) != 1 and t.shape[-1] > 1):
@@ -505,16 +511,26 @@ def _want(t: torch.Tensor, name: str, dtype, ndim: int):
                          f"got {tuple(t.shape)} {t.dtype}, strides {t.stride()}, {t.device}")
 
 
-def _rows(t: torch.Tensor, name: str, n: int):
-    """_want for an int32 or fp32 array of n values (int32 unless the name says otherwise)."""
-    _want(t, name, torch.float32 if name in ("lse", "entropy", "dlogprob", "dentropy") else torch.int32, 1)
-    if t.shape[0] != n:
-        raise ValueError(f"{name}: want {n} values, got {t.shape[0]}")
+def _rows(t: torch.Tensor, name: str, n: int, dtype=torch.int32) -> int:
+    """The address of a contiguous CUDA array of n values of this type; ValueError for anything else."""
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or not t.is_cuda or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: want a contiguous CUDA tensor of {n} values, {dtype}; got {tuple(t.shape)} "
+                         f"{t.dtype}, strides {t.stride()}, {t.device}")
+    return t.data_ptr()
 
 
 def _strides(t: torch.Tensor):
     """t's strides, 0 for a dimension of one element (torch leaves those arbitrary)."""
     return [st if n > 1 else 0 for st, n in zip(t.stride(), t.shape)]
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_of(t: torch.Tensor) -> int:
+    """The current stream of t's device, as the handle itself."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def status_word(device="cuda") -> torch.Tensor:
@@ -543,9 +559,10 @@ class KVCache:
             exp = _strides(k_exp)
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
         n, page, heads, dim = k.shape
-        self.c = MoEKVCache(k.data_ptr(), v.data_ptr(), k_exp.data_ptr() if e4m3 else None,
-                            v_exp.data_ptr() if e4m3 else None, KV_E4M3 if e4m3 else KV_BF16, n, page, heads, dim,
-                            *_strides(k)[:3], *exp)
+        self.n_kv_heads, self.head_dim = heads, dim
+        self.c = MoEKVCache(k.data_ptr(), v.data_ptr(), _ptr(k_exp), _ptr(v_exp), KV_E4M3 if e4m3 else KV_BF16, n, page,
+                            heads, dim, *_strides(k)[:3], *exp)
+        self.ref = ctypes.byref(self.c)
 
     @classmethod
     def empty(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, e4m3=False, device="cuda"):
@@ -577,17 +594,14 @@ def kv_append(cache: KVCache, k, v, pos, page_table, q=None, phase=None, seq=Non
     _want(k, "k", torch.bfloat16, 3)
     _want(v, "v", torch.bfloat16, 3)
     _want(page_table, "page_table", torch.int32, 2)
-    T, c = k.shape[0], cache.c
-    _rows(pos, "pos", T)
-    if seq is not None:
-        _rows(seq, "seq", T)
-    if k.shape[1:] != (c.n_kv_heads, c.head_dim) or v.shape != k.shape:
-        raise ValueError(f"k, v: want [T, {c.n_kv_heads}, {c.head_dim}], got {tuple(k.shape)}, {tuple(v.shape)}")
-    heads, qp, qs, op, os_ = 0, None, (0, 0), None, (0, 0)
+    T = k.shape[0]
+    if k.shape[1] != cache.n_kv_heads or k.shape[2] != cache.head_dim or v.shape != k.shape:
+        raise ValueError(f"k, v: want [T, {cache.n_kv_heads}, {cache.head_dim}], got {tuple(k.shape)}, {tuple(v.shape)}")
+    heads, qp, qs, op, os_ = 0, 0, (0, 0), 0, (0, 0)
     if q is not None:
         _want(q, "q", torch.bfloat16, 3)
-        if q.shape[0] != T or q.shape[2] != c.head_dim:
-            raise ValueError(f"q: want [{T}, n_heads, {c.head_dim}], got {tuple(q.shape)}")
+        if q.shape[0] != T or q.shape[2] != cache.head_dim:
+            raise ValueError(f"q: want [{T}, n_heads, {cache.head_dim}], got {tuple(q.shape)}")
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
         else:
@@ -596,14 +610,17 @@ def kv_append(cache: KVCache, k, v, pos, page_table, q=None, phase=None, seq=Non
                 raise ValueError(f"q_out: want {tuple(q.shape)}, got {tuple(q_out.shape)}")
         heads, qp, qs, op, os_ = q.shape[1], q.data_ptr(), _strides(q), q_out.data_ptr(), _strides(q_out)
     ks, vs = _strides(k), _strides(v)
-    rot, pp = 0, None
+    rot, pp = 0, 0
     if phase is not None:
-        _want(phase, "phase", torch.int64, 1)
-        rot, pp = 2 * phase.shape[0], phase.data_ptr()
-    a = MoEAppend(T, page_table.shape[0], page_table.shape[1], heads, rot, ROTATE_INTERLEAVED if interleaved else 0,
-                  pos.data_ptr(), None if seq is None else seq.data_ptr(), page_table.data_ptr(), _strides(page_table)[0],
-                  pp, qp, k.data_ptr(), v.data_ptr(), op, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1])
-    _check(lib().moe_kv_append(ctypes.byref(c), ctypes.byref(a), _p(status), _stream()), "moe_kv_append")
+        rot = 2 * phase.shape[0]
+        pp = _rows(phase, "phase", rot // 2, torch.int64)
+    a = _APPEND.pack(T, page_table.shape[0], page_table.shape[1], heads, rot, ROTATE_INTERLEAVED if interleaved else 0,
+                     _rows(pos, "pos", T), 0 if seq is None else _rows(seq, "seq", T), page_table.data_ptr(),
+                     _strides(page_table)[0], pp, qp, k.data_ptr(), v.data_ptr(), op, qs[0], qs[1], ks[0], ks[1], vs[0],
+                     vs[1], os_[0], os_[1])
+    st = lib().moe_kv_append(cache.ref, a, _ptr(status), _stream_of(k))
+    if st:
+        raise MoEError(st, "moe_kv_append")
     return q_out if q is not None else None
 
 
@@ -624,11 +641,11 @@ def paged_attention(cache: KVCache, ws, q, seq_len, page_table, scale=None, wind
     _want(q, "q", torch.bfloat16, 3)
     _want(page_table, "page_table", torch.int32, 2)
     B, heads, dim = q.shape
-    c = cache.c
-    _rows(seq_len, "seq_len", B)
-    if dim != c.head_dim or page_table.shape[0] != B:
-        raise ValueError(f"q, page_table: want [B, n_heads, {c.head_dim}] and [B, max_pages], got {tuple(q.shape)}, "
+    if dim != cache.head_dim or page_table.shape[0] != B:
+        raise ValueError(f"q, page_table: want [B, n_heads, {cache.head_dim}] and [B, max_pages], got {tuple(q.shape)}, "
                          f"{tuple(page_table.shape)}")
+    if not 0 <= window < 2 ** 31:
+        raise ValueError(f"window: want 0 .. 2^31 - 1, got {window}")
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     else:
@@ -637,13 +654,12 @@ def paged_attention(cache: KVCache, ws, q, seq_len, page_table, scale=None, wind
             raise ValueError(f"out: want {tuple(q.shape)}, got {tuple(out.shape)}")
     lse = torch.empty(B, heads, dtype=torch.float32, device=q.device) if return_lse else None
     qs, os_ = _strides(q), _strides(out)
-    if not 0 <= window < 2 ** 31:
-        raise ValueError(f"window: want 0 .. 2^31 - 1, got {window}")
-    a = MoEAttention(B, heads, page_table.shape[1], window, dim ** -0.5 if scale is None else scale, seq_len.data_ptr(),
-                     page_table.data_ptr(), _strides(page_table)[0], q.data_ptr(), out.data_ptr(),
-                     lse.data_ptr() if return_lse else None, qs[0], qs[1], os_[0], os_[1])
-    _check(lib().moe_paged_attention(ctypes.byref(c), ctypes.byref(a), _p(ws), ws.numel() * ws.element_size(), _stream()),
-           "moe_paged_attention")
+    a = _ATTENTION.pack(B, heads, page_table.shape[1], window, dim ** -0.5 if scale is None else scale,
+                        _rows(seq_len, "seq_len", B), page_table.data_ptr(), _strides(page_table)[0], q.data_ptr(),
+                        out.data_ptr(), lse.data_ptr() if return_lse else 0, qs[0], qs[1], os_[0], os_[1])
+    st = lib().moe_paged_attention(cache.ref, a, ws.data_ptr(), ws.numel() * ws.element_size(), _stream_of(q))
+    if st:
+        raise MoEError(st, "moe_paged_attention")
     return (out, lse) if return_lse else out
 
 
@@ -656,18 +672,17 @@ def token_logprobs(logits, token=None, top=0, status=None):
     _want(logits, "logits", logits.dtype, 2)
     n, v = logits.shape
     dev = logits.device
-    out = dict(lse=torch.empty(n, dtype=torch.float32, device=dev), entropy=torch.empty(n, dtype=torch.float32, device=dev))
-    if token is not None:
-        _rows(token, "token", n)
-        out["logprob"] = torch.empty(n, dtype=torch.float32, device=dev)
+    out = dict(zip(("lse", "entropy", "logprob"), torch.empty(2 if token is None else 3, n, dtype=torch.float32,
+                                                              device=dev).unbind()))
     if top > 0:
         out["top_ids"] = torch.empty(n, top, dtype=torch.int32, device=dev)
         out["top_logprobs"] = torch.empty(n, top, dtype=torch.float32, device=dev)
-    g = out.get
-    st = lib().moe_token_logprobs(n, v, LOGITS[logits.dtype], _p(logits), _strides(logits)[0], _p(token), top,
-                                  _p(g("logprob")), _p(out["entropy"]), _p(out["lse"]), _p(g("top_ids")),
-                                  _p(g("top_logprobs")), _p(status), _stream())
-    _check(st, "moe_token_logprobs")
+    st = lib().moe_token_logprobs(n, v, LOGITS[logits.dtype], logits.data_ptr(), _strides(logits)[0],
+                                  None if token is None else _rows(token, "token", n), top, _ptr(out.get("logprob")),
+                                  out["entropy"].data_ptr(), out["lse"].data_ptr(), _ptr(out.get("top_ids")),
+                                  _ptr(out.get("top_logprobs")), _ptr(status), _stream_of(logits))
+    if st:
+        raise MoEError(st, "moe_token_logprobs")
     return out
 
 
@@ -678,17 +693,20 @@ def token_logprobs_backward(logits, token, lse, entropy=None, dlogprob=None, den
         raise ValueError(f"logits: want float32 or bfloat16, got {logits.dtype}")
     _want(logits, "logits", logits.dtype, 2)
     n, v = logits.shape
-    for t, name in ((token, "token"), (lse, "lse"), (entropy, "entropy"), (dlogprob, "dlogprob"), (dentropy, "dentropy")):
-        if t is not None:
-            _rows(t, name, n)
+    f = torch.float32
     if out is None:
         out = torch.empty(n, v, dtype=logits.dtype, device=logits.device)
     else:
         _want(out, "out", logits.dtype, 2)
         if out.shape != logits.shape:
             raise ValueError(f"out: want {tuple(logits.shape)}, got {tuple(out.shape)}")
-    st = lib().moe_token_logprobs_backward(n, v, LOGITS[logits.dtype], _p(logits), _strides(logits)[0], _p(token), _p(lse),
-                                           _p(entropy), _p(dlogprob), _p(dentropy), _p(out), _strides(out)[0], _p(status),
-                                           _stream())
-    _check(st, "moe_token_logprobs_backward")
+    st = lib().moe_token_logprobs_backward(
+        n, v, LOGITS[logits.dtype], logits.data_ptr(), _strides(logits)[0],
+        None if token is None else _rows(token, "token", n), _rows(lse, "lse", n, f),
+        None if entropy is None else _rows(entropy, "entropy", n, f),
+        None if dlogprob is None else _rows(dlogprob, "dlogprob", n, f),
+        None if dentropy is None else _rows(dentropy, "dentropy", n, f), out.data_ptr(), _strides(out)[0], _ptr(status),
+        _stream_of(logits))
+    if st:
+        raise MoEError(st, "moe_token_logprobs_backward")
     return out
