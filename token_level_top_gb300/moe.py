@@ -521,7 +521,8 @@ def _rows(t: torch.Tensor, name: str, n: int, dtype=torch.int32) -> int:
 
 def _strides(t: torch.Tensor):
     """t's strides, 0 for a dimension of one element (torch leaves those arbitrary)."""
-    return [st if n > 1 else 0 for st, n in zip(t.stride(), t.shape)]
+    strides, shape = t.stride(), t.shape
+    return strides if 1 not in shape else [st if n > 1 else 0 for st, n in zip(strides, shape)]
 
 
 def _ptr(t):
@@ -594,27 +595,31 @@ def kv_append(cache: KVCache, k, v, pos, page_table, q=None, phase=None, seq=Non
     _want(k, "k", torch.bfloat16, 3)
     _want(v, "v", torch.bfloat16, 3)
     _want(page_table, "page_table", torch.int32, 2)
-    T = k.shape[0]
-    if k.shape[1] != cache.n_kv_heads or k.shape[2] != cache.head_dim or v.shape != k.shape:
+    shape = k.shape
+    T, kv_heads, dim = shape
+    if kv_heads != cache.n_kv_heads or dim != cache.head_dim or v.shape != shape:
         raise ValueError(f"k, v: want [T, {cache.n_kv_heads}, {cache.head_dim}], got {tuple(k.shape)}, {tuple(v.shape)}")
     heads, qp, qs, op, os_ = 0, 0, (0, 0), 0, (0, 0)
     if q is not None:
         _want(q, "q", torch.bfloat16, 3)
-        if q.shape[0] != T or q.shape[2] != cache.head_dim:
-            raise ValueError(f"q: want [{T}, n_heads, {cache.head_dim}], got {tuple(q.shape)}")
+        shape = q.shape
+        if shape[0] != T or shape[2] != dim:
+            raise ValueError(f"q: want [{T}, n_heads, {dim}], got {tuple(shape)}")
+        heads = shape[1]
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            q_out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
         else:
             _want(q_out, "q_out", torch.bfloat16, 3)
-            if q_out.shape != q.shape:
-                raise ValueError(f"q_out: want {tuple(q.shape)}, got {tuple(q_out.shape)}")
-        heads, qp, qs, op, os_ = q.shape[1], q.data_ptr(), _strides(q), q_out.data_ptr(), _strides(q_out)
+            if q_out.shape != shape:
+                raise ValueError(f"q_out: want {tuple(shape)}, got {tuple(q_out.shape)}")
+        qp, qs, op, os_ = q.data_ptr(), _strides(q), q_out.data_ptr(), _strides(q_out)
     ks, vs = _strides(k), _strides(v)
     rot, pp = 0, 0
     if phase is not None:
         rot = 2 * phase.shape[0]
         pp = _rows(phase, "phase", rot // 2, torch.int64)
-    a = _APPEND.pack(T, page_table.shape[0], page_table.shape[1], heads, rot, ROTATE_INTERLEAVED if interleaved else 0,
+    n_seqs, max_pages = page_table.shape
+    a = _APPEND.pack(T, n_seqs, max_pages, heads, rot, ROTATE_INTERLEAVED if interleaved else 0,
                      _rows(pos, "pos", T), 0 if seq is None else _rows(seq, "seq", T), page_table.data_ptr(),
                      _strides(page_table)[0], pp, qp, k.data_ptr(), v.data_ptr(), op, qs[0], qs[1], ks[0], ks[1], vs[0],
                      vs[1], os_[0], os_[1])
@@ -640,24 +645,26 @@ def paged_attention(cache: KVCache, ws, q, seq_len, page_table, scale=None, wind
     Returns out [B, n_heads, head_dim] bf16, and lse [B, n_heads] fp32 with return_lse."""
     _want(q, "q", torch.bfloat16, 3)
     _want(page_table, "page_table", torch.int32, 2)
-    B, heads, dim = q.shape
-    if dim != cache.head_dim or page_table.shape[0] != B:
+    shape = q.shape
+    B, heads, dim = shape
+    n_seqs, max_pages = page_table.shape
+    if dim != cache.head_dim or n_seqs != B:
         raise ValueError(f"q, page_table: want [B, n_heads, {cache.head_dim}] and [B, max_pages], got {tuple(q.shape)}, "
                          f"{tuple(page_table.shape)}")
     if not 0 <= window < 2 ** 31:
         raise ValueError(f"window: want 0 .. 2^31 - 1, got {window}")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
     else:
         _want(out, "out", torch.bfloat16, 3)
-        if out.shape != q.shape:
-            raise ValueError(f"out: want {tuple(q.shape)}, got {tuple(out.shape)}")
+        if out.shape != shape:
+            raise ValueError(f"out: want {tuple(shape)}, got {tuple(out.shape)}")
     lse = torch.empty(B, heads, dtype=torch.float32, device=q.device) if return_lse else None
     qs, os_ = _strides(q), _strides(out)
-    a = _ATTENTION.pack(B, heads, page_table.shape[1], window, dim ** -0.5 if scale is None else scale,
+    a = _ATTENTION.pack(B, heads, max_pages, window, dim ** -0.5 if scale is None else scale,
                         _rows(seq_len, "seq_len", B), page_table.data_ptr(), _strides(page_table)[0], q.data_ptr(),
                         out.data_ptr(), lse.data_ptr() if return_lse else 0, qs[0], qs[1], os_[0], os_[1])
-    st = lib().moe_paged_attention(cache.ref, a, ws.data_ptr(), ws.numel() * ws.element_size(), _stream_of(q))
+    st = lib().moe_paged_attention(cache.ref, a, ws.data_ptr(), ws.nbytes, _stream_of(q))
     if st:
         raise MoEError(st, "moe_paged_attention")
     return (out, lse) if return_lse else out
@@ -672,15 +679,19 @@ def token_logprobs(logits, token=None, top=0, status=None):
     _want(logits, "logits", logits.dtype, 2)
     n, v = logits.shape
     dev = logits.device
-    out = dict(zip(("lse", "entropy", "logprob"), torch.empty(2 if token is None else 3, n, dtype=torch.float32,
-                                                              device=dev).unbind()))
+    f, empty = torch.float32, torch.empty   # (one allocation per output: views of a common one cost more)
+    lse, entropy = empty(n, dtype=f, device=dev), empty(n, dtype=f, device=dev)
+    out = dict(lse=lse, entropy=entropy)
+    lp = tp = ids = tops = None
+    if token is not None:
+        out["logprob"] = logprob = empty(n, dtype=f, device=dev)
+        lp, tp = logprob.data_ptr(), _rows(token, "token", n)
     if top > 0:
-        out["top_ids"] = torch.empty(n, top, dtype=torch.int32, device=dev)
-        out["top_logprobs"] = torch.empty(n, top, dtype=torch.float32, device=dev)
-    st = lib().moe_token_logprobs(n, v, LOGITS[logits.dtype], logits.data_ptr(), _strides(logits)[0],
-                                  None if token is None else _rows(token, "token", n), top, _ptr(out.get("logprob")),
-                                  out["entropy"].data_ptr(), out["lse"].data_ptr(), _ptr(out.get("top_ids")),
-                                  _ptr(out.get("top_logprobs")), _ptr(status), _stream_of(logits))
+        out["top_ids"] = ids = empty(n, top, dtype=torch.int32, device=dev)
+        out["top_logprobs"] = tops = empty(n, top, dtype=f, device=dev)
+        ids, tops = ids.data_ptr(), tops.data_ptr()
+    st = lib().moe_token_logprobs(n, v, LOGITS[logits.dtype], logits.data_ptr(), _strides(logits)[0], tp, top, lp,
+                                  entropy.data_ptr(), lse.data_ptr(), ids, tops, _ptr(status), _stream_of(logits))
     if st:
         raise MoEError(st, "moe_token_logprobs")
     return out
