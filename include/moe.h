@@ -503,7 +503,8 @@ typedef struct {
 
 /* New tokens for moe_kv_append.  q, k and v may be views of one projection's
  * output: strides are multiples of 8 elements, pointers 16-byte aligned, the
- * head_dim values of one head contiguous. */
+ * head_dim values of one head contiguous.  A head stride (the cache's too) of 2^30
+ * elements or more is MOE_ERR_UNSUPPORTED. */
 typedef struct {
     int32_t T;                   /* tokens */
     int32_t n_seqs, max_pages;   /* page table [n_seqs, max_pages], rows table_stride apart */

@@ -50,10 +50,12 @@ def test_append_refusals(L):
                    (dict(table_stride=-1), 1), (dict(flags=2), 1), (dict(pos=None), 1), (dict(page_table=None), 1),
                    (dict(k=None), 1), (dict(v=None), 1), (dict(phase=None), 1), (dict(q=None), 1), (dict(q_out=None), 1),
                    (dict(n_heads=0), 1), (dict(T=4), 1), (dict(rot_dim=24), 2), (dict(rot_dim=144), 2),
-                   (dict(rot_dim=-16), 2), (dict(n_heads=1025), 2), (dict(q=FAKE + 8), 3), (dict(k=FAKE + 2), 3),
+                   (dict(rot_dim=-16), 2), (dict(n_heads=1025), 2),
+                   (dict(q_head_stride=2 ** 32), 2), (dict(v_head_stride=-2 ** 33), 2), (dict(q=FAKE + 8), 3), (dict(k=FAKE + 2), 3),
                    (dict(v=FAKE + 8), 3), (dict(q_out=FAKE + 4), 3), (dict(phase=FAKE + 8), 3),
                    (dict(k_token_stride=260), 3), (dict(q_head_stride=129), 3), (dict(q_out_token_stride=4), 3)]:
         assert L.moe_kv_append(R(_cache()), R(_append(**kw)), None, None) == st, kw
+    assert L.moe_kv_append(R(_cache(head_stride=2 ** 31)), R(_append()), None, None) == 2
     assert L.moe_kv_append(None, R(_append()), None, None) == 1
     assert L.moe_kv_append(R(_cache()), None, None, None) == 1
     assert L.moe_kv_append(R(_cache()), R(_append(T=0)), None, None) == 0

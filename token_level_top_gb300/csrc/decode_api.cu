@@ -65,6 +65,8 @@ moe_status_t moe_kv_append(const moe_kv_cache_t* c, const moe_append_t* p, int32
                                p->v_token_stride, p->v_head_stride, p->q_out_token_stride, p->q_out_head_stride};
     for (int64_t s : strides)
         if (s % 8) return MOE_ERR_MISALIGNED;
+    for (int64_t s : {p->q_head_stride, p->k_head_stride, p->v_head_stride, p->q_out_head_stride, 2 * c->head_stride})
+        if (s > INT32_MAX || s < INT32_MIN) return MOE_ERR_UNSUPPORTED;   // the kernel holds them in 32 bits
     if (!aligned(p->q, 16) || !aligned(p->k, 16) || !aligned(p->v, 16) || !aligned(p->q_out, 16) || !aligned(p->phase, 16))
         return MOE_ERR_MISALIGNED;
     AppendArgs a{};
@@ -87,20 +89,20 @@ moe_status_t moe_kv_append(const moe_kv_cache_t* c, const moe_append_t* p, int32
     a.v = static_cast<const __nv_bfloat16*>(p->v);
     a.q_out = static_cast<__nv_bfloat16*>(p->q_out);
     a.q_token_stride = p->q_token_stride;
-    a.q_head_stride = p->q_head_stride;
     a.k_token_stride = p->k_token_stride;
-    a.k_head_stride = p->k_head_stride;
     a.v_token_stride = p->v_token_stride;
-    a.v_head_stride = p->v_head_stride;
     a.q_out_token_stride = p->q_out_token_stride;
-    a.q_out_head_stride = p->q_out_head_stride;
+    a.q_head = static_cast<int>(p->q_head_stride);
+    a.k_head = static_cast<int>(p->k_head_stride);
+    a.v_head = static_cast<int>(p->v_head_stride);
+    a.q_out_head = static_cast<int>(p->q_out_head_stride);
+    a.cache_head = static_cast<int>(c->head_stride * (c->type == MOE_KV_E4M3 ? 1 : 2));
     a.cache_k = c->k;
     a.cache_v = c->v;
     a.k_exp = static_cast<uint8_t*>(c->k_exp);
     a.v_exp = static_cast<uint8_t*>(c->v_exp);
     a.page_stride = c->page_stride;
     a.token_stride = c->token_stride;
-    a.head_stride = c->head_stride;
     a.exp_page_stride = c->exp_page_stride;
     a.exp_token_stride = c->exp_token_stride;
     a.exp_head_stride = c->exp_head_stride;

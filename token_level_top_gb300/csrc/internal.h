@@ -280,13 +280,13 @@ struct AppendArgs {
     const uint64_t* phase;       // [rot_dim / 2], 2^-64 turns per position
     const __nv_bfloat16 *q, *k, *v;
     __nv_bfloat16* q_out;
-    long long q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride;
-    long long q_out_token_stride, q_out_head_stride;
+    long long q_token_stride, k_token_stride, v_token_stride, q_out_token_stride;
     void *cache_k, *cache_v;
     uint8_t *k_exp, *v_exp;      // e4m3 cache only
-    long long page_stride, token_stride, head_stride;
+    long long page_stride, token_stride;
     long long exp_page_stride, exp_token_stride, exp_head_stride;
     int* status;
+    int q_head, k_head, v_head, q_out_head, cache_head;   // head strides (the cache's in bytes)
     int parts;                   // warps per token (set by the launcher)
 };
 cudaError_t launch_kv_append(AppendArgs a, int head_dim, bool e4m3, cudaStream_t s);
