@@ -204,8 +204,9 @@ def test_append_e4m3_special_rows():
     v = v.to(torch.bfloat16).cuda()
     cache = moe.KVCache.empty(1, 8, 1, D, e4m3=True)
     pos = torch.arange(6, dtype=torch.int32).cuda()
-    moe.kv_append(cache, v, v, pos, torch.zeros(1, 1, dtype=torch.int32).cuda(),
-                  seq=torch.zeros(6, dtype=torch.int32).cuda())
+    q = moe.kv_append(cache, v, v, pos, torch.zeros(1, 1, dtype=torch.int32).cuda(), q=v,
+                      seq=torch.zeros(6, dtype=torch.int32).cuda())
+    assert ((q == v) | (q.isnan() & v.isnan())).all(), "rows of q keep their infinities"
     exp = cache.v_exp.cpu()[0, :6, 0].tolist()
     val = ref.e4m3_value(cache.v.cpu()[0, :6, 0], cache.v_exp.cpu()[0, :6, 0])
     want = ref.f64(v[:, 0])

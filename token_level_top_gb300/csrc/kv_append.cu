@@ -195,11 +195,11 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a)
         const bool stored = live && !is_q && place >= 0;
         if (kE4m3) {
             float amax = row_max<kLanes>(x0, x1);
-            if (__any_sync(0xffffffffu, amax == INFINITY)) {   // infinities are stored as NaN and do not count
+            if (__any_sync(0xffffffffu, !is_q && amax == INFINITY)) {   // infinities are stored as NaN and do not count
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    x0.x[i] = fabsf(x0.x[i]) < INFINITY ? x0.x[i] : NAN;
-                    x1.x[i] = fabsf(x1.x[i]) < INFINITY ? x1.x[i] : NAN;
+                    x0.x[i] = is_q || fabsf(x0.x[i]) < INFINITY ? x0.x[i] : NAN;
+                    x1.x[i] = is_q || fabsf(x1.x[i]) < INFINITY ? x1.x[i] : NAN;
                 }
                 amax = row_max<kLanes>(x0, x1);
             }

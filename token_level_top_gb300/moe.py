@@ -592,38 +592,48 @@ def kv_append(cache: KVCache, k, v, pos, page_table, q=None, phase=None, seq=Non
     (None: token t belongs to row t of page_table [n_seqs, max_pages]) int32; phase from rope_phase on the device
     (None: no rotation).  Returns the rotated q (q_out when given, which may be q), or None without q.  status: a
     status_word or workspace that records indices out of range."""
-    _want(k, "k", torch.bfloat16, 3)
-    _want(v, "v", torch.bfloat16, 3)
-    _want(page_table, "page_table", torch.int32, 2)
+    ks, vs, ts = k.stride(), v.stride(), page_table.stride()
+    for t, strides, name in ((k, ks, "k"), (v, vs, "v")):
+        if len(strides) != 3 or strides[2] != 1 or t.dtype is not torch.bfloat16 or not t.is_cuda:
+            _want(t, name, torch.bfloat16, 3)
+    if len(ts) != 2 or ts[1] != 1 or page_table.dtype is not torch.int32 or not page_table.is_cuda:
+        _want(page_table, "page_table", torch.int32, 2)
     shape = k.shape
     T, kv_heads, dim = shape
     if kv_heads != cache.n_kv_heads or dim != cache.head_dim or v.shape != shape:
         raise ValueError(f"k, v: want [T, {cache.n_kv_heads}, {cache.head_dim}], got {tuple(k.shape)}, {tuple(v.shape)}")
     heads, qp, qs, op, os_ = 0, 0, (0, 0), 0, (0, 0)
     if q is not None:
-        _want(q, "q", torch.bfloat16, 3)
+        qs = q.stride()
+        if len(qs) != 3 or qs[2] != 1 or q.dtype is not torch.bfloat16 or not q.is_cuda:
+            _want(q, "q", torch.bfloat16, 3)
         shape = q.shape
+        heads = shape[1]
         if shape[0] != T or shape[2] != dim:
             raise ValueError(f"q: want [{T}, n_heads, {dim}], got {tuple(shape)}")
-        heads = shape[1]
         if q_out is None:
             q_out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+            os_ = (heads * dim, dim)
         else:
             _want(q_out, "q_out", torch.bfloat16, 3)
             if q_out.shape != shape:
                 raise ValueError(f"q_out: want {tuple(shape)}, got {tuple(q_out.shape)}")
-        qp, qs, op, os_ = q.data_ptr(), _strides(q), q_out.data_ptr(), _strides(q_out)
-    ks, vs = _strides(k), _strides(v)
+            os_ = _strides(q_out)
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    if T == 1 or heads == 1 or kv_heads == 1:
+        ks, vs = _strides(k), _strides(v)
+        if q is not None:
+            qs = _strides(q)
     rot, pp = 0, 0
     if phase is not None:
         rot = 2 * phase.shape[0]
         pp = _rows(phase, "phase", rot // 2, torch.int64)
     n_seqs, max_pages = page_table.shape
-    a = _APPEND.pack(T, n_seqs, max_pages, heads, rot, ROTATE_INTERLEAVED if interleaved else 0,
-                     _rows(pos, "pos", T), 0 if seq is None else _rows(seq, "seq", T), page_table.data_ptr(),
-                     _strides(page_table)[0], pp, qp, k.data_ptr(), v.data_ptr(), op, qs[0], qs[1], ks[0], ks[1], vs[0],
-                     vs[1], os_[0], os_[1])
-    st = lib().moe_kv_append(cache.ref, a, _ptr(status), _stream_of(k))
+    a = _APPEND.pack(T, n_seqs, max_pages, heads, rot, ROTATE_INTERLEAVED if interleaved else 0, _rows(pos, "pos", T),
+                     0 if seq is None else _rows(seq, "seq", T), page_table.data_ptr(), ts[0] if n_seqs > 1 else 0, pp, qp,
+                     k.data_ptr(), v.data_ptr(), op, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1])
+    st = (_lib or lib()).moe_kv_append(cache.ref, a, None if status is None else status.data_ptr(),
+                                       torch._C._cuda_getCurrentRawStream(k.device.index))
     if st:
         raise MoEError(st, "moe_kv_append")
     return q_out if q is not None else None
@@ -643,8 +653,11 @@ def paged_attention(cache: KVCache, ws, q, seq_len, page_table, scale=None, wind
     """Attention of one new token per sequence over the cache (moe_paged_attention): q [B, n_heads, head_dim] bf16,
     seq_len [B] and page_table [B, max_pages] int32, scale (None: head_dim ** -0.5), window (0: all cached tokens).
     Returns out [B, n_heads, head_dim] bf16, and lse [B, n_heads] fp32 with return_lse."""
-    _want(q, "q", torch.bfloat16, 3)
-    _want(page_table, "page_table", torch.int32, 2)
+    qs, ts = q.stride(), page_table.stride()
+    if len(qs) != 3 or qs[2] != 1 or q.dtype is not torch.bfloat16 or not q.is_cuda:
+        _want(q, "q", torch.bfloat16, 3)
+    if len(ts) != 2 or ts[1] != 1 or page_table.dtype is not torch.int32 or not page_table.is_cuda:
+        _want(page_table, "page_table", torch.int32, 2)
     shape = q.shape
     B, heads, dim = shape
     n_seqs, max_pages = page_table.shape
@@ -653,18 +666,23 @@ def paged_attention(cache: KVCache, ws, q, seq_len, page_table, scale=None, wind
                          f"{tuple(page_table.shape)}")
     if not 0 <= window < 2 ** 31:
         raise ValueError(f"window: want 0 .. 2^31 - 1, got {window}")
+    dev = q.device
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        os_ = (heads * dim, dim)
     else:
         _want(out, "out", torch.bfloat16, 3)
         if out.shape != shape:
             raise ValueError(f"out: want {tuple(shape)}, got {tuple(out.shape)}")
-    lse = torch.empty(B, heads, dtype=torch.float32, device=q.device) if return_lse else None
-    qs, os_ = _strides(q), _strides(out)
+        os_ = _strides(out)
+    lse = torch.empty(B, heads, dtype=torch.float32, device=dev) if return_lse else None
+    if B == 1 or heads == 1:
+        qs = _strides(q)
     a = _ATTENTION.pack(B, heads, max_pages, window, dim ** -0.5 if scale is None else scale,
-                        _rows(seq_len, "seq_len", B), page_table.data_ptr(), _strides(page_table)[0], q.data_ptr(),
+                        _rows(seq_len, "seq_len", B), page_table.data_ptr(), ts[0] if B > 1 else 0, q.data_ptr(),
                         out.data_ptr(), lse.data_ptr() if return_lse else 0, qs[0], qs[1], os_[0], os_[1])
-    st = lib().moe_paged_attention(cache.ref, a, ws.data_ptr(), ws.nbytes, _stream_of(q))
+    st = (_lib or lib()).moe_paged_attention(cache.ref, a, ws.data_ptr(), ws.nbytes,
+                                             torch._C._cuda_getCurrentRawStream(dev.index))
     if st:
         raise MoEError(st, "moe_paged_attention")
     return (out, lse) if return_lse else out
@@ -674,9 +692,12 @@ def token_logprobs(logits, token=None, top=0, status=None):
     """Log probabilities read off logits [rows, vocab] (fp32 or bf16, moe_token_logprobs): dict(lse, entropy [rows],
     with token [rows] int32 (negative: none) logprob [rows], with top > 0 top_ids int32 and top_logprobs
     [rows, top])."""
-    if logits.dtype not in LOGITS:
+    kind = LOGITS.get(logits.dtype)
+    if kind is None:
         raise ValueError(f"logits: want float32 or bfloat16, got {logits.dtype}")
-    _want(logits, "logits", logits.dtype, 2)
+    xs = logits.stride()
+    if len(xs) != 2 or xs[1] != 1 or not logits.is_cuda:
+        _want(logits, "logits", logits.dtype, 2)
     n, v = logits.shape
     dev = logits.device
     f, empty = torch.float32, torch.empty   # (one allocation per output: views of a common one cost more)
@@ -690,8 +711,10 @@ def token_logprobs(logits, token=None, top=0, status=None):
         out["top_ids"] = ids = empty(n, top, dtype=torch.int32, device=dev)
         out["top_logprobs"] = tops = empty(n, top, dtype=f, device=dev)
         ids, tops = ids.data_ptr(), tops.data_ptr()
-    st = lib().moe_token_logprobs(n, v, LOGITS[logits.dtype], logits.data_ptr(), _strides(logits)[0], tp, top, lp,
-                                  entropy.data_ptr(), lse.data_ptr(), ids, tops, _ptr(status), _stream_of(logits))
+    st = (_lib or lib()).moe_token_logprobs(n, v, kind, logits.data_ptr(), xs[0] if n > 1 else 0, tp, top, lp,
+                                            entropy.data_ptr(), lse.data_ptr(), ids, tops,
+                                            None if status is None else status.data_ptr(),
+                                            torch._C._cuda_getCurrentRawStream(dev.index))
     if st:
         raise MoEError(st, "moe_token_logprobs")
     return out
