@@ -178,7 +178,8 @@ struct Shape {
     // 256 sequences up to 4096)
     static constexpr int kAhead = kE4m3 ? 1 : 2;
     static constexpr int kGranule = kTileKeys * kWarps;       // keys
-    static constexpr int kMerge = kWarps * 4 * D * 4;         // the block's join of 4 heads
+    static constexpr int kJoin = D == 64 && kHeads == 16 ? 8 : 4;   // heads that the block joins at a time, as memory allows
+    static constexpr int kMerge = kWarps * kJoin * D * 4;
     // beside a tile: which of its keys are live, and the exponent bytes of its e4m3 keys and values
     static constexpr int kMask = kE4m3 ? 2 * kTileKeys : 0, kMeta = kMask + 4;
     // as many slots (key or value tiles) as the block's share of 228 KB holds beside the join, at most 16
@@ -784,47 +785,47 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                         for (int j = 0; j < 4; ++j) o[hh][t][j] += __shfl_xor_sync(0xffffffffu, o[hh][t][j], 2);
                 }
             }
-            // four heads at a time through shared memory
+            // kJoin heads at a time through shared memory
 #pragma unroll
-            for (int four = 0; four < kHeads / 4; ++four) {
-                if (four * 4 >= live_heads) break;
-                if (four > 0) __syncthreads();
-                if ((c >> 1) == (four & 1)) {
+            for (int first = 0; first < kHeads; first += S::kJoin) {
+                if (first >= live_heads) break;
+                if (first > 0) __syncthreads();
+                if (S::kJoin == 8 || (c >> 1) == ((first >> 2) & 1)) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float* dst = s_merge + (warp * 4 + (2 * c & 3) + e) * D + g * S::kValElts;
+                        float* dst = s_merge + (warp * S::kJoin + ((2 * c) & (S::kJoin - 1)) + e) * D + g * S::kValElts;
 #pragma unroll
                         for (int u = 0; u < S::kValSegs; ++u)
 #pragma unroll
                             for (int j = 0; j < S::kValElts; j += 4) {
                                 const int t = (u * S::kValElts + j) / 2;
                                 *reinterpret_cast<float4*>(dst + u * 8 * S::kValElts + j) =
-                                    make_float4(o[four >> 1][t][e], o[four >> 1][t][2 + e], o[four >> 1][t + 1][e], o[four >> 1][t + 1][2 + e]);
+                                    make_float4(o[first >> 3][t][e], o[first >> 3][t][2 + e], o[first >> 3][t + 1][e], o[first >> 3][t + 1][2 + e]);
                             }
                     }
                 }
                 __syncthreads();
-                for (int at = threadIdx.x; at < D; at += kThreads) {   // D = 4 rows of D / 4 float4
+                for (int at = threadIdx.x; at < S::kJoin * (D / 4); at += kThreads) {
                     const int r = at / (D / 4), d = at % (D / 4) * 4;
-                    if (four * 4 + r >= live_heads) break;
+                    if (first + r >= live_heads) break;
                     float M = -INFINITY;
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * 16 + four * 4 + r].x);
+                    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * 16 + first + r].x);
                     const float ref = M == -INFINITY ? 0.0f : M;
                     float L = 0.0f;
                     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) {
-                        const float2 ml = s_ml[w * 16 + four * 4 + r];
+                        const float2 ml = s_ml[w * 16 + first + r];
                         const float f = exp2_fast(ml.x - ref);
-                        const float4 y = *reinterpret_cast<const float4*>(s_merge + (w * 4 + r) * D + d);
+                        const float4 y = *reinterpret_cast<const float4*>(s_merge + (w * S::kJoin + r) * D + d);
                         L += ml.y * f;
                         x.x += y.x * f;
                         x.y += y.y * f;
                         x.z += y.z * f;
                         x.w += y.w * f;
                     }
-                    const int head = head0 + four * 4 + r;
+                    const int head = head0 + first + r;
                     if (whole) {
                         const float inv = L == 0.0f ? 0.0f : 1.0f / L;
                         *reinterpret_cast<uint2*>(a.out + cw.b * a.out_token_stride + head * a.out_head_stride + d) =
@@ -833,8 +834,8 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                             a.lse[static_cast<long long>(cw.b) * a.n_heads + head] =
                                 L == 0.0f ? -INFINITY : ((kE4m3 ? M - kShift : M) + log2f(L)) * kLn2;
                     } else {
-                        *reinterpret_cast<float4*>(part + (four * 4 + r) * D + d) = x;
-                        if (d == 0) *reinterpret_cast<float2*>(part + 16 * D + 2 * (four * 4 + r)) = make_float2(M, L);
+                        *reinterpret_cast<float4*>(part + (first + r) * D + d) = x;
+                        if (d == 0) *reinterpret_cast<float2*>(part + 16 * D + 2 * (first + r)) = make_float2(M, L);
                     }
                 }
             }
@@ -852,22 +853,33 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                     const float* base = slots + 2 * static_cast<size_t>(first) * kSlot;
                     auto slot_of = [&](int k) { return base + (2 * static_cast<size_t>(k) + (k == 0 ? 1 : 0)) * kSlot; };
                     float2* const s_row = s_ml;   // per head: maximum, 1 / sum
-                    for (int r = warp; r < live_heads; r += kWarps) {
+                    // eight lanes to a head, each with every eighth part
+                    for (int r = threadIdx.x / 8; r < 16; r += kThreads / 8) {
                         float M = -INFINITY, L = 0.0f;
-                        for (int k = lane; k < parts; k += 32) {
-                            const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot_of(k) + 16 * D + 2 * r));
-                            const float mn = fmaxf(M, ml.x), at = mn == -INFINITY ? 0.0f : mn;
-                            L = L * exp2_fast(M - at) + ml.y * exp2_fast(ml.x - at);
-                            M = mn;
-                        }
+                        if (r < live_heads)
+                            for (int k0 = lane & 7; k0 < parts; k0 += 32) {
+                                float2 ml[4];
 #pragma unroll
-                        for (int off = 16; off >= 1; off >>= 1) {
+                                for (int k = 0; k < 4; ++k)
+                                    ml[k] = k0 + 8 * k < parts ? __ldcg(reinterpret_cast<const float2*>(slot_of(k0 + 8 * k) + 16 * D + 2 * r))
+                                                               : make_float2(-INFINITY, 0.0f);
+                                float mn = M;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) mn = fmaxf(mn, ml[k].x);
+                                const float at = mn == -INFINITY ? 0.0f : mn;
+                                L *= exp2_fast(M - at);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) L += ml[k].y * exp2_fast(ml[k].x - at);
+                                M = mn;
+                            }
+#pragma unroll
+                        for (int off = 4; off >= 1; off >>= 1) {
                             const float M2 = __shfl_xor_sync(0xffffffffu, M, off), L2 = __shfl_xor_sync(0xffffffffu, L, off);
                             const float mn = fmaxf(M, M2), at = mn == -INFINITY ? 0.0f : mn;
                             L = L * exp2_fast(M - at) + L2 * exp2_fast(M2 - at);
                             M = mn;
                         }
-                        if (lane == 0) {
+                        if ((lane & 7) == 0 && r < live_heads) {
                             s_row[r] = make_float2(M == -INFINITY ? 0.0f : M, L == 0.0f ? 0.0f : 1.0f / L);
                             if (a.lse)
                                 a.lse[static_cast<long long>(cw.b) * a.n_heads + head0 + r] =
@@ -890,7 +902,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                             }
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {
-                                const float w = k0 + k < parts ? exp2_fast(f[k] - row.x) : 0.0f;
+                                const float w = exp2_fast(f[k] - row.x);
                                 if (k0 + k < parts) {
                                     x.x += y[k].x * w;
                                     x.y += y[k].y * w;
