@@ -484,6 +484,35 @@ def test_logprobs(rows, vocab, bf16, top, pad):
 
 
 @pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("vocab,times", [(515, 90), (40001, 65)])
+def test_logprobs_odd_rows_in_a_large_batch(vocab, times, bf16):
+    """Rows of every odd kind many times over (more rows than blocks fit).  Copies of a row differ in alignment, so
+    their sums may differ in the last bits; their alternatives may not."""
+    x, _ = _logits(12, vocab, bf16, 3, 5)
+    x = x.clone()
+    x[0], x[1, 1:] = -float("inf"), -float("inf")
+    x[2] = torch.finfo(x.dtype).min
+    x[3] = 1.5
+    x[4, : vocab // 2] = float("nan")
+    x[5] = float("nan")
+    x[6, 7] = float("inf")
+    x[7] = torch.sort(x[7].float()).values.to(x.dtype)
+    x[8] = torch.sort(x[8].float(), descending=True).values.to(x.dtype)
+    x[9, vocab - 1], x[9, 0] = 99.0, 98.0
+    token = (torch.arange(12) * 41 % vocab).to(torch.int32).cuda()
+    token[3] = vocab + 5
+    one = moe.token_logprobs(x, token, top=20)
+    many = moe.token_logprobs(x.repeat(times, 1), token.repeat(times), top=20)
+    keep = token.clone()
+    keep[3] = -1
+    _check_logprobs(one, x, keep, 20)
+    ids = many["top_ids"].view(times, 12, 20)
+    assert (ids == one["top_ids"]).all()
+    for copy in (0, 1, times // 2, times - 1):
+        _check_logprobs({name: got[12 * copy: 12 * copy + 12] for name, got in many.items()}, x, keep, 20)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("vocab", [515, 40001])
 def test_logprobs_masks_ties_and_orders(vocab, bf16):
     """Rows of one value, sorted rows, banned tokens (-inf and the type's lowest), rows with nothing left."""

@@ -186,19 +186,47 @@ struct Stats {
     }
 };
 
-// Kept small: what shared memory leaves of the SM's 256 KB holds the loads in flight (with 33 KB a block the
-// 4096 x 131072 fp32 rows took 377 us instead of TODO).
-struct Shared {
-    Stats stats[kWarps];
-    uint64_t best[MOE_MAX_TOP];     // this block's best keys, in order
+// What the search for the best keys of a row needs beside the maxima and room for kMaxFound keys.  Shared memory is
+// kept small, since what it leaves of the SM's 256 KB holds the loads in flight (with 33 KB a block 4096 x 131072
+// fp32 rows took 377 us instead of 325).
+struct Finder {
+    uint64_t best[MOE_MAX_TOP];     // the block's best keys, in order
     uint32_t least[kWarps];
     int entries, found, before[kWarps];
     uint16_t entry[kMaxGroups * kThreads];
+};
+
+struct Shared {
+    Stats stats[kWarps];
+    Finder f;
     union {
         float top[kMaxGroups * kThreads];          // until the entries are listed
         alignas(16) uint64_t keys[kMaxFound];      // from then on
     };
 };
+
+constexpr int kFinishers = 64;   // threads that finish rows while the others read
+struct StreamShared {
+    Stats stats[2][kWarps];
+    Finder f;
+    float top[2][kMaxGroups * kThreads];
+    alignas(16) uint64_t keys[kMaxFound];
+};
+
+// Named barriers of the streaming kernel: of the finishers; rows handed over and taken (one each per buffer).
+enum Barrier : int { kBarFinish = 1, kBarFull = 2, kBarEmpty = 4 };
+__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+__device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
+// A barrier of the NT threads that look for the best: the block, or its finishers.
+template <int NT>
+__device__ __forceinline__ void sync_finders()
+{
+    if (NT == kThreads)
+        __syncthreads();
+    else
+        bar_sync(kBarFinish, NT);
+}
 
 // How many of the pairs part, part + kParts, .. of keys[0, count) (16-byte aligned) exceed key.
 template <int kParts>
@@ -213,18 +241,22 @@ __device__ __forceinline__ int rank_in(const uint64_t* keys, int count, uint64_t
     return rank;
 }
 
-// The best n keys of the block's share of a row into s.best (0 where there are none), sorted.
-template <class T>
-__device__ void find_best(Shared& s, const Row<T>& row, int vocab, int n, int lo, int hi, int per_group, int groups,
-                          float thread_top, int edge, float edge_value)
+// The best n keys of pieces [lo, hi) of a row and the edge values into s.best (0 where there are none), sorted: by
+// NT threads, from the maxima of the groups of pieces that the kThreads readers took.
+template <class T, int NT>
+__device__ void find_best(Finder& s, const float* tops, uint64_t* keys, const Row<T>& row, int n, int lo, int hi,
+                          int per_group, int groups, int t, int edge, float edge_value)
 {
-    constexpr int kN = Piece<T>::kN;
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    constexpr int kN = Piece<T>::kN, kNTWarps = NT / 32;
+    const int lane = t & 31, warp = t >> 5;
+    float thread_top = -INFINITY;
+    for (int g = 0; g < groups; ++g)
+        for (int i = t; i < kThreads; i += NT) thread_top = fmaxf(thread_top, tops[g * kThreads + i]);
     if (t < MOE_MAX_TOP) s.best[t] = 0;
     if (t == 0) s.entries = s.found = 0;
     // threshold: with k = ceil(n / full warps), the least of the full warps' k-th largest thread maxima is
-    // reached by at least n values (a warp is full when each of its threads has read something)
-    const int full = min((hi - lo) / 32, kWarps);
+    // reached by at least n values (a warp is full when each of its threads has maxima of something read)
+    const int full = min((hi - lo) / 32, kNTWarps);
     uint32_t mine = order_of(thread_top), kth = 0xffffffffu;
     if (warp < full) {
         for (int k = (n + full - 1) / full; k > 0; --k) {
@@ -234,22 +266,22 @@ __device__ void find_best(Shared& s, const Row<T>& row, int vocab, int n, int lo
         }
     }
     if (lane == 0) s.least[warp] = kth;
-    __syncthreads();
+    sync_finders<NT>();
     uint32_t level = full ? 0xffffffffu : 0u;
     for (int w = 0; w < full; ++w) level = min(level, s.least[w]);
     // compared as values: NaN never reaches the level, unless that is 0 and takes everything
     const float level_value = value_of(level);
     const bool any = level == 0u;
-    for (int g = 0; g < groups; ++g) {
-        const uint32_t who = __ballot_sync(0xffffffffu, any || s.top[g * kThreads + t] >= level_value);
+    for (int i = t; i < groups * kThreads; i += NT) {
+        const uint32_t who = __ballot_sync(0xffffffffu, any || tops[i] >= level_value);
         if (who) {
             int at = 0;
             if (lane == 0) at = atomicAdd(&s.entries, __popc(who));
             at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & lanemask_lt());
-            if ((who >> lane) & 1) s.entry[at] = static_cast<uint16_t>(g * kThreads + t);
+            if ((who >> lane) & 1) s.entry[at] = static_cast<uint16_t>(i);
         }
     }
-    __syncthreads();
+    sync_finders<NT>();
     const int entries = s.entries;
     // (one more pass, for the values above the level alone, when those at it are too many to rank)
     int strict = 0;
@@ -257,12 +289,12 @@ __device__ void find_best(Shared& s, const Row<T>& row, int vocab, int n, int lo
         auto reaches = [&](float x) { return any || (strict ? x > level_value : x >= level_value); };
         // the entries' pieces, one per thread and step, two steps' loads in flight
         const int per_entry = per_group * kBatch, all = entries * per_entry;
-        for (int q0 = t; q0 < all; q0 += 2 * kThreads) {
+        for (int q0 = t; q0 < all; q0 += 2 * NT) {
             uint4 v[2];
             int first[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int q = q0 + j * kThreads;
+                const int q = q0 + j * NT;
                 const int e = q < all ? s.entry[q / per_entry] : 0;
                 const int piece = lo + e % kThreads + kThreads * (e / kThreads * per_entry + q % per_entry);
                 first[j] = q < all && piece < hi ? row.head + piece * kN : -1;
@@ -279,41 +311,41 @@ __device__ void find_best(Shared& s, const Row<T>& row, int vocab, int n, int lo
                 int at = atomicAdd(&s.found, count);
 #pragma unroll
                 for (int i = 0; i < kN; ++i)
-                    if (reaches(x[i]) && at++ < kMaxFound) s.keys[at - 1] = key_of(order_of(x[i]), first[j] + i);
+                    if (reaches(x[i]) && at++ < kMaxFound) keys[at - 1] = key_of(order_of(x[i]), first[j] + i);
             }
         }
         if (edge >= 0 && reaches(edge_value)) {
             const int at = atomicAdd(&s.found, 1);
-            if (at < kMaxFound) s.keys[at] = key_of(order_of(edge_value), edge);
+            if (at < kMaxFound) keys[at] = key_of(order_of(edge_value), edge);
         }
-        __syncthreads();
+        sync_finders<NT>();
         if (s.found <= kMaxFound || strict) break;
-        __syncthreads();
+        sync_finders<NT>();
         if (t == 0) s.found = 0;
-        __syncthreads();
+        sync_finders<NT>();
     }
     const int found = s.found;
     if (found <= kMaxFound) {
         // four lanes to a key, each with a quarter of the comparisons
-        for (int a0 = 0; a0 < found; a0 += kThreads / 4) {
+        for (int a0 = 0; a0 < found; a0 += NT / 4) {
             const int a = a0 + t / 4;
-            const uint64_t key = a < found ? s.keys[a] : ~0ull;
-            int rank = rank_in<4>(s.keys, found, key, t & 3);
+            const uint64_t key = a < found ? keys[a] : ~0ull;
+            int rank = rank_in<4>(keys, found, key, t & 3);
             rank += __shfl_xor_sync(0xffffffffu, rank, 1);
             rank += __shfl_xor_sync(0xffffffffu, rank, 2);
             if (a < found && (t & 3) == 0 && rank < n) s.best[rank] = key;
         }
-        __syncthreads();
+        sync_finders<NT>();
         // fewer than n: the values at the level when those above it alone were ranked, then (level = that of
         // -inf) the NaNs, each in the order of their indices
         int have = found;
         for (int pass = strict ? 0 : 1; pass < 2 && have < n; ++pass) {
             const uint32_t want = pass == 0 ? level : 0u;
             if (pass == 1 && level == 0u) break;   // they were ranked with the rest
-            const int steps = (hi - lo + kThreads - 1) / kThreads;
+            const int steps = (hi - lo + NT - 1) / NT;
             // the edge values before the body, the body, the edge values behind it
             for (int step = -1; step <= steps && have < n; ++step) {
-                const int piece = lo + step * kThreads + t;
+                const int piece = lo + step * NT + t;
                 const bool side = step < 0 || step == steps;
                 int count = 0;
                 if (side)
@@ -327,9 +359,9 @@ __device__ void find_best(Shared& s, const Row<T>& row, int vocab, int n, int lo
                     if (lane >= off) incl += o;
                 }
                 if (lane == 31) s.before[warp] = incl;
-                __syncthreads();
+                sync_finders<NT>();
                 int at = have + incl - count;
-                for (int w = 0; w < kWarps; ++w) {
+                for (int w = 0; w < kNTWarps; ++w) {
                     if (w < warp) at += s.before[w];
                     have += s.before[w];
                 }
@@ -339,7 +371,7 @@ __device__ void find_best(Shared& s, const Row<T>& row, int vocab, int n, int lo
                         const int i = row.head + piece * kN + j;
                         if (order_of(static_cast<float>(row.x[i])) == want) s.best[at++] = key_of(want, i);
                     }
-                __syncthreads();
+                sync_finders<NT>();
             }
         }
         return;
@@ -352,7 +384,7 @@ __device__ void find_best(Shared& s, const Row<T>& row, int vocab, int n, int lo
             const uint64_t key = key_of(order_of(x), i);
             if (key < last && key > best) best = key;
         };
-        for (int p = lo + t; p < hi; p += kThreads)
+        for (int p = lo + t; p < hi; p += NT)
             for (int j = 0; j < kN; ++j) see(static_cast<float>(row.x[row.head + p * kN + j]), row.head + p * kN + j);
         if (edge >= 0) see(edge_value, edge);
 #pragma unroll
@@ -360,47 +392,24 @@ __device__ void find_best(Shared& s, const Row<T>& row, int vocab, int n, int lo
             const uint64_t o = __shfl_xor_sync(0xffffffffu, best, off);
             best = o > best ? o : best;
         }
-        if (lane == 0) s.keys[warp] = best;
-        __syncthreads();
-        for (int w = 0; w < kWarps; ++w) best = s.keys[w] > best ? s.keys[w] : best;
-        __syncthreads();
+        if (lane == 0) keys[warp] = best;
+        sync_finders<NT>();
+        for (int w = 0; w < kNTWarps; ++w) best = keys[w] > best ? keys[w] : best;
+        sync_finders<NT>();
         if (t == 0) s.best[k] = best;
         last = best;
     }
-    __syncthreads();
+    sync_finders<NT>();
 }
 
+// One thread's part of pieces [lo, hi) of a row: its statistics, and with kTop the maxima of its groups of pieces.
 template <class T, bool kTop>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) token_logprobs_kernel(const LogprobArgs a)
+__device__ __forceinline__ Stats read_pieces(const Row<T>& row, int lo, int hi, int t, int batches, int per_group, float* tops)
 {
     constexpr int kN = Piece<T>::kN;
-    extern __shared__ __align__(16) unsigned char smem[];
-    Shared& s = *reinterpret_cast<Shared*>(smem);
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int rank = static_cast<int>(blockIdx.x) & (a.split - 1);
-    const long long r = blockIdx.x / static_cast<unsigned>(a.split);
-    const Row<T> row(a.logits, a.row_stride, r, a.vocab);
-    // this block's share of the pieces
-    const int share = (row.pieces + a.split - 1) / a.split;
-    const int lo = min(row.pieces, rank * share), hi = min(row.pieces, lo + share);
-    const int batches = (hi - lo + kThreads * kBatch - 1) / (kThreads * kBatch);
-    const int per_group = (batches + kMaxGroups - 1) / kMaxGroups;    // batches under one maximum
-
-    // asked for early: the given token and its logit
-    int token = -1;
-    float given = 0.0f;
-    if (a.logprob && rank == 0 && t == 0) {
-        token = a.token[r];
-        if (token >= a.vocab) {
-            record_error(a.status, MOE_ERR_INDEX);
-            token = -1;
-        }
-        if (token >= 0) given = static_cast<float>(row.x[token]);
-    }
-
     Stats st{-INFINITY, 0.0f, 0.0f};
     float group_top = -INFINITY;
-    int group = 0, in_group = 0;
+    int in_group = 0;
     for (int b = 0; b < batches; ++b) {
         uint4 v[kBatch];
 #pragma unroll
@@ -441,14 +450,71 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) token_logpro
         if (kTop) {
             group_top = fmaxf(group_top, top);
             if (++in_group == per_group || b + 1 == batches) {
-                s.top[group * kThreads + t] = group_top;
+                tops[t] = group_top;
+                tops += kThreads;
                 group_top = -INFINITY;
                 in_group = 0;
-                ++group;
             }
         }
     }
-    const float thread_top = st.m;
+    return st;
+}
+
+// The given token of row r, or -1 (also for one that is out of range, which is recorded).
+__device__ __forceinline__ int given_token(const LogprobArgs& a, long long r)
+{
+    const int token = a.token[r];
+    if (token >= a.vocab) record_error(a.status, MOE_ERR_INDEX);
+    return token >= a.vocab ? -1 : token;
+}
+
+// What the outputs of a row take from its statistics.
+struct Result {
+    bool none;            // nothing but -inf in the row
+    float ref, log_l;
+    __device__ __forceinline__ explicit Result(const Stats& s)
+        : none(s.m == -INFINITY && s.l == 0.0f), ref(s.m == -INFINITY ? 0.0f : s.m), log_l(logf(s.l))
+    {
+    }
+    __device__ __forceinline__ float logprob(float x) const { return none ? -INFINITY : x - ref - log_l; }
+    // by one thread
+    __device__ __forceinline__ void write(const LogprobArgs& a, long long r, const Stats& s, int token, float given) const
+    {
+        if (s.l != s.l) record_error(a.status, MOE_ERR_NONFINITE);
+        if (a.lse) a.lse[r] = ref + log_l;
+        if (a.entropy) a.entropy[r] = none ? 0.0f : log_l - s.w / s.l * kLn2;
+        if (a.logprob) a.logprob[r] = token < 0 ? 0.0f : logprob(given);
+    }
+    __device__ __forceinline__ void write_top(const LogprobArgs& a, long long r, int at, uint64_t key) const
+    {
+        a.top_ids[r * a.n_top + at] = key ? static_cast<int>(~static_cast<uint32_t>(key)) : -1;
+        a.top_logprobs[r * a.n_top + at] = key ? logprob(value_of(static_cast<uint32_t>(key >> 32))) : -INFINITY;
+    }
+};
+
+// A row to a block, or to a cluster of a.split blocks.
+template <class T, bool kTop>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) token_logprobs_kernel(const LogprobArgs a)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    Shared& s = *reinterpret_cast<Shared*>(smem);
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int rank = static_cast<int>(blockIdx.x) & (a.split - 1);
+    const long long r = blockIdx.x / static_cast<unsigned>(a.split);
+    const Row<T> row(a.logits, a.row_stride, r, a.vocab);
+    // this block's share of the pieces
+    const int share = (row.pieces + a.split - 1) / a.split;
+    const int lo = min(row.pieces, rank * share), hi = min(row.pieces, lo + share);
+    const int batches = (hi - lo + kThreads * kBatch - 1) / (kThreads * kBatch);
+    const int per_group = (batches + kMaxGroups - 1) / kMaxGroups;    // batches under one maximum
+    // asked for early: the given token and its logit
+    int token = -1;
+    float given = 0.0f;
+    if (a.logprob && rank == 0 && t == 0) {
+        token = given_token(a, r);
+        if (token >= 0) given = static_cast<float>(row.x[token]);
+    }
+    Stats st = read_pieces<T, kTop>(row, lo, hi, t, batches, per_group, s.top);
     // the values beside the whole pieces: rank 0's threads, one each
     const int edge = rank == 0 ? row.edge(t, a.vocab) : -1;
     const float edge_value = edge >= 0 ? static_cast<float>(row.x[edge]) : -INFINITY;
@@ -458,8 +524,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) token_logpro
     }
     st.join_warp();
     if (lane == 0) s.stats[warp] = st;
-    if (kTop)
-        find_best<T>(s, row, a.vocab, a.n_top, lo, hi, per_group, group, thread_top, edge, edge_value);
+    if (kTop) {
+        const int groups = per_group ? (batches + per_group - 1) / per_group : 0;
+        find_best<T, kThreads>(s.f, s.top, s.keys, row, a.n_top, lo, hi, per_group, groups, t, edge, edge_value);
+    }
     if (a.split > 1)
         cluster_sync_all();
     else
@@ -477,39 +545,80 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) token_logpro
             all.w += o.w;
         }
         all.join_warp();
-        const bool none = all.m == -INFINITY && all.l == 0.0f;      // nothing but -inf
-        const float ref = all.m == -INFINITY ? 0.0f : all.m, log_l = logf(all.l);
-        if (t == 0) {
-            if (all.l != all.l) record_error(a.status, MOE_ERR_NONFINITE);
-            if (a.lse) a.lse[r] = ref + log_l;
-            if (a.entropy) a.entropy[r] = none ? 0.0f : log_l - all.w / all.l * kLn2;
-            if (a.logprob) a.logprob[r] = token < 0 ? 0.0f : (none ? -INFINITY : given - ref - log_l);
-        }
+        const Result res(all);
+        if (t == 0) res.write(a, r, all, token, given);
         if (kTop) {
             // thread t ranks key t % n of block t / n among all blocks' best
             const int n = a.n_top, total = a.split * n;
             uint64_t key = 0;
             if (t < total) {
-                const uint32_t mine = map_to_rank(smem_u32(&s.best[t % n]), t / n);
+                const uint32_t mine = map_to_rank(smem_u32(&s.f.best[t % n]), t / n);
                 key = static_cast<uint64_t>(static_cast<uint32_t>(ld_cluster_s32(mine + 4))) << 32 |
                       static_cast<uint32_t>(ld_cluster_s32(mine));
                 s.keys[t] = key;
             }
-            if (t < n && t >= a.vocab) {
-                a.top_ids[r * n + t] = -1;
-                a.top_logprobs[r * n + t] = -INFINITY;
-            }
             if (a.split > 1) __syncthreads();
-            if (key) {
-                const int at = a.split == 1 ? t : rank_in<1>(s.keys, total, key, 0);
-                if (at < n) {
-                    a.top_ids[r * n + at] = static_cast<int>(~static_cast<uint32_t>(key));
-                    a.top_logprobs[r * n + at] = none ? -INFINITY : value_of(static_cast<uint32_t>(key >> 32)) - ref - log_l;
-                }
-            }
+            // (a row has n keys, unless it is shorter: then there is no split, and the places behind stay empty)
+            const int at = a.split == 1 ? t : rank_in<1>(s.keys, total, key, 0);
+            if (t < total && at < n && (key || a.split == 1)) res.write_top(a, r, at, key);
         }
     }
     if (a.split > 1) cluster_sync_all();   // a block's shared memory stays until it has been read
+}
+
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ..: kThreads threads read them one after the other, kFinishers threads
+// finish each behind them.
+template <class T>
+__global__ void __launch_bounds__(kThreads + kFinishers, 4) token_logprobs_stream_kernel(const LogprobArgs a)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    StreamShared& s = *reinterpret_cast<StreamShared*>(smem);
+    constexpr int kAll = kThreads + kFinishers;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int buffer = 0;
+    if (warp < kWarps) {
+        const int t = threadIdx.x;
+        long long handed = 0;
+        for (long long r = blockIdx.x; r < a.rows; r += gridDim.x, buffer ^= 1, ++handed) {
+            const Row<T> row(a.logits, a.row_stride, r, a.vocab);
+            const int batches = (row.pieces + kThreads * kBatch - 1) / (kThreads * kBatch);
+            const int per_group = (batches + kMaxGroups - 1) / kMaxGroups;
+            if (handed >= 2) bar_sync(kBarEmpty + buffer, kAll);
+            Stats st = read_pieces<T, true>(row, 0, row.pieces, t, batches, per_group, s.top[buffer]);
+            if (const int edge = row.edge(t, a.vocab); edge >= 0) {
+                const float x = static_cast<float>(row.x[edge]);
+                st.raise(fmaxf(st.m, x));
+                st.add(x);
+            }
+            st.join_warp();
+            if (lane == 0) s.stats[buffer][warp] = st;
+            bar_arrive(kBarFull + buffer, kAll);
+        }
+    } else {
+        const int t = threadIdx.x - kThreads;
+        for (long long r = blockIdx.x; r < a.rows; r += gridDim.x, buffer ^= 1) {
+            const Row<T> row(a.logits, a.row_stride, r, a.vocab);
+            const int batches = (row.pieces + kThreads * kBatch - 1) / (kThreads * kBatch);
+            const int per_group = (batches + kMaxGroups - 1) / kMaxGroups;
+            const int groups = per_group ? (batches + per_group - 1) / per_group : 0;
+            const int edge = row.edge(t, a.vocab);
+            const float edge_value = edge >= 0 ? static_cast<float>(row.x[edge]) : -INFINITY;
+            const int token = a.logprob ? given_token(a, r) : -1;
+            const float given = token >= 0 ? static_cast<float>(row.x[token]) : 0.0f;
+            bar_sync(kBarFull + buffer, kAll);
+            find_best<T, kFinishers>(s.f, s.top[buffer], s.keys, row, a.n_top, 0, row.pieces, per_group, groups, t, edge, edge_value);
+            sync_finders<kFinishers>();
+            if (t < 32) {
+                Stats all = lane < kWarps ? s.stats[buffer][lane] : Stats{-INFINITY, 0.0f, 0.0f};
+                all.join_warp();
+                const Result res(all);
+                if (t == 0) res.write(a, r, all, token, given);
+                if (t < a.n_top) res.write_top(a, r, t, s.f.best[t]);
+            }
+            sync_finders<kFinishers>();   // s.f is free for the next row
+            if (r + 2 * static_cast<long long>(gridDim.x) < a.rows) bar_arrive(kBarEmpty + buffer, kAll);
+        }
+    }
 }
 
 // dx_i = g (1[i = token] - p_i) - h p_i (ln p_i + H) = g 1[i = token] - p_i (g + h (z_i + H)), z = x - lse.
@@ -583,10 +692,18 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t s)
     a.split = 1;
     while (a.split < 8 && a.rows * a.split * 2 <= 4LL * num_sms() && pieces / (a.split * 2) >= 2 * kThreads) a.split *= 2;
     if (a.rows * a.split > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (a.n_top > 0 && a.rows > 4LL * num_sms()) {   // more rows than blocks fit: read ahead of the alternatives
+        const unsigned grid = static_cast<unsigned>(4 * num_sms());
+        if (a.bf16)
+            token_logprobs_stream_kernel<__nv_bfloat16><<<grid, kThreads + kFinishers, sizeof(StreamShared), s>>>(a);
+        else
+            token_logprobs_stream_kernel<float><<<grid, kThreads + kFinishers, sizeof(StreamShared), s>>>(a);
+        return cudaGetLastError();
+    }
     cudaLaunchConfig_t c{};
     c.gridDim = dim3(static_cast<unsigned>(a.rows * a.split));
     c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = a.n_top > 0 ? sizeof(Shared) : offsetof(Shared, least);
+    c.dynamicSmemBytes = a.n_top > 0 ? sizeof(Shared) : offsetof(Shared, f);
     c.stream = s;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
