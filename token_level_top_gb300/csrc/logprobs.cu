@@ -205,6 +205,7 @@ struct Shared {
     };
 };
 
+constexpr int kStreamBlocks = 4; // blocks per SM of the streaming kernel
 constexpr int kFinishers = 64;   // threads that finish rows while the others read
 struct StreamShared {
     Stats stats[2][kWarps];
@@ -409,21 +410,18 @@ __device__ __forceinline__ Stats read_pieces(const Row<T>& row, int lo, int hi, 
     constexpr int kN = Piece<T>::kN;
     Stats st{-INFINITY, 0.0f, 0.0f};
     float group_top = -INFINITY;
-    int in_group = 0;
-    for (int b = 0; b < batches; ++b) {
-        uint4 v[kBatch];
+    auto work = [&](const auto& v) {
+        constexpr int kPieces = sizeof(v) / 16;
+        float top = Piece<T>::top(v[0]);
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int p = lo + t + kThreads * (b * kBatch + j);
-            v[j] = p < hi ? __ldg(row.body + p) : Piece<T>::nothing();
-        }
-        float top = fmaxf(fmaxf(Piece<T>::top(v[0]), Piece<T>::top(v[1])), fmaxf(Piece<T>::top(v[2]), Piece<T>::top(v[3])));
+        for (int j = 1; j < kPieces; ++j) top = fmaxf(top, Piece<T>::top(v[j]));
+        if (kTop) group_top = fmaxf(group_top, top);
         st.raise(fmaxf(st.m, top));
         if (!st.far()) {
             const float minus_base = -st.base();
             float l2 = 0.0f, w2 = 0.0f;   // a second pair of sums halves the chains
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
+            for (int j = 0; j < kPieces; ++j) {
                 float x[kN];
                 Piece<T>::unpack(Piece<T>::floored(v[j]), x);
 #pragma unroll
@@ -439,23 +437,45 @@ __device__ __forceinline__ Stats read_pieces(const Row<T>& row, int lo, int hi, 
             st.l += l2;
             st.w += w2;
         } else {
-#pragma unroll 1
-            for (int j = 0; j < kBatch; ++j) {
-                float x[kN];
-                Piece<T>::unpack(j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3], x);
 #pragma unroll
-                for (int i = 0; i < kN; ++i) st.add(x[i]);
+            for (int j = 0; j < kPieces; ++j) {
+                float x[kN];
+                Piece<T>::unpack(v[j], x);
+#pragma unroll 1
+                for (int i = 0; i < kN; ++i) {
+                    float one = x[0];
+#pragma unroll
+                    for (int k = 1; k < kN; ++k) one = i == k ? x[k] : one;
+                    st.add(one);
+                }
             }
         }
-        if (kTop) {
-            group_top = fmaxf(group_top, top);
-            if (++in_group == per_group || b + 1 == batches) {
-                tops[t] = group_top;
-                tops += kThreads;
-                group_top = -INFINITY;
-                in_group = 0;
-            }
+    };
+    auto close_group = [&]() {
+        tops[t] = group_top;
+        tops += kThreads;
+        group_top = -INFINITY;
+    };
+    const uint4* src = row.body + lo + t;
+    const int full = (hi - lo) / (kThreads * kBatch);   // batches without a missing piece
+    for (int b = 0, in_group = 0; b < full; ++b) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) v[j] = __ldg(src + j * kThreads);
+        src += kThreads * kBatch;
+        work(v);
+        if (kTop && (++in_group == per_group || b + 1 == batches)) {
+            close_group();
+            in_group = 0;
         }
+    }
+    if (full < batches) {   // piece by piece: the last batch may hold few
+        const int rest = hi - lo - full * kThreads * kBatch;
+        for (int j = 0; j < rest; j += kThreads) {
+            uint4 v[1] = {j + t < rest ? __ldg(src + j) : Piece<T>::nothing()};
+            work(v);
+        }
+        if (kTop) close_group();
     }
     return st;
 }
@@ -494,7 +514,7 @@ struct Result {
 
 // A row to a block, or to a cluster of a.split blocks.
 template <class T, bool kTop>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) token_logprobs_kernel(const LogprobArgs a)
+__global__ void __launch_bounds__(kThreads, 5) token_logprobs_kernel(const LogprobArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     Shared& s = *reinterpret_cast<Shared*>(smem);
@@ -569,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) token_logpro
 // Rows blockIdx.x, blockIdx.x + gridDim.x, ..: kThreads threads read them one after the other, kFinishers threads
 // finish each behind them.
 template <class T>
-__global__ void __launch_bounds__(kThreads + kFinishers, 4) token_logprobs_stream_kernel(const LogprobArgs a)
+__global__ void __launch_bounds__(kThreads + kFinishers, kStreamBlocks) token_logprobs_stream_kernel(const LogprobArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     StreamShared& s = *reinterpret_cast<StreamShared*>(smem);
@@ -692,8 +712,8 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t s)
     a.split = 1;
     while (a.split < 8 && a.rows * a.split * 2 <= 4LL * num_sms() && pieces / (a.split * 2) >= 2 * kThreads) a.split *= 2;
     if (a.rows * a.split > 0x7fffffffLL) return cudaErrorInvalidValue;
-    if (a.n_top > 0 && a.rows > 4LL * num_sms()) {   // more rows than blocks fit: read ahead of the alternatives
-        const unsigned grid = static_cast<unsigned>(4 * num_sms());
+    if (a.n_top > 0 && a.rows > kStreamBlocks * static_cast<long long>(num_sms())) {   // more rows than blocks fit: read ahead of the alternatives
+        const unsigned grid = static_cast<unsigned>(kStreamBlocks * num_sms());
         if (a.bf16)
             token_logprobs_stream_kernel<__nv_bfloat16><<<grid, kThreads + kFinishers, sizeof(StreamShared), s>>>(a);
         else
