@@ -23,9 +23,9 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;   // of a block that reads a row (or its share) alone
 constexpr int kBatch = 4;          // 16-byte pieces that a thread has in flight
-constexpr int kMaxGroups = 8;      // maxima kept per thread
+constexpr int kMaxima = 2048;       // maxima kept of a row, at most 2048 / readers per reader
 constexpr int kMaxFound = 1024;    // values at or above the threshold that are ranked at once
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Values are raised to this: their exponentials are 0 all the same, and 0 times them is 0 (-inf would make NaN).
@@ -191,26 +191,27 @@ struct Stats {
 // fp32 rows took 377 us instead of 325).
 struct Finder {
     uint64_t best[MOE_MAX_TOP];     // the block's best keys, in order
-    uint32_t least[kWarps];
+    uint32_t least[kWarps];         // (at most kThreads threads look for the best)
     int entries, found, before[kWarps];
-    uint16_t entry[kMaxGroups * kThreads];
+    uint16_t entry[kMaxima];
 };
 
 struct Shared {
     Stats stats[kWarps];
     Finder f;
     union {
-        float top[kMaxGroups * kThreads];          // until the entries are listed
+        float top[kMaxima];                        // until the entries are listed
         alignas(16) uint64_t keys[kMaxFound];      // from then on
     };
 };
 
-constexpr int kStreamBlocks = 4; // blocks per SM of the streaming kernel
-constexpr int kFinishers = 64;   // threads that finish rows while the others read
+constexpr int kStreamBlocks = 4; // blocks per SM of the streaming kernel,
+constexpr int kReaders = 256;    // their threads that read rows
+constexpr int kFinishers = 64;  // and that finish them
 struct StreamShared {
-    Stats stats[2][kWarps];
+    Stats stats[2][kReaders / 32];
     Finder f;
-    float top[2][kMaxGroups * kThreads];
+    float top[2][kMaxima];
     alignas(16) uint64_t keys[kMaxFound];
 };
 
@@ -223,7 +224,7 @@ __device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("
 template <int NT>
 __device__ __forceinline__ void sync_finders()
 {
-    if (NT == kThreads)
+    if (NT == kThreads)   // (the finishers are fewer)
         __syncthreads();
     else
         bar_sync(kBarFinish, NT);
@@ -243,8 +244,8 @@ __device__ __forceinline__ int rank_in(const uint64_t* keys, int count, uint64_t
 }
 
 // The best n keys of pieces [lo, hi) of a row and the edge values into s.best (0 where there are none), sorted: by
-// NT threads, from the maxima of the groups of pieces that the kThreads readers took.
-template <class T, int NT>
+// NT threads, from the maxima of the groups of pieces that R readers took.
+template <class T, int NT, int R>
 __device__ void find_best(Finder& s, const float* tops, uint64_t* keys, const Row<T>& row, int n, int lo, int hi,
                           int per_group, int groups, int t, int edge, float edge_value)
 {
@@ -252,7 +253,7 @@ __device__ void find_best(Finder& s, const float* tops, uint64_t* keys, const Ro
     const int lane = t & 31, warp = t >> 5;
     float thread_top = -INFINITY;
     for (int g = 0; g < groups; ++g)
-        for (int i = t; i < kThreads; i += NT) thread_top = fmaxf(thread_top, tops[g * kThreads + i]);
+        for (int i = t; i < R; i += NT) thread_top = fmaxf(thread_top, tops[g * R + i]);
     if (t < MOE_MAX_TOP) s.best[t] = 0;
     if (t == 0) s.entries = s.found = 0;
     // threshold: with k = ceil(n / full warps), the least of the full warps' k-th largest thread maxima is
@@ -273,51 +274,57 @@ __device__ void find_best(Finder& s, const float* tops, uint64_t* keys, const Ro
     // compared as values: NaN never reaches the level, unless that is 0 and takes everything
     const float level_value = value_of(level);
     const bool any = level == 0u;
-    for (int i = t; i < groups * kThreads; i += NT) {
-        const uint32_t who = __ballot_sync(0xffffffffu, any || tops[i] >= level_value);
-        if (who) {
-            int at = 0;
-            if (lane == 0) at = atomicAdd(&s.entries, __popc(who));
-            at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & lanemask_lt());
-            if ((who >> lane) & 1) s.entry[at] = static_cast<uint16_t>(i);
-        }
+    // the maxima that reach it, listed warp by warp
+    static_assert(kMaxima / NT <= 32, "a bit per maximum of a thread");
+    uint32_t hits = 0;
+    for (int i = t, k = 0; i < groups * R; i += NT, ++k) hits |= static_cast<uint32_t>(any || tops[i] >= level_value) << k;
+    const int hit_count = __popc(hits);
+    int at = hit_count;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, at, off);
+        if (lane >= off) at += o;
     }
+    int begin = 0;
+    if (lane == 31) begin = atomicAdd(&s.entries, at);
+    at += __shfl_sync(0xffffffffu, begin, 31) - hit_count;
+    for (; hits; hits &= hits - 1) s.entry[at++] = static_cast<uint16_t>(t + (__ffs(hits) - 1) * NT);
     sync_finders<NT>();
     const int entries = s.entries;
     // (one more pass, for the values above the level alone, when those at it are too many to rank)
     int strict = 0;
     for (;; ++strict) {
         auto reaches = [&](float x) { return any || (strict ? x > level_value : x >= level_value); };
-        // the entries' pieces, one per thread and step, two steps' loads in flight
+        // the entries' pieces, one per thread and step, four steps' loads in flight
         const int per_entry = per_group * kBatch, all = entries * per_entry;
-        for (int q0 = t; q0 < all; q0 += 2 * NT) {
-            uint4 v[2];
-            int first[2];
+        for (int q0 = t; q0 < all; q0 += 4 * NT) {
+            uint4 v[4];
+            int first[4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 4; ++j) {
                 const int q = q0 + j * NT;
                 const int e = q < all ? s.entry[q / per_entry] : 0;
-                const int piece = lo + e % kThreads + kThreads * (e / kThreads * per_entry + q % per_entry);
+                const int piece = lo + e % R + R * (e / R * per_entry + q % per_entry);
                 first[j] = q < all && piece < hi ? row.head + piece * kN : -1;
                 v[j] = first[j] >= 0 ? __ldg(row.body + piece) : Piece<T>::nothing();
             }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 4; ++j) {
                 if (first[j] < 0 || !reaches(Piece<T>::top(v[j]))) continue;
                 float x[kN];
                 Piece<T>::unpack(v[j], x);
                 int count = 0;
 #pragma unroll
                 for (int i = 0; i < kN; ++i) count += reaches(x[i]);
-                int at = atomicAdd(&s.found, count);
+                int place = atomicAdd(&s.found, count);
 #pragma unroll
                 for (int i = 0; i < kN; ++i)
-                    if (reaches(x[i]) && at++ < kMaxFound) keys[at - 1] = key_of(order_of(x[i]), first[j] + i);
+                    if (reaches(x[i]) && place++ < kMaxFound) keys[place - 1] = key_of(order_of(x[i]), first[j] + i);
             }
         }
         if (edge >= 0 && reaches(edge_value)) {
-            const int at = atomicAdd(&s.found, 1);
-            if (at < kMaxFound) keys[at] = key_of(order_of(edge_value), edge);
+            const int place = atomicAdd(&s.found, 1);
+            if (place < kMaxFound) keys[place] = key_of(order_of(edge_value), edge);
         }
         sync_finders<NT>();
         if (s.found <= kMaxFound || strict) break;
@@ -404,7 +411,7 @@ __device__ void find_best(Finder& s, const float* tops, uint64_t* keys, const Ro
 }
 
 // One thread's part of pieces [lo, hi) of a row: its statistics, and with kTop the maxima of its groups of pieces.
-template <class T, bool kTop>
+template <class T, bool kTop, int R>
 __device__ __forceinline__ Stats read_pieces(const Row<T>& row, int lo, int hi, int t, int batches, int per_group, float* tops)
 {
     constexpr int kN = Piece<T>::kN;
@@ -453,16 +460,16 @@ __device__ __forceinline__ Stats read_pieces(const Row<T>& row, int lo, int hi, 
     };
     auto close_group = [&]() {
         tops[t] = group_top;
-        tops += kThreads;
+        tops += R;
         group_top = -INFINITY;
     };
     const uint4* src = row.body + lo + t;
-    const int full = (hi - lo) / (kThreads * kBatch);   // batches without a missing piece
+    const int full = (hi - lo) / (R * kBatch);   // batches without a missing piece
     for (int b = 0, in_group = 0; b < full; ++b) {
         uint4 v[kBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) v[j] = __ldg(src + j * kThreads);
-        src += kThreads * kBatch;
+        for (int j = 0; j < kBatch; ++j) v[j] = __ldg(src + j * R);
+        src += R * kBatch;
         work(v);
         if (kTop && (++in_group == per_group || b + 1 == batches)) {
             close_group();
@@ -470,14 +477,21 @@ __device__ __forceinline__ Stats read_pieces(const Row<T>& row, int lo, int hi, 
         }
     }
     if (full < batches) {   // piece by piece: the last batch may hold few
-        const int rest = hi - lo - full * kThreads * kBatch;
-        for (int j = 0; j < rest; j += kThreads) {
+        const int rest = hi - lo - full * R * kBatch;
+        for (int j = 0; j < rest; j += R) {
             uint4 v[1] = {j + t < rest ? __ldg(src + j) : Piece<T>::nothing()};
             work(v);
         }
         if (kTop) close_group();
     }
     return st;
+}
+
+// Batches under one maximum of a reader.
+template <int R>
+__device__ __forceinline__ int per_maximum(int batches)
+{
+    return (batches + kMaxima / R - 1) / (kMaxima / R);
 }
 
 // The given token of row r, or -1 (also for one that is out of range, which is recorded).
@@ -526,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 5) token_logprobs_kernel(const Logpr
     const int share = (row.pieces + a.split - 1) / a.split;
     const int lo = min(row.pieces, rank * share), hi = min(row.pieces, lo + share);
     const int batches = (hi - lo + kThreads * kBatch - 1) / (kThreads * kBatch);
-    const int per_group = (batches + kMaxGroups - 1) / kMaxGroups;    // batches under one maximum
+    const int per_group = per_maximum<kThreads>(batches);
     // asked for early: the given token and its logit
     int token = -1;
     float given = 0.0f;
@@ -534,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 5) token_logprobs_kernel(const Logpr
         token = given_token(a, r);
         if (token >= 0) given = static_cast<float>(row.x[token]);
     }
-    Stats st = read_pieces<T, kTop>(row, lo, hi, t, batches, per_group, s.top);
+    Stats st = read_pieces<T, kTop, kThreads>(row, lo, hi, t, batches, per_group, s.top);
     // the values beside the whole pieces: rank 0's threads, one each
     const int edge = rank == 0 ? row.edge(t, a.vocab) : -1;
     const float edge_value = edge >= 0 ? static_cast<float>(row.x[edge]) : -INFINITY;
@@ -546,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 5) token_logprobs_kernel(const Logpr
     if (lane == 0) s.stats[warp] = st;
     if (kTop) {
         const int groups = per_group ? (batches + per_group - 1) / per_group : 0;
-        find_best<T, kThreads>(s.f, s.top, s.keys, row, a.n_top, lo, hi, per_group, groups, t, edge, edge_value);
+        find_best<T, kThreads, kThreads>(s.f, s.top, s.keys, row, a.n_top, lo, hi, per_group, groups, t, edge, edge_value);
     }
     if (a.split > 1)
         cluster_sync_all();
@@ -586,25 +600,25 @@ __global__ void __launch_bounds__(kThreads, 5) token_logprobs_kernel(const Logpr
     if (a.split > 1) cluster_sync_all();   // a block's shared memory stays until it has been read
 }
 
-// Rows blockIdx.x, blockIdx.x + gridDim.x, ..: kThreads threads read them one after the other, kFinishers threads
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ..: kReaders threads read them one after the other, kFinishers threads
 // finish each behind them.
 template <class T>
-__global__ void __launch_bounds__(kThreads + kFinishers, kStreamBlocks) token_logprobs_stream_kernel(const LogprobArgs a)
+__global__ void __launch_bounds__(kReaders + kFinishers, kStreamBlocks) token_logprobs_stream_kernel(const LogprobArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     StreamShared& s = *reinterpret_cast<StreamShared*>(smem);
-    constexpr int kAll = kThreads + kFinishers;
+    constexpr int kAll = kReaders + kFinishers;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int buffer = 0;
-    if (warp < kWarps) {
+    if (warp < kReaders / 32) {
         const int t = threadIdx.x;
         long long handed = 0;
         for (long long r = blockIdx.x; r < a.rows; r += gridDim.x, buffer ^= 1, ++handed) {
             const Row<T> row(a.logits, a.row_stride, r, a.vocab);
-            const int batches = (row.pieces + kThreads * kBatch - 1) / (kThreads * kBatch);
-            const int per_group = (batches + kMaxGroups - 1) / kMaxGroups;
+            const int batches = (row.pieces + kReaders * kBatch - 1) / (kReaders * kBatch);
+            const int per_group = per_maximum<kReaders>(batches);
             if (handed >= 2) bar_sync(kBarEmpty + buffer, kAll);
-            Stats st = read_pieces<T, true>(row, 0, row.pieces, t, batches, per_group, s.top[buffer]);
+            Stats st = read_pieces<T, true, kReaders>(row, 0, row.pieces, t, batches, per_group, s.top[buffer]);
             if (const int edge = row.edge(t, a.vocab); edge >= 0) {
                 const float x = static_cast<float>(row.x[edge]);
                 st.raise(fmaxf(st.m, x));
@@ -615,21 +629,21 @@ __global__ void __launch_bounds__(kThreads + kFinishers, kStreamBlocks) token_lo
             bar_arrive(kBarFull + buffer, kAll);
         }
     } else {
-        const int t = threadIdx.x - kThreads;
+        const int t = threadIdx.x - kReaders;
         for (long long r = blockIdx.x; r < a.rows; r += gridDim.x, buffer ^= 1) {
             const Row<T> row(a.logits, a.row_stride, r, a.vocab);
-            const int batches = (row.pieces + kThreads * kBatch - 1) / (kThreads * kBatch);
-            const int per_group = (batches + kMaxGroups - 1) / kMaxGroups;
+            const int batches = (row.pieces + kReaders * kBatch - 1) / (kReaders * kBatch);
+            const int per_group = per_maximum<kReaders>(batches);
             const int groups = per_group ? (batches + per_group - 1) / per_group : 0;
             const int edge = row.edge(t, a.vocab);
             const float edge_value = edge >= 0 ? static_cast<float>(row.x[edge]) : -INFINITY;
             const int token = a.logprob ? given_token(a, r) : -1;
             const float given = token >= 0 ? static_cast<float>(row.x[token]) : 0.0f;
             bar_sync(kBarFull + buffer, kAll);
-            find_best<T, kFinishers>(s.f, s.top[buffer], s.keys, row, a.n_top, 0, row.pieces, per_group, groups, t, edge, edge_value);
+            find_best<T, kFinishers, kReaders>(s.f, s.top[buffer], s.keys, row, a.n_top, 0, row.pieces, per_group, groups, t, edge, edge_value);
             sync_finders<kFinishers>();
             if (t < 32) {
-                Stats all = lane < kWarps ? s.stats[buffer][lane] : Stats{-INFINITY, 0.0f, 0.0f};
+                Stats all = lane < kReaders / 32 ? s.stats[buffer][lane] : Stats{-INFINITY, 0.0f, 0.0f};
                 all.join_warp();
                 const Result res(all);
                 if (t == 0) res.write(a, r, all, token, given);
@@ -715,9 +729,9 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t s)
     if (a.n_top > 0 && a.rows > kStreamBlocks * static_cast<long long>(num_sms())) {   // more rows than blocks fit: read ahead of the alternatives
         const unsigned grid = static_cast<unsigned>(kStreamBlocks * num_sms());
         if (a.bf16)
-            token_logprobs_stream_kernel<__nv_bfloat16><<<grid, kThreads + kFinishers, sizeof(StreamShared), s>>>(a);
+            token_logprobs_stream_kernel<__nv_bfloat16><<<grid, kReaders + kFinishers, sizeof(StreamShared), s>>>(a);
         else
-            token_logprobs_stream_kernel<float><<<grid, kThreads + kFinishers, sizeof(StreamShared), s>>>(a);
+            token_logprobs_stream_kernel<float><<<grid, kReaders + kFinishers, sizeof(StreamShared), s>>>(a);
         return cudaGetLastError();
     }
     cudaLaunchConfig_t c{};
