@@ -59,6 +59,7 @@ def test_append_refusals(L):
     assert L.moe_kv_append(None, R(_append()), None, None) == 1
     assert L.moe_kv_append(R(_cache()), None, None, None) == 1
     assert L.moe_kv_append(R(_cache()), R(_append(T=0)), None, None) == 0
+    assert L.moe_kv_append(R(_cache()), R(_append(T=0, n_seqs=0, max_pages=0)), None, None) == 0
 
 
 def test_attention_refusals(L):
@@ -92,6 +93,7 @@ def test_attention_refusals(L):
     assert call(_cache(), att(), ws=FAKE + 16) == 3
     assert call(_cache(), att(), nb=n - 1) == 4
     assert call(_cache(), att(B=0)) == 0
+    assert call(_cache(), att(B=0, max_pages=0)) == 0
     assert L.moe_paged_attention(None, R(att()), P(FAKE), n, None) == 1
     assert L.moe_paged_attention(R(_cache()), None, P(FAKE), n, None) == 1
     assert L.moe_paged_attention_workspace_init(None, n, None) == 1

@@ -52,13 +52,12 @@ moe_status_t moe_kv_append(const moe_kv_cache_t* c, const moe_append_t* p, int32
 {
     moe_status_t st = check_cache(c);
     if (st != MOE_OK) return st;
-    if (!p || p->T < 0 || p->n_seqs <= 0 || p->max_pages <= 0 || p->n_heads < 0 ||
-        p->table_stride < 0 || (p->flags & ~MOE_ROTATE_INTERLEAVED) != 0)
+    if (!p || p->T < 0 || p->n_seqs < 0 || p->max_pages < 0 || p->n_heads < 0 || p->table_stride < 0 || (p->flags & ~MOE_ROTATE_INTERLEAVED) != 0)
         return MOE_ERR_INVALID_ARG;
     if (p->rot_dim < 0 || p->rot_dim > c->head_dim || p->rot_dim % 16 != 0 || p->n_heads > kMaxHeads)
         return MOE_ERR_UNSUPPORTED;
     if (p->T == 0) return MOE_OK;
-    if (!p->pos || !p->page_table || !p->k || !p->v || (p->rot_dim > 0 && !p->phase)) return MOE_ERR_INVALID_ARG;
+    if (p->max_pages == 0 || !p->pos || !p->page_table || !p->k || !p->v || (p->rot_dim > 0 && !p->phase)) return MOE_ERR_INVALID_ARG;
     if ((p->n_heads > 0) != (p->q != nullptr) || (p->n_heads > 0) != (p->q_out != nullptr)) return MOE_ERR_INVALID_ARG;
     if (!p->seq && p->T > p->n_seqs) return MOE_ERR_INVALID_ARG;
     const int64_t strides[] = {p->q_token_stride, p->q_head_stride, p->k_token_stride,     p->k_head_stride,
@@ -126,7 +125,7 @@ moe_status_t moe_paged_attention(const moe_kv_cache_t* c, const moe_attention_t*
 {
     moe_status_t st = check_cache(c);
     if (st != MOE_OK) return st;
-    if (!p || p->B < 0 || p->n_heads <= 0 || p->n_heads % c->n_kv_heads != 0 || p->max_pages <= 0 || p->window < 0 ||
+    if (!p || p->B < 0 || p->n_heads <= 0 || p->n_heads % c->n_kv_heads != 0 || p->max_pages < 0 || p->window < 0 ||
         p->table_stride < 0 || !isfinite(p->scale))
         return MOE_ERR_INVALID_ARG;
     // the kernel's place of a row in a page is a 32-bit byte offset
@@ -138,7 +137,7 @@ moe_status_t moe_paged_attention(const moe_kv_cache_t* c, const moe_attention_t*
     if (!aligned(ws, 256)) return MOE_ERR_MISALIGNED;
     if (ws_bytes < paged_attention_ws_bytes(c->head_dim)) return MOE_ERR_WORKSPACE;
     if (p->B == 0) return MOE_OK;
-    if (!p->seq_len || !p->page_table || !p->q || !p->out) return MOE_ERR_INVALID_ARG;
+    if (p->max_pages == 0 || !p->seq_len || !p->page_table || !p->q || !p->out) return MOE_ERR_INVALID_ARG;
     if (!aligned(p->q, 16) || !aligned(p->out, 16) || p->q_token_stride % 8 || p->q_head_stride % 8 ||
         p->out_token_stride % 8 || p->out_head_stride % 8)
         return MOE_ERR_MISALIGNED;
