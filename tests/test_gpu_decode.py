@@ -239,6 +239,10 @@ ATT = [
     ([250, 2], 6, 3, 256, 8, True, True, 0),
     ([40] * 400, 4, 2, 64, 16, False, True, 0),         # many short sequences
     ([20000] + [1] * 37, 8, 2, 128, 64, False, True, 0),   # one long one among short ones
+    ([9000, 8000, 10001], 4, 1, 128, 16, False, True, 0),  # parts in groups, items that share a block
+    ([3001] * 5, 2, 1, 64, 32, False, False, 0),
+    ([7000, 9000], 20, 2, 64, 16, True, True, 8000),
+    ([12345], 16, 2, 256, 48, False, True, 0),
 ]
 
 

@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
             const bool starts = cw.off >= lo, ends = cw.off + cw.n <= hi, whole = starts && ends;
             constexpr int kSlot = 16 * D + 32;                                   // floats per part
             float* const slots = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kAttentionCtrlBytes);
-            float* const part = slots + (2 * static_cast<size_t>(blockIdx.x) + (starts ? 1 : 0)) * kSlot;
+            float* const part = slots + (3 * static_cast<size_t>(blockIdx.x) + (starts ? 1 : 0)) * kSlot;
 #pragma unroll
             for (int hh = 0; hh < kCols; ++hh) {
 #pragma unroll
@@ -844,80 +844,92 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                 }
             }
             if (!whole) {
-                // the last of the item's blocks (first .. first + parts - 1) joins the parts, in their order
-                __syncthreads();
+                // the last of the item's blocks (first .. first + parts - 1) joins the parts, in their order; when
+                // they are many, the last of each group of blocks joins the group's first
                 const unsigned first = starts ? blockIdx.x : static_cast<unsigned>(quotient(cw.off, run));
                 const int parts = static_cast<int>((ends ? blockIdx.x : static_cast<unsigned>(quotient(cw.off + cw.n - 1, run))) - first) + 1;
-                if (threadIdx.x == 0) {
-                    unsigned* counter = reinterpret_cast<unsigned*>(static_cast<char*>(a.ws) + 256) + first;
-                    s_last = count_arrival(counter, parts - 1) == static_cast<unsigned>(parts - 1);   // back to 0 by itself
-                }
-                __syncthreads();
-                if (s_last) {
-                    const float* base = slots + 2 * static_cast<size_t>(first) * kSlot;
-                    auto slot_of = [&](int k) { return base + (2 * static_cast<size_t>(k) + (k == 0 ? 1 : 0)) * kSlot; };
-                    float2* const s_row = s_ml;   // per head: maximum, 1 / sum
-                    // eight lanes to a head, each with every eighth part
-                    for (int r = threadIdx.x / 8; r < 16; r += kThreads / 8) {
-                        float M = -INFINITY, L = 0.0f;
-                        if (r < live_heads)
-                            for (int k0 = lane & 7; k0 < parts; k0 += 32) {
-                                float2 ml[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    ml[k] = k0 + 8 * k < parts ? __ldcg(reinterpret_cast<const float2*>(slot_of(k0 + 8 * k) + 16 * D + 2 * r))
-                                                               : make_float2(-INFINITY, 0.0f);
-                                float mn = M;
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) mn = fmaxf(mn, ml[k].x);
-                                const float at = mn == -INFINITY ? 0.0f : mn;
-                                L *= exp2_fast(M - at);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) L += ml[k].y * exp2_fast(ml[k].x - at);
-                                M = mn;
-                            }
-#pragma unroll
-                        for (int off = 4; off >= 1; off >>= 1) {
-                            const float M2 = __shfl_xor_sync(0xffffffffu, M, off), L2 = __shfl_xor_sync(0xffffffffu, L, off);
-                            const float mn = fmaxf(M, M2), at = mn == -INFINITY ? 0.0f : mn;
-                            L = L * exp2_fast(M - at) + L2 * exp2_fast(M2 - at);
-                            M = mn;
-                        }
-                        if ((lane & 7) == 0 && r < live_heads) {
-                            s_row[r] = make_float2(M == -INFINITY ? 0.0f : M, L == 0.0f ? 0.0f : 1.0f / L);
-                            if (a.lse)
-                                a.lse[static_cast<long long>(cw.b) * a.n_heads + head0 + r] =
-                                    L == 0.0f ? -INFINITY : ((kE4m3 ? M - kShift : M) + log2f(L)) * kLn2;
-                        }
-                    }
+                const int mine = static_cast<int>(blockIdx.x - first);
+                unsigned* const counters = reinterpret_cast<unsigned*>(static_cast<char*>(a.ws) + 256) + first;
+                // whether this block's arrival is the last of `count`, for all its threads
+                auto last_of = [&](unsigned* counter, int count) {
                     __syncthreads();
+                    if (threadIdx.x == 0) s_last = count_arrival(counter, count - 1) == static_cast<unsigned>(count - 1);
+                    __syncthreads();
+                    return s_last != 0;
+                };
+                // Results k0, k0 + stride, .. of the item, `count` of them: to the output, or to k0's group result.
+                constexpr int kLoads = S::kCtas == 4 ? 4 : 8;   // results whose loads are in flight, as registers allow
+                auto join = [&](int k0, int count, int stride, bool grouped, bool final) {
+                    auto slot_of = [&](int i) {
+                        const int k = k0 + i * stride;
+                        return slots + (3 * static_cast<size_t>(first + k) + (grouped ? 2 : k == 0 ? 1 : 0)) * kSlot;
+                    };
                     for (int at = threadIdx.x; at < live_heads * (D / 4); at += kThreads) {
                         const int r = at / (D / 4), d = at % (D / 4) * 4;
-                        const float2 row = s_row[r];
+                        float M = -INFINITY, L = 0.0f;
                         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        for (int k0 = 0; k0 < parts; k0 += 8) {   // eight parts' loads at a time
-                            float f[8];
-                            float4 y[8];
+                        for (int i0 = 0; i0 < count; i0 += kLoads) {
+                            float2 ml[kLoads];
+                            float4 y[kLoads];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const float* p = slot_of(min(k0 + k, parts - 1));
-                                f[k] = __ldcg(p + 16 * D + 2 * r);
-                                y[k] = __ldcg(reinterpret_cast<const float4*>(p + r * D + d));
+                            for (int i = 0; i < kLoads; ++i) {
+                                const float* p = slot_of(min(i0 + i, count - 1));
+                                ml[i] = __ldcg(reinterpret_cast<const float2*>(p + 16 * D + 2 * r));
+                                y[i] = __ldcg(reinterpret_cast<const float4*>(p + r * D + d));
                             }
+                            float mn = M;
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const float w = exp2_fast(f[k] - row.x);
-                                if (k0 + k < parts) {
-                                    x.x += y[k].x * w;
-                                    x.y += y[k].y * w;
-                                    x.z += y[k].z * w;
-                                    x.w += y[k].w * w;
+                            for (int i = 0; i < kLoads; ++i) mn = fmaxf(mn, ml[i].x);   // (a repeated one changes nothing)
+                            const float ref = mn == -INFINITY ? 0.0f : mn, fix = exp2_fast(M - ref);
+                            L *= fix;
+                            x.x *= fix;
+                            x.y *= fix;
+                            x.z *= fix;
+                            x.w *= fix;
+                            M = mn;
+#pragma unroll
+                            for (int i = 0; i < kLoads; ++i) {
+                                const float w = exp2_fast(ml[i].x - ref);
+                                if (i0 + i < count) {
+                                    L += ml[i].y * w;
+                                    x.x += y[i].x * w;
+                                    x.y += y[i].y * w;
+                                    x.z += y[i].z * w;
+                                    x.w += y[i].w * w;
                                 }
                             }
                         }
-                        *reinterpret_cast<uint2*>(a.out + cw.b * a.out_token_stride + (head0 + r) * a.out_head_stride + d) =
-                            make_uint2(pack_bf16x2(x.x * row.y, x.y * row.y), pack_bf16x2(x.z * row.y, x.w * row.y));
+                        if (final) {
+                            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+                            *reinterpret_cast<uint2*>(a.out + cw.b * a.out_token_stride + (head0 + r) * a.out_head_stride + d) =
+                                make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+                            if (d == 0 && a.lse)
+                                a.lse[static_cast<long long>(cw.b) * a.n_heads + head0 + r] =
+                                    L == 0.0f ? -INFINITY : ((kE4m3 ? M - kShift : M) + log2f(L)) * kLn2;
+                        } else {
+                            float* to = slots + (3 * static_cast<size_t>(first + k0) + 2) * kSlot;
+                            *reinterpret_cast<float4*>(to + r * D + d) = x;
+                            if (d == 0) *reinterpret_cast<float2*>(to + 16 * D + 2 * r) = make_float2(M, L);
+                        }
                     }
+                };
+                // groups of about the square root of the parts; none of one block, whose counter and result could meet
+                // those of the next item, which starts in this item's last block
+                int group = parts;
+                if (parts > 16)
+                    for (group = 8; group * group < parts || parts % group == 1;) ++group;
+                const int groups = (parts + group - 1) / group;
+                bool final = groups == 1;
+                int k0 = mine / group * group, count = min(group, parts - k0), stride = 1;
+                unsigned* counter = final ? counters : counters + kAttentionCtas + k0;
+                while (last_of(counter, count)) {
+                    join(k0, count, stride, stride > 1, final);
+                    if (final) break;
+                    final = true;
+                    counter = counters;
+                    k0 = 0;
+                    count = groups;
+                    stride = group;
                 }
             }
             __syncthreads();   // the shared rows are free for the next item
@@ -971,7 +983,7 @@ cudaError_t launch_d(const AttentionArgs& a, cudaStream_t s)
 size_t paged_attention_ws_bytes(int head_dim)
 {
     if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
-    return kAttentionCtrlBytes + 2 * static_cast<size_t>(kAttentionCtas) * (16 * head_dim + 32) * 4;
+    return kAttentionCtrlBytes + 3 * static_cast<size_t>(kAttentionCtas) * (16 * head_dim + 32) * 4;
 }
 
 cudaError_t launch_paged_attention(const AttentionArgs& a, int head_dim, bool e4m3, cudaStream_t s)

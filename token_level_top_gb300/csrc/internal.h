@@ -311,7 +311,7 @@ struct AttentionArgs {
     int page_shift;
 };
 // The attention workspace starts with the status word and the counters of the join.
-constexpr size_t kAttentionCtrlBytes = 4096;
+constexpr size_t kAttentionCtrlBytes = 8192;
 size_t paged_attention_ws_bytes(int head_dim);   // 0: unsupported head_dim
 cudaError_t launch_paged_attention(const AttentionArgs& a, int head_dim, bool e4m3, cudaStream_t s);
 
