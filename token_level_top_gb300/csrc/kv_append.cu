@@ -244,7 +244,9 @@ cudaError_t launch_d(const AppendArgs& a, bool e4m3, cudaStream_t s)
 cudaError_t launch_kv_append(AppendArgs a, int head_dim, bool e4m3, cudaStream_t s)
 {
     if (a.T <= 0) return cudaSuccess;
-    // one warp per token, more (down to kRows rows each) while the tokens alone do not fill the machine
+    // One warp per token, more (down to kRows rows each) while the tokens alone do not fill the machine: 24 warps an SM in
+    // all (32 + 8 + 8 heads, us with 1 / 2 / 4 / 12 warps a token: 8 tokens 6.9 / 5.2 / 4.0 / 3.1, 300 tokens 7.2 / 5.1 /
+    // 4.2 / 4.1, 1000 tokens 7.2 / 7.0 / 7.0 / 8.6, 4000 tokens 20.0 / 20.9 / 25.5 / 32.1).
     const int groups = (a.n_heads + 2 * a.n_kv_heads + 512 / head_dim - 1) / (512 / head_dim);
     const int want = static_cast<int>((24LL * num_sms() + a.T - 1) / a.T);
     a.parts = want < 1 ? 1 : (want > groups ? groups : want);

@@ -23,7 +23,8 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;   // of a block that reads a row (or its share) alone
+constexpr int kThreads = 256, kWarps = kThreads / 32;   // of a block that reads a row (or its share) alone,
+constexpr int kBlocks = 5;         // and how many of those an SM holds
 constexpr int kBatch = 4;          // 16-byte pieces that a thread has in flight
 constexpr int kMaxima = 2048;       // maxima kept of a row, at most 2048 / readers per reader
 constexpr int kMaxFound = 1024;    // values at or above the threshold that are ranked at once
@@ -528,7 +529,7 @@ struct Result {
 
 // A row to a block, or to a cluster of a.split blocks.
 template <class T, bool kTop>
-__global__ void __launch_bounds__(kThreads, 5) token_logprobs_kernel(const LogprobArgs a)
+__global__ void __launch_bounds__(kThreads, kBlocks) token_logprobs_kernel(const LogprobArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     Shared& s = *reinterpret_cast<Shared*>(smem);
@@ -720,13 +721,17 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t s)
 {
     if (args.rows <= 0) return cudaSuccess;
     LogprobArgs a = args;
-    // few rows: a cluster of blocks per row, while that leaves a block two pieces per thread at least and
-    // the rows' blocks still fit the machine at once
+    // Few rows: a cluster of blocks per row, while a block keeps 8 pieces per thread and the rows' blocks are at most two
+    // an SM.  Long rows gain (us for the 20 best of bf16 rows, with 1 / 2 / 4 / 8 blocks a row: one row of 131072 14.4 /
+    // 11.5 / 9.8 / 9.9, 128 rows 21.0 / 16.5 / 17.8 / 27.5); short ones and many rows lose (one row of 32000 8.2 / 8.7 /
+    // 8.6 / 8.6, 256 rows 11.3 / 14.7 / 23.0 / 23.1; of 131072 24.9 / 23.7 / 32.3 / 50.4).
     const long long pieces = static_cast<long long>(a.vocab) * (a.bf16 ? 2 : 4) / 16;
     a.split = 1;
-    while (a.split < 8 && a.rows * a.split * 2 <= 4LL * num_sms() && pieces / (a.split * 2) >= 2 * kThreads) a.split *= 2;
+    while (a.split < 8 && a.rows * a.split <= num_sms() && pieces / (a.split * 2) >= 8 * kThreads) a.split *= 2;
     if (a.rows * a.split > 0x7fffffffLL) return cudaErrorInvalidValue;
-    if (a.n_top > 0 && a.rows > kStreamBlocks * static_cast<long long>(num_sms())) {   // more rows than blocks fit: read ahead of the alternatives
+    // More rows than blocks of the other kernel fit at once: rows are read ahead of their alternatives (20 best of 131072
+    // bf16: 760 rows 43.5 us, 48.0 streamed; 800 rows 57.4 and 49.4; 4096 rows 202 and 186).
+    if (a.n_top > 0 && a.rows > kBlocks * static_cast<long long>(num_sms())) {
         const unsigned grid = static_cast<unsigned>(kStreamBlocks * num_sms());
         if (a.bf16)
             token_logprobs_stream_kernel<__nv_bfloat16><<<grid, kReaders + kFinishers, sizeof(StreamShared), s>>>(a);
