@@ -243,6 +243,9 @@ ATT = [
     ([3001] * 5, 2, 1, 64, 32, False, False, 0),
     ([7000, 9000], 20, 2, 64, 16, True, True, 8000),
     ([12345], 16, 2, 256, 48, False, True, 0),
+    ([0, 1, 0, 0, 65, 2] * 90, 6, 3, 128, 16, False, True, 0),   # runs that begin or end between items
+    ([300, 1, 129] * 70, 4, 2, 64, 16, True, False, 0),
+    ([777], 4, 4, 256, 16, True, True, 0),
 ]
 
 

@@ -6,10 +6,10 @@
 //
 // Work: the live keys of every (sequence, key head, block of query heads) are
 // cut into granules of 4 tiles, one per warp.  The granules of the whole batch, in
-// that order, are dealt out in equal runs to the blocks that fit the GPU at once
-// (2 to 4 an SM), whatever the lengths: each block finds its run from the lengths
-// alone (a scan over them), so nothing is planned on the host and a captured graph
-// follows the lengths.
+// that order and with a gap for the end of each item, are dealt out in equal runs
+// to the blocks that fit the GPU at once (2 to 4 an SM), whatever the lengths: each
+// block finds its run from the lengths alone (a scan over them), so nothing is
+// planned on the host and a captured graph follows the lengths.
 // A run may end inside an item; such an item's parts (maximum, sum and
 // unnormalised output) go to the workspace and the block that finishes last
 // joins them, always in the same order.
@@ -41,7 +41,7 @@
 // Measured (32 query heads on 8, D = 128, 6801 GB/s copied): 64 sequences up to
 // 8192, bf16, 1083 MB in 166 us (0.96 of the copy rate); one of 131072, 537 MB in
 // 89 us (0.88: the start and the join of 456 parts); 256 up to 4096, e4m3, 1091 MB
-// in 212 us (0.76).  The bf16 kernel waits for its copies (issue slots 30% busy).
+// in 179 us (0.90).  The bf16 kernel waits for its copies (issue slots 30% busy).
 // The e4m3 one has half the bytes per key and the same products on top of two
 // conversions a code pair: some 890 instructions per 32 keys, a half of its issue
 // slots, and 167 registers leave 12 warps an SM to fill them.
@@ -192,6 +192,10 @@ struct Shape {
     // 256 sequences up to 4096)
     static constexpr int kAhead = kE4m3 ? 1 : 2;
     static constexpr int kGranule = kTileKeys * kWarps;       // keys
+    // What an item costs beside its granules (the block's join of its warps, the output or the part): so many places of
+    // the list are left empty behind it.  With none the blocks that met the most items set the time (64 + 8 heads of
+    // 128, e4m3, 256 sequences up to 4096: 209 us; 1 185, 2 180, 3 182; 512 up to 1024: 149, 127, 122, 126).
+    static constexpr int kGap = 2;
     static constexpr int kJoin = D == 64 && kHeads == 16 ? 8 : 4;   // heads that the block joins at a time, as memory allows
     static constexpr int kMerge = kWarps * kJoin * D * 4;
     // beside a tile: which of its keys are live, and the exponent bytes of its e4m3 keys and values
@@ -221,7 +225,7 @@ struct Walk {
     int b, hk, block;    // sequence, key head, block of query heads
     int len, first, n;   // its live keys [first, len) and its granules (per key head and block)
     int g;               // granule within the item
-    long long off;       // the item's first granule in the whole list
+    long long off;       // the item's first place in the whole list
     // Tiles start at multiples of 16, so that with pages of 16 k tokens the 16 keys of a part lie in one page.
     __device__ __forceinline__ int base() const { return first & ~15; }
 };
@@ -247,19 +251,26 @@ __device__ __forceinline__ int granules_of(const AttentionArgs& a, int len)
     return static_cast<int>((static_cast<unsigned>(len - (first_key(a, len) & ~15)) + kGranule - 1) / kGranule);
 }
 
-template <int kGranule>
+template <class S>
 __device__ __forceinline__ void load_item(const AttentionArgs& a, Walk& w)
 {
     w.len = clamped_len(a, w.b, false);
     w.first = first_key(a, w.len);
-    w.n = granules_of<kGranule>(a, w.len);
+    w.n = granules_of<S::kGranule>(a, w.len);
+}
+
+// Places of an item of n granules in the list.
+template <class S>
+__device__ __forceinline__ int places_of(int n)
+{
+    return n ? n + S::kGap : 0;
 }
 
 // To the next item; past the end of the batch the walk stays behind its last one (n = 0).
-template <int kGranule>
+template <class S>
 __device__ __forceinline__ void next_item(const AttentionArgs& a, Walk& w, int blocks)
 {
-    w.off += w.n;
+    w.off += places_of<S>(w.n);
     w.g = 0;
     if (++w.block < blocks) return;
     w.block = 0;
@@ -270,7 +281,7 @@ __device__ __forceinline__ void next_item(const AttentionArgs& a, Walk& w, int b
             w.n = 0;
             return;
         }
-        load_item<kGranule>(a, w);
+        load_item<S>(a, w);
     } while (w.n == 0);
 }
 
@@ -293,12 +304,12 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
     const int blocks = (group + kHeads - 1) / kHeads;           // head blocks per key head
     const int heads = a.n_kv_heads * blocks;                    // items per sequence
 
-    // ---- the batch's granules, and where this block's run begins
+    // ---- the batch's places, and where this block's run begins
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
     long long mine = 0;
     for (int b = b0; b < b1; ++b)
-        mine += granules_of<S::kGranule>(a, clamped_len(a, b, blockIdx.x == 0));
+        mine += places_of<S>(granules_of<S::kGranule>(a, clamped_len(a, b, blockIdx.x == 0)));
     long long incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -323,32 +334,34 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
         total += s_scan[i];
     }
     const long long all = total * heads;
-    const long long run = quotient(all + gridDim.x - 1, gridDim.x);    // granules per block
+    const long long run = quotient(all + gridDim.x - 1, gridDim.x);    // places per block
     const long long lo = run * blockIdx.x, hi = min(all, lo + run);
     if (lo >= hi) return;
     if (mine > 0 && before * heads <= lo && lo < (before + mine) * heads) {
         Walk w{};
         w.b = b0;
         w.off = before * heads;
-        load_item<S::kGranule>(a, w);
-        while (w.off + static_cast<long long>(w.n) * heads <= lo) {
-            w.off += static_cast<long long>(w.n) * heads;
+        load_item<S>(a, w);
+        while (w.off + static_cast<long long>(places_of<S>(w.n)) * heads <= lo) {
+            w.off += static_cast<long long>(places_of<S>(w.n)) * heads;
             ++w.b;
-            load_item<S::kGranule>(a, w);
+            load_item<S>(a, w);
         }
-        const int h = static_cast<int>(quotient(lo - w.off, w.n));
+        const int h = static_cast<int>(quotient(lo - w.off, places_of<S>(w.n)));
         w.hk = h / blocks;
         w.block = h - w.hk * blocks;
-        w.off += static_cast<long long>(h) * w.n;
+        w.off += static_cast<long long>(h) * places_of<S>(w.n);
         w.g = static_cast<int>(lo - w.off);
+        if (w.g >= w.n) next_item<S>(a, w, blocks);
         s_start = w;
     }
     __syncthreads();
+    if (s_start.off + s_start.g >= hi) return;   // nothing but gaps
 
     const uint32_t ring = smem_u32(smem) + warp * kSlots * S::kTile;
     unsigned char* const meta = s_meta + warp * kMetas * S::kMeta;
     Walk iw = s_start, cw = s_start;
-    const int count = static_cast<int>(hi - lo);
+    int left = static_cast<int>(hi - cw.off) - cw.g, to_copy = left;   // places from the walks to the end of the run
 
     // ---- the copying side
     constexpr int kElt = kE4m3 ? 1 : 2;
@@ -477,8 +490,10 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
         if (lane == 0) *reinterpret_cast<uint32_t*>(to + S::kMask) = rows_live;
         imeta = imeta + 1 == kMetas ? 0 : imeta + 1;
         next_key += S::kGranule;
+        --to_copy;
         if (uniform(++iw.g == iw.n)) {
-            next_item<S::kGranule>(a, iw, blocks);
+            to_copy -= S::kGap;
+            next_item<S>(a, iw, blocks);
             if (iw.n > 0) {
                 start_item();
                 look_up(0);
@@ -496,11 +511,15 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
         for (int h = 0; h < S::kParts; ++h)
             copy_part(to_v + slot + h * S::kPart, 64, row_v[h], rows_live >> (16 * h) & 0xffffu, static_cast<const char*>(a.v));
     };
-    // The run as a sequence of 2 * count tiles (keys, values, keys, ...): number k goes to slot k % kSlots,
-    // issued when number k - kSlots has been used.
-    auto issue_number = [&](int k, bool values, uint32_t slot) {
-        if (!values) store_exponents();
-        if (uniform(k < 2 * count)) {
+    // The run as a sequence of tiles (keys, values, keys, ...): number k goes to slot k % kSlots, issued when number
+    // k - kSlots has been used.
+    bool keys_issued = false;
+    auto issue_next = [&](bool values, uint32_t slot) {
+        if (!values) {
+            store_exponents();
+            keys_issued = uniform(to_copy > 0);
+        }
+        if (keys_issued) {
             if (values)
                 issue_values(slot);
             else
@@ -535,7 +554,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
     look_up(0);
     if (S::kAhead == 2) look_up(S::kAhead - 1);
 #pragma unroll 1
-    for (int k = 0; k < kSlots; ++k) issue_number(k, (k & 1) != 0, k * S::kTile);
+    for (int k = 0; k < kSlots; ++k) issue_next((k & 1) != 0, k * S::kTile);
 
     // ---- the computing side
     float qscale[kCols][2];           // scores in units of log2: accumulator * qscale (* the key's exponent)
@@ -544,9 +563,9 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
     float ref[kCols][2], limit[kCols][2];   // what the exponents are taken against, and the score that raises m
     uint32_t slot = 0;                // byte offset in the ring
     int cmeta = 0;
-    for (int i = 0; i < count; ++i) {
+    for (bool first_tile = true; left > 0; first_tile = false) {
         const int head0 = cw.hk * group + cw.block * kHeads, live_heads = min(kHeads, group - cw.block * kHeads);
-        if (uniform(i == 0 || cw.g == 0)) {    // a new item
+        if (uniform(first_tile || cw.g == 0)) {    // a new item
 #pragma unroll
             for (int hh = 0; hh < kCols; ++hh) {
 #pragma unroll
@@ -622,14 +641,15 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
             }
         }
         __syncwarp();
-        issue_number(2 * i + kSlots, kOdd, slot);
+        issue_next(kOdd, slot);
         slot = slot + S::kTile == kSlots * S::kTile ? 0 : slot + S::kTile;
 
         // Q of the block's next item arrives while this one ends
         const bool last = uniform(cw.g + 1 == cw.n);
         Walk nw = cw;
-        if (last && i + 1 < count) {
-            next_item<S::kGranule>(a, nw, blocks);
+        left -= last ? 1 + S::kGap : 1;
+        if (last && left > 0) {
+            next_item<S>(a, nw, blocks);
             load_q(nw);
         }
 
@@ -776,11 +796,11 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                 }
             }
         __syncwarp();
-        issue_number(2 * i + 1 + kSlots, !kOdd, slot);
+        issue_next(!kOdd, slot);
         slot = slot + S::kTile == kSlots * S::kTile ? 0 : slot + S::kTile;
 
         // ---- the end of an item, or of this block's part of it
-        if (last || i + 1 == count) {
+        if (last || left <= 0) {
             const bool starts = cw.off >= lo, ends = cw.off + cw.n <= hi, whole = starts && ends;
             constexpr int kSlot = 16 * D + 32;                                   // floats per part
             float* const slots = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kAttentionCtrlBytes);
@@ -966,7 +986,7 @@ cudaError_t launch_heads(const AttentionArgs& a, cudaStream_t s)
     const long long items = static_cast<long long>(a.B) * a.n_kv_heads * ((group + kHeads - 1) / kHeads);
     const long long granules = (keys + 15 + S::kGranule - 1) / S::kGranule;
     long long grid = std::min(num_sms() * S::kCtas, kAttentionCtas);
-    if (items < grid && granules < grid && items * granules < grid) grid = items * granules;
+    if (items < grid && granules < grid && items * (granules + S::kGap) < grid) grid = items * (granules + S::kGap);
     AttentionArgs b = a;
     // key / page_size for 0 <= key < 2^31 as a product and a shift: with 2^l the power of two at or above
     // page_size and mul = ceil(2^(31 + l) / page_size), mul * page_size exceeds 2^(31 + l) by less than 2^l
