@@ -181,8 +181,10 @@ struct Shape {
     static constexpr int kCols = kHeads <= 8 ? 1 : 2;         // column tiles of 8
     static constexpr int kOut = D / 16 * 4 * kCols;           // output registers
     static constexpr int kWarps = 4;
-    // blocks per SM, as the registers of outputs and queries allow: 128, 168 or 255 a thread
-    static constexpr int kCtas = kOut + D / 8 * kCols <= 24 ? 4 : (kOut + D / 8 * kCols <= 48 ? 3 : 2);
+    // blocks per SM, as the registers of outputs and queries allow: 128, 168 or 255 a thread (16 heads of 64, e4m3, whose
+    // conversions need more beside them: 64 sequences up to 8192 in 53 us, 69 with three blocks that spill)
+    static constexpr int kHeld = kOut + D / 8 * kCols;
+    static constexpr int kCtas = kHeld <= 24 ? 4 : (kHeld <= 48 && !(kE4m3 && kCols == 2) ? 3 : 2);
     // 16-key parts of a tile: two where a row is short, so that a pass of the loop does twice the work
     static constexpr int kParts = kRow <= 128 ? 2 : 1;
     static constexpr int kPart = 16 * kRow;                   // bytes of 16 keys
