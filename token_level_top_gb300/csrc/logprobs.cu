@@ -39,6 +39,28 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+// Two floats of a packed instruction, each rounded as a single one's.
+struct Pair {
+    float x, y;
+};
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c)
+{
+    Pair r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b)
+{
+    Pair r;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
 // max that keeps NaN
 __device__ __forceinline__ float max_nan(float a, float b)
 {
@@ -427,23 +449,22 @@ __device__ __forceinline__ Stats read_pieces(const Row<T>& row, int lo, int hi, 
         st.raise(fmaxf(st.m, top));
         if (!st.far()) {
             const float minus_base = -st.base();
-            float l2 = 0.0f, w2 = 0.0f;   // a second pair of sums halves the chains
+            // two sums each, of even and odd places, in packed pairs: one instruction for two values
+            Pair l = {st.l, 0.0f}, w = {st.w, 0.0f};
+            const Pair log2e = {kLog2e, kLog2e}, from = {minus_base, minus_base};
 #pragma unroll
             for (int j = 0; j < kPieces; ++j) {
                 float x[kN];
                 Piece<T>::unpack(Piece<T>::floored(v[j]), x);
 #pragma unroll
                 for (int i = 0; i < kN; i += 2) {
-                    const float z0 = fmaf(x[i], kLog2e, minus_base), z1 = fmaf(x[i + 1], kLog2e, minus_base);
-                    const float e0 = exp2_fast(z0), e1 = exp2_fast(z1);
-                    st.l += e0;
-                    l2 += e1;
-                    st.w = fmaf(e0, z0, st.w);
-                    w2 = fmaf(e1, z1, w2);
+                    const Pair z = fma(Pair{x[i], x[i + 1]}, log2e, from), e = {exp2_fast(z.x), exp2_fast(z.y)};
+                    l = add(l, e);
+                    w = fma(e, z, w);
                 }
             }
-            st.l += l2;
-            st.w += w2;
+            st.l = l.x + l.y;
+            st.w = w.x + w.y;
         } else {
 #pragma unroll
             for (int j = 0; j < kPieces; ++j) {
