@@ -318,31 +318,32 @@ __device__ void find_best(Finder& s, const float* tops, uint64_t* keys, const Ro
     int strict = 0;
     for (;; ++strict) {
         auto reaches = [&](float x) { return any || (strict ? x > level_value : x >= level_value); };
-        // the entries' pieces, one per thread and step, four steps' loads in flight
-        const int per_entry = per_group * kBatch, all = entries * per_entry;
-        for (int q0 = t; q0 < all; q0 += 4 * NT) {
-            uint4 v[4];
-            int first[4];
+        // the entries' pieces, one per thread and step (a batch's to neighbours), four steps' loads in flight
+        constexpr int kStep = NT / kBatch;
+        for (int b = 0; b < per_group; ++b) {
+            for (int e0 = t / kBatch; e0 < entries; e0 += 4 * kStep) {
+                uint4 v[4];
+                int first[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int q = q0 + j * NT;
-                const int e = q < all ? s.entry[q / per_entry] : 0;
-                const int piece = lo + e % R + R * (e / R * per_entry + q % per_entry);
-                first[j] = q < all && piece < hi ? row.head + piece * kN : -1;
-                v[j] = first[j] >= 0 ? __ldg(row.body + piece) : Piece<T>::nothing();
-            }
+                for (int j = 0; j < 4; ++j) {
+                    const int at = e0 + j * kStep, e = at < entries ? s.entry[at] : 0;
+                    const int piece = lo + e % R + R * ((e / R * per_group + b) * kBatch + t % kBatch);
+                    first[j] = at < entries && piece < hi ? row.head + piece * kN : -1;
+                    v[j] = first[j] >= 0 ? __ldg(row.body + piece) : Piece<T>::nothing();
+                }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (first[j] < 0 || !reaches(Piece<T>::top(v[j]))) continue;
-                float x[kN];
-                Piece<T>::unpack(v[j], x);
-                int count = 0;
+                for (int j = 0; j < 4; ++j) {
+                    if (first[j] < 0 || !reaches(Piece<T>::top(v[j]))) continue;
+                    float x[kN];
+                    Piece<T>::unpack(v[j], x);
+                    int count = 0;
 #pragma unroll
-                for (int i = 0; i < kN; ++i) count += reaches(x[i]);
-                int place = atomicAdd(&s.found, count);
+                    for (int i = 0; i < kN; ++i) count += reaches(x[i]);
+                    int place = atomicAdd(&s.found, count);
 #pragma unroll
-                for (int i = 0; i < kN; ++i)
-                    if (reaches(x[i]) && place++ < kMaxFound) keys[place - 1] = key_of(order_of(x[i]), first[j] + i);
+                    for (int i = 0; i < kN; ++i)
+                        if (reaches(x[i]) && place++ < kMaxFound) keys[place - 1] = key_of(order_of(x[i]), first[j] + i);
+                }
             }
         }
         if (edge >= 0 && reaches(edge_value)) {
