@@ -110,6 +110,10 @@ struct Piece<float> {
     {
         return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
     }
+    static __device__ __forceinline__ float at(const uint4 v, int i)
+    {
+        return __uint_as_float(i & 2 ? (i & 1 ? v.w : v.z) : (i & 1 ? v.y : v.x));
+    }
     static __device__ __forceinline__ float top(const uint4 v)
     {
         return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
@@ -140,6 +144,11 @@ struct Piece<__nv_bfloat16> {
     static __device__ __forceinline__ uint4 pack(const float (&x)[8])
     {
         return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    }
+    static __device__ __forceinline__ float at(const uint4 v, int i)
+    {
+        const uint32_t w = i & 4 ? (i & 2 ? v.w : v.z) : (i & 2 ? v.y : v.x);
+        return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
     }
     static __device__ __forceinline__ float top(const uint4 v)
     {
@@ -275,8 +284,12 @@ __device__ void find_best(Finder& s, const float* tops, uint64_t* keys, const Ro
     constexpr int kN = Piece<T>::kN, kNTWarps = NT / 32;
     const int lane = t & 31, warp = t >> 5;
     float thread_top = -INFINITY;
-    for (int g = 0; g < groups; ++g)
-        for (int i = t; i < R; i += NT) thread_top = fmaxf(thread_top, tops[g * R + i]);
+    constexpr int kPer = R / NT;   // readers per finder
+    static_assert(R % NT == 0, "equal shares");
+    for (int g = 0; g < groups; ++g) {
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) thread_top = fmaxf(thread_top, tops[g * R + c * NT + t]);
+    }
     if (t < MOE_MAX_TOP) s.best[t] = 0;
     if (t == 0) s.entries = s.found = 0;
     // threshold: with k = ceil(n / full warps), the least of the full warps' k-th largest thread maxima is
@@ -300,7 +313,12 @@ __device__ void find_best(Finder& s, const float* tops, uint64_t* keys, const Ro
     // the maxima that reach it, listed warp by warp
     static_assert(kMaxima / NT <= 32, "a bit per maximum of a thread");
     uint32_t hits = 0;
-    for (int i = t, k = 0; i < groups * R; i += NT, ++k) hits |= static_cast<uint32_t>(any || tops[i] >= level_value) << k;
+    for (int g = 0; g < groups; ++g) {
+        uint32_t some = 0;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) some |= (any || tops[g * R + c * NT + t] >= level_value) ? 1u << c : 0u;
+        hits |= some << (g * kPer);
+    }
     const int hit_count = __popc(hits);
     int at = hit_count;
 #pragma unroll
@@ -336,13 +354,14 @@ __device__ void find_best(Finder& s, const float* tops, uint64_t* keys, const Ro
                     if (first[j] < 0 || !reaches(Piece<T>::top(v[j]))) continue;
                     float x[kN];
                     Piece<T>::unpack(v[j], x);
-                    int count = 0;
+                    uint32_t which = 0;
 #pragma unroll
-                    for (int i = 0; i < kN; ++i) count += reaches(x[i]);
-                    int place = atomicAdd(&s.found, count);
-#pragma unroll
-                    for (int i = 0; i < kN; ++i)
-                        if (reaches(x[i]) && place++ < kMaxFound) keys[place - 1] = key_of(order_of(x[i]), first[j] + i);
+                    for (int i = 0; i < kN; ++i) which |= reaches(x[i]) ? 1u << i : 0u;
+                    int place = atomicAdd(&s.found, __popc(which));
+                    for (; which; which &= which - 1, ++place) {   // one, as a rule
+                        const int i = __ffs(which) - 1;
+                        if (place < kMaxFound) keys[place] = key_of(order_of(Piece<T>::at(v[j], i)), first[j] + i);
+                    }
                 }
             }
         }
