@@ -228,11 +228,12 @@ struct Finder {
     uint16_t entry[kMaxima];
 };
 
+template <class T>
 struct Shared {
     Stats stats[kWarps];
     Finder f;
     union {
-        float top[kMaxima];                        // until the entries are listed
+        T top[kMaxima];                            // until the entries are listed
         alignas(16) uint64_t keys[kMaxFound];      // from then on
     };
 };
@@ -240,10 +241,11 @@ struct Shared {
 constexpr int kStreamBlocks = 4; // blocks per SM of the streaming kernel,
 constexpr int kReaders = 256;    // their threads that read rows
 constexpr int kFinishers = 64;  // and that finish them
+template <class T>
 struct StreamShared {
     Stats stats[2][kReaders / 32];
     Finder f;
-    float top[2][kMaxima];
+    T top[2][kMaxima];
     alignas(16) uint64_t keys[kMaxFound];
 };
 
@@ -275,20 +277,46 @@ __device__ __forceinline__ int rank_in(const uint64_t* keys, int count, uint64_t
     return rank;
 }
 
+// Maxima are kept in the logits' type.  Where a finder looks at several readers' bf16 maxima, two share a word: those of
+// readers r and r + R / 2.
+template <class T, int NT, int R>
+constexpr int maxima_in_a_word = sizeof(T) == 2 && R >= 2 * NT ? 2 : 1;
+template <class T, int NT, int R>
+__device__ __forceinline__ int maximum_place(int reader)
+{
+    return maxima_in_a_word<T, NT, R> == 2 ? reader % (R / 2) * 2 + reader / (R / 2) : reader;
+}
+
 // The best n keys of pieces [lo, hi) of a row and the edge values into s.best (0 where there are none), sorted: by
 // NT threads, from the maxima of the groups of pieces that R readers took.
 template <class T, int NT, int R>
-__device__ void find_best(Finder& s, const float* tops, uint64_t* keys, const Row<T>& row, int n, int lo, int hi,
+__device__ void find_best(Finder& s, const T* tops, uint64_t* keys, const Row<T>& row, int n, int lo, int hi,
                           int per_group, int groups, int t, int edge, float edge_value)
 {
     constexpr int kN = Piece<T>::kN, kNTWarps = NT / 32;
     const int lane = t & 31, warp = t >> 5;
     float thread_top = -INFINITY;
-    constexpr int kPer = R / NT;   // readers per finder
-    static_assert(R % NT == 0, "equal shares");
-    for (int g = 0; g < groups; ++g) {
+    // a thread looks at kWords words a group, of kWide maxima each
+    constexpr int kWide = maxima_in_a_word<T, NT, R>, kWords = R / NT / kWide, kPer = kWords * kWide;
+    static_assert(R % (NT * kWide) == 0, "equal shares");
+    auto reader = [&](int c) { return c / kWide * NT + t + c % kWide * (R / 2); };
+    auto maxima = [&](int g, float (&x)[kPer]) {
 #pragma unroll
-        for (int c = 0; c < kPer; ++c) thread_top = fmaxf(thread_top, tops[g * R + c * NT + t]);
+        for (int c = 0; c < kWords; ++c) {
+            if constexpr (kWide == 2) {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(tops + g * R + 2 * (c * NT + t));
+                x[2 * c] = __uint_as_float(w << 16);
+                x[2 * c + 1] = __uint_as_float(w & 0xffff0000u);
+            } else {
+                x[c] = static_cast<float>(tops[g * R + c * NT + t]);
+            }
+        }
+    };
+    for (int g = 0; g < groups; ++g) {
+        float x[kPer];
+        maxima(g, x);
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) thread_top = fmaxf(thread_top, x[c]);
     }
     if (t < MOE_MAX_TOP) s.best[t] = 0;
     if (t == 0) s.entries = s.found = 0;
@@ -314,9 +342,11 @@ __device__ void find_best(Finder& s, const float* tops, uint64_t* keys, const Ro
     static_assert(kMaxima / NT <= 32, "a bit per maximum of a thread");
     uint32_t hits = 0;
     for (int g = 0; g < groups; ++g) {
+        float x[kPer];
+        maxima(g, x);
         uint32_t some = 0;
 #pragma unroll
-        for (int c = 0; c < kPer; ++c) some |= (any || tops[g * R + c * NT + t] >= level_value) ? 1u << c : 0u;
+        for (int c = 0; c < kPer; ++c) some |= (any || x[c] >= level_value) ? 1u << c : 0u;
         hits |= some << (g * kPer);
     }
     const int hit_count = __popc(hits);
@@ -329,7 +359,10 @@ __device__ void find_best(Finder& s, const float* tops, uint64_t* keys, const Ro
     int begin = 0;
     if (lane == 31) begin = atomicAdd(&s.entries, at);
     at += __shfl_sync(0xffffffffu, begin, 31) - hit_count;
-    for (; hits; hits &= hits - 1) s.entry[at++] = static_cast<uint16_t>(t + (__ffs(hits) - 1) * NT);
+    for (; hits; hits &= hits - 1) {
+        const int k = __ffs(hits) - 1;
+        s.entry[at++] = static_cast<uint16_t>(k / kPer * R + reader(k % kPer));
+    }
     sync_finders<NT>();
     const int entries = s.entries;
     // (one more pass, for the values above the level alone, when those at it are too many to rank)
@@ -453,9 +486,10 @@ __device__ void find_best(Finder& s, const float* tops, uint64_t* keys, const Ro
     sync_finders<NT>();
 }
 
-// One thread's part of pieces [lo, hi) of a row: its statistics, and with kTop the maxima of its groups of pieces.
+// One thread's part of pieces [lo, hi) of a row: its statistics, and with kTop the maxima of its groups of pieces, every
+// R places from `tops` on.
 template <class T, bool kTop, int R>
-__device__ __forceinline__ Stats read_pieces(const Row<T>& row, int lo, int hi, int t, int batches, int per_group, float* tops)
+__device__ __forceinline__ Stats read_pieces(const Row<T>& row, int lo, int hi, int t, int batches, int per_group, T* tops)
 {
     constexpr int kN = Piece<T>::kN;
     Stats st{-INFINITY, 0.0f, 0.0f};
@@ -501,7 +535,7 @@ __device__ __forceinline__ Stats read_pieces(const Row<T>& row, int lo, int hi, 
         }
     };
     auto close_group = [&]() {
-        tops[t] = group_top;
+        *tops = static_cast<T>(group_top);
         tops += R;
         group_top = -INFINITY;
     };
@@ -573,7 +607,7 @@ template <class T, bool kTop>
 __global__ void __launch_bounds__(kThreads, kBlocks) token_logprobs_kernel(const LogprobArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    Shared& s = *reinterpret_cast<Shared*>(smem);
+    Shared<T>& s = *reinterpret_cast<Shared<T>*>(smem);
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int rank = static_cast<int>(blockIdx.x) & (a.split - 1);
     const long long r = blockIdx.x / static_cast<unsigned>(a.split);
@@ -590,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) token_logprobs_kernel(const
         token = given_token(a, r);
         if (token >= 0) given = static_cast<float>(row.x[token]);
     }
-    Stats st = read_pieces<T, kTop, kThreads>(row, lo, hi, t, batches, per_group, s.top);
+    Stats st = read_pieces<T, kTop, kThreads>(row, lo, hi, t, batches, per_group, s.top + maximum_place<T, kThreads, kThreads>(t));
     // the values beside the whole pieces: rank 0's threads, one each
     const int edge = rank == 0 ? row.edge(t, a.vocab) : -1;
     const float edge_value = edge >= 0 ? static_cast<float>(row.x[edge]) : -INFINITY;
@@ -648,7 +682,7 @@ template <class T>
 __global__ void __launch_bounds__(kReaders + kFinishers, kStreamBlocks) token_logprobs_stream_kernel(const LogprobArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    StreamShared& s = *reinterpret_cast<StreamShared*>(smem);
+    StreamShared<T>& s = *reinterpret_cast<StreamShared<T>*>(smem);
     constexpr int kAll = kReaders + kFinishers;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int buffer = 0;
@@ -660,7 +694,8 @@ __global__ void __launch_bounds__(kReaders + kFinishers, kStreamBlocks) token_lo
             const int batches = (row.pieces + kReaders * kBatch - 1) / (kReaders * kBatch);
             const int per_group = per_maximum<kReaders>(batches);
             if (handed >= 2) bar_sync(kBarEmpty + buffer, kAll);
-            Stats st = read_pieces<T, true, kReaders>(row, 0, row.pieces, t, batches, per_group, s.top[buffer]);
+            Stats st = read_pieces<T, true, kReaders>(row, 0, row.pieces, t, batches, per_group,
+                                                         s.top[buffer] + maximum_place<T, kFinishers, kReaders>(t));
             if (const int edge = row.edge(t, a.vocab); edge >= 0) {
                 const float x = static_cast<float>(row.x[edge]);
                 st.raise(fmaxf(st.m, x));
@@ -775,15 +810,15 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t s)
     if (a.n_top > 0 && a.rows > kBlocks * static_cast<long long>(num_sms())) {
         const unsigned grid = static_cast<unsigned>(kStreamBlocks * num_sms());
         if (a.bf16)
-            token_logprobs_stream_kernel<__nv_bfloat16><<<grid, kReaders + kFinishers, sizeof(StreamShared), s>>>(a);
+            token_logprobs_stream_kernel<__nv_bfloat16><<<grid, kReaders + kFinishers, sizeof(StreamShared<__nv_bfloat16>), s>>>(a);
         else
-            token_logprobs_stream_kernel<float><<<grid, kReaders + kFinishers, sizeof(StreamShared), s>>>(a);
+            token_logprobs_stream_kernel<float><<<grid, kReaders + kFinishers, sizeof(StreamShared<float>), s>>>(a);
         return cudaGetLastError();
     }
     cudaLaunchConfig_t c{};
     c.gridDim = dim3(static_cast<unsigned>(a.rows * a.split));
     c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = a.n_top > 0 ? sizeof(Shared) : offsetof(Shared, f);
+    c.dynamicSmemBytes = a.n_top == 0 ? offsetof(Shared<float>, f) : (a.bf16 ? sizeof(Shared<__nv_bfloat16>) : sizeof(Shared<float>));
     c.stream = s;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
