@@ -605,7 +605,8 @@ def test_logprobs_of_one_row_repeated():
 
 
 GRAD = [(1, 1, False, 0), (3, 7, True, 1), (5, 1000, False, 0), (4, 1003, True, 5), (33, 4099, False, 3),
-        (7, 32000, True, 0), (2, 50257, False, 0), (3, 50257, True, 0), (700, 129, True, 0)]
+        (7, 32000, True, 0), (2, 50257, False, 0), (3, 50257, True, 0), (700, 129, True, 0),
+        (9, 8203, True, 1), (40, 300, False, 0), (3, 4101, False, 2)]
 
 
 @pytest.mark.parametrize("rows,vocab,bf16,pad", GRAD)
