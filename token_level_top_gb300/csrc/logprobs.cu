@@ -25,8 +25,9 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;   // of a block that reads a row (or its share) alone,
-constexpr int kBlocks = 5;         // and how many of those an SM holds
+constexpr int kThreads = 256, kWarps = kThreads / 32;   // of a block that reads a row (or its share) alone, or at most,
+constexpr int kBlocks = 5;         // and how many of those an SM holds;
+constexpr int kFewThreads = 64;    // of a block that reads a short row of many
 constexpr int kBatch = 4;          // 16-byte pieces that a thread has in flight
 constexpr int kMaxima = 2048;       // maxima kept of a row, at most 2048 / readers per reader
 constexpr int kMaxFound = 1024;    // values at or above the threshold that are ranked at once
@@ -604,9 +605,9 @@ struct Result {
     }
 };
 
-// A row to a block, or to a cluster of a.split blocks.
-template <class T, bool kTop>
-__global__ void __launch_bounds__(kThreads, kBlocks) token_logprobs_kernel(const LogprobArgs a)
+// A row to a block of NT threads, or to a cluster of a.split blocks.
+template <class T, bool kTop, int NT>
+__global__ void __launch_bounds__(NT, NT == kThreads ? kBlocks : 16) token_logprobs_kernel(const LogprobArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     Shared<T>& s = *reinterpret_cast<Shared<T>*>(smem);
@@ -617,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) token_logprobs_kernel(const
     // this block's share of the pieces
     const int share = (row.pieces + a.split - 1) / a.split;
     const int lo = min(row.pieces, rank * share), hi = min(row.pieces, lo + share);
-    const int batches = (hi - lo + kThreads * kBatch - 1) / (kThreads * kBatch);
-    const int per_group = per_maximum<kThreads>(batches);
+    const int batches = (hi - lo + NT * kBatch - 1) / (NT * kBatch);
+    const int per_group = per_maximum<NT>(batches);
     // asked for early: the given token and its logit
     int token = -1;
     float given = 0.0f;
@@ -626,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) token_logprobs_kernel(const
         token = given_token(a, r);
         if (token >= 0) given = static_cast<float>(row.x[token]);
     }
-    Stats st = read_pieces<T, kTop, kThreads>(row, lo, hi, t, batches, per_group, s.top + maximum_place<T, kThreads, kThreads>(t));
+    Stats st = read_pieces<T, kTop, NT>(row, lo, hi, t, batches, per_group, s.top + maximum_place<T, NT, NT>(t));
     // the values beside the whole pieces: rank 0's threads, one each
     const int edge = rank == 0 ? row.edge(t, a.vocab) : -1;
     const float edge_value = edge >= 0 ? static_cast<float>(row.x[edge]) : -INFINITY;
@@ -638,17 +639,18 @@ __global__ void __launch_bounds__(kThreads, kBlocks) token_logprobs_kernel(const
     if (lane == 0) s.stats[warp] = st;
     if (kTop) {
         const int groups = per_group ? (batches + per_group - 1) / per_group : 0;
-        find_best<T, kThreads, kThreads>(s.f, s.top, s.keys, row, a.n_top, lo, hi, per_group, groups, t, edge, edge_value);
+        find_best<T, NT, NT>(s.f, s.top, s.keys, row, a.n_top, lo, hi, per_group, groups, t, edge, edge_value);
     }
     if (a.split > 1)
         cluster_sync_all();
     else
         __syncthreads();
     if (rank == 0 && (warp == 0 || a.split > 1)) {   // (without a split the first warp does the rest)
-        // the row's statistics, by every warp for itself: lane i has warp i % 8 of block i / 8, then the next four
+        // the row's statistics, by every warp for itself: lane i has warp i % kOwn of block i / kOwn, then the next ones
         Stats all{-INFINITY, 0.0f, 0.0f};
-        for (int i = lane; i < a.split * kWarps; i += 32) {
-            const uint32_t at = map_to_rank(smem_u32(&s.stats[i % kWarps]), i / kWarps);
+        constexpr int kOwn = NT / 32;
+        for (int i = lane; i < a.split * kOwn; i += 32) {
+            const uint32_t at = map_to_rank(smem_u32(&s.stats[i % kOwn]), i / kOwn);
             Stats o{ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)};
             const float to = fmaxf(all.m, o.m);
             all.raise(to);
@@ -807,9 +809,20 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t s)
     a.split = 1;
     while (a.split < 8 && a.rows * a.split <= num_sms() && pieces / (a.split * 2) >= 8 * kThreads) a.split *= 2;
     if (a.rows * a.split > 0x7fffffffLL) return cudaErrorInvalidValue;
-    // More rows than blocks of the other kernel fit at once: rows are read ahead of their alternatives (20 best of 131072
-    // bf16: 760 rows 43.5 us, 48.0 streamed; 800 rows 57.4 and 49.4; 4096 rows 202 and 186).
-    if (a.n_top > 0 && a.rows > kBlocks * static_cast<long long>(num_sms())) {
+    const size_t smem = a.n_top == 0 ? offsetof(Shared<float>, f) : (a.bf16 ? sizeof(Shared<__nv_bfloat16>) : sizeof(Shared<float>));
+    const bool many = a.rows > kBlocks * static_cast<long long>(num_sms());   // more rows than blocks fit at once
+    // Many short rows: what a row waits for (its loads, its search) is long against its work, so as many as fit, two
+    // warps each (us for the 20 best of 4096 bf16 rows, two warps and otherwise: of 4000 23.2 and 39.5, of 16000 42.5 and
+    // 52.4, of 32000 66.0 and 65.4, of 50257 108 and 80; statistics alone of 16000 29.5 and 36.0).
+    if (many && pieces <= 2560) {
+        const auto kernel = a.bf16 ? (a.n_top > 0 ? token_logprobs_kernel<__nv_bfloat16, true, kFewThreads> : token_logprobs_kernel<__nv_bfloat16, false, kFewThreads>)
+                                   : (a.n_top > 0 ? token_logprobs_kernel<float, true, kFewThreads> : token_logprobs_kernel<float, false, kFewThreads>);
+        kernel<<<static_cast<unsigned>(a.rows), kFewThreads, smem, s>>>(a);
+        return cudaGetLastError();
+    }
+    // Many long ones: rows are read ahead of their alternatives (20 best of 131072 bf16: 760 rows 43.5 us, 48.0 streamed;
+    // 800 rows 57.4 and 49.4; 4096 rows 202 and 186).
+    if (a.n_top > 0 && many) {
         const unsigned grid = static_cast<unsigned>(kStreamBlocks * num_sms());
         if (a.bf16)
             token_logprobs_stream_kernel<__nv_bfloat16><<<grid, kReaders + kFinishers, sizeof(StreamShared<__nv_bfloat16>), s>>>(a);
@@ -820,7 +833,7 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t s)
     cudaLaunchConfig_t c{};
     c.gridDim = dim3(static_cast<unsigned>(a.rows * a.split));
     c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = a.n_top == 0 ? offsetof(Shared<float>, f) : (a.bf16 ? sizeof(Shared<__nv_bfloat16>) : sizeof(Shared<float>));
+    c.dynamicSmemBytes = smem;
     c.stream = s;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -828,8 +841,8 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t s)
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     c.attrs = &attr;
     c.numAttrs = a.split > 1 ? 1 : 0;
-    const auto kernel = a.bf16 ? (a.n_top > 0 ? token_logprobs_kernel<__nv_bfloat16, true> : token_logprobs_kernel<__nv_bfloat16, false>)
-                               : (a.n_top > 0 ? token_logprobs_kernel<float, true> : token_logprobs_kernel<float, false>);
+    const auto kernel = a.bf16 ? (a.n_top > 0 ? token_logprobs_kernel<__nv_bfloat16, true, kThreads> : token_logprobs_kernel<__nv_bfloat16, false, kThreads>)
+                               : (a.n_top > 0 ? token_logprobs_kernel<float, true, kThreads> : token_logprobs_kernel<float, false, kThreads>);
     return cudaLaunchKernelEx(&c, kernel, a);
 }
 
