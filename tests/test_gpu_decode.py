@@ -447,6 +447,7 @@ LOGP = [
     (9, 4097, False, 5, 0), (4, 32000, True, 20, 0), (300, 1003, True, 1, 5), (3, 50257, True, 20, 0),
     (2, 50257, False, 32, 2), (1, 200001, True, 20, 0), (1000, 300, False, 4, 0), (17, 65536, True, 0, 0),
     (900, 3001, True, 32, 1), (800, 10239, False, 20, 0), (770, 20487, True, 0, 0), (1, 20001, False, 20, 3),
+    (170, 100003, True, 20, 0), (153, 49999, False, 32, 1), (160, 98310, True, 0, 0),
 ]
 
 

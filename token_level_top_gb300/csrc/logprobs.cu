@@ -14,9 +14,11 @@
 // exceed each (keys of value and index are distinct, so the ranks are too).
 // Backward: element by element, from lse and entropy.
 //
-// Both are bound by memory where rows are many; the arithmetic per bf16 value
-// (unpack, fma, clamp, ex2, add, fma) fills about half of the issue slots at that
-// rate.
+// Measured (6801 GB/s copied): 4096 x 131072 fp32 with the 5 best, 2147 MB read in
+// 310 us (1.02 of the copy rate); 2047 x 50257 bf16 with the 20 best, 206 MB in 43 us
+// (0.70); the gradient of 4096 x 50257 bf16, 823 MB in 119 us (1.02).  fp32 rows and
+// gradients are bound by memory; bf16 rows by instructions as well (some 50 for the 8
+// values of a piece: unpack, raise, fma, ex2, add, fma) and by what a row waits for.
 #include <algorithm>
 
 #include "common.cuh"
@@ -25,9 +27,10 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;   // of a block that reads a row (or its share) alone, or at most,
-constexpr int kBlocks = 5;         // and how many of those an SM holds;
-constexpr int kFewThreads = 64;    // of a block that reads a short row of many
+constexpr int kThreads = 256;      // of a block that reads a row or its share; fewer for a short row of many, more for a
+constexpr int kFewThreads = 64, kMoreThreads = 512;   // long one of some hundreds
+constexpr int kMostWarps = kMoreThreads / 32;
+constexpr int blocks_of(int threads) { return threads == kThreads ? 5 : (threads == kMoreThreads ? 2 : 16); }   // per SM
 constexpr int kBatch = 4;          // 16-byte pieces that a thread has in flight
 constexpr int kMaxima = 2048;       // maxima kept of a row, at most 2048 / readers per reader
 constexpr int kMaxFound = 1024;    // values at or above the threshold that are ranked at once
@@ -226,14 +229,14 @@ struct Stats {
 // fp32 rows took 377 us instead of 325).
 struct Finder {
     uint64_t best[MOE_MAX_TOP];     // the block's best keys, in order
-    uint32_t least[kWarps];         // (at most kThreads threads look for the best)
-    int entries, found, before[kWarps];
+    uint32_t least[kMostWarps];
+    int entries, found, before[kMostWarps];
     uint16_t entry[kMaxima];
 };
 
 template <class T>
 struct Shared {
-    Stats stats[kWarps];
+    Stats stats[kMostWarps];
     Finder f;
     union {
         T top[kMaxima];                            // until the entries are listed
@@ -261,10 +264,7 @@ __device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("
 template <int NT>
 __device__ __forceinline__ void sync_finders()
 {
-    if (NT == kThreads)   // (the finishers are fewer)
-        __syncthreads();
-    else
-        bar_sync(kBarFinish, NT);
+    bar_sync(kBarFinish, NT);
 }
 
 // How many of the pairs part, part + kParts, .. of keys[0, count) (16-byte aligned) exceed key.
@@ -607,7 +607,7 @@ struct Result {
 
 // A row to a block of NT threads, or to a cluster of a.split blocks.
 template <class T, bool kTop, int NT>
-__global__ void __launch_bounds__(NT, NT == kThreads ? kBlocks : 16) token_logprobs_kernel(const LogprobArgs a)
+__global__ void __launch_bounds__(NT, blocks_of(NT)) token_logprobs_kernel(const LogprobArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     Shared<T>& s = *reinterpret_cast<Shared<T>*>(smem);
@@ -795,6 +795,26 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_backward_kernel(const
     }
 }
 
+// Rows to blocks of NT threads, or to clusters of a.split of them.
+template <int NT>
+cudaError_t launch_rows(const LogprobArgs& a, cudaStream_t s)
+{
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(static_cast<unsigned>(a.rows * a.split));
+    c.blockDim = dim3(NT);
+    c.dynamicSmemBytes = a.n_top == 0 ? offsetof(Shared<float>, f) : (a.bf16 ? sizeof(Shared<__nv_bfloat16>) : sizeof(Shared<float>));
+    c.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(a.split);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    c.attrs = &attr;
+    c.numAttrs = a.split > 1 ? 1 : 0;
+    const auto kernel = a.bf16 ? (a.n_top > 0 ? token_logprobs_kernel<__nv_bfloat16, true, NT> : token_logprobs_kernel<__nv_bfloat16, false, NT>)
+                               : (a.n_top > 0 ? token_logprobs_kernel<float, true, NT> : token_logprobs_kernel<float, false, NT>);
+    return cudaLaunchKernelEx(&c, kernel, a);
+}
+
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t s)
@@ -809,17 +829,11 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t s)
     a.split = 1;
     while (a.split < 8 && a.rows * a.split <= num_sms() && pieces / (a.split * 2) >= 8 * kThreads) a.split *= 2;
     if (a.rows * a.split > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const size_t smem = a.n_top == 0 ? offsetof(Shared<float>, f) : (a.bf16 ? sizeof(Shared<__nv_bfloat16>) : sizeof(Shared<float>));
-    const bool many = a.rows > kBlocks * static_cast<long long>(num_sms());   // more rows than blocks fit at once
+    const bool many = a.rows > blocks_of(kThreads) * static_cast<long long>(num_sms());   // more rows than blocks fit at once
     // Many short rows: what a row waits for (its loads, its search) is long against its work, so as many as fit, two
     // warps each (us for the 20 best of 4096 bf16 rows, two warps and otherwise: of 4000 23.2 and 39.5, of 16000 42.5 and
     // 52.4, of 32000 66.0 and 65.4, of 50257 108 and 80; statistics alone of 16000 29.5 and 36.0).
-    if (many && pieces <= 2560) {
-        const auto kernel = a.bf16 ? (a.n_top > 0 ? token_logprobs_kernel<__nv_bfloat16, true, kFewThreads> : token_logprobs_kernel<__nv_bfloat16, false, kFewThreads>)
-                                   : (a.n_top > 0 ? token_logprobs_kernel<float, true, kFewThreads> : token_logprobs_kernel<float, false, kFewThreads>);
-        kernel<<<static_cast<unsigned>(a.rows), kFewThreads, smem, s>>>(a);
-        return cudaGetLastError();
-    }
+    if (many && pieces <= 2560) return launch_rows<kFewThreads>(a, s);
     // Many long ones: rows are read ahead of their alternatives (20 best of 131072 bf16: 760 rows 43.5 us, 48.0 streamed;
     // 800 rows 57.4 and 49.4; 4096 rows 202 and 186).
     if (a.n_top > 0 && many) {
@@ -830,20 +844,10 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t s)
             token_logprobs_stream_kernel<float><<<grid, kReaders + kFinishers, sizeof(StreamShared<float>), s>>>(a);
         return cudaGetLastError();
     }
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3(static_cast<unsigned>(a.rows * a.split));
-    c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = smem;
-    c.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(a.split);
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    c.attrs = &attr;
-    c.numAttrs = a.split > 1 ? 1 : 0;
-    const auto kernel = a.bf16 ? (a.n_top > 0 ? token_logprobs_kernel<__nv_bfloat16, true, kThreads> : token_logprobs_kernel<__nv_bfloat16, false, kThreads>)
-                               : (a.n_top > 0 ? token_logprobs_kernel<float, true, kThreads> : token_logprobs_kernel<float, false, kThreads>);
-    return cudaLaunchKernelEx(&c, kernel, a);
+    // One or two long rows an SM: more loads in flight for each (20 best of 200 / 300 rows of 131072 fp32: 28.5 / 34.5 us,
+    // 35.7 / 38.7 with 256 threads; of 65536 bf16 13.2 / 15.4 and 12.5 / 15.9).
+    if (a.split == 1 && a.rows > num_sms() && a.rows <= 2LL * num_sms() && pieces >= 12288) return launch_rows<kMoreThreads>(a, s);
+    return launch_rows<kThreads>(a, s);
 }
 
 cudaError_t launch_token_logprobs_backward(const LogprobGradArgs& args, cudaStream_t s)
