@@ -10,7 +10,8 @@
 // copies), and hands them around in shared memory.  A warp's rows arrive through a
 // ring of its own in shared memory, some KB ahead of the writes and before the
 // token's page and angles are known; held in registers they were too few in flight
-// (72 us for 16384 tokens of 32 + 8 + 8 heads, D = 128; 65 us like this, 402 MB).
+// (72 us for 16384 tokens of 32 + 8 + 8 heads, D = 128; 63.5 us like this, 403 MB
+// at 0.93 of the copy rate).
 #include "common.cuh"
 #include "internal.h"
 
@@ -33,9 +34,13 @@ __device__ __forceinline__ void cos_sin_turn(uint64_t f, float& c, float& s)
     s = (quarter & 2) ? -b : b;
 }
 
-// Groups of rows that a warp has in its ring: 3 at 4 blocks an SM; with more, blocks or groups, reads and writes get
-// in each other's way in memory (16384 tokens: 65 us; 5 groups 67, 6 groups 69, 12 groups in 2 blocks 93).
+// Groups of rows that a warp has in its ring: 3 at 32 warps an SM; with more, warps or groups, reads and writes get in
+// each other's way in memory (16384 tokens: 63.5 us, 40 warps 65; in blocks of 8 warps 5 groups 67, 6 groups 69; 48682
+// tokens of 15 + 3 + 3 heads: 99 us, 4 groups 104, 40 warps 105).
 constexpr int kDepth = 3;
+// Warps work alone; small blocks free their places sooner (8 warps a block: 65 us instead of 63.5; 76622 tokens of 3 + 3 +
+// 3 heads 95 and 86).
+constexpr int kWarps = 2;
 
 struct Piece {
     float x[8];
@@ -85,14 +90,14 @@ __device__ __forceinline__ float row_max(const Piece& x0, const Piece& x1)
 }
 
 template <int D, bool kE4m3, bool kInterleaved>
-__global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a)
+__global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) kv_append_kernel(const AppendArgs a)
 {
     constexpr int kLanes = D / 16;          // lanes per row
     constexpr int kRows = 32 / kLanes;      // rows of a warp at a time
-    extern __shared__ __align__(16) unsigned char smem[];   // [8 warps][kDepth] rings, then the angles
-    float2(*const s_angle)[D / 2] = reinterpret_cast<float2(*)[D / 2]>(smem + 8 * kDepth * 1024);
+    extern __shared__ __align__(16) unsigned char smem[];   // [kWarps][kDepth] rings, then the angles
+    float2(*const s_angle)[D / 2] = reinterpret_cast<float2(*)[D / 2]>(smem + kWarps * kDepth * 1024);
     const int lane = threadIdx.x & 31;
-    const long long warp = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const long long warp = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     if (warp >= static_cast<long long>(a.T) * a.parts) return;
     const int t = a.parts == 1 ? static_cast<int>(warp) : static_cast<int>(warp / a.parts);
     const int part = a.parts == 1 ? 0 : static_cast<int>(warp - static_cast<long long>(t) * a.parts);
@@ -230,12 +235,12 @@ template <int D>
 cudaError_t launch_d(const AppendArgs& a, bool e4m3, cudaStream_t s)
 {
     const long long warps = static_cast<long long>(a.T) * a.parts;
-    const unsigned grid = static_cast<unsigned>((warps + 7) / 8);
-    constexpr int kSmem = 8 * kDepth * 1024 + 8 * (D / 2) * 8;
+    const unsigned grid = static_cast<unsigned>((warps + kWarps - 1) / kWarps);
+    constexpr int kSmem = kWarps * (kDepth * 1024 + D / 2 * 8);
     const auto kernel = e4m3 ? (a.interleaved ? kv_append_kernel<D, true, true> : kv_append_kernel<D, true, false>)
                              : (a.interleaved ? kv_append_kernel<D, false, true> : kv_append_kernel<D, false, false>);
     static_assert(kSmem <= 48 * 1024, "within the limit that needs no asking");
-    kernel<<<grid, 256, kSmem, s>>>(a);
+    kernel<<<grid, 32 * kWarps, kSmem, s>>>(a);
     return cudaGetLastError();
 }
 
