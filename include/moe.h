@@ -590,8 +590,8 @@ moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_attentio
  *   top_ids, top_logprobs [rows, n_top]: the n_top largest x, ties to the lowest index
  * all in fp32.  token_dev [rows]: < 0 means none (logprob 0); >= vocab records
  * MOE_ERR_INDEX and counts as none.  n_top <= MOE_MAX_TOP; past vocab entries are id -1,
- * -inf.  A masked logit (-inf, or the type's lowest value) has probability 0, and
- * logprob -inf where it is -inf; a row of -inf alone has lse -inf, entropy 0.  NaN or
+ * -inf.  A masked logit (-inf, or a finite value far below the row's others) has probability 0,
+ * and logprob -inf where it is -inf; a row of -inf alone has lse -inf, entropy 0.  NaN or
  * +inf makes the row's lse, logprob and entropy NaN and records MOE_ERR_NONFINITE; NaN
  * ranks last.  Each output may be NULL (token_dev with logprob_dev; top_*
  * with n_top = 0).  status_dev: NULL, or the int32 status word. */

@@ -37,6 +37,7 @@ constexpr int kMaxFound = 1024;    // values at or above the threshold that are 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Values are raised to this: their exponentials are 0 all the same, and 0 times them is 0 (-inf would make NaN).
 constexpr float kFloor = -1e30f;
+constexpr float kNear = 0x1p24f;   // the largest |maximum| against which a row's values are taken in one fma
 
 __device__ __forceinline__ float exp2_fast(float x)
 {
@@ -189,15 +190,32 @@ struct Row {
 
 // The running statistics of one thread, warp, block or cluster.
 struct Stats {
-    float m, l, w;   // maximum, sum 2^z, sum 2^z z with z = (x - m) log2 e
+    float m, l, w;   // maximum, sum 2^z, sum 2^z z with z = (x - m) log2 e + off(m)
+    // z = x log2 e - base(m) in one fma, while |m| <= kNear.  The base's rounding off(m) is in every z, up to |m| log2 e
+    // 2^-24: 7e-4 at 10^4.  Maxima are raised and log probabilities taken with it, so that it costs neither anything.
+    // Past kNear it would be more than an exponential can hold (from some 1e9 on: finite masks until something else is
+    // read, rows of nothing else), and the base overflows at the type's lowest value: there the difference comes first.
+    static __device__ __forceinline__ bool is_far(float v) { return fabsf(v) > kNear && fabsf(v) < INFINITY; }
+    static __device__ __forceinline__ float base_of(float v) { return __fmul_rn(v, kLog2e); }
+    static __device__ __forceinline__ float off(float v) { return fabsf(v) <= kNear ? fmaf(v, kLog2e, -base_of(v)) : 0.0f; }
+    __device__ __forceinline__ bool far() const { return is_far(m); }
+    __device__ __forceinline__ float base() const { return base_of(m == -INFINITY ? 0.0f : m); }
+    __device__ __forceinline__ void raise_by(float d, float to)
+    {
+        d = fmaxf(d, -1e20f);
+        const float f = exp2_fast(d);
+        w = f * (w + d * l);
+        l *= f;
+        m = to;
+    }
+    // to >= m, neither far
+    __device__ __forceinline__ void raise_near(float to)
+    {
+        if (to > m) raise_by(base_of(m) - base_of(to), to);
+    }
     __device__ __forceinline__ void raise(float to)   // to >= m
     {
-        if (to > m) {
-            const float d = fmaxf((m - to) * kLog2e, -1e20f), f = exp2_fast(d);
-            w = f * (w + d * l);
-            l *= f;
-            m = to;
-        }
+        if (to > m) raise_by(fmaf(m - to, kLog2e, off(to) - off(m)), to);
     }
     // The warp's, in every lane: the maximum first, then plain sums.
     __device__ __forceinline__ void join_warp()
@@ -205,16 +223,16 @@ struct Stats {
         float to = m;
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, off));
-        raise(to);
+        if (__any_sync(0xffffffffu, is_far(m) || is_far(to)))
+            raise(to);
+        else
+            raise_near(to);
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) {
             l += __shfl_xor_sync(0xffffffffu, l, off);
             w += __shfl_xor_sync(0xffffffffu, w, off);
         }
     }
-    // z = x log2 e - base in one fma, unless the base would overflow (masks of the type's lowest value)
-    __device__ __forceinline__ bool far() const { return fabsf(m) > 2e38f && fabsf(m) < INFINITY; }
-    __device__ __forceinline__ float base() const { return (m == -INFINITY ? 0.0f : m) * kLog2e; }
     // one value, against any maximum
     __device__ __forceinline__ void add(float x)
     {
@@ -497,14 +515,18 @@ __device__ __forceinline__ Stats read_pieces(const Row<T>& row, int lo, int hi, 
     constexpr int kN = Piece<T>::kN;
     Stats st{-INFINITY, 0.0f, 0.0f};
     float group_top = -INFINITY;
+    bool far = false;   // st.far()
     auto work = [&](const auto& v) {
         constexpr int kPieces = sizeof(v) / 16;
         float top = Piece<T>::top(v[0]);
 #pragma unroll
         for (int j = 1; j < kPieces; ++j) top = fmaxf(top, Piece<T>::top(v[j]));
         if (kTop) group_top = fmaxf(group_top, top);
-        st.raise(fmaxf(st.m, top));
-        if (!st.far()) {
+        const float to = fmaxf(st.m, top);
+        const bool was_far = far;
+        far = Stats::is_far(to);
+        if (!(far || was_far)) {
+            st.raise_near(to);
             const float minus_base = -st.base();
             // two sums each, of even and odd places, in packed pairs: one instruction for two values
             Pair l = {st.l, 0.0f}, w = {st.w, 0.0f};
@@ -523,18 +545,23 @@ __device__ __forceinline__ Stats read_pieces(const Row<T>& row, int lo, int hi, 
             st.l = l.x + l.y;
             st.w = w.x + w.y;
         } else {
+            st.raise(to);
+            Pair l = {st.l, 0.0f}, w = {st.w, 0.0f};
+            const float minus_m = far ? -st.m : 0.0f, minus_base = far ? 0.0f : -st.base();
 #pragma unroll
             for (int j = 0; j < kPieces; ++j) {
                 float x[kN];
                 Piece<T>::unpack(v[j], x);
-#pragma unroll 1
-                for (int i = 0; i < kN; ++i) {
-                    float one = x[0];
 #pragma unroll
-                    for (int k = 1; k < kN; ++k) one = i == k ? x[k] : one;
-                    st.add(one);
+                for (int i = 0; i < kN; i += 2) {
+                    const Pair d = fma(add(Pair{x[i], x[i + 1]}, Pair{minus_m, minus_m}), Pair{kLog2e, kLog2e}, Pair{minus_base, minus_base});
+                    const Pair z = {max_nan(d.x, kFloor), max_nan(d.y, kFloor)}, e = {exp2_fast(z.x), exp2_fast(z.y)};
+                    l = add(l, e);
+                    w = fma(e, z, w);
                 }
             }
+            st.l = l.x + l.y;
+            st.w = w.x + w.y;
         }
     };
     auto close_group = [&]() {
@@ -584,9 +611,9 @@ __device__ __forceinline__ int given_token(const LogprobArgs& a, long long r)
 // What the outputs of a row take from its statistics.
 struct Result {
     bool none;            // nothing but -inf in the row
-    float ref, log_l;
+    float ref, log_l;     // log_l: ln sum e^(x - ref)
     __device__ __forceinline__ explicit Result(const Stats& s)
-        : none(s.m == -INFINITY && s.l == 0.0f), ref(s.m == -INFINITY ? 0.0f : s.m), log_l(logf(s.l))
+        : none(s.m == -INFINITY && s.l == 0.0f), ref(s.m == -INFINITY ? 0.0f : s.m), log_l(fmaf(-Stats::off(s.m), kLn2, logf(s.l)))
     {
     }
     __device__ __forceinline__ float logprob(float x) const { return none ? -INFINITY : x - ref - log_l; }
@@ -595,7 +622,7 @@ struct Result {
     {
         if (s.l != s.l) record_error(a.status, MOE_ERR_NONFINITE);
         if (a.lse) a.lse[r] = ref + log_l;
-        if (a.entropy) a.entropy[r] = none ? 0.0f : log_l - s.w / s.l * kLn2;
+        if (a.entropy) a.entropy[r] = none ? 0.0f : logf(s.l) - s.w / s.l * kLn2;   // (the same off(m) in both)
         if (a.logprob) a.logprob[r] = token < 0 ? 0.0f : logprob(given);
     }
     __device__ __forceinline__ void write_top(const LogprobArgs& a, long long r, int at, uint64_t key) const
