@@ -36,7 +36,9 @@
 // e4m3 rows become f16 in one conversion per two codes (exact), so that path
 // multiplies in f16: Q is scaled by a power of two per head, and the value rows'
 // exponents enter as 2^(s + e) in the weights, whose running maximum is taken
-// over s + e; the sum of the softmax uses 2^s against the same maximum.
+// over s + e.  The sum of the softmax has a maximum of its own, over s: against
+// that of s + e its terms could be anything from 2^-250 to 2^250 (256 sequences
+// up to 4096: 179 us with one maximum for both, 181 with two).
 //
 // Measured (32 query heads on 8, D = 128, 6801 GB/s copied): 64 sequences up to
 // 8192, bf16, 1083 MB in 166 us (0.96 of the copy rate); one of 131072, 537 MB in
@@ -58,6 +60,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;
 // e4m3 path: weights are held times 2^6 (at most 2^14), so that f16 keeps those 2^-30 of the maximum's
 constexpr float kShift = 6.0f;
+// the sum of the softmax stays in fp32, whose range asks for a new maximum less often
+constexpr float kSlackSum = 32.0f;
+constexpr float kNone = -3.402823466e38f;   // a maximum of nothing: finite, so that differences of two are
 
 __device__ __forceinline__ float exp2_fast(float x)
 {
@@ -200,16 +205,18 @@ struct Shape {
     static constexpr int kGap = 2;
     static constexpr int kJoin = D == 64 && kHeads == 16 ? 8 : 4;   // heads that the block joins at a time, as memory allows
     static constexpr int kMerge = kWarps * kJoin * D * 4;
+    static constexpr int kStats = kWarps * 16 * (kE4m3 ? 12 : 8);   // bytes: the warps' maxima and sums
+    static constexpr int kSlot = 16 * D + 32;                       // floats of a part: outputs, maxima and sums
     // beside a tile: which of its keys are live, and the exponent bytes of its e4m3 keys and values
     static constexpr int kMask = kE4m3 ? 2 * kTileKeys : 0, kMeta = kMask + 4;
     // as many slots (key or value tiles) as the block's share of 228 KB holds beside the join, at most 16
     static constexpr int kShare = 233472 / kCtas - 1024 - 384;
-    static constexpr int kRoom = kShare - kMerge - kWarps * 128;
+    static constexpr int kRoom = kShare - kMerge - kStats;
     static constexpr int kFit = (2 * kRoom / kWarps - 2 * kMeta) / (2 * kTile + kMeta);
     static constexpr int kSlots = kFit < 16 ? kFit : 16;
     static constexpr int kMetas = (kSlots + 3) / 2;           // tiles begun and not finished
     static constexpr int kRing = kWarps * kSlots * kTile;
-    static constexpr int kSmem = kRing + kMerge + kWarps * (kMetas * kMeta + 128);
+    static constexpr int kSmem = kRing + kMerge + kWarps * kMetas * kMeta + kStats;
     static_assert(kSlots >= 3 && kSmem <= kShare && kWarps * kMetas * kMeta % 8 == 0, "the ring");
     static constexpr int kCopyRows = kRow >= 128 ? 4 : 2;     // rows of a part that a lane copies from, 16 bytes of each
     static constexpr int kCopySegs = kRow >= 128 ? kRow / 128 : 1;   // ... per 128-byte segment
@@ -299,6 +306,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
     float* const s_merge = reinterpret_cast<float*>(smem + S::kRing);
     unsigned char* const s_meta = smem + S::kRing + S::kMerge;              // [warp][tile]
     float2* const s_ml = reinterpret_cast<float2*>(s_meta + kWarps * kMetas * S::kMeta);   // [warp][16]
+    float* const s_sm = reinterpret_cast<float*>(s_ml + kWarps * 16);                       // [warp][16], e4m3
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
@@ -561,8 +569,9 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
     // ---- the computing side
     float qscale[kCols][2];           // scores in units of log2: accumulator * qscale (* the key's exponent)
     float o[kCols][S::kTiles][4];
-    float m[kCols][2], l[kCols][2];   // of the heads 2c and 2c + 1 of the column tile
-    float ref[kCols][2], limit[kCols][2];   // what the exponents are taken against, and the score that raises m
+    // of the heads 2c and 2c + 1 of the column tile: the maximum that the weights are taken against, the sum of the
+    // softmax, and (e4m3) the maximum that the sum is taken against
+    float m[kCols][2], l[kCols][2], sm[kCols][2];
     uint32_t slot = 0;                // byte offset in the ring
     int cmeta = 0;
     for (bool first_tile = true; left > 0; first_tile = false) {
@@ -572,8 +581,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
             for (int hh = 0; hh < kCols; ++hh) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    m[hh][e] = limit[hh][e] = -INFINITY;
-                    ref[hh][e] = 0.0f;
+                    m[hh][e] = sm[hh][e] = kNone;
                     l[hh][e] = 0.0f;
                     qscale[hh][e] = a.scale * kLog2e;
                 }
@@ -688,30 +696,37 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
             }
         }
         auto y = [&](int h, int hh, int j) { return kE4m3 ? x[h][hh][j] + vexp[h][j >> 1] : x[h][hh][j]; };
+        auto top_y = [&](int hh, int e) {
+            const float top = fmaxf(y(0, hh, e), y(0, hh, 2 + e));
+            return S::kParts == 2 ? fmaxf(top, fmaxf(y(S::kParts - 1, hh, e), y(S::kParts - 1, hh, 2 + e))) : top;
+        };
+        auto top_x = [&](int hh, int e) {
+            const float top = fmaxf(x[0][hh][e], x[0][hh][2 + e]);
+            return S::kParts == 2 ? fmaxf(top, fmaxf(x[S::kParts - 1][hh][e], x[S::kParts - 1][hh][2 + e])) : top;
+        };
         bool grew = false;
 #pragma unroll
         for (int hh = 0; hh < kCols; ++hh)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float top = fmaxf(y(0, hh, e), y(0, hh, 2 + e));
-                if (S::kParts == 2) top = fmaxf(top, fmaxf(y(S::kParts - 1, hh, e), y(S::kParts - 1, hh, 2 + e)));
-                grew |= top > limit[hh][e];
+                grew |= top_y(hh, e) > m[hh][e] + kSlack;
+                if (kE4m3) grew |= top_x(hh, e) > sm[hh][e] + kSlackSum;
             }
         if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
             for (int hh = 0; hh < kCols; ++hh)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float top = fmaxf(y(0, hh, e), y(0, hh, 2 + e));
-                    if (S::kParts == 2) top = fmaxf(top, fmaxf(y(S::kParts - 1, hh, e), y(S::kParts - 1, hh, 2 + e)));
+                    // from old to the maximum of it and the tile's: the factor of what was taken against old
+                    auto raise = [&](float& old, float top) {
 #pragma unroll
-                    for (int off = 4; off <= 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                    const float mn = fmaxf(m[hh][e], top);
-                    const float fix = mn > m[hh][e] ? exp2_fast(m[hh][e] - mn) : 1.0f;
-                    m[hh][e] = mn;
-                    limit[hh][e] = mn + kSlack;
-                    ref[hh][e] = mn == -INFINITY ? 0.0f : (kE4m3 ? mn - kShift : mn);
-                    l[hh][e] *= fix;
+                        for (int off = 4; off <= 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                        const float mn = fmaxf(old, top), fix = mn > old ? exp2_fast(old - mn) : 1.0f;
+                        old = mn;
+                        return fix;
+                    };
+                    const float fix = raise(m[hh][e], top_y(hh, e));
+                    l[hh][e] *= kE4m3 ? raise(sm[hh][e], top_x(hh, e)) : fix;
 #pragma unroll
                     for (int t = 0; t < S::kTiles; ++t) {
                         o[hh][t][e] *= fix;
@@ -726,11 +741,11 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
             for (int hh = 0; hh < kCols; ++hh) {
                 float p[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) p[j] = exp2_fast(y(h, hh, j) - ref[hh][j & 1]);
+                for (int j = 0; j < 4; ++j) p[j] = exp2_fast(y(h, hh, j) - (kE4m3 ? m[hh][j & 1] - kShift : m[hh][j & 1]));
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if (kE4m3)
-                        l[hh][e] += exp2_fast(x[h][hh][e] - ref[hh][e]) + exp2_fast(x[h][hh][2 + e] - ref[hh][e]);
+                        l[hh][e] += exp2_fast(x[h][hh][e] - sm[hh][e]) + exp2_fast(x[h][hh][2 + e] - sm[hh][e]);
                     else
                         l[hh][e] += p[e] + p[2 + e];
                 }
@@ -804,7 +819,22 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
         // ---- the end of an item, or of this block's part of it
         if (last || left <= 0) {
             const bool starts = cw.off >= lo, ends = cw.off + cw.n <= hi, whole = starts && ends;
-            constexpr int kSlot = 16 * D + 32;                                   // floats per part
+            constexpr int kSlot = S::kSlot;
+            // an output from the sums x of weights and L of the softmax; in e4m3 the one is in units of 2^(M - kShift), the
+            // other of 2^Ms (their quotient in two halves: the whole may not fit a float where the output does)
+            auto write_row = [&](int head, int d, float4 x, float M, float Ms, float L) {
+                const float inv = L == 0.0f ? 0.0f : 1.0f / L, up = kE4m3 ? exp2_fast(0.5f * (M - kShift - Ms)) : 1.0f;
+                auto scaled = [&](float v) { return kE4m3 ? v * inv * up * up : v * inv; };
+                *reinterpret_cast<uint2*>(a.out + cw.b * a.out_token_stride + head * a.out_head_stride + d) =
+                    make_uint2(pack_bf16x2(scaled(x.x), scaled(x.y)), pack_bf16x2(scaled(x.z), scaled(x.w)));
+                if (d == 0 && a.lse)
+                    a.lse[static_cast<long long>(cw.b) * a.n_heads + head] = L == 0.0f ? -INFINITY : ((kE4m3 ? Ms : M) + log2f(L)) * kLn2;
+            };
+            // a part, or a group's result; in e4m3 with its softmax's sum as the logarithm, whose rounding is that of a score
+            auto write_part = [&](float* to, int r, int d, float4 x, float M, float Ms, float L) {
+                *reinterpret_cast<float4*>(to + r * D + d) = x;
+                if (d == 0) *reinterpret_cast<float2*>(to + 16 * D + 2 * r) = make_float2(M, !kE4m3 ? L : L == 0.0f ? kNone : Ms + log2f(L));
+            };
             float* const slots = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kAttentionCtrlBytes);
             float* const part = slots + (3 * static_cast<size_t>(blockIdx.x) + (starts ? 1 : 0)) * kSlot;
 #pragma unroll
@@ -814,7 +844,10 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                     float sum = l[hh][e];
 #pragma unroll
                     for (int off = 4; off <= 16; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                    if (g == 0 && (kHeads != 4 || c < 2)) s_ml[warp * 16 + hh * 8 + 2 * c + e] = make_float2(m[hh][e], sum);
+                    if (g == 0 && (kHeads != 4 || c < 2)) {
+                        s_ml[warp * 16 + hh * 8 + 2 * c + e] = make_float2(m[hh][e], sum);
+                        if (kE4m3) s_sm[warp * 16 + hh * 8 + 2 * c + e] = sm[hh][e];
+                    }
                 }
                 if (kHeads == 4) {   // the low parts' columns
 #pragma unroll
@@ -846,35 +879,29 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                 for (int at = threadIdx.x; at < S::kJoin * (D / 4); at += kThreads) {
                     const int r = at / (D / 4), d = at % (D / 4) * 4;
                     if (first + r >= live_heads) break;
-                    float M = -INFINITY;
+                    float M = kNone, Ms = kNone;
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * 16 + first + r].x);
-                    const float ref = M == -INFINITY ? 0.0f : M;
+                    for (int w = 0; w < kWarps; ++w) {
+                        M = fmaxf(M, s_ml[w * 16 + first + r].x);
+                        if (kE4m3) Ms = fmaxf(Ms, s_sm[w * 16 + first + r]);
+                    }
                     float L = 0.0f;
                     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) {
                         const float2 ml = s_ml[w * 16 + first + r];
-                        const float f = exp2_fast(ml.x - ref);
+                        const float f = exp2_fast(ml.x - M);
                         const float4 y = *reinterpret_cast<const float4*>(s_merge + (w * S::kJoin + r) * D + d);
-                        L += ml.y * f;
+                        L += ml.y * (kE4m3 ? exp2_fast(s_sm[w * 16 + first + r] - Ms) : f);
                         x.x += y.x * f;
                         x.y += y.y * f;
                         x.z += y.z * f;
                         x.w += y.w * f;
                     }
-                    const int head = head0 + first + r;
-                    if (whole) {
-                        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-                        *reinterpret_cast<uint2*>(a.out + cw.b * a.out_token_stride + head * a.out_head_stride + d) =
-                            make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-                        if (d == 0 && a.lse)
-                            a.lse[static_cast<long long>(cw.b) * a.n_heads + head] =
-                                L == 0.0f ? -INFINITY : ((kE4m3 ? M - kShift : M) + log2f(L)) * kLn2;
-                    } else {
-                        *reinterpret_cast<float4*>(part + (first + r) * D + d) = x;
-                        if (d == 0) *reinterpret_cast<float2*>(part + 16 * D + 2 * (first + r)) = make_float2(M, L);
-                    }
+                    if (whole)
+                        write_row(head0 + first + r, d, x, M, Ms, L);
+                    else
+                        write_part(part, first + r, d, x, M, Ms, L);
                 }
             }
             if (!whole) {
@@ -900,7 +927,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                     };
                     for (int at = threadIdx.x; at < live_heads * (D / 4); at += kThreads) {
                         const int r = at / (D / 4), d = at % (D / 4) * 4;
-                        float M = -INFINITY, L = 0.0f;
+                        float M = kNone, Ms = 0.5f * kNone, L = 0.0f;   // (2^(kNone - Ms) is 0)
                         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         for (int i0 = 0; i0 < count; i0 += kLoads) {
                             float2 ml[kLoads];
@@ -911,21 +938,25 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                                 ml[i] = __ldcg(reinterpret_cast<const float2*>(p + 16 * D + 2 * r));
                                 y[i] = __ldcg(reinterpret_cast<const float4*>(p + r * D + d));
                             }
-                            float mn = M;
+                            float mn = M, sn = Ms;
 #pragma unroll
-                            for (int i = 0; i < kLoads; ++i) mn = fmaxf(mn, ml[i].x);   // (a repeated one changes nothing)
-                            const float ref = mn == -INFINITY ? 0.0f : mn, fix = exp2_fast(M - ref);
-                            L *= fix;
+                            for (int i = 0; i < kLoads; ++i) {   // (a repeated one changes nothing)
+                                mn = fmaxf(mn, ml[i].x);
+                                if (kE4m3) sn = fmaxf(sn, ml[i].y);
+                            }
+                            const float fix = exp2_fast(M - mn);
+                            L *= kE4m3 ? exp2_fast(Ms - sn) : fix;
                             x.x *= fix;
                             x.y *= fix;
                             x.z *= fix;
                             x.w *= fix;
                             M = mn;
+                            Ms = sn;
 #pragma unroll
                             for (int i = 0; i < kLoads; ++i) {
-                                const float w = exp2_fast(ml[i].x - ref);
+                                const float w = exp2_fast(ml[i].x - M);
                                 if (i0 + i < count) {
-                                    L += ml[i].y * w;
+                                    L += kE4m3 ? exp2_fast(ml[i].y - Ms) : ml[i].y * w;
                                     x.x += y[i].x * w;
                                     x.y += y[i].y * w;
                                     x.z += y[i].z * w;
@@ -933,18 +964,10 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                                 }
                             }
                         }
-                        if (final) {
-                            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-                            *reinterpret_cast<uint2*>(a.out + cw.b * a.out_token_stride + (head0 + r) * a.out_head_stride + d) =
-                                make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-                            if (d == 0 && a.lse)
-                                a.lse[static_cast<long long>(cw.b) * a.n_heads + head0 + r] =
-                                    L == 0.0f ? -INFINITY : ((kE4m3 ? M - kShift : M) + log2f(L)) * kLn2;
-                        } else {
-                            float* to = slots + (3 * static_cast<size_t>(first + k0) + 2) * kSlot;
-                            *reinterpret_cast<float4*>(to + r * D + d) = x;
-                            if (d == 0) *reinterpret_cast<float2*>(to + 16 * D + 2 * r) = make_float2(M, L);
-                        }
+                        if (final)
+                            write_row(head0 + r, d, x, M, Ms, L);
+                        else
+                            write_part(slots + (3 * static_cast<size_t>(first + k0) + 2) * kSlot, r, d, x, M, Ms, L);
                     }
                 };
                 // groups of about the square root of the parts; none of one block, whose counter and result could meet
