@@ -572,7 +572,8 @@ moe_status_t moe_paged_attention_workspace_init(void* ws_dev, size_t ws_bytes, v
  * with fp32 scores, statistics and sums.  A row with no live position, or no score above
  * -inf, gets zeros and lse = -inf.  What the cache holds in other places (NaN included) has no effect.
  * MOE_KV_E4M3: a key whose weight times 2^(exponent of its value row) is below 2^-30 of the
- * head's largest such product loses bits of its share of out, down to none (not of lse).
+ * head's largest such product loses bits of its share of out, down to none (not of lse); a
+ * value row of zeros with exponent byte 127, as moe_kv_append stores it, is no such product.
  * Lengths are read on the device: a captured graph replays at other lengths.  A
  * length outside [0, max_pages * page_size] (at most 2^31 - 65536) is brought to its nearer end, and keys
  * of a page outside [0, n_pages) are left out; both record MOE_ERR_INDEX.  Page and token

@@ -91,5 +91,45 @@ def test_value_exponents(lens, heads, kv, D, page, e):
 
 
 @pytest.mark.parametrize("lens,heads,kv,D,page", SHAPES)
+@pytest.mark.parametrize("e", [-7, -20, -28, -30, -32, -40, -120])
+def test_rows_of_zeros_among_small_ones(lens, heads, kv, D, page, e):
+    """A row of zeros has exponent 0, as the append stores it, whatever its neighbours' are."""
+    def zero(n):
+        z = torch.zeros(n, kv, dtype=torch.bool)
+        z[min(5, n - 1):: 64] = True
+        return z
+
+    _run(lens, heads, kv, D, page, _cycle(kv, e, e - 1), zero, seed=-e)
+    _run(lens, heads, kv, D, page, _cycle(kv, e, e - 1), zero, window=70, far=True, seed=-e)
+
+
+@pytest.mark.parametrize("lens,heads,kv,D,page", SHAPES)
 def test_rows_of_zeros_alone(lens, heads, kv, D, page):
     _run(lens, heads, kv, D, page, _cycle(kv, 0), lambda n: torch.ones(n, kv, dtype=torch.bool))
+
+
+def test_appended_rows_of_all_sizes():
+    """Values from 1e-37 to 1e30 and rows of zeros through the append and back."""
+    g = torch.Generator().manual_seed(8)
+    n, kv, D, page, heads = 97, 2, 128, 16, 8
+    for sizes in ((1e-37,), (1e-36, 0.0), (1e-9, 0.0, 1e-8), (1e-30, 1e30), (1.0, 0.0, 1e-3)):
+        scale = torch.tensor(sizes).repeat(n)[:n, None, None]
+        k = torch.randn(n, kv, D, generator=g).to(torch.bfloat16).cuda()
+        v = (torch.randn(n, kv, D, generator=g) * scale).to(torch.bfloat16).cuda()
+        table = torch.randperm(7, generator=g).to(torch.int32)[None].cuda()
+        cache, ws = moe.KVCache.empty(7, page, kv, D, e4m3=True), moe.attention_workspace(D)
+        moe.kv_append(cache, k, v, torch.arange(n, dtype=torch.int32).cuda(), table, status=ws,
+                      seq=torch.zeros(n, dtype=torch.int32).cuda())
+        q = torch.randn(1, heads, D, generator=g).to(torch.bfloat16).cuda()
+        out, lse = moe.paged_attention(cache, ws, q, torch.tensor([n], dtype=torch.int32).cuda(), table, return_lse=True)
+        assert moe.device_status(ws) == 0
+        j = torch.arange(n)
+        at = table[0].cpu().long()[j // page], j % page
+        kd, vd = [ref.e4m3_value(st.cpu()[at], ex.cpu()[at]) for st, ex in ((cache.k, cache.k_exp), (cache.v, cache.v_exp))]
+        for h in range(heads):
+            hk = h // (heads // kv)
+            o, s, eo, es = ref.attention(ref.f64(q)[0, h], kd[:, hk], vd[:, hk], D ** -0.5)
+            p = np.exp(D ** -0.5 * (kd[:, hk] @ ref.f64(q)[0, h]) - s)
+            eo = eo + 2.0 ** -31 * n * (p[:, None] * np.abs(vd[:, hk])).max() * 2
+            assert abs(float(lse[0, h]) - s) <= es
+            assert (np.abs(ref.f64(out)[0, h] - o) <= eo).all(), (sizes, h)

@@ -62,6 +62,7 @@ constexpr float kSlack = 8.0f;
 constexpr float kShift = 6.0f;
 // the sum of the softmax stays in fp32, whose range asks for a new maximum less often
 constexpr float kSlackSum = 32.0f;
+constexpr int kZeroByte = 127;   // the exponent byte of a row of zeros, as the append stores it: an exponent of 0
 constexpr float kNone = -3.402823466e38f;   // a maximum of nothing: finite, so that differences of two are
 
 __device__ __forceinline__ float exp2_fast(float x)
@@ -489,7 +490,8 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
             const int h = S::kParts == 2 ? lane >> 4 : 0;
             const int page = S::kParts == 2 && h ? next_page[S::kParts - 1] : next_page[0];
             const int at = S::kParts == 2 && h ? next_at[S::kParts - 1] : next_at[0];
-            exp_k = exp_v = 127;
+            exp_k = 127;
+            exp_v = kZeroByte - 1;
             if (lane < S::kTileKeys && ((rows_live >> lane) & 1)) {
                 const long long e = lane_exp + page * a.exp_page_stride + at * a.exp_token_stride;
                 exp_k = __ldg(a.k_exp + e);
@@ -704,7 +706,11 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
             const float top = fmaxf(x[0][hh][e], x[0][hh][2 + e]);
             return S::kParts == 2 ? fmaxf(top, fmaxf(x[S::kParts - 1][hh][e], x[S::kParts - 1][hh][2 + e])) : top;
         };
-        bool grew = false;
+        bool grew = false;   // or (e4m3) a value row may be one of zeros
+        if (kE4m3) {
+#pragma unroll
+            for (int h = 0; h < S::kParts; ++h) grew |= vexp[h][0] == 0.0f || vexp[h][1] == 0.0f;
+        }
 #pragma unroll
         for (int hh = 0; hh < kCols; ++hh)
 #pragma unroll
@@ -713,6 +719,33 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
                 if (kE4m3) grew |= top_x(hh, e) > sm[hh][e] + kSlackSum;
             }
         if (__any_sync(0xffffffffu, grew)) {
+            if (kE4m3) {
+                // A value row of zeros would count as one of values near 448, and beside rows of 1e-6 their weights would lose
+                // their bits.  Rows with its exponent are looked at, a lane to a row and each at another piece, until all
+                // have shown something else.
+                const int at = lane & (S::kTileKeys - 1);
+                bool zero = lane < S::kTileKeys && (mask >> at & 1) &&
+                            *static_cast<const volatile unsigned char*>(me + S::kTileKeys + at) == kZeroByte;
+                if (__any_sync(0xffffffffu, zero)) {
+                    copy_wait<kSlots - 1>();
+                    __syncwarp();
+                    const int r = at & 15;
+                    const uint32_t row = ring + slot + (at >> 4) * S::kPart +
+                                         (S::kRow >= 128 ? r * 128 : (r >> 1) * 128 + ((r & 1) ^ (r >> 2 & 1)) * 64);
+                    constexpr int kLine = S::kRow >= 128 ? 8 : 4;   // pieces of a row side by side
+#pragma unroll 1
+                    for (int i = 0; i < S::kRow / 16 && __any_sync(0xffffffffu, zero); ++i) {
+                        const uint4 v = lds128(row + i / kLine * 2048 + ((i + lane) & (kLine - 1)) * 16);
+                        zero = zero && ((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) == 0;
+                    }
+                    const uint32_t zeros = __ballot_sync(0xffffffffu, zero);
+#pragma unroll
+                    for (int h = 0; h < S::kParts; ++h)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            if (zeros >> (16 * h + 8 * k + g) & 1) vexp[h][k] = -INFINITY;
+                }
+            }
 #pragma unroll
             for (int hh = 0; hh < kCols; ++hh)
 #pragma unroll
