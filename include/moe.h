@@ -479,7 +479,8 @@ moe_status_t moe_dispatch_static(const moe_config_t* cfg, const float* scores_de
 /* A paged key-value cache: stores k and v, [n_pages, page_size, n_kv_heads,
  * head_dim] by shape, with any strides (the same for k and v) whose last one is
  * 1: token-major and head-major pages are both fine.  head_dim is 64, 128 or 256.
- * k and v are 16-byte aligned, their strides multiples of 16 bytes.
+ * k and v are 16-byte aligned, their strides multiples of 16 bytes; a page or token
+ * stride below 0 is MOE_ERR_UNSUPPORTED.
  * MOE_KV_E4M3: a row's values are e4m3(code) * 2^(byte - 127); the exponent bytes
  * k_exp, v_exp are [n_pages, page_size, n_kv_heads] by shape with strides of their
  * own.  A power of two leaves every stored value exact in bf16 and costs no
@@ -577,7 +578,7 @@ moe_status_t moe_paged_attention_workspace_init(void* ws_dev, size_t ws_bytes, v
  * Lengths are read on the device: a captured graph replays at other lengths.  A
  * length outside [0, max_pages * page_size] (at most 2^31 - 65536) is brought to its nearer end, and keys
  * of a page outside [0, n_pages) are left out; both record MOE_ERR_INDEX.  Page and token
- * strides of 4 GB and more, or below 0, are MOE_ERR_UNSUPPORTED. */
+ * strides of 4 GB and more are MOE_ERR_UNSUPPORTED. */
 moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_attention_t* a, void* ws_dev,
                                  size_t ws_bytes, void* stream);
 

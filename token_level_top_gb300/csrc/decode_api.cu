@@ -21,7 +21,7 @@ moe_status_t check_cache(const moe_kv_cache_t* c)
     const bool e4m3 = c->type == MOE_KV_E4M3;
     if ((c->k_exp != nullptr) != e4m3 || (c->v_exp != nullptr) != e4m3) return MOE_ERR_INVALID_ARG;
     if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return MOE_ERR_UNSUPPORTED;
-    if (c->n_kv_heads > kMaxHeads) return MOE_ERR_UNSUPPORTED;
+    if (c->n_kv_heads > kMaxHeads || c->page_stride < 0 || c->token_stride < 0) return MOE_ERR_UNSUPPORTED;
     const int64_t unit = e4m3 ? 16 : 8;   // elements per 16 bytes
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % unit || c->token_stride % unit ||
         c->head_stride % unit)
@@ -130,9 +130,7 @@ moe_status_t moe_paged_attention(const moe_kv_cache_t* c, const moe_attention_t*
         return MOE_ERR_INVALID_ARG;
     // the kernel's place of a row in a page is a 32-bit byte offset
     const int64_t elt = c->type == MOE_KV_E4M3 ? 1 : 2, far = int64_t{1} << 32;
-    if (p->n_heads > kMaxHeads || c->page_stride < 0 || c->token_stride < 0 || c->page_stride >= far / elt ||
-        c->token_stride >= far / elt)
-        return MOE_ERR_UNSUPPORTED;
+    if (p->n_heads > kMaxHeads || c->page_stride >= far / elt || c->token_stride >= far / elt) return MOE_ERR_UNSUPPORTED;
     if (!ws) return MOE_ERR_INVALID_ARG;
     if (!aligned(ws, 256)) return MOE_ERR_MISALIGNED;
     if (ws_bytes < paged_attention_ws_bytes(c->head_dim)) return MOE_ERR_WORKSPACE;
