@@ -33,3 +33,21 @@ def test_negative_page_and_token_strides_are_refused(L, e4m3, kw):
     t = moe.MoEAttention(3, 4, 2, 0, 0.1, FAKE, FAKE, 2, FAKE, FAKE, None, 512, 128, 512, 128)
     n = L.moe_paged_attention_workspace_size(128)
     assert L.moe_paged_attention(R(_cache(e4m3, **kw)), R(t), ctypes.c_void_p(FAKE), n, None) == 2
+
+
+def test_memory_of_another_kind_is_refused():
+    """Status words and workspaces reach a kernel as addresses: host memory and too little of it are refused before."""
+    import torch
+    host = torch.zeros(64, dtype=torch.int32)
+    for t in (host, host[:0], host.view(torch.uint8)[1:9], host[::2]):
+        with pytest.raises(ValueError, match="status"):
+            moe._memory(t, "status", 0)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        moe._device(host, "k")
+    with pytest.raises(ValueError, match="CUDA device 0"):
+        moe._rows(host, "pos", 64, 0)
+    # the last condition by itself: what get_device() says of host memory is -1
+    assert moe._memory(host, "status", -1) == host.data_ptr()
+    for t in (host[:0], host.view(torch.uint8)[1:9], host.view(torch.uint8)[:3], host[::2], host[:1].expand(64)):
+        with pytest.raises(ValueError, match="status"):
+            moe._memory(t, "status", -1)

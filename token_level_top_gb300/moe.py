@@ -504,19 +504,36 @@ _APPEND = struct.Struct("=5iI3Qq5Q8q")
 _ATTENTION = struct.Struct("=4if4x2Qq3Q4q")
 
 
-def _want(t: torch.Tensor, name: str, dtype, ndim: int):
-    """Raises ValueError unless t is a CUDA tensor of this type and rank whose last dimension is contiguous."""
-    if t.dtype is not dtype or t.dim() != ndim or not t.is_cuda or (t.stride(-1) != 1 and t.shape[-1] > 1):
-        raise ValueError(f"{name}: want a CUDA tensor of {ndim} dimensions, {dtype}, last one contiguous; "
+def _device(t: torch.Tensor, name: str) -> int:
+    """The index of t's device, where a call's kernel goes and its other tensors have to be: the current CUDA device."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name}: want a tensor of the current CUDA device, got one of {t.device}")
+    return dev
+
+
+def _want(t: torch.Tensor, name: str, dtype, ndim: int, dev: int):
+    """Raises ValueError unless t is a tensor of CUDA device dev, this type and rank, with its last dimension contiguous."""
+    if t.dtype is not dtype or t.dim() != ndim or t.get_device() != dev or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{name}: want a tensor of {ndim} dimensions, {dtype}, last one contiguous, on CUDA device {dev}; "
                          f"got {tuple(t.shape)} {t.dtype}, strides {t.stride()}, {t.device}")
 
 
-def _rows(t: torch.Tensor, name: str, n: int, dtype=torch.int32) -> int:
-    """The address of a contiguous CUDA array of n values of this type; ValueError for anything else."""
-    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or not t.is_cuda or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name}: want a contiguous CUDA tensor of {n} values, {dtype}; got {tuple(t.shape)} "
-                         f"{t.dtype}, strides {t.stride()}, {t.device}")
+def _rows(t: torch.Tensor, name: str, n: int, dev: int, dtype=torch.int32) -> int:
+    """The address of a contiguous array of n values of this type on CUDA device dev; ValueError for anything else."""
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or t.get_device() != dev or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: want a contiguous tensor of {n} values, {dtype}, on CUDA device {dev}; got "
+                         f"{tuple(t.shape)} {t.dtype}, strides {t.stride()}, {t.device}")
     return t.data_ptr()
+
+
+def _memory(t: torch.Tensor, name: str, dev: int) -> int:
+    """The address of a status word or workspace: contiguous memory of CUDA device dev that starts with an int32."""
+    p = t.data_ptr()
+    if t.get_device() != dev or t.nbytes < 4 or p % 4 or not t.is_contiguous():
+        raise ValueError(f"{name}: want a status_word or workspace on CUDA device {dev}; got {tuple(t.shape)} {t.dtype}, "
+                         f"strides {t.stride()}, {t.device}")
+    return p
 
 
 def _strides(t: torch.Tensor):
@@ -527,11 +544,6 @@ def _strides(t: torch.Tensor):
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
-
-
-def _stream_of(t: torch.Tensor) -> int:
-    """The current stream of t's device, as the handle itself."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def status_word(device="cuda") -> torch.Tensor:
@@ -546,15 +558,16 @@ class KVCache:
 
     def __init__(self, k, v, k_exp=None, v_exp=None):
         e4m3 = k_exp is not None
+        self.device = dev = _device(k, "k")
         for t, name in ((k, "k"), (v, "v")):
-            _want(t, name, torch.uint8 if e4m3 else torch.bfloat16, 4)
+            _want(t, name, torch.uint8 if e4m3 else torch.bfloat16, 4, dev)
         if k.shape != v.shape or _strides(k) != _strides(v) or e4m3 != (v_exp is not None):
             raise ValueError("k and v (and k_exp and v_exp) must have the same shape and strides")
         exp = (0, 0, 0)
         if e4m3:
             for t in (k_exp, v_exp):
-                if t.dtype is not torch.uint8 or t.shape != k.shape[:3] or not t.is_cuda:
-                    raise ValueError("k_exp, v_exp: want uint8 CUDA tensors [n_pages, page_size, n_kv_heads]")
+                if t.dtype is not torch.uint8 or t.shape != k.shape[:3] or t.get_device() != dev:
+                    raise ValueError("k_exp, v_exp: want uint8 tensors [n_pages, page_size, n_kv_heads] on the device of k")
             if _strides(k_exp) != _strides(v_exp):
                 raise ValueError("k_exp and v_exp must have the same strides")
             exp = _strides(k_exp)
@@ -592,21 +605,24 @@ def kv_append(cache: KVCache, k, v, pos, page_table, q=None, phase=None, seq=Non
     (None: token t belongs to row t of page_table [n_seqs, max_pages]) int32; phase from rope_phase on the device
     (None: no rotation).  Returns the rotated q (q_out when given, which may be q), or None without q.  status: a
     status_word or workspace that records indices out of range."""
+    dev = _device(k, "k")
     ks, vs, ts = k.stride(), v.stride(), page_table.stride()
     for t, strides, name in ((k, ks, "k"), (v, vs, "v")):
-        if len(strides) != 3 or strides[2] != 1 or t.dtype is not torch.bfloat16 or not t.is_cuda:
-            _want(t, name, torch.bfloat16, 3)
-    if len(ts) != 2 or ts[1] != 1 or page_table.dtype is not torch.int32 or not page_table.is_cuda:
-        _want(page_table, "page_table", torch.int32, 2)
+        if len(strides) != 3 or strides[2] != 1 or t.dtype is not torch.bfloat16 or t.get_device() != dev:
+            _want(t, name, torch.bfloat16, 3, dev)
+    if len(ts) != 2 or ts[1] != 1 or page_table.dtype is not torch.int32 or page_table.get_device() != dev:
+        _want(page_table, "page_table", torch.int32, 2, dev)
     shape = k.shape
     T, kv_heads, dim = shape
+    if cache.device != dev:
+        raise ValueError(f"cache: want one of CUDA device {dev}, got one of {cache.device}")
     if kv_heads != cache.n_kv_heads or dim != cache.head_dim or v.shape != shape:
         raise ValueError(f"k, v: want [T, {cache.n_kv_heads}, {cache.head_dim}], got {tuple(k.shape)}, {tuple(v.shape)}")
     heads, qp, qs, op, os_ = 0, 0, (0, 0), 0, (0, 0)
     if q is not None:
         qs = q.stride()
-        if len(qs) != 3 or qs[2] != 1 or q.dtype is not torch.bfloat16 or not q.is_cuda:
-            _want(q, "q", torch.bfloat16, 3)
+        if len(qs) != 3 or qs[2] != 1 or q.dtype is not torch.bfloat16 or q.get_device() != dev:
+            _want(q, "q", torch.bfloat16, 3, dev)
         shape = q.shape
         heads = shape[1]
         if shape[0] != T or shape[2] != dim:
@@ -615,7 +631,7 @@ def kv_append(cache: KVCache, k, v, pos, page_table, q=None, phase=None, seq=Non
             q_out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
             os_ = (heads * dim, dim)
         else:
-            _want(q_out, "q_out", torch.bfloat16, 3)
+            _want(q_out, "q_out", torch.bfloat16, 3, dev)
             if q_out.shape != shape:
                 raise ValueError(f"q_out: want {tuple(shape)}, got {tuple(q_out.shape)}")
             os_ = _strides(q_out)
@@ -627,13 +643,13 @@ def kv_append(cache: KVCache, k, v, pos, page_table, q=None, phase=None, seq=Non
     rot, pp = 0, 0
     if phase is not None:
         rot = 2 * phase.shape[0]
-        pp = _rows(phase, "phase", rot // 2, torch.int64)
+        pp = _rows(phase, "phase", rot // 2, dev, torch.int64)
     n_seqs, max_pages = page_table.shape
-    a = _APPEND.pack(T, n_seqs, max_pages, heads, rot, ROTATE_INTERLEAVED if interleaved else 0, _rows(pos, "pos", T),
-                     0 if seq is None else _rows(seq, "seq", T), page_table.data_ptr(), ts[0] if n_seqs > 1 else 0, pp, qp,
+    a = _APPEND.pack(T, n_seqs, max_pages, heads, rot, ROTATE_INTERLEAVED if interleaved else 0, _rows(pos, "pos", T, dev),
+                     0 if seq is None else _rows(seq, "seq", T, dev), page_table.data_ptr(), ts[0] if n_seqs > 1 else 0, pp, qp,
                      k.data_ptr(), v.data_ptr(), op, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1])
-    st = (_lib or lib()).moe_kv_append(cache.ref, a, None if status is None else status.data_ptr(),
-                                       torch._C._cuda_getCurrentRawStream(k.device.index))
+    st = (_lib or lib()).moe_kv_append(cache.ref, a, None if status is None else _memory(status, "status", dev),
+                                       torch._C._cuda_getCurrentRawStream(dev))
     if st:
         raise MoEError(st, "moe_kv_append")
     return q_out if q is not None else None
@@ -645,6 +661,7 @@ def attention_workspace(head_dim: int, device="cuda") -> torch.Tensor:
     if n == 0:
         raise MoEError(2, "moe_paged_attention_workspace_size")
     ws = torch.empty(n, dtype=torch.uint8, device=device)
+    _device(ws, "device")
     _check(lib().moe_paged_attention_workspace_init(_p(ws), n, _stream()), "moe_paged_attention_workspace_init")
     return ws
 
@@ -653,11 +670,14 @@ def paged_attention(cache: KVCache, ws, q, seq_len, page_table, scale=None, wind
     """Attention of one new token per sequence over the cache (moe_paged_attention): q [B, n_heads, head_dim] bf16,
     seq_len [B] and page_table [B, max_pages] int32, scale (None: head_dim ** -0.5), window (0: all cached tokens).
     Returns out [B, n_heads, head_dim] bf16, and lse [B, n_heads] fp32 with return_lse."""
+    dev = _device(q, "q")
     qs, ts = q.stride(), page_table.stride()
-    if len(qs) != 3 or qs[2] != 1 or q.dtype is not torch.bfloat16 or not q.is_cuda:
-        _want(q, "q", torch.bfloat16, 3)
-    if len(ts) != 2 or ts[1] != 1 or page_table.dtype is not torch.int32 or not page_table.is_cuda:
-        _want(page_table, "page_table", torch.int32, 2)
+    if len(qs) != 3 or qs[2] != 1 or q.dtype is not torch.bfloat16:
+        _want(q, "q", torch.bfloat16, 3, dev)
+    if len(ts) != 2 or ts[1] != 1 or page_table.dtype is not torch.int32 or page_table.get_device() != dev:
+        _want(page_table, "page_table", torch.int32, 2, dev)
+    if cache.device != dev:
+        raise ValueError(f"cache: want one of CUDA device {dev}, got one of {cache.device}")
     shape = q.shape
     B, heads, dim = shape
     n_seqs, max_pages = page_table.shape
@@ -666,23 +686,22 @@ def paged_attention(cache: KVCache, ws, q, seq_len, page_table, scale=None, wind
                          f"{tuple(page_table.shape)}")
     if not 0 <= window < 2 ** 31:
         raise ValueError(f"window: want 0 .. 2^31 - 1, got {window}")
-    dev = q.device
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
         os_ = (heads * dim, dim)
     else:
-        _want(out, "out", torch.bfloat16, 3)
+        _want(out, "out", torch.bfloat16, 3, dev)
         if out.shape != shape:
             raise ValueError(f"out: want {tuple(shape)}, got {tuple(out.shape)}")
         os_ = _strides(out)
-    lse = torch.empty(B, heads, dtype=torch.float32, device=dev) if return_lse else None
+    lse = torch.empty(B, heads, dtype=torch.float32, device=q.device) if return_lse else None
     if B == 1 or heads == 1:
         qs = _strides(q)
     a = _ATTENTION.pack(B, heads, max_pages, window, dim ** -0.5 if scale is None else scale,
-                        _rows(seq_len, "seq_len", B), page_table.data_ptr(), ts[0] if B > 1 else 0, q.data_ptr(),
+                        _rows(seq_len, "seq_len", B, dev), page_table.data_ptr(), ts[0] if B > 1 else 0, q.data_ptr(),
                         out.data_ptr(), lse.data_ptr() if return_lse else 0, qs[0], qs[1], os_[0], os_[1])
-    st = (_lib or lib()).moe_paged_attention(cache.ref, a, ws.data_ptr(), ws.nbytes,
-                                             torch._C._cuda_getCurrentRawStream(dev.index))
+    st = (_lib or lib()).moe_paged_attention(cache.ref, a, _memory(ws, "ws", dev), ws.nbytes,
+                                             torch._C._cuda_getCurrentRawStream(dev))
     if st:
         raise MoEError(st, "moe_paged_attention")
     return (out, lse) if return_lse else out
@@ -695,9 +714,10 @@ def token_logprobs(logits, token=None, top=0, status=None):
     kind = LOGITS.get(logits.dtype)
     if kind is None:
         raise ValueError(f"logits: want float32 or bfloat16, got {logits.dtype}")
+    index = _device(logits, "logits")
     xs = logits.stride()
-    if len(xs) != 2 or xs[1] != 1 or not logits.is_cuda:
-        _want(logits, "logits", logits.dtype, 2)
+    if len(xs) != 2 or xs[1] != 1:
+        _want(logits, "logits", logits.dtype, 2, index)
     n, v = logits.shape
     dev = logits.device
     f, empty = torch.float32, torch.empty   # (one allocation per output: views of a common one cost more)
@@ -706,15 +726,15 @@ def token_logprobs(logits, token=None, top=0, status=None):
     lp = tp = ids = tops = None
     if token is not None:
         out["logprob"] = logprob = empty(n, dtype=f, device=dev)
-        lp, tp = logprob.data_ptr(), _rows(token, "token", n)
+        lp, tp = logprob.data_ptr(), _rows(token, "token", n, index)
     if top > 0:
         out["top_ids"] = ids = empty(n, top, dtype=torch.int32, device=dev)
         out["top_logprobs"] = tops = empty(n, top, dtype=f, device=dev)
         ids, tops = ids.data_ptr(), tops.data_ptr()
     st = (_lib or lib()).moe_token_logprobs(n, v, kind, logits.data_ptr(), xs[0] if n > 1 else 0, tp, top, lp,
                                             entropy.data_ptr(), lse.data_ptr(), ids, tops,
-                                            None if status is None else status.data_ptr(),
-                                            torch._C._cuda_getCurrentRawStream(dev.index))
+                                            None if status is None else _memory(status, "status", index),
+                                            torch._C._cuda_getCurrentRawStream(index))
     if st:
         raise MoEError(st, "moe_token_logprobs")
     return out
@@ -725,22 +745,23 @@ def token_logprobs_backward(logits, token, lse, entropy=None, dlogprob=None, den
     its lse and entropy.  Returns dlogits [rows, vocab] of the logits' type (out when given, which may be logits)."""
     if logits.dtype not in LOGITS:
         raise ValueError(f"logits: want float32 or bfloat16, got {logits.dtype}")
-    _want(logits, "logits", logits.dtype, 2)
+    dev = _device(logits, "logits")
+    _want(logits, "logits", logits.dtype, 2, dev)
     n, v = logits.shape
     f = torch.float32
     if out is None:
         out = torch.empty(n, v, dtype=logits.dtype, device=logits.device)
     else:
-        _want(out, "out", logits.dtype, 2)
+        _want(out, "out", logits.dtype, 2, dev)
         if out.shape != logits.shape:
             raise ValueError(f"out: want {tuple(logits.shape)}, got {tuple(out.shape)}")
     st = lib().moe_token_logprobs_backward(
         n, v, LOGITS[logits.dtype], logits.data_ptr(), _strides(logits)[0],
-        None if token is None else _rows(token, "token", n), _rows(lse, "lse", n, f),
-        None if entropy is None else _rows(entropy, "entropy", n, f),
-        None if dlogprob is None else _rows(dlogprob, "dlogprob", n, f),
-        None if dentropy is None else _rows(dentropy, "dentropy", n, f), out.data_ptr(), _strides(out)[0], _ptr(status),
-        _stream_of(logits))
+        None if token is None else _rows(token, "token", n, dev), _rows(lse, "lse", n, dev, f),
+        None if entropy is None else _rows(entropy, "entropy", n, dev, f),
+        None if dlogprob is None else _rows(dlogprob, "dlogprob", n, dev, f),
+        None if dentropy is None else _rows(dentropy, "dentropy", n, dev, f), out.data_ptr(), _strides(out)[0],
+        None if status is None else _memory(status, "status", dev), torch._C._cuda_getCurrentRawStream(dev))
     if st:
         raise MoEError(st, "moe_token_logprobs_backward")
     return out
