@@ -607,7 +607,9 @@ moe_status_t moe_token_logprobs(int64_t rows, int32_t vocab, uint32_t type, cons
 
 /* Gradient of logprob and entropy with respect to the logits, from the forward's
  * lse and entropy:  dx_i = g (1[i = token] - p_i) - h p_i (ln p_i + entropy),
- * g = dlogprob (0 for a row without a token), h = dentropy; either may be NULL (0).
+ * p_i = e^(x_i - lse), g = dlogprob (0 for a row without a token), h = dentropy; either may
+ * be NULL (0).  lse is fp32, so p_i is off by up to |lse| 2^-24 of itself: rows around values
+ * of some thousands and more are better shifted to their maximum before both calls.
  * dlogits_dev [rows, vocab] of the logits' type, rows drow_stride apart; it may be the
  * logits themselves. */
 moe_status_t moe_token_logprobs_backward(int64_t rows, int32_t vocab, uint32_t type,

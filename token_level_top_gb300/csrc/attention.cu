@@ -25,9 +25,10 @@
 //   values: C[d][head] += V^T P.  A lane holds pieces of four keys' rows, which
 //   byte permutes pair up over the keys; the order of d is free.  The weights
 //   get from the layout of C to that of B by a matrix transpose across the warp.
-// The weights go in as the sum of two 16-bit parts (their own rounding would
-// cost more than the output's); with at most 4 query heads the columns 4..7
-// carry the low parts, so both take one product.
+// The weights go in as the sum of two 16-bit parts (one rounding of them to bf16
+// would cost as much as the output's; an f16 one is finer, but not for weights far
+// below the largest); with at most 4 query heads the columns 4..7 carry the low
+// parts, so both take one product.
 //
 // The running maximum is raised only when a score passes it by 2^kSlack: the
 // weights stay below 2^kSlack, sums are fp32, and the usual tile needs neither
@@ -41,12 +42,14 @@
 // up to 4096: 179 us with one maximum for both, 181 with two).
 //
 // Measured (32 query heads on 8, D = 128, 6801 GB/s copied): 64 sequences up to
-// 8192, bf16, 1083 MB in 166 us (0.96 of the copy rate); one of 131072, 537 MB in
-// 89 us (0.88: the start and the join of 456 parts); 256 up to 4096, e4m3, 1091 MB
-// in 179 us (0.90).  The bf16 kernel waits for its copies (issue slots 30% busy).
-// The e4m3 one has half the bytes per key and the same products on top of two
-// conversions a code pair: some 890 instructions per 32 keys, a half of its issue
-// slots, and 167 registers leave 12 warps an SM to fill them.
+// 8192, bf16, 1083 MB in 167 us (0.96 of the copy rate); one of 131072, 537 MB in
+// 89 us (0.89: the start, and the join of 57 parts for each of 8 key heads); 256 up
+// to 4096, e4m3, 64 heads on 8, 1091 MB in 181 us (0.89).  The bf16 kernel waits for
+// its copies (issue slots 30% busy).  The e4m3 one has half the bytes per key and the
+// same products on top of a conversion per code pair: some 910 instructions per 32
+// keys, 55% of its issue slots, and 168 registers leave 12 warps an SM to fill them.
+// Of the same batch with a fiftieth of the value rows zeros 207 us (they are looked
+// at), with exponents anywhere in 130 powers of two 184.
 #include <algorithm>
 
 #include "common.cuh"
@@ -162,7 +165,7 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint3
 }
 
 // A condition that all lanes of the (converged) warp agree on, in a form that the compiler knows as such: what it cannot
-// prove uniform it branches on with reconvergence bookkeeping (256 sequences up to 4096, e4m3: 220 us without).
+// prove uniform it branches on with reconvergence bookkeeping (256 sequences up to 4096, e4m3: 4% slower without).
 __device__ __forceinline__ bool uniform(bool x) { return __any_sync(0xffffffffu, x); }
 
 // *counter == last ? 0 : *counter + 1, and the value before: the block's writes so far (ordered before thread
@@ -188,7 +191,7 @@ struct Shape {
     static constexpr int kOut = D / 16 * 4 * kCols;           // output registers
     static constexpr int kWarps = 4;
     // blocks per SM, as the registers of outputs and queries allow: 128, 168 or 255 a thread (16 heads of 64, e4m3, whose
-    // conversions need more beside them: 64 sequences up to 8192 in 53 us, 69 with three blocks that spill)
+    // conversions need more beside them: 64 sequences up to 8192, 128 heads on 8, in 94 us, 132 with three blocks that spill)
     static constexpr int kHeld = kOut + D / 8 * kCols;
     static constexpr int kCtas = kHeld <= 24 ? 4 : (kHeld <= 48 && !(kE4m3 && kCols == 2) ? 3 : 2);
     // 16-key parts of a tile: two where a row is short, so that a pass of the loop does twice the work
@@ -196,13 +199,13 @@ struct Shape {
     static constexpr int kPart = 16 * kRow;                   // bytes of 16 keys
     static constexpr int kTile = kParts * kPart;              // bytes of a warp's key (or value) tile
     static constexpr int kTileKeys = 16 * kParts;
-    // tiles whose pages are looked up in advance; the e4m3 loop has no registers for two (230 against 220 us,
+    // tiles whose pages are looked up in advance; the e4m3 loop has no registers for two (186 against 180 us,
     // 256 sequences up to 4096)
     static constexpr int kAhead = kE4m3 ? 1 : 2;
     static constexpr int kGranule = kTileKeys * kWarps;       // keys
     // What an item costs beside its granules (the block's join of its warps, the output or the part): so many places of
     // the list are left empty behind it.  With none the blocks that met the most items set the time (64 + 8 heads of
-    // 128, e4m3, 256 sequences up to 4096: 209 us; 1 185, 2 180, 3 182; 512 up to 1024: 149, 127, 122, 126).
+    // 128, e4m3, 256 sequences up to 4096: 213 us; 1 188, 2 180, 3 182; 512 up to 1024: 154, 131, 125, 129).
     static constexpr int kGap = 2;
     static constexpr int kJoin = D == 64 && kHeads == 16 ? 8 : 4;   // heads that the block joins at a time, as memory allows
     static constexpr int kMerge = kWarps * kJoin * D * 4;
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(32 * Shape<D, kE4m3, kHeads>::kWarps, Shape<D,
     const uint32_t to_v = ring + sub * 128 + (S::kRow >= 128 ? piece ^ (sub >> 1) << 1 : piece ^ sub << 1) * 16;
     const uint32_t from_k = ring + (S::kRow >= 128 ? g * 128 + (c ^ ((g & 1) << 2 | g >> 1)) * 16 : lane * 16);
     const uint32_t from_v = ring + (S::kRow >= 128 ? c * 256 + (g ^ c << 1) * 16 : c * 128 + ((g >> 1) ^ c << 1) * 16 + (g & 1) * 8);
-    // a part's keys lie in one page, and one look-up serves them (64 sequences up to 8192, 168 us, otherwise 172; e4m3 100 and
+    // a part's keys lie in one page, and one look-up serves them (64 sequences up to 8192, 167 us, otherwise 172; e4m3 92 and
     // 130)
     const bool one_page = a.page_size % 16 == 0;
     // of the item whose tiles are copied: its table row, this lane's place in a page of its key head (for
@@ -1060,9 +1063,9 @@ template <int D, bool kE4m3>
 cudaError_t launch_d(const AttentionArgs& a, cudaStream_t s)
 {
     // Up to 4 query heads per key head take both parts of the weights in one product (64 sequences up to 8192, D = 64,
-    // e4m3: 69 us, 73 as 8; bf16 and D = 128 within 1%); at D = 256 the 8-wide form is as fast, and its join is
-    // shorter (1 of 777: 9.4 us against 15.4).  More than 8 share one read of the cache between 16 (16 on one key
-    // head, D = 128: 98 us, 162 as two blocks of 8); at D = 256 the registers hold 8.
+    // e4m3: 66 us, 68 as 8; bf16 and D = 128 within 1%); at D = 256 the 8-wide form is as fast, and its join is
+    // shorter (1 of 777: 9.4 us against 15.4).  More than 8 share one read of the cache between 16 (the same with 128 heads
+    // on 8, D = 128: 173 us, 321 as two blocks of 8; e4m3 133 and 174); at D = 256 the registers hold 8.
     const int group = a.n_heads / a.n_kv_heads;
     if constexpr (D < 256) {
         if (group <= 4) return launch_heads<D, kE4m3, 4>(a, s);

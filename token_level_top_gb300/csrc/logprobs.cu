@@ -6,7 +6,8 @@
 // A thread keeps the running maximum m of what it has read and, against it,
 //   l = sum 2^z,  w = sum 2^z z,  z = (x - m) log2 e,
 // so that lse = m + ln l and entropy = ln l - ln 2 * w / l: sums of terms of one
-// sign, whatever the size of the logits.
+// sign, whatever the size of the logits (z as it is computed has a known rounding of
+// m log2 e in it, which is taken out again: Stats).
 // Alternatives: no list is kept while streaming, only the maximum of every few
 // pieces that a thread reads.  From the threads' maxima comes a threshold that at
 // least n values reach; the pieces whose maximum reaches it -- some dozens, still
@@ -15,7 +16,7 @@
 // Backward: element by element, from lse and entropy.
 //
 // Measured (6801 GB/s copied): 4096 x 131072 fp32 with the 5 best, 2147 MB read in
-// 310 us (1.02 of the copy rate); 2047 x 50257 bf16 with the 20 best, 206 MB in 43 us
+// 312 us (1.01 of the copy rate); 2047 x 50257 bf16 with the 20 best, 206 MB in 43 us
 // (0.70); the gradient of 4096 x 50257 bf16, 823 MB in 119 us (1.02).  fp32 rows and
 // gradients are bound by memory; bf16 rows by instructions as well (some 50 for the 8
 // values of a piece: unpack, raise, fma, ex2, add, fma) and by what a row waits for.
@@ -849,20 +850,20 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t s)
     if (args.rows <= 0) return cudaSuccess;
     LogprobArgs a = args;
     // Few rows: a cluster of blocks per row, while a block keeps 8 pieces per thread and the rows' blocks are at most two
-    // an SM.  Long rows gain (us for the 20 best of bf16 rows, with 1 / 2 / 4 / 8 blocks a row: one row of 131072 14.4 /
-    // 11.5 / 9.8 / 9.9, 128 rows 21.0 / 16.5 / 17.8 / 27.5); short ones and many rows lose (one row of 32000 8.2 / 8.7 /
-    // 8.6 / 8.6, 256 rows 11.3 / 14.7 / 23.0 / 23.1; of 131072 24.9 / 23.7 / 32.3 / 50.4).
+    // an SM.  Long rows gain (us for the 20 best of bf16 rows, with 1 / 2 / 4 / 8 blocks a row: one row of 131072 14.1 /
+    // 10.3 / 8.8 / 8.7, 128 rows 20.4 / 15.4 / 16.4 / 25.7); short ones and many rows lose or stay (one row of 32000 7.8 / 8.2
+    // / 7.7 / 7.9, 256 rows 10.3 / 13.7 / 20.9 / 40.8; of 131072 24.2 / 21.7 / 29.7 / 48.1).
     const long long pieces = static_cast<long long>(a.vocab) * (a.bf16 ? 2 : 4) / 16;
     a.split = 1;
     while (a.split < 8 && a.rows * a.split <= num_sms() && pieces / (a.split * 2) >= 8 * kThreads) a.split *= 2;
     if (a.rows * a.split > 0x7fffffffLL) return cudaErrorInvalidValue;
     const bool many = a.rows > blocks_of(kThreads) * static_cast<long long>(num_sms());   // more rows than blocks fit at once
     // Many short rows: what a row waits for (its loads, its search) is long against its work, so as many as fit, two
-    // warps each (us for the 20 best of 4096 bf16 rows, two warps and otherwise: of 4000 23.2 and 39.5, of 16000 42.5 and
-    // 52.4, of 32000 66.0 and 65.4, of 50257 108 and 80; statistics alone of 16000 29.5 and 36.0).
+    // warps each (us for the 20 best of 4096 bf16 rows, two warps and otherwise: of 4000 22.7 and 39.5, of 16000 42.7 and
+    // 51.7, of 20000 53.7 and 54.2, of 32000 66.8 and 64.8, of 50257 109 and 81; statistics alone of 16000 29.4 and 36.6).
     if (many && pieces <= 2560) return launch_rows<kFewThreads>(a, s);
-    // Many long ones: rows are read ahead of their alternatives (20 best of 131072 bf16: 760 rows 43.5 us, 48.0 streamed;
-    // 800 rows 57.4 and 49.4; 4096 rows 202 and 186).
+    // Many long ones: rows are read ahead of their alternatives (20 best of 131072 bf16: 760 rows 40.8 us, 46.3 streamed;
+    // 800 rows 54.9 and 46.6; 4096 rows 192 and 179).
     if (a.n_top > 0 && many) {
         const unsigned grid = static_cast<unsigned>(kStreamBlocks * num_sms());
         if (a.bf16)
@@ -871,8 +872,8 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t s)
             token_logprobs_stream_kernel<float><<<grid, kReaders + kFinishers, sizeof(StreamShared<float>), s>>>(a);
         return cudaGetLastError();
     }
-    // One or two long rows an SM: more loads in flight for each (20 best of 200 / 300 rows of 131072 fp32: 28.5 / 34.5 us,
-    // 35.7 / 38.7 with 256 threads; of 65536 bf16 13.2 / 15.4 and 12.5 / 15.9).
+    // One or two long rows an SM: more loads in flight for each (20 best of 200 / 300 rows of 131072 fp32: 28.2 / 35.0 us,
+    // 34.9 / 38.4 with 256 threads; of 65536 bf16, which gain nothing, 13.2 / 15.4 and 12.5 / 15.9).
     if (a.split == 1 && a.rows > num_sms() && a.rows <= 2LL * num_sms() && pieces >= 12288) return launch_rows<kMoreThreads>(a, s);
     return launch_rows<kThreads>(a, s);
 }
