@@ -543,6 +543,24 @@ moe_status_t moe_rope_phase(int32_t n, const double* inv_freq, uint64_t* phase);
 moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const moe_append_t* a, int32_t* status_dev,
                            void* stream);
 
+#define MOE_MAX_AXES 4
+
+/* Positions of rotation that are not the place in the sequence: drafted tokens (the
+ * place goes by the order of drafting, the position by the depth in the tree), and
+ * images and video (time, height, width).  Pair i turns by rotary[axis[i], t] *
+ * inv_freq[i]; moe_append_t.pos stays the place in the cache (< 0: padding). */
+typedef struct {
+    int32_t n_axes;              /* 1 .. MOE_MAX_AXES */
+    const int32_t* rotary;       /* [n_axes, T] positions, negative ones too; axes axis_stride elements apart */
+    int64_t axis_stride;
+    const uint8_t* axis;         /* [rot_dim / 2] the axis of each pair, or NULL: axis 0 */
+} moe_rotation_t;
+
+/* moe_kv_append with the positions of rotation given apart (rot_dim > 0).  An axis
+ * past n_axes records MOE_ERR_INDEX, and its pairs are not turned. */
+moe_status_t moe_kv_append_axes(const moe_kv_cache_t* cache, const moe_append_t* a, const moe_rotation_t* rotation,
+                                int32_t* status_dev, void* stream);
+
 /* One new token per sequence for moe_paged_attention. */
 typedef struct {
     int32_t B;                   /* sequences */
@@ -582,6 +600,48 @@ moe_status_t moe_paged_attention_workspace_init(void* ws_dev, size_t ws_bytes, v
 moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_attention_t* a, void* ws_dev,
                                  size_t ws_bytes, void* stream);
 
+/* A tree of drafted tokens per sequence for moe_tree_attention. */
+#define MOE_MAX_DRAFTED 64
+typedef struct {
+    int32_t B;                   /* sequences */
+    int32_t T;                   /* rows of q and out */
+    int32_t n_heads;             /* as in moe_attention_t */
+    int32_t max_pages;           /* page table [B, max_pages], rows table_stride apart */
+    int32_t window;              /* > 0: only the last `window` tokens of a row's path; 0: all */
+    float scale;                 /* of the scores, finite */
+    const int32_t* row_start;    /* [B + 1] sequence b's drafted tokens are rows row_start[b] .. row_start[b + 1] - 1:
+                                    none, or up to MOE_MAX_DRAFTED */
+    const int32_t* seq_len;      /* [B] cached tokens, the drafted ones included (they are the last) */
+    const uint64_t* mask;        /* [T] bit j: the row sees drafted token j of its sequence; NULL: bits 0 .. its own */
+    const int32_t* page_table;
+    int64_t table_stride;
+    const void* q;               /* [T, n_heads, head_dim] bf16 */
+    void* out;                   /* [T, n_heads, head_dim] bf16 */
+    float* lse;                  /* [T, n_heads] fp32 or NULL */
+    int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+} moe_tree_attention_t;
+
+/* As moe_paged_attention_workspace_size and _init, for moe_tree_attention. */
+size_t moe_tree_attention_workspace_size(int32_t head_dim);
+moe_status_t moe_tree_attention_workspace_init(void* ws_dev, size_t ws_bytes, void* stream);
+
+/* Attention of several new tokens per sequence over the cache that holds them: a tree
+ * of drafted tokens (a token sees its ancestors and itself), or a short run of a prompt.
+ *   row i of sequence b sees the context, tokens 0 .. c - 1 with c = seq_len[b] - n, and
+ *   the drafted tokens (number j is cached at c + j) whose bit its mask has,
+ * and its output is moe_paged_attention's over what it sees.  With a window those are the
+ * last `window` of its path: the drafted tokens it sees, the highest numbers first, then
+ * the context from its end.  A row that sees nothing, or no score above -inf, gets zeros
+ * and lse = -inf.  What a row does not see (NaN and infinities included) has no effect on
+ * it.  Row_start and lengths are read on the device: a captured graph replays at others.
+ * Rows of q before row_start[0] and from row_start[B] on are not read, theirs of out and lse not written.
+ * A row_start that falls, ends past T or gives a sequence more than MOE_MAX_DRAFTED rows
+ * (the sequence then has no rows), a length that moe_paged_attention would correct, or one
+ * below the number of its drafted tokens (the first ones then are in no place and not seen), and keys of a
+ * page outside [0, n_pages) (left out) record MOE_ERR_INDEX. */
+moe_status_t moe_tree_attention(const moe_kv_cache_t* cache, const moe_tree_attention_t* a, void* ws_dev, size_t ws_bytes,
+                                void* stream);
+
 /* moe_token_logprobs type */
 #define MOE_LOGITS_F32 0u
 #define MOE_LOGITS_BF16 1u
@@ -618,6 +678,109 @@ moe_status_t moe_token_logprobs_backward(int64_t rows, int32_t vocab, uint32_t t
                                          const float* entropy_dev, const float* dlogprob_dev,
                                          const float* dentropy_dev, void* dlogits_dev,
                                          int64_t drow_stride, int32_t* status_dev, void* stream);
+
+#define MOE_MAX_BEAMS 64
+
+/* Bytes of the workspace for moe_beam_select with up to `rows` rows of logits (sequences
+ * times beams) and n candidates (0: unsupported), and its set-up, enqueued on `stream` once
+ * after allocating it (256-byte aligned).  The first word is a status word.  Calls that
+ * share a workspace must not overlap. */
+size_t moe_beam_workspace_size(int64_t rows, int32_t n);
+moe_status_t moe_beam_workspace_init(void* ws_dev, size_t ws_bytes, void* stream);
+
+/* The best continuations of a step of beam search: of the totals
+ *   scores[b, w] + x[v] - ln sum_i e^(x_i),  x: row b * beams + w of the logits [seqs * beams, vocab]
+ * the n largest of each sequence, in order: out_scores [seqs, n] (each total formed in fp64 and rounded
+ * once), parents [seqs, n] (w) and tokens [seqs, n] (v).  Ties go to the lower beam, then
+ * to the larger logit, then to the lower token.  logits as in moe_token_logprobs.
+ * scores_dev [seqs, beams] fp32: -inf for a beam that is not alive; a masked logit is
+ * -inf too, so a finished beam is a row of -inf but for one token.  Totals of -inf are
+ * no candidates; places past the last one hold -inf, -1, -1.  A row with NaN or +inf, or a NaN
+ * score, gives none and records MOE_ERR_NONFINITE.  1 <= n <= MOE_MAX_TOP, beams <=
+ * MOE_MAX_BEAMS.  status: the workspace's. */
+moe_status_t moe_beam_select(int32_t seqs, int32_t beams, int32_t vocab, uint32_t type, const void* logits_dev,
+                             int64_t row_stride, const float* scores_dev, int32_t n, float* out_scores_dev,
+                             int32_t* parents_dev, int32_t* tokens_dev, void* ws_dev, size_t ws_bytes, void* stream);
+
+/* The beams' cached tokens after a selection, for moe_beam_reorder. */
+typedef struct {
+    int32_t seqs, beams;         /* beam w of sequence b is row b * beams + w of the tables */
+    int32_t max_pages;
+    const int32_t* parents;      /* [seqs, beams], rows parent_stride apart: the beam whose tokens beam w goes on from;
+                                    < 0: none (the row's tokens do not matter any more) */
+    int64_t parent_stride;
+    const int32_t* seq_len;      /* [seqs] cached tokens of each of the sequence's beams */
+    const int32_t* page_table;   /* [seqs * beams, max_pages], rows table_stride apart */
+    int64_t table_stride;
+    int32_t* page_table_out;     /* another table of that shape */
+    int64_t table_out_stride;
+} moe_beam_reorder_t;
+
+/* Gives every beam its parent's cached tokens, one launch.  The pages that are full (seq_len /
+ * page_size of them) become entries of both; the page after them, when it holds tokens
+ * already, has to be each beam's own before and after: the first child of a parent keeps the
+ * parent's, the other children (and beams without a parent), in order, take those of the
+ * beams that no beam goes on from, in order, and the children's get the parent's rows copied
+ * into them.  Later entries stay with their row.  A parent past `beams` counts as none, a length outside
+ * [0, max_pages * page_size] is brought to its nearer end, a page outside [0, n_pages) is
+ * not copied; each records MOE_ERR_INDEX.  Full pages that no table names any more are the caller's to reuse. */
+moe_status_t moe_beam_reorder(const moe_kv_cache_t* cache, const moe_beam_reorder_t* a, int32_t* status_dev, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The norm of a decoder layer's input rows.
+ * ------------------------------------------------------------------------ */
+
+/* type, weight_type, dy_type */
+#define MOE_ROWS_F32 0u
+#define MOE_ROWS_BF16 1u
+
+/* Rows [rows, cols] at any alignment of their type, strides in elements; an input's
+ * stride may be 0 (one row for all).  cols <= 16384. */
+typedef struct {
+    int64_t rows;
+    int32_t cols;
+    uint32_t type;               /* MOE_ROWS_*: of x, residual, sum and y */
+    uint32_t weight_type;
+    float eps;                   /* 1e-30 or more, finite */
+    const void* x;
+    const void* residual;        /* or NULL */
+    const void* weight;          /* [cols], or NULL: ones */
+    void* sum;                   /* x + residual, or NULL (NULL without a residual); may be x or residual itself */
+    void* y;                     /* or NULL; may be x or residual itself */
+    void* codes;                 /* e4m3 codes, or NULL */
+    float* scales;               /* [rows], with codes */
+    int64_t x_stride, residual_stride, sum_stride, y_stride, codes_stride;
+} moe_rms_norm_t;
+
+/* s = x + residual, rounded to the rows' type; y = s * (mean of s^2 + eps)^(-1/2) * weight in
+ * fp32, rounded once to y and, as moe_quantize_fp8 does, to codes = e4m3(y / scale), scale =
+ * max|y| / 448 (1 for a row of zeros).  Any finite s has a norm (squares that overflow are
+ * scaled).  A row with a NaN or an infinity is NaN, its scale too, and records MOE_ERR_NONFINITE. */
+moe_status_t moe_rms_norm(const moe_rms_norm_t* a, int32_t* status_dev, void* stream);
+
+typedef struct {
+    int64_t rows;
+    int32_t cols;
+    uint32_t type;               /* of x, dsum and dx */
+    uint32_t dy_type;            /* of dy: fp32, or that of x */
+    uint32_t weight_type;
+    float eps;
+    const void* x;               /* what was normalised: sum, or x without a residual */
+    const void* weight;          /* or NULL: ones */
+    const void* dy;
+    const void* dsum;            /* gradient that reaches the sum from elsewhere (the residual stream), or NULL */
+    void* dx;                    /* gradient of the sum, of x and of residual; may be x, dsum or (of its type) dy itself */
+    float* dweight;              /* [cols] fp32, or NULL */
+    int64_t x_stride, dy_stride, dsum_stride, dx_stride;
+} moe_rms_norm_grad_t;
+
+/* Gradient of moe_rms_norm's y with respect to the sum and the weight, with u = s (mean s^2 + eps)^(-1/2):
+ *   dx = (w dy - u mean(w dy u)) (mean s^2 + eps)^(-1/2) + dsum,  dweight = sum over rows of dy u
+ * in fp32, dx rounded once; the order of the sums is fixed by the shape.  ws_dev (256-byte aligned, of
+ * moe_rms_norm_workspace_size; 0: unsupported cols) holds nothing from one call to the next and needs no
+ * set-up; NULL without dweight.  Calls that share it must not overlap. */
+size_t moe_rms_norm_workspace_size(int32_t cols);
+moe_status_t moe_rms_norm_backward(const moe_rms_norm_grad_t* a, void* ws_dev, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -288,6 +288,11 @@ struct AppendArgs {
     int* status;
     int q_head, k_head, v_head, q_out_head, cache_head;   // head strides (the cache's in bytes)
     int parts;                   // warps per token (set by the launcher)
+    // positions of rotation apart from the place in the sequence (rotary NULL: pos turns every pair)
+    const int32_t* rotary;       // [n_axes, T], axes axis_stride apart
+    const uint8_t* axis;         // [rot_dim / 2] the axis of each pair, or NULL: 0
+    long long axis_stride;
+    int n_axes;
 };
 cudaError_t launch_kv_append(AppendArgs a, int head_dim, bool e4m3, cudaStream_t s);
 
@@ -315,6 +320,31 @@ constexpr size_t kAttentionCtrlBytes = 8192;
 size_t paged_attention_ws_bytes(int head_dim);   // 0: unsupported head_dim
 cudaError_t launch_paged_attention(const AttentionArgs& a, int head_dim, bool e4m3, cudaStream_t s);
 
+// Attention of drafted tokens over the paged cache (tree_attention.cu).  Strides of the cache count bytes.
+struct TreeArgs {
+    int B, T, n_heads, n_kv_heads, max_pages, window, n_pages, page_size;
+    float scale;
+    const int32_t *row_start, *seq_len;
+    const uint64_t* mask;        // or NULL
+    const int32_t* page_table;
+    long long table_stride;
+    const __nv_bfloat16* q;
+    __nv_bfloat16* out;
+    float* lse;                  // or NULL
+    long long q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+    const char *k, *v;
+    const uint8_t *k_exp, *v_exp;   // e4m3 cache only
+    long long page_bytes, token_bytes, head_bytes;
+    long long exp_page_stride, exp_token_stride, exp_head_stride;
+    void* ws;
+    int* status;
+    uint32_t page_mul;           // key / page_size = key * page_mul >> page_shift (set by the launcher)
+    int page_shift;
+};
+constexpr size_t kTreeCtrlBytes = 256;
+size_t tree_attention_ws_bytes(int head_dim);   // 0: unsupported head_dim
+cudaError_t launch_tree_attention(const TreeArgs& a, int head_dim, bool e4m3, cudaStream_t s);
+
 // Log probabilities read off logits (logprobs.cu).
 struct LogprobArgs {
     long long rows;
@@ -329,6 +359,8 @@ struct LogprobArgs {
     float* top_logprobs;
     int* status;
     int split;               // blocks per row (set by the launcher)
+    // or NULL; else gets each row's maximum and sum of e^(x - maximum), and top_logprobs the values x themselves
+    float2* stats;
 };
 cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t s);
 struct LogprobGradArgs {
@@ -345,6 +377,72 @@ struct LogprobGradArgs {
     int runs;                // blocks per row (set by the launcher)
 };
 cudaError_t launch_token_logprobs_backward(const LogprobGradArgs& a, cudaStream_t s);
+
+// A step of beam search (beam.cu).
+struct BeamArgs {
+    int seqs, beams, vocab, n;
+    bool bf16;
+    const void* logits;
+    long long row_stride;
+    const float* scores;     // [seqs, beams]
+    float* out_scores;       // [seqs, n]
+    int32_t *parents, *tokens;
+    float2* stats;           // workspace: [seqs * beams], and the beams' n largest
+    int32_t* top_ids;
+    float* top_x;
+    int* status;
+};
+constexpr size_t kBeamCtrlBytes = 256;
+struct BeamWorkspace {
+    size_t stats, ids, x;
+};
+size_t beam_ws_bytes(long long rows, int n, BeamWorkspace* at);   // 0: unsupported
+cudaError_t launch_beam_select(const BeamArgs& a, cudaStream_t s);
+struct BeamMoveArgs {
+    int seqs, beams, max_pages, n_pages, page_size, n_kv_heads, row_bytes;
+    const int32_t* parents;
+    long long parent_stride;
+    const int32_t* seq_len;
+    const int32_t* table;
+    long long table_stride;
+    int32_t* table_out;
+    long long table_out_stride;
+    void *k, *v;
+    uint8_t *k_exp, *v_exp;  // or NULL
+    long long page_bytes, token_bytes, head_bytes;
+    long long exp_page_stride, exp_token_stride, exp_head_stride;
+    int* status;
+};
+cudaError_t launch_beam_reorder(const BeamMoveArgs& a, cudaStream_t s);
+
+// The root-mean-square norm of rows and its gradient (norm.cu).  Strides count elements.
+constexpr int kMaxNormCols = 16384;
+struct NormArgs {
+    long long rows;
+    int cols;
+    bool bf16, weight_f32;
+    float eps, inv_cols;          // inv_cols: set by the launcher
+    const void *x, *residual, *weight;   // residual, weight: or NULL
+    void *sum, *y;                // or NULL
+    uint8_t* codes;               // or NULL
+    float* scales;
+    long long x_stride, residual_stride, sum_stride, y_stride, codes_stride;
+    int* status;
+};
+cudaError_t launch_rms_norm(NormArgs a, cudaStream_t s);
+struct NormGradArgs {
+    long long rows;
+    int cols;
+    bool bf16, dy_f32, weight_f32;
+    float eps, inv_cols;
+    const void *x, *weight, *dy, *dsum;   // weight, dsum: or NULL
+    void* dx;
+    float* dweight;               // or NULL
+    float* parts;                 // the blocks' sums of dweight
+    long long x_stride, dy_stride, dsum_stride, dx_stride;
+};
+size_t rms_norm_ws_bytes(int cols);   // 0: unsupported
+cudaError_t launch_rms_norm_backward(NormGradArgs a, cudaStream_t s);
 
 cudaError_t launch_timeout_probe(int* status, long long budget, cudaStream_t s);
 

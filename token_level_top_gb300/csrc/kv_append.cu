@@ -89,7 +89,7 @@ __device__ __forceinline__ float row_max(const Piece& x0, const Piece& x1)
     return m;
 }
 
-template <int D, bool kE4m3, bool kInterleaved>
+template <int D, bool kE4m3, bool kInterleaved, bool kAxes>
 __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) kv_append_kernel(const AppendArgs a)
 {
     constexpr int kLanes = D / 16;          // lanes per row
@@ -145,7 +145,13 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) kv_append_kernel(con
         }
         for (int i = lane; i < a.rot_dim / 2; i += 32) {
             float x, y;
-            cos_sin_turn(a.phase[i] * static_cast<uint64_t>(static_cast<uint32_t>(pos)), x, y);
+            int at_axis = pos;
+            if (kAxes) {   // a product modulo 2^64 takes negative positions as well
+                const int ax = a.axis ? a.axis[i] : 0;
+                at_axis = ax < a.n_axes ? a.rotary[ax * a.axis_stride + t] : 0;
+                if (ax >= a.n_axes) record_error(a.status, MOE_ERR_INDEX);
+            }
+            cos_sin_turn(a.phase[i] * static_cast<uint64_t>(static_cast<int64_t>(at_axis)), x, y);
             cs[i] = make_float2(x, y);
         }
         if (place < 0 && lane == 0) record_error(a.status, MOE_ERR_INDEX);
@@ -231,14 +237,14 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) kv_append_kernel(con
     }
 }
 
-template <int D>
+template <int D, bool kAxes>
 cudaError_t launch_d(const AppendArgs& a, bool e4m3, cudaStream_t s)
 {
     const long long warps = static_cast<long long>(a.T) * a.parts;
     const unsigned grid = static_cast<unsigned>((warps + kWarps - 1) / kWarps);
     constexpr int kSmem = kWarps * (kDepth * 1024 + D / 2 * 8);
-    const auto kernel = e4m3 ? (a.interleaved ? kv_append_kernel<D, true, true> : kv_append_kernel<D, true, false>)
-                             : (a.interleaved ? kv_append_kernel<D, false, true> : kv_append_kernel<D, false, false>);
+    const auto kernel = e4m3 ? (a.interleaved ? kv_append_kernel<D, true, true, kAxes> : kv_append_kernel<D, true, false, kAxes>)
+                             : (a.interleaved ? kv_append_kernel<D, false, true, kAxes> : kv_append_kernel<D, false, false, kAxes>);
     static_assert(kSmem <= 48 * 1024, "within the limit that needs no asking");
     kernel<<<grid, 32 * kWarps, kSmem, s>>>(a);
     return cudaGetLastError();
@@ -256,9 +262,9 @@ cudaError_t launch_kv_append(AppendArgs a, int head_dim, bool e4m3, cudaStream_t
     const int want = static_cast<int>((24LL * num_sms() + a.T - 1) / a.T);
     a.parts = want < 1 ? 1 : (want > groups ? groups : want);
     switch (head_dim) {
-        case 64: return launch_d<64>(a, e4m3, s);
-        case 128: return launch_d<128>(a, e4m3, s);
-        default: return launch_d<256>(a, e4m3, s);
+        case 64: return a.rotary ? launch_d<64, true>(a, e4m3, s) : launch_d<64, false>(a, e4m3, s);
+        case 128: return a.rotary ? launch_d<128, true>(a, e4m3, s) : launch_d<128, false>(a, e4m3, s);
+        default: return a.rotary ? launch_d<256, true>(a, e4m3, s) : launch_d<256, false>(a, e4m3, s);
     }
 }
 

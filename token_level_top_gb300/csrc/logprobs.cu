@@ -617,11 +617,18 @@ struct Result {
         : none(s.m == -INFINITY && s.l == 0.0f), ref(s.m == -INFINITY ? 0.0f : s.m), log_l(fmaf(-Stats::off(s.m), kLn2, logf(s.l)))
     {
     }
+    // 2^-off, to a rounding or two
+    static __device__ __forceinline__ float unturned(float off)
+    {
+        const float y = off * kLn2;
+        return fabsf(y) < 1e-3f ? fmaf(y, fmaf(y, 0.5f, -1.0f), 1.0f) : exp2f(-off);
+    }
     __device__ __forceinline__ float logprob(float x) const { return none ? -INFINITY : x - ref - log_l; }
     // by one thread
     __device__ __forceinline__ void write(const LogprobArgs& a, long long r, const Stats& s, int token, float given) const
     {
         if (s.l != s.l) record_error(a.status, MOE_ERR_NONFINITE);
+        if (a.stats) a.stats[r] = make_float2(ref, s.l * unturned(Stats::off(s.m)));
         if (a.lse) a.lse[r] = ref + log_l;
         if (a.entropy) a.entropy[r] = none ? 0.0f : logf(s.l) - s.w / s.l * kLn2;   // (the same off(m) in both)
         if (a.logprob) a.logprob[r] = token < 0 ? 0.0f : logprob(given);
@@ -629,7 +636,7 @@ struct Result {
     __device__ __forceinline__ void write_top(const LogprobArgs& a, long long r, int at, uint64_t key) const
     {
         a.top_ids[r * a.n_top + at] = key ? static_cast<int>(~static_cast<uint32_t>(key)) : -1;
-        a.top_logprobs[r * a.n_top + at] = key ? logprob(value_of(static_cast<uint32_t>(key >> 32))) : -INFINITY;
+        a.top_logprobs[r * a.n_top + at] = !key ? -INFINITY : (a.stats ? value_of(static_cast<uint32_t>(key >> 32)) : logprob(value_of(static_cast<uint32_t>(key >> 32))));
     }
 };
 

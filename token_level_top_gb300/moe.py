@@ -70,6 +70,40 @@ class MoEAttention(ctypes.Structure):
                     (n + s, ctypes.c_int64) for n in ("q", "out") for s in ("_token_stride", "_head_stride")]
 
 
+class MoERotation(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int32), ("rotary", ctypes.c_void_p), ("axis_stride", ctypes.c_int64),
+                ("axis", ctypes.c_void_p)]
+
+
+class MoETreeAttention(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("row_start", ctypes.c_void_p),
+                ("seq_len", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("q", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p)] + [(n + s, ctypes.c_int64) for n in ("q", "out") for s in ("_token_stride", "_head_stride")]
+
+
+class MoEBeamReorder(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int32), ("beams", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("parents", ctypes.c_void_p), ("parent_stride", ctypes.c_int64), ("seq_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("page_table_out", ctypes.c_void_p),
+                ("table_out_stride", ctypes.c_int64)]
+
+
+class MoERmsNorm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int32), ("type", ctypes.c_uint32),
+                ("weight_type", ctypes.c_uint32), ("eps", ctypes.c_float)] + [
+                    (n, ctypes.c_void_p) for n in ("x", "residual", "weight", "sum", "y", "codes", "scales")] + [
+                    (n + "_stride", ctypes.c_int64) for n in ("x", "residual", "sum", "y", "codes")]
+
+
+class MoERmsNormGrad(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int32), ("type", ctypes.c_uint32), ("dy_type", ctypes.c_uint32),
+                ("weight_type", ctypes.c_uint32), ("eps", ctypes.c_float)] + [
+                    (n, ctypes.c_void_p) for n in ("x", "weight", "dy", "dsum", "dx", "dweight")] + [
+                    (n + "_stride", ctypes.c_int64) for n in ("x", "dy", "dsum", "dx")]
+
+
 @dataclass
 class Config:
     T: int
@@ -163,6 +197,17 @@ _SIGS = {
     "moe_paged_attention": (I32, [P, P, P, SZ, P]),
     "moe_token_logprobs": (I32, [I64, I32, ctypes.c_uint32, P, I64, P, I32] + [P] * 7),
     "moe_token_logprobs_backward": (I32, [I64, I32, ctypes.c_uint32, P, I64] + [P] * 6 + [I64, P, P]),
+    "moe_kv_append_axes": (I32, [P, P, P, P, P]),
+    "moe_tree_attention_workspace_size": (SZ, [I32]),
+    "moe_tree_attention_workspace_init": (I32, [P, SZ, P]),
+    "moe_tree_attention": (I32, [P, P, P, SZ, P]),
+    "moe_beam_workspace_size": (SZ, [I64, I32]),
+    "moe_beam_workspace_init": (I32, [P, SZ, P]),
+    "moe_beam_select": (I32, [I32, I32, I32, ctypes.c_uint32, P, I64, P, I32, P, P, P, P, SZ, P]),
+    "moe_beam_reorder": (I32, [P, P, P, P]),
+    "moe_rms_norm": (I32, [P, P, P]),
+    "moe_rms_norm_workspace_size": (SZ, [I32]),
+    "moe_rms_norm_backward": (I32, [P, P, SZ, P]),
 }
 
 
@@ -498,10 +543,15 @@ LOGITS = {torch.float32: 0, torch.bfloat16: 1}   # MOE_LOGITS_*
 ROTATE_INTERLEAVED = 1             # MOE_ROTATE_INTERLEAVED
 
 
-# A call's structure is packed in one go (the fields of MoEAppend and MoEAttention in their order, padded as C pads
+# A call's structure is packed in one go (the fields of its ctypes structure above in their order, padded as C pads
 # them): filling a ctypes structure field by field costs as much as the launch.
 _APPEND = struct.Struct("=5iI3Qq5Q8q")
 _ATTENTION = struct.Struct("=4if4x2Qq3Q4q")
+_ROTATION = struct.Struct("=i4xQqQ")
+_TREE = struct.Struct("=5if4Qq3Q4q")
+_REORDER = struct.Struct("=3i4xQqQQqQq")
+_NORM = struct.Struct("=qi2If7Q5q")
+_NORM_GRAD = struct.Struct("=qi3If4x6Q4q")
 
 
 def _device(t: torch.Tensor, name: str) -> int:
@@ -599,12 +649,14 @@ def rope_phase(inv_freq) -> torch.Tensor:
 
 
 def kv_append(cache: KVCache, k, v, pos, page_table, q=None, phase=None, seq=None, interleaved=False, q_out=None,
-              status=None):
+              status=None, rotary=None, axis=None):
     """Rotates q and k by their positions and writes k, v into the cache (moe_kv_append).  k, v [T, n_kv_heads,
     head_dim] and q [T, n_heads, head_dim] bf16 (views of one projection's output are fine); pos [T], seq [T]
     (None: token t belongs to row t of page_table [n_seqs, max_pages]) int32; phase from rope_phase on the device
     (None: no rotation).  Returns the rotated q (q_out when given, which may be q), or None without q.  status: a
-    status_word or workspace that records indices out of range."""
+    status_word or workspace that records indices out of range.
+    rotary [axes, T] int32 (moe_kv_append_axes; None: pos): positions of rotation that are not the place in the cache,
+    up to four axes, and axis [dims / 2] uint8 the axis of each rotated pair (None: the first)."""
     dev = _device(k, "k")
     ks, vs, ts = k.stride(), v.stride(), page_table.stride()
     for t, strides, name in ((k, ks, "k"), (v, vs, "v")):
@@ -648,8 +700,19 @@ def kv_append(cache: KVCache, k, v, pos, page_table, q=None, phase=None, seq=Non
     a = _APPEND.pack(T, n_seqs, max_pages, heads, rot, ROTATE_INTERLEAVED if interleaved else 0, _rows(pos, "pos", T, dev),
                      0 if seq is None else _rows(seq, "seq", T, dev), page_table.data_ptr(), ts[0] if n_seqs > 1 else 0, pp, qp,
                      k.data_ptr(), v.data_ptr(), op, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1])
-    st = (_lib or lib()).moe_kv_append(cache.ref, a, None if status is None else _memory(status, "status", dev),
-                                       torch._C._cuda_getCurrentRawStream(dev))
+    word, stream = None if status is None else _memory(status, "status", dev), torch._C._cuda_getCurrentRawStream(dev)
+    if rotary is None:
+        if axis is not None:
+            raise ValueError("axis: it says which row of rotary turns a pair, and there is no rotary")
+        st = (_lib or lib()).moe_kv_append(cache.ref, a, word, stream)
+    else:
+        _want(rotary, "rotary", torch.int32, 2, dev)
+        axes = rotary.shape[0]
+        if rotary.shape[1] != T or phase is None:
+            raise ValueError(f"rotary: want [axes, {T}] and a phase to turn by, got {tuple(rotary.shape)}, phase {phase}")
+        r = _ROTATION.pack(axes, rotary.data_ptr(), rotary.stride(0) if axes > 1 else 0,
+                           0 if axis is None else _rows(axis, "axis", rot // 2, dev, torch.uint8))
+        st = (_lib or lib()).moe_kv_append_axes(cache.ref, a, r, word, stream)
     if st:
         raise MoEError(st, "moe_kv_append")
     return q_out if q is not None else None
@@ -765,3 +828,218 @@ def token_logprobs_backward(logits, token, lse, entropy=None, dlogprob=None, den
     if st:
         raise MoEError(st, "moe_token_logprobs_backward")
     return out
+
+
+# ------------------------------------------------------------ several continuations of a sequence
+
+def tree_attention_workspace(head_dim: int, device="cuda") -> torch.Tensor:
+    """A workspace for tree_attention at this head_dim (any batch), initialised."""
+    n = int(lib().moe_tree_attention_workspace_size(head_dim))
+    if n == 0:
+        raise MoEError(2, "moe_tree_attention_workspace_size")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    _device(ws, "device")
+    _check(lib().moe_tree_attention_workspace_init(_p(ws), n, _stream()), "moe_tree_attention_workspace_init")
+    return ws
+
+
+def tree_attention(cache: KVCache, ws, q, row_start, seq_len, page_table, mask=None, scale=None, window=0, out=None,
+                   return_lse=False):
+    """Attention of the drafted tokens of every sequence, up to 64 each, over the cache that holds them behind the
+    sequence's context (moe_tree_attention): q [T, n_heads, head_dim] bf16, sequence b's rows from row_start[b] to
+    row_start[b + 1] (row_start [B + 1] int32), seq_len [B] int32 (the drafted tokens included), page_table [B, max_pages]
+    int32; mask [T] int64: bit j says that the row sees drafted token j of its sequence (None: those up to itself).
+    scale, window as in paged_attention.  Returns out [T, n_heads, head_dim] bf16, and lse [T, n_heads] fp32 with
+    return_lse; rows of no sequence are left as they were (in a new out: not set)."""
+    dev = _device(q, "q")
+    _want(q, "q", torch.bfloat16, 3, dev)
+    _want(page_table, "page_table", torch.int32, 2, dev)
+    if cache.device != dev:
+        raise ValueError(f"cache: want one of CUDA device {dev}, got one of {cache.device}")
+    T, heads, dim = q.shape
+    B, max_pages = page_table.shape
+    if dim != cache.head_dim:
+        raise ValueError(f"q: want [T, n_heads, {cache.head_dim}], got {tuple(q.shape)}")
+    if not 0 <= window < 2 ** 31:
+        raise ValueError(f"window: want 0 .. 2^31 - 1, got {window}")
+    if out is None:
+        out = torch.empty(T, heads, dim, dtype=torch.bfloat16, device=q.device)
+    else:
+        _want(out, "out", torch.bfloat16, 3, dev)
+        if out.shape != q.shape:
+            raise ValueError(f"out: want {tuple(q.shape)}, got {tuple(out.shape)}")
+    lse = torch.empty(T, heads, dtype=torch.float32, device=q.device) if return_lse else None
+    qs, os_ = _strides(q), _strides(out)
+    a = _TREE.pack(B, T, heads, max_pages, window, dim ** -0.5 if scale is None else scale,
+                   _rows(row_start, "row_start", B + 1, dev), _rows(seq_len, "seq_len", B, dev),
+                   0 if mask is None else _rows(mask, "mask", T, dev, torch.int64), page_table.data_ptr(),
+                   page_table.stride(0) if B > 1 else 0, q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else 0,
+                   qs[0], qs[1], os_[0], os_[1])
+    st = (_lib or lib()).moe_tree_attention(cache.ref, a, _memory(ws, "ws", dev), ws.nbytes,
+                                            torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        raise MoEError(st, "moe_tree_attention")
+    return (out, lse) if return_lse else out
+
+
+def beam_workspace(rows: int, n: int, device="cuda") -> torch.Tensor:
+    """A workspace for beam_select with up to this many rows of logits and n candidates, initialised."""
+    size = int(lib().moe_beam_workspace_size(rows, n))
+    if size == 0:
+        raise MoEError(2, "moe_beam_workspace_size")
+    ws = torch.empty(size, dtype=torch.uint8, device=device)
+    _device(ws, "device")
+    _check(lib().moe_beam_workspace_init(_p(ws), size, _stream()), "moe_beam_workspace_init")
+    return ws
+
+
+def beam_select(ws, logits, scores, n: int):
+    """The n best continuations of each sequence over its beams and the vocabulary (moe_beam_select): logits
+    [seqs * beams, vocab] fp32 or bf16, scores [seqs, beams] fp32 (-inf: no live beam).  Returns dict(scores, parents,
+    tokens), each [seqs, n], in order; past the last candidate -inf, -1, -1."""
+    kind = LOGITS.get(logits.dtype)
+    if kind is None:
+        raise ValueError(f"logits: want float32 or bfloat16, got {logits.dtype}")
+    dev = _device(logits, "logits")
+    _want(logits, "logits", logits.dtype, 2, dev)
+    _want(scores, "scores", torch.float32, 2, dev)
+    seqs, beams = scores.shape
+    rows, vocab = logits.shape
+    if rows != seqs * beams or not scores.is_contiguous():
+        raise ValueError(f"logits, scores: want [seqs * beams, vocab] and contiguous [seqs, beams], got {tuple(logits.shape)}, "
+                         f"{tuple(scores.shape)}, strides {scores.stride()}")
+    size = (seqs, max(n, 0))
+    out = dict(scores=torch.empty(size, dtype=torch.float32, device=logits.device),
+               parents=torch.empty(size, dtype=torch.int32, device=logits.device),
+               tokens=torch.empty(size, dtype=torch.int32, device=logits.device))
+    st = (_lib or lib()).moe_beam_select(seqs, beams, vocab, kind, logits.data_ptr(), logits.stride(0) if rows > 1 else 0,
+                                         scores.data_ptr(), n, out["scores"].data_ptr(), out["parents"].data_ptr(),
+                                         out["tokens"].data_ptr(), _memory(ws, "ws", dev), ws.nbytes,
+                                         torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        raise MoEError(st, "moe_beam_select")
+    return out
+
+
+def beam_reorder(cache: KVCache, parents, seq_len, page_table, out=None, status=None):
+    """Gives every beam its parent's cached tokens (moe_beam_reorder): parents [seqs, beams] int32 (a view of
+    beam_select's is fine), seq_len [seqs] int32, page_table [seqs * beams, max_pages] int32.  Full pages are shared, a page
+    that is still filling stays each beam's own (rows of the cache are copied where two beams go on from one).  Returns the
+    new page table (out when given; not page_table itself)."""
+    dev = _device(parents, "parents")
+    _want(parents, "parents", torch.int32, 2, dev)
+    _want(page_table, "page_table", torch.int32, 2, dev)
+    if cache.device != dev:
+        raise ValueError(f"cache: want one of CUDA device {dev}, got one of {cache.device}")
+    seqs, beams = parents.shape
+    rows, max_pages = page_table.shape
+    if rows != seqs * beams:
+        raise ValueError(f"parents, page_table: want [seqs, beams] and [seqs * beams, max_pages], got {tuple(parents.shape)}, "
+                         f"{tuple(page_table.shape)}")
+    if out is None:
+        out = torch.empty(rows, max_pages, dtype=torch.int32, device=page_table.device)
+    else:
+        _want(out, "out", torch.int32, 2, dev)
+        if out.shape != page_table.shape:
+            raise ValueError(f"out: want {tuple(page_table.shape)}, got {tuple(out.shape)}")
+    a = _REORDER.pack(seqs, beams, max_pages, parents.data_ptr(), parents.stride(0) if seqs > 1 else 0,
+                      _rows(seq_len, "seq_len", seqs, dev), page_table.data_ptr(), page_table.stride(0) if rows > 1 else 0,
+                      out.data_ptr(), out.stride(0) if rows > 1 else 0)
+    st = (_lib or lib()).moe_beam_reorder(cache.ref, a, None if status is None else _memory(status, "status", dev),
+                                          torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        raise MoEError(st, "moe_beam_reorder")
+    return out
+
+
+# ------------------------------------------------------------ the norm before attention and experts
+
+def _norm_rows(t, name, like, dev, dtype=None):
+    """The address and row stride of a matrix of `like`'s shape (and type, unless given)."""
+    _want(t, name, dtype or like.dtype, 2, dev)
+    if t.shape != like.shape:
+        raise ValueError(f"{name}: want {tuple(like.shape)}, got {tuple(t.shape)}")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _norm_weight(weight, cols, dev):
+    """The address and type of the weights."""
+    if weight is None:
+        return 0, 0
+    if weight.dtype not in LOGITS:
+        raise ValueError(f"weight: want float32 or bfloat16, got {weight.dtype}")
+    return _rows(weight, "weight", cols, dev, weight.dtype), LOGITS[weight.dtype]
+
+
+def rms_norm(x, weight=None, residual=None, eps=1e-6, y=True, e4m3=False, out=None, sum_out=None, status=None):
+    """The root-mean-square norm of rows x (+ residual) [rows, cols] fp32 or bf16 (moe_rms_norm), times weight [cols] fp32 or
+    bf16.  Returns a dict: sum (with a residual: x + residual in the rows' type), y (unless y is False) of the rows' type,
+    and with e4m3 codes (uint8) and scales [rows] fp32 as quantize_fp8 has them.  out, sum_out: where y and sum go; either may
+    be x or residual.  status: a status_word or workspace that records NaN and infinities."""
+    kind = LOGITS.get(x.dtype)
+    if kind is None:
+        raise ValueError(f"x: want float32 or bfloat16, got {x.dtype}")
+    dev = _device(x, "x")
+    _want(x, "x", x.dtype, 2, dev)
+    rows, cols = x.shape
+    xs = x.stride(0) if rows > 1 else 0
+    wp, wk = _norm_weight(weight, cols, dev)
+    got = {}
+    rp = rs = sp = ss = yp = ys = cp = cs = scp = 0
+    if residual is not None:
+        rp, rs = _norm_rows(residual, "residual", x, dev)
+        got["sum"] = sum_out = torch.empty(rows, cols, dtype=x.dtype, device=x.device) if sum_out is None else sum_out
+        sp, ss = _norm_rows(sum_out, "sum_out", x, dev)
+    elif sum_out is not None:
+        raise ValueError("sum_out: there is no residual")
+    if y:
+        got["y"] = out = torch.empty(rows, cols, dtype=x.dtype, device=x.device) if out is None else out
+        yp, ys = _norm_rows(out, "out", x, dev)
+    elif out is not None:
+        raise ValueError("out: y is not asked for")
+    if e4m3:
+        got["codes"] = torch.empty(rows, cols, dtype=torch.uint8, device=x.device)
+        got["scales"] = torch.empty(rows, dtype=torch.float32, device=x.device)
+        cp, cs, scp = got["codes"].data_ptr(), cols, got["scales"].data_ptr()
+    a = _NORM.pack(rows, cols, kind, wk, eps, x.data_ptr(), rp, wp, sp, yp, cp, scp, xs, rs, ss, ys, cs)
+    st = (_lib or lib()).moe_rms_norm(a, None if status is None else _memory(status, "status", dev),
+                                      torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        raise MoEError(st, "moe_rms_norm")
+    return got
+
+
+def norm_workspace(cols: int, device="cuda") -> torch.Tensor:
+    """A workspace for rms_norm_backward of rows of this many values (any number of rows)."""
+    n = int(lib().moe_rms_norm_workspace_size(cols))
+    if n == 0:
+        raise MoEError(2, "moe_rms_norm_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def rms_norm_backward(ws, x, weight, dy, dsum=None, eps=1e-6, out=None, weight_grad=True):
+    """Gradient of rms_norm's y (moe_rms_norm_backward): x what was normalised (the sum, with a residual), dy [rows, cols] fp32
+    or of x's type, dsum of x's type: what reaches the sum from elsewhere.  Returns dx of x's type (out when given, which may
+    be x, dsum or, of x's type, dy) and dweight [cols] fp32 (None, and ws may be None, without weight_grad)."""
+    kind = LOGITS.get(x.dtype)
+    if kind is None or dy.dtype not in LOGITS:
+        raise ValueError(f"x, dy: want float32 or bfloat16, got {x.dtype}, {dy.dtype}")
+    dev = _device(x, "x")
+    _want(x, "x", x.dtype, 2, dev)
+    rows, cols = x.shape
+    xs = x.stride(0) if rows > 1 else 0
+    wp, wk = _norm_weight(weight, cols, dev)
+    gp, gs = _norm_rows(dy, "dy", x, dev, dy.dtype)
+    dp, ds = _norm_rows(dsum, "dsum", x, dev) if dsum is not None else (0, 0)
+    out = torch.empty(rows, cols, dtype=x.dtype, device=x.device) if out is None else out
+    op, os_ = _norm_rows(out, "out", x, dev)
+    dweight, wsp, wsn = None, None, 0
+    if weight_grad:
+        dweight = torch.empty(cols, dtype=torch.float32, device=x.device)
+        wsp, wsn = _memory(ws, "ws", dev), ws.nbytes
+    a = _NORM_GRAD.pack(rows, cols, kind, LOGITS[dy.dtype], wk, eps, x.data_ptr(), wp, gp, dp, op,
+                        dweight.data_ptr() if weight_grad else 0, xs, gs, ds, os_)
+    st = (_lib or lib()).moe_rms_norm_backward(a, wsp, wsn, torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        raise MoEError(st, "moe_rms_norm_backward")
+    return out, dweight
