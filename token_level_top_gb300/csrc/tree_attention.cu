@@ -43,8 +43,8 @@ constexpr float kSlack = 8.0f;
 constexpr float kNone = -3.402823466e38f;   // a maximum of nothing: finite, so that differences of two are
 constexpr int kRowsTile = 128, kKeys = 64;
 constexpr int kPanel = kKeys * 128;         // bytes of 64 values of a tile's 64 rows
-constexpr int kSoftmaxWarps = 4, kCopyWarps = 4, kCopyThreads = 32 * kCopyWarps;
-constexpr int kThreads = 32 * (kSoftmaxWarps + kCopyWarps + 1);
+// Eight warps, so that two blocks an SM leave a thread 128 registers.
+constexpr int kSoftmaxWarps = 4, kCopyWarps = 3, kProductWarp = kSoftmaxWarps + kCopyWarps, kThreads = 32 * (kProductWarp + 1);
 constexpr int kGap = 2;                     // places of the list that an item's start and end are worth
 constexpr int kMaxSms = 152;
 
@@ -84,16 +84,54 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// D[tmem] (+)= A[tmem] * B[smem]: one instruction of K = 16, A 8 columns of bf16 pairs.
-__device__ __forceinline__ void mma_bf16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A condition that all lanes of the (converged) warp agree on, in a form that the compiler knows as such.
+__device__ __forceinline__ bool uniform(bool x) { return __any_sync(0xffffffffu, x); }
+
+// The warp that issues the products runs as one, and its elected lane issues them under a predicate: in a branch of one
+// lane every operand's way into the uniform registers costs some 100 cycles (TAG).
+__device__ __forceinline__ uint32_t elected()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+// D[tmem] (+)= A[smem] * B[smem]^T, one instruction of K = 16.
+__device__ __forceinline__ void mma_if(uint32_t leader, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+// The same with A in TMEM: 8 columns of bf16 pairs.
+__device__ __forceinline__ void mma_tmem_a_if(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t leader, uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar), "r"(leader)
         : "memory");
 }
 
@@ -233,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
     volatile int* const s_odd = reinterpret_cast<volatile int*>(s_tmem + 1);   // NaN or infinities were taken from value rows
     auto bar = [&](int i) { return smem_u32(bars + i); };
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // (the same in all lanes)
     const int group = a.n_heads / a.n_kv_heads;
 
     // ---- the batch's places, and where this block's run begins
@@ -300,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(bar(kFull + i), kCopyThreads);
+            mbar_init(bar(kFull + i), 32);
             mbar_init(bar(kEmpty + i), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -309,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
         }
         mbar_init(bar(kODone), 1);
         mbar_init(bar(kOFree), kSoftmaxWarps);
-        mbar_init(bar(kQFull), kCopyThreads);
+        mbar_init(bar(kQFull), 32 * kCopyWarps);
         mbar_init(bar(kQEmpty), 1);
         mbar_init(bar(kItemDone), 1);
         mbar_fence_init();
@@ -317,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
     }
     __syncthreads();
     if (s_start->item.n == 0 || s_start->item.off + s_start->g >= hi) return;   // nothing but gaps
-    if (warp == kSoftmaxWarps + kCopyWarps) {
+    if (warp == kProductWarp) {
         tmem_alloc(smem_u32(const_cast<uint32_t*>(s_tmem)), S::kCols);
         tmem_relinquish();
     }
@@ -331,9 +369,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
     bool ok = true;
     int seg = 0, tiles = 0;       // segments and tiles done
 
-    if (warp >= kSoftmaxWarps && warp < kSoftmaxWarps + kCopyWarps) {
+    if (warp >= kSoftmaxWarps && warp < kProductWarp) {
         // ------------------------------------------------------------ copies
-        const int p = threadIdx.x - 32 * kSoftmaxWarps;
+        // A warp takes every third slot's tile as a whole.
+        const int mine_of = warp - kSoftmaxWarps;
         auto page_of = [&](int key) {
             return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(key)) * a.page_mul) >> a.page_shift);
         };
@@ -341,52 +380,55 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
             const int g1 = static_cast<int>(min(static_cast<long long>(it.n), hi - it.off));
             const int mtiles = it.items / a.n_kv_heads, hk = it.h / mtiles, row_at = (it.h - hk * mtiles) * kRowsTile;
             const int32_t* const table = a.page_table + it.b * a.table_stride;
-            // pages of this lane's keys of the next tile
+            // this warp's slots n of the segment: from n0 on, every third
+            const int n_end = 2 * (tiles + g1 - g0);
+            int n = 2 * tiles + (mine_of + 2 * kCopyWarps * 1024 - (2 * tiles) % kCopyWarps) % kCopyWarps;
+            // pages of this lane's two keys of slot n's tile
             int entry[2];
-            auto look_up = [&](int g) {
+            auto look_up = [&](int n) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int key = it.base + g * kKeys + 32 * h + lane;
-                    entry[h] = g < g1 && key < it.len ? __ldg(table + page_of(key)) : -1;
+                    const int key = it.base + (g0 + (n >> 1) - tiles) * kKeys + 32 * h + lane;
+                    entry[h] = n < n_end && key < it.len ? __ldg(table + page_of(key)) : -1;
                 }
             };
             // their places in the cache, and their exponents', or -1
             long long place[2], exp_place[2];
-            auto locate = [&](int g) {
+            auto locate = [&](int n) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int key = it.base + g * kKeys + 32 * h + lane;
+                    const int key = it.base + (g0 + (n >> 1) - tiles) * kKeys + 32 * h + lane;
                     const bool live = entry[h] >= 0 && entry[h] < a.n_pages;
                     const int at = key - page_of(key) * a.page_size;
                     place[h] = live ? entry[h] * a.page_bytes + at * a.token_bytes : -1;
                     if (kE4m3) exp_place[h] = live ? entry[h] * a.exp_page_stride + at * a.exp_token_stride : -1;
                 }
             };
-            look_up(g0);
-            // ---- the rows of q
+            look_up(n);
+            // ---- the rows of q, eight at a time
             if (seg > 0) ok = mbar_wait(bar(kQEmpty), (seg - 1) & 1, kSpinBudget);
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
             }
             {
-                constexpr int kPieces = D / 8, kStep = kCopyThreads / kPieces;   // 16-byte pieces of a row
-                const int piece = p % kPieces, r0 = p / kPieces;
+                constexpr int kPieces = D / 8;   // 16-byte pieces of a row
                 const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll 1
-                for (int r1 = 0; r1 < kRowsTile; r1 += 8 * kStep) {
-                    uint4 x[8];
+                for (int r1 = 8 * mine_of; r1 < kRowsTile; r1 += 8 * kCopyWarps) {
+                    uint4 x[kPieces / 4];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int row = row_at + r1 + i * kStep + r0, t = row / group;
+                    for (int i = 0; i < kPieces / 4; ++i) {
+                        const int r = r1 + (i * 32 + lane) / kPieces, piece = (i * 32 + lane) % kPieces;
+                        const int row = row_at + r, t = row / group;
                         x[i] = make_uint4(0, 0, 0, 0);
                         if (t < it.draft && a.scale != 0.0f)
                             x[i] = *reinterpret_cast<const uint4*>(a.q + (it.row0 + t) * a.q_token_stride +
                                                                    (hk * group + (row - t * group)) * a.q_head_stride + 8 * piece);
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = r1 + i * kStep + r0;
+                    for (int i = 0; i < kPieces / 4; ++i) {
+                        const int r = r1 + (i * 32 + lane) / kPieces, piece = (i * 32 + lane) % kPieces;
                         x[i].x ^= flip, x[i].y ^= flip, x[i].z ^= flip, x[i].w ^= flip;
                         sts128(smem_u32(s_q) + (piece >> 3) * (kRowsTile * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4), x[i]);
                     }
@@ -396,118 +438,106 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
             }
             // ---- the key and value tiles
             const int odd_from = a.window > 0 ? max(0, it.ctx - a.window + it.draft) : 0;   // below it, and from ctx on, rows differ
-            auto mixed = [&](int g) {
-                const int k0 = it.base + g * kKeys;
-                return k0 < odd_from || k0 + kKeys > it.ctx;
+            auto mixed = [&](int n) {   // values of a tile where rows differ
+                const int k0 = it.base + (g0 + (n >> 1) - tiles) * kKeys;
+                return (n & 1) != 0 && (k0 < odd_from || k0 + kKeys > it.ctx);
             };
-            auto slot_of = [&](int n) { return n % kSlots; };
             auto wait_empty = [&](int n) {
-                const bool got = mbar_wait(bar(kEmpty + slot_of(n)), ((n / kSlots) & 1) ^ 1, kSpinBudget);
+                const bool got = mbar_wait(bar(kEmpty + n % kSlots), ((n / kSlots) & 1) ^ 1, kSpinBudget);
                 return __all_sync(0xffffffffu, got) != 0;
             };
             if constexpr (!kE4m3) {
-                constexpr int kPieces = D / 8, kStep = kCopyThreads / kPieces;
-                const int piece = p % kPieces, r0 = p / kPieces;
-                const char* const from_k = a.k + hk * a.head_bytes + 16 * piece;
-                const char* const from_v = a.v + hk * a.head_bytes + 16 * piece;
-                const uint32_t to = smem_u32(s_ring) + (piece >> 3) * kPanel;
-                for (int g = g0; g < g1; ++g) {
-                    locate(g);
-                    look_up(g + 1);
-                    const int n = 2 * (tiles + g - g0);
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        if (!wait_empty(n + v)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t slot = to + slot_of(n + v) * S::kTile;
-#pragma unroll
-                        for (int i = 0; i < kKeys / kStep; ++i) {
-                            const int r = i * kStep + r0;
-                            const long long at = __shfl_sync(0xffffffffu, place[i * kStep / 32], r & 31);
-                            copy_async_or_zeros(slot + r * 128 + (((piece & 7) ^ (r & 7)) << 4), (v ? from_v : from_k) + (at < 0 ? 0 : at), at >= 0);
-                        }
-                        if (v == 1 && mixed(g)) {   // (these are looked at here, so they are waited for)
-                            copy_wait_all();
-                            uint32_t odd = 0;
-#pragma unroll
-                            for (int i = 0; i < kKeys / kStep; ++i) {
-                                const int r = i * kStep + r0;
-                                const uint32_t at = slot + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
-                                uint4 x = lds128(at);
-                                if (any_odd(x)) {
-                                    odd = 1;
-                                    x = make_uint4(without_odd(x.x), without_odd(x.y), without_odd(x.z), without_odd(x.w));
-                                    sts128(at, x);
-                                }
-                            }
-                            if (odd) *s_odd = 1;
-                            fence_proxy_async_shared();
-                            mbar_arrive(bar(kFull + slot_of(n + v)));
-                        } else {
-                            copy_arrive(bar(kFull + slot_of(n + v)));
-                        }
+                constexpr int kPieces = D / 8, kStep = 32 / kPieces > 0 ? 32 / kPieces : 1;   // rows an instruction copies
+                constexpr int kCount = kKeys * kPieces / 32;
+                const int piece = lane % kPieces, r0 = lane / kPieces;
+                for (; n < n_end; n += kCopyWarps) {
+                    locate(n);
+                    look_up(n + kCopyWarps);
+                    if (!wait_empty(n)) {
+                        ok = false;
+                        break;
                     }
-                    if (!ok) break;
-                }
-            } else {
-                constexpr int kPieces = D / 16, kStep = kCopyThreads / kPieces, kMine = kKeys / kStep;   // pieces of 16 codes
-                const int piece = p % kPieces, r0 = p / kPieces;
-                uint4 raw[2][kMine];
-                uint32_t exps[2][2];
-                auto fetch = [&](int v) {   // of the located tile
-                    const char* const from = (v ? a.v : a.k) + hk * a.head_bytes + 16 * piece;
-                    const uint8_t* const from_exp = (v ? a.v_exp : a.k_exp) + hk * a.exp_head_stride;
+                    const char* const from = (n & 1 ? a.v : a.k) + hk * a.head_bytes + 16 * piece;
+                    const uint32_t slot = smem_u32(s_ring) + (n % kSlots) * S::kTile + (piece >> 3) * kPanel;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) exps[v][h] = exp_place[h] >= 0 ? __ldg(from_exp + exp_place[h]) : 127u;
-#pragma unroll
-                    for (int i = 0; i < kMine; ++i) {
+                    for (int i = 0; i < kCount; ++i) {
                         const int r = i * kStep + r0;
                         const long long at = __shfl_sync(0xffffffffu, place[i * kStep / 32], r & 31);
-                        raw[v][i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(from + at)) : make_uint4(0, 0, 0, 0);
+                        copy_async_or_zeros(slot + r * 128 + (((piece & 7) ^ (r & 7)) << 4), from + (at < 0 ? 0 : at), at >= 0);
                     }
-                };
-                locate(g0);
-                look_up(g0 + 1);
-                fetch(0);
-                fetch(1);
-                for (int g = g0; g < g1; ++g) {
-                    locate(g + 1);
-                    look_up(g + 2);
-                    const int n = 2 * (tiles + g - g0);
-                    uint32_t odd = 0;
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        if (!wait_empty(n + v)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t slot = smem_u32(s_ring) + slot_of(n + v) * S::kTile + (piece >> 2) * kPanel;
-#pragma unroll
-                        for (int i = 0; i < kMine; ++i) {
+                    if (mixed(n)) {   // (these are looked at here, so they are waited for)
+                        copy_wait_all();
+                        uint32_t odd = 0;
+#pragma unroll 4
+                        for (int i = 0; i < kCount; ++i) {
                             const int r = i * kStep + r0;
-                            const float scale = pow2_of_byte(__shfl_sync(0xffffffffu, exps[v][i * kStep / 32], r & 31));
-                            uint4 x, y;
-                            bf16_of_codes(raw[v][i].x, scale, x.x, x.y);
-                            bf16_of_codes(raw[v][i].y, scale, x.z, x.w);
-                            bf16_of_codes(raw[v][i].z, scale, y.x, y.y);
-                            bf16_of_codes(raw[v][i].w, scale, y.z, y.w);
-                            if (v == 1 && mixed(g) && (any_odd(x) | any_odd(y))) {
+                            const uint32_t at = slot + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+                            uint4 x = lds128(at);
+                            if (any_odd(x)) {
                                 odd = 1;
                                 x = make_uint4(without_odd(x.x), without_odd(x.y), without_odd(x.z), without_odd(x.w));
-                                y = make_uint4(without_odd(y.x), without_odd(y.y), without_odd(y.z), without_odd(y.w));
+                                sts128(at, x);
                             }
-                            const int at = (2 * piece) & 7;
-                            sts128(slot + r * 128 + ((at ^ (r & 7)) << 4), x);
-                            sts128(slot + r * 128 + (((at + 1) ^ (r & 7)) << 4), y);
                         }
                         if (odd) *s_odd = 1;
                         fence_proxy_async_shared();
-                        mbar_arrive(bar(kFull + slot_of(n + v)));
-                        if (g + 1 < g1) fetch(v);
+                        mbar_arrive(bar(kFull + n % kSlots));
+                    } else {
+                        copy_arrive(bar(kFull + n % kSlots));
                     }
-                    if (!ok) break;
+                }
+            } else {
+                constexpr int kPieces = D / 16, kStep = 32 / kPieces, kCount = kKeys * kPieces / 32;   // pieces of 16 codes
+                const int piece = lane % kPieces, r0 = lane / kPieces;
+                uint4 raw[kCount];
+                uint32_t exps[2];
+                auto fetch = [&](int n) {   // of the located tile
+                    const char* const from = (n & 1 ? a.v : a.k) + hk * a.head_bytes + 16 * piece;
+                    const uint8_t* const from_exp = (n & 1 ? a.v_exp : a.k_exp) + hk * a.exp_head_stride;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) exps[h] = exp_place[h] >= 0 ? __ldg(from_exp + exp_place[h]) : 127u;
+#pragma unroll
+                    for (int i = 0; i < kCount; ++i) {
+                        const int r = i * kStep + r0;
+                        const long long at = __shfl_sync(0xffffffffu, place[i * kStep / 32], r & 31);
+                        raw[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(from + at)) : make_uint4(0, 0, 0, 0);
+                    }
+                };
+                locate(n);
+                look_up(n + kCopyWarps);
+                fetch(n);
+                for (; n < n_end; n += kCopyWarps) {
+                    locate(n + kCopyWarps);
+                    look_up(n + 2 * kCopyWarps);
+                    if (!wait_empty(n)) {
+                        ok = false;
+                        break;
+                    }
+                    const bool look = mixed(n);
+                    uint32_t odd = 0;
+                    const uint32_t slot = smem_u32(s_ring) + (n % kSlots) * S::kTile + (piece >> 2) * kPanel;
+#pragma unroll
+                    for (int i = 0; i < kCount; ++i) {
+                        const int r = i * kStep + r0;
+                        const float scale = pow2_of_byte(__shfl_sync(0xffffffffu, exps[i * kStep / 32], r & 31));
+                        uint4 x, y;
+                        bf16_of_codes(raw[i].x, scale, x.x, x.y);
+                        bf16_of_codes(raw[i].y, scale, x.z, x.w);
+                        bf16_of_codes(raw[i].z, scale, y.x, y.y);
+                        bf16_of_codes(raw[i].w, scale, y.z, y.w);
+                        if (look && (any_odd(x) | any_odd(y))) {
+                            odd = 1;
+                            x = make_uint4(without_odd(x.x), without_odd(x.y), without_odd(x.z), without_odd(x.w));
+                            y = make_uint4(without_odd(y.x), without_odd(y.y), without_odd(y.z), without_odd(y.w));
+                        }
+                        const int at = (2 * piece) & 7;
+                        sts128(slot + r * 128 + ((at ^ (r & 7)) << 4), x);
+                        sts128(slot + r * 128 + (((at + 1) ^ (r & 7)) << 4), y);
+                    }
+                    if (odd) *s_odd = 1;
+                    fence_proxy_async_shared();
+                    mbar_arrive(bar(kFull + n % kSlots));
+                    if (n + kCopyWarps < n_end) fetch(n + kCopyWarps);
                 }
             }
             tiles += g1 - g0;
@@ -516,64 +546,67 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
         }
         copy_wait_all();
         if (!ok) record_error(a.status, MOE_ERR_TIMEOUT);
-    } else if (warp == kSoftmaxWarps + kCopyWarps) {
+    } else if (warp == kProductWarp) {
         // ------------------------------------------------------------ products
-        if (lane == 0) {
+        {
+            const uint32_t leader = elected();
             constexpr uint32_t kIdescS = idesc_bf16_f32(kRowsTile, kKeys), kIdescO = idesc_bf16_f32(kRowsTile, D) | (1u << 16);
             auto wait = [&](int i, uint32_t parity) {
-                if (ok) ok = mbar_wait(bar(i), parity, kSpinBudget);
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(i), parity, kSpinBudget));
                 return ok;
             };
-            bool any = false;
-            for (; it.n > 0 && it.off + g0 < hi && ok; ++seg) {
+            for (; uniform(it.n > 0 && it.off + g0 < hi && ok); ++seg) {
                 const int g1 = static_cast<int>(min(static_cast<long long>(it.n), hi - it.off)), count = g1 - g0;
-                if (!wait(kQFull, seg & 1)) break;
-                for (int i = 0; i <= count && ok; ++i) {
-                    // The scores take the place of weights that the product two tiles back has read.  (Every phase of this
-                    // barrier is waited for before the next but one can begin: a wait tells only neighbours apart.)
-                    if (tiles + i >= 2 && (i > 0 || seg == 0) && !wait(kODone, (tiles + i) & 1)) break;
-                    if (i < count) {
-                        const int t = tiles + i, n = 2 * t;
-                        if (!wait(kFull + n % kSlots, (n / kSlots) & 1)) break;
-                        tc_fence_after();
-                        fence_proxy_async_shared();   // the copies were written through the generic proxy
+                for (int i = 0; uniform(i <= count && ok); ++i) {
+                    const int t = tiles + i, n = 2 * t, u = t - 1, nv = n - 1;   // tile t's scores, tile u's product with the values
+                    const bool back = t >= 2 && (i > 0 || seg == 0);
+                    if (uniform(i < count) && !wait(kFull + n % kSlots, (n / kSlots) & 1)) break;
+                    if (uniform(i == 0) && !wait(kQFull, seg & 1)) break;
+                    if (uniform(i > 0) && !wait(kFull + nv % kSlots, (nv / kSlots) & 1)) break;
+                    // The scores take the place of weights that the product two tiles back has read; the slot of its values is
+                    // free then.  (Every phase of this barrier is waited for before the next but one can begin: a wait tells
+                    // only neighbours apart.)
+                    if (uniform(back)) {
+                        if (!wait(kODone, t & 1)) break;
+                        if (lane == 0) mbar_arrive(bar(kEmpty + (nv - 2) % kSlots));
+                        __syncwarp();
+                    }
+                    tc_fence_after();
+                    fence_proxy_async_shared();   // the copies were written through the generic proxy
+                    if (uniform(i < count)) {
                         const uint32_t d = tmem + D + (t & 1) * kKeys, k0 = smem_u32(s_ring) + (n % kSlots) * S::kTile;
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
-                            mma_bf16(d, sdesc_k_sw128(smem_u32(s_q) + (k >> 2) * (kRowsTile * 128) + (k & 3) * 32),
-                                     sdesc_k_sw128(k0 + (k >> 2) * kPanel + (k & 3) * 32), kIdescS, k > 0);
-                        mma_commit(bar(kEmpty + n % kSlots));
-                        mma_commit(bar(kSFull + (t & 1)));
-                        if (i == count - 1) mma_commit(bar(kQEmpty));
+                            mma_if(leader, d, sdesc_k_sw128(smem_u32(s_q) + (k >> 2) * (kRowsTile * 128) + (k & 3) * 32),
+                                   sdesc_k_sw128(k0 + (k >> 2) * kPanel + (k & 3) * 32), kIdescS, k > 0);
+                        commit_if(leader, bar(kSFull + (t & 1)));   // (the keys' slot is handed on by the softmax)
+                        if (uniform(i == count - 1)) commit_if(leader, bar(kQEmpty));
                     }
-                    if (i > 0) {
-                        const int t = tiles + i - 1, n = 2 * t + 1;
-                        if (!wait(kPFull + (t & 1), (t >> 1) & 1)) break;
-                        if (!wait(kFull + n % kSlots, (n / kSlots) & 1)) break;
-                        if (i == 1 && seg > 0 && !wait(kOFree, (seg - 1) & 1)) break;
+                    if (uniform(i > 0)) {
+                        if (!wait(kPFull + (u & 1), (u >> 1) & 1)) break;
+                        if (uniform(i == 1 && seg > 0) && !wait(kOFree, (seg - 1) & 1)) break;
                         tc_fence_after();
-                        fence_proxy_async_shared();
-                        const uint32_t pt = tmem + D + (t & 1) * kKeys, v0 = smem_u32(s_ring) + (n % kSlots) * S::kTile;
+                        const uint32_t pt = tmem + D + (u & 1) * kKeys, v0 = smem_u32(s_ring) + (nv % kSlots) * S::kTile;
 #pragma unroll
                         for (int k = 0; k < kKeys / 16; ++k) {
-                            mma_bf16_tmem_a(tmem, pt + 8 * k, sdesc_values(v0 + k * 2048), kIdescO, i > 1 || k > 0);
-                            mma_bf16_tmem_a(tmem, pt + kKeys / 2 + 8 * k, sdesc_values(v0 + k * 2048), kIdescO, 1);
+                            mma_tmem_a_if(leader, tmem, pt + 8 * k, sdesc_values(v0 + k * 2048), kIdescO, i > 1 || k > 0);
+                            mma_tmem_a_if(leader, tmem, pt + kKeys / 2 + 8 * k, sdesc_values(v0 + k * 2048), kIdescO, 1);
                         }
-                        mma_commit(bar(kEmpty + n % kSlots));
-                        mma_commit(bar(kODone));
-                        if (i == count) mma_commit(bar(kItemDone));
-                        any = true;
+                        commit_if(leader, bar(kODone));
+                        if (uniform(i == count)) commit_if(leader, bar(kItemDone));
                     }
                 }
                 tiles += count;
                 next_item(a, it);
                 g0 = 0;
             }
+            // No arrival on a barrier is under way when the block ends, and no product when TMEM is released.
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(kODone), (tiles - 1) & 1, kSpinBudget));
             if (!ok) {
-                record_error(a.status, MOE_ERR_TIMEOUT);
-                // what was issued is complete before TMEM is released (the commit counts everything before it)
-                mma_commit(bar(kQEmpty));
-                if (any) mbar_wait(bar(kQEmpty), seg & 1, kSpinBudget);
+                if (lane == 0) record_error(a.status, MOE_ERR_TIMEOUT);
+                __syncwarp();
+                commit_if(leader, bar(kQEmpty));   // counts everything before it
+                mbar_wait(bar(kQEmpty), seg & 1, kSpinBudget);
             }
         }
         __syncwarp();
@@ -642,6 +675,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
                     ok = false;
                     break;
                 }
+                if (threadIdx.x == 0) mbar_arrive(bar(kEmpty + (2 * t) % kSlots));   // the keys have been read
+                __syncwarp();   // (TMEM is read by whole, converged warps)
                 tc_fence_after();
                 if (!idle) {
                     const uint32_t at = quarter + D + (t & 1) * kKeys;
@@ -687,19 +722,22 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
                         }
                     }
                     float sum[2] = {0.0f, 0.0f};
-                    uint32_t hi_part[32], lo_part[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float p0 = exp2_fast(fmaf(__uint_as_float(x[j >> 4][2 * (j & 15)]), c, -m));
-                        const float p1 = exp2_fast(fmaf(__uint_as_float(x[j >> 4][2 * (j & 15) + 1]), c, -m));
-                        sum[0] += p0;
-                        sum[1] += p1;
-                        hi_part[j] = pack_bf16x2(p0, p1);
-                        lo_part[j] = pack_bf16x2(p0 - __uint_as_float(hi_part[j] << 16), p1 - __uint_as_float(hi_part[j] & 0xffff0000u));
+                    for (int h = 0; h < 2; ++h) {   // 32 keys: 16 columns of pairs
+                        uint32_t hi_part[16], lo_part[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float p0 = exp2_fast(fmaf(__uint_as_float(x[h][2 * j]), c, -m));
+                            const float p1 = exp2_fast(fmaf(__uint_as_float(x[h][2 * j + 1]), c, -m));
+                            sum[0] += p0;
+                            sum[1] += p1;
+                            hi_part[j] = pack_bf16x2(p0, p1);
+                            lo_part[j] = pack_bf16x2(p0 - __uint_as_float(hi_part[j] << 16), p1 - __uint_as_float(hi_part[j] & 0xffff0000u));
+                        }
+                        tmem_st16(at + 16 * h, hi_part);
+                        tmem_st16(at + 32 + 16 * h, lo_part);
                     }
                     l += sum[0] + sum[1];
-                    tmem_st32(at, hi_part);
-                    tmem_st32(at + 32, lo_part);
                     tmem_st_wait();
                 }
                 tc_fence_before();
@@ -790,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kSoftmaxWarps + kCopyWarps) {
+    if (warp == kProductWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, S::kCols);
     }
