@@ -563,6 +563,27 @@ bool encode_bf16_map(CUtensorMap* tm, const void* ptr, uint64_t rows, uint64_t c
     return make_map(tm, ptr, rows, cols, box_rows);
 }
 
+bool encode_cache_map(CUtensorMap* tm, const void* ptr, bool codes, int head_dim, int page_size, int heads, int pages,
+                      long long token_bytes, long long head_bytes, long long page_bytes, int rows)
+{
+    auto enc = get_encode();
+    if (!enc) return false;
+    const long long strides[3] = {token_bytes, head_bytes, page_bytes};
+    cuuint64_t gdim[4] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(heads),
+                          static_cast<cuuint64_t>(pages)};
+    cuuint64_t gstride[3];
+    for (int i = 0; i < 3; ++i) {
+        const bool one = gdim[i + 1] == 1;   // its stride is never used, and may be anything
+        if (!one && (strides[i] <= 0 || strides[i] >= 1LL << 40)) return false;
+        gstride[i] = one ? 16 : static_cast<cuuint64_t>(strides[i]);
+    }
+    cuuint32_t box[4] = {codes ? static_cast<cuuint32_t>(head_dim) : 64u, static_cast<cuuint32_t>(rows), 1, 1};
+    cuuint32_t estride[4] = {1, 1, 1, 1};
+    return enc(tm, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), gdim, gstride,
+               box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 uint32_t pow2_cols(int n)

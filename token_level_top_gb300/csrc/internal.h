@@ -320,6 +320,11 @@ constexpr size_t kAttentionCtrlBytes = 8192;
 size_t paged_attention_ws_bytes(int head_dim);   // 0: unsupported head_dim
 cudaError_t launch_paged_attention(const AttentionArgs& a, int head_dim, bool e4m3, cudaStream_t s);
 
+// 4-D map (value, token of a page, head, page) of one side of a paged cache, box [1, 1, rows, 64 values] of bf16 with the
+// 128-byte swizzle, or [1, 1, rows, head_dim] of e4m3 codes without one.  False where TMA cannot take such a layout.
+bool encode_cache_map(CUtensorMap* tm, const void* ptr, bool codes, int head_dim, int page_size, int heads, int pages,
+                      long long token_bytes, long long head_bytes, long long page_bytes, int rows);
+
 // Attention of drafted tokens over the paged cache (tree_attention.cu).  Strides of the cache count bytes.
 struct TreeArgs {
     int B, T, n_heads, n_kv_heads, max_pages, window, n_pages, page_size;
@@ -340,6 +345,7 @@ struct TreeArgs {
     int* status;
     uint32_t page_mul;           // key / page_size = key * page_mul >> page_shift (set by the launcher)
     int page_shift;
+    int box_rows;                // rows of a TMA box, or 0: pieces of 16 bytes instead (set by the launcher)
 };
 constexpr size_t kTreeCtrlBytes = 256;
 size_t tree_attention_ws_bytes(int head_dim);   // 0: unsupported head_dim

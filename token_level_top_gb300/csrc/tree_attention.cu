@@ -46,20 +46,23 @@ constexpr int kPanel = kKeys * 128;         // bytes of 64 values of a tile's 64
 // Eight warps, so that two blocks an SM leave a thread 128 registers.
 constexpr int kSoftmaxWarps = 4, kCopyWarps = 3, kProductWarp = kSoftmaxWarps + kCopyWarps, kThreads = 32 * (kProductWarp + 1);
 constexpr int kGap = 2;                     // places of the list that an item's start and end are worth
-constexpr int kMaxSms = 152;
+constexpr int kMaxSms = 152, kMaxBlocks = 2 * kMaxSms;
 
-template <int D>
+template <int D, bool kE4m3>
 struct Shape {
     static constexpr int kCtas = D <= 128 ? 2 : 1;                        // blocks per SM
     static constexpr int kTile = kPanel * D / 64;                         // bytes of a key or value tile
     static constexpr int kQ = kRowsTile * D * 2;
-    static constexpr int kBars = 512;
-    static constexpr int kShare = 233472 / kCtas - 1024;
-    static constexpr int kSlots = std::min((kShare - kBars - kQ) / kTile, 12);
-    static constexpr int kSmem = kQ + kSlots * kTile + kBars;
+    static constexpr int kBars = 640;
+    static constexpr int kShare = std::min(233472 / kCtas - 1024, 232448);
+    // a ring of slots for tiles; e4m3 tiles have half of the room as they come in, in a ring of their own
+    static constexpr int kRaw = kE4m3 ? kKeys * D : 0, kRoom = kShare - kBars - kQ;
+    static constexpr int kSlots = kE4m3 ? (D == 64 ? 6 : 3) : std::min(kRoom / kTile, 12);
+    static constexpr int kRaws = kE4m3 ? (kRoom - kSlots * kTile) / kRaw : 0;
+    static constexpr int kSmem = kQ + kSlots * kTile + kRaws * kRaw + kBars;
     static constexpr int kCols = D <= 128 ? 256 : 512;                    // TMEM columns: O, then two tiles of scores
     static constexpr int kPart = kRowsTile * (D + 2);                     // floats of a part
-    static_assert(kSlots >= 4 && kSmem <= kShare && kSmem <= 232448 && D + 2 * kKeys <= kCols, "room");
+    static_assert(kSlots >= 3 && kSmem <= kShare && D + 2 * kKeys <= kCols, "room");
 };
 
 struct Header {   // of the item that begins in a block's run and does not end there
@@ -147,6 +150,17 @@ __device__ __forceinline__ uint64_t sdesc_values(uint32_t saddr)
     return d;
 }
 
+// A box of the cache's map at (value, token, head, page), counted on `bar`.
+__device__ __forceinline__ void copy_box_if(uint32_t leader, uint32_t dst, const CUtensorMap* map, int x, int token, int head, int page,
+                                            uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        "\n\t}\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(token), "r"(head), "r"(page), "r"(bar), "r"(leader)
+        : "memory");
+}
 // Copies 16 bytes, or writes 16 zeros when !live (src is then not read).
 __device__ __forceinline__ void copy_async_or_zeros(uint32_t dst, const void* src, bool live)
 {
@@ -252,18 +266,20 @@ struct Start {
 };
 
 template <int D, bool kE4m3>
-__global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kernel(const TreeArgs a)
+__global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
+    tree_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const TreeArgs a)
 {
-    using S = Shape<D>;
-    constexpr int kSlots = S::kSlots;
+    using S = Shape<D, kE4m3>;
+    constexpr int kSlots = S::kSlots, kRaws = S::kRaws;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char* const s_q = smem;
     unsigned char* const s_ring = smem + S::kQ;
-    uint64_t* const bars = reinterpret_cast<uint64_t*>(s_ring + kSlots * S::kTile);
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(s_ring + kSlots * S::kTile + kRaws * S::kRaw);
     // A tile's scores are there (two buffers), its weights, its product with the values done; an item's last product
     // done, its output read; its rows of q there, and no longer read.
     constexpr int kFull = 0, kEmpty = kSlots, kSFull = 2 * kSlots, kPFull = kSFull + 2, kODone = kPFull + 2, kOFree = kODone + 1,
-                  kQFull = kOFree + 1, kQEmpty = kQFull + 1, kItemDone = kQEmpty + 1, kCount = kItemDone + 1;
+                  kQFull = kOFree + 1, kQEmpty = kQFull + 1, kItemDone = kQEmpty + 1, kRawFull = kItemDone + 1, kRawEmpty = kRawFull + (kE4m3 ? kRaws : kCopyWarps),
+                  kCount = kRawEmpty + kRaws;
     static_assert(kCount * 8 + static_cast<int>(sizeof(Start)) + 16 * 8 + 16 <= S::kBars, "room for the barriers");
     Start* const s_start = reinterpret_cast<Start*>(bars + kCount);
     long long* const s_scan = reinterpret_cast<long long*>(s_start + 1);
@@ -350,6 +366,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
         mbar_init(bar(kQFull), 32 * kCopyWarps);
         mbar_init(bar(kQEmpty), 1);
         mbar_init(bar(kItemDone), 1);
+        for (int i = 0; i < (kE4m3 ? kRaws : kCopyWarps); ++i) mbar_init(bar(kRawFull + i), 32);
+        for (int i = 0; i < kRaws; ++i) mbar_init(bar(kRawEmpty + i), 1);
         mbar_fence_init();
         *s_odd = 0;
     }
@@ -371,40 +389,77 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
 
     if (warp >= kSoftmaxWarps && warp < kProductWarp) {
         // ------------------------------------------------------------ copies
-        // A warp takes every third slot's tile as a whole.
+        // bf16: a warp takes every third slot's tile as a whole.  e4m3: the first warp copies, the others turn keys and
+        // values into bf16.
         const int mine_of = warp - kSoftmaxWarps;
+        const uint32_t leader = elected();
+        int looked = 0;   // bf16: tiles that this warp has looked at
+        if (a.box_rows > 0 && lane == 0) {
+            tma_prefetch_desc(&map_k);
+            tma_prefetch_desc(&map_v);
+        }
         auto page_of = [&](int key) {
             return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(key)) * a.page_mul) >> a.page_shift);
         };
-        for (; it.n > 0 && it.off + g0 < hi && ok; ++seg) {
+        for (; uniform(it.n > 0 && it.off + g0 < hi && ok); ++seg) {
             const int g1 = static_cast<int>(min(static_cast<long long>(it.n), hi - it.off));
             const int mtiles = it.items / a.n_kv_heads, hk = it.h / mtiles, row_at = (it.h - hk * mtiles) * kRowsTile;
             const int32_t* const table = a.page_table + it.b * a.table_stride;
-            // this warp's slots n of the segment: from n0 on, every third
-            const int n_end = 2 * (tiles + g1 - g0);
-            int n = 2 * tiles + (mine_of + 2 * kCopyWarps * 1024 - (2 * tiles) % kCopyWarps) % kCopyWarps;
+            const int n0 = 2 * tiles, n_end = 2 * (tiles + g1 - g0);   // the segment's slots
+            auto first_key = [&](int n) { return it.base + (g0 + ((n - n0) >> 1)) * kKeys; };
             // pages of this lane's two keys of slot n's tile
             int entry[2];
             auto look_up = [&](int n) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int key = it.base + (g0 + (n >> 1) - tiles) * kKeys + 32 * h + lane;
+                    const int key = first_key(n) + 32 * h + lane;
                     entry[h] = n < n_end && key < it.len ? __ldg(table + page_of(key)) : -1;
                 }
             };
-            // their places in the cache, and their exponents', or -1
-            long long place[2], exp_place[2];
-            auto locate = [&](int n) {
+            // A tile's rows to dst: boxes, or pieces of 16 bytes (zeros where no key is), kRowBytes each; `full` gets 32 arrivals.
+            auto copy_tile = [&](int n, const int (&pages)[2], uint32_t dst, uint32_t full) {
+                constexpr int kRowBytes = kE4m3 ? D : 2 * D;
+                const int k0 = first_key(n), live = min(kKeys, it.len - k0);
+                const bool bad = (lane < live && static_cast<unsigned>(pages[0]) >= static_cast<unsigned>(a.n_pages)) ||
+                                 (lane + 32 < live && static_cast<unsigned>(pages[1]) >= static_cast<unsigned>(a.n_pages));
+                if (a.box_rows > 0 && !uniform(bad)) {
+                    const int boxes = (live + a.box_rows - 1) / a.box_rows;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * a.box_rows * kRowBytes));
+                    else
+                        mbar_arrive(full);
+                    __syncwarp();
+                    for (int j = 0; uniform(j < boxes); ++j) {
+                        const int r = j * a.box_rows, key = k0 + r;
+                        const int page = __shfl_sync(0xffffffffu, r < 32 ? pages[0] : pages[1], r & 31);
+                        const int token = key - page_of(key) * a.page_size;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int key = it.base + (g0 + (n >> 1) - tiles) * kKeys + 32 * h + lane;
-                    const bool live = entry[h] >= 0 && entry[h] < a.n_pages;
-                    const int at = key - page_of(key) * a.page_size;
-                    place[h] = live ? entry[h] * a.page_bytes + at * a.token_bytes : -1;
-                    if (kE4m3) exp_place[h] = live ? entry[h] * a.exp_page_stride + at * a.exp_token_stride : -1;
+                        for (int x = 0; x < (kE4m3 ? 1 : D / 64); ++x)
+                            copy_box_if(leader, dst + x * kPanel + r * (kE4m3 ? D : 128), n & 1 ? &map_v : &map_k, 64 * x, token, hk, page, full);
+                    }
+                } else {
+                    long long place[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int key = k0 + 32 * h + lane;
+                        const bool there = pages[h] >= 0 && pages[h] < a.n_pages;
+                        place[h] = there ? pages[h] * a.page_bytes + (key - page_of(key) * a.page_size) * a.token_bytes : -1;
+                    }
+                    constexpr int kPieces = kRowBytes / 16, kStep = 32 / kPieces, kCount = kKeys * kPieces / 32;
+                    const int piece = lane % kPieces, r0 = lane / kPieces;
+                    const char* const from = (n & 1 ? a.v : a.k) + hk * a.head_bytes + 16 * piece;
+#pragma unroll 8
+                    for (int i = 0; i < kCount; ++i) {
+                        const int r = i * kStep + r0;
+                        const long long p0 = __shfl_sync(0xffffffffu, place[0], r & 31), p1 = __shfl_sync(0xffffffffu, place[1], r & 31);
+                        const long long at = r < 32 ? p0 : p1;
+                        copy_async_or_zeros(kE4m3 ? dst + r * D + 16 * piece
+                                                  : dst + (piece >> 3) * kPanel + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
+                                            from + (at < 0 ? 0 : at), at >= 0);
+                    }
+                    copy_arrive(full);
                 }
             };
-            look_up(n);
             // ---- the rows of q, eight at a time
             if (seg > 0) ok = mbar_wait(bar(kQEmpty), (seg - 1) & 1, kSpinBudget);
             if (!__all_sync(0xffffffffu, ok)) {
@@ -435,96 +490,102 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
                 }
                 fence_proxy_async_shared();
                 mbar_arrive(bar(kQFull));
+                __syncwarp();
             }
             // ---- the key and value tiles
             const int odd_from = a.window > 0 ? max(0, it.ctx - a.window + it.draft) : 0;   // below it, and from ctx on, rows differ
             auto mixed = [&](int n) {   // values of a tile where rows differ
-                const int k0 = it.base + (g0 + (n >> 1) - tiles) * kKeys;
+                const int k0 = first_key(n);
                 return (n & 1) != 0 && (k0 < odd_from || k0 + kKeys > it.ctx);
             };
-            auto wait_empty = [&](int n) {
-                const bool got = mbar_wait(bar(kEmpty + n % kSlots), ((n / kSlots) & 1) ^ 1, kSpinBudget);
-                return __all_sync(0xffffffffu, got) != 0;
+            auto wait_for = [&](int i, uint32_t parity) {
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(i), parity, kSpinBudget));
+                return ok;
             };
             if constexpr (!kE4m3) {
-                constexpr int kPieces = D / 8, kStep = 32 / kPieces > 0 ? 32 / kPieces : 1;   // rows an instruction copies
-                constexpr int kCount = kKeys * kPieces / 32;
-                const int piece = lane % kPieces, r0 = lane / kPieces;
-                for (; n < n_end; n += kCopyWarps) {
-                    locate(n);
+                int n = n0 + (mine_of + kCopyWarps - n0 % kCopyWarps) % kCopyWarps;
+                look_up(n);
+                for (; uniform(n < n_end); n += kCopyWarps) {
+                    const int pages[2] = {entry[0], entry[1]};
                     look_up(n + kCopyWarps);
-                    if (!wait_empty(n)) {
-                        ok = false;
-                        break;
+                    if (!wait_for(kEmpty + n % kSlots, ((n / kSlots) & 1) ^ 1)) break;
+                    const uint32_t slot = smem_u32(s_ring) + (n % kSlots) * S::kTile;
+                    if (!uniform(mixed(n))) {
+                        copy_tile(n, pages, slot, bar(kFull + n % kSlots));
+                        continue;
                     }
-                    const char* const from = (n & 1 ? a.v : a.k) + hk * a.head_bytes + 16 * piece;
-                    const uint32_t slot = smem_u32(s_ring) + (n % kSlots) * S::kTile + (piece >> 3) * kPanel;
-#pragma unroll
-                    for (int i = 0; i < kCount; ++i) {
-                        const int r = i * kStep + r0;
-                        const long long at = __shfl_sync(0xffffffffu, place[i * kStep / 32], r & 31);
-                        copy_async_or_zeros(slot + r * 128 + (((piece & 7) ^ (r & 7)) << 4), from + (at < 0 ? 0 : at), at >= 0);
-                    }
-                    if (mixed(n)) {   // (these are looked at here, so they are waited for)
-                        copy_wait_all();
-                        uint32_t odd = 0;
+                    copy_tile(n, pages, slot, bar(kRawFull + mine_of));
+                    if (!wait_for(kRawFull + mine_of, looked++ & 1)) break;
+                    const int live = min(kKeys, it.len - first_key(n));
+                    uint32_t odd = 0;
 #pragma unroll 4
-                        for (int i = 0; i < kCount; ++i) {
-                            const int r = i * kStep + r0;
-                            const uint32_t at = slot + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
-                            uint4 x = lds128(at);
-                            if (any_odd(x)) {
-                                odd = 1;
-                                x = make_uint4(without_odd(x.x), without_odd(x.y), without_odd(x.z), without_odd(x.w));
-                                sts128(at, x);
-                            }
+                    for (int i = lane; i < S::kTile / 16; i += 32) {   // (rows of 128 bytes: the order within does not matter)
+                        const uint32_t at = slot + 16 * i;
+                        uint4 x = lds128(at);
+                        const bool dead = ((i >> 3) & (kKeys - 1)) >= live;
+                        if (dead || any_odd(x)) {
+                            odd |= !dead;
+                            x = dead ? make_uint4(0, 0, 0, 0) : make_uint4(without_odd(x.x), without_odd(x.y), without_odd(x.z), without_odd(x.w));
+                            sts128(at, x);
                         }
-                        if (odd) *s_odd = 1;
-                        fence_proxy_async_shared();
-                        mbar_arrive(bar(kFull + n % kSlots));
-                    } else {
-                        copy_arrive(bar(kFull + n % kSlots));
                     }
+                    if (odd) *s_odd = 1;
+                    fence_proxy_async_shared();
+                    mbar_arrive(bar(kFull + n % kSlots));
+                }
+            } else if (mine_of == 0) {
+                int n = n0;
+                look_up(n);
+                for (; uniform(n < n_end); n += 2) {   // keys and values of a tile lie in the same pages
+                    const int pages[2] = {entry[0], entry[1]};
+                    look_up(n + 2);
+#pragma unroll 1
+                    for (int v = 0; v < 2; ++v) {
+                        const int m = n + v;
+                        if (!wait_for(kRawEmpty + m % kRaws, ((m / kRaws) & 1) ^ 1)) break;
+                        copy_tile(m, pages, smem_u32(s_ring) + kSlots * S::kTile + (m % kRaws) * S::kRaw, bar(kRawFull + m % kRaws));
+                    }
+                    if (!ok) break;
                 }
             } else {
                 constexpr int kPieces = D / 16, kStep = 32 / kPieces, kCount = kKeys * kPieces / 32;   // pieces of 16 codes
-                const int piece = lane % kPieces, r0 = lane / kPieces;
-                uint4 raw[kCount];
-                uint32_t exps[2];
-                auto fetch = [&](int n) {   // of the located tile
-                    const char* const from = (n & 1 ? a.v : a.k) + hk * a.head_bytes + 16 * piece;
-                    const uint8_t* const from_exp = (n & 1 ? a.v_exp : a.k_exp) + hk * a.exp_head_stride;
+                const int piece = lane % kPieces, r0 = lane / kPieces, v = mine_of - 1;
+                const uint8_t* const from_exp = (v ? a.v_exp : a.k_exp) + hk * a.exp_head_stride;
+                uint32_t next[2];   // exponent bytes of this lane's two keys
+                auto exponents = [&](int n) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) exps[h] = exp_place[h] >= 0 ? __ldg(from_exp + exp_place[h]) : 127u;
-#pragma unroll
-                    for (int i = 0; i < kCount; ++i) {
-                        const int r = i * kStep + r0;
-                        const long long at = __shfl_sync(0xffffffffu, place[i * kStep / 32], r & 31);
-                        raw[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(from + at)) : make_uint4(0, 0, 0, 0);
+                    for (int h = 0; h < 2; ++h) {
+                        const int key = first_key(n) + 32 * h + lane, at = key - page_of(key) * a.page_size;
+                        next[h] = entry[h] >= 0 && entry[h] < a.n_pages
+                                      ? __ldg(from_exp + entry[h] * a.exp_page_stride + at * a.exp_token_stride) : 127u;
                     }
                 };
-                locate(n);
-                look_up(n + kCopyWarps);
-                fetch(n);
-                for (; n < n_end; n += kCopyWarps) {
-                    locate(n + kCopyWarps);
-                    look_up(n + 2 * kCopyWarps);
-                    if (!wait_empty(n)) {
-                        ok = false;
-                        break;
-                    }
-                    const bool look = mixed(n);
-                    uint32_t odd = 0;
+                look_up(n0 + v);
+                exponents(n0 + v);
+                look_up(n0 + v + 2);
+                for (int n = n0 + v; uniform(n < n_end); n += 2) {
+                    const uint32_t exps[2] = {next[0], next[1]};
+                    exponents(n + 2);
+                    look_up(n + 4);
+                    const bool look = uniform(mixed(n));
+                    const int live = min(kKeys, it.len - first_key(n));
+                    if (!wait_for(kEmpty + n % kSlots, ((n / kSlots) & 1) ^ 1)) break;
+                    if (!wait_for(kRawFull + n % kRaws, (n / kRaws) & 1)) break;
+                    const uint32_t raw = smem_u32(s_ring) + kSlots * S::kTile + (n % kRaws) * S::kRaw + r0 * D + 16 * piece;
                     const uint32_t slot = smem_u32(s_ring) + (n % kSlots) * S::kTile + (piece >> 2) * kPanel;
-#pragma unroll
+                    uint32_t odd = 0;
+#pragma unroll 4
                     for (int i = 0; i < kCount; ++i) {
                         const int r = i * kStep + r0;
-                        const float scale = pow2_of_byte(__shfl_sync(0xffffffffu, exps[i * kStep / 32], r & 31));
+                        uint4 w = lds128(raw + i * kStep * D);
+                        if (r >= live) w = make_uint4(0, 0, 0, 0);
+                        const uint32_t e0 = __shfl_sync(0xffffffffu, exps[0], r & 31), e1 = __shfl_sync(0xffffffffu, exps[1], r & 31);
+                        const float scale = pow2_of_byte(r < 32 ? e0 : e1);
                         uint4 x, y;
-                        bf16_of_codes(raw[i].x, scale, x.x, x.y);
-                        bf16_of_codes(raw[i].y, scale, x.z, x.w);
-                        bf16_of_codes(raw[i].z, scale, y.x, y.y);
-                        bf16_of_codes(raw[i].w, scale, y.z, y.w);
+                        bf16_of_codes(w.x, scale, x.x, x.y);
+                        bf16_of_codes(w.y, scale, x.z, x.w);
+                        bf16_of_codes(w.z, scale, y.x, y.y);
+                        bf16_of_codes(w.w, scale, y.z, y.w);
                         if (look && (any_odd(x) | any_odd(y))) {
                             odd = 1;
                             x = make_uint4(without_odd(x.x), without_odd(x.y), without_odd(x.z), without_odd(x.w));
@@ -537,7 +598,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
                     if (odd) *s_odd = 1;
                     fence_proxy_async_shared();
                     mbar_arrive(bar(kFull + n % kSlots));
-                    if (n + kCopyWarps < n_end) fetch(n + kCopyWarps);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kRawEmpty + n % kRaws));
+                    __syncwarp();
                 }
             }
             tiles += g1 - g0;
@@ -545,7 +608,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
             g0 = 0;
         }
         copy_wait_all();
-        if (!ok) record_error(a.status, MOE_ERR_TIMEOUT);
+        if (!ok) {
+            record_error(a.status, MOE_ERR_TIMEOUT);
+            for (const long long t0 = clock64(); clock64() - t0 < kSpinBudget / 100;) {   // boxes that nobody waited for land
+            }
+        }
     } else if (warp == kProductWarp) {
         // ------------------------------------------------------------ products
         {
@@ -559,18 +626,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
                 const int g1 = static_cast<int>(min(static_cast<long long>(it.n), hi - it.off)), count = g1 - g0;
                 for (int i = 0; uniform(i <= count && ok); ++i) {
                     const int t = tiles + i, n = 2 * t, u = t - 1, nv = n - 1;   // tile t's scores, tile u's product with the values
-                    const bool back = t >= 2 && (i > 0 || seg == 0);
-                    if (uniform(i < count) && !wait(kFull + n % kSlots, (n / kSlots) & 1)) break;
-                    if (uniform(i == 0) && !wait(kQFull, seg & 1)) break;
-                    if (uniform(i > 0) && !wait(kFull + nv % kSlots, (nv / kSlots) & 1)) break;
                     // The scores take the place of weights that the product two tiles back has read; the slot of its values is
-                    // free then.  (Every phase of this barrier is waited for before the next but one can begin: a wait tells
-                    // only neighbours apart.)
-                    if (uniform(back)) {
+                    // free then, and the keys waited for next may need it.  (Every phase of this barrier is waited for before
+                    // the next but one can begin: a wait tells only neighbours apart.)
+                    if (uniform(t >= 2 && (i > 0 || seg == 0))) {
                         if (!wait(kODone, t & 1)) break;
                         if (lane == 0) mbar_arrive(bar(kEmpty + (nv - 2) % kSlots));
                         __syncwarp();
                     }
+                    if (uniform(i < count) && !wait(kFull + n % kSlots, (n / kSlots) & 1)) break;
+                    if (uniform(i == 0) && !wait(kQFull, seg & 1)) break;
+                    if (uniform(i > 0) && !wait(kFull + nv % kSlots, (nv / kSlots) & 1)) break;
                     tc_fence_after();
                     fence_proxy_async_shared();   // the copies were written through the generic proxy
                     if (uniform(i < count)) {
@@ -751,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
             if (!idle) {
                 const bool whole = g0 == 0 && g1 == it.n;
                 const int slot = 2 * blockIdx.x + (g0 == 0 ? 1 : 0);
-                float* const part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kTreeCtrlBytes + sizeof(Header) * S::kCtas * kMaxSms) +
+                float* const part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kTreeCtrlBytes + sizeof(Header) * kMaxBlocks) +
                                     static_cast<long long>(slot) * S::kPart;
                 const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : NAN);
                 const bool odd = *s_odd != 0;
@@ -840,13 +906,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) tree_attention_kern
 template <int D>
 __global__ void __launch_bounds__(256) tree_attention_join_kernel(const TreeArgs a)
 {
-    using S = Shape<D>;
+    using S = Shape<D, false>;
     const Header h = reinterpret_cast<const Header*>(static_cast<const char*>(a.ws) + kTreeCtrlBytes)[blockIdx.x];
     const int row0 = (blockIdx.y & 3) * 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (h.last < 0 || row0 >= h.rows) return;
     const int row = row0 + lane, col4 = (blockIdx.y >> 2) * 8 + warp;   // four columns
     const int parts = h.last - static_cast<int>(blockIdx.x) + 1;
-    const float* const base = reinterpret_cast<const float*>(static_cast<const char*>(a.ws) + kTreeCtrlBytes + sizeof(Header) * S::kCtas * kMaxSms);
+    const float* const base = reinterpret_cast<const float*>(static_cast<const char*>(a.ws) + kTreeCtrlBytes + sizeof(Header) * kMaxBlocks);
     auto part = [&](int i) { return base + (2LL * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * S::kPart; };
     float m = kNone;
 #pragma unroll 4
@@ -874,14 +940,21 @@ __global__ void __launch_bounds__(256) tree_attention_join_kernel(const TreeArgs
 }
 
 template <int D, bool kE4m3>
-cudaError_t launch(const TreeArgs& a, cudaStream_t s)
+cudaError_t launch(TreeArgs& a, cudaStream_t s)
 {
-    using S = Shape<D>;
+    using S = Shape<D, kE4m3>;
     const auto kernel = tree_attention_kernel<D, kE4m3>;
     const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), S::kSmem);
     if (e != cudaSuccess) return e;
+    // boxes of as many rows as a page and a tile have in common (the swizzle's pattern is 8 rows high)
+    CUtensorMap map_k{}, map_v{};
+    int rows = kKeys;
+    while (a.page_size % rows != 0) rows /= 2;
+    a.box_rows = rows >= 8 && encode_cache_map(&map_k, a.k, kE4m3, D, a.page_size, a.n_kv_heads, a.n_pages, a.token_bytes, a.head_bytes, a.page_bytes, rows) &&
+                         encode_cache_map(&map_v, a.v, kE4m3, D, a.page_size, a.n_kv_heads, a.n_pages, a.token_bytes, a.head_bytes, a.page_bytes, rows)
+                     ? rows : 0;
     const unsigned grid = static_cast<unsigned>(S::kCtas * std::min(num_sms(), kMaxSms));
-    kernel<<<grid, kThreads, S::kSmem, s>>>(a);
+    kernel<<<grid, kThreads, S::kSmem, s>>>(map_k, map_v, a);
     tree_attention_join_kernel<D><<<dim3(grid, 4 * D / 32), 256, 0, s>>>(a);
     return cudaGetLastError();
 }
@@ -889,9 +962,8 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t s)
 template <int D>
 size_t ws_bytes()
 {
-    using S = Shape<D>;
-    constexpr size_t kBlocks = S::kCtas * kMaxSms;
-    return kTreeCtrlBytes + kBlocks * (sizeof(Header) + 2 * S::kPart * sizeof(float));
+    using S = Shape<D, false>;
+    return kTreeCtrlBytes + kMaxBlocks * sizeof(Header) + static_cast<size_t>(S::kCtas) * kMaxSms * 2 * S::kPart * sizeof(float);
 }
 
 }  // namespace
