@@ -45,7 +45,7 @@ constexpr int kRowsTile = 128, kKeys = 64;
 constexpr int kPanel = kKeys * 128;         // bytes of 64 values of a tile's 64 rows
 // Eight warps, so that two blocks an SM leave a thread 128 registers.
 constexpr int kSoftmaxWarps = 4, kCopyWarps = 3, kProductWarp = kSoftmaxWarps + kCopyWarps, kThreads = 32 * (kProductWarp + 1);
-constexpr int kGap = 2;                     // places of the list that an item's start and end are worth
+constexpr int kGap = 4;                     // places of the list that an item's start and end are worth
 constexpr int kMaxSms = 152, kMaxBlocks = 2 * kMaxSms;
 
 template <int D, bool kE4m3>
@@ -460,38 +460,44 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     copy_arrive(full);
                 }
             };
-            // ---- the rows of q, eight at a time
-            if (seg > 0) ok = mbar_wait(bar(kQEmpty), (seg - 1) & 1, kSpinBudget);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            {
+            // ---- the rows of q, eight at a time; asked for behind the first tile
+            auto copy_q = [&]() {
+                if (seg > 0) ok = mbar_wait(bar(kQEmpty), (seg - 1) & 1, kSpinBudget);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return false;
                 constexpr int kPieces = D / 8;   // 16-byte pieces of a row
-                const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+                auto at = [&](int r, int piece) {
+                    return smem_u32(s_q) + (piece >> 3) * (kRowsTile * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+                };
 #pragma unroll 1
                 for (int r1 = 8 * mine_of; r1 < kRowsTile; r1 += 8 * kCopyWarps) {
-                    uint4 x[kPieces / 4];
 #pragma unroll
                     for (int i = 0; i < kPieces / 4; ++i) {
                         const int r = r1 + (i * 32 + lane) / kPieces, piece = (i * 32 + lane) % kPieces;
                         const int row = row_at + r, t = row / group;
-                        x[i] = make_uint4(0, 0, 0, 0);
-                        if (t < it.draft && a.scale != 0.0f)
-                            x[i] = *reinterpret_cast<const uint4*>(a.q + (it.row0 + t) * a.q_token_stride +
-                                                                   (hk * group + (row - t * group)) * a.q_head_stride + 8 * piece);
-                    }
-#pragma unroll
-                    for (int i = 0; i < kPieces / 4; ++i) {
-                        const int r = r1 + (i * 32 + lane) / kPieces, piece = (i * 32 + lane) % kPieces;
-                        x[i].x ^= flip, x[i].y ^= flip, x[i].z ^= flip, x[i].w ^= flip;
-                        sts128(smem_u32(s_q) + (piece >> 3) * (kRowsTile * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4), x[i]);
+                        const bool live = t < it.draft && a.scale != 0.0f;
+                        copy_async_or_zeros(at(r, piece), a.q + (live ? (it.row0 + t) * a.q_token_stride +
+                                                                            (hk * group + (row - t * group)) * a.q_head_stride : 0) + 8 * piece, live);
                     }
                 }
-                fence_proxy_async_shared();
-                mbar_arrive(bar(kQFull));
+                if (a.scale >= 0.0f) {
+                    copy_arrive(bar(kQFull));
+                } else {
+                    copy_wait_all();
+#pragma unroll 1
+                    for (int r1 = 8 * mine_of; r1 < kRowsTile; r1 += 8 * kCopyWarps)
+#pragma unroll
+                        for (int i = 0; i < kPieces / 4; ++i) {
+                            const uint32_t to = at(r1 + (i * 32 + lane) / kPieces, (i * 32 + lane) % kPieces);
+                            const uint4 x = lds128(to);
+                            sts128(to, make_uint4(x.x ^ 0x80008000u, x.y ^ 0x80008000u, x.z ^ 0x80008000u, x.w ^ 0x80008000u));
+                        }
+                    fence_proxy_async_shared();
+                    mbar_arrive(bar(kQFull));
+                }
                 __syncwarp();
-            }
+                return true;
+            };
             // ---- the key and value tiles
             const int odd_from = a.window > 0 ? max(0, it.ctx - a.window + it.draft) : 0;   // below it, and from ctx on, rows differ
             auto mixed = [&](int n) {   // values of a tile where rows differ
@@ -505,16 +511,17 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
             if constexpr (!kE4m3) {
                 int n = n0 + (mine_of + kCopyWarps - n0 % kCopyWarps) % kCopyWarps;
                 look_up(n);
+                bool q_there = false;
                 for (; uniform(n < n_end); n += kCopyWarps) {
                     const int pages[2] = {entry[0], entry[1]};
                     look_up(n + kCopyWarps);
                     if (!wait_for(kEmpty + n % kSlots, ((n / kSlots) & 1) ^ 1)) break;
                     const uint32_t slot = smem_u32(s_ring) + (n % kSlots) * S::kTile;
-                    if (!uniform(mixed(n))) {
-                        copy_tile(n, pages, slot, bar(kFull + n % kSlots));
-                        continue;
-                    }
-                    copy_tile(n, pages, slot, bar(kRawFull + mine_of));
+                    const bool look = uniform(mixed(n));
+                    copy_tile(n, pages, slot, look ? bar(kRawFull + mine_of) : bar(kFull + n % kSlots));
+                    if (!q_there && !copy_q()) break;
+                    q_there = true;
+                    if (!look) continue;
                     if (!wait_for(kRawFull + mine_of, looked++ & 1)) break;
                     const int live = min(kKeys, it.len - first_key(n));
                     uint32_t odd = 0;
@@ -532,10 +539,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     if (odd) *s_odd = 1;
                     fence_proxy_async_shared();
                     mbar_arrive(bar(kFull + n % kSlots));
+                    __syncwarp();
                 }
+                if (ok && !q_there && !copy_q()) break;
             } else if (mine_of == 0) {
                 int n = n0;
                 look_up(n);
+                bool q_there = false;
                 for (; uniform(n < n_end); n += 2) {   // keys and values of a tile lie in the same pages
                     const int pages[2] = {entry[0], entry[1]};
                     look_up(n + 2);
@@ -545,9 +555,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                         if (!wait_for(kRawEmpty + m % kRaws, ((m / kRaws) & 1) ^ 1)) break;
                         copy_tile(m, pages, smem_u32(s_ring) + kSlots * S::kTile + (m % kRaws) * S::kRaw, bar(kRawFull + m % kRaws));
                     }
-                    if (!ok) break;
+                    if (!ok || (!q_there && !copy_q())) break;
+                    q_there = true;
                 }
             } else {
+                if (!copy_q()) break;
                 constexpr int kPieces = D / 16, kStep = 32 / kPieces, kCount = kKeys * kPieces / 32;   // pieces of 16 codes
                 const int piece = lane % kPieces, r0 = lane / kPieces, v = mine_of - 1;
                 const uint8_t* const from_exp = (v ? a.v_exp : a.k_exp) + hk * a.exp_head_stride;
