@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(kSelectThreads) beam_select_kernel(const BeamA
 {
     __shared__ double s_total[kMaxCandidates];
     __shared__ int s_valid;
+    wait_for_previous();
     const int W = a.beams, n = a.n, count = W * n;
     const long long b = blockIdx.x;
     if (threadIdx.x == 0) s_valid = 0;
@@ -83,13 +84,12 @@ __global__ void __launch_bounds__(kSelectThreads) beam_select_kernel(const BeamA
 
 // ---------------------------------------------------------------- reordering
 
-constexpr int kMoveThreads = 256, kMoveDepth = 4;   // 16-byte pieces that a thread has in flight
+constexpr int kMoveThreads = 256, kMoveDepth = 8;   // 16-byte pieces that a thread has in flight
 
-// Where the beams' filling pages come from, decided by the first 64 threads of a block.
-struct Homes {
-    int parent[MOE_MAX_BEAMS];     // checked; -1: none
-    int home[MOE_MAX_BEAMS];       // the beam whose filling page this one gets
-    unsigned first[2], free[2];    // bits: the first of its parent's children; beams that nobody continues
+// Beam w's parent (-1: none) and the beam whose filling page it gets, found by each warp for itself: lane l looks after
+// beams l and l + 32.
+struct Home {
+    int parent, home;
 };
 
 __device__ __forceinline__ int nth_bit(const unsigned (&m)[2], int n)
@@ -98,53 +98,52 @@ __device__ __forceinline__ int nth_bit(const unsigned (&m)[2], int n)
     return n < low ? __fns(m[0], 0, n + 1) : 32 + __fns(m[1], 0, n - low + 1);
 }
 
-__device__ __forceinline__ void find_homes(const BeamMoveArgs& a, long long b, Homes& h)
+__device__ __forceinline__ Home find_home(const BeamMoveArgs& a, long long b, int w)
 {
-    const int w = threadIdx.x, W = a.beams;
-    if (w < MOE_MAX_BEAMS) {
-        int p = -1;
-        if (w < W) {
-            p = a.parents[b * a.parent_stride + w];
-            if (p >= W) {
-                if (blockIdx.y == 0) record_error(a.status, MOE_ERR_INDEX);
-                p = -1;
-            }
-        }
-        h.parent[w] = p < 0 ? -1 : p;
+    const int lane = threadIdx.x & 31, W = a.beams;
+    int p[2] = {-1, -1};
+    bool bad = false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int beam = lane + 32 * h;
+        if (beam < W) p[h] = a.parents[b * a.parent_stride + beam];
+        bad = bad || p[h] >= W;
+        if (p[h] >= W || p[h] < 0) p[h] = -1;
     }
-    __syncthreads();
-    if (w < MOE_MAX_BEAMS) {
-        const int p = h.parent[w];
-        bool first = p >= 0, free = w < W;
-        for (int o = 0; o < W; ++o) {
-            const int q = h.parent[o];
-            if (o < w && q == p) first = false;
-            if (q == w) free = false;
-        }
-        const unsigned fb = __ballot_sync(0xffffffffu, first), eb = __ballot_sync(0xffffffffu, free);
-        if ((w & 31) == 0) {
-            h.first[w >> 5] = fb;
-            h.free[w >> 5] = eb;
-        }
+    if (bad && blockIdx.y == 0 && w == 0 && threadIdx.x < 32) record_error(a.status, MOE_ERR_INDEX);
+    // bits: the first of its parent's children; beams that somebody goes on from
+    unsigned first[2] = {0, 0}, taken[2] = {0, 0};
+    const unsigned same0 = __match_any_sync(0xffffffffu, p[0]);
+    first[0] = __ballot_sync(0xffffffffu, p[0] >= 0 && __ffs(same0) - 1 == lane);
+    taken[0] = __reduce_or_sync(0xffffffffu, p[0] >= 0 && p[0] < 32 ? 1u << p[0] : 0u);
+    if (W > 32) {
+        const unsigned same1 = __match_any_sync(0xffffffffu, p[1]);
+        taken[1] = __reduce_or_sync(0xffffffffu, p[0] >= 32 ? 1u << (p[0] - 32) : 0u);
+        // (p[1] is no first child if the lower beams have its parent)
+        const unsigned low = p[1] < 0 ? 0u : (p[1] < 32 ? taken[0] >> p[1] : taken[1] >> (p[1] - 32)) & 1u;
+        first[1] = __ballot_sync(0xffffffffu, p[1] >= 0 && !low && __ffs(same1) - 1 == lane);
+        taken[0] |= __reduce_or_sync(0xffffffffu, p[1] >= 0 && p[1] < 32 ? 1u << p[1] : 0u);
+        taken[1] |= __reduce_or_sync(0xffffffffu, p[1] >= 32 ? 1u << (p[1] - 32) : 0u);
     }
-    __syncthreads();
-    if (w < W) {
-        // the n-th beam that is no first child takes the n-th page left over
-        const unsigned below = w < 32 ? (1u << w) - 1u : 0xffffffffu, above = w < 32 ? 0u : (1u << (w - 32)) - 1u;
-        const bool first = h.first[w >> 5] >> (w & 31) & 1u;
-        h.home[w] = first ? h.parent[w] : nth_bit(h.free, __popc(~h.first[0] & below) + __popc(~h.first[1] & above));
-    }
-    __syncthreads();
+    const unsigned free[2] = {~taken[0] & (W >= 32 ? 0xffffffffu : (1u << W) - 1u),
+                              W > 32 ? ~taken[1] & (W >= 64 ? 0xffffffffu : (1u << (W - 32)) - 1u) : 0u};
+    Home h;
+    h.parent = __shfl_sync(0xffffffffu, w < 32 ? p[0] : p[1], w & 31);
+    // the n-th beam that is no first child takes the n-th page left over
+    const unsigned below = w < 32 ? (1u << w) - 1u : 0xffffffffu, above = w < 32 ? 0u : (1u << (w - 32)) - 1u;
+    const bool is_first = (w < 32 ? first[0] >> w : first[1] >> (w - 32)) & 1u;
+    h.home = is_first ? h.parent : nth_bit(free, __popc(~first[0] & below) + __popc(~first[1] & above));
+    return h;
 }
 
 // Block (x, y): beam x of the batch, part y of its table row and of the rows it gets.
 __global__ void __launch_bounds__(kMoveThreads) beam_reorder_kernel(const BeamMoveArgs a)
 {
-    __shared__ Homes h;
+    wait_for_previous();
     const int W = a.beams;
     const long long b = blockIdx.x / static_cast<unsigned>(W), row = blockIdx.x;
     const int w = static_cast<int>(row - b * W);
-    find_homes(a, b, h);
+    const Home h = find_home(a, b, w);
     const long long most = static_cast<long long>(a.max_pages) * a.page_size;
     long long len = a.seq_len[b];
     if (len < 0 || len > most) {
@@ -152,7 +151,7 @@ __global__ void __launch_bounds__(kMoveThreads) beam_reorder_kernel(const BeamMo
         len = len < 0 ? 0 : most;
     }
     const int full = static_cast<int>(len / a.page_size), rest = static_cast<int>(len - static_cast<long long>(full) * a.page_size);
-    const int p = h.parent[w], home = h.home[w];
+    const int p = h.parent, home = h.home;
     const int32_t* const mine = a.table + row * a.table_stride;
     const int32_t* const parent = a.table + (b * W + (p < 0 ? w : p)) * a.table_stride;
     const int32_t* const kept = a.table + (b * W + home) * a.table_stride;
@@ -227,18 +226,17 @@ cudaError_t launch_beam_select(const BeamArgs& a, cudaStream_t s)
     l.status = a.status;
     const cudaError_t e = launch_token_logprobs(l, s);
     if (e != cudaSuccess) return e;
-    beam_select_kernel<<<static_cast<unsigned>(a.seqs), kSelectThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_after(beam_select_kernel, dim3(static_cast<unsigned>(a.seqs)), kSelectThreads, 0, s, a);
 }
 
 cudaError_t launch_beam_reorder(const BeamMoveArgs& a, cudaStream_t s)
 {
     if (a.seqs <= 0) return cudaSuccess;
-    // parts of a beam: its threads move kMoveDepth pieces twice each when its page is full
-    const long long pieces = 2LL * a.page_size * a.n_kv_heads * (a.row_bytes / 16);
-    const unsigned parts = static_cast<unsigned>(std::clamp<long long>(pieces / (2 * kMoveThreads * kMoveDepth), 1, 32));
-    beam_reorder_kernel<<<dim3(static_cast<unsigned>(a.seqs) * a.beams, parts), kMoveThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    // parts of a beam: when its page is full a thread moves kMoveDepth pieces twice, or once while that fills the GPU
+    const long long pieces = 2LL * a.page_size * a.n_kv_heads * (a.row_bytes / 16), beams = static_cast<long long>(a.seqs) * a.beams;
+    const long long once = (pieces + kMoveThreads * kMoveDepth - 1) / (kMoveThreads * kMoveDepth);
+    const unsigned parts = static_cast<unsigned>(std::clamp<long long>(beams * once <= 8LL * num_sms() ? once : (once + 1) / 2, 1, 32));
+    return launch_after(beam_reorder_kernel, dim3(static_cast<unsigned>(beams), parts), kMoveThreads, 0, s, a);
 }
 
 }  // namespace moe

@@ -313,7 +313,7 @@ __device__ __forceinline__ int maximum_place(int reader)
 // NT threads, from the maxima of the groups of pieces that R readers took.
 template <class T, int NT, int R>
 __device__ void find_best(Finder& s, const T* tops, uint64_t* keys, const Row<T>& row, int n, int lo, int hi,
-                          int per_group, int groups, int t, int edge, float edge_value)
+                          int per_group, int groups, int t, int edge, float edge_value, bool masked_too)
 {
     constexpr int kN = Piece<T>::kN, kNTWarps = NT / 32;
     const int lane = t & 31, warp = t >> 5;
@@ -360,6 +360,9 @@ __device__ void find_best(Finder& s, const T* tops, uint64_t* keys, const Row<T>
     // compared as values: NaN never reaches the level, unless that is 0 and takes everything
     const float level_value = value_of(level);
     const bool any = level == 0u;
+    // fewer than n threads with anything but masked values: those above are looked for at once (64 x 8 rows of 131072
+    // fp32, one in twenty masked but for a value: TAG us, TAG when the masked ones were counted first)
+    const bool masked = level_value == -INFINITY;
     // the maxima that reach it, listed warp by warp
     static_assert(kMaxima / NT <= 32, "a bit per maximum of a thread");
     uint32_t hits = 0;
@@ -368,7 +371,7 @@ __device__ void find_best(Finder& s, const T* tops, uint64_t* keys, const Row<T>
         maxima(g, x);
         uint32_t some = 0;
 #pragma unroll
-        for (int c = 0; c < kPer; ++c) some |= (any || x[c] >= level_value) ? 1u << c : 0u;
+        for (int c = 0; c < kPer; ++c) some |= (any || (masked ? x[c] > level_value : x[c] >= level_value)) ? 1u << c : 0u;
         hits |= some << (g * kPer);
     }
     const int hit_count = __popc(hits);
@@ -388,7 +391,7 @@ __device__ void find_best(Finder& s, const T* tops, uint64_t* keys, const Row<T>
     sync_finders<NT>();
     const int entries = s.entries;
     // (one more pass, for the values above the level alone, when those at it are too many to rank)
-    int strict = 0;
+    int strict = masked ? 1 : 0;
     for (;; ++strict) {
         auto reaches = [&](float x) { return any || (strict ? x > level_value : x >= level_value); };
         // the entries' pieces, one per thread and step (a batch's to neighbours), four steps' loads in flight
@@ -444,7 +447,7 @@ __device__ void find_best(Finder& s, const T* tops, uint64_t* keys, const Row<T>
         sync_finders<NT>();
         // fewer than n: the values at the level when those above it alone were ranked, then (level = that of
         // -inf) the NaNs, each in the order of their indices
-        int have = found;
+        int have = masked && !masked_too ? n : found;
         for (int pass = strict ? 0 : 1; pass < 2 && have < n; ++pass) {
             const uint32_t want = pass == 0 ? level : 0u;
             if (pass == 1 && level == 0u) break;   // they were ranked with the rest
@@ -674,7 +677,7 @@ __global__ void __launch_bounds__(NT, blocks_of(NT)) token_logprobs_kernel(const
     if (lane == 0) s.stats[warp] = st;
     if (kTop) {
         const int groups = per_group ? (batches + per_group - 1) / per_group : 0;
-        find_best<T, NT, NT>(s.f, s.top, s.keys, row, a.n_top, lo, hi, per_group, groups, t, edge, edge_value);
+        find_best<T, NT, NT>(s.f, s.top, s.keys, row, a.n_top, lo, hi, per_group, groups, t, edge, edge_value, a.stats == nullptr);
     }
     if (a.split > 1)
         cluster_sync_all();
@@ -756,7 +759,7 @@ __global__ void __launch_bounds__(kReaders + kFinishers, kStreamBlocks) token_lo
             const int token = a.logprob ? given_token(a, r) : -1;
             const float given = token >= 0 ? static_cast<float>(row.x[token]) : 0.0f;
             bar_sync(kBarFull + buffer, kAll);
-            find_best<T, kFinishers, kReaders>(s.f, s.top[buffer], s.keys, row, a.n_top, 0, row.pieces, per_group, groups, t, edge, edge_value);
+            find_best<T, kFinishers, kReaders>(s.f, s.top[buffer], s.keys, row, a.n_top, 0, row.pieces, per_group, groups, t, edge, edge_value, a.stats == nullptr);
             sync_finders<kFinishers>();
             if (t < 32) {
                 Stats all = lane < kReaders / 32 ? s.stats[buffer][lane] : Stats{-INFINITY, 0.0f, 0.0f};

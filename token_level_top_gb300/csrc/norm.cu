@@ -407,6 +407,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) rms_norm_weight_sum_kernel(con
                                                                            float* __restrict__ dw)
 {
     __shared__ float s_sum[kSumWarps][32];
+    wait_for_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float v = 0.0f;
     if (c < cols)
@@ -508,8 +509,10 @@ cudaError_t launch_rms_norm_backward(NormGradArgs a, cudaStream_t s)
         if (a.dy_f32) return backward<__nv_bfloat16, float, kVec, W, P>(a, s);
         return backward<__nv_bfloat16, __nv_bfloat16, kVec, W, P>(a, s);
     });
-    if (a.dweight) rms_norm_weight_sum_kernel<<<(a.cols + 31) / 32, 32 * kSumWarps, 0, s>>>(a.parts, grid, a.cols, a.dweight);
-    return cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !a.dweight) return e;
+    return launch_after(rms_norm_weight_sum_kernel, dim3(static_cast<unsigned>((a.cols + 31) / 32)), 32 * kSumWarps, 0, s, a.parts, grid,
+                        a.cols, a.dweight);
 }
 
 }  // namespace moe
