@@ -577,7 +577,7 @@ bool encode_cache_map(CUtensorMap* tm, const void* ptr, bool codes, int head_dim
         if (!one && (strides[i] <= 0 || strides[i] >= 1LL << 40)) return false;
         gstride[i] = one ? 16 : static_cast<cuuint64_t>(strides[i]);
     }
-    cuuint32_t box[4] = {codes ? static_cast<cuuint32_t>(head_dim) : 64u, static_cast<cuuint32_t>(rows), 1, 1};
+    cuuint32_t box[4] = {codes ? static_cast<cuuint32_t>(std::min(head_dim, 128)) : 64u, static_cast<cuuint32_t>(rows), 1, 1};
     cuuint32_t estride[4] = {1, 1, 1, 1};
     return enc(tm, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), gdim, gstride,
                box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,

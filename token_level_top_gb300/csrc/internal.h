@@ -321,7 +321,7 @@ size_t paged_attention_ws_bytes(int head_dim);   // 0: unsupported head_dim
 cudaError_t launch_paged_attention(const AttentionArgs& a, int head_dim, bool e4m3, cudaStream_t s);
 
 // 4-D map (value, token of a page, head, page) of one side of a paged cache, box [1, 1, rows, 64 values] of bf16 with the
-// 128-byte swizzle, or [1, 1, rows, head_dim] of e4m3 codes without one.  False where TMA cannot take such a layout.
+// 128-byte swizzle, or [1, 1, rows, up to 128] of e4m3 codes without one.  False where TMA cannot take such a layout.
 bool encode_cache_map(CUtensorMap* tm, const void* ptr, bool codes, int head_dim, int page_size, int heads, int pages,
                       long long token_bytes, long long head_bytes, long long page_bytes, int rows);
 

@@ -31,6 +31,7 @@
 // infinities in shared memory, since 0 times them would reach every row, and the rows
 // that do see them get them added at the end.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -40,6 +41,10 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;
+// e4m3: weights are held times 2^6 (at most 2^14), so that f16 keeps those 2^-30 of the maximum's
+constexpr float kShift = 6.0f;
+// exponents of a tile's rows within this many of the largest: the rows go in relative to it (their bits are f16's then)
+constexpr int kNarrow = 14;
 constexpr float kNone = -3.402823466e38f;   // a maximum of nothing: finite, so that differences of two are
 constexpr int kRowsTile = 128, kKeys = 64;
 constexpr int kPanel = kKeys * 128;         // bytes of 64 values of a tile's 64 rows
@@ -53,16 +58,13 @@ struct Shape {
     static constexpr int kCtas = D <= 128 ? 2 : 1;                        // blocks per SM
     static constexpr int kTile = kPanel * D / 64;                         // bytes of a key or value tile
     static constexpr int kQ = kRowsTile * D * 2;
-    static constexpr int kBars = 640;
+    static constexpr int kBars = kE4m3 && D == 64 ? 1280 : 1024;
     static constexpr int kShare = std::min(233472 / kCtas - 1024, 232448);
-    // a ring of slots for tiles; e4m3 tiles have half of the room as they come in, in a ring of their own
-    static constexpr int kRaw = kE4m3 ? kKeys * D : 0, kRoom = kShare - kBars - kQ;
-    static constexpr int kSlots = kE4m3 ? (D == 64 ? 6 : 3) : std::min(kRoom / kTile, 12);
-    static constexpr int kRaws = kE4m3 ? (kRoom - kSlots * kTile) / kRaw : 0;
-    static constexpr int kSmem = kQ + kSlots * kTile + kRaws * kRaw + kBars;
+    static constexpr int kSlots = std::min((kShare - kBars - kQ) / kTile, kE4m3 ? 10 : 12);   // the ring of tiles
+    static constexpr int kSmem = kQ + kSlots * kTile + kBars;
     static constexpr int kCols = D <= 128 ? 256 : 512;                    // TMEM columns: O, then two tiles of scores
-    static constexpr int kPart = kRowsTile * (D + 2);                     // floats of a part
-    static_assert(kSlots >= 3 && kSmem <= kShare && D + 2 * kKeys <= kCols, "room");
+    static constexpr int kPart = kRowsTile * (D + 4);                     // floats of a part: O, then maximum, sum and O's maximum
+    static_assert(kSlots >= 4 && kSmem <= kShare && D + 2 * kKeys <= kCols, "room");
 };
 
 struct Header {   // of the item that begins in a block's run and does not end there
@@ -74,6 +76,28 @@ __device__ __forceinline__ float exp2_fast(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Two floats of a packed instruction, each rounded as a single one's.
+struct Pair {
+    float x, y;
+};
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)
+{
+    Pair r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b)
+{
+    Pair r;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
 }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
@@ -94,6 +118,23 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "%16};" ::"r"(taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// 16 columns, there when it returns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -196,16 +237,49 @@ __device__ __forceinline__ uint32_t any_odd(uint4 v) { return odd_bits(v.x) | od
 // 2^(byte - 127); byte 0 is a subnormal.
 __device__ __forceinline__ float pow2_of_byte(uint32_t b) { return __uint_as_float(b ? b << 23 : 0x00400000u); }
 
-// Four e4m3 codes times a power of two, as two bf16 pairs: exact.
-__device__ __forceinline__ void bf16_of_codes(uint32_t w, float scale, uint32_t& lo, uint32_t& hi)
+// The same of f16 values.
+__device__ __forceinline__ uint32_t odd_bits_f16(uint32_t w) { return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u; }
+__device__ __forceinline__ uint32_t without_odd_f16(uint32_t w) { return w & ~((odd_bits_f16(w) >> 15) * 0xffffu); }
+
+// Four e4m3 codes as two f16 pairs, times a power of two: exact while the products are f16 values.
+__device__ __forceinline__ uint32_t times(uint32_t pair, uint32_t scale)
+{
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&pair), *reinterpret_cast<const __half2*>(&scale));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void f16_of_codes(uint32_t w, uint32_t scale, uint32_t& lo, uint32_t& hi)
 {
     uint32_t a, b;
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
         : "=r"(a), "=r"(b)
         : "r"(w));
-    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a)), y = __half22float2(*reinterpret_cast<const __half2*>(&b));
-    lo = pack_bf16x2(x.x * scale, x.y * scale);
-    hi = pack_bf16x2(y.x * scale, y.y * scale);
+    lo = times(a, scale);
+    hi = times(b, scale);
+}
+// Where byte c of row r of an e4m3 tile lies in its slot until it is turned into f16 in place.  A row's codes lie where the
+// second half of each 128 f16 values of that row goes (D = 64: where rows go whose codes are read by then), so rows may
+// be read and written in order.
+template <int D>
+__device__ __forceinline__ uint32_t raw_at(uint32_t slot, int r, int c)
+{
+    return D == 64 ? slot + kPanel / 2 + r * 64 + c : slot + (c >> 7) * (2 * kPanel) + kPanel + r * 128 + (c & 127);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// e4m3: a row of q goes in as f16 times 2^-e, its largest magnitude (bits `top`, sign cleared) at 2^13 and above.
+__device__ __forceinline__ int row_exponent(uint32_t top)
+{
+    const int e = static_cast<int>(top >> 7);
+    return e == 255 ? 0 : max(e - 127 - 13, -100);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }   // -126 .. 127
+__device__ __forceinline__ uint32_t largest(uint32_t top, uint32_t w)
+{
+    return max(top, max(w & 0x7fffu, w >> 16 & 0x7fffu));
 }
 
 __device__ __forceinline__ long long quotient(long long a, long long b)
@@ -258,6 +332,80 @@ __device__ __forceinline__ void next_item(const TreeArgs& a, Item& w)
     } while (w.n == 0);
 }
 
+// ---------------------------------------------------------------- e4m3 tiles whose rows' exponents lie far apart
+// Each key's score is scaled by its own exponent, its weight by its value row's; the sum of the softmax takes an exponential
+// of its own, since against the maximum of score + exponent its terms could be anything.  Rare, so it is kept out of the way of
+// the usual path: the scores are read from TMEM again, 16 at a time.
+struct Apart {
+    uint32_t kb[2], vb[2];   // exponent bytes of the keys `lane` and `lane + 32`
+    __device__ __forceinline__ Apart(const TreeArgs& a, const int32_t* table, int len, int k0, int hk, uint32_t info)
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int key = k0 + 32 * h + lane, pg = key / a.page_size;
+            const int e = key < len ? __ldg(table + pg) : -1;
+            const bool there = e >= 0 && e < a.n_pages;
+            const long long at = there ? e * a.exp_page_stride + (key - pg * a.page_size) * a.exp_token_stride + hk * a.exp_head_stride : 0;
+            kb[h] = there && (info & 1u << 16) ? __ldg(a.k_exp + at) : info & 255u;
+            vb[h] = there && (info & 1u << 17) ? __ldg(a.v_exp + at) : info >> 8 & 255u;
+        }
+    }
+    __device__ __forceinline__ float score(uint32_t s, int j, uint64_t keep, float c_row) const
+    {
+        const float f = fminf(fmaxf(c_row * pow2_of_byte(__shfl_sync(0xffffffffu, j < 32 ? kb[0] : kb[1], j & 31)), 1e-37f), 3e38f);
+        return keep >> j & 1 ? __uint_as_float(s) * f : -INFINITY;
+    }
+    __device__ __forceinline__ float exponent(int j) const
+    {
+        return static_cast<float>(static_cast<int>(__shfl_sync(0xffffffffu, j < 32 ? vb[0] : vb[1], j & 31)) - 127);
+    }
+};
+// The largest score, and score + exponent, of the keys that the row sees.
+__device__ __noinline__ float2 apart_maxima(const TreeArgs& a, uint32_t at, uint64_t keep, const int32_t* table, int len, int k0, int hk, uint32_t info,
+                                            float c_row)
+{
+    const Apart e(a, table, len, k0, hk, info);
+    float top = -INFINITY, top_out = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < kKeys; c += 16) {
+        uint32_t x[16];
+        tmem_ld16(at + c, x);
+        for (int j = 0; j < 16; ++j) {
+            const float v = e.score(x[j], c + j, keep, c_row);
+            top = fmaxf(top, v);
+            top_out = fmaxf(top_out, v + e.exponent(c + j));
+        }
+    }
+    return make_float2(top, top_out);
+}
+// Writes the weights over the scores; their sum.
+__device__ __noinline__ float apart_weights(const TreeArgs& a, uint32_t at, uint64_t keep, const int32_t* table, int len, int k0, int hk, uint32_t info,
+                                            float c_row, float m, float m_out)
+{
+    const Apart e(a, table, len, k0, hk, info);
+    float sum = 0.0f;
+    uint32_t lo_part[32];   // (their columns hold scores until the end)
+#pragma unroll
+    for (int c = 0; c < kKeys; c += 16) {
+        uint32_t x[16], hi_part[8];
+        tmem_ld16(at + c, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float s0 = e.score(x[2 * j], c + 2 * j, keep, c_row), s1 = e.score(x[2 * j + 1], c + 2 * j + 1, keep, c_row);
+            sum += exp2_fast(s0 - m) + exp2_fast(s1 - m);
+            const float p0 = exp2_fast(s0 + (e.exponent(c + 2 * j) + kShift - m_out));
+            const float p1 = exp2_fast(s1 + (e.exponent(c + 2 * j + 1) + kShift - m_out));
+            hi_part[j] = pack_f16x2(p0, p1);
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi_part[j]));
+            lo_part[c / 2 + j] = pack_f16x2(p0 - back.x, p1 - back.y);
+        }
+        tmem_st8(at + c / 2, hi_part);
+    }
+    tmem_st32(at + 32, lo_part);
+    return sum;
+}
+
 // ---------------------------------------------------------------- the main kernel
 
 struct Start {
@@ -267,24 +415,30 @@ struct Start {
 
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
-    tree_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const TreeArgs a)
+    tree_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                          const __grid_constant__ TreeArgs a)
 {
     using S = Shape<D, kE4m3>;
-    constexpr int kSlots = S::kSlots, kRaws = S::kRaws;
+    constexpr int kSlots = S::kSlots;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char* const s_q = smem;
     unsigned char* const s_ring = smem + S::kQ;
-    uint64_t* const bars = reinterpret_cast<uint64_t*>(s_ring + kSlots * S::kTile + kRaws * S::kRaw);
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(s_ring + kSlots * S::kTile);
     // A tile's scores are there (two buffers), its weights, its product with the values done; an item's last product
-    // done, its output read; its rows of q there, and no longer read.
+    // done, its output read; its rows of q there, and no longer read.  e4m3: a slot's codes there; bf16: a tile that the
+    // warp which copies it looks at.
+    constexpr int kInfos = 16;
     constexpr int kFull = 0, kEmpty = kSlots, kSFull = 2 * kSlots, kPFull = kSFull + 2, kODone = kPFull + 2, kOFree = kODone + 1,
-                  kQFull = kOFree + 1, kQEmpty = kQFull + 1, kItemDone = kQEmpty + 1, kRawFull = kItemDone + 1, kRawEmpty = kRawFull + (kE4m3 ? kRaws : kCopyWarps),
-                  kCount = kRawEmpty + kRaws;
-    static_assert(kCount * 8 + static_cast<int>(sizeof(Start)) + 16 * 8 + 16 <= S::kBars, "room for the barriers");
+                  kQFull = kOFree + 1, kQEmpty = kQFull + 1, kItemDone = kQEmpty + 1, kRawFull = kItemDone + 1, kCount = kRawFull + (kE4m3 ? kSlots : kCopyWarps);
+    static_assert(kCount * 8 + static_cast<int>(sizeof(Start)) + 16 * 8 + 8 + kInfos * 4 + (kE4m3 ? kSlots * kKeys : 0) <= S::kBars, "room for the barriers");
     Start* const s_start = reinterpret_cast<Start*>(bars + kCount);
     long long* const s_scan = reinterpret_cast<long long*>(s_start + 1);
     volatile uint32_t* const s_tmem = reinterpret_cast<volatile uint32_t*>(s_scan + 16);
     volatile int* const s_odd = reinterpret_cast<volatile int*>(s_tmem + 1);   // NaN or infinities were taken from value rows
+    // e4m3: of tile t at t % kInfos: the exponent bytes of its keys and values, bits 16 and 17: each row's own.  And of the
+    // slots' rows the exponent bytes.
+    volatile uint32_t* const s_info = s_tmem + 2;
+    volatile uint8_t* const s_exp = reinterpret_cast<volatile uint8_t*>(const_cast<uint32_t*>(s_info) + kInfos);
     auto bar = [&](int i) { return smem_u32(bars + i); };
 
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // (the same in all lanes)
@@ -354,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(bar(kFull + i), 32);
+            mbar_init(bar(kFull + i), kE4m3 || a.box_rows > 0 ? 1 : 32);
             mbar_init(bar(kEmpty + i), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -366,8 +520,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
         mbar_init(bar(kQFull), 32 * kCopyWarps);
         mbar_init(bar(kQEmpty), 1);
         mbar_init(bar(kItemDone), 1);
-        for (int i = 0; i < (kE4m3 ? kRaws : kCopyWarps); ++i) mbar_init(bar(kRawFull + i), 32);
-        for (int i = 0; i < kRaws; ++i) mbar_init(bar(kRawEmpty + i), 1);
+        for (int i = 0; i < (kE4m3 ? kSlots : kCopyWarps); ++i) mbar_init(bar(kRawFull + i), a.box_rows > 0 ? 1 : 32);
         mbar_fence_init();
         *s_odd = 0;
     }
@@ -416,26 +569,32 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     entry[h] = n < n_end && key < it.len ? __ldg(table + page_of(key)) : -1;
                 }
             };
-            // A tile's rows to dst: boxes, or pieces of 16 bytes (zeros where no key is), kRowBytes each; `full` gets 32 arrivals.
-            auto copy_tile = [&](int n, const int (&pages)[2], uint32_t dst, uint32_t full) {
+            // Slot n's rows to its place (e4m3: and those of the next slot, the same keys' values, to theirs): boxes, or pieces of
+            // 16 bytes (zeros where no key is).  Counted on full[0] (and full[1]).
+            constexpr int kSides = kE4m3 ? 2 : 1;
+            auto copy_tile = [&](int n, const int (&pages)[2], const uint32_t (&dst)[kSides], const uint32_t (&full)[kSides]) {
                 constexpr int kRowBytes = kE4m3 ? D : 2 * D;
                 const int k0 = first_key(n), live = min(kKeys, it.len - k0);
                 const bool bad = (lane < live && static_cast<unsigned>(pages[0]) >= static_cast<unsigned>(a.n_pages)) ||
                                  (lane + 32 < live && static_cast<unsigned>(pages[1]) >= static_cast<unsigned>(a.n_pages));
                 if (a.box_rows > 0 && !uniform(bad)) {
-                    const int boxes = (live + a.box_rows - 1) / a.box_rows;
+                    const uint32_t bytes = static_cast<uint32_t>((live + a.box_rows - 1) / a.box_rows * a.box_rows * kRowBytes);
                     if (lane == 0)
-                        mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * a.box_rows * kRowBytes));
-                    else
-                        mbar_arrive(full);
-                    __syncwarp();
-                    for (int j = 0; uniform(j < boxes); ++j) {
-                        const int r = j * a.box_rows, key = k0 + r;
-                        const int page = __shfl_sync(0xffffffffu, r < 32 ? pages[0] : pages[1], r & 31);
-                        const int token = key - page_of(key) * a.page_size;
 #pragma unroll
-                        for (int x = 0; x < (kE4m3 ? 1 : D / 64); ++x)
-                            copy_box_if(leader, dst + x * kPanel + r * (kE4m3 ? D : 128), n & 1 ? &map_v : &map_k, 64 * x, token, hk, page, full);
+                        for (int v = 0; v < kSides; ++v) mbar_arrive_expect_tx(full[v], bytes);
+                    // lane j: where box j begins (at most eight of them)
+                    const int first = min(lane * a.box_rows, kKeys - 1), at_page = __shfl_sync(0xffffffffu, pages[0], first & 31),
+                              at_page1 = __shfl_sync(0xffffffffu, pages[1], first & 31);
+                    const int box_page = first < 32 ? at_page : at_page1, box_token = k0 + first - page_of(k0 + first) * a.page_size;
+#pragma unroll 1
+                    for (int j = 0, r = 0; uniform(r < live); ++j, r += a.box_rows) {
+                        const int page = __shfl_sync(0xffffffffu, box_page, j), token = __shfl_sync(0xffffffffu, box_token, j);
+#pragma unroll
+                        for (int v = 0; v < kSides; ++v)
+#pragma unroll
+                            for (int x = 0; x < (kE4m3 ? (D + 127) / 128 : D / 64); ++x)
+                                copy_box_if(leader, kE4m3 ? raw_at<D>(dst[v], r, 128 * x) : dst[v] + x * kPanel + r * 128,
+                                            (kE4m3 ? v : n & 1) ? &map_v : &map_k, (kE4m3 ? 128 : 64) * x, token, hk, page, full[v]);
                     }
                 } else {
                     long long place[2];
@@ -447,17 +606,29 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     }
                     constexpr int kPieces = kRowBytes / 16, kStep = 32 / kPieces, kCount = kKeys * kPieces / 32;
                     const int piece = lane % kPieces, r0 = lane / kPieces;
-                    const char* const from = (n & 1 ? a.v : a.k) + hk * a.head_bytes + 16 * piece;
-#pragma unroll 8
-                    for (int i = 0; i < kCount; ++i) {
-                        const int r = i * kStep + r0;
-                        const long long p0 = __shfl_sync(0xffffffffu, place[0], r & 31), p1 = __shfl_sync(0xffffffffu, place[1], r & 31);
-                        const long long at = r < 32 ? p0 : p1;
-                        copy_async_or_zeros(kE4m3 ? dst + r * D + 16 * piece
-                                                  : dst + (piece >> 3) * kPanel + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
-                                            from + (at < 0 ? 0 : at), at >= 0);
+#pragma unroll 1
+                    for (int v = 0; v < kSides; ++v) {
+                        const char* const from = ((kE4m3 ? v : n & 1) ? a.v : a.k) + hk * a.head_bytes + 16 * piece;
+                        const uint32_t to = kE4m3 && v ? dst[kSides - 1] : dst[0];
+#pragma unroll 4
+                        for (int i = 0; i < kCount; ++i) {
+                            const int r = i * kStep + r0;
+                            const long long p0 = __shfl_sync(0xffffffffu, place[0], r & 31), p1 = __shfl_sync(0xffffffffu, place[1], r & 31);
+                            const long long at = r < 32 ? p0 : p1;
+                            copy_async_or_zeros(kE4m3 ? raw_at<D>(to, r, 16 * piece)
+                                                      : to + (piece >> 3) * kPanel + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
+                                                from + (at < 0 ? 0 : at), at >= 0);
+                        }
                     }
-                    copy_arrive(full);
+                    if (a.box_rows > 0) {   // (a page out of range: the barriers count one arrival)
+                        copy_wait_all();
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                    }
+                    if (a.box_rows == 0 || lane == 0)
+#pragma unroll
+                        for (int v = 0; v < kSides; ++v) copy_arrive(full[v]);
+                    __syncwarp();
                 }
             };
             // ---- the rows of q, eight at a time; asked for behind the first tile
@@ -480,8 +651,25 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                                                                             (hk * group + (row - t * group)) * a.q_head_stride : 0) + 8 * piece, live);
                     }
                 }
-                if (a.scale >= 0.0f) {
+                if (!kE4m3 && a.scale >= 0.0f) {
                     copy_arrive(bar(kQFull));
+                } else if (kE4m3) {
+                    copy_wait_all();
+#pragma unroll 1
+                    for (int r1 = 8 * mine_of; r1 < kRowsTile; r1 += 8 * kCopyWarps)
+#pragma unroll
+                        for (int i = 0; i < kPieces / 4; ++i) {
+                            const uint32_t to = at(r1 + (i * 32 + lane) / kPieces, (i * 32 + lane) % kPieces);
+                            const uint4 x = lds128(to);
+                            uint32_t top = largest(largest(largest(largest(0, x.x), x.y), x.z), x.w);
+#pragma unroll
+                            for (int off = kPieces / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+                            const float f = (a.scale < 0.0f ? -1.0f : 1.0f) * pow2(-row_exponent(top));
+                            auto half = [&](uint32_t w) { return pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f); };
+                            sts128(to, make_uint4(half(x.x), half(x.y), half(x.z), half(x.w)));
+                        }
+                    fence_proxy_async_shared();
+                    mbar_arrive(bar(kQFull));
                 } else {
                     copy_wait_all();
 #pragma unroll 1
@@ -518,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     if (!wait_for(kEmpty + n % kSlots, ((n / kSlots) & 1) ^ 1)) break;
                     const uint32_t slot = smem_u32(s_ring) + (n % kSlots) * S::kTile;
                     const bool look = uniform(mixed(n));
-                    copy_tile(n, pages, slot, look ? bar(kRawFull + mine_of) : bar(kFull + n % kSlots));
+                    copy_tile(n, pages, {slot}, {look ? bar(kRawFull + mine_of) : bar(kFull + n % kSlots)});
                     if (!q_there && !copy_q()) break;
                     q_there = true;
                     if (!look) continue;
@@ -538,80 +726,116 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     }
                     if (odd) *s_odd = 1;
                     fence_proxy_async_shared();
-                    mbar_arrive(bar(kFull + n % kSlots));
+                    __syncwarp();
+                    if (a.box_rows == 0 || lane == 0) mbar_arrive(bar(kFull + n % kSlots));
                     __syncwarp();
                 }
                 if (ok && !q_there && !copy_q()) break;
             } else if (mine_of == 0) {
-                int n = n0;
-                look_up(n);
-                bool q_there = false;
-                for (; uniform(n < n_end); n += 2) {   // keys and values of a tile lie in the same pages
-                    const int pages[2] = {entry[0], entry[1]};
-                    look_up(n + 2);
-#pragma unroll 1
-                    for (int v = 0; v < 2; ++v) {
-                        const int m = n + v;
-                        if (!wait_for(kRawEmpty + m % kRaws, ((m / kRaws) & 1) ^ 1)) break;
-                        copy_tile(m, pages, smem_u32(s_ring) + kSlots * S::kTile + (m % kRaws) * S::kRaw, bar(kRawFull + m % kRaws));
-                    }
-                    if (!ok || (!q_there && !copy_q())) break;
-                    q_there = true;
-                }
-            } else {
-                if (!copy_q()) break;
-                constexpr int kPieces = D / 16, kStep = 32 / kPieces, kCount = kKeys * kPieces / 32;   // pieces of 16 codes
-                const int piece = lane % kPieces, r0 = lane / kPieces, v = mine_of - 1;
-                const uint8_t* const from_exp = (v ? a.v_exp : a.k_exp) + hk * a.exp_head_stride;
-                uint32_t next[2];   // exponent bytes of this lane's two keys
+                // exponent bytes of this lane's two keys, keys' and values' (256: no such key), of the tile after this one
+                uint32_t next[2][2];
                 auto exponents = [&](int n) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int key = first_key(n) + 32 * h + lane, at = key - page_of(key) * a.page_size;
-                        next[h] = entry[h] >= 0 && entry[h] < a.n_pages
-                                      ? __ldg(from_exp + entry[h] * a.exp_page_stride + at * a.exp_token_stride) : 127u;
+                        const bool there = entry[h] >= 0 && entry[h] < a.n_pages;
+                        const long long place = there ? entry[h] * a.exp_page_stride + at * a.exp_token_stride + hk * a.exp_head_stride : 0;
+                        next[0][h] = there ? __ldg(a.k_exp + place) : 256u;
+                        next[1][h] = there ? __ldg(a.v_exp + place) : 256u;
                     }
                 };
-                look_up(n0 + v);
-                exponents(n0 + v);
-                look_up(n0 + v + 2);
-                for (int n = n0 + v; uniform(n < n_end); n += 2) {
-                    const uint32_t exps[2] = {next[0], next[1]};
+                // of a tile: its rows' largest exponent byte (127 without rows); bit 8: not all are near it
+                auto reference = [&](const uint32_t (&e)[2]) {
+                    const uint32_t top = __reduce_max_sync(0xffffffffu, max(e[0] == 256u ? 0u : e[0] + 1, e[1] == 256u ? 0u : e[1] + 1));
+                    const uint32_t least = __reduce_min_sync(0xffffffffu, min(e[0], e[1]));
+                    return top == 0 ? 127u : (top - 1 - least <= static_cast<uint32_t>(kNarrow) ? top - 1 : top - 1 | 256u);
+                };
+                // (what a tile needs is asked for a tile and two tiles before)
+                int n = n0, pages[2];
+                look_up(n);
+                pages[0] = entry[0], pages[1] = entry[1];
+                exponents(n);
+                look_up(n + 2);
+                bool q_there = false;
+                for (; uniform(n < n_end); n += 2) {   // keys and values of a tile lie in the same pages
+                    const uint32_t exps[2][2] = {{next[0][0], next[0][1]}, {next[1][0], next[1][1]}};
                     exponents(n + 2);
+                    const int following[2] = {entry[0], entry[1]};
                     look_up(n + 4);
+                    const uint32_t ref_k = reference(exps[0]), ref_v = reference(exps[1]);
+                    const int slot_k = n % kSlots, slot_v = (n + 1) % kSlots;
+                    if (!wait_for(kEmpty + slot_k, ((n / kSlots) & 1) ^ 1)) break;
+                    if (!wait_for(kEmpty + slot_v, (((n + 1) / kSlots) & 1) ^ 1)) break;
+                    s_exp[slot_k * kKeys + lane] = static_cast<uint8_t>(exps[0][0]);
+                    s_exp[slot_k * kKeys + 32 + lane] = static_cast<uint8_t>(exps[0][1]);
+                    s_exp[slot_v * kKeys + lane] = static_cast<uint8_t>(exps[1][0]);
+                    s_exp[slot_v * kKeys + 32 + lane] = static_cast<uint8_t>(exps[1][1]);
+                    if (lane == 0)   // (tiles here and in the softmax are at most 8 apart)
+                        s_info[(n >> 1) % kInfos] = (ref_k & 255u) | (ref_v & 255u) << 8 | (ref_k >> 8) << 16 | (ref_v >> 8) << 17;
+                    __syncwarp();
+                    copy_tile(n, pages, {smem_u32(s_ring) + slot_k * S::kTile, smem_u32(s_ring) + slot_v * S::kTile},
+                              {bar(kRawFull + slot_k), bar(kRawFull + slot_v)});
+                    if (!ok || (!q_there && !copy_q())) break;
+                    q_there = true;
+                    pages[0] = following[0], pages[1] = following[1];
+                }
+            } else {
+                if (!copy_q()) break;
+                constexpr int kPieces = D / 16, kStep = 32 / kPieces, kCount = kKeys * kPieces / 32;   // pieces of 16 codes
+                constexpr int kBatch = 4;
+                const int piece = lane % kPieces, r0 = lane / kPieces, v = mine_of - 1;
+                for (int n = n0 + v; uniform(n < n_end); n += 2) {
                     const bool look = uniform(mixed(n));
                     const int live = min(kKeys, it.len - first_key(n));
-                    if (!wait_for(kEmpty + n % kSlots, ((n / kSlots) & 1) ^ 1)) break;
-                    if (!wait_for(kRawFull + n % kRaws, (n / kRaws) & 1)) break;
-                    const uint32_t raw = smem_u32(s_ring) + kSlots * S::kTile + (n % kRaws) * S::kRaw + r0 * D + 16 * piece;
-                    const uint32_t slot = smem_u32(s_ring) + (n % kSlots) * S::kTile + (piece >> 2) * kPanel;
+                    const int slot = n % kSlots;
+                    if (!wait_for(kRawFull + slot, (n / kSlots) & 1)) break;
+                    // f16 2^(e - that of the tile), or 1 where the softmax takes each row's own exponent
+                    const uint32_t info = s_info[(n >> 1) % kInfos] >> (8 * v);
+                    uint32_t mine[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int e = s_exp[slot * kKeys + 32 * h + lane], d = e - static_cast<int>(info & 255u);
+                        const float f = (info >> (16 - 7 * v) & 1u) != 0 || lane + 32 * h >= live ? 1.0f : pow2(max(d, -kNarrow));
+                        mine[h] = pack_f16x2(f, f);
+                    }
+                    const uint32_t at = smem_u32(s_ring) + slot * S::kTile, to = at + (piece >> 2) * kPanel;
                     uint32_t odd = 0;
-#pragma unroll 4
-                    for (int i = 0; i < kCount; ++i) {
-                        const int r = i * kStep + r0;
-                        uint4 w = lds128(raw + i * kStep * D);
-                        if (r >= live) w = make_uint4(0, 0, 0, 0);
-                        const uint32_t e0 = __shfl_sync(0xffffffffu, exps[0], r & 31), e1 = __shfl_sync(0xffffffffu, exps[1], r & 31);
-                        const float scale = pow2_of_byte(r < 32 ? e0 : e1);
-                        uint4 x, y;
-                        bf16_of_codes(w.x, scale, x.x, x.y);
-                        bf16_of_codes(w.y, scale, x.z, x.w);
-                        bf16_of_codes(w.z, scale, y.x, y.y);
-                        bf16_of_codes(w.w, scale, y.z, y.w);
-                        if (look && (any_odd(x) | any_odd(y))) {
-                            odd = 1;
-                            x = make_uint4(without_odd(x.x), without_odd(x.y), without_odd(x.z), without_odd(x.w));
-                            y = make_uint4(without_odd(y.x), without_odd(y.y), without_odd(y.z), without_odd(y.w));
+#pragma unroll 1
+                    for (int i0 = 0; i0 < kCount; i0 += kBatch) {   // (rolled: the block's warps share one instruction cache)
+                        uint4 w[kBatch];
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) w[i] = lds128(raw_at<D>(at, (i0 + i) * kStep + r0, 16 * piece));
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) {
+                            const int r = (i0 + i) * kStep + r0;
+                            if (r >= live) w[i] = make_uint4(0, 0, 0, 0);
+                            const uint32_t scale = __shfl_sync(0xffffffffu, (i0 + i) * kStep < 32 ? mine[0] : mine[1], r & 31);
+                            uint4 x, y;
+                            f16_of_codes(w[i].x, scale, x.x, x.y);
+                            f16_of_codes(w[i].y, scale, x.z, x.w);
+                            f16_of_codes(w[i].z, scale, y.x, y.y);
+                            f16_of_codes(w[i].w, scale, y.z, y.w);
+                            if (look) {   // (a branch of its own: not on the usual way)
+                                const uint32_t any = odd_bits_f16(x.x) | odd_bits_f16(x.y) | odd_bits_f16(x.z) | odd_bits_f16(x.w) |
+                                                     odd_bits_f16(y.x) | odd_bits_f16(y.y) | odd_bits_f16(y.z) | odd_bits_f16(y.w);
+                                odd |= any;
+                                if (any) {
+                                    x = make_uint4(without_odd_f16(x.x), without_odd_f16(x.y), without_odd_f16(x.z), without_odd_f16(x.w));
+                                    y = make_uint4(without_odd_f16(y.x), without_odd_f16(y.y), without_odd_f16(y.z), without_odd_f16(y.w));
+                                }
+                            }
+                            // pieces 2 p and 2 p + 1 of the row, in the order that keeps a row's lanes in different banks
+                            const bool turn = (piece & 4) != 0;
+                            const int c = (2 * piece) & 7, c0 = turn ? c + 1 : c, c1 = turn ? c : c + 1;
+                            sts128(to + r * 128 + ((c0 ^ (r & 7)) << 4), turn ? y : x);
+                            sts128(to + r * 128 + ((c1 ^ (r & 7)) << 4), turn ? x : y);
                         }
-                        const int at = (2 * piece) & 7;
-                        sts128(slot + r * 128 + ((at ^ (r & 7)) << 4), x);
-                        sts128(slot + r * 128 + (((at + 1) ^ (r & 7)) << 4), y);
                     }
                     if (odd) *s_odd = 1;
                     fence_proxy_async_shared();
-                    mbar_arrive(bar(kFull + n % kSlots));
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kRawEmpty + n % kRaws));
+                    if (lane == 0) mbar_arrive(bar(kFull + slot));
                     __syncwarp();
                 }
             }
@@ -629,7 +853,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
         // ------------------------------------------------------------ products
         {
             const uint32_t leader = elected();
-            constexpr uint32_t kIdescS = idesc_bf16_f32(kRowsTile, kKeys), kIdescO = idesc_bf16_f32(kRowsTile, D) | (1u << 16);
+            // (f16 operands: format 0 for both)
+            constexpr uint32_t kF16 = kE4m3 ? ~(1u << 7 | 1u << 10) : ~0u;
+            constexpr uint32_t kIdescS = idesc_bf16_f32(kRowsTile, kKeys) & kF16, kIdescO = (idesc_bf16_f32(kRowsTile, D) | 1u << 16) & kF16;
             auto wait = [&](int i, uint32_t parity) {
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(i), parity, kSpinBudget));
                 return ok;
@@ -746,7 +972,22 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 }
                 return m;
             };
-            float m = kNone, l = 0.0f;
+            // e4m3: the scale of this row's scores, apart from the keys' exponent
+            float c_row = c;
+            if (kE4m3 && live) {
+                const uint4* const q = reinterpret_cast<const uint4*>(a.q + static_cast<long long>(it.row0 + t_row) * a.q_token_stride +
+                                                                      static_cast<long long>(head) * a.q_head_stride);
+                uint32_t bits = 0;
+#pragma unroll 8
+                for (int j = 0; j < D / 8; ++j) {
+                    const uint4 x = __ldg(q + j);
+                    bits = largest(largest(largest(largest(bits, x.x), x.y), x.z), x.w);
+                }
+                c_row = a.scale != 0.0f ? c * pow2(row_exponent(bits)) : c;
+            }
+            // The running maximum of the scores (to 2^kSlack) with the sum of the softmax against it; O is held against
+            // m_out, for e4m3 that of score + exponent of the value row, times 2^kShift.
+            float m = kNone, l = 0.0f, m_out = kNone;
             for (int i = 0; i < count; ++i) {
                 const int t = tiles + i, k0 = key_lo + i * kKeys;
                 if (!__all_sync(0xffffffffu, mbar_wait(bar(kSFull + (t & 1)), (t >> 1) & 1, kSpinBudget))) {
@@ -773,49 +1014,94 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                                 if (!(k >> j & 1u)) x[h][j] = 0xff800000u;
                         }
                     }
+                    // of the tile: exponents of the keys and of the values, the same for all rows as a rule
+                    uint32_t info = 0;
+                    float cs = c, ev = 0.0f;
+                    if (kE4m3) {
+                        info = s_info[t % kInfos];
+                        cs = fminf(fmaxf(c_row * pow2_of_byte(info & 255u), 1e-37f), 3e38f);   // (0 times -inf would be NaN)
+                        ev = static_cast<float>(static_cast<int>(info >> 8 & 255u) - 127);
+                    }
                     float top = -INFINITY;
 #pragma unroll
                     for (int j = 0; j < 32; ++j) top = fmaxf(top, fmaxf(__uint_as_float(x[0][j]), __uint_as_float(x[1][j])));
-                    top *= c;
-                    const bool raise = top > m + kSlack;
-                    if (__any_sync(0xffffffffu, raise)) {
-                        const float to = raise ? top : m, f = raise ? exp2_fast(m - to) : 1.0f;
-                        l *= f;
-                        m = to;
-                        if (i > 0) {
-                            if (!__all_sync(0xffffffffu, mbar_wait(bar(kODone), (t - 1) & 1, kSpinBudget))) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
+                    top *= cs;
+                    float top_out = top + ev;
+                    bool apart = false;   // each key with its own exponents, and the softmax's sum with an exponential of its own
+                    if (kE4m3) apart = uniform((info >> 16) != 0 || fmaxf(m_out, top_out) - fmaxf(m, top) - ev > 60.0f);
+                    uint64_t keep = ~0ULL;
+                    if (kE4m3 && apart) {
+                        if (bad || k0 < odd_from || k0 + kKeys > it.ctx) keep = sees(k0) & (bad ? resident(k0) : ~0ULL);
+                        const float2 tops = apart_maxima(a, at, keep, table, it.len, k0, hk, info, c_row);
+                        top = tops.x;
+                        top_out = tops.y;
+                    }
+                    bool raise = top > m + kSlack;
+                    float f_out = 1.0f;
+                    if (kE4m3) {
+                        if (raise) {
+                            l *= exp2_fast(m - top);
+                            m = top;
+                        }
+                        raise = top_out > m_out + kSlack;
+                        if (raise) {
+                            f_out = exp2_fast(m_out - top_out);
+                            m_out = top_out;
+                        }
+                    } else if (raise) {
+                        f_out = exp2_fast(m - top);
+                        l *= f_out;
+                        m = m_out = top;
+                    }
+                    if (uniform(raise) && i > 0) {
+                        if (!__all_sync(0xffffffffu, mbar_wait(bar(kODone), (t - 1) & 1, kSpinBudget))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
 #pragma unroll 1
-                            for (int d = 0; d < D; d += 32) {
-                                uint32_t o[32];
-                                tmem_ld32(quarter + d, o);
-                                tmem_ld_wait(o);
+                        for (int d = 0; d < D; d += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(quarter + d, o);
+                            tmem_ld_wait(o);
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                                tmem_st32(quarter + d, o);
+                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f_out);
+                            tmem_st32(quarter + d, o);
+                        }
+                    }
+                    if (kE4m3 && apart) {
+                        l += apart_weights(a, at, keep, table, it.len, k0, hk, info, c_row, m, m_out);
+                    } else {
+                        const float off = kE4m3 ? ev + kShift - m_out : -m;
+                        Pair sum = {0.0f, 0.0f};
+                        const Pair by = {cs, cs}, from = {off, off};
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {   // 32 keys: 16 columns of pairs
+                            uint32_t hi_part[16], lo_part[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                Pair p = fma2(Pair{__uint_as_float(x[h][2 * j]), __uint_as_float(x[h][2 * j + 1])}, by, from);
+                                p.x = exp2_fast(p.x);
+                                p.y = exp2_fast(p.y);
+                                sum = add2(sum, p);
+                                Pair minus;
+                                if constexpr (kE4m3) {
+                                    hi_part[j] = pack_f16x2(p.x, p.y);
+                                    const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi_part[j]));
+                                    minus = {-back.x, -back.y};
+                                } else {
+                                    hi_part[j] = pack_bf16x2(p.x, p.y);
+                                    // (signs flipped: one operation each with the shift and the mask)
+                                    minus = {__uint_as_float((hi_part[j] << 16) ^ 0x80000000u), __uint_as_float((hi_part[j] & 0xffff0000u) ^ 0x80000000u)};
+                                }
+                                const Pair rest = add2(p, minus);
+                                lo_part[j] = kE4m3 ? pack_f16x2(rest.x, rest.y) : pack_bf16x2(rest.x, rest.y);
                             }
+                            tmem_st16(at + 16 * h, hi_part);
+                            tmem_st16(at + 32 + 16 * h, lo_part);
                         }
+                        l += kE4m3 ? (sum.x + sum.y) * exp2_fast(-off - m) : sum.x + sum.y;
                     }
-                    float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {   // 32 keys: 16 columns of pairs
-                        uint32_t hi_part[16], lo_part[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float p0 = exp2_fast(fmaf(__uint_as_float(x[h][2 * j]), c, -m));
-                            const float p1 = exp2_fast(fmaf(__uint_as_float(x[h][2 * j + 1]), c, -m));
-                            sum[0] += p0;
-                            sum[1] += p1;
-                            hi_part[j] = pack_bf16x2(p0, p1);
-                            lo_part[j] = pack_bf16x2(p0 - __uint_as_float(hi_part[j] << 16), p1 - __uint_as_float(hi_part[j] & 0xffff0000u));
-                        }
-                        tmem_st16(at + 16 * h, hi_part);
-                        tmem_st16(at + 32 + 16 * h, lo_part);
-                    }
-                    l += sum[0] + sum[1];
                     tmem_st_wait();
                 }
                 tc_fence_before();
@@ -831,7 +1117,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 const int slot = 2 * blockIdx.x + (g0 == 0 ? 1 : 0);
                 float* const part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kTreeCtrlBytes + sizeof(Header) * kMaxBlocks) +
                                     static_cast<long long>(slot) * S::kPart;
-                const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : NAN);
+                // (what O is held against, as a power of two over the sum's)
+                const float over = kE4m3 ? m_out - kShift - m : 0.0f;
+                const float inv = l > 0.0f ? (kE4m3 ? exp2_fast(fminf(over, 126.0f)) : 1.0f) / l : (l == 0.0f ? 0.0f : NAN);
                 const bool odd = *s_odd != 0;
                 __nv_bfloat16* const out = a.out + static_cast<long long>(it.row0 + t_row) * a.out_token_stride + static_cast<long long>(head) * a.out_head_stride;
 #pragma unroll 1
@@ -884,7 +1172,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 }
                 if (live && whole && a.lse)
                     a.lse[static_cast<long long>(it.row0 + t_row) * a.n_heads + head] = l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l));
-                if (live && !whole) reinterpret_cast<float2*>(part + kRowsTile * D)[row] = make_float2(m, l);
+                if (live && !whole) reinterpret_cast<float4*>(part + kRowsTile * D)[row] = make_float4(m, l, kE4m3 ? m_out - kShift : m, 0.0f);
                 if (threadIdx.x == 0 && g0 == 0 && !whole) {
                     Header h;
                     h.b = it.b;
@@ -926,24 +1214,28 @@ __global__ void __launch_bounds__(256) tree_attention_join_kernel(const TreeArgs
     const int parts = h.last - static_cast<int>(blockIdx.x) + 1;
     const float* const base = reinterpret_cast<const float*>(static_cast<const char*>(a.ws) + kTreeCtrlBytes + sizeof(Header) * kMaxBlocks);
     auto part = [&](int i) { return base + (2LL * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * S::kPart; };
-    float m = kNone;
+    float m = kNone, m_out = -INFINITY;
 #pragma unroll 4
-    for (int i = 0; i < parts; ++i) m = fmaxf(m, reinterpret_cast<const float2*>(part(i) + kRowsTile * D)[row].x);
+    for (int i = 0; i < parts; ++i) {
+        const float4 q = reinterpret_cast<const float4*>(part(i) + kRowsTile * D)[row];
+        m = fmaxf(m, q.x);
+        m_out = fmaxf(m_out, q.z);
+    }
     float l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
     for (int i = 0; i < parts; ++i) {
-        const float2 ml = reinterpret_cast<const float2*>(part(i) + kRowsTile * D)[row];
+        const float4 q = reinterpret_cast<const float4*>(part(i) + kRowsTile * D)[row];
         const float4 x = reinterpret_cast<const float4*>(part(i))[col4 * kRowsTile + row];
-        const float f = exp2_fast(ml.x - m);
-        l = fmaf(ml.y, f, l);
+        const float f = exp2_fast(q.z - m_out);
+        l = fmaf(q.y, exp2_fast(q.x - m), l);
         o.x = fmaf(x.x, f, o.x);
         o.y = fmaf(x.y, f, o.y);
         o.z = fmaf(x.z, f, o.z);
         o.w = fmaf(x.w, f, o.w);
     }
     if (row >= h.rows) return;
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : NAN);
+    const float inv = l > 0.0f ? exp2_fast(fminf(m_out - m, 126.0f)) / l : (l == 0.0f ? 0.0f : NAN);
     const int group = a.n_heads / a.n_kv_heads, t = (h.first_row + row) / group, head = h.hk * group + (h.first_row + row) - t * group;
     const long long token = a.row_start[h.b] + t;
     *reinterpret_cast<uint2*>(a.out + token * a.out_token_stride + head * a.out_head_stride + 4 * col4) =
