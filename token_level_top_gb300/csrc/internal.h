@@ -346,6 +346,7 @@ struct TreeArgs {
     uint32_t page_mul;           // key / page_size = key * page_mul >> page_shift (set by the launcher)
     int page_shift;
     int box_rows;                // rows of a TMA box, or 0: pieces of 16 bytes instead (set by the launcher)
+    int by_item;                 // at most so many items, which have a header each; 0: more than blocks (set by the launcher)
 };
 constexpr size_t kTreeCtrlBytes = 256;
 size_t tree_attention_ws_bytes(int head_dim);   // 0: unsupported head_dim

@@ -67,8 +67,11 @@ struct Shape {
     static_assert(kSlots >= 4 && kSmem <= kShare && D + 2 * kKeys <= kCols, "room");
 };
 
-struct Header {   // of the item that begins in a block's run and does not end there
-    int b, hk, first_row, rows, last;   // rows of the tile, from first_row on; last: the block that ends it; -1: no such item
+// Of the item that begins in a block's run and does not end there.  Headers go by item while there are no more items than
+// blocks, else by block: the join has a few blocks to each.
+struct Header {
+    int b, hk, first_row, rows;   // rows of the tile, from first_row on
+    int first, last;              // the blocks that begin and end it; last -1: no such item
 };
 
 __device__ __forceinline__ float exp2_fast(float x)
@@ -296,6 +299,7 @@ struct Item {
     int len, ctx;               // cached tokens; those before the drafted ones (below 0 only with a wrong length)
     int base, n;                // first key of the first tile, tiles
     long long off;              // the item's first place in the list
+    int ordinal;                // among the items
 };
 
 // A sequence's lengths as the checks leave them.
@@ -321,6 +325,7 @@ __device__ __forceinline__ int places(const Item& w) { return w.n ? w.n + kGap :
 __device__ __forceinline__ void next_item(const TreeArgs& a, Item& w)
 {
     w.off += places(w);
+    ++w.ordinal;
     if (++w.h < w.items) return;
     w.h = 0;
     do {
@@ -444,23 +449,34 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // (the same in all lanes)
     const int group = a.n_heads / a.n_kv_heads;
 
+    let_next_start();
     // ---- the batch's places, and where this block's run begins
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
     long long mine = 0;
+    int mine_items = 0;
     for (int b = b0; b < b1; ++b) {
         Item w;
         w.b = b;
         load_seq(a, w, blockIdx.x == 0);
         mine += static_cast<long long>(places(w)) * w.items;
+        mine_items += w.n ? w.items : 0;
     }
     long long incl = mine;
+    int incl_items = mine_items;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const long long o = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += o;
+        const int i = __shfl_up_sync(0xffffffffu, incl_items, off);
+        if (lane >= off) {
+            incl += o;
+            incl_items += i;
+        }
     }
-    if (lane == 31) s_scan[warp] = incl;
+    if (lane == 31) {
+        s_scan[warp] = incl;
+        s_scan[kThreads / 32 + warp] = incl_items;
+    }
     // drafted tokens without any key (their length is wrong): zeros
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         Item w;
@@ -475,28 +491,40 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
     }
     __syncthreads();
     long long total = 0, before = incl - mine;
+    int items = 0, before_items = incl_items - mine_items;
 #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) {
-        if (i < warp) before += s_scan[i];
+        if (i < warp) {
+            before += s_scan[i];
+            before_items += static_cast<int>(s_scan[kThreads / 32 + i]);
+        }
         total += s_scan[i];
+        items += static_cast<int>(s_scan[kThreads / 32 + i]);
     }
     const long long run = quotient(total + gridDim.x - 1, gridDim.x);    // places per block
     const long long lo = run * blockIdx.x, hi = min(total, lo + run);
-    Header* const header = reinterpret_cast<Header*>(static_cast<char*>(a.ws) + kTreeCtrlBytes) + blockIdx.x;
-    if (threadIdx.x == 0) header->last = -1;
+    Header* const headers = reinterpret_cast<Header*>(static_cast<char*>(a.ws) + kTreeCtrlBytes);
+    if (a.by_item == 0) {
+        if (threadIdx.x == 0) headers[blockIdx.x].last = -1;
+    } else if (blockIdx.x == 0) {
+        for (int i = items + static_cast<int>(threadIdx.x); i < a.by_item; i += kThreads) headers[i].last = -1;
+    }
     if (lo >= hi) return;
     if (mine > 0 && before <= lo && lo < before + mine) {
         Item w;
         w.b = b0;
         w.h = 0;
         w.off = before;
+        w.ordinal = before_items;
         load_seq(a, w, false);
         while (w.off + static_cast<long long>(places(w)) * w.items <= lo) {
             w.off += static_cast<long long>(places(w)) * w.items;
+            w.ordinal += w.n ? w.items : 0;
             ++w.b;
             load_seq(a, w, false);
         }
         w.h = static_cast<int>(quotient(lo - w.off, places(w)));
+        w.ordinal += w.h;
         w.off += static_cast<long long>(w.h) * places(w);
         int g = static_cast<int>(lo - w.off);
         if (g >= w.n) {
@@ -1022,10 +1050,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                         cs = fminf(fmaxf(c_row * pow2_of_byte(info & 255u), 1e-37f), 3e38f);   // (0 times -inf would be NaN)
                         ev = static_cast<float>(static_cast<int>(info >> 8 & 255u) - 127);
                     }
-                    float top = -INFINITY;
+                    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // (four chains)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) top = fmaxf(top, fmaxf(__uint_as_float(x[0][j]), __uint_as_float(x[1][j])));
-                    top *= cs;
+                    for (int j = 0; j < 32; ++j)
+                        tops[j & 3] = fmaxf(tops[j & 3], fmaxf(__uint_as_float(x[0][j]), __uint_as_float(x[1][j])));
+                    float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * cs;
                     float top_out = top + ev;
                     bool apart = false;   // each key with its own exponents, and the softmax's sum with an exponential of its own
                     if (kE4m3) apart = uniform((info >> 16) != 0 || fmaxf(m_out, top_out) - fmaxf(m, top) - ev > 60.0f);
@@ -1173,14 +1202,16 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 if (live && whole && a.lse)
                     a.lse[static_cast<long long>(it.row0 + t_row) * a.n_heads + head] = l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l));
                 if (live && !whole) reinterpret_cast<float4*>(part + kRowsTile * D)[row] = make_float4(m, l, kE4m3 ? m_out - kShift : m, 0.0f);
+                if (threadIdx.x == 0 && whole && a.by_item > 0) headers[it.ordinal].last = -1;
                 if (threadIdx.x == 0 && g0 == 0 && !whole) {
                     Header h;
+                    h.first = blockIdx.x;
                     h.b = it.b;
                     h.hk = hk;
                     h.first_row = row_at;
                     h.rows = rows;
                     h.last = static_cast<int>(quotient(it.off + it.n - 1, run));
-                    *header = h;
+                    headers[a.by_item > 0 ? it.ordinal : static_cast<int>(blockIdx.x)] = h;
                 }
             }
             tc_fence_before();
@@ -1202,18 +1233,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
 
 // ---------------------------------------------------------------- the join
 
-// Block (x, y): the item that begins in block x's run and ends in another's; 32 of its rows, and 32 columns of them.
+// Block (x, y): header x's item; 32 of its rows, and 32 columns of them.
 template <int D>
 __global__ void __launch_bounds__(256) tree_attention_join_kernel(const TreeArgs a)
 {
     using S = Shape<D, false>;
+    wait_for_previous();
     const Header h = reinterpret_cast<const Header*>(static_cast<const char*>(a.ws) + kTreeCtrlBytes)[blockIdx.x];
     const int row0 = (blockIdx.y & 3) * 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (h.last < 0 || row0 >= h.rows) return;
     const int row = row0 + lane, col4 = (blockIdx.y >> 2) * 8 + warp;   // four columns
-    const int parts = h.last - static_cast<int>(blockIdx.x) + 1;
+    const int parts = h.last - h.first + 1;
     const float* const base = reinterpret_cast<const float*>(static_cast<const char*>(a.ws) + kTreeCtrlBytes + sizeof(Header) * kMaxBlocks);
-    auto part = [&](int i) { return base + (2LL * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * S::kPart; };
+    auto part = [&](int i) { return base + (2LL * (h.first + i) + (i == 0 ? 1 : 0)) * S::kPart; };
     float m = kNone, m_out = -INFINITY;
 #pragma unroll 4
     for (int i = 0; i < parts; ++i) {
@@ -1258,9 +1290,13 @@ cudaError_t launch(TreeArgs& a, cudaStream_t s)
                          encode_cache_map(&map_v, a.v, kE4m3, D, a.page_size, a.n_kv_heads, a.n_pages, a.token_bytes, a.head_bytes, a.page_bytes, rows)
                      ? rows : 0;
     const unsigned grid = static_cast<unsigned>(S::kCtas * std::min(num_sms(), kMaxSms));
+    // at most so many items: every sequence has one row tile a key head, and one more per 128 rows
+    const long long items = static_cast<long long>(a.n_kv_heads) * (a.B + static_cast<long long>(a.T) * (a.n_heads / a.n_kv_heads) / kRowsTile);
+    a.by_item = items <= grid ? static_cast<int>(items) : 0;
     kernel<<<grid, kThreads, S::kSmem, s>>>(map_k, map_v, a);
-    tree_attention_join_kernel<D><<<dim3(grid, 4 * D / 32), 256, 0, s>>>(a);
-    return cudaGetLastError();
+    const cudaError_t launched = cudaGetLastError();
+    if (launched != cudaSuccess) return launched;
+    return launch_after(tree_attention_join_kernel<D>, dim3(a.by_item > 0 ? static_cast<unsigned>(a.by_item) : grid, 4 * D / 32), 256, 0, s, a);
 }
 
 template <int D>

@@ -706,11 +706,13 @@ def kv_append(cache: KVCache, k, v, pos, page_table, q=None, phase=None, seq=Non
             raise ValueError("axis: it says which row of rotary turns a pair, and there is no rotary")
         st = (_lib or lib()).moe_kv_append(cache.ref, a, word, stream)
     else:
-        _want(rotary, "rotary", torch.int32, 2, dev)
-        axes = rotary.shape[0]
-        if rotary.shape[1] != T or phase is None:
+        rst = rotary.stride()
+        if len(rst) != 2 or rst[1] != 1 or rotary.dtype is not torch.int32 or rotary.get_device() != dev:
+            _want(rotary, "rotary", torch.int32, 2, dev)
+        axes, width = rotary.shape
+        if width != T or phase is None:
             raise ValueError(f"rotary: want [axes, {T}] and a phase to turn by, got {tuple(rotary.shape)}, phase {phase}")
-        r = _ROTATION.pack(axes, rotary.data_ptr(), rotary.stride(0) if axes > 1 else 0,
+        r = _ROTATION.pack(axes, rotary.data_ptr(), rst[0] if axes > 1 else 0,
                            0 if axis is None else _rows(axis, "axis", rot // 2, dev, torch.uint8))
         st = (_lib or lib()).moe_kv_append_axes(cache.ref, a, r, word, stream)
     if st:
@@ -852,28 +854,35 @@ def tree_attention(cache: KVCache, ws, q, row_start, seq_len, page_table, mask=N
     scale, window as in paged_attention.  Returns out [T, n_heads, head_dim] bf16, and lse [T, n_heads] fp32 with
     return_lse; rows of no sequence are left as they were (in a new out: not set)."""
     dev = _device(q, "q")
-    _want(q, "q", torch.bfloat16, 3, dev)
-    _want(page_table, "page_table", torch.int32, 2, dev)
+    qs, ts = q.stride(), page_table.stride()
+    if len(qs) != 3 or qs[2] != 1 or q.dtype is not torch.bfloat16:
+        _want(q, "q", torch.bfloat16, 3, dev)
+    if len(ts) != 2 or ts[1] != 1 or page_table.dtype is not torch.int32 or page_table.get_device() != dev:
+        _want(page_table, "page_table", torch.int32, 2, dev)
     if cache.device != dev:
         raise ValueError(f"cache: want one of CUDA device {dev}, got one of {cache.device}")
-    T, heads, dim = q.shape
+    shape = q.shape
+    T, heads, dim = shape
     B, max_pages = page_table.shape
     if dim != cache.head_dim:
-        raise ValueError(f"q: want [T, n_heads, {cache.head_dim}], got {tuple(q.shape)}")
+        raise ValueError(f"q: want [T, n_heads, {cache.head_dim}], got {tuple(shape)}")
     if not 0 <= window < 2 ** 31:
         raise ValueError(f"window: want 0 .. 2^31 - 1, got {window}")
     if out is None:
-        out = torch.empty(T, heads, dim, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        os_ = (heads * dim, dim)
     else:
         _want(out, "out", torch.bfloat16, 3, dev)
-        if out.shape != q.shape:
-            raise ValueError(f"out: want {tuple(q.shape)}, got {tuple(out.shape)}")
-    lse = torch.empty(T, heads, dtype=torch.float32, device=q.device) if return_lse else None
-    qs, os_ = _strides(q), _strides(out)
+        if out.shape != shape:
+            raise ValueError(f"out: want {tuple(shape)}, got {tuple(out.shape)}")
+        os_ = _strides(out)
+    lse = torch.empty((T, heads), dtype=torch.float32, device=q.device) if return_lse else None
+    if T == 1 or heads == 1:
+        qs = _strides(q)
     a = _TREE.pack(B, T, heads, max_pages, window, dim ** -0.5 if scale is None else scale,
                    _rows(row_start, "row_start", B + 1, dev), _rows(seq_len, "seq_len", B, dev),
                    0 if mask is None else _rows(mask, "mask", T, dev, torch.int64), page_table.data_ptr(),
-                   page_table.stride(0) if B > 1 else 0, q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else 0,
+                   ts[0] if B > 1 else 0, q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else 0,
                    qs[0], qs[1], os_[0], os_[1])
     st = (_lib or lib()).moe_tree_attention(cache.ref, a, _memory(ws, "ws", dev), ws.nbytes,
                                             torch._C._cuda_getCurrentRawStream(dev))
@@ -901,24 +910,24 @@ def beam_select(ws, logits, scores, n: int):
     if kind is None:
         raise ValueError(f"logits: want float32 or bfloat16, got {logits.dtype}")
     dev = _device(logits, "logits")
-    _want(logits, "logits", logits.dtype, 2, dev)
-    _want(scores, "scores", torch.float32, 2, dev)
+    xs = logits.stride()
+    if len(xs) != 2 or xs[1] != 1:
+        _want(logits, "logits", logits.dtype, 2, dev)
+    if scores.dtype is not torch.float32 or scores.dim() != 2 or scores.get_device() != dev or not scores.is_contiguous():
+        raise ValueError(f"scores: want contiguous [seqs, beams], float32, on CUDA device {dev}; got {tuple(scores.shape)} "
+                         f"{scores.dtype}, strides {scores.stride()}, {scores.device}")
     seqs, beams = scores.shape
     rows, vocab = logits.shape
-    if rows != seqs * beams or not scores.is_contiguous():
-        raise ValueError(f"logits, scores: want [seqs * beams, vocab] and contiguous [seqs, beams], got {tuple(logits.shape)}, "
-                         f"{tuple(scores.shape)}, strides {scores.stride()}")
-    size = (seqs, max(n, 0))
-    out = dict(scores=torch.empty(size, dtype=torch.float32, device=logits.device),
-               parents=torch.empty(size, dtype=torch.int32, device=logits.device),
-               tokens=torch.empty(size, dtype=torch.int32, device=logits.device))
-    st = (_lib or lib()).moe_beam_select(seqs, beams, vocab, kind, logits.data_ptr(), logits.stride(0) if rows > 1 else 0,
-                                         scores.data_ptr(), n, out["scores"].data_ptr(), out["parents"].data_ptr(),
-                                         out["tokens"].data_ptr(), _memory(ws, "ws", dev), ws.nbytes,
-                                         torch._C._cuda_getCurrentRawStream(dev))
+    if rows != seqs * beams:
+        raise ValueError(f"logits, scores: want [seqs * beams, vocab] and [seqs, beams], got {tuple(logits.shape)}, {tuple(scores.shape)}")
+    size, where, empty, i32 = (seqs, max(n, 0)), logits.device, torch.empty, torch.int32
+    best, parents, tokens = empty(size, dtype=torch.float32, device=where), empty(size, dtype=i32, device=where), empty(size, dtype=i32, device=where)
+    st = (_lib or lib()).moe_beam_select(seqs, beams, vocab, kind, logits.data_ptr(), xs[0] if rows > 1 else 0,
+                                         scores.data_ptr(), n, best.data_ptr(), parents.data_ptr(), tokens.data_ptr(),
+                                         _memory(ws, "ws", dev), ws.nbytes, torch._C._cuda_getCurrentRawStream(dev))
     if st:
         raise MoEError(st, "moe_beam_select")
-    return out
+    return dict(scores=best, parents=parents, tokens=tokens)
 
 
 def beam_reorder(cache: KVCache, parents, seq_len, page_table, out=None, status=None):
@@ -927,24 +936,28 @@ def beam_reorder(cache: KVCache, parents, seq_len, page_table, out=None, status=
     that is still filling stays each beam's own (rows of the cache are copied where two beams go on from one).  Returns the
     new page table (out when given; not page_table itself)."""
     dev = _device(parents, "parents")
-    _want(parents, "parents", torch.int32, 2, dev)
-    _want(page_table, "page_table", torch.int32, 2, dev)
+    ps, ts = parents.stride(), page_table.stride()
+    if len(ps) != 2 or ps[1] != 1 or parents.dtype is not torch.int32:
+        _want(parents, "parents", torch.int32, 2, dev)
+    if len(ts) != 2 or ts[1] != 1 or page_table.dtype is not torch.int32 or page_table.get_device() != dev:
+        _want(page_table, "page_table", torch.int32, 2, dev)
     if cache.device != dev:
         raise ValueError(f"cache: want one of CUDA device {dev}, got one of {cache.device}")
     seqs, beams = parents.shape
-    rows, max_pages = page_table.shape
+    shape = page_table.shape
+    rows, max_pages = shape
     if rows != seqs * beams:
         raise ValueError(f"parents, page_table: want [seqs, beams] and [seqs * beams, max_pages], got {tuple(parents.shape)}, "
-                         f"{tuple(page_table.shape)}")
+                         f"{tuple(shape)}")
     if out is None:
-        out = torch.empty(rows, max_pages, dtype=torch.int32, device=page_table.device)
+        out, os_ = torch.empty(shape, dtype=torch.int32, device=page_table.device), max_pages
     else:
         _want(out, "out", torch.int32, 2, dev)
-        if out.shape != page_table.shape:
-            raise ValueError(f"out: want {tuple(page_table.shape)}, got {tuple(out.shape)}")
-    a = _REORDER.pack(seqs, beams, max_pages, parents.data_ptr(), parents.stride(0) if seqs > 1 else 0,
-                      _rows(seq_len, "seq_len", seqs, dev), page_table.data_ptr(), page_table.stride(0) if rows > 1 else 0,
-                      out.data_ptr(), out.stride(0) if rows > 1 else 0)
+        if out.shape != shape:
+            raise ValueError(f"out: want {tuple(shape)}, got {tuple(out.shape)}")
+        os_ = out.stride(0)
+    a = _REORDER.pack(seqs, beams, max_pages, parents.data_ptr(), ps[0] if seqs > 1 else 0, _rows(seq_len, "seq_len", seqs, dev),
+                      page_table.data_ptr(), ts[0] if rows > 1 else 0, out.data_ptr(), os_ if rows > 1 else 0)
     st = (_lib or lib()).moe_beam_reorder(cache.ref, a, None if status is None else _memory(status, "status", dev),
                                           torch._C._cuda_getCurrentRawStream(dev))
     if st:
@@ -954,21 +967,24 @@ def beam_reorder(cache: KVCache, parents, seq_len, page_table, out=None, status=
 
 # ------------------------------------------------------------ the norm before attention and experts
 
-def _norm_rows(t, name, like, dev, dtype=None):
-    """The address and row stride of a matrix of `like`'s shape (and type, unless given)."""
-    _want(t, name, dtype or like.dtype, 2, dev)
-    if t.shape != like.shape:
-        raise ValueError(f"{name}: want {tuple(like.shape)}, got {tuple(t.shape)}")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0
+def _norm_rows(t, name, shape, dtype, dev):
+    """The address and row stride of a matrix of this shape and type."""
+    st = t.stride()
+    if len(st) != 2 or st[1] != 1 or t.dtype is not dtype or t.get_device() != dev:
+        _want(t, name, dtype, 2, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name}: want {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr(), st[0] if shape[0] > 1 else 0
 
 
 def _norm_weight(weight, cols, dev):
     """The address and type of the weights."""
     if weight is None:
         return 0, 0
-    if weight.dtype not in LOGITS:
+    kind = LOGITS.get(weight.dtype)
+    if kind is None:
         raise ValueError(f"weight: want float32 or bfloat16, got {weight.dtype}")
-    return _rows(weight, "weight", cols, dev, weight.dtype), LOGITS[weight.dtype]
+    return _rows(weight, "weight", cols, dev, weight.dtype), kind
 
 
 def rms_norm(x, weight=None, residual=None, eps=1e-6, y=True, e4m3=False, out=None, sum_out=None, status=None):
@@ -976,32 +992,41 @@ def rms_norm(x, weight=None, residual=None, eps=1e-6, y=True, e4m3=False, out=No
     bf16.  Returns a dict: sum (with a residual: x + residual in the rows' type), y (unless y is False) of the rows' type,
     and with e4m3 codes (uint8) and scales [rows] fp32 as quantize_fp8 has them.  out, sum_out: where y and sum go; either may
     be x or residual.  status: a status_word or workspace that records NaN and infinities."""
-    kind = LOGITS.get(x.dtype)
+    dtype = x.dtype
+    kind = LOGITS.get(dtype)
     if kind is None:
-        raise ValueError(f"x: want float32 or bfloat16, got {x.dtype}")
+        raise ValueError(f"x: want float32 or bfloat16, got {dtype}")
     dev = _device(x, "x")
-    _want(x, "x", x.dtype, 2, dev)
-    rows, cols = x.shape
-    xs = x.stride(0) if rows > 1 else 0
+    shape = x.shape
+    xp, xs = _norm_rows(x, "x", shape, dtype, dev)
+    rows, cols = shape
     wp, wk = _norm_weight(weight, cols, dev)
-    got = {}
+    got, where, empty = {}, x.device, torch.empty
     rp = rs = sp = ss = yp = ys = cp = cs = scp = 0
     if residual is not None:
-        rp, rs = _norm_rows(residual, "residual", x, dev)
-        got["sum"] = sum_out = torch.empty(rows, cols, dtype=x.dtype, device=x.device) if sum_out is None else sum_out
-        sp, ss = _norm_rows(sum_out, "sum_out", x, dev)
+        rp, rs = _norm_rows(residual, "residual", shape, dtype, dev)
+        if sum_out is None:
+            sum_out, ss = empty(shape, dtype=dtype, device=where), cols
+            sp = sum_out.data_ptr()
+        else:
+            sp, ss = _norm_rows(sum_out, "sum_out", shape, dtype, dev)
+        got["sum"] = sum_out
     elif sum_out is not None:
         raise ValueError("sum_out: there is no residual")
     if y:
-        got["y"] = out = torch.empty(rows, cols, dtype=x.dtype, device=x.device) if out is None else out
-        yp, ys = _norm_rows(out, "out", x, dev)
+        if out is None:
+            out, ys = empty(shape, dtype=dtype, device=where), cols
+            yp = out.data_ptr()
+        else:
+            yp, ys = _norm_rows(out, "out", shape, dtype, dev)
+        got["y"] = out
     elif out is not None:
         raise ValueError("out: y is not asked for")
     if e4m3:
-        got["codes"] = torch.empty(rows, cols, dtype=torch.uint8, device=x.device)
-        got["scales"] = torch.empty(rows, dtype=torch.float32, device=x.device)
-        cp, cs, scp = got["codes"].data_ptr(), cols, got["scales"].data_ptr()
-    a = _NORM.pack(rows, cols, kind, wk, eps, x.data_ptr(), rp, wp, sp, yp, cp, scp, xs, rs, ss, ys, cs)
+        got["codes"] = codes = empty(shape, dtype=torch.uint8, device=where)
+        got["scales"] = scales = empty(rows, dtype=torch.float32, device=where)
+        cp, cs, scp = codes.data_ptr(), cols, scales.data_ptr()
+    a = _NORM.pack(rows, cols, kind, wk, eps, xp, rp, wp, sp, yp, cp, scp, xs, rs, ss, ys, cs)
     st = (_lib or lib()).moe_rms_norm(a, None if status is None else _memory(status, "status", dev),
                                       torch._C._cuda_getCurrentRawStream(dev))
     if st:
@@ -1021,24 +1046,27 @@ def rms_norm_backward(ws, x, weight, dy, dsum=None, eps=1e-6, out=None, weight_g
     """Gradient of rms_norm's y (moe_rms_norm_backward): x what was normalised (the sum, with a residual), dy [rows, cols] fp32
     or of x's type, dsum of x's type: what reaches the sum from elsewhere.  Returns dx of x's type (out when given, which may
     be x, dsum or, of x's type, dy) and dweight [cols] fp32 (None, and ws may be None, without weight_grad)."""
-    kind = LOGITS.get(x.dtype)
-    if kind is None or dy.dtype not in LOGITS:
-        raise ValueError(f"x, dy: want float32 or bfloat16, got {x.dtype}, {dy.dtype}")
+    dtype, dy_type = x.dtype, dy.dtype
+    kind, dy_kind = LOGITS.get(dtype), LOGITS.get(dy_type)
+    if kind is None or dy_kind is None:
+        raise ValueError(f"x, dy: want float32 or bfloat16, got {dtype}, {dy_type}")
     dev = _device(x, "x")
-    _want(x, "x", x.dtype, 2, dev)
-    rows, cols = x.shape
-    xs = x.stride(0) if rows > 1 else 0
+    shape = x.shape
+    xp, xs = _norm_rows(x, "x", shape, dtype, dev)
+    rows, cols = shape
     wp, wk = _norm_weight(weight, cols, dev)
-    gp, gs = _norm_rows(dy, "dy", x, dev, dy.dtype)
-    dp, ds = _norm_rows(dsum, "dsum", x, dev) if dsum is not None else (0, 0)
-    out = torch.empty(rows, cols, dtype=x.dtype, device=x.device) if out is None else out
-    op, os_ = _norm_rows(out, "out", x, dev)
-    dweight, wsp, wsn = None, None, 0
+    gp, gs = _norm_rows(dy, "dy", shape, dy_type, dev)
+    dp, ds = _norm_rows(dsum, "dsum", shape, dtype, dev) if dsum is not None else (0, 0)
+    if out is None:
+        out, os_ = torch.empty(shape, dtype=dtype, device=x.device), cols
+        op = out.data_ptr()
+    else:
+        op, os_ = _norm_rows(out, "out", shape, dtype, dev)
+    dweight, dwp, wsp, wsn = None, 0, None, 0
     if weight_grad:
         dweight = torch.empty(cols, dtype=torch.float32, device=x.device)
-        wsp, wsn = _memory(ws, "ws", dev), ws.nbytes
-    a = _NORM_GRAD.pack(rows, cols, kind, LOGITS[dy.dtype], wk, eps, x.data_ptr(), wp, gp, dp, op,
-                        dweight.data_ptr() if weight_grad else 0, xs, gs, ds, os_)
+        dwp, wsp, wsn = dweight.data_ptr(), _memory(ws, "ws", dev), ws.nbytes
+    a = _NORM_GRAD.pack(rows, cols, kind, dy_kind, wk, eps, xp, wp, gp, dp, op, dwp, xs, gs, ds, os_)
     st = (_lib or lib()).moe_rms_norm_backward(a, wsp, wsn, torch._C._cuda_getCurrentRawStream(dev))
     if st:
         raise MoEError(st, "moe_rms_norm_backward")
