@@ -346,6 +346,11 @@ struct TreeArgs {
     uint32_t page_mul;           // key / page_size = key * page_mul >> page_shift (set by the launcher)
     int page_shift;
     int box_rows;                // rows of a TMA box, or 0: pieces of 16 bytes instead (set by the launcher)
+    uint32_t group_mul;          // 2^32 over the query heads of a key head, rounded up; 0: one (set by the launcher)
+    __host__ __device__ int tokens_of(int row) const   // row / query heads of a key head
+    {
+        return group_mul ? static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(row)) * group_mul) >> 32) : row;
+    }
     int by_item;                 // at most so many items, which have a header each; 0: more than blocks (set by the launcher)
 };
 constexpr size_t kTreeCtrlBytes = 256;

@@ -534,24 +534,18 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
         s_start->item = w;
         s_start->g = g;
     }
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(bar(kFull + i), kE4m3 || a.box_rows > 0 ? 1 : 32);
-            mbar_init(bar(kEmpty + i), 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(kSFull + i), 1);
-            mbar_init(bar(kPFull + i), kSoftmaxWarps);
-        }
-        mbar_init(bar(kODone), 1);
-        mbar_init(bar(kOFree), kSoftmaxWarps);
-        mbar_init(bar(kQFull), 32 * kCopyWarps);
-        mbar_init(bar(kQEmpty), 1);
-        mbar_init(bar(kItemDone), 1);
-        for (int i = 0; i < (kE4m3 ? kSlots : kCopyWarps); ++i) mbar_init(bar(kRawFull + i), a.box_rows > 0 ? 1 : 32);
+    static_assert(kCount <= kThreads, "a thread to each barrier");
+    if (threadIdx.x < kCount) {
+        const int i = threadIdx.x, copies = a.box_rows > 0 ? 1 : 32;   // one arrival by boxes, else each lane's
+        int count = 1;
+        if (i < kEmpty) count = kE4m3 ? 1 : copies;
+        if (i >= kRawFull) count = copies;
+        if ((i >= kPFull && i < kODone) || i == kOFree) count = kSoftmaxWarps;
+        if (i == kQFull) count = 32 * kCopyWarps;
+        mbar_init(bar(i), count);
         mbar_fence_init();
-        *s_odd = 0;
     }
+    if (threadIdx.x == 0) *s_odd = 0;
     __syncthreads();
     if (s_start->item.n == 0 || s_start->item.off + s_start->g >= hi) return;   // nothing but gaps
     if (warp == kProductWarp) {
@@ -668,15 +662,18 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 auto at = [&](int r, int piece) {
                     return smem_u32(s_q) + (piece >> 3) * (kRowsTile * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
                 };
+                const int rows = a.scale != 0.0f ? it.draft * group - row_at : 0;   // live ones
 #pragma unroll 1
                 for (int r1 = 8 * mine_of; r1 < kRowsTile; r1 += 8 * kCopyWarps) {
+                    // lane j: row r1 + j % 8
+                    const int mine = r1 + (lane & 7), t = a.tokens_of(row_at + mine);
+                    const long long place = mine < rows ? (it.row0 + t) * a.q_token_stride +
+                                                              (hk * group + (row_at + mine - t * group)) * a.q_head_stride : 0;
 #pragma unroll
                     for (int i = 0; i < kPieces / 4; ++i) {
-                        const int r = r1 + (i * 32 + lane) / kPieces, piece = (i * 32 + lane) % kPieces;
-                        const int row = row_at + r, t = row / group;
-                        const bool live = t < it.draft && a.scale != 0.0f;
-                        copy_async_or_zeros(at(r, piece), a.q + (live ? (it.row0 + t) * a.q_token_stride +
-                                                                            (hk * group + (row - t * group)) * a.q_head_stride : 0) + 8 * piece, live);
+                        const int r = (i * 32 + lane) / kPieces, piece = (i * 32 + lane) % kPieces;
+                        const long long from = __shfl_sync(0xffffffffu, place, r);
+                        copy_async_or_zeros(at(r1 + r, piece), a.q + from + 8 * piece, r1 + r < rows);
                     }
                 }
                 if (!kE4m3 && a.scale >= 0.0f) {
@@ -951,7 +948,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
             const int mtiles = it.items / a.n_kv_heads, hk = it.h / mtiles, row_at = (it.h - hk * mtiles) * kRowsTile;
             const int rows = min(kRowsTile, it.draft * group - row_at);
             const bool live = row < rows, idle = warp * 32 >= rows;   // idle: none of the warp's rows is a live one
-            const int t_row = (row_at + row) / group, head = hk * group + (row_at + row) - t_row * group;
+            const int t_row = a.tokens_of(row_at + row), head = hk * group + (row_at + row) - t_row * group;
             // what the row sees: drafted tokens `seen`, context from `from` on
             uint64_t seen = 0;
             int from = 0;
@@ -1322,6 +1319,9 @@ cudaError_t launch_tree_attention(const TreeArgs& args, int head_dim, bool e4m3,
 {
     if (args.B <= 0 || args.T <= 0) return cudaSuccess;
     TreeArgs a = args;
+    // row / group for the at most 2^16 rows of a key head: with mul = 2^32 / group rounded up, row * (mul * group - 2^32) < 2^32
+    const uint32_t group = static_cast<uint32_t>(a.n_heads / a.n_kv_heads);
+    a.group_mul = group > 1 ? static_cast<uint32_t>(((1ULL << 32) + group - 1) / group) : 0;
     // key / page_size for 0 <= key < 2^31 as a product and a shift: with 2^l the power of two at or above
     // page_size and mul = ceil(2^(31 + l) / page_size), mul * page_size exceeds 2^(31 + l) by less than 2^l
     int l = 0;
