@@ -162,43 +162,33 @@ struct Scale {
     bool finite;
 };
 
+// Every warp of a block with several rows takes part; a block's other rows go through it unchanged.  Leaves `buf` in use.
 template <int W, int P, int N, class R>
-__device__ __forceinline__ Scale scale_of(const R (&s)[P], float sum, float inv_cols, float eps, float* buf, int warp_of_row,
-                                          int lane)
+__device__ __forceinline__ Scale scale_of(const R (&s)[P], float sum, float inv_cols, float eps, float* buf, int warp_of_row, int lane)
 {
     Scale o;
-    o.f = 1.0f;
-    o.finite = true;
-    // (every warp of the block has to take part in a reduction; a block's other rows go through it unchanged)
-    const bool odd = !(sum < INFINITY);
-    if (W == 1 ? __any_sync(0xffffffffu, odd) : __syncthreads_or(odd)) {
-        float amax = 0.0f;
-        bool nan = false;
+    float amax = 0.0f;
+    bool nan = false;
 #pragma unroll
-        for (int p = 0; p < P; ++p)
+    for (int p = 0; p < P; ++p)
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float v = s[p].at(i);
-                amax = fmaxf(amax, fabsf(v));
-                nan = nan || v != v;
-            }
-        amax = reduce<W, true>(nan ? INFINITY : amax, buf, warp_of_row, lane);
-        const float f = odd && amax < INFINITY ? 0x1p-96f : 1.0f;
-        float again = 0.0f;
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-            for (int i = 0; i < N; ++i) again = fmaf(s[p].at(i) * f, s[p].at(i) * f, again);
-        if (W > 1) __syncthreads();   // the maxima are read
-        again = reduce<W, false>(again, buf, warp_of_row, lane);
-        if (odd) {
-            o.f = f;
-            o.finite = amax < INFINITY;
-            sum = again;
-            eps = f == 1.0f ? eps : 0.0f;   // (what is left of it is below 2^-100 of the sum)
+        for (int i = 0; i < N; ++i) {
+            const float v = s[p].at(i);
+            amax = fmaxf(amax, fabsf(v));
+            nan = nan || v != v;
         }
-    }
-    o.r = o.finite ? __frsqrt_rn(fmaf(sum, inv_cols, eps)) : NAN;
+    amax = reduce<W, true>(nan ? INFINITY : amax, buf, warp_of_row, lane);
+    o.finite = amax < INFINITY;
+    o.f = !(sum < INFINITY) && o.finite ? 0x1p-96f : 1.0f;
+    float again = 0.0f;
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < N; ++i) again = fmaf(s[p].at(i) * o.f, s[p].at(i) * o.f, again);
+    if (W > 1) __syncthreads();   // the maxima are read
+    again = reduce<W, false>(again, buf, warp_of_row, lane);
+    // (what is left of eps in the scaled sum is below 2^-100 of it)
+    o.r = o.finite ? __frsqrt_rn(fmaf(again, inv_cols, o.f == 1.0f ? eps : 0.0f)) : NAN;
     return o;
 }
 
@@ -248,7 +238,13 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256) rms_norm_kernel(const N
 #pragma unroll
         for (int i = 0; i < N; ++i) sum = fmaf(s[p].at(i), s[p].at(i), sum);
     sum = reduce<W, false>(sum, s_buf[0] + row_of * W, in_row, lane);
-    const Scale scale = scale_of<W, P, N>(s, sum, a.inv_cols, a.eps, s_buf[1] + row_of * W, in_row, lane);
+    Scale scale{1.0f, 0.0f, true};
+    const bool odd = !(sum < INFINITY);
+    // (a row to itself is agreed on by all its warps; of several in a block each has to take part)
+    if (W == 1 ? __any_sync(0xffffffffu, odd) : (W >= 8 ? odd : __syncthreads_or(odd) != 0))
+        scale = scale_of<W, P, N>(s, sum, a.inv_cols, a.eps, s_buf[1] + row_of * W, in_row, lane);
+    else
+        scale.r = __frsqrt_rn(fmaf(sum, a.inv_cols, a.eps));
     if (!live && W > 1 && !a.codes) return;
     if (live && !scale.finite && first == 0) record_error(a.status, MOE_ERR_NONFINITE);
 
@@ -301,16 +297,26 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256) rms_norm_kernel(const N
 
 // ---------------------------------------------------------------- gradient
 
+// Blocks an SM that the gradient's registers are held to.
+// (80 registers for pieces of eight bf16 values, of which a lane sums as many weights' gradients, 64 for four of fp32).
+template <class T, bool kVec, int W>
+constexpr int grad_blocks()
+{
+    return kVec && sizeof(T) == 2 ? (W <= 8 ? 3 : 1) : (W <= 8 ? kGradBlocksPerSm : (W == 16 ? 2 : 1));
+}
+
 template <class T, class D, bool kVec, int W, int P>
-__global__ void __launch_bounds__(W >= 8 ? 32 * W : 256) rms_norm_backward_kernel(const NormGradArgs a)
+__global__ void __launch_bounds__(W >= 8 ? 32 * W : 256, (grad_blocks<T, kVec, W>())) rms_norm_backward_kernel(const NormGradArgs a)
 {
     constexpr int N = kVec ? 16 / static_cast<int>(sizeof(T)) : 1;
     constexpr int kRows = W >= 8 ? 1 : 8 / W;
-    __shared__ float s_buf[2][4][kRows * W];
+    __shared__ float2 s_sums[2][kRows * W];
+    __shared__ float s_buf[kRows * W];
     __shared__ float s_dw[kRows > 1 ? (kRows - 1) * 32 * W * P * N : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row_of = warp / W, in_row = warp - row_of * W;
     const int units = kVec ? a.cols / N : a.cols, first = in_row * 32 + lane;
+    let_next_start();
 
     float dw[P][N];
 #pragma unroll
@@ -338,15 +344,8 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256) rms_norm_backward_kerne
                 if (a.dsum) d[p].load(dsum + u * N);
             }
         }
-        float sum = 0.0f, dot = 0.0f;
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-            for (int i = 0; i < N; ++i) sum = fmaf(s[p].at(i), s[p].at(i), sum);
-        // (two sets of buffers in turn: a row's sums are read while another warp may be at the next row's first one)
-        sum = reduce<W, false>(sum, s_buf[turn][0] + row_of * W, in_row, lane);
-        const Scale scale = scale_of<W, P, N>(s, sum, a.inv_cols, a.eps, s_buf[turn][1] + row_of * W, in_row, lane);
-        const float r = scale.f * scale.r;
+        // sum of s^2 and of w dy s, in one exchange between the warps
+        float2 sums = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const int u = first + p * 32 * W;
@@ -355,27 +354,69 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256) rms_norm_backward_kerne
             load_weight<kVec, N>(a.weight, a.weight_f32, u * N, w);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float unit = s[p].at(i) * scale.f * scale.r, gy = g[p].at(i);
-                dw[p][i] = fmaf(gy, unit, dw[p][i]);
-                dot = fmaf(gy * w[i], unit, dot);
+                const float v = s[p].at(i);
+                sums.x = fmaf(v, v, sums.x);
+                sums.y = fmaf(g[p].at(i) * w[i], v, sums.y);
             }
         }
-        dot = reduce<W, false>(dot, s_buf[turn][2] + row_of * W, in_row, lane) * a.inv_cols;
-        if (live) {
-            T* const dx = static_cast<T*>(a.dx) + row * a.dx_stride;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) {
+            sums.x += __shfl_xor_sync(0xffffffffu, sums.x, off);
+            sums.y += __shfl_xor_sync(0xffffffffu, sums.y, off);
+        }
+        if (W > 1) {
+            // (two buffers in turn: a row's sums are read while another warp may be at the next row's)
+            float2* const buf = s_sums[turn] + row_of * W;
+            if (lane == 0) buf[in_row] = sums;
+            __syncthreads();
+            sums = buf[0];
+#pragma unroll
+            for (int i = 1; i < W; ++i) {
+                sums.x += buf[i].x;
+                sums.y += buf[i].y;
+            }
+            turn ^= 1;
+        }
+        float f = 1.0f, r, dot = sums.y;
+        const bool odd = !(sums.x < INFINITY) || !(fabsf(dot) < INFINITY);
+        // (a row to itself is agreed on by all its warps; of several in a block each has to take part)
+        if (W == 1 ? __any_sync(0xffffffffu, odd) : (W >= 8 ? odd : __syncthreads_or(odd) != 0)) {
+            float* const buf = s_buf + row_of * W;
+            const Scale scale = scale_of<W, P, N>(s, sums.x, a.inv_cols, a.eps, buf, in_row, lane);
+            f = scale.f;
+            r = scale.r;
+            dot = 0.0f;
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 const int u = first + p * 32 * W;
                 if (u >= units) continue;
-                float w[N], out[N];
+                float w[N];
                 load_weight<kVec, N>(a.weight, a.weight_f32, u * N, w);
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    out[i] = fmaf(r, fmaf(-(s[p].at(i) * scale.f * scale.r), dot, g[p].at(i) * w[i]), d[p].at(i));
-                store<T, kVec, N>(dx + u * N, out);
+                for (int i = 0; i < N; ++i) dot = fmaf(g[p].at(i) * w[i], s[p].at(i) * f * r, dot);
             }
+            if (W > 1) __syncthreads();   // (what scale_of left has been read)
+            dot = reduce<W, false>(dot, buf, in_row, lane) * a.inv_cols;
+            if (W > 1) __syncthreads();
+        } else {
+            r = __frsqrt_rn(fmaf(sums.x, a.inv_cols, a.eps));
+            dot *= r * a.inv_cols;
         }
-        turn ^= 1;
+        T* const dx = static_cast<T*>(a.dx) + (live ? row * a.dx_stride : 0);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int u = first + p * 32 * W;
+            if (u >= units) continue;
+            float w[N], out[N];
+            load_weight<kVec, N>(a.weight, a.weight_f32, u * N, w);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float unit = s[p].at(i) * f * r, gy = g[p].at(i);
+                dw[p][i] = fmaf(gy, unit, dw[p][i]);
+                out[i] = fmaf(f * r, fmaf(-unit, dot, gy * w[i]), d[p].at(i));
+            }
+            if (live) store<T, kVec, N>(dx + u * N, out);
+        }
     }
     if (!a.dweight) return;
     // the block's rows that went side by side, then its row of the workspace
@@ -401,8 +442,8 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256) rms_norm_backward_kerne
     }
 }
 
-// dw[c] = the sum of the blocks' parts: 32 columns a block, 16 warps that take every 16th part.
-constexpr int kSumWarps = 16;
+// dw[c] = the sum of the blocks' parts: 32 columns a block, 32 warps that take every 32nd part.
+constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(32 * kSumWarps) rms_norm_weight_sum_kernel(const float* __restrict__ parts, int n, int cols,
                                                                            float* __restrict__ dw)
 {
@@ -411,7 +452,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) rms_norm_weight_sum_kernel(con
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float v = 0.0f;
     if (c < cols)
-#pragma unroll 8
+#pragma unroll 10
         for (int i = warp; i < n; i += kSumWarps) v += parts[static_cast<long long>(i) * cols + c];
     s_sum[warp][lane] = v;
     __syncthreads();
@@ -434,7 +475,7 @@ template <class T, class D, bool kVec, int W, int P>
 int backward(const NormGradArgs& a, cudaStream_t s)
 {
     constexpr int kRows = W >= 8 ? 1 : 8 / W;
-    const long long most = std::min(kGradBlocksPerSm * num_sms(), kGradBlocks);
+    const long long most = std::min(grad_blocks<T, kVec, W>() * num_sms(), kGradBlocks);
     const int grid = static_cast<int>(std::min<long long>((a.rows + kRows - 1) / kRows, most));
     rms_norm_backward_kernel<T, D, kVec, W, P><<<grid, W >= 8 ? 32 * W : 256, 0, s>>>(a);
     return grid;

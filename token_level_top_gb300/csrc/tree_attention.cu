@@ -724,7 +724,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
             if constexpr (!kE4m3) {
                 int n = n0 + (mine_of + kCopyWarps - n0 % kCopyWarps) % kCopyWarps;
                 look_up(n);
-                bool q_there = false;
+                bool q_there = seg == 0;   // (the first rows of q while the pages are looked up, later ones behind a tile)
+                if (q_there && !copy_q()) break;
                 for (; uniform(n < n_end); n += kCopyWarps) {
                     const int pages[2] = {entry[0], entry[1]};
                     look_up(n + kCopyWarps);
@@ -778,10 +779,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 // (what a tile needs is asked for a tile and two tiles before)
                 int n = n0, pages[2];
                 look_up(n);
+                bool q_there = seg == 0;
+                if (q_there && !copy_q()) break;
                 pages[0] = entry[0], pages[1] = entry[1];
                 exponents(n);
                 look_up(n + 2);
-                bool q_there = false;
                 for (; uniform(n < n_end); n += 2) {   // keys and values of a tile lie in the same pages
                     const uint32_t exps[2][2] = {{next[0][0], next[0][1]}, {next[1][0], next[1][1]}};
                     exponents(n + 2);
