@@ -563,7 +563,7 @@ bool encode_bf16_map(CUtensorMap* tm, const void* ptr, uint64_t rows, uint64_t c
     return make_map(tm, ptr, rows, cols, box_rows);
 }
 
-bool encode_cache_map(CUtensorMap* tm, const void* ptr, bool codes, int head_dim, int page_size, int heads, int pages,
+bool encode_cache_map(CUtensorMap* tm, const void* ptr, CacheBox kind, int head_dim, int page_size, int heads, int pages,
                       long long token_bytes, long long head_bytes, long long page_bytes, int rows)
 {
     auto enc = get_encode();
@@ -577,10 +577,13 @@ bool encode_cache_map(CUtensorMap* tm, const void* ptr, bool codes, int head_dim
         if (!one && (strides[i] <= 0 || strides[i] >= 1LL << 40)) return false;
         gstride[i] = one ? 16 : static_cast<cuuint64_t>(strides[i]);
     }
+    const bool codes = kind != kBf16Swizzled;
+    const CUtensorMapSwizzle swizzle = kind == kCodes ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                       : (codes && head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     cuuint32_t box[4] = {codes ? static_cast<cuuint32_t>(std::min(head_dim, 128)) : 64u, static_cast<cuuint32_t>(rows), 1, 1};
     cuuint32_t estride[4] = {1, 1, 1, 1};
     return enc(tm, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), gdim, gstride,
-               box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+               box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

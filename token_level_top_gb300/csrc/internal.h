@@ -320,9 +320,14 @@ constexpr size_t kAttentionCtrlBytes = 8192;
 size_t paged_attention_ws_bytes(int head_dim);   // 0: unsupported head_dim
 cudaError_t launch_paged_attention(const AttentionArgs& a, int head_dim, bool e4m3, cudaStream_t s);
 
-// 4-D map (value, token of a page, head, page) of one side of a paged cache, box [1, 1, rows, 64 values] of bf16 with the
-// 128-byte swizzle, or [1, 1, rows, up to 128] of e4m3 codes without one.  False where TMA cannot take such a layout.
-bool encode_cache_map(CUtensorMap* tm, const void* ptr, bool codes, int head_dim, int page_size, int heads, int pages,
+// 4-D map (value, token of a page, head, page) of one side of a paged cache, boxes of `rows` tokens.  False where TMA
+// cannot take such a layout.
+enum CacheBox : int {
+    kBf16Swizzled,    // 64 bf16 values, 128-byte swizzle
+    kCodes,           // up to 128 e4m3 codes, no swizzle
+    kCodesSwizzled,   // 128 codes with the 128-byte swizzle, of a head_dim of 64 those with the 64-byte one
+};
+bool encode_cache_map(CUtensorMap* tm, const void* ptr, CacheBox kind, int head_dim, int page_size, int heads, int pages,
                       long long token_bytes, long long head_bytes, long long page_bytes, int rows);
 
 // Attention of drafted tokens over the paged cache (tree_attention.cu).  Strides of the cache count bytes.

@@ -56,15 +56,20 @@ constexpr int kMaxSms = 152, kMaxBlocks = 2 * kMaxSms;
 template <int D, bool kE4m3>
 struct Shape {
     static constexpr int kCtas = D <= 128 ? 2 : 1;                        // blocks per SM
-    static constexpr int kTile = kPanel * D / 64;                         // bytes of a key or value tile
+    static constexpr int kTile = kPanel * D / 64;                         // bytes of a key or value tile of 16-bit values
     static constexpr int kQ = kRowsTile * D * 2;
-    static constexpr int kBars = kE4m3 && D == 64 ? 1280 : 1024;
-    static constexpr int kShare = std::min(233472 / kCtas - 1024, 232448);
-    static constexpr int kSlots = std::min((kShare - kBars - kQ) / kTile, kE4m3 ? 10 : 12);   // the ring of tiles
-    static constexpr int kSmem = kQ + kSlots * kTile + kBars;
+    static constexpr int kBars = kE4m3 ? 4096 : 1024;
+    static constexpr int kShare = std::min(233472 / kCtas - 1024, 232448), kRoom = kShare - kBars - kQ;
+    // One ring of slots for tiles; e4m3: one for keys, which stay codes, and one for values, which become f16 in their slots
+    // (D = 64: behind the codes).
+    static constexpr int kTileK = kE4m3 ? kKeys * D : kTile, kTileV = kE4m3 && D == 64 ? kTile + kKeys * D : kTile;
+    static constexpr int kSlotsK = kE4m3 ? (D == 64 ? 6 : 3) : 0, kSlotsV = kE4m3 ? (kRoom - kSlotsK * kTileK) / kTileV : 0;
+    static constexpr int kSlots = kE4m3 ? kSlotsK + kSlotsV : std::min(kRoom / kTile, 12);
+    static constexpr int kRing = kE4m3 ? kSlotsK * kTileK + kSlotsV * kTileV : kSlots * kTile;
+    static constexpr int kSmem = kQ + kRing + kBars;
     static constexpr int kCols = D <= 128 ? 256 : 512;                    // TMEM columns: O, then two tiles of scores
     static constexpr int kPart = kRowsTile * (D + 4);                     // floats of a part: O, then maximum, sum and O's maximum
-    static_assert(kSlots >= 4 && kSmem <= kShare && D + 2 * kKeys <= kCols, "room");
+    static_assert(kSlots >= 4 && (!kE4m3 || kSlotsV >= 3) && kSmem <= kShare && D + 2 * kKeys <= kCols, "room");
 };
 
 // Of the item that begins in a block's run and does not end there.  Headers go by item while there are no more items than
@@ -92,6 +97,14 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)
         "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
         : "=f"(r.x), "=f"(r.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b)
+{
+    Pair r;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
 __device__ __forceinline__ Pair add2(Pair a, Pair b)
@@ -163,7 +176,17 @@ __device__ __forceinline__ void mma_if(uint32_t leader, uint32_t d_tmem, uint64_
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
 }
-// The same with A in TMEM: 8 columns of bf16 pairs.
+// The same of e4m3 operands, K = 32.
+__device__ __forceinline__ void mma_e4m3_if(uint32_t leader, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+// The same with A in TMEM: 8 columns of pairs.
 __device__ __forceinline__ void mma_tmem_a_if(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                               uint32_t accumulate)
 {
@@ -205,6 +228,29 @@ __device__ __forceinline__ void copy_box_if(uint32_t leader, uint32_t dst, const
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(token), "r"(head), "r"(page), "r"(bar), "r"(leader)
         : "memory");
 }
+// A K-major operand whose rows are 64 bytes, with the 64-byte swizzle: groups of 8 rows 512 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_k_sw64(uint32_t saddr)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(1) << 16;
+    d |= static_cast<uint64_t>(512 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(4) << 61;
+    return d;
+}
+// Where byte c of row r of a K-major e4m3 operand of `rows` rows lies: panels of 128 bytes (D = 64: rows of 64), swizzled.
+template <int D>
+__device__ __forceinline__ uint32_t code_at(uint32_t base, int rows, int r, int c)
+{
+    if (D == 64) return base + r * 64 + ((((c >> 4) ^ (r >> 1)) & 3) << 4) + (c & 15);
+    return base + (c >> 7) * (rows * 128) + r * 128 + ((((c >> 4) ^ r) & 7) << 4) + (c & 15);
+}
+__device__ __forceinline__ void sts64(uint32_t a, uint2 v)
+{
+    asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(a), "r"(v.x), "r"(v.y) : "memory");
+}
+
 // Copies 16 bytes, or writes 16 zeros when !live (src is then not read).
 __device__ __forceinline__ void copy_async_or_zeros(uint32_t dst, const void* src, bool live)
 {
@@ -259,13 +305,12 @@ __device__ __forceinline__ void f16_of_codes(uint32_t w, uint32_t scale, uint32_
     lo = times(a, scale);
     hi = times(b, scale);
 }
-// Where byte c of row r of an e4m3 tile lies in its slot until it is turned into f16 in place.  A row's codes lie where the
-// second half of each 128 f16 values of that row goes (D = 64: where rows go whose codes are read by then), so rows may
-// be read and written in order.
+// Where byte c of row r of an e4m3 value tile lies in its slot until it is turned into f16: where the second half of each
+// 128 f16 values of that row goes (D = 64: behind them), so rows may be read and written one after another.
 template <int D>
 __device__ __forceinline__ uint32_t raw_at(uint32_t slot, int r, int c)
 {
-    return D == 64 ? slot + kPanel / 2 + r * 64 + c : slot + (c >> 7) * (2 * kPanel) + kPanel + r * 128 + (c & 127);
+    return D == 64 ? slot + kPanel + r * 64 + c : slot + (c >> 7) * (2 * kPanel) + kPanel + r * 128 + (c & 127);
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 {
@@ -273,11 +318,25 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// e4m3: a row of q goes in as f16 times 2^-e, its largest magnitude (bits `top`, sign cleared) at 2^13 and above.
+// e4m3: a row of q goes in times 2^-e as the sum of two e4m3 rows, e the smallest with its largest magnitude (bits `top`,
+// sign cleared) at most 448 * 2^e.  A bf16 value is such a sum exactly, down to 2^-10 of the largest; below, the error is
+// at most 2^-17 of the largest.
 __device__ __forceinline__ int row_exponent(uint32_t top)
 {
     const int e = static_cast<int>(top >> 7);
-    return e == 255 ? 0 : max(e - 127 - 13, -100);
+    return e == 255 ? 0 : max(e - 135 + ((top & 127u) > 96u ? 1 : 0), -100);
+}
+__device__ __forceinline__ uint32_t two_codes(float lo, float hi)
+{
+    uint16_t two;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(hi), "f"(lo));
+    return two;
+}
+__device__ __forceinline__ float2 of_two_codes(uint32_t two)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }   // -126 .. 127
 __device__ __forceinline__ uint32_t largest(uint32_t top, uint32_t w)
@@ -352,8 +411,8 @@ struct Apart {
             const int e = key < len ? __ldg(table + pg) : -1;
             const bool there = e >= 0 && e < a.n_pages;
             const long long at = there ? e * a.exp_page_stride + (key - pg * a.page_size) * a.exp_token_stride + hk * a.exp_head_stride : 0;
-            kb[h] = there && (info & 1u << 16) ? __ldg(a.k_exp + at) : info & 255u;
-            vb[h] = there && (info & 1u << 17) ? __ldg(a.v_exp + at) : info >> 8 & 255u;
+            kb[h] = there ? __ldg(a.k_exp + at) : 127u;
+            vb[h] = there && (info & 256u) ? __ldg(a.v_exp + at) : info & 255u;
         }
     }
     __device__ __forceinline__ float score(uint32_t s, int j, uint64_t keep, float c_row) const
@@ -428,23 +487,48 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char* const s_q = smem;
     unsigned char* const s_ring = smem + S::kQ;
-    uint64_t* const bars = reinterpret_cast<uint64_t*>(s_ring + kSlots * S::kTile);
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(s_ring + S::kRing);
     // A tile's scores are there (two buffers), its weights, its product with the values done; an item's last product
     // done, its output read; its rows of q there, and no longer read.  e4m3: a slot's codes there; bf16: a tile that the
     // warp which copies it looks at.
-    constexpr int kInfos = 16;
+    constexpr int kInfos = 8;
     constexpr int kFull = 0, kEmpty = kSlots, kSFull = 2 * kSlots, kPFull = kSFull + 2, kODone = kPFull + 2, kOFree = kODone + 1,
-                  kQFull = kOFree + 1, kQEmpty = kQFull + 1, kItemDone = kQEmpty + 1, kRawFull = kItemDone + 1, kCount = kRawFull + (kE4m3 ? kSlots : kCopyWarps);
-    static_assert(kCount * 8 + static_cast<int>(sizeof(Start)) + 16 * 8 + 8 + kInfos * 4 + (kE4m3 ? kSlots * kKeys : 0) <= S::kBars, "room for the barriers");
+                  kQFull = kOFree + 1, kQEmpty = kQFull + 1, kItemDone = kQEmpty + 1, kRawFull = kItemDone + 1, kCount = kRawFull + (kE4m3 ? S::kSlotsV : kCopyWarps);
+    static_assert(kCount * 8 + static_cast<int>(sizeof(Start)) + 16 * 8 + 16 + (kE4m3 ? kInfos * (4 + 4 * kKeys) + S::kSlotsV * kKeys + 4 * kRowsTile : 0) <= S::kBars, "room for the barriers");
     Start* const s_start = reinterpret_cast<Start*>(bars + kCount);
     long long* const s_scan = reinterpret_cast<long long*>(s_start + 1);
     volatile uint32_t* const s_tmem = reinterpret_cast<volatile uint32_t*>(s_scan + 16);
     volatile int* const s_odd = reinterpret_cast<volatile int*>(s_tmem + 1);   // NaN or infinities were taken from value rows
-    // e4m3: of tile t at t % kInfos: the exponent bytes of its keys and values, bits 16 and 17: each row's own.  And of the
-    // slots' rows the exponent bytes.
-    volatile uint32_t* const s_info = s_tmem + 2;
+    // e4m3: of tile t at t % kInfos: its values' exponent byte, bit 8: each row's own; and 2^exponent of each key.  (The tile
+    // that is copied is at most 7 ahead of the softmax.)  Of the slots' value rows the exponent bytes.
+    float* const s_kf = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(const_cast<uint32_t*>(s_tmem) + 2) + 15) & ~static_cast<uintptr_t>(15));
+    volatile uint32_t* const s_info = reinterpret_cast<volatile uint32_t*>(s_kf + kInfos * kKeys);
     volatile uint8_t* const s_exp = reinterpret_cast<volatile uint8_t*>(const_cast<uint32_t*>(s_info) + kInfos);
+    // Exponents of the rows of q, of item i at i % 4.  (Those of item i + 4 are written when the scores of item i + 3 are
+    // done; the weights of item i are done then, so they have been read.)
+    volatile int8_t* const s_qe = reinterpret_cast<volatile int8_t*>(s_exp + (kE4m3 ? S::kSlotsV * kKeys : 0));
     auto bar = [&](int i) { return smem_u32(bars + i); };
+    // Tiles are numbered through all of the block's items, keys of tile t as 2 t and values as 2 t + 1: their slot (a barrier's
+    // index too), how often it has gone round, and where it is.
+    struct Slot {
+        int index;
+        uint32_t turn, at;
+    };
+    auto slot_of = [&](int n) {
+        Slot o;
+        const uint32_t ring = smem_u32(s_ring);
+        if constexpr (!kE4m3) {
+            o.index = n % kSlots;
+            o.turn = static_cast<uint32_t>(n / kSlots) & 1;
+            o.at = ring + o.index * S::kTile;
+        } else {
+            const int t = n >> 1, k = t % S::kSlotsK, v = t % S::kSlotsV;
+            o.index = n & 1 ? S::kSlotsK + v : k;
+            o.turn = static_cast<uint32_t>(n & 1 ? t / S::kSlotsV : t / S::kSlotsK) & 1;
+            o.at = n & 1 ? ring + S::kSlotsK * S::kTileK + v * S::kTileV : ring + k * S::kTileK;
+        }
+        return o;
+    };
 
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // (the same in all lanes)
     const int group = a.n_heads / a.n_kv_heads;
@@ -538,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
     if (threadIdx.x < kCount) {
         const int i = threadIdx.x, copies = a.box_rows > 0 ? 1 : 32;   // one arrival by boxes, else each lane's
         int count = 1;
-        if (i < kEmpty) count = kE4m3 ? 1 : copies;
+        if (i < kEmpty) count = kE4m3 && i >= S::kSlotsK ? kCopyWarps - 1 : copies;   // (e4m3 values: the warps that turn them into f16)
         if (i >= kRawFull) count = copies;
         if ((i >= kPFull && i < kODone) || i == kOFree) count = kSoftmaxWarps;
         if (i == kQFull) count = 32 * kCopyWarps;
@@ -615,7 +699,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                         for (int v = 0; v < kSides; ++v)
 #pragma unroll
                             for (int x = 0; x < (kE4m3 ? (D + 127) / 128 : D / 64); ++x)
-                                copy_box_if(leader, kE4m3 ? raw_at<D>(dst[v], r, 128 * x) : dst[v] + x * kPanel + r * 128,
+                                copy_box_if(leader, kE4m3 && v == 1 ? raw_at<D>(dst[v], r, 128 * x)
+                                                                    : dst[v] + x * kPanel + r * (kE4m3 && D == 64 ? 64 : 128),
                                             (kE4m3 ? v : n & 1) ? &map_v : &map_k, (kE4m3 ? 128 : 64) * x, token, hk, page, full[v]);
                     }
                 } else {
@@ -637,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                             const int r = i * kStep + r0;
                             const long long p0 = __shfl_sync(0xffffffffu, place[0], r & 31), p1 = __shfl_sync(0xffffffffu, place[1], r & 31);
                             const long long at = r < 32 ? p0 : p1;
-                            copy_async_or_zeros(kE4m3 ? raw_at<D>(to, r, 16 * piece)
+                            copy_async_or_zeros(kE4m3 ? (v ? raw_at<D>(to, r, 16 * piece) : code_at<D>(to, kKeys, r, 16 * piece))
                                                       : to + (piece >> 3) * kPanel + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
                                                 from + (at < 0 ? 0 : at), at >= 0);
                         }
@@ -663,53 +748,82 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     return smem_u32(s_q) + (piece >> 3) * (kRowsTile * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
                 };
                 const int rows = a.scale != 0.0f ? it.draft * group - row_at : 0;   // live ones
+                if constexpr (kE4m3) {
+                    // Two e4m3 rows for each, one tile behind the other.  (One piece a turn: the code is run once an item, so what it
+                    // costs is to fetch it.)
+                    constexpr int kRows = 32 / kPieces, kStep = kRows * kCopyWarps;   // rows of a warp at a time
+                    const int piece = lane % kPieces;
+                    auto fetch = [&](int r) {
+                        if (r >= rows || r >= kRowsTile) return make_uint4(0, 0, 0, 0);
+                        const int t = a.tokens_of(row_at + r);
+                        return __ldg(reinterpret_cast<const uint4*>(a.q + (it.row0 + t) * a.q_token_stride +
+                                                                    (hk * group + (row_at + r - t * group)) * a.q_head_stride + 8 * piece));
+                    };
+                    int r = kRows * mine_of + lane / kPieces;
+                    uint4 next = fetch(r), after = fetch(r + kStep);
 #pragma unroll 1
-                for (int r1 = 8 * mine_of; r1 < kRowsTile; r1 += 8 * kCopyWarps) {
-                    // lane j: row r1 + j % 8
-                    const int mine = r1 + (lane & 7), t = a.tokens_of(row_at + mine);
-                    const long long place = mine < rows ? (it.row0 + t) * a.q_token_stride +
-                                                              (hk * group + (row_at + mine - t * group)) * a.q_head_stride : 0;
+                    for (; uniform(r - lane / kPieces < kRowsTile); r += kStep) {
+                        const uint4 x = next;
+                        next = after;
+                        after = fetch(r + 2 * kStep);
+                        uint32_t top = largest(largest(largest(largest(0, x.x), x.y), x.z), x.w);
 #pragma unroll
-                    for (int i = 0; i < kPieces / 4; ++i) {
-                        const int r = (i * 32 + lane) / kPieces, piece = (i * 32 + lane) % kPieces;
-                        const long long from = __shfl_sync(0xffffffffu, place, r);
-                        copy_async_or_zeros(at(r1 + r, piece), a.q + from + 8 * piece, r1 + r < rows);
+                        for (int off = kPieces / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+                        const int e = row_exponent(top);
+                        // (a row with a NaN or an infinity is NaN)
+                        const float f = top >> 7 == 255u ? NAN : (a.scale < 0.0f ? -1.0f : 1.0f) * pow2(-e);
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float v0 = __uint_as_float(w[j] << 16) * f, v1 = __uint_as_float(w[j] & 0xffff0000u) * f;
+                            const uint32_t two = two_codes(v0, v1);
+                            const float2 back = of_two_codes(two);
+                            hi[j >> 1] |= two << (16 * (j & 1));
+                            lo[j >> 1] |= two_codes(v0 - back.x, v1 - back.y) << (16 * (j & 1));
+                        }
+                        if (r < kRowsTile) {
+                            sts64(code_at<D>(smem_u32(s_q), kRowsTile, r, 8 * piece), make_uint2(hi[0], hi[1]));
+                            sts64(code_at<D>(smem_u32(s_q) + kRowsTile * D, kRowsTile, r, 8 * piece), make_uint2(lo[0], lo[1]));
+                            if (piece == 0) s_qe[(seg & 3) * kRowsTile + r] = static_cast<int8_t>(e);
+                        }
                     }
-                }
-                if (!kE4m3 && a.scale >= 0.0f) {
-                    copy_arrive(bar(kQFull));
-                } else if (kE4m3) {
-                    copy_wait_all();
-#pragma unroll 1
-                    for (int r1 = 8 * mine_of; r1 < kRowsTile; r1 += 8 * kCopyWarps)
-#pragma unroll
-                        for (int i = 0; i < kPieces / 4; ++i) {
-                            const uint32_t to = at(r1 + (i * 32 + lane) / kPieces, (i * 32 + lane) % kPieces);
-                            const uint4 x = lds128(to);
-                            uint32_t top = largest(largest(largest(largest(0, x.x), x.y), x.z), x.w);
-#pragma unroll
-                            for (int off = kPieces / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-                            const float f = (a.scale < 0.0f ? -1.0f : 1.0f) * pow2(-row_exponent(top));
-                            auto half = [&](uint32_t w) { return pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f); };
-                            sts128(to, make_uint4(half(x.x), half(x.y), half(x.z), half(x.w)));
-                        }
                     fence_proxy_async_shared();
                     mbar_arrive(bar(kQFull));
+                    __syncwarp();
+                    return true;
                 } else {
-                    copy_wait_all();
 #pragma unroll 1
-                    for (int r1 = 8 * mine_of; r1 < kRowsTile; r1 += 8 * kCopyWarps)
+                    for (int r1 = 8 * mine_of; r1 < kRowsTile; r1 += 8 * kCopyWarps) {
+                        // lane j: row r1 + j % 8
+                        const int mine = r1 + (lane & 7), t = a.tokens_of(row_at + mine);
+                        const long long place = mine < rows ? (it.row0 + t) * a.q_token_stride +
+                                                                  (hk * group + (row_at + mine - t * group)) * a.q_head_stride : 0;
 #pragma unroll
                         for (int i = 0; i < kPieces / 4; ++i) {
-                            const uint32_t to = at(r1 + (i * 32 + lane) / kPieces, (i * 32 + lane) % kPieces);
-                            const uint4 x = lds128(to);
-                            sts128(to, make_uint4(x.x ^ 0x80008000u, x.y ^ 0x80008000u, x.z ^ 0x80008000u, x.w ^ 0x80008000u));
+                            const int r = (i * 32 + lane) / kPieces, piece = (i * 32 + lane) % kPieces;
+                            const long long from = __shfl_sync(0xffffffffu, place, r);
+                            copy_async_or_zeros(at(r1 + r, piece), a.q + from + 8 * piece, r1 + r < rows);
                         }
-                    fence_proxy_async_shared();
-                    mbar_arrive(bar(kQFull));
+                    }
+                    if (a.scale >= 0.0f) {
+                        copy_arrive(bar(kQFull));
+                    } else {
+                        copy_wait_all();
+#pragma unroll 1
+                        for (int r1 = 8 * mine_of; r1 < kRowsTile; r1 += 8 * kCopyWarps)
+#pragma unroll
+                            for (int i = 0; i < kPieces / 4; ++i) {
+                                const uint32_t to = at(r1 + (i * 32 + lane) / kPieces, (i * 32 + lane) % kPieces);
+                                const uint4 x = lds128(to);
+                                sts128(to, make_uint4(x.x ^ 0x80008000u, x.y ^ 0x80008000u, x.z ^ 0x80008000u, x.w ^ 0x80008000u));
+                            }
+                        fence_proxy_async_shared();
+                        mbar_arrive(bar(kQFull));
+                    }
+                    __syncwarp();
+                    return true;
                 }
-                __syncwarp();
-                return true;
             };
             // ---- the key and value tiles
             const int odd_from = a.window > 0 ? max(0, it.ctx - a.window + it.draft) : 0;   // below it, and from ctx on, rows differ
@@ -729,10 +843,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 for (; uniform(n < n_end); n += kCopyWarps) {
                     const int pages[2] = {entry[0], entry[1]};
                     look_up(n + kCopyWarps);
-                    if (!wait_for(kEmpty + n % kSlots, ((n / kSlots) & 1) ^ 1)) break;
-                    const uint32_t slot = smem_u32(s_ring) + (n % kSlots) * S::kTile;
+                    const Slot to = slot_of(n);
+                    if (!wait_for(kEmpty + to.index, to.turn ^ 1)) break;
                     const bool look = uniform(mixed(n));
-                    copy_tile(n, pages, {slot}, {look ? bar(kRawFull + mine_of) : bar(kFull + n % kSlots)});
+                    copy_tile(n, pages, {to.at}, {look ? bar(kRawFull + mine_of) : bar(kFull + to.index)});
                     if (!q_there && !copy_q()) break;
                     q_there = true;
                     if (!look) continue;
@@ -741,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     uint32_t odd = 0;
 #pragma unroll 4
                     for (int i = lane; i < S::kTile / 16; i += 32) {   // (rows of 128 bytes: the order within does not matter)
-                        const uint32_t at = slot + 16 * i;
+                        const uint32_t at = to.at + 16 * i;
                         uint4 x = lds128(at);
                         const bool dead = ((i >> 3) & (kKeys - 1)) >= live;
                         if (dead || any_odd(x)) {
@@ -753,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     if (odd) *s_odd = 1;
                     fence_proxy_async_shared();
                     __syncwarp();
-                    if (a.box_rows == 0 || lane == 0) mbar_arrive(bar(kFull + n % kSlots));
+                    if (a.box_rows == 0 || lane == 0) mbar_arrive(bar(kFull + to.index));
                     __syncwarp();
                 }
                 if (ok && !q_there && !copy_q()) break;
@@ -770,11 +884,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                         next[1][h] = there ? __ldg(a.v_exp + place) : 256u;
                     }
                 };
-                // of a tile: its rows' largest exponent byte (127 without rows); bit 8: not all are near it
-                auto reference = [&](const uint32_t (&e)[2]) {
+                // of a tile: its value rows' largest exponent byte (127 without rows); bit 8: not all are near it, or a key's is one
+                // with which a score times 2^exponent might leave the range of its sums
+                auto reference = [&](const uint32_t (&k)[2], const uint32_t (&e)[2]) {
+                    const bool far = (k[0] != 256u && k[0] - 63u > 128u) || (k[1] != 256u && k[1] - 63u > 128u);
                     const uint32_t top = __reduce_max_sync(0xffffffffu, max(e[0] == 256u ? 0u : e[0] + 1, e[1] == 256u ? 0u : e[1] + 1));
                     const uint32_t least = __reduce_min_sync(0xffffffffu, min(e[0], e[1]));
-                    return top == 0 ? 127u : (top - 1 - least <= static_cast<uint32_t>(kNarrow) ? top - 1 : top - 1 | 256u);
+                    if (top == 0) return 127u;
+                    return top - 1 - least <= static_cast<uint32_t>(kNarrow) && !__any_sync(0xffffffffu, far) ? top - 1 : top - 1 | 256u;
                 };
                 // (what a tile needs is asked for a tile and two tiles before)
                 int n = n0, pages[2];
@@ -789,55 +906,53 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     exponents(n + 2);
                     const int following[2] = {entry[0], entry[1]};
                     look_up(n + 4);
-                    const uint32_t ref_k = reference(exps[0]), ref_v = reference(exps[1]);
-                    const int slot_k = n % kSlots, slot_v = (n + 1) % kSlots;
-                    if (!wait_for(kEmpty + slot_k, ((n / kSlots) & 1) ^ 1)) break;
-                    if (!wait_for(kEmpty + slot_v, (((n + 1) / kSlots) & 1) ^ 1)) break;
-                    s_exp[slot_k * kKeys + lane] = static_cast<uint8_t>(exps[0][0]);
-                    s_exp[slot_k * kKeys + 32 + lane] = static_cast<uint8_t>(exps[0][1]);
-                    s_exp[slot_v * kKeys + lane] = static_cast<uint8_t>(exps[1][0]);
-                    s_exp[slot_v * kKeys + 32 + lane] = static_cast<uint8_t>(exps[1][1]);
-                    if (lane == 0)   // (tiles here and in the softmax are at most 8 apart)
-                        s_info[(n >> 1) % kInfos] = (ref_k & 255u) | (ref_v & 255u) << 8 | (ref_k >> 8) << 16 | (ref_v >> 8) << 17;
+                    const uint32_t ref = reference(exps[0], exps[1]);
+                    const Slot k = slot_of(n), v = slot_of(n + 1);
+                    if (!wait_for(kEmpty + k.index, k.turn ^ 1)) break;
+                    if (!wait_for(kEmpty + v.index, v.turn ^ 1)) break;
+                    const int tile = (n >> 1) % kInfos, raw = v.index - S::kSlotsK;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        s_kf[tile * kKeys + 32 * h + lane] = exps[0][h] == 256u ? 1.0f : pow2_of_byte(exps[0][h]);
+                        s_exp[raw * kKeys + 32 * h + lane] = static_cast<uint8_t>(exps[1][h]);
+                    }
+                    if (lane == 0) s_info[tile] = ref;
                     __syncwarp();
-                    copy_tile(n, pages, {smem_u32(s_ring) + slot_k * S::kTile, smem_u32(s_ring) + slot_v * S::kTile},
-                              {bar(kRawFull + slot_k), bar(kRawFull + slot_v)});
+                    copy_tile(n, pages, {k.at, v.at}, {bar(kFull + k.index), bar(kRawFull + raw)});
                     if (!ok || (!q_there && !copy_q())) break;
                     q_there = true;
                     pages[0] = following[0], pages[1] = following[1];
                 }
             } else {
                 if (!copy_q()) break;
-                constexpr int kPieces = D / 16, kStep = 32 / kPieces, kCount = kKeys * kPieces / 32;   // pieces of 16 codes
-                constexpr int kBatch = 4;
-                const int piece = lane % kPieces, r0 = lane / kPieces, v = mine_of - 1;
-                for (int n = n0 + v; uniform(n < n_end); n += 2) {
+                // value tiles into f16, half of the rows a warp
+                constexpr int kPieces = D / 16, kStep = 32 / kPieces, kCount = kKeys / 2 * kPieces / 32;   // pieces of 16 codes
+                constexpr int kBatch = std::min(kCount, 4);
+                const int piece = lane % kPieces, half = 32 * (mine_of - 1), r0 = half + lane / kPieces;
+                for (int n = n0 + 1; uniform(n < n_end); n += 2) {
                     const bool look = uniform(mixed(n));
                     const int live = min(kKeys, it.len - first_key(n));
-                    const int slot = n % kSlots;
-                    if (!wait_for(kRawFull + slot, (n / kSlots) & 1)) break;
+                    const Slot v = slot_of(n);
+                    const int raw = v.index - S::kSlotsK;
+                    if (!wait_for(kRawFull + raw, v.turn)) break;
                     // f16 2^(e - that of the tile), or 1 where the softmax takes each row's own exponent
-                    const uint32_t info = s_info[(n >> 1) % kInfos] >> (8 * v);
-                    uint32_t mine[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int e = s_exp[slot * kKeys + 32 * h + lane], d = e - static_cast<int>(info & 255u);
-                        const float f = (info >> (16 - 7 * v) & 1u) != 0 || lane + 32 * h >= live ? 1.0f : pow2(max(d, -kNarrow));
-                        mine[h] = pack_f16x2(f, f);
-                    }
-                    const uint32_t at = smem_u32(s_ring) + slot * S::kTile, to = at + (piece >> 2) * kPanel;
+                    const uint32_t info = s_info[(n >> 1) % kInfos];
+                    const int d = s_exp[raw * kKeys + half + lane] - static_cast<int>(info & 255u);
+                    const float f = (info & 256u) != 0 || half + lane >= live ? 1.0f : pow2(max(d, -kNarrow));
+                    const uint32_t mine = pack_f16x2(f, f);
+                    const uint32_t to = v.at + (piece >> 2) * kPanel;
                     uint32_t odd = 0;
 #pragma unroll 1
                     for (int i0 = 0; i0 < kCount; i0 += kBatch) {   // (rolled: the block's warps share one instruction cache)
                         uint4 w[kBatch];
 #pragma unroll
-                        for (int i = 0; i < kBatch; ++i) w[i] = lds128(raw_at<D>(at, (i0 + i) * kStep + r0, 16 * piece));
+                        for (int i = 0; i < kBatch; ++i) w[i] = lds128(raw_at<D>(v.at, (i0 + i) * kStep + r0, 16 * piece));
                         __syncwarp();
 #pragma unroll
                         for (int i = 0; i < kBatch; ++i) {
                             const int r = (i0 + i) * kStep + r0;
                             if (r >= live) w[i] = make_uint4(0, 0, 0, 0);
-                            const uint32_t scale = __shfl_sync(0xffffffffu, (i0 + i) * kStep < 32 ? mine[0] : mine[1], r & 31);
+                            const uint32_t scale = __shfl_sync(0xffffffffu, mine, r & 31);
                             uint4 x, y;
                             f16_of_codes(w[i].x, scale, x.x, x.y);
                             f16_of_codes(w[i].y, scale, x.z, x.w);
@@ -862,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     if (odd) *s_odd = 1;
                     fence_proxy_async_shared();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kFull + slot));
+                    if (lane == 0) mbar_arrive(bar(kFull + v.index));
                     __syncwarp();
                 }
             }
@@ -881,8 +996,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
         {
             const uint32_t leader = elected();
             // (f16 operands: format 0 for both)
-            constexpr uint32_t kF16 = kE4m3 ? ~(1u << 7 | 1u << 10) : ~0u;
-            constexpr uint32_t kIdescS = idesc_bf16_f32(kRowsTile, kKeys) & kF16, kIdescO = (idesc_bf16_f32(kRowsTile, D) | 1u << 16) & kF16;
+            constexpr uint32_t kIdescS = kE4m3 ? idesc_e4m3_f32(kRowsTile, kKeys) : idesc_bf16_f32(kRowsTile, kKeys);
+            constexpr uint32_t kIdescO = (idesc_bf16_f32(kRowsTile, D) | 1u << 16) & (kE4m3 ? ~(1u << 7 | 1u << 10) : ~0u);
             auto wait = [&](int i, uint32_t parity) {
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(i), parity, kSpinBudget));
                 return ok;
@@ -896,20 +1011,35 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     // the next but one can begin: a wait tells only neighbours apart.)
                     if (uniform(t >= 2 && (i > 0 || seg == 0))) {
                         if (!wait(kODone, t & 1)) break;
-                        if (lane == 0) mbar_arrive(bar(kEmpty + (nv - 2) % kSlots));
+                        if (lane == 0) mbar_arrive(bar(kEmpty + slot_of(nv - 2).index));
                         __syncwarp();
                     }
-                    if (uniform(i < count) && !wait(kFull + n % kSlots, (n / kSlots) & 1)) break;
+                    const Slot keys = slot_of(n), values = slot_of(max(nv, 1));
+                    if (uniform(i < count) && !wait(kFull + keys.index, keys.turn)) break;
                     if (uniform(i == 0) && !wait(kQFull, seg & 1)) break;
-                    if (uniform(i > 0) && !wait(kFull + nv % kSlots, (nv / kSlots) & 1)) break;
+                    if (uniform(i > 0) && !wait(kFull + values.index, values.turn)) break;
                     tc_fence_after();
                     fence_proxy_async_shared();   // the copies were written through the generic proxy
                     if (uniform(i < count)) {
-                        const uint32_t d = tmem + D + (t & 1) * kKeys, k0 = smem_u32(s_ring) + (n % kSlots) * S::kTile;
+                        const uint32_t d = tmem + D + (t & 1) * kKeys, k0 = keys.at, q0 = smem_u32(s_q);
+                        if constexpr (kE4m3) {
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            mma_if(leader, d, sdesc_k_sw128(smem_u32(s_q) + (k >> 2) * (kRowsTile * 128) + (k & 3) * 32),
-                                   sdesc_k_sw128(k0 + (k >> 2) * kPanel + (k & 3) * 32), kIdescS, k > 0);
+                            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                                for (int k = 0; k < D / 32; ++k) {
+                                    const uint32_t qp = q0 + part * kRowsTile * D;
+                                    if (D == 64)
+                                        mma_e4m3_if(leader, d, sdesc_k_sw64(qp + k * 32), sdesc_k_sw64(k0 + k * 32), kIdescS, part + k > 0);
+                                    else
+                                        mma_e4m3_if(leader, d, sdesc_k_sw128(qp + (k >> 2) * (kRowsTile * 128) + (k & 3) * 32),
+                                                    sdesc_k_sw128(k0 + (k >> 2) * kPanel + (k & 3) * 32), kIdescS, part + k > 0);
+                                }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k)
+                                mma_if(leader, d, sdesc_k_sw128(q0 + (k >> 2) * (kRowsTile * 128) + (k & 3) * 32),
+                                       sdesc_k_sw128(k0 + (k >> 2) * kPanel + (k & 3) * 32), kIdescS, k > 0);
+                        }
                         commit_if(leader, bar(kSFull + (t & 1)));   // (the keys' slot is handed on by the softmax)
                         if (uniform(i == count - 1)) commit_if(leader, bar(kQEmpty));
                     }
@@ -917,7 +1047,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                         if (!wait(kPFull + (u & 1), (u >> 1) & 1)) break;
                         if (uniform(i == 1 && seg > 0) && !wait(kOFree, (seg - 1) & 1)) break;
                         tc_fence_after();
-                        const uint32_t pt = tmem + D + (u & 1) * kKeys, v0 = smem_u32(s_ring) + (nv % kSlots) * S::kTile;
+                        const uint32_t pt = tmem + D + (u & 1) * kKeys, v0 = values.at;
 #pragma unroll
                         for (int k = 0; k < kKeys / 16; ++k) {
                             mma_tmem_a_if(leader, tmem, pt + 8 * k, sdesc_values(v0 + k * 2048), kIdescO, i > 1 || k > 0);
@@ -999,19 +1129,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 }
                 return m;
             };
-            // e4m3: the scale of this row's scores, apart from the keys' exponent
-            float c_row = c;
-            if (kE4m3 && live) {
-                const uint4* const q = reinterpret_cast<const uint4*>(a.q + static_cast<long long>(it.row0 + t_row) * a.q_token_stride +
-                                                                      static_cast<long long>(head) * a.q_head_stride);
-                uint32_t bits = 0;
-#pragma unroll 8
-                for (int j = 0; j < D / 8; ++j) {
-                    const uint4 x = __ldg(q + j);
-                    bits = largest(largest(largest(largest(bits, x.x), x.y), x.z), x.w);
-                }
-                c_row = a.scale != 0.0f ? c * pow2(row_exponent(bits)) : c;
-            }
+            float c_row = c;   // e4m3: the scale of this row's scores, apart from the keys' exponent
             // The running maximum of the scores (to 2^kSlack) with the sum of the softmax against it; O is held against
             // m_out, for e4m3 that of score + exponent of the value row, times 2^kShift.
             float m = kNone, l = 0.0f, m_out = kNone;
@@ -1021,7 +1139,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     ok = false;
                     break;
                 }
-                if (threadIdx.x == 0) mbar_arrive(bar(kEmpty + (2 * t) % kSlots));   // the keys have been read
+                if (threadIdx.x == 0) mbar_arrive(bar(kEmpty + slot_of(2 * t).index));   // the keys have been read
                 __syncwarp();   // (TMEM is read by whole, converged warps)
                 tc_fence_after();
                 if (!idle) {
@@ -1030,6 +1148,24 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     tmem_ld32(at, x[0]);
                     tmem_ld32(at + 32, x[1]);
                     tmem_ld_wait2(x[0], x[1]);
+                    // e4m3: the keys' exponents; that of the values, as a rule one for all
+                    uint32_t info = 0;
+                    float cs = c, ev = 0.0f;
+                    if constexpr (kE4m3) {
+                        if (i == 0) c_row = fminf(fmaxf(c * pow2(s_qe[(seg & 3) * kRowsTile + row]), 1e-37f), 3e38f);   // (0 times -inf would be NaN)
+                        info = s_info[t % kInfos];
+                        cs = c_row;
+                        ev = static_cast<float>(static_cast<int>(info & 255u) - 127);
+                        const float4* const kf = reinterpret_cast<const float4*>(s_kf + t % kInfos * kKeys);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float4 f = kf[j];
+                            uint32_t* const v = &x[j >> 3][4 * (j & 7)];
+                            const Pair p0 = mul2(Pair{__uint_as_float(v[0]), __uint_as_float(v[1])}, Pair{f.x, f.y});
+                            const Pair p1 = mul2(Pair{__uint_as_float(v[2]), __uint_as_float(v[3])}, Pair{f.z, f.w});
+                            v[0] = __float_as_uint(p0.x), v[1] = __float_as_uint(p0.y), v[2] = __float_as_uint(p1.x), v[3] = __float_as_uint(p1.y);
+                        }
+                    }
                     if (bad || k0 < odd_from || k0 + kKeys > it.ctx) {
                         uint64_t keep = sees(k0);
                         if (bad) keep &= resident(k0);
@@ -1041,14 +1177,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                                 if (!(k >> j & 1u)) x[h][j] = 0xff800000u;
                         }
                     }
-                    // of the tile: exponents of the keys and of the values, the same for all rows as a rule
-                    uint32_t info = 0;
-                    float cs = c, ev = 0.0f;
-                    if (kE4m3) {
-                        info = s_info[t % kInfos];
-                        cs = fminf(fmaxf(c_row * pow2_of_byte(info & 255u), 1e-37f), 3e38f);   // (0 times -inf would be NaN)
-                        ev = static_cast<float>(static_cast<int>(info >> 8 & 255u) - 127);
-                    }
                     float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // (four chains)
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
@@ -1056,7 +1184,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * cs;
                     float top_out = top + ev;
                     bool apart = false;   // each key with its own exponents, and the softmax's sum with an exponential of its own
-                    if (kE4m3) apart = uniform((info >> 16) != 0 || fmaxf(m_out, top_out) - fmaxf(m, top) - ev > 60.0f);
+                    if (kE4m3) apart = uniform((info & 256u) != 0 || fmaxf(m_out, top_out) - fmaxf(m, top) - ev > 60.0f);
                     uint64_t keep = ~0ULL;
                     if (kE4m3 && apart) {
                         if (bad || k0 < odd_from || k0 + kKeys > it.ctx) keep = sees(k0) & (bad ? resident(k0) : ~0ULL);
@@ -1285,8 +1413,10 @@ cudaError_t launch(TreeArgs& a, cudaStream_t s)
     CUtensorMap map_k{}, map_v{};
     int rows = kKeys;
     while (a.page_size % rows != 0) rows /= 2;
-    a.box_rows = rows >= 8 && encode_cache_map(&map_k, a.k, kE4m3, D, a.page_size, a.n_kv_heads, a.n_pages, a.token_bytes, a.head_bytes, a.page_bytes, rows) &&
-                         encode_cache_map(&map_v, a.v, kE4m3, D, a.page_size, a.n_kv_heads, a.n_pages, a.token_bytes, a.head_bytes, a.page_bytes, rows)
+    auto encode = [&](CUtensorMap* map, const void* rows_of, CacheBox box) {
+        return encode_cache_map(map, rows_of, box, D, a.page_size, a.n_kv_heads, a.n_pages, a.token_bytes, a.head_bytes, a.page_bytes, rows);
+    };
+    a.box_rows = rows >= 8 && encode(&map_k, a.k, kE4m3 ? kCodesSwizzled : kBf16Swizzled) && encode(&map_v, a.v, kE4m3 ? kCodes : kBf16Swizzled)
                      ? rows : 0;
     const unsigned grid = static_cast<unsigned>(S::kCtas * std::min(num_sms(), kMaxSms));
     // at most so many items: every sequence has one row tile a key head, and one more per 128 rows
