@@ -136,12 +136,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
 // 16 columns, there when it returns.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
 {
@@ -449,24 +443,25 @@ __device__ __noinline__ float apart_weights(const TreeArgs& a, uint32_t at, uint
 {
     const Apart e(a, table, len, k0, hk, info);
     float sum = 0.0f;
-    uint32_t lo_part[32];   // (their columns hold scores until the end)
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        uint32_t x[32], hi_part[16], lo_part[16];
+        tmem_ld32(at + 32 * h, x);
+        tmem_ld_wait(x);
 #pragma unroll
-    for (int c = 0; c < kKeys; c += 16) {
-        uint32_t x[16], hi_part[8];
-        tmem_ld16(at + c, x);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float s0 = e.score(x[2 * j], c + 2 * j, keep, c_row), s1 = e.score(x[2 * j + 1], c + 2 * j + 1, keep, c_row);
+        for (int j = 0; j < 16; ++j) {
+            const int k = 32 * h + 2 * j;
+            const float s0 = e.score(x[2 * j], k, keep, c_row), s1 = e.score(x[2 * j + 1], k + 1, keep, c_row);
             sum += exp2_fast(s0 - m) + exp2_fast(s1 - m);
-            const float p0 = exp2_fast(s0 + (e.exponent(c + 2 * j) + kShift - m_out));
-            const float p1 = exp2_fast(s1 + (e.exponent(c + 2 * j + 1) + kShift - m_out));
+            const float p0 = exp2_fast(s0 + (e.exponent(k) + kShift - m_out));
+            const float p1 = exp2_fast(s1 + (e.exponent(k + 1) + kShift - m_out));
             hi_part[j] = pack_f16x2(p0, p1);
             const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi_part[j]));
-            lo_part[c / 2 + j] = pack_f16x2(p0 - back.x, p1 - back.y);
+            lo_part[j] = pack_f16x2(p0 - back.x, p1 - back.y);
         }
-        tmem_st8(at + c / 2, hi_part);
+        tmem_st16(at + 32 * h, hi_part);
+        tmem_st16(at + 32 * h + 16, lo_part);
     }
-    tmem_st32(at + 32, lo_part);
     return sum;
 }
 
@@ -1050,8 +1045,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                         const uint32_t pt = tmem + D + (u & 1) * kKeys, v0 = values.at;
 #pragma unroll
                         for (int k = 0; k < kKeys / 16; ++k) {
-                            mma_tmem_a_if(leader, tmem, pt + 8 * k, sdesc_values(v0 + k * 2048), kIdescO, i > 1 || k > 0);
-                            mma_tmem_a_if(leader, tmem, pt + kKeys / 2 + 8 * k, sdesc_values(v0 + k * 2048), kIdescO, 1);
+                            const uint32_t part = pt + 32 * (k >> 1) + 8 * (k & 1);
+                            mma_tmem_a_if(leader, tmem, part, sdesc_values(v0 + k * 2048), kIdescO, i > 1 || k > 0);
+                            mma_tmem_a_if(leader, tmem, part + 16, sdesc_values(v0 + k * 2048), kIdescO, 1);
                         }
                         commit_if(leader, bar(kODone));
                         if (uniform(i == count)) commit_if(leader, bar(kItemDone));
@@ -1144,10 +1140,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 tc_fence_after();
                 if (!idle) {
                     const uint32_t at = quarter + D + (t & 1) * kKeys;
-                    uint32_t x[2][32];
-                    tmem_ld32(at, x[0]);
-                    tmem_ld32(at + 32, x[1]);
-                    tmem_ld_wait2(x[0], x[1]);
                     // e4m3: the keys' exponents; that of the values, as a rule one for all
                     uint32_t info = 0;
                     float cs = c, ev = 0.0f;
@@ -1156,38 +1148,50 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                         info = s_info[t % kInfos];
                         cs = c_row;
                         ev = static_cast<float>(static_cast<int>(info & 255u) - 127);
-                        const float4* const kf = reinterpret_cast<const float4*>(s_kf + t % kInfos * kKeys);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float4 f = kf[j];
-                            uint32_t* const v = &x[j >> 3][4 * (j & 7)];
-                            const Pair p0 = mul2(Pair{__uint_as_float(v[0]), __uint_as_float(v[1])}, Pair{f.x, f.y});
-                            const Pair p1 = mul2(Pair{__uint_as_float(v[2]), __uint_as_float(v[3])}, Pair{f.z, f.w});
-                            v[0] = __float_as_uint(p0.x), v[1] = __float_as_uint(p0.y), v[2] = __float_as_uint(p1.x), v[3] = __float_as_uint(p1.y);
-                        }
                     }
-                    if (bad || k0 < odd_from || k0 + kKeys > it.ctx) {
-                        uint64_t keep = sees(k0);
+                    const bool masked = bad || k0 < odd_from || k0 + kKeys > it.ctx;
+                    uint64_t keep = ~0ULL;
+                    if (masked) {
+                        keep = sees(k0);
                         if (bad) keep &= resident(k0);
+                    }
+                    // half of the scores; -infinity where the row does not see the key
+                    auto scores = [&](int h, uint32_t (&x)[32]) {
+                        tmem_ld32(at + 32 * h, x);
+                        tmem_ld_wait(x);
+                        if constexpr (kE4m3) {
+                            const float4* const kf = reinterpret_cast<const float4*>(s_kf + t % kInfos * kKeys + 32 * h);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                            for (int j = 0; j < 8; ++j) {
+                                const float4 f = kf[j];
+                                uint32_t* const v = &x[4 * j];
+                                const Pair p0 = mul2(Pair{__uint_as_float(v[0]), __uint_as_float(v[1])}, Pair{f.x, f.y});
+                                const Pair p1 = mul2(Pair{__uint_as_float(v[2]), __uint_as_float(v[3])}, Pair{f.z, f.w});
+                                v[0] = __float_as_uint(p0.x), v[1] = __float_as_uint(p0.y), v[2] = __float_as_uint(p1.x), v[3] = __float_as_uint(p1.y);
+                            }
+                        }
+                        if (masked) {
                             const uint32_t k = static_cast<uint32_t>(keep >> (32 * h));
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                if (!(k >> j & 1u)) x[h][j] = 0xff800000u;
+                                if (!(k >> j & 1u)) x[j] = 0xff800000u;
                         }
-                    }
-                    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // (four chains)
+                    };
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t x[32];
+                        scores(h, x);
+                        float tops[4] = {top, -INFINITY, -INFINITY, -INFINITY};   // (four chains)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        tops[j & 3] = fmaxf(tops[j & 3], fmaxf(__uint_as_float(x[0][j]), __uint_as_float(x[1][j])));
-                    float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * cs;
+                        for (int j = 0; j < 32; ++j) tops[j & 3] = fmaxf(tops[j & 3], __uint_as_float(x[j]));
+                        top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                    }
+                    top *= cs;
                     float top_out = top + ev;
                     bool apart = false;   // each key with its own exponents, and the softmax's sum with an exponential of its own
                     if (kE4m3) apart = uniform((info & 256u) != 0 || fmaxf(m_out, top_out) - fmaxf(m, top) - ev > 60.0f);
-                    uint64_t keep = ~0ULL;
                     if (kE4m3 && apart) {
-                        if (bad || k0 < odd_from || k0 + kKeys > it.ctx) keep = sees(k0) & (bad ? resident(k0) : ~0ULL);
                         const float2 tops = apart_maxima(a, at, keep, table, it.len, k0, hk, info, c_row);
                         top = tops.x;
                         top_out = tops.y;
@@ -1231,12 +1235,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                         const float off = kE4m3 ? ev + kShift - m_out : -m;
                         Pair sum = {0.0f, 0.0f};
                         const Pair by = {cs, cs}, from = {off, off};
-#pragma unroll
+#pragma unroll 1
                         for (int h = 0; h < 2; ++h) {   // 32 keys: 16 columns of pairs
-                            uint32_t hi_part[16], lo_part[16];
+                            uint32_t x[32], hi_part[16], lo_part[16];
+                            scores(h, x);
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
-                                Pair p = fma2(Pair{__uint_as_float(x[h][2 * j]), __uint_as_float(x[h][2 * j + 1])}, by, from);
+                                Pair p = fma2(Pair{__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])}, by, from);
                                 p.x = exp2_fast(p.x);
                                 p.y = exp2_fast(p.y);
                                 sum = add2(sum, p);
@@ -1253,8 +1258,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                                 const Pair rest = add2(p, minus);
                                 lo_part[j] = kE4m3 ? pack_f16x2(rest.x, rest.y) : pack_bf16x2(rest.x, rest.y);
                             }
-                            tmem_st16(at + 16 * h, hi_part);
-                            tmem_st16(at + 32 + 16 * h, lo_part);
+                            tmem_st16(at + 32 * h, hi_part);
+                            tmem_st16(at + 32 * h + 16, lo_part);
                         }
                         l += kE4m3 ? (sum.x + sum.y) * exp2_fast(-off - m) : sum.x + sum.y;
                     }
