@@ -629,7 +629,8 @@ moe_status_t moe_tree_attention_workspace_init(void* ws_dev, size_t ws_bytes, vo
  * of drafted tokens (a token sees its ancestors and itself), or a short run of a prompt.
  *   row i of sequence b sees the context, tokens 0 .. c - 1 with c = seq_len[b] - n, and
  *   the drafted tokens (number j is cached at c + j) whose bit its mask has,
- * and its output is moe_paged_attention's over what it sees.  With a window those are the
+ * and its output is moe_paged_attention's over what it sees (MOE_KV_E4M3: of q's rows, values
+ * below 2^-10 of the largest are rounded to 2^-17 of it).  With a window those are the
  * last `window` of its path: the drafted tokens it sees, the highest numbers first, then
  * the context from its end.  A row that sees nothing, or no score above -inf, gets zeros
  * and lse = -inf.  What a row does not see (NaN and infinities included) has no effect on
