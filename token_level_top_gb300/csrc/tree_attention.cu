@@ -59,14 +59,19 @@ struct Shape {
     static constexpr int kTile = kPanel * D / 64;                         // bytes of a key or value tile of 16-bit values
     static constexpr int kQ = kRowsTile * D * 2;
     static constexpr int kBars = kE4m3 ? 4096 : 1024;
-    static constexpr int kShare = std::min(233472 / kCtas - 1024, 232448), kRoom = kShare - kBars - kQ;
+    // Items of at most 64 rows have them twice in the tile, each half with half of a tile's keys: where the softmax, not the
+    // copies, is what takes longest.  The halves are joined through 4 KB of shared memory.
+    static constexpr bool kSplit = kE4m3 || D == 64;
+    static constexpr int kSwap = kSplit ? 4096 : 0;
+    static constexpr int kCut = kE4m3 ? 16 : 32;                          // keys that a turn of the softmax's loops takes
+    static constexpr int kShare = std::min(233472 / kCtas - 1024, 232448), kRoom = kShare - kBars - kSwap - kQ;
     // One ring of slots for tiles; e4m3: one for keys, which stay codes, and one for values, which become f16 in their slots
     // (D = 64: behind the codes).
     static constexpr int kTileK = kE4m3 ? kKeys * D : kTile, kTileV = kE4m3 && D == 64 ? kTile + kKeys * D : kTile;
     static constexpr int kSlotsK = kE4m3 ? (D == 64 ? 6 : 3) : 0, kSlotsV = kE4m3 ? (kRoom - kSlotsK * kTileK) / kTileV : 0;
     static constexpr int kSlots = kE4m3 ? kSlotsK + kSlotsV : std::min(kRoom / kTile, 12);
     static constexpr int kRing = kE4m3 ? kSlotsK * kTileK + kSlotsV * kTileV : kSlots * kTile;
-    static constexpr int kSmem = kQ + kRing + kBars;
+    static constexpr int kSmem = kQ + kRing + kBars + kSwap;
     static constexpr int kCols = D <= 128 ? 256 : 512;                    // TMEM columns: O, then two tiles of scores
     static constexpr int kPart = kRowsTile * (D + 4);                     // floats of a part: O, then maximum, sum and O's maximum
     static_assert(kSlots >= 4 && (!kE4m3 || kSlotsV >= 3) && kSmem <= kShare && D + 2 * kKeys <= kCols, "room");
@@ -127,7 +132,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16])
 {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -136,8 +141,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 // 16 columns, there when it returns.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16])
 {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
@@ -146,6 +157,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
           "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32])
+{
+    tmem_ld32(taddr, r);
+    tmem_ld_wait(r);
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -428,7 +444,7 @@ __device__ __noinline__ float2 apart_maxima(const TreeArgs& a, uint32_t at, uint
 #pragma unroll 1
     for (int c = 0; c < kKeys; c += 16) {
         uint32_t x[16];
-        tmem_ld16(at + c, x);
+        tmem_ld(at + c, x);
         for (int j = 0; j < 16; ++j) {
             const float v = e.score(x[j], c + j, keep, c_row);
             top = fmaxf(top, v);
@@ -444,13 +460,12 @@ __device__ __noinline__ float apart_weights(const TreeArgs& a, uint32_t at, uint
     const Apart e(a, table, len, k0, hk, info);
     float sum = 0.0f;
 #pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-        uint32_t x[32], hi_part[16], lo_part[16];
-        tmem_ld32(at + 32 * h, x);
-        tmem_ld_wait(x);
+    for (int c = 0; c < kKeys; c += 16) {
+        uint32_t x[16], hi_part[8], lo_part[8];
+        tmem_ld(at + c, x);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const int k = 32 * h + 2 * j;
+        for (int j = 0; j < 8; ++j) {
+            const int k = c + 2 * j;
             const float s0 = e.score(x[2 * j], k, keep, c_row), s1 = e.score(x[2 * j + 1], k + 1, keep, c_row);
             sum += exp2_fast(s0 - m) + exp2_fast(s1 - m);
             const float p0 = exp2_fast(s0 + (e.exponent(k) + kShift - m_out));
@@ -459,8 +474,8 @@ __device__ __noinline__ float apart_weights(const TreeArgs& a, uint32_t at, uint
             const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi_part[j]));
             lo_part[j] = pack_f16x2(p0 - back.x, p1 - back.y);
         }
-        tmem_st16(at + 32 * h, hi_part);
-        tmem_st16(at + 32 * h + 16, lo_part);
+        tmem_st(at + c, hi_part);
+        tmem_st(at + c + 8, lo_part);
     }
     return sum;
 }
@@ -485,10 +500,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
     uint64_t* const bars = reinterpret_cast<uint64_t*>(s_ring + S::kRing);
     // A tile's scores are there (two buffers), its weights, its product with the values done; an item's last product
     // done, its output read; its rows of q there, and no longer read.  e4m3: a slot's codes there; bf16: a tile that the
-    // warp which copies it looks at.
+    // warp which copies it looks at.  One half's sums there, and read, for each of two pairs of warps.
     constexpr int kInfos = 8;
     constexpr int kFull = 0, kEmpty = kSlots, kSFull = 2 * kSlots, kPFull = kSFull + 2, kODone = kPFull + 2, kOFree = kODone + 1,
-                  kQFull = kOFree + 1, kQEmpty = kQFull + 1, kItemDone = kQEmpty + 1, kRawFull = kItemDone + 1, kCount = kRawFull + (kE4m3 ? S::kSlotsV : kCopyWarps);
+                  kQFull = kOFree + 1, kQEmpty = kQFull + 1, kItemDone = kQEmpty + 1, kRawFull = kItemDone + 1, kSwapFull = kRawFull + (kE4m3 ? S::kSlotsV : kCopyWarps), kSwapEmpty = kSwapFull + 2, kCount = kSwapFull + (S::kSplit ? 4 : 0);
     static_assert(kCount * 8 + static_cast<int>(sizeof(Start)) + 16 * 8 + 16 + (kE4m3 ? kInfos * (4 + 4 * kKeys) + S::kSlotsV * kKeys + 4 * kRowsTile : 0) <= S::kBars, "room for the barriers");
     Start* const s_start = reinterpret_cast<Start*>(bars + kCount);
     long long* const s_scan = reinterpret_cast<long long*>(s_start + 1);
@@ -618,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
         const int i = threadIdx.x, copies = a.box_rows > 0 ? 1 : 32;   // one arrival by boxes, else each lane's
         int count = 1;
         if (i < kEmpty) count = kE4m3 && i >= S::kSlotsK ? kCopyWarps - 1 : copies;   // (e4m3 values: the warps that turn them into f16)
-        if (i >= kRawFull) count = copies;
+        if (i >= kRawFull && i < kSwapFull) count = copies;
         if ((i >= kPFull && i < kODone) || i == kOFree) count = kSoftmaxWarps;
         if (i == kQFull) count = 32 * kCopyWarps;
         mbar_init(bar(i), count);
@@ -743,6 +758,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     return smem_u32(s_q) + (piece >> 3) * (kRowsTile * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
                 };
                 const int rows = a.scale != 0.0f ? it.draft * group - row_at : 0;   // live ones
+                const bool twice = S::kSplit && it.draft * group - row_at <= kRowsTile / 2;
+                const int distinct = twice ? kRowsTile / 2 : kRowsTile;
                 if constexpr (kE4m3) {
                     // Two e4m3 rows for each, one tile behind the other.  (One piece a turn: the code is run once an item, so what it
                     // costs is to fetch it.)
@@ -757,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     int r = kRows * mine_of + lane / kPieces;
                     uint4 next = fetch(r), after = fetch(r + kStep);
 #pragma unroll 1
-                    for (; uniform(r - lane / kPieces < kRowsTile); r += kStep) {
+                    for (; uniform(r - lane / kPieces < distinct); r += kStep) {
                         const uint4 x = next;
                         next = after;
                         after = fetch(r + 2 * kStep);
@@ -777,9 +794,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                             hi[j >> 1] |= two << (16 * (j & 1));
                             lo[j >> 1] |= two_codes(v0 - back.x, v1 - back.y) << (16 * (j & 1));
                         }
-                        if (r < kRowsTile) {
+                        if (r < distinct) {
                             sts64(code_at<D>(smem_u32(s_q), kRowsTile, r, 8 * piece), make_uint2(hi[0], hi[1]));
                             sts64(code_at<D>(smem_u32(s_q) + kRowsTile * D, kRowsTile, r, 8 * piece), make_uint2(lo[0], lo[1]));
+                            if (twice) {
+                                sts64(code_at<D>(smem_u32(s_q), kRowsTile, r + distinct, 8 * piece), make_uint2(hi[0], hi[1]));
+                                sts64(code_at<D>(smem_u32(s_q) + kRowsTile * D, kRowsTile, r + distinct, 8 * piece), make_uint2(lo[0], lo[1]));
+                            }
                             if (piece == 0) s_qe[(seg & 3) * kRowsTile + r] = static_cast<int8_t>(e);
                         }
                     }
@@ -791,14 +812,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
 #pragma unroll 1
                     for (int r1 = 8 * mine_of; r1 < kRowsTile; r1 += 8 * kCopyWarps) {
                         // lane j: row r1 + j % 8
-                        const int mine = r1 + (lane & 7), t = a.tokens_of(row_at + mine);
+                        const int first = r1 & (distinct - 1), mine = first + (lane & 7), t = a.tokens_of(row_at + mine);
                         const long long place = mine < rows ? (it.row0 + t) * a.q_token_stride +
                                                                   (hk * group + (row_at + mine - t * group)) * a.q_head_stride : 0;
 #pragma unroll
                         for (int i = 0; i < kPieces / 4; ++i) {
                             const int r = (i * 32 + lane) / kPieces, piece = (i * 32 + lane) % kPieces;
                             const long long from = __shfl_sync(0xffffffffu, place, r);
-                            copy_async_or_zeros(at(r1 + r, piece), a.q + from + 8 * piece, r1 + r < rows);
+                            copy_async_or_zeros(at(r1 + r, piece), a.q + from + 8 * piece, first + r < rows);
                         }
                     }
                     if (a.scale >= 0.0f) {
@@ -1045,9 +1066,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                         const uint32_t pt = tmem + D + (u & 1) * kKeys, v0 = values.at;
 #pragma unroll
                         for (int k = 0; k < kKeys / 16; ++k) {
-                            const uint32_t part = pt + 32 * (k >> 1) + 8 * (k & 1);
+                            const uint32_t part = pt + 16 * k / S::kCut * S::kCut + 16 * k % S::kCut / 2;
                             mma_tmem_a_if(leader, tmem, part, sdesc_values(v0 + k * 2048), kIdescO, i > 1 || k > 0);
-                            mma_tmem_a_if(leader, tmem, part + 16, sdesc_values(v0 + k * 2048), kIdescO, 1);
+                            mma_tmem_a_if(leader, tmem, part + S::kCut / 2, sdesc_values(v0 + k * 2048), kIdescO, 1);
                         }
                         commit_if(leader, bar(kODone));
                         if (uniform(i == count)) commit_if(leader, bar(kItemDone));
@@ -1069,13 +1090,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax and output
-        const int row = threadIdx.x;
+        int swaps = 0;   // buffers that have gone from half to half
         const uint32_t quarter = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         for (; it.n > 0 && it.off + g0 < hi && ok; ++seg) {
             const int g1 = static_cast<int>(min(static_cast<long long>(it.n), hi - it.off)), count = g1 - g0;
             const int mtiles = it.items / a.n_kv_heads, hk = it.h / mtiles, row_at = (it.h - hk * mtiles) * kRowsTile;
             const int rows = min(kRowsTile, it.draft * group - row_at);
-            const bool live = row < rows, idle = warp * 32 >= rows;   // idle: none of the warp's rows is a live one
+            const bool twice = S::kSplit && rows <= kRowsTile / 2;
+            const int distinct = twice ? kRowsTile / 2 : kRowsTile, row = threadIdx.x & (distinct - 1), half = threadIdx.x / distinct;
+            const bool live = row < rows, idle = (warp * 32 & (distinct - 1)) >= rows;   // idle: none of the warp's rows is a live one
             const int t_row = a.tokens_of(row_at + row), head = hk * group + (row_at + row) - t_row * group;
             // what the row sees: drafted tokens `seen`, context from `from` on
             uint64_t seen = 0;
@@ -1149,20 +1172,21 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                         cs = c_row;
                         ev = static_cast<float>(static_cast<int>(info & 255u) - 127);
                     }
+                    const int c0 = twice ? kKeys / 2 * half : 0, c1 = twice ? c0 + kKeys / 2 : kKeys;   // the row's keys of the tile
                     const bool masked = bad || k0 < odd_from || k0 + kKeys > it.ctx;
                     uint64_t keep = ~0ULL;
                     if (masked) {
                         keep = sees(k0);
                         if (bad) keep &= resident(k0);
                     }
-                    // half of the scores; -infinity where the row does not see the key
-                    auto scores = [&](int h, uint32_t (&x)[32]) {
-                        tmem_ld32(at + 32 * h, x);
-                        tmem_ld_wait(x);
+                    // some of the scores; -infinity where the row does not see the key
+                    constexpr int kCut = S::kCut;
+                    auto scores = [&](int c, uint32_t (&x)[kCut]) {
+                        tmem_ld(at + c, x);
                         if constexpr (kE4m3) {
-                            const float4* const kf = reinterpret_cast<const float4*>(s_kf + t % kInfos * kKeys + 32 * h);
+                            const float4* const kf = reinterpret_cast<const float4*>(s_kf + t % kInfos * kKeys + c);
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
+                            for (int j = 0; j < kCut / 4; ++j) {
                                 const float4 f = kf[j];
                                 uint32_t* const v = &x[4 * j];
                                 const Pair p0 = mul2(Pair{__uint_as_float(v[0]), __uint_as_float(v[1])}, Pair{f.x, f.y});
@@ -1171,20 +1195,20 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                             }
                         }
                         if (masked) {
-                            const uint32_t k = static_cast<uint32_t>(keep >> (32 * h));
+                            const uint32_t k = static_cast<uint32_t>(keep >> c);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
+                            for (int j = 0; j < kCut; ++j)
                                 if (!(k >> j & 1u)) x[j] = 0xff800000u;
                         }
                     };
                     float top = -INFINITY;
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t x[32];
-                        scores(h, x);
+                    for (int c = c0; c < c1; c += kCut) {
+                        uint32_t x[kCut];
+                        scores(c, x);
                         float tops[4] = {top, -INFINITY, -INFINITY, -INFINITY};   // (four chains)
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) tops[j & 3] = fmaxf(tops[j & 3], __uint_as_float(x[j]));
+                        for (int j = 0; j < kCut; ++j) tops[j & 3] = fmaxf(tops[j & 3], __uint_as_float(x[j]));
                         top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                     }
                     top *= cs;
@@ -1192,6 +1216,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     bool apart = false;   // each key with its own exponents, and the softmax's sum with an exponential of its own
                     if (kE4m3) apart = uniform((info & 256u) != 0 || fmaxf(m_out, top_out) - fmaxf(m, top) - ev > 60.0f);
                     if (kE4m3 && apart) {
+                        if (twice) keep &= 0xffffffffULL << (32 * half);
                         const float2 tops = apart_maxima(a, at, keep, table, it.len, k0, hk, info, c_row);
                         top = tops.x;
                         top_out = tops.y;
@@ -1236,11 +1261,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                         Pair sum = {0.0f, 0.0f};
                         const Pair by = {cs, cs}, from = {off, off};
 #pragma unroll 1
-                        for (int h = 0; h < 2; ++h) {   // 32 keys: 16 columns of pairs
-                            uint32_t x[32], hi_part[16], lo_part[16];
-                            scores(h, x);
+                        for (int c = c0; c < c1; c += kCut) {   // in the scores' place: the first parts, two a column, then the second
+                            uint32_t x[kCut], hi_part[kCut / 2], lo_part[kCut / 2];
+                            scores(c, x);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
+                            for (int j = 0; j < kCut / 2; ++j) {
                                 Pair p = fma2(Pair{__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])}, by, from);
                                 p.x = exp2_fast(p.x);
                                 p.y = exp2_fast(p.y);
@@ -1258,10 +1283,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                                 const Pair rest = add2(p, minus);
                                 lo_part[j] = kE4m3 ? pack_f16x2(rest.x, rest.y) : pack_bf16x2(rest.x, rest.y);
                             }
-                            tmem_st16(at + 32 * h, hi_part);
-                            tmem_st16(at + 32 * h + 16, lo_part);
+                            tmem_st(at + c, hi_part);
+                            tmem_st(at + c + kCut / 2, lo_part);
                         }
                         l += kE4m3 ? (sum.x + sum.y) * exp2_fast(-off - m) : sum.x + sum.y;
+                        if (twice) {
+                            const uint32_t none[16] = {0};
+                            tmem_st(at + 32 * (1 - half), none);
+                            tmem_st(at + 32 * (1 - half) + 16, none);
+                        }
                     }
                     tmem_st_wait();
                 }
@@ -1278,16 +1308,70 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 const int slot = 2 * blockIdx.x + (g0 == 0 ? 1 : 0);
                 float* const part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kTreeCtrlBytes + sizeof(Header) * kMaxBlocks) +
                                     static_cast<long long>(slot) * S::kPart;
+                // Rows that are there twice: the upper half's maxima and sum, then its O by 16 columns, to the lower half, which joins
+                // them.  Four float4 [32] for each of the two pairs of warps.
+                float f_mine = 1.0f, f_other = 0.0f;
+                const int pair = warp & 1;
+                const uint32_t swap = smem_u32(bars) + S::kBars + pair * 2048 + lane * 16;
+                auto give = [&](const uint32_t (&x)[16], int n) {   // the upper half
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(kSwapEmpty + pair), (swaps & 1) ^ 1, kSpinBudget));
+                    if (!ok) return;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (4 * i < n) sts128(swap + 512 * i, make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kSwapFull + pair));
+                    ++swaps;
+                };
+                auto take = [&](uint32_t (&x)[16], int n) {   // the lower half
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(kSwapFull + pair), swaps & 1, kSpinBudget));
+                    if (!ok) return;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (4 * i < n) {
+                            const uint4 v = lds128(swap + 512 * i);
+                            x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+                        }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kSwapEmpty + pair));
+                    ++swaps;
+                };
+                if (twice) {
+                    uint32_t u[16] = {__float_as_uint(m), __float_as_uint(l), __float_as_uint(m_out)};
+                    if (half == 1) {
+                        give(u, 4);
+                    } else {
+                        take(u, 4);
+                        const float m1 = __uint_as_float(u[0]), l1 = __uint_as_float(u[1]), out1 = __uint_as_float(u[2]);
+                        const float both = fmaxf(m, m1), both_out = fmaxf(m_out, out1);
+                        l = l * exp2_fast(m - both) + l1 * exp2_fast(m1 - both);
+                        f_mine = exp2_fast(m_out - both_out);
+                        f_other = exp2_fast(out1 - both_out);
+                        m = both;
+                        m_out = both_out;
+                    }
+                }
                 // (what O is held against, as a power of two over the sum's)
                 const float over = kE4m3 ? m_out - kShift - m : 0.0f;
                 const float inv = l > 0.0f ? (kE4m3 ? exp2_fast(fminf(over, 126.0f)) : 1.0f) / l : (l == 0.0f ? 0.0f : NAN);
                 const bool odd = *s_odd != 0;
                 __nv_bfloat16* const out = a.out + static_cast<long long>(it.row0 + t_row) * a.out_token_stride + static_cast<long long>(head) * a.out_head_stride;
 #pragma unroll 1
-                for (int d = 0; d < D; d += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(quarter + d, o);
-                    tmem_ld_wait(o);
+                for (int d = 0; d < D; d += 16) {
+                    uint32_t o[16];
+                    tmem_ld(quarter + d, o);
+                    if (twice) {
+                        if (half == 1) {
+                            give(o, 16);
+                        } else {
+                            uint32_t other[16] = {};
+                            take(other, 16);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                o[j] = __float_as_uint(fmaf(__uint_as_float(o[j]), f_mine, __uint_as_float(other[j]) * f_other));
+                        }
+                        if (half == 1) continue;
+                    }
                     if (odd) {
                         // value rows of tiles where rows differ have lost their NaN and infinities: to the rows that see them
                         for (int i = 0; i < count; ++i) {
@@ -1301,7 +1385,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                                 if (e < 0 || e >= a.n_pages) continue;
                                 const char* const v = a.v + e * a.page_bytes + (key - pg * a.page_size) * a.token_bytes + hk * a.head_bytes;
 #pragma unroll
-                                for (int u = 0; u < 32; ++u) {
+                                for (int u = 0; u < 16; ++u) {
                                     float x = 0.0f;
                                     if (kE4m3) {
                                         const uint8_t code = __ldg(reinterpret_cast<const uint8_t*>(v) + d + u);
@@ -1315,9 +1399,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                             }
                         }
                     }
-                    if (live && whole) {
+                    if (live && whole) {   // (the upper half of rows that are there twice is through)
 #pragma unroll
-                        for (int u = 0; u < 32; u += 8) {
+                        for (int u = 0; u < 16; u += 8) {
                             uint32_t w[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
@@ -1326,14 +1410,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                         }
                     } else if (live) {   // [4 columns][row]: whole lines
 #pragma unroll
-                        for (int u = 0; u < 32; u += 4)
+                        for (int u = 0; u < 16; u += 4)
                             reinterpret_cast<uint4*>(part)[((d + u) >> 2) * kRowsTile + row] = make_uint4(o[u], o[u + 1], o[u + 2], o[u + 3]);
                     }
                     __syncwarp();   // TMEM is read by whole warps
                 }
-                if (live && whole && a.lse)
+                if (live && half == 0 && whole && a.lse)
                     a.lse[static_cast<long long>(it.row0 + t_row) * a.n_heads + head] = l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l));
-                if (live && !whole) reinterpret_cast<float4*>(part + kRowsTile * D)[row] = make_float4(m, l, kE4m3 ? m_out - kShift : m, 0.0f);
+                if (live && half == 0 && !whole) reinterpret_cast<float4*>(part + kRowsTile * D)[row] = make_float4(m, l, kE4m3 ? m_out - kShift : m, 0.0f);
                 if (threadIdx.x == 0 && whole && a.by_item > 0) headers[it.ordinal].last = -1;
                 if (threadIdx.x == 0 && g0 == 0 && !whole) {
                     Header h;
