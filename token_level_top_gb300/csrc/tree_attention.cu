@@ -480,6 +480,49 @@ __device__ __noinline__ float apart_weights(const TreeArgs& a, uint32_t at, uint
     return sum;
 }
 
+// Bit j: the row that sees the context's keys from `from` on and drafted tokens `seen` sees key k0 + j.
+__device__ __forceinline__ uint64_t seen_of(int k0, int from, int ctx, uint64_t seen)
+{
+    const int lo_bit = min(max(from - k0, 0), 64), hi_bit = min(max(ctx - k0, 0), 64), shift = k0 - ctx;
+    uint64_t m = 0;
+    if (hi_bit > lo_bit) m = (hi_bit == 64 ? ~0ULL : (1ULL << hi_bit) - 1ULL) & (~0ULL << lo_bit);
+    if (shift >= 0)
+        m |= shift < 64 ? seen >> shift : 0ULL;
+    else
+        m |= shift > -64 ? seen << -shift : 0ULL;
+    return m;
+}
+// Value rows of tiles where rows differ have lost their NaN and infinities: to the outputs of the row, or the sums of its
+// part, if it sees them.  (Rare, so it is as little code as can be, out of the way.)
+template <int D, bool kE4m3>
+__device__ __noinline__ void add_odd(const TreeArgs& a, const int32_t* table, __nv_bfloat16* out, float* part, int key_lo, int key_hi, int odd_from,
+                                     int ctx, int from, int hk, uint64_t seen)
+{
+#pragma unroll 1
+    for (int key = key_lo; key < key_hi; ++key) {
+        const int k0 = key - (key - key_lo) % kKeys;
+        if (!(k0 < odd_from || k0 + kKeys > ctx) || !(seen_of(key, from, ctx, seen) & 1)) continue;
+        const int pg = key / a.page_size, e = __ldg(table + pg);
+        if (e < 0 || e >= a.n_pages) continue;
+        const char* const v = a.v + e * a.page_bytes + (key - pg * a.page_size) * a.token_bytes + hk * a.head_bytes;
+#pragma unroll 1
+        for (int d = 0; d < D; ++d) {
+            float x = 0.0f;
+            if (kE4m3) {
+                if ((__ldg(reinterpret_cast<const uint8_t*>(v) + d) & 0x7f) == 0x7f) x = NAN;
+            } else {
+                const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(v) + d);
+                if ((h & 0x7f80u) == 0x7f80u) x = __uint_as_float(h << 16);
+            }
+            if (x == 0.0f) continue;
+            if (out)
+                out[d] = __float2bfloat16(__bfloat162float(out[d]) + x);
+            else
+                part[(d >> 2) * (4 * kRowsTile) + (d & 3)] += x;
+        }
+    }
+}
+
 // ---------------------------------------------------------------- the main kernel
 
 struct Start {
@@ -635,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
         if (i < kEmpty) count = kE4m3 && i >= S::kSlotsK ? kCopyWarps - 1 : copies;   // (e4m3 values: the warps that turn them into f16)
         if (i >= kRawFull && i < kSwapFull) count = copies;
         if ((i >= kPFull && i < kODone) || i == kOFree) count = kSoftmaxWarps;
-        if (i == kQFull) count = 32 * kCopyWarps;
+        if (i == kQFull) count = 32 * (kE4m3 ? kCopyWarps - 1 : kCopyWarps);
         mbar_init(bar(i), count);
         mbar_fence_init();
     }
@@ -658,8 +701,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
 
     if (warp >= kSoftmaxWarps && warp < kProductWarp) {
         // ------------------------------------------------------------ copies
-        // bf16: a warp takes every third slot's tile as a whole.  e4m3: the first warp copies, the others turn keys and
-        // values into bf16.
+        // bf16: a warp takes every third slot's tile as a whole.  e4m3: the first warp copies, the others turn rows of q into two
+        // of e4m3 and values into f16.
         const int mine_of = warp - kSoftmaxWarps;
         const uint32_t leader = elected();
         int looked = 0;   // bf16: tiles that this warp has looked at
@@ -763,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 if constexpr (kE4m3) {
                     // Two e4m3 rows for each, one tile behind the other.  (One piece a turn: the code is run once an item, so what it
                     // costs is to fetch it.)
-                    constexpr int kRows = 32 / kPieces, kStep = kRows * kCopyWarps;   // rows of a warp at a time
+                    constexpr int kRows = 32 / kPieces, kStep = kRows * (kCopyWarps - 1);   // rows of a warp at a time
                     const int piece = lane % kPieces;
                     auto fetch = [&](int r) {
                         if (r >= rows || r >= kRowsTile) return make_uint4(0, 0, 0, 0);
@@ -771,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                         return __ldg(reinterpret_cast<const uint4*>(a.q + (it.row0 + t) * a.q_token_stride +
                                                                     (hk * group + (row_at + r - t * group)) * a.q_head_stride + 8 * piece));
                     };
-                    int r = kRows * mine_of + lane / kPieces;
+                    int r = kRows * (mine_of - 1) + lane / kPieces;
                     uint4 next = fetch(r), after = fetch(r + kStep);
 #pragma unroll 1
                     for (; uniform(r - lane / kPieces < distinct); r += kStep) {
@@ -869,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     if (!wait_for(kRawFull + mine_of, looked++ & 1)) break;
                     const int live = min(kKeys, it.len - first_key(n));
                     uint32_t odd = 0;
-#pragma unroll 4
+#pragma unroll 1
                     for (int i = lane; i < S::kTile / 16; i += 32) {   // (rows of 128 bytes: the order within does not matter)
                         const uint32_t at = to.at + 16 * i;
                         uint4 x = lds128(at);
@@ -912,8 +955,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 // (what a tile needs is asked for a tile and two tiles before)
                 int n = n0, pages[2];
                 look_up(n);
-                bool q_there = seg == 0;
-                if (q_there && !copy_q()) break;
                 pages[0] = entry[0], pages[1] = entry[1];
                 exponents(n);
                 look_up(n + 2);
@@ -935,15 +976,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     if (lane == 0) s_info[tile] = ref;
                     __syncwarp();
                     copy_tile(n, pages, {k.at, v.at}, {bar(kFull + k.index), bar(kRawFull + raw)});
-                    if (!ok || (!q_there && !copy_q())) break;
-                    q_there = true;
+                    if (!ok) break;
                     pages[0] = following[0], pages[1] = following[1];
                 }
             } else {
                 if (!copy_q()) break;
                 // value tiles into f16, half of the rows a warp
                 constexpr int kPieces = D / 16, kStep = 32 / kPieces, kCount = kKeys / 2 * kPieces / 32;   // pieces of 16 codes
-                constexpr int kBatch = std::min(kCount, 4);
+                constexpr int kBatch = std::min(kCount, 2);
                 const int piece = lane % kPieces, half = 32 * (mine_of - 1), r0 = half + lane / kPieces;
                 for (int n = n0 + 1; uniform(n < n_end); n += 2) {
                     const bool look = uniform(mixed(n));
@@ -957,7 +997,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     const float f = (info & 256u) != 0 || half + lane >= live ? 1.0f : pow2(max(d, -kNarrow));
                     const uint32_t mine = pack_f16x2(f, f);
                     const uint32_t to = v.at + (piece >> 2) * kPanel;
-                    uint32_t odd = 0;
 #pragma unroll 1
                     for (int i0 = 0; i0 < kCount; i0 += kBatch) {   // (rolled: the block's warps share one instruction cache)
                         uint4 w[kBatch];
@@ -974,15 +1013,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                             f16_of_codes(w[i].y, scale, x.z, x.w);
                             f16_of_codes(w[i].z, scale, y.x, y.y);
                             f16_of_codes(w[i].w, scale, y.z, y.w);
-                            if (look) {   // (a branch of its own: not on the usual way)
-                                const uint32_t any = odd_bits_f16(x.x) | odd_bits_f16(x.y) | odd_bits_f16(x.z) | odd_bits_f16(x.w) |
-                                                     odd_bits_f16(y.x) | odd_bits_f16(y.y) | odd_bits_f16(y.z) | odd_bits_f16(y.w);
-                                odd |= any;
-                                if (any) {
-                                    x = make_uint4(without_odd_f16(x.x), without_odd_f16(x.y), without_odd_f16(x.z), without_odd_f16(x.w));
-                                    y = make_uint4(without_odd_f16(y.x), without_odd_f16(y.y), without_odd_f16(y.z), without_odd_f16(y.w));
-                                }
-                            }
                             // pieces 2 p and 2 p + 1 of the row, in the order that keeps a row's lanes in different banks
                             const bool turn = (piece & 4) != 0;
                             const int c = (2 * piece) & 7, c0 = turn ? c + 1 : c, c1 = turn ? c : c + 1;
@@ -990,7 +1020,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                             sts128(to + r * 128 + ((c1 ^ (r & 7)) << 4), turn ? x : y);
                         }
                     }
-                    if (odd) *s_odd = 1;
+                    if (look) {   // the warp's rows, 128 bytes of each panel
+                        uint32_t odd = 0;
+                        __syncwarp();
+#pragma unroll 1
+                        for (int i = lane; i < kKeys / 2 * (D / 8); i += 32) {
+                            const uint32_t at = v.at + (i >> 8) * kPanel + half * 128 + (i & 255) * 16;
+                            const uint4 x = lds128(at);
+                            const uint32_t any = odd_bits_f16(x.x) | odd_bits_f16(x.y) | odd_bits_f16(x.z) | odd_bits_f16(x.w);
+                            odd |= any;
+                            if (any) sts128(at, make_uint4(without_odd_f16(x.x), without_odd_f16(x.y), without_odd_f16(x.z), without_odd_f16(x.w)));
+                        }
+                        if (odd) *s_odd = 1;
+                    }
                     fence_proxy_async_shared();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(kFull + v.index));
@@ -1126,18 +1168,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 if (bad && lane == 0) record_error(a.status, MOE_ERR_INDEX);
             }
             const int odd_from = a.window > 0 ? max(0, it.ctx - a.window + it.draft) : 0;
-            // bit j: the row sees key k0 + j
-            auto sees = [&](int k0) {
-                const int lo_bit = min(max(from - k0, 0), 64), hi_bit = min(max(it.ctx - k0, 0), 64);
-                uint64_t m = 0;
-                if (hi_bit > lo_bit) m = (hi_bit == 64 ? ~0ULL : (1ULL << hi_bit) - 1ULL) & (~0ULL << lo_bit);
-                const int shift = k0 - it.ctx;
-                if (shift >= 0)
-                    m |= shift < 64 ? seen >> shift : 0ULL;
-                else
-                    m |= shift > -64 ? seen << -shift : 0ULL;
-                return m;
-            };
+            auto sees = [&](int k0) { return seen_of(k0, from, it.ctx, seen); };
             auto resident = [&](int k0) {   // the same of all rows: keys of a page in range
                 uint64_t m = 0;
 #pragma unroll
@@ -1354,7 +1385,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 // (what O is held against, as a power of two over the sum's)
                 const float over = kE4m3 ? m_out - kShift - m : 0.0f;
                 const float inv = l > 0.0f ? (kE4m3 ? exp2_fast(fminf(over, 126.0f)) : 1.0f) / l : (l == 0.0f ? 0.0f : NAN);
-                const bool odd = *s_odd != 0;
                 __nv_bfloat16* const out = a.out + static_cast<long long>(it.row0 + t_row) * a.out_token_stride + static_cast<long long>(head) * a.out_head_stride;
 #pragma unroll 1
                 for (int d = 0; d < D; d += 16) {
@@ -1372,33 +1402,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                         }
                         if (half == 1) continue;
                     }
-                    if (odd) {
-                        // value rows of tiles where rows differ have lost their NaN and infinities: to the rows that see them
-                        for (int i = 0; i < count; ++i) {
-                            const int k0 = key_lo + i * kKeys;
-                            if (!(k0 < odd_from || k0 + kKeys > it.ctx)) continue;
-                            const uint64_t keep = sees(k0);
-                            for (int j = 0; j < kKeys; ++j) {
-                                const int key = k0 + j;
-                                if (!live || !(keep >> j & 1) || key >= it.len) continue;
-                                const int pg = key / a.page_size, e = __ldg(table + pg);
-                                if (e < 0 || e >= a.n_pages) continue;
-                                const char* const v = a.v + e * a.page_bytes + (key - pg * a.page_size) * a.token_bytes + hk * a.head_bytes;
-#pragma unroll
-                                for (int u = 0; u < 16; ++u) {
-                                    float x = 0.0f;
-                                    if (kE4m3) {
-                                        const uint8_t code = __ldg(reinterpret_cast<const uint8_t*>(v) + d + u);
-                                        if ((code & 0x7f) == 0x7f) x = NAN;
-                                    } else {
-                                        const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(v) + d + u);
-                                        if ((h & 0x7f80u) == 0x7f80u) x = __uint_as_float(h << 16);
-                                    }
-                                    if (x != 0.0f) o[u] = __float_as_uint(__uint_as_float(o[u]) + x);
-                                }
-                            }
-                        }
-                    }
                     if (live && whole) {   // (the upper half of rows that are there twice is through)
 #pragma unroll
                         for (int u = 0; u < 16; u += 8) {
@@ -1415,6 +1418,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     }
                     __syncwarp();   // TMEM is read by whole warps
                 }
+                if (*s_odd != 0 && live && half == 0)
+                    add_odd<D, kE4m3>(a, table, whole ? out : nullptr, part + row * 4, key_lo, key_hi, odd_from, it.ctx, from, hk, seen);
                 if (live && half == 0 && whole && a.lse)
                     a.lse[static_cast<long long>(it.row0 + t_row) * a.n_heads + head] = l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l));
                 if (live && half == 0 && !whole) reinterpret_cast<float4*>(part + kRowsTile * D)[row] = make_float4(m, l, kE4m3 ? m_out - kShift : m, 0.0f);
