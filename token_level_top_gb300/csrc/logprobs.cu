@@ -311,9 +311,9 @@ __device__ __forceinline__ int maximum_place(int reader)
 
 // The best n keys of pieces [lo, hi) of a row and the edge values into s.best (0 where there are none), sorted: by
 // NT threads, from the maxima of the groups of pieces that R readers took.
-template <class T, int NT, int R>
+template <class T, int NT, int R, bool kBeam>
 __device__ void find_best(Finder& s, const T* tops, uint64_t* keys, const Row<T>& row, int n, int lo, int hi,
-                          int per_group, int groups, int t, int edge, float edge_value, bool masked_too)
+                          int per_group, int groups, int t, int edge, float edge_value)
 {
     constexpr int kN = Piece<T>::kN, kNTWarps = NT / 32;
     const int lane = t & 31, warp = t >> 5;
@@ -360,9 +360,9 @@ __device__ void find_best(Finder& s, const T* tops, uint64_t* keys, const Row<T>
     // compared as values: NaN never reaches the level, unless that is 0 and takes everything
     const float level_value = value_of(level);
     const bool any = level == 0u;
-    // fewer than n threads with anything but masked values: those above are looked for at once (64 x 8 rows of 131072
-    // fp32, one in twenty masked but for a value: TAG us, TAG when the masked ones were counted first)
-    const bool masked = level_value == -INFINITY;
+    // Beams: fewer than n threads with anything but masked values, which are no candidates; those above are looked for at
+    // once (64 x 8 rows of 131072 fp32, one in twenty masked but for a value: 50 us, 132 when the masked ones were counted).
+    const bool masked = kBeam && level_value == -INFINITY;
     // the maxima that reach it, listed warp by warp
     static_assert(kMaxima / NT <= 32, "a bit per maximum of a thread");
     uint32_t hits = 0;
@@ -447,7 +447,7 @@ __device__ void find_best(Finder& s, const T* tops, uint64_t* keys, const Row<T>
         sync_finders<NT>();
         // fewer than n: the values at the level when those above it alone were ranked, then (level = that of
         // -inf) the NaNs, each in the order of their indices
-        int have = masked && !masked_too ? n : found;
+        int have = masked ? n : found;
         for (int pass = strict ? 0 : 1; pass < 2 && have < n; ++pass) {
             const uint32_t want = pass == 0 ? level : 0u;
             if (pass == 1 && level == 0u) break;   // they were ranked with the rest
@@ -612,7 +612,8 @@ __device__ __forceinline__ int given_token(const LogprobArgs& a, long long r)
     return token >= a.vocab ? -1 : token;
 }
 
-// What the outputs of a row take from its statistics.
+// What the outputs of a row take from its statistics; kBeam: the values themselves, with the maximum and sum beside them.
+template <bool kBeam>
 struct Result {
     bool none;            // nothing but -inf in the row
     float ref, log_l;     // log_l: ln sum e^(x - ref)
@@ -631,7 +632,7 @@ struct Result {
     __device__ __forceinline__ void write(const LogprobArgs& a, long long r, const Stats& s, int token, float given) const
     {
         if (s.l != s.l) record_error(a.status, MOE_ERR_NONFINITE);
-        if (a.stats) a.stats[r] = make_float2(ref, s.l * unturned(Stats::off(s.m)));
+        if (kBeam) a.stats[r] = make_float2(ref, s.l * unturned(Stats::off(s.m)));
         if (a.lse) a.lse[r] = ref + log_l;
         if (a.entropy) a.entropy[r] = none ? 0.0f : logf(s.l) - s.w / s.l * kLn2;   // (the same off(m) in both)
         if (a.logprob) a.logprob[r] = token < 0 ? 0.0f : logprob(given);
@@ -639,12 +640,13 @@ struct Result {
     __device__ __forceinline__ void write_top(const LogprobArgs& a, long long r, int at, uint64_t key) const
     {
         a.top_ids[r * a.n_top + at] = key ? static_cast<int>(~static_cast<uint32_t>(key)) : -1;
-        a.top_logprobs[r * a.n_top + at] = !key ? -INFINITY : (a.stats ? value_of(static_cast<uint32_t>(key >> 32)) : logprob(value_of(static_cast<uint32_t>(key >> 32))));
+        const float x = value_of(static_cast<uint32_t>(key >> 32));
+        a.top_logprobs[r * a.n_top + at] = key ? (kBeam ? x : logprob(x)) : -INFINITY;
     }
 };
 
 // A row to a block of NT threads, or to a cluster of a.split blocks.
-template <class T, bool kTop, int NT>
+template <class T, bool kTop, int NT, bool kBeam>
 __global__ void __launch_bounds__(NT, blocks_of(NT)) token_logprobs_kernel(const LogprobArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -677,7 +679,7 @@ __global__ void __launch_bounds__(NT, blocks_of(NT)) token_logprobs_kernel(const
     if (lane == 0) s.stats[warp] = st;
     if (kTop) {
         const int groups = per_group ? (batches + per_group - 1) / per_group : 0;
-        find_best<T, NT, NT>(s.f, s.top, s.keys, row, a.n_top, lo, hi, per_group, groups, t, edge, edge_value, a.stats == nullptr);
+        find_best<T, NT, NT, kBeam>(s.f, s.top, s.keys, row, a.n_top, lo, hi, per_group, groups, t, edge, edge_value);
     }
     if (a.split > 1)
         cluster_sync_all();
@@ -697,7 +699,7 @@ __global__ void __launch_bounds__(NT, blocks_of(NT)) token_logprobs_kernel(const
             all.w += o.w;
         }
         all.join_warp();
-        const Result res(all);
+        const Result<kBeam> res(all);
         if (t == 0) res.write(a, r, all, token, given);
         if (kTop) {
             // thread t ranks key t % n of block t / n among all blocks' best
@@ -720,7 +722,7 @@ __global__ void __launch_bounds__(NT, blocks_of(NT)) token_logprobs_kernel(const
 
 // Rows blockIdx.x, blockIdx.x + gridDim.x, ..: kReaders threads read them one after the other, kFinishers threads
 // finish each behind them.
-template <class T>
+template <class T, bool kBeam>
 __global__ void __launch_bounds__(kReaders + kFinishers, kStreamBlocks) token_logprobs_stream_kernel(const LogprobArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -759,12 +761,12 @@ __global__ void __launch_bounds__(kReaders + kFinishers, kStreamBlocks) token_lo
             const int token = a.logprob ? given_token(a, r) : -1;
             const float given = token >= 0 ? static_cast<float>(row.x[token]) : 0.0f;
             bar_sync(kBarFull + buffer, kAll);
-            find_best<T, kFinishers, kReaders>(s.f, s.top[buffer], s.keys, row, a.n_top, 0, row.pieces, per_group, groups, t, edge, edge_value, a.stats == nullptr);
+            find_best<T, kFinishers, kReaders, kBeam>(s.f, s.top[buffer], s.keys, row, a.n_top, 0, row.pieces, per_group, groups, t, edge, edge_value);
             sync_finders<kFinishers>();
             if (t < 32) {
                 Stats all = lane < kReaders / 32 ? s.stats[buffer][lane] : Stats{-INFINITY, 0.0f, 0.0f};
                 all.join_warp();
-                const Result res(all);
+                const Result<kBeam> res(all);
                 if (t == 0) res.write(a, r, all, token, given);
                 if (t < a.n_top) res.write_top(a, r, t, s.f.best[t]);
             }
@@ -848,8 +850,10 @@ cudaError_t launch_rows(const LogprobArgs& a, cudaStream_t s)
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     c.attrs = &attr;
     c.numAttrs = a.split > 1 ? 1 : 0;
-    const auto kernel = a.bf16 ? (a.n_top > 0 ? token_logprobs_kernel<__nv_bfloat16, true, NT> : token_logprobs_kernel<__nv_bfloat16, false, NT>)
-                               : (a.n_top > 0 ? token_logprobs_kernel<float, true, NT> : token_logprobs_kernel<float, false, NT>);
+    using B = __nv_bfloat16;
+    if (a.stats) return cudaLaunchKernelEx(&c, a.bf16 ? token_logprobs_kernel<B, true, NT, true> : token_logprobs_kernel<float, true, NT, true>, a);
+    const auto kernel = a.bf16 ? (a.n_top > 0 ? token_logprobs_kernel<B, true, NT, false> : token_logprobs_kernel<B, false, NT, false>)
+                               : (a.n_top > 0 ? token_logprobs_kernel<float, true, NT, false> : token_logprobs_kernel<float, false, NT, false>);
     return cudaLaunchKernelEx(&c, kernel, a);
 }
 
@@ -876,10 +880,10 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t s)
     // 800 rows 54.9 and 46.6; 4096 rows 192 and 179).
     if (a.n_top > 0 && many) {
         const unsigned grid = static_cast<unsigned>(kStreamBlocks * num_sms());
-        if (a.bf16)
-            token_logprobs_stream_kernel<__nv_bfloat16><<<grid, kReaders + kFinishers, sizeof(StreamShared<__nv_bfloat16>), s>>>(a);
-        else
-            token_logprobs_stream_kernel<float><<<grid, kReaders + kFinishers, sizeof(StreamShared<float>), s>>>(a);
+        using B = __nv_bfloat16;
+        const auto kernel = a.bf16 ? (a.stats ? token_logprobs_stream_kernel<B, true> : token_logprobs_stream_kernel<B, false>)
+                                   : (a.stats ? token_logprobs_stream_kernel<float, true> : token_logprobs_stream_kernel<float, false>);
+        kernel<<<grid, kReaders + kFinishers, a.bf16 ? sizeof(StreamShared<B>) : sizeof(StreamShared<float>), s>>>(a);
         return cudaGetLastError();
     }
     // One or two long rows an SM: more loads in flight for each (20 best of 200 / 300 rows of 131072 fp32: 28.2 / 35.0 us,
