@@ -26,34 +26,51 @@ namespace {
 constexpr int kSelectThreads = 256;
 constexpr int kMaxCandidates = MOE_MAX_BEAMS * MOE_MAX_TOP;
 
+// A double's bits as an integer of the same order (-0 comes below 0; there is none here).
+__device__ __forceinline__ long long ordered(double x)
+{
+    const long long bits = __double_as_longlong(x);
+    return bits ^ (bits >> 63 & 0x7fffffffffffffffLL);
+}
+constexpr long long kNoTotal = -0x7ff0000000000001LL;   // of -inf
+
+// (Few fp64 operations: the chip does two a cycle and SM.  A logarithm a row instead of one a candidate, and ranking by integers:
+// 60.1 to 57.4 us for 64 x 8 beams with 16 candidates, the logits read in 50.)
 __global__ void __launch_bounds__(kSelectThreads) beam_select_kernel(const BeamArgs a)
 {
-    __shared__ double s_total[kMaxCandidates];
+    __shared__ long long s_total[kMaxCandidates];
+    __shared__ double s_log[MOE_MAX_BEAMS];
     __shared__ int s_valid;
     wait_for_previous();
     const int W = a.beams, n = a.n, count = W * n;
     const long long b = blockIdx.x;
     if (threadIdx.x == 0) s_valid = 0;
+    if (threadIdx.x < W) {
+        s_log[threadIdx.x] = log(static_cast<double>(a.stats[b * W + threadIdx.x].y));   // sum of e^(x - maximum)
+        const float score = a.scores[b * W + threadIdx.x];
+        if (score != score) record_error(a.status, MOE_ERR_NONFINITE);
+    }
     __syncthreads();
     int valid = 0;
     for (int i = threadIdx.x; i < count; i += kSelectThreads) {
         const int w = i / n;
         const long long row = b * W + w;
         const float x = a.top_x[row * n + (i - w * n)], score = a.scores[row];
-        const float2 stat = a.stats[row];   // maximum, sum of e^(x - maximum)
+        const float maximum = a.stats[row].x;
+        const double log_sum = s_log[w];
         double total = -INFINITY;
         // a row with NaN or +inf has no log probabilities (recorded where it was read), one of -inf alone no candidates
-        if (x > -INFINITY && score > -INFINITY && stat.y == stat.y)
-            total = static_cast<double>(score) + ((static_cast<double>(x) - stat.x) - log(static_cast<double>(stat.y)));
-        if (score != score) record_error(a.status, MOE_ERR_NONFINITE);
-        s_total[i] = total;
-        valid += total > -INFINITY;
+        if (x > -INFINITY && score > -INFINITY && log_sum == log_sum)
+            total = static_cast<double>(score) + ((static_cast<double>(x) - maximum) - log_sum) + 0.0;
+        const long long key = total > -INFINITY ? ordered(total) : kNoTotal;
+        s_total[i] = key;
+        valid += key != kNoTotal;
     }
     if (valid) atomicAdd(&s_valid, valid);
     __syncthreads();
     for (int i = threadIdx.x; i < count; i += kSelectThreads) {
-        const double total = s_total[i];
-        if (!(total > -INFINITY)) continue;
+        const long long total = s_total[i];
+        if (total == kNoTotal) continue;
         const int w = i / n;
         int rank = i - w * n;
         for (int o = 0; o < W && rank < n; ++o) {
@@ -62,7 +79,7 @@ __global__ void __launch_bounds__(kSelectThreads) beam_select_kernel(const BeamA
             int lo = 0, hi = n;
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
-                const double t = s_total[o * n + mid];
+                const long long t = s_total[o * n + mid];
                 if (o < w ? t >= total : t > total)
                     lo = mid + 1;
                 else
@@ -71,7 +88,7 @@ __global__ void __launch_bounds__(kSelectThreads) beam_select_kernel(const BeamA
             rank += lo;
         }
         if (rank >= n) continue;
-        a.out_scores[b * n + rank] = static_cast<float>(total);
+        a.out_scores[b * n + rank] = static_cast<float>(__longlong_as_double(total ^ (total >> 63 & 0x7fffffffffffffffLL)));
         a.parents[b * n + rank] = w;
         a.tokens[b * n + rank] = a.top_ids[b * count + i];
     }
