@@ -9,12 +9,16 @@
 // of that beam's come before it (a binary search: the lists are in order).  Totals
 // are formed in fp64 from the value, the maximum and the logarithm of the sum: in
 // fp32 two candidates a rounding apart (1e-6 at a total of 12) would change places.
+// Bounded by reading the logits: 64 x 8 rows of 131072 fp32 with the 16 best, one in
+// twenty finished, 50 us of the 57 (268 MB: 0.80 of the copy rate).  A single search
+// of 4 beams over 32000 tokens 12 us, two launches and the row's chain of searches.
 //
 // Reordering: beam w continues beam p = parent[w].  The full pages of p are shared
 // (table entries only).  The page that fills next has to be a beam's own: the first
 // child of p keeps p's, every other child gets the one of a beam that nobody
 // continues -- there are as many -- and the cached rows of p's copied into it.  So a
-// step in which every beam goes on moves no cache at all.
+// step in which every beam goes on moves no cache at all.  64 x 8 beams with a third
+// to be moved (47 MB of rows both ways) 10.4 us; one search 3 us.
 #include <algorithm>
 
 #include "common.cuh"

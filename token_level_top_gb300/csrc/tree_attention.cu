@@ -8,17 +8,34 @@
 //   P = 2^(S c - m)          four warps, a row of S a thread (TMEM lane)
 //   O[128, D] += P V         tcgen05.mma, P from TMEM (over S), the value tile as
 //                            it lies in shared memory: a row is one index of the sum
-// P goes in as two bf16 parts, P = hi + lo: one rounding to bf16 would cost as much
+// P goes in as two 16-bit parts, P = hi + lo: one rounding to bf16 would cost as much
 // as the output's, and the second product is on units that are idle anyway.  The
 // running maximum is raised only when a score passes it by 2^kSlack, so that O is
 // rarely touched between products.  Sums are of the unrounded weights, in fp32.
 //
-// A block is 9 warps: four for the softmax and the output, four that copy, one whose
-// first thread issues the products.  A ring of tiles in shared memory takes keys and
-// values in turn (cp.async in 16-byte pieces, swizzled as the products read them:
-// pages of any size and any strides); e4m3 rows pass through registers and become
-// bf16 there, exactly, their power of two included.  D up to 128 leaves room for two
-// blocks an SM, which fill each other's gaps.
+// A block is 8 warps: four for the softmax and the output, three that copy, one that
+// issues the products; two blocks an SM for D up to 128, which fill each other's
+// gaps.  Key and value tiles take turns in a ring of slots, each with a pair of
+// barriers: full (a box or boxes of TMA landed, or cp.async pieces where a page's
+// rows and a tile have no 8 in common) and empty (the product that read it is done).
+// Scores have two buffers, so S of a tile is computed while the last one's weights are.
+//
+// e4m3: keys stay codes and q goes in as two e4m3 rows (kind::f8f6f4), the keys'
+// powers of two multiply the scores; value codes become f16 in their slots, times
+// 2^(their exponent - the tile's largest), which is exact, and the tile's exponent
+// goes into the weights.  Tiles whose exponents lie too far apart for that take a way
+// of their own (Apart).
+//
+// What bounds it: bf16 of 128 and 256 memory (64 sequences of up to 8192, 16 drafted,
+// 32 heads on 8: 189 us, 0.87 of the copy rate with the join; 4 x 65536: 178 us,
+// 0.90).  With 64 values a head, and e4m3, a tile has half the bytes and the same
+// softmax, and what is left is a block's chain: scores there -> maximum -> weights
+// -> products (1100 to 2400 cycles a tile, a good part of it waiting for instructions: the
+// roles' loops together are more than the first level of the cache holds, so loops
+// are rolled and rare ways are out of line).  Items of at most 64 rows therefore have
+// their rows twice in the tile of 128, each copy with half of the tile's keys, joined
+// at the end: 4 x 65536 e4m3 226 -> 186 us, D = 64 bf16 127 -> 116 us; 128 sequences of up
+// to 4096, 64 heads on 8, e4m3: 246 us, 0.35 of the copy rate.
 //
 // Work is dealt out as in attention.cu: all (sequence, key head, row tile) items in
 // order, each its number of key tiles and a gap long, cut into equal runs for the
@@ -50,7 +67,9 @@ constexpr int kRowsTile = 128, kKeys = 64;
 constexpr int kPanel = kKeys * 128;         // bytes of 64 values of a tile's 64 rows
 // Eight warps, so that two blocks an SM leave a thread 128 registers.
 constexpr int kSoftmaxWarps = 4, kCopyWarps = 3, kProductWarp = kSoftmaxWarps + kCopyWarps, kThreads = 32 * (kProductWarp + 1);
-constexpr int kGap = 4;                     // places of the list that an item's start and end are worth
+// Places of the list that an item's start and end are worth (64 sequences of up to 8192: with 2 / 4 / 6 / 8 / 12 places 215 /
+// 198 / 198 / 200 / 203 us).
+constexpr int kGap = 4;
 constexpr int kMaxSms = 152, kMaxBlocks = 2 * kMaxSms;
 
 template <int D, bool kE4m3>
@@ -60,10 +79,11 @@ struct Shape {
     static constexpr int kQ = kRowsTile * D * 2;
     static constexpr int kBars = kE4m3 ? 4096 : 1024;
     // Items of at most 64 rows have them twice in the tile, each half with half of a tile's keys: where the softmax, not the
-    // copies, is what takes longest.  The halves are joined through 4 KB of shared memory.
+    // copies, is what takes longest (bf16 of 128 gains nothing: 178 us both ways, and would lose a slot).  The halves are joined
+    // through 4 KB of shared memory.
     static constexpr bool kSplit = kE4m3 || D == 64;
     static constexpr int kSwap = kSplit ? 4096 : 0;
-    static constexpr int kCut = kE4m3 ? 16 : 32;                          // keys that a turn of the softmax's loops takes
+    static constexpr int kCut = kE4m3 ? 16 : 32;                          // keys that a turn of the softmax's loops takes (e4m3: 32 lost 5%; bf16, D = 64, without halves: 16 lost 5%)
     static constexpr int kShare = std::min(233472 / kCtas - 1024, 232448), kRoom = kShare - kBars - kSwap - kQ;
     // One ring of slots for tiles; e4m3: one for keys, which stay codes, and one for values, which become f16 in their slots
     // (D = 64: behind the codes).
@@ -169,7 +189,7 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ bool uniform(bool x) { return __any_sync(0xffffffffu, x); }
 
 // The warp that issues the products runs as one, and its elected lane issues them under a predicate: in a branch of one
-// lane every operand's way into the uniform registers costs some 100 cycles (TAG).
+// lane every operand's way into the uniform registers costs some 100 cycles (4 sequences of 65536, 16 drafted: 222 us so, 195 with a predicate).
 __device__ __forceinline__ uint32_t elected()
 {
     uint32_t r;
