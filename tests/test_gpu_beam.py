@@ -78,6 +78,33 @@ def test_dead_finished_and_masked_beams():
     assert 0 not in got["parents"][4].tolist()
 
 
+@pytest.mark.parametrize("B,W,V,dtype,live", [
+    (2, 8, 78130, torch.float32, 1), (1, 2, 131072, torch.float32, 5), (3, 4, 32000, torch.bfloat16, 1), (2, 3, 131072, torch.bfloat16, 7),
+    (30, 8, 40000, torch.float32, 2), (200, 8, 20000, torch.float32, 3), (1300, 1, 3000, torch.bfloat16, 1)])
+def test_rows_with_few_candidates(B, W, V, dtype, live):
+    """Rows read by clusters, blocks and streams of blocks with fewer tokens than places: the rest is empty, whatever the
+    workspace held before."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    n = 8
+    ws = moe.beam_workspace(B * W, n)
+    x = torch.randn(B * W, V, generator=g, device="cuda").to(dtype)
+    scores = -torch.rand(B, W, generator=g, device="cuda")
+    moe.beam_select(ws, x, scores, n)
+    few = torch.rand(B * W, generator=g, device="cuda") < 0.6
+    few[0] = True
+    keep = torch.randint(0, V, (B * W, live), generator=g, device="cuda")
+    kept = x.gather(1, keep)
+    x[few] = -float("inf")
+    x.scatter_(1, keep, kept)
+    got = moe.beam_select(ws, x, scores, n)
+    assert moe.device_status(ws) == 0
+    some = slice(0, 6)
+    _check({k: t[some] for k, t in got.items()}, x[: 6 * W], scores[some], n)
+    if W == 1:
+        rows = few.nonzero().flatten()
+        assert ((got["tokens"][rows] >= 0).sum(1) <= live).all()
+
+
 def test_ties():
     """Equal totals: the lower beam, then the larger logit, then the lower token."""
     V, W, n = 64, 3, 12

@@ -711,7 +711,13 @@ __global__ void __launch_bounds__(NT, blocks_of(NT)) token_logprobs_kernel(const
                       static_cast<uint32_t>(ld_cluster_s32(mine));
                 s.keys[t] = key;
             }
-            if (a.split > 1) __syncthreads();
+            // beams, whose rows may have fewer candidates: the places behind them are empty
+            if (kBeam && a.split > 1) {
+                const int filled = __syncthreads_count(key != 0);
+                if (t >= filled && t < n) res.write_top(a, r, t, 0);
+            } else if (a.split > 1) {
+                __syncthreads();
+            }
             // (a row has n keys, unless it is shorter: then there is no split, and the places behind stay empty)
             const int at = a.split == 1 ? t : rank_in<1>(s.keys, total, key, 0);
             if (t < total && at < n && (key || a.split == 1)) res.write_top(a, r, at, key);
