@@ -157,6 +157,41 @@ def test_large_scores_and_scales(scale):
     c.check(out, lse, scale=scale)
 
 
+@pytest.mark.parametrize("scale", [0.3, -0.7, 0.0])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scales_over_an_e4m3_cache(scale, D):
+    c = Case([300, 20], [9, 40], 4, 1, D, 16, True, True, "tree")
+    out, lse = c.run(scale=scale, return_lse=True)
+    c.check(out, lse, scale=scale)
+
+
+@pytest.mark.parametrize("e4m3,D", [(True, 64), (True, 128), (False, 64), (True, 256), (False, 128)])
+def test_few_and_many_rows_in_turn(e4m3, D):
+    """Items of few rows and of many, long and short, one after the other in the same blocks."""
+    n = 140
+    ctx, drafted = [[0, 130, 700, 5, 64][i % 5] for i in range(n)], [[2, 40, 1, 64, 16, 0, 33][i % 7] for i in range(n)]
+    c = Case(ctx, drafted, 8, 2, D, 16, e4m3, True, "tree")
+    ws = moe.tree_attention_workspace(D)
+    out, lse = c.run(ws, return_lse=True)
+    assert moe.device_status(ws) == 0
+    c.check(out, lse, rows=set(range(0, c.T, 13)))
+    out2, lse2 = c.run(ws, return_lse=True)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_row_of_q_that_is_not_a_number(e4m3):
+    c = Case([200, 90], [20, 3], 4, 2, 64, 16, e4m3, True, "tree")
+    want, wlse = c.run(return_lse=True)
+    q = c.q.clone()
+    q[5, 1, 7], q[21, 3, 0] = float("nan"), float("nan")
+    out, lse = c.run(q=q, return_lse=True)
+    hit = torch.zeros(c.T, 4, dtype=torch.bool, device="cuda")
+    hit[5, 1] = hit[21, 3] = True
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], wlse[~hit])
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+
+
 def test_scores_that_rise_and_fall():
     """The running maximum is raised many times, also late and by different rows."""
     c = Case([1500], [30], 8, 1, 64, 16, False, True, "tree")
