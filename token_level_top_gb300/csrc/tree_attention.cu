@@ -1095,7 +1095,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     const Slot keys = slot_of(n), values = slot_of(max(nv, 1));
                     if (uniform(i < count) && !wait(kFull + keys.index, keys.turn)) break;
                     if (uniform(i == 0) && !wait(kQFull, seg & 1)) break;
-                    if (uniform(i > 0) && !wait(kFull + values.index, values.turn)) break;
                     tc_fence_after();
                     fence_proxy_async_shared();   // the copies were written through the generic proxy
                     if (uniform(i < count)) {
@@ -1122,9 +1121,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                         if (uniform(i == count - 1)) commit_if(leader, bar(kQEmpty));
                     }
                     if (uniform(i > 0)) {
+                        // (the values are waited for behind the next scores: e4m3 ones are converted just in time)
+                        if (!wait(kFull + values.index, values.turn)) break;
                         if (!wait(kPFull + (u & 1), (u >> 1) & 1)) break;
                         if (uniform(i == 1 && seg > 0) && !wait(kOFree, (seg - 1) & 1)) break;
                         tc_fence_after();
+                        fence_proxy_async_shared();
                         const uint32_t pt = tmem + D + (u & 1) * kKeys, v0 = values.at;
 #pragma unroll
                         for (int k = 0; k < kKeys / 16; ++k) {
