@@ -1084,13 +1084,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 const int g1 = static_cast<int>(min(static_cast<long long>(it.n), hi - it.off)), count = g1 - g0;
                 for (int i = 0; uniform(i <= count && ok); ++i) {
                     const int t = tiles + i, n = 2 * t, u = t - 1, nv = n - 1;   // tile t's scores, tile u's product with the values
-                    // The scores take the place of weights that the product two tiles back has read; the slot of its values is
-                    // free then, and the keys waited for next may need it.  (Every phase of this barrier is waited for before
-                    // the next but one can begin: a wait tells only neighbours apart.)
+                    // The scores take the place of weights that the product two tiles back has read.  (Every phase of this barrier
+                    // is waited for before the next but one can begin: a wait tells only neighbours apart.)
                     if (uniform(t >= 2 && (i > 0 || seg == 0))) {
                         if (!wait(kODone, t & 1)) break;
-                        if (lane == 0) mbar_arrive(bar(kEmpty + slot_of(nv - 2).index));
-                        __syncwarp();
                     }
                     const Slot keys = slot_of(n), values = slot_of(max(nv, 1));
                     if (uniform(i < count) && !wait(kFull + keys.index, keys.turn)) break;
@@ -1098,26 +1095,26 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     tc_fence_after();
                     fence_proxy_async_shared();   // the copies were written through the generic proxy
                     if (uniform(i < count)) {
-                        const uint32_t d = tmem + D + (t & 1) * kKeys, k0 = keys.at, q0 = smem_u32(s_q);
+                        // (descriptors of later operands are sums: fewer instructions than from the address each time)
+                        const uint32_t d = tmem + D + (t & 1) * kKeys;
+                        const bool narrow_rows = kE4m3 && D == 64;
+                        const uint64_t q0 = narrow_rows ? sdesc_k_sw64(smem_u32(s_q)) : sdesc_k_sw128(smem_u32(s_q));
+                        const uint64_t k0 = narrow_rows ? sdesc_k_sw64(keys.at) : sdesc_k_sw128(keys.at);
                         if constexpr (kE4m3) {
 #pragma unroll
                             for (int part = 0; part < 2; ++part)
 #pragma unroll
-                                for (int k = 0; k < D / 32; ++k) {
-                                    const uint32_t qp = q0 + part * kRowsTile * D;
-                                    if (D == 64)
-                                        mma_e4m3_if(leader, d, sdesc_k_sw64(qp + k * 32), sdesc_k_sw64(k0 + k * 32), kIdescS, part + k > 0);
-                                    else
-                                        mma_e4m3_if(leader, d, sdesc_k_sw128(qp + (k >> 2) * (kRowsTile * 128) + (k & 3) * 32),
-                                                    sdesc_k_sw128(k0 + (k >> 2) * kPanel + (k & 3) * 32), kIdescS, part + k > 0);
-                                }
+                                for (int k = 0; k < D / 32; ++k)
+                                    mma_e4m3_if(leader, d, q0 + (part * kRowsTile * D + (k >> 2) * (kRowsTile * 128) + (k & 3) * 32) / 16,
+                                                k0 + ((k >> 2) * kPanel + (k & 3) * 32) / 16, kIdescS, part + k > 0);
                         } else {
 #pragma unroll
                             for (int k = 0; k < D / 16; ++k)
-                                mma_if(leader, d, sdesc_k_sw128(q0 + (k >> 2) * (kRowsTile * 128) + (k & 3) * 32),
-                                       sdesc_k_sw128(k0 + (k >> 2) * kPanel + (k & 3) * 32), kIdescS, k > 0);
+                                mma_if(leader, d, q0 + ((k >> 2) * (kRowsTile * 128) + (k & 3) * 32) / 16,
+                                       k0 + ((k >> 2) * kPanel + (k & 3) * 32) / 16, kIdescS, k > 0);
                         }
-                        commit_if(leader, bar(kSFull + (t & 1)));   // (the keys' slot is handed on by the softmax)
+                        commit_if(leader, bar(kEmpty + keys.index));
+                        commit_if(leader, bar(kSFull + (t & 1)));
                         if (uniform(i == count - 1)) commit_if(leader, bar(kQEmpty));
                     }
                     if (uniform(i > 0)) {
@@ -1127,13 +1124,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                         if (uniform(i == 1 && seg > 0) && !wait(kOFree, (seg - 1) & 1)) break;
                         tc_fence_after();
                         fence_proxy_async_shared();
-                        const uint32_t pt = tmem + D + (u & 1) * kKeys, v0 = values.at;
+                        const uint32_t pt = tmem + D + (u & 1) * kKeys;
+                        const uint64_t v0 = sdesc_values(values.at);
 #pragma unroll
                         for (int k = 0; k < kKeys / 16; ++k) {
                             const uint32_t part = pt + 16 * k / S::kCut * S::kCut + 16 * k % S::kCut / 2;
-                            mma_tmem_a_if(leader, tmem, part, sdesc_values(v0 + k * 2048), kIdescO, i > 1 || k > 0);
-                            mma_tmem_a_if(leader, tmem, part + S::kCut / 2, sdesc_values(v0 + k * 2048), kIdescO, 1);
+                            mma_tmem_a_if(leader, tmem, part, v0 + k * 2048 / 16, kIdescO, i > 1 || k > 0);
+                            mma_tmem_a_if(leader, tmem, part + S::kCut / 2, v0 + k * 2048 / 16, kIdescO, 1);
                         }
+                        commit_if(leader, bar(kEmpty + values.index));
                         commit_if(leader, bar(kODone));
                         if (uniform(i == count)) commit_if(leader, bar(kItemDone));
                     }
@@ -1144,6 +1143,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
             }
             // No arrival on a barrier is under way when the block ends, and no product when TMEM is released.
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(kODone), (tiles - 1) & 1, kSpinBudget));
+            for (int n = max(0, 2 * tiles - 2 * kSlots); uniform(ok && n < 2 * tiles); ++n) {   // the last uses of the slots
+                const int again = n + (kE4m3 ? 2 * (n & 1 ? S::kSlotsV : S::kSlotsK) : kSlots);
+                const Slot o = slot_of(n);
+                if (again >= 2 * tiles) ok = __all_sync(0xffffffffu, mbar_wait(bar(kEmpty + o.index), o.turn, kSpinBudget));
+            }
             if (!ok) {
                 if (lane == 0) record_error(a.status, MOE_ERR_TIMEOUT);
                 __syncwarp();
@@ -1211,7 +1215,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     ok = false;
                     break;
                 }
-                if (threadIdx.x == 0) mbar_arrive(bar(kEmpty + slot_of(2 * t).index));   // the keys have been read
                 __syncwarp();   // (TMEM is read by whole, converged warps)
                 tc_fence_after();
                 if (!idle) {
