@@ -110,6 +110,24 @@ def test_norm_gradient(rows, cols, dtype, wtype, residual, pad, at, dy32):
         assert torch.equal(moe.rms_norm_backward(ws, x, w, hold, dsum=dsum, eps=1e-5, out=hold)[0], dx)
 
 
+@pytest.mark.parametrize("rows,cols,dtype,dy32", [
+    (2500, 1501, torch.bfloat16, False), (1300, 1501, torch.bfloat16, True), (1900, 3001, torch.bfloat16, False), (1600, 1407, F32, True),
+    (900, 3583, F32, True), (3001, 255, torch.bfloat16, False), (4000, 1023, torch.bfloat16, True), (700, 5001, torch.bfloat16, False)])
+def test_gradient_of_many_odd_rows(rows, cols, dtype, dy32):
+    """Several rows a block, taken value by value."""
+    g = torch.Generator().manual_seed(rows + cols)
+    x, dsum = (2 * torch.randn(rows, cols, generator=g)).to(dtype).cuda(), torch.randn(rows, cols, generator=g).to(dtype).cuda()
+    dy = torch.randn(rows, cols, generator=g).to(F32 if dy32 else dtype).cuda()
+    w = (1 + 0.2 * torch.randn(cols, generator=g)).cuda()
+    dx, dw = moe.rms_norm_backward(moe.norm_workspace(cols), x, w, dy, dsum=dsum)
+    want, want_w, e, e_w = cref.norm_grad(ref.f64(x), ref.f64(w), ref.f64(dy), ref.f64(dsum), 1e-6)
+    assert (np.abs(ref.f64(dx) - want) <= e + cref.HALF_STEP[dtype] * (np.abs(want) + e)).all()
+    assert (np.abs(ref.f64(dw) - want_w) <= e_w).all()
+    y = moe.rms_norm(x, w, residual=dsum)
+    s = ref.f64(y["sum"])
+    assert (np.abs(ref.f64(y["y"]) - cref.norm(s, ref.f64(w), 1e-6)) <= (cref.HALF_STEP[dtype] * 1.01 + cref.NORM) * np.abs(cref.norm(s, ref.f64(w), 1e-6)) + 1e-38).all()
+
+
 def test_gradient_against_differences():
     """The formula's gradient against differences of the 64-bit norm, so that the kernel is held to the function."""
     g = np.random.default_rng(0)

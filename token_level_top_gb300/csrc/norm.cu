@@ -16,7 +16,7 @@
 // Measured on rows in memory (the copy rate is 6.7 TB/s): 16384 x 4096 bf16 with a
 // residual 79 us, at the copy rate; its gradient with fp32 dy 114 us, 0.88 of it, the
 // weights' sum being 6 us of that.  64 rows: 4 us, a launch and one chain of loads.  Rows
-// of 1407 fp32 are taken value by value: the gradient of 5001 24 us, 0.52.
+// of 1407 fp32 are taken value by value: the gradient of 5001 23 us, 0.54.
 //
 // Squares are summed in fp32.  A row whose sum is not finite is looked at again,
 // scaled by a power of two: values up to the type's largest have a norm.
@@ -30,8 +30,8 @@
 namespace moe {
 namespace {
 
-// (Blocks an SM, 5001 x 1407 fp32: 4 / 5 / 6 / 8 24.1 / 27.4 / 31.6 / 51.6 us; three fit of the rows of 4096 bf16, 114 us, 126 with two.)
-constexpr int kGradBlocksPerSm = 4, kGradBlocks = kGradBlocksPerSm * 152;   // most blocks of the gradient, each with a row of the workspace
+// (Blocks an SM, 5001 x 1407 fp32: 4 / 5 / 6 25.4 / 23.4 / 27.6 us; three fit of the rows of 4096 bf16, 114 us, 126 with two.)
+constexpr int kGradBlocksPerSm = 5, kGradBlocks = kGradBlocksPerSm * 152;   // most blocks of the gradient, each with a row of the workspace
 
 // A piece as it lies in memory: N values (16 bytes of the rows' type) or one, unpacked where they are used.
 template <class E, bool kVec, int N>
@@ -305,14 +305,16 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256) rms_norm_kernel(const N
 
 // Blocks an SM that the gradient's registers are held to.
 // (80 registers for pieces of eight bf16 values, of which a lane sums as many weights' gradients, 64 for four of fp32).
-template <class T, bool kVec, int W>
+template <class T, bool kVec, int W, int P>
 constexpr int grad_blocks()
 {
-    return kVec && sizeof(T) == 2 ? (W <= 8 ? 3 : 1) : (W <= 8 ? kGradBlocksPerSm : (W == 16 ? 2 : 1));
+    if (!kVec && W == 8 && P == 6 && sizeof(T) == 4) return kGradBlocksPerSm;
+    if (!kVec && sizeof(T) == 2) return W <= 8 ? 3 : (W == 16 ? 2 : 1);
+    return kVec && sizeof(T) == 2 ? (W <= 8 ? 3 : 1) : (W <= 8 ? 4 : (W == 16 ? 2 : 1));
 }
 
 template <class T, class D, bool kVec, int W, int P>
-__global__ void __launch_bounds__(W >= 8 ? 32 * W : 256, (grad_blocks<T, kVec, W>())) rms_norm_backward_kernel(const NormGradArgs a)
+__global__ void __launch_bounds__(W >= 8 ? 32 * W : 256, (grad_blocks<T, kVec, W, P>())) rms_norm_backward_kernel(const NormGradArgs a)
 {
     constexpr int N = kVec ? 16 / static_cast<int>(sizeof(T)) : 1;
     constexpr int kRows = W >= 8 ? 1 : 8 / W;
@@ -330,14 +332,16 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256, (grad_blocks<T, kVec, W
 #pragma unroll
         for (int i = 0; i < N; ++i) dw[p][i] = 0.0f;
     int turn = 0;
-    for (long long row0 = static_cast<long long>(blockIdx.x) * kRows; row0 < a.rows; row0 += static_cast<long long>(gridDim.x) * kRows) {
-        const long long row = row0 + row_of;
+    // Rows of single bf16 values ask for the next row before they work on this one: 9000 x 1500 52 us, 68 without, 5001 x 1407
+    // of fp32, whose blocks hide more of each other's waits, 29 us and 23.
+    constexpr bool kAhead = !kVec && sizeof(T) == 2;
+    Raw<T, kVec, N> next_s[P], next_d[P];
+    Raw<D, kVec, N> next_g[P];
+    auto fetch = [&](long long row, Raw<T, kVec, N> (&s)[P], Raw<D, kVec, N> (&g)[P], Raw<T, kVec, N> (&d)[P]) {
         const bool live = row < a.rows;
         const T* const x = static_cast<const T*>(a.x) + (live ? row * a.x_stride : 0);
         const D* const dy = static_cast<const D*>(a.dy) + (live ? row * a.dy_stride : 0);
         const T* const dsum = static_cast<const T*>(a.dsum) + (live && a.dsum ? row * a.dsum_stride : 0);
-        Raw<T, kVec, N> s[P], d[P];
-        Raw<D, kVec, N> g[P];
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const int u = first + p * 32 * W;
@@ -349,6 +353,20 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256, (grad_blocks<T, kVec, W
                 g[p].load(dy + u * N);
                 if (a.dsum) d[p].load(dsum + u * N);
             }
+        }
+    };
+    if (kAhead) fetch(static_cast<long long>(blockIdx.x) * kRows + row_of, next_s, next_g, next_d);
+    for (long long row0 = static_cast<long long>(blockIdx.x) * kRows; row0 < a.rows; row0 += static_cast<long long>(gridDim.x) * kRows) {
+        const long long row = row0 + row_of;
+        const bool live = row < a.rows;
+        Raw<T, kVec, N> s[P], d[P];
+        Raw<D, kVec, N> g[P];
+        if (!kAhead) {
+            fetch(row, s, g, d);
+        } else {
+#pragma unroll
+            for (int p = 0; p < P; ++p) s[p] = next_s[p], g[p] = next_g[p], d[p] = next_d[p];
+            fetch(row + static_cast<long long>(gridDim.x) * kRows, next_s, next_g, next_d);
         }
         // sum of s^2 and of w dy s, in one exchange between the warps
         float2 sums = make_float2(0.0f, 0.0f);
@@ -481,14 +499,14 @@ template <class T, class D, bool kVec, int W, int P>
 int backward(const NormGradArgs& a, cudaStream_t s)
 {
     constexpr int kRows = W >= 8 ? 1 : 8 / W;
-    const long long most = std::min(grad_blocks<T, kVec, W>() * num_sms(), kGradBlocks);
+    const long long most = std::min(grad_blocks<T, kVec, W, P>() * num_sms(), kGradBlocks);
     const int grid = static_cast<int>(std::min<long long>((a.rows + kRows - 1) / kRows, most));
     rms_norm_backward_kernel<T, D, kVec, W, P><<<grid, W >= 8 ? 32 * W : 256, 0, s>>>(a);
     return grid;
 }
 
 // Warps and pieces for a row of this many units: as few warps as take it at two pieces a lane, past 8 warps at four and
-// more (and of single values at eight and 32).
+// more (single values: six to eight a lane, and sixteen).
 static_assert(kMaxNormCols <= 16384, "what the largest variants hold");
 template <class F>
 auto by_size(bool vec, int units, F&& f)
@@ -508,7 +526,9 @@ auto by_size(bool vec, int units, F&& f)
     constexpr std::false_type v{};
     if (units <= 256) return go(v, integral_constant<int, 1>{}, integral_constant<int, 8>{});
     if (units <= 1024) return go(v, integral_constant<int, 4>{}, integral_constant<int, 8>{});
+    if (units <= 1536) return go(v, integral_constant<int, 8>{}, integral_constant<int, 6>{});
     if (units <= 2048) return go(v, integral_constant<int, 8>{}, integral_constant<int, 8>{});
+    if (units <= 3584) return go(v, integral_constant<int, 16>{}, integral_constant<int, 7>{});
     if (units <= 8192) return go(v, integral_constant<int, 32>{}, integral_constant<int, 8>{});
     return go(v, integral_constant<int, 32>{}, integral_constant<int, 16>{});
 }
