@@ -27,15 +27,15 @@
 // of their own (Apart).
 //
 // What bounds it: bf16 of 128 and 256 memory (64 sequences of up to 8192, 16 drafted,
-// 32 heads on 8: 189 us, 0.87 of the copy rate with the join; 4 x 65536: 178 us,
-// 0.90).  With 64 values a head, and e4m3, a tile has half the bytes and the same
+// 32 heads on 8: 189 us, 0.87 of the copy rate with the join; 4 x 65536: 179 us,
+// 0.90; 256: 347 us, 0.93).  With 64 values a head, and e4m3, a tile has half the bytes and the same
 // softmax, and what is left is a block's chain: scores there -> maximum -> weights
 // -> products (1100 to 2400 cycles a tile, a good part of it waiting for instructions: the
 // roles' loops together are more than the first level of the cache holds, so loops
 // are rolled and rare ways are out of line).  Items of at most 64 rows therefore have
 // their rows twice in the tile of 128, each copy with half of the tile's keys, joined
-// at the end: 4 x 65536 e4m3 226 -> 186 us, D = 64 bf16 127 -> 116 us; 128 sequences of up
-// to 4096, 64 heads on 8, e4m3: 246 us, 0.35 of the copy rate.
+// at the end: 4 x 65536 e4m3 226 -> 190 us, D = 64 bf16 127 -> 115 us; 128 sequences of up
+// to 4096, 64 heads on 8, e4m3: 242 us, 0.35 of the copy rate.
 //
 // Work is dealt out as in attention.cu: all (sequence, key head, row tile) items in
 // order, each its number of key tiles and a gap long, cut into equal runs for the
