@@ -389,3 +389,25 @@ def test_binding_refusals():
         moe.tree_attention_workspace(96)
     with pytest.raises(moe.MoEError):
         c.run(ws, scale=float("nan"))
+
+
+@pytest.mark.parametrize("falls,ctx,e4m3", [(1, 3000, False), (1, 3000, True), (38, 300, False)])
+def test_rows_that_fall_leave_other_sequences_theirs(falls, ctx, e4m3):
+    """A row_start that falls and rises again, so that the sequences' rows add up to more than there are: what falls has no
+    rows, and the last sequence, whose rows are its own, has all of them."""
+    n = 2 * falls + 1
+    drafted = [64, 0] * falls + [64, 64]
+    c = Case([ctx] + [0] * (n - 1) + [ctx], drafted, 16, 1, 64, 16, e4m3, True, "tree")
+    last = c.T - 64
+    q, mask = (torch.cat([t[:64], t[last:]]) for t in (c.q, c.mask))
+    start = torch.tensor([0, 64] * (falls + 1) + [128], dtype=torch.int32).cuda()
+    assert len(start) == len(c.seq_len) + 1
+    ws = moe.tree_attention_workspace(64)
+    out, lse = c.run(ws, q=q, mask=mask, row_start=start, out=torch.full_like(q, 5.0), return_lse=True)
+    assert moe.device_status(ws) == 8
+    whole, wlse = torch.zeros_like(c.q), torch.zeros(c.T, 16, device="cuda")
+    whole[last:], wlse[last:] = out[64:], lse[64:]
+    c.check(whole, wlse, rows=range(last, c.T))
+    # and a call that is as it should be finds the workspace as it should be
+    want, got = c.run(return_lse=True), c.run(ws, return_lse=True)
+    assert moe.device_status(ws) == 0 and all(torch.equal(a, b) for a, b in zip(want, got))

@@ -661,10 +661,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
     const long long run = quotient(total + gridDim.x - 1, gridDim.x);    // places per block
     const long long lo = run * blockIdx.x, hi = min(total, lo + run);
     Header* const headers = reinterpret_cast<Header*>(static_cast<char*>(a.ws) + kTreeCtrlBytes);
+    // Sequences that share rows, in a row_start that falls and rises again, may have more items than the launch made room for.
+    // A block then has the items that begin in its run as a whole, and no header says anything.
+    const bool uncut = a.by_item > 0 && items > a.by_item;
     if (a.by_item == 0) {
         if (threadIdx.x == 0) headers[blockIdx.x].last = -1;
     } else if (blockIdx.x == 0) {
-        for (int i = items + static_cast<int>(threadIdx.x); i < a.by_item; i += kThreads) headers[i].last = -1;
+        for (int i = (uncut ? 0 : items) + static_cast<int>(threadIdx.x); i < a.by_item; i += kThreads) headers[i].last = -1;
     }
     if (lo >= hi) return;
     if (mine > 0 && before <= lo && lo < before + mine) {
@@ -684,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
         w.ordinal += w.h;
         w.off += static_cast<long long>(w.h) * places(w);
         int g = static_cast<int>(lo - w.off);
-        if (g >= w.n) {
+        if (g >= w.n || (uncut && g > 0)) {
             next_item(a, w);
             g = 0;
         }
@@ -718,6 +721,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
     const float c = a.scale == 0.0f ? kLog2e : fabsf(a.scale) * kLog2e;   // (a scale of 0 zeroes q, one below 0 negates it)
     bool ok = true;
     int seg = 0, tiles = 0;       // segments and tiles done
+    auto end_of = [&](const Item& w) { return uncut ? w.n : static_cast<int>(min(static_cast<long long>(w.n), hi - w.off)); };
 
     if (warp >= kSoftmaxWarps && warp < kProductWarp) {
         // ------------------------------------------------------------ copies
@@ -734,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
             return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(key)) * a.page_mul) >> a.page_shift);
         };
         for (; uniform(it.n > 0 && it.off + g0 < hi && ok); ++seg) {
-            const int g1 = static_cast<int>(min(static_cast<long long>(it.n), hi - it.off));
+            const int g1 = end_of(it);
             const int mtiles = it.items / a.n_kv_heads, hk = it.h / mtiles, row_at = (it.h - hk * mtiles) * kRowsTile;
             const int32_t* const table = a.page_table + it.b * a.table_stride;
             const int n0 = 2 * tiles, n_end = 2 * (tiles + g1 - g0);   // the segment's slots
@@ -1081,7 +1085,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 return ok;
             };
             for (; uniform(it.n > 0 && it.off + g0 < hi && ok); ++seg) {
-                const int g1 = static_cast<int>(min(static_cast<long long>(it.n), hi - it.off)), count = g1 - g0;
+                const int g1 = end_of(it), count = g1 - g0;
                 for (int i = 0; uniform(i <= count && ok); ++i) {
                     const int t = tiles + i, n = 2 * t, u = t - 1, nv = n - 1;   // tile t's scores, tile u's product with the values
                     // The scores take the place of weights that the product two tiles back has read.  (Every phase of this barrier
@@ -1161,7 +1165,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
         int swaps = 0;   // buffers that have gone from half to half
         const uint32_t quarter = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         for (; it.n > 0 && it.off + g0 < hi && ok; ++seg) {
-            const int g1 = static_cast<int>(min(static_cast<long long>(it.n), hi - it.off)), count = g1 - g0;
+            const int g1 = end_of(it), count = g1 - g0;
             const int mtiles = it.items / a.n_kv_heads, hk = it.h / mtiles, row_at = (it.h - hk * mtiles) * kRowsTile;
             const int rows = min(kRowsTile, it.draft * group - row_at);
             const bool twice = S::kSplit && rows <= kRowsTile / 2;
@@ -1448,7 +1452,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 if (live && half == 0 && whole && a.lse)
                     a.lse[static_cast<long long>(it.row0 + t_row) * a.n_heads + head] = l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l));
                 if (live && half == 0 && !whole) reinterpret_cast<float4*>(part + kRowsTile * D)[row] = make_float4(m, l, kE4m3 ? m_out - kShift : m, 0.0f);
-                if (threadIdx.x == 0 && whole && a.by_item > 0) headers[it.ordinal].last = -1;
+                if (threadIdx.x == 0 && whole && a.by_item > 0 && !uncut) headers[it.ordinal].last = -1;
                 if (threadIdx.x == 0 && g0 == 0 && !whole) {
                     Header h;
                     h.first = blockIdx.x;
@@ -1538,7 +1542,7 @@ cudaError_t launch(TreeArgs& a, cudaStream_t s)
     a.box_rows = rows >= 8 && encode(&map_k, a.k, kE4m3 ? kCodesSwizzled : kBf16Swizzled) && encode(&map_v, a.v, kE4m3 ? kCodes : kBf16Swizzled)
                      ? rows : 0;
     const unsigned grid = static_cast<unsigned>(S::kCtas * std::min(num_sms(), kMaxSms));
-    // at most so many items: every sequence has one row tile a key head, and one more per 128 rows
+    // at most so many items while no row is in two sequences: every sequence has one row tile a key head, and one more per 128 rows
     const long long items = static_cast<long long>(a.n_kv_heads) * (a.B + static_cast<long long>(a.T) * (a.n_heads / a.n_kv_heads) / kRowsTile);
     a.by_item = items <= grid ? static_cast<int>(items) : 0;
     kernel<<<grid, kThreads, S::kSmem, s>>>(map_k, map_v, a);
