@@ -411,3 +411,15 @@ def test_rows_that_fall_leave_other_sequences_theirs(falls, ctx, e4m3):
     # and a call that is as it should be finds the workspace as it should be
     want, got = c.run(return_lse=True), c.run(ws, return_lse=True)
     assert moe.device_status(ws) == 0 and all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("ctx,drafted", [([2000, 3, 700], [16, 16, 4]), ([300] * 3 + [0] * 2, [16, 0, 1, 2, 40]), ([90] * 90, [16] * 90)])
+def test_the_workspace_held_another_batch(ctx, drafted):
+    """What a workspace held says nothing: here the lists of items that a batch of one cut item everywhere would leave, whose
+    rows and parts all are in range."""
+    c = Case(ctx, drafted, 16, 2, 128, 16, False, True, "tree")
+    want, wlse = c.run(return_lse=True)
+    ws = moe.tree_attention_workspace(128)
+    ws[256: 256 + 304 * 24].view(torch.int32).view(304, 6).copy_(torch.tensor([0, 0, 0, 128, 0, 0], dtype=torch.int32))
+    out, lse = c.run(ws, return_lse=True)
+    assert moe.device_status(ws) == 0 and torch.equal(out, want) and torch.equal(lse, wlse)

@@ -543,6 +543,14 @@ __device__ __noinline__ void add_odd(const TreeArgs& a, const int32_t* table, __
     }
 }
 
+// A wait has run out: the items of the block's run that have no header yet get one that the join passes over, since what the
+// workspace held before is no header.  (From the item at hand on; g0 > 0: it began in another block.)
+__device__ __noinline__ void give_up(const TreeArgs& a, Header* headers, Item w, int g0, long long hi)
+{
+    for (; w.n > 0 && w.off + g0 < hi; next_item(a, w), g0 = 0)
+        if (g0 == 0) headers[w.ordinal].last = -1;
+}
+
 // ---------------------------------------------------------------- the main kernel
 
 struct Start {
@@ -1471,7 +1479,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
             next_item(a, it);
             g0 = 0;
         }
-        if (!ok) record_error(a.status, MOE_ERR_TIMEOUT);
+        if (!ok) {
+            record_error(a.status, MOE_ERR_TIMEOUT);
+            if (threadIdx.x == 0 && a.by_item > 0 && !uncut) give_up(a, headers, it, g0, hi);
+        }
     }
     tc_fence_before();
     __syncthreads();
