@@ -691,8 +691,10 @@ moe_status_t moe_beam_workspace_init(void* ws_dev, size_t ws_bytes, void* stream
 
 /* The best continuations of a step of beam search: of the totals
  *   scores[b, w] + x[v] - ln sum_i e^(x_i),  x: row b * beams + w of the logits [seqs * beams, vocab]
- * the n largest of each sequence, in order: out_scores [seqs, n] (each total formed in fp64 and rounded
- * once), parents [seqs, n] (w) and tokens [seqs, n] (v).  Ties go to the lower beam, then
+ * the n largest of each sequence, in order: out_scores [seqs, n], parents [seqs, n] (w) and tokens [seqs, n] (v).
+ * Each total is formed in fp64 of an fp32 sum of exponentials and rounded once: candidates of different
+ * rows that lie closer than that sum's error (at most 2^-17, and 2^-24 more for every 64 of the
+ * vocabulary; as a rule below 1e-6) may change places.  Ties, those between equal rows with equal scores among them, go to the lower beam, then
  * to the larger logit, then to the lower token.  logits as in moe_token_logprobs.
  * scores_dev [seqs, beams] fp32: -inf for a beam that is not alive; a masked logit is
  * -inf too, so a finished beam is a row of -inf but for one token.  Totals of -inf are

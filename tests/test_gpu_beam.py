@@ -293,3 +293,33 @@ def test_binding_refusals():
             moe.beam_reorder(*a)
     with pytest.raises(moe.MoEError):   # in place: a row would be made of rows already new
         moe.beam_reorder(cache, parents, lens, table, out=table)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,W,V,pad", [
+    (3, 8, 777, 0), (2, 64, 130, 1), (1, 8, 50257, 0), (1, 3, 131071, 0), (40, 5, 50257, 0), (150, 8, 50257, 0), (300, 8, 1001, 3), (30, 8, 131072, 1),
+    (2, 4, 3, 0), (20, 8, 4096, 5)])
+def test_ties_of_equal_rows_wherever_they_start(B, W, V, pad, dtype):
+    """Equal rows that start at different places of 16 bytes have equal totals, whichever kernel reads them."""
+    g = torch.Generator(device="cuda").manual_seed(V + B)
+    n = 16
+    two = (3 * torch.randn(B, 2, V, generator=g, device="cuda")).to(dtype)
+    x = torch.empty(B * W, V + pad, dtype=dtype, device="cuda")[:, :V]
+    kind = torch.arange(W, device="cuda") % 3 // 2     # beams 0, 1, 3, 4, .. of one row, beams 2, 5, .. of another
+    x.copy_(two[:, kind].reshape(B * W, V))
+    ws = moe.beam_workspace(B * W, n)
+    got = moe.beam_select(ws, x, torch.zeros(B, W, device="cuda"), n)
+    assert moe.device_status(ws) == 0
+    s, p, t = got["scores"].cpu(), got["parents"].cpu(), got["tokens"].cpu()
+    kind = kind.cpu()
+    for b in range(B):
+        for i in range(n - 1):
+            if p[b, i + 1] < 0:
+                break
+            if kind[p[b, i]] == kind[p[b, i + 1]] and (x[b * W + p[b, i], t[b, i]] == x[b * W + p[b, i + 1], t[b, i + 1]]):
+                # the same value of the same row: the lower beam first, of one beam the lower token
+                assert s[b, i] == s[b, i + 1] and (p[b, i], t[b, i]) < (p[b, i + 1], t[b, i + 1]), (b, i)
+    # the first place is the first beam of its row
+    assert all(int(p[b, 0]) in (0, 2) for b in range(B))
+    some = slice(0, 4)
+    _check({k: v[some] for k, v in got.items()}, x[: 4 * W], torch.zeros(min(B, 4), W), n)

@@ -9,6 +9,10 @@
 // of that beam's come before it (a binary search: the lists are in order).  Totals
 // are formed in fp64 from the value, the maximum and the logarithm of the sum: in
 // fp32 two candidates a rounding apart (1e-6 at a total of 12) would change places.
+// The sum itself is of fp32 terms in fp32, in an order that follows the row's 16-byte
+// pieces; equal rows that start at other places of 16 bytes would have sums some 1e-7
+// apart, and their candidates no ties.  So where rows start at several, the sums of
+// beams that may be equal rows are taken again, by index (sum_by_index).
 // Bounded by reading the logits: 64 x 8 rows of 131072 fp32 with the 16 best, one in
 // twenty finished, 50 us of the 57 (268 MB: 0.80 of the copy rate).  A single search
 // of 4 beams over 32000 tokens 12 us, two launches and the row's chain of searches.
@@ -30,6 +34,13 @@ namespace {
 constexpr int kSelectThreads = 256;
 constexpr int kMaxCandidates = MOE_MAX_BEAMS * MOE_MAX_TOP;
 
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // A double's bits as an integer of the same order (-0 comes below 0; there is none here).
 __device__ __forceinline__ long long ordered(double x)
 {
@@ -38,8 +49,30 @@ __device__ __forceinline__ long long ordered(double x)
 }
 constexpr long long kNoTotal = -0x7ff0000000000001LL;   // of -inf
 
+// A row's sum of e^(x - maximum), by threads that take every kSelectThreads-th value: the same bits for equal rows, wherever
+// they start.  For all threads of the block.  (Rare: loads of single values, 16 in flight a thread.)
+template <class T>
+__device__ __noinline__ float sum_by_index(const BeamArgs& a, long long row, float maximum, float* buf)
+{
+    const T* const x = static_cast<const T*>(a.logits) + row * a.row_stride;
+    float l = 0.0f;
+#pragma unroll 16
+    for (unsigned i = threadIdx.x; i < static_cast<unsigned>(a.vocab); i += kSelectThreads)
+        l += exp2_fast((static_cast<float>(x[i]) - maximum) * 1.4426950408889634f);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = l;
+    __syncthreads();
+    l = buf[0];
+    for (int i = 1; i < kSelectThreads / 32; ++i) l += buf[i];
+    __syncthreads();
+    return l;
+}
+
 // (Few fp64 operations: the chip does two a cycle and SM.  A logarithm a row instead of one a candidate, and ranking by integers:
-// 60.1 to 57.4 us for 64 x 8 beams with 16 candidates, the logits read in 50.)
+// 60.1 to 57.4 us for 64 x 8 beams with 16 candidates, the logits read in 50.  Looking for equal rows only where they start
+// apart, in an instance of its own: 0.4 us of 12.2 and 1 of 57.2.)
+template <bool kApart>
 __global__ void __launch_bounds__(kSelectThreads) beam_select_kernel(const BeamArgs a)
 {
     __shared__ long long s_total[kMaxCandidates];
@@ -54,7 +87,32 @@ __global__ void __launch_bounds__(kSelectThreads) beam_select_kernel(const BeamA
         const float score = a.scores[b * W + threadIdx.x];
         if (score != score) record_error(a.status, MOE_ERR_NONFINITE);
     }
+    __shared__ int s_again[kApart ? MOE_MAX_BEAMS : 1];
+    __shared__ float s_buf[kApart ? kSelectThreads / 32 : 1];
+    if (kApart && threadIdx.x < W) s_again[threadIdx.x] = 0;
     __syncthreads();
+    if constexpr (kApart) {
+        // beams that may be equal rows: the same best values, sums that differ, by no more than an order's roundings
+        bool any = false;
+        for (int i = threadIdx.x; i < W * W; i += kSelectThreads) {
+            const int w = i / W, o = i - w * W;
+            const float2 p = a.stats[b * W + w], q = a.stats[b * W + o];
+            bool same = p.x == q.x && p.y != q.y && fabsf(p.y - q.y) <= 0x1p-10f * (p.y + q.y) && a.scores[b * W + w] > -INFINITY &&
+                        a.scores[b * W + o] > -INFINITY;
+            for (int j = 0; same && j < n; ++j) same = a.top_x[(b * W + w) * n + j] == a.top_x[(b * W + o) * n + j];
+            if (same) s_again[w] = 1;
+            any = any || same;
+        }
+        if (__syncthreads_or(any)) {
+            for (int w = 0; w < W; ++w) {
+                if (!s_again[w]) continue;
+                const float maximum = a.stats[b * W + w].x;
+                const float l = a.bf16 ? sum_by_index<__nv_bfloat16>(a, b * W + w, maximum, s_buf) : sum_by_index<float>(a, b * W + w, maximum, s_buf);
+                if (threadIdx.x == 0) s_log[w] = log(static_cast<double>(l));
+            }
+            __syncthreads();
+        }
+    }
     int valid = 0;
     for (int i = threadIdx.x; i < count; i += kSelectThreads) {
         const int w = i / n;
@@ -259,7 +317,7 @@ cudaError_t launch_beam_select(const BeamArgs& a, cudaStream_t s)
     l.status = a.status;
     const cudaError_t e = launch_token_logprobs(l, s);
     if (e != cudaSuccess) return e;
-    return launch_after(beam_select_kernel, dim3(static_cast<unsigned>(a.seqs)), kSelectThreads, 0, s, a);
+    return launch_after(a.apart ? beam_select_kernel<true> : beam_select_kernel<false>, dim3(static_cast<unsigned>(a.seqs)), kSelectThreads, 0, s, a);
 }
 
 cudaError_t launch_beam_reorder(const BeamMoveArgs& a, cudaStream_t s)

@@ -344,6 +344,7 @@ moe_status_t moe_beam_select(int32_t seqs, int32_t beams, int32_t vocab, uint32_
     a.vocab = vocab;
     a.n = n;
     a.bf16 = type == MOE_LOGITS_BF16;
+    a.apart = beams > 1 && row_stride % (a.bf16 ? 8 : 4) != 0;
     a.logits = logits;
     a.row_stride = row_stride;
     a.scores = scores;

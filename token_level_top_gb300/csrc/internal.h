@@ -399,6 +399,7 @@ cudaError_t launch_token_logprobs_backward(const LogprobGradArgs& a, cudaStream_
 struct BeamArgs {
     int seqs, beams, vocab, n;
     bool bf16;
+    bool apart;              // a sequence's rows start at different places of 16 bytes
     const void* logits;
     long long row_stride;
     const float* scores;     // [seqs, beams]
