@@ -240,3 +240,22 @@ def test_on_a_side_stream_and_in_a_graph():
     replayed = [t.clone() for t in (dw, y, s, dx)]
     for a, b, c in zip(replayed, [t.clone() for t in (step(), y, s, dx)], want):
         assert torch.equal(a, b) and not torch.equal(a, c)
+
+
+@pytest.mark.parametrize("dtype,dy32", [(BF, False), (BF, True), (F32, True)])
+@pytest.mark.parametrize("cols", [100, 300, 520, 1000, 1001, 2000, 4096])
+def test_a_row_keeps_its_bits_beside_any_neighbour(cols, dtype, dy32):
+    """Rows of a block with rows whose squares overflow, or with NaN: every other row's outputs and gradient to the last bit."""
+    g = torch.Generator().manual_seed(cols)
+    x = torch.randn(23, cols, generator=g).to(dtype).cuda()
+    dy = torch.randn(23, cols, generator=g).to(F32 if dy32 else dtype).cuda()
+    w = (1 + 0.2 * torch.randn(cols, generator=g)).cuda()
+    odd = x.clone()
+    odd[5] *= 1e30
+    odd[10, 3], odd[21, 0] = float("nan"), float("inf")
+    keep = [r for r in range(23) if r not in (5, 10, 21)]
+    want, got = (moe.rms_norm(t, w, e4m3=True) for t in (x, odd))
+    for k in want:
+        assert torch.equal(want[k][keep], got[k][keep]), k
+    want, got = (moe.rms_norm_backward(None, t, w, dy, weight_grad=False)[0] for t in (x, odd))
+    assert torch.equal(want[keep], got[keep])

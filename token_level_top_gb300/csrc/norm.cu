@@ -143,10 +143,22 @@ __device__ __forceinline__ uint16_t two_codes(float lo, float hi)
     return two;
 }
 
+// A barrier of the W warps of a row (of one warp none), or of the block's rows together.  Rows of the gradient go their own
+// ways, so that none does anything for a neighbour's sake (67000 x 1000 bf16 138 us, together 147); those of the forward,
+// which have a block's start and end in common, go together (79.5 us, apart 82.6).
+template <int W, bool kApart>
+__device__ __forceinline__ void sync_row(int row_of)
+{
+    if (W >= 8 || (W > 1 && !kApart))
+        __syncthreads();
+    else if (W > 1)
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + row_of), "n"(32 * W) : "memory");
+}
+
 // Sums (or maxima) over the W warps of a row, in every lane: the same order on every lane and call.  `buf` holds W
-// values per row; a block's rows reduce together.
-template <int W, bool kMax>
-__device__ __forceinline__ float reduce(float v, float* buf, int warp_of_row, int lane)
+// values of the row's.
+template <int W, bool kMax, bool kApart>
+__device__ __forceinline__ float reduce(float v, float* buf, int row_of, int warp_of_row, int lane)
 {
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) {
@@ -155,7 +167,7 @@ __device__ __forceinline__ float reduce(float v, float* buf, int warp_of_row, in
     }
     if (W == 1) return v;
     if (lane == 0) buf[warp_of_row] = v;
-    __syncthreads();
+    sync_row<W, kApart>(row_of);
     v = buf[0];
 #pragma unroll
     for (int i = 1; i < W; ++i) v = kMax ? fmaxf(v, buf[i]) : v + buf[i];
@@ -168,9 +180,9 @@ struct Scale {
     bool finite;
 };
 
-// Every warp of a block with several rows takes part; a block's other rows go through it unchanged.  Leaves `buf` in use.
-template <int W, int P, int N, class R>
-__device__ __forceinline__ Scale scale_of(const R (&s)[P], float sum, float inv_cols, float eps, float* buf, int warp_of_row, int lane)
+// By the row's warps; where rows go together by all of the block, an ordinary row's result is what it was.  Leaves `buf` in use.
+template <int W, int P, int N, bool kApart, class R>
+__device__ __forceinline__ Scale scale_of(const R (&s)[P], float sum, float inv_cols, float eps, float* buf, int row_of, int warp_of_row, int lane)
 {
     Scale o;
     float amax = 0.0f;
@@ -183,7 +195,7 @@ __device__ __forceinline__ Scale scale_of(const R (&s)[P], float sum, float inv_
             amax = fmaxf(amax, fabsf(v));
             nan = nan || v != v;
         }
-    amax = reduce<W, true>(nan ? INFINITY : amax, buf, warp_of_row, lane);
+    amax = reduce<W, true, kApart>(nan ? INFINITY : amax, buf, row_of, warp_of_row, lane);
     o.finite = amax < INFINITY;
     o.f = !(sum < INFINITY) && o.finite ? 0x1p-96f : 1.0f;
     float again = 0.0f;
@@ -191,8 +203,8 @@ __device__ __forceinline__ Scale scale_of(const R (&s)[P], float sum, float inv_
     for (int p = 0; p < P; ++p)
 #pragma unroll
         for (int i = 0; i < N; ++i) again = fmaf(s[p].at(i) * o.f, s[p].at(i) * o.f, again);
-    if (W > 1) __syncthreads();   // the maxima are read
-    again = reduce<W, false>(again, buf, warp_of_row, lane);
+    sync_row<W, kApart>(row_of);   // the maxima are read
+    again = reduce<W, false, kApart>(again, buf, row_of, warp_of_row, lane);
     // (what is left of eps in the scaled sum is below 2^-100 of it)
     o.r = o.finite ? __frsqrt_rn(fmaf(again, inv_cols, o.f == 1.0f ? eps : 0.0f)) : NAN;
     return o;
@@ -243,12 +255,12 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256) rms_norm_kernel(const N
     for (int p = 0; p < P; ++p)
 #pragma unroll
         for (int i = 0; i < N; ++i) sum = fmaf(s[p].at(i), s[p].at(i), sum);
-    sum = reduce<W, false>(sum, s_buf[0] + row_of * W, in_row, lane);
+    sum = reduce<W, false, false>(sum, s_buf[0] + row_of * W, row_of, in_row, lane);
     Scale scale{1.0f, 0.0f, true};
     const bool odd = !(sum < INFINITY);
     // (a row to itself is agreed on by all its warps; of several in a block each has to take part)
     if (W == 1 ? __any_sync(0xffffffffu, odd) : (W >= 8 ? odd : __syncthreads_or(odd) != 0))
-        scale = scale_of<W, P, N>(s, sum, a.inv_cols, a.eps, s_buf[1] + row_of * W, in_row, lane);
+        scale = scale_of<W, P, N, false>(s, sum, a.inv_cols, a.eps, s_buf[1] + row_of * W, row_of, in_row, lane);
     else
         scale.r = __frsqrt_rn(fmaf(sum, a.inv_cols, a.eps));
     if (!live && W > 1 && !a.codes) return;
@@ -274,7 +286,7 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256) rms_norm_kernel(const N
         }
     }
     if (!a.codes) return;
-    amax = reduce<W, true>(amax, s_buf[2] + row_of * W, in_row, lane);
+    amax = reduce<W, true, false>(amax, s_buf[2] + row_of * W, row_of, in_row, lane);
     if (!live) return;
     // the scale of moe_quantize_fp8 (one rounding from fp32 to a code; the rounded y is not looked at again)
     const float sc = !scale.finite ? NAN : (amax > 0.0f ? amax / 448.0f : 1.0f);
@@ -392,7 +404,7 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256, (grad_blocks<T, kVec, W
             // (two buffers in turn: a row's sums are read while another warp may be at the next row's)
             float2* const buf = s_sums[turn] + row_of * W;
             if (lane == 0) buf[in_row] = sums;
-            __syncthreads();
+            sync_row<W, true>(row_of);
             sums = buf[0];
 #pragma unroll
             for (int i = 1; i < W; ++i) {
@@ -403,10 +415,9 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256, (grad_blocks<T, kVec, W
         }
         float f = 1.0f, r, dot = sums.y;
         const bool odd = !(sums.x < INFINITY) || !(fabsf(dot) < INFINITY);
-        // (a row to itself is agreed on by all its warps; of several in a block each has to take part)
-        if (W == 1 ? __any_sync(0xffffffffu, odd) : (W >= 8 ? odd : __syncthreads_or(odd) != 0)) {
+        if (W == 1 ? __any_sync(0xffffffffu, odd) : odd) {   // (a row's lanes have the same sums)
             float* const buf = s_buf + row_of * W;
-            const Scale scale = scale_of<W, P, N>(s, sums.x, a.inv_cols, a.eps, buf, in_row, lane);
+            const Scale scale = scale_of<W, P, N, true>(s, sums.x, a.inv_cols, a.eps, buf, row_of, in_row, lane);
             f = scale.f;
             r = scale.r;
             dot = 0.0f;
@@ -419,9 +430,9 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256, (grad_blocks<T, kVec, W
 #pragma unroll
                 for (int i = 0; i < N; ++i) dot = fmaf(g[p].at(i) * w[i], s[p].at(i) * f * r, dot);
             }
-            if (W > 1) __syncthreads();   // (what scale_of left has been read)
-            dot = reduce<W, false>(dot, buf, in_row, lane) * a.inv_cols;
-            if (W > 1) __syncthreads();
+            sync_row<W, true>(row_of);   // (what scale_of left has been read)
+            dot = reduce<W, false, true>(dot, buf, row_of, in_row, lane) * a.inv_cols;
+            sync_row<W, true>(row_of);
         } else {
             r = __frsqrt_rn(fmaf(sums.x, a.inv_cols, a.eps));
             dot *= r * a.inv_cols;
