@@ -519,7 +519,7 @@ int backward(const NormGradArgs& a, cudaStream_t s)
 // Warps and pieces for a row of this many units: as few warps as take it at two pieces a lane, past 8 warps at four and
 // more (single values: six to eight a lane, and sixteen).
 static_assert(kMaxNormCols <= 16384, "what the largest variants hold");
-template <class F>
+template <class T, class F>
 auto by_size(bool vec, int units, F&& f)
 {
     const auto go = [&](auto v, auto w, auto p) { return f(v, w, p); };
@@ -531,8 +531,10 @@ auto by_size(bool vec, int units, F&& f)
         if (units <= 256) return go(v, integral_constant<int, 4>{}, integral_constant<int, 2>{});
         if (units <= 512) return go(v, integral_constant<int, 8>{}, integral_constant<int, 2>{});
         if (units <= 1024) return go(v, integral_constant<int, 16>{}, integral_constant<int, 2>{});
-        if (units <= 2048) return go(v, integral_constant<int, 16>{}, integral_constant<int, 4>{});
-        return go(v, integral_constant<int, 32>{}, integral_constant<int, 4>{});
+        if constexpr (kMaxNormCols * sizeof(T) / 16 > 2048) {   // (bf16 rows have no more)
+            if (units > 2048) return go(v, integral_constant<int, 32>{}, integral_constant<int, 4>{});
+        }
+        return go(v, integral_constant<int, 16>{}, integral_constant<int, 4>{});
     }
     constexpr std::false_type v{};
     if (units <= 256) return go(v, integral_constant<int, 1>{}, integral_constant<int, 8>{});
@@ -563,12 +565,12 @@ cudaError_t launch_rms_norm(NormArgs a, cudaStream_t s)
     for (long long st : {a.x_stride, a.residual_stride, a.sum_stride, a.y_stride, a.codes_stride})
         vec = vec && (a.rows == 1 || st % n == 0);
     vec = vec && on(a.codes, n);
-    by_size(vec, vec ? a.cols / n : a.cols, [&](auto v, auto w, auto p) {
-        if (a.bf16)
-            forward<__nv_bfloat16, decltype(v)::value, decltype(w)::value, decltype(p)::value>(a, s);
-        else
-            forward<float, decltype(v)::value, decltype(w)::value, decltype(p)::value>(a, s);
-    });
+    const auto run = [&](auto type) {
+        using T = decltype(type);
+        by_size<T>(vec, vec ? a.cols / n : a.cols,
+                   [&](auto v, auto w, auto p) { forward<T, decltype(v)::value, decltype(w)::value, decltype(p)::value>(a, s); });
+    };
+    a.bf16 ? run(__nv_bfloat16{}) : run(0.0f);
     return cudaGetLastError();
 }
 
@@ -580,13 +582,14 @@ cudaError_t launch_rms_norm_backward(NormGradArgs a, cudaStream_t s)
     bool vec = a.cols % n == 0 && on(a.weight, 16);
     for (const void* p : {a.x, a.dy, a.dsum, static_cast<const void*>(a.dx)}) vec = vec && on(p, 16);
     for (long long st : {a.x_stride, a.dy_stride, a.dsum_stride, a.dx_stride}) vec = vec && (a.rows == 1 || st % n == 0);
-    const int grid = by_size(vec, vec ? a.cols / n : a.cols, [&](auto v, auto w, auto p) {
-        constexpr bool kVec = decltype(v)::value;
-        constexpr int W = decltype(w)::value, P = decltype(p)::value;
-        if (!a.bf16) return backward<float, float, kVec, W, P>(a, s);
-        if (a.dy_f32) return backward<__nv_bfloat16, float, kVec, W, P>(a, s);
-        return backward<__nv_bfloat16, __nv_bfloat16, kVec, W, P>(a, s);
-    });
+    const auto run = [&](auto type, auto dy_type) {
+        using T = decltype(type);
+        return by_size<T>(vec, vec ? a.cols / n : a.cols, [&](auto v, auto w, auto p) {
+            return backward<T, decltype(dy_type), decltype(v)::value, decltype(w)::value, decltype(p)::value>(a, s);
+        });
+    };
+    const __nv_bfloat16 b16{};
+    const int grid = !a.bf16 ? run(0.0f, 0.0f) : (a.dy_f32 ? run(b16, 0.0f) : run(b16, b16));
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.dweight) return e;
     return launch_after(rms_norm_weight_sum_kernel, dim3(static_cast<unsigned>((a.cols + 31) / 32)), 32 * kSumWarps, 0, s, a.parts, grid,
