@@ -259,3 +259,21 @@ def test_a_row_keeps_its_bits_beside_any_neighbour(cols, dtype, dy32):
         assert torch.equal(want[k][keep], got[k][keep]), k
     want, got = (moe.rms_norm_backward(None, t, w, dy, weight_grad=False)[0] for t in (x, odd))
     assert torch.equal(want[keep], got[keep])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cols,size,eps", [(16384, 2e18, 1e38), (1000, 1e19, 3e38), (16, 3e38, 3e38), (1, 1.8e19, 3.3e38), (4096, 1.0, 3e38)])
+def test_eps_of_any_size(cols, size, eps, dtype):
+    """An eps that counts beside squares whose sum overflows."""
+    g = torch.Generator().manual_seed(cols)
+    x = (size * (0.25 + 0.75 * torch.rand(5, cols, generator=g))).to(dtype).cuda()
+    y = cref.norm(ref.f64(x), None, eps)
+    got = moe.rms_norm(x, eps=eps)["y"]
+    assert (np.abs(ref.f64(got) - y) <= (cref.NORM + cref.HALF_STEP[dtype]) * np.abs(y) + 1e-38).all()
+    dy = torch.randn(5, cols, generator=g).to(dtype).cuda()
+    dsum = torch.zeros(5, cols, dtype=dtype, device="cuda")
+    dx, dw = moe.rms_norm_backward(moe.norm_workspace(cols), x, None, dy, dsum=dsum, eps=eps)
+    want, want_w, e, e_w = cref.norm_grad(ref.f64(x), None, ref.f64(dy), None, eps)
+    # (dx is below the smallest normal number of fp32, or near it: to a step of the subnormal ones of either type)
+    assert (np.abs(ref.f64(dx) - want) <= e + cref.HALF_STEP[dtype] * (np.abs(want) + e) + (2.0 ** -134 if dtype is BF else 2.0 ** -148)).all()
+    assert (np.abs(ref.f64(dw) - want_w) <= e_w).all()

@@ -182,7 +182,7 @@ struct Scale {
 
 // By the row's warps; where rows go together by all of the block, an ordinary row's result is what it was.  Leaves `buf` in use.
 template <int W, int P, int N, bool kApart, class R>
-__device__ __forceinline__ Scale scale_of(const R (&s)[P], float sum, float inv_cols, float eps, float* buf, int row_of, int warp_of_row, int lane)
+__device__ __forceinline__ Scale scale_of(const R (&s)[P], float mean, float inv_cols, float eps, float* buf, int row_of, int warp_of_row, int lane)
 {
     Scale o;
     float amax = 0.0f;
@@ -197,7 +197,7 @@ __device__ __forceinline__ Scale scale_of(const R (&s)[P], float sum, float inv_
         }
     amax = reduce<W, true, kApart>(nan ? INFINITY : amax, buf, row_of, warp_of_row, lane);
     o.finite = amax < INFINITY;
-    o.f = !(sum < INFINITY) && o.finite ? 0x1p-96f : 1.0f;
+    o.f = !(mean < INFINITY) && o.finite ? 0x1p-96f : 1.0f;
     float again = 0.0f;
 #pragma unroll
     for (int p = 0; p < P; ++p)
@@ -205,8 +205,8 @@ __device__ __forceinline__ Scale scale_of(const R (&s)[P], float sum, float inv_
         for (int i = 0; i < N; ++i) again = fmaf(s[p].at(i) * o.f, s[p].at(i) * o.f, again);
     sync_row<W, kApart>(row_of);   // the maxima are read
     again = reduce<W, false, kApart>(again, buf, row_of, warp_of_row, lane);
-    // (what is left of eps in the scaled sum is below 2^-100 of it)
-    o.r = o.finite ? __frsqrt_rn(fmaf(again, inv_cols, o.f == 1.0f ? eps : 0.0f)) : NAN;
+    // (of eps, as of the squares, what f^2 leaves: as a rule nothing)
+    o.r = o.finite ? __frsqrt_rn(fmaf(again, inv_cols, eps * o.f * o.f)) : NAN;
     return o;
 }
 
@@ -257,12 +257,13 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256) rms_norm_kernel(const N
         for (int i = 0; i < N; ++i) sum = fmaf(s[p].at(i), s[p].at(i), sum);
     sum = reduce<W, false, false>(sum, s_buf[0] + row_of * W, row_of, in_row, lane);
     Scale scale{1.0f, 0.0f, true};
-    const bool odd = !(sum < INFINITY);
+    const float mean = fmaf(sum, a.inv_cols, a.eps);
+    const bool odd = !(mean < INFINITY);
     // (a row to itself is agreed on by all its warps; of several in a block each has to take part)
     if (W == 1 ? __any_sync(0xffffffffu, odd) : (W >= 8 ? odd : __syncthreads_or(odd) != 0))
-        scale = scale_of<W, P, N, false>(s, sum, a.inv_cols, a.eps, s_buf[1] + row_of * W, row_of, in_row, lane);
+        scale = scale_of<W, P, N, false>(s, mean, a.inv_cols, a.eps, s_buf[1] + row_of * W, row_of, in_row, lane);
     else
-        scale.r = __frsqrt_rn(fmaf(sum, a.inv_cols, a.eps));
+        scale.r = __frsqrt_rn(mean);
     if (!live && W > 1 && !a.codes) return;
     if (live && !scale.finite && first == 0) record_error(a.status, MOE_ERR_NONFINITE);
 
@@ -414,10 +415,11 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256, (grad_blocks<T, kVec, W
             turn ^= 1;
         }
         float f = 1.0f, r, dot = sums.y;
-        const bool odd = !(sums.x < INFINITY) || !(fabsf(dot) < INFINITY);
+        const float mean = fmaf(sums.x, a.inv_cols, a.eps);
+        const bool odd = !(mean < INFINITY) || !(fabsf(dot) < INFINITY);
         if (W == 1 ? __any_sync(0xffffffffu, odd) : odd) {   // (a row's lanes have the same sums)
             float* const buf = s_buf + row_of * W;
-            const Scale scale = scale_of<W, P, N, true>(s, sums.x, a.inv_cols, a.eps, buf, row_of, in_row, lane);
+            const Scale scale = scale_of<W, P, N, true>(s, mean, a.inv_cols, a.eps, buf, row_of, in_row, lane);
             f = scale.f;
             r = scale.r;
             dot = 0.0f;
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256, (grad_blocks<T, kVec, W
             dot = reduce<W, false, true>(dot, buf, row_of, in_row, lane) * a.inv_cols;
             sync_row<W, true>(row_of);
         } else {
-            r = __frsqrt_rn(fmaf(sums.x, a.inv_cols, a.eps));
+            r = __frsqrt_rn(mean);
             dot *= r * a.inv_cols;
         }
         T* const dx = static_cast<T*>(a.dx) + (live ? row * a.dx_stride : 0);
