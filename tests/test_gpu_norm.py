@@ -277,3 +277,18 @@ def test_eps_of_any_size(cols, size, eps, dtype):
     # (dx is below the smallest normal number of fp32, or near it: to a step of the subnormal ones of either type)
     assert (np.abs(ref.f64(dx) - want) <= e + cref.HALF_STEP[dtype] * (np.abs(want) + e) + (2.0 ** -134 if dtype is BF else 2.0 ** -148)).all()
     assert (np.abs(ref.f64(dw) - want_w) <= e_w).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cols", [260, 500, 520, 1000, 1001, 2000, 257])
+def test_ends_of_the_range_where_rows_share_a_block(dtype, cols):
+    """Two and four warps a row, vector rows and odd ones: the nine rows fill blocks of two or four and one in part."""
+    test_values_at_the_ends_of_the_range(dtype, cols)
+
+
+@pytest.mark.parametrize("rows,cols,dtype,dy32", [
+    (9001, 520, BF, True), (8003, 1000, BF, False), (7001, 1000, BF, True), (4001, 2048, BF, True), (3501, 1600, BF, False), (12001, 256, BF, True),
+    (9001, 260, F32, True), (8001, 512, F32, True), (5003, 1000, F32, True), (2003, 4096, F32, True), (1201, 8192, BF, True), (901, 5120, BF, False)])
+def test_gradient_of_many_aligned_rows(rows, cols, dtype, dy32):
+    """Several passes of the grid over vector rows: the sums' buffers in turn, and dw carried from row to row."""
+    test_gradient_of_many_odd_rows(rows, cols, dtype, dy32)
