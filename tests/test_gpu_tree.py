@@ -423,3 +423,20 @@ def test_the_workspace_held_another_batch(ctx, drafted):
     ws[256: 256 + 304 * 24].view(torch.int32).view(304, 6).copy_(torch.tensor([0, 0, 0, 128, 0, 0], dtype=torch.int32))
     out, lse = c.run(ws, return_lse=True)
     assert moe.device_status(ws) == 0 and torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+@pytest.mark.parametrize("ctx", [[40, 20], [3000, 500]])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_value_rows_of_the_lowest_exponents(D, ctx):
+    """Exponent bytes from 1 to 6: outputs below 2^-110, in whole items and in parts, of rows once and twice in a tile."""
+    c = Case(ctx, [9, 40], 4, 1, D, 16, True, True, "tree")
+    exps = c.cache.v_exp
+    exps.copy_((exps.int() - 118).clamp(1, 6))
+    for b, n in enumerate(c.lens):
+        j = torch.arange(n, device="cuda")
+        at = c.table[b].long()[j // 16], j % 16
+        c.dense[1][b] = ref.e4m3_value(c.cache.v[at], exps[at])
+    ws = moe.tree_attention_workspace(D)
+    out, lse = c.run(ws, return_lse=True)
+    assert moe.device_status(ws) == 0 and float((out == 0).float().mean()) < 0.1
+    c.check(out, lse, rows=range(0, c.T, 3))

@@ -111,6 +111,12 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+// 2^x of an exponent that may lie below a normal float's (value rows whose own is near the lowest) is within(x)'s power of two
+// times rest_of(x).
+constexpr float kLeast = -80.0f;
+__device__ __forceinline__ float within(float x) { return x < kLeast ? x + 60.0f : fminf(x, 126.0f); }
+__device__ __forceinline__ float rest_of(float x) { return x < kLeast ? 0x1p-60f : 1.0f; }
+
 // Two floats of a packed instruction, each rounded as a single one's.
 struct Pair {
     float x, y;
@@ -1421,7 +1427,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 }
                 // (what O is held against, as a power of two over the sum's)
                 const float over = kE4m3 ? m_out - kShift - m : 0.0f;
-                const float inv = l > 0.0f ? (kE4m3 ? exp2_fast(fminf(over, 126.0f)) : 1.0f) / l : (l == 0.0f ? 0.0f : NAN);
+                const float inv = l > 0.0f ? (kE4m3 ? exp2_fast(within(over)) : 1.0f) / l : (l == 0.0f ? 0.0f : NAN);
                 __nv_bfloat16* const out = a.out + static_cast<long long>(it.row0 + t_row) * a.out_token_stride + static_cast<long long>(head) * a.out_head_stride;
 #pragma unroll 1
                 for (int d = 0; d < D; d += 16) {
@@ -1438,6 +1444,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                                 o[j] = __float_as_uint(fmaf(__uint_as_float(o[j]), f_mine, __uint_as_float(other[j]) * f_other));
                         }
                         if (half == 1) continue;
+                    }
+                    if (kE4m3 && whole && uniform(over < kLeast)) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * rest_of(over));
                     }
                     if (live && whole) {   // (the upper half of rows that are there twice is through)
 #pragma unroll
@@ -1528,11 +1538,11 @@ __global__ void __launch_bounds__(256) tree_attention_join_kernel(const TreeArgs
         o.w = fmaf(x.w, f, o.w);
     }
     if (row >= h.rows) return;
-    const float inv = l > 0.0f ? exp2_fast(fminf(m_out - m, 126.0f)) / l : (l == 0.0f ? 0.0f : NAN);
+    const float inv = l > 0.0f ? exp2_fast(within(m_out - m)) / l : (l == 0.0f ? 0.0f : NAN), rest = rest_of(m_out - m);
     const int group = a.n_heads / a.n_kv_heads, t = (h.first_row + row) / group, head = h.hk * group + (h.first_row + row) - t * group;
     const long long token = a.row_start[h.b] + t;
     *reinterpret_cast<uint2*>(a.out + token * a.out_token_stride + head * a.out_head_stride + 4 * col4) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        make_uint2(pack_bf16x2(o.x * rest * inv, o.y * rest * inv), pack_bf16x2(o.z * rest * inv, o.w * rest * inv));
     if (a.lse && col4 == 0) a.lse[token * a.n_heads + head] = l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l));
 }
 
