@@ -590,6 +590,7 @@ moe_status_t moe_paged_attention_workspace_init(void* ws_dev, size_t ws_bytes, v
  *   seq_len), out = sum_j softmax(s)_j v_j, lse = ln sum_j e^(s_j)
  * with fp32 scores, statistics and sums.  A row with no live position, or no score above
  * -inf, gets zeros and lse = -inf.  What the cache holds in other places (NaN included) has no effect.
+ * An infinity among the live values makes that output an infinity or NaN (weights go in as two parts).
  * MOE_KV_E4M3: a key whose weight times 2^(exponent of its value row) is below 2^-30 of the
  * head's largest such product loses bits of its share of out, down to none (not of lse); a
  * value row of zeros with exponent byte 127, as moe_kv_append stores it, is no such product.
@@ -634,7 +635,8 @@ moe_status_t moe_tree_attention_workspace_init(void* ws_dev, size_t ws_bytes, vo
  * last `window` of its path: the drafted tokens it sees, the highest numbers first, then
  * the context from its end.  A row that sees nothing, or no score above -inf, gets zeros
  * and lse = -inf.  What a row does not see (NaN and infinities included) has no effect on
- * it.  Row_start and lengths are read on the device: a captured graph replays at others.
+ * it.  An infinity among the values that it sees is its output in that column, whatever the weight; with the
+ * other infinity, or NaN, beside it the output is NaN.  Row_start and lengths are read on the device: a captured graph replays at others.
  * Rows of q before row_start[0] and from row_start[B] on are not read, theirs of out and lse not written.
  * A row_start that falls, ends past T or gives a sequence more than MOE_MAX_DRAFTED rows
  * (the sequence then has no rows), a length that moe_paged_attention would correct, or one

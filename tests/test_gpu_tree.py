@@ -440,3 +440,48 @@ def test_value_rows_of_the_lowest_exponents(D, ctx):
     out, lse = c.run(ws, return_lse=True)
     assert moe.device_status(ws) == 0 and float((out == 0).float().mean()) < 0.1
     c.check(out, lse, rows=range(0, c.T, 3))
+
+
+@pytest.mark.parametrize("window", [0, 150])
+@pytest.mark.parametrize("D,ctx,drafted,heads,kv", [
+    (64, [200, 90], [20, 13], 4, 2), (128, [200, 90], [20, 13], 4, 2), (256, [300], [40], 8, 2), (64, [5000], [50], 8, 2), (128, [5000, 64], [16, 3], 8, 2),
+    (64, [130], [1], 1, 1), (128, [63], [2], 2, 1)])
+def test_infinite_values(D, ctx, drafted, heads, kv, window):
+    """An infinity among the values that a row sees is its output, whatever its weight and wherever it lies; with the other
+    one, or NaN, the output is NaN.  All else keeps its bits."""
+    c = Case(ctx, drafted, heads, kv, D, 16, False, True, "tree")
+    inf, nan = float("inf"), float("nan")
+
+    def at(key):
+        return int(c.table[0, key // 16]), key % 16, 0
+
+    n = ctx[0]
+    c.cache.k[at(n - 20)] *= 300.0     # a key that takes all the weight of a row, or has none
+    base, blse = c.run(window=window, return_lse=True)
+    odd = [(n // 2, 3, inf), (n - 40, 7, -inf), (n // 3, 11, inf), (n - 10, 11, -inf), (n, 13, inf), (n // 4, 17, inf), (n, 17, inf),
+           (n - 33, 19, nan), (n - 34, 19, inf), (n - 20, 23, inf), (n - 21, 29, -inf), (1, 31, inf), (n - 5, 31, inf)]
+    for key, col, v in odd:
+        c.cache.v[at(key) + (col,)] = v
+    ws = moe.tree_attention_workspace(D)
+    out, lse = c.run(ws, window=window, return_lse=True)
+    assert moe.device_status(ws) == 0 and torch.equal(lse, blse)
+    want = base.clone()
+    for t in range(drafted[0]):
+        keys = set(cref.seen_by(c.masks[t], drafted[0], n, window, t))
+        for col in {o[1] for o in odd}:
+            seen = [v for key, j, v in odd if j == col and key in keys]
+            if seen:
+                want[t, : heads // kv, col] = sum(seen)
+    assert torch.equal(torch.isnan(out), torch.isnan(want)) and torch.equal(out.nan_to_num(0.5, inf, -inf), want.nan_to_num(0.5, inf, -inf))
+
+
+def test_no_score_above_minus_infinity():
+    """Zeros and -inf, whatever the values are: of keys with an infinity, in whole items and in parts."""
+    for n in (150, 4000):
+        c = Case([n], [5], 2, 1, 64, 16, False, True, "tree")
+        c.q[..., 4] = 1.0
+        c.cache.k[..., 4] = -float("inf")
+        c.cache.v[..., 9] = float("inf")
+        c.cache.v[..., 11] = float("nan")
+        out, lse = c.run(return_lse=True)
+        assert (out == 0).all() and (lse == -float("inf")).all()

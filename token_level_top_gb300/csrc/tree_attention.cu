@@ -46,7 +46,8 @@
 // What a row does not see: keys that no row sees are masked (their value rows are
 // written as zeros); in tiles where rows differ the value rows lose their NaN and
 // infinities in shared memory, since 0 times them would reach every row, and the rows
-// that do see them get them added at the end.
+// that do see them get them added at the end.  In other tiles all rows see all keys, and
+// outputs that came out as NaN or an infinity are settled at the end (settle_odd).
 #include <algorithm>
 #include <type_traits>
 
@@ -546,6 +547,43 @@ __device__ __noinline__ void add_odd(const TreeArgs& a, const int32_t* table, __
             else
                 part[(d >> 2) * (4 * kRowsTile) + (d & 3)] += x;
         }
+    }
+}
+
+// bf16: where a product with the values came out as NaN or an infinity, that of a row is what it sees: the sum of the column's
+// values that are either (hi and lo parts of a weight times an infinity make NaN as a rule, a weight too small for a float
+// does, and the halves' zeros do).  For a whole warp, a row a lane (`mine`: one with such an output); none: a row with no
+// score above -infinity, whose outputs are zeros.
+template <int D>
+__device__ __noinline__ void settle_odd(const TreeArgs& a, const int32_t* table, __nv_bfloat16* out, float* part, int key_lo, int key_hi, int ctx,
+                                        int from, int hk, uint64_t seen, bool mine, bool none)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int d = 0; d < D; ++d) {
+        float* const at = part + (d >> 2) * (4 * kRowsTile) + (d & 3);
+        const float now = !mine ? 0.0f : (out ? __bfloat162float(out[d]) : *at);
+        const bool odd = !(fabsf(now) < INFINITY);
+        if (!__any_sync(0xffffffffu, odd)) continue;
+        float x = 0.0f;
+#pragma unroll 1
+        for (int k0 = key_lo; k0 < key_hi && !__all_sync(0xffffffffu, !odd || x != x); k0 += 32) {
+            const int key = k0 + lane, pg = key / a.page_size, e = key < key_hi ? __ldg(table + pg) : -1;
+            uint32_t h = 0;
+            if (e >= 0 && e < a.n_pages)
+                h = __ldg(reinterpret_cast<const uint16_t*>(a.v + e * a.page_bytes + (key - pg * a.page_size) * a.token_bytes + hk * a.head_bytes) + d);
+            for (uint32_t hits = __ballot_sync(0xffffffffu, (h & 0x7f80u) == 0x7f80u); hits; hits &= hits - 1) {
+                const int j = __ffs(hits) - 1;
+                const float v = __uint_as_float(__shfl_sync(0xffffffffu, h, j) << 16);
+                if (seen_of(k0 + j, from, ctx, seen) & 1) x += v;
+            }
+        }
+        if (!odd || (x == 0.0f && !none)) continue;
+        if (none) x = 0.0f;
+        if (out)
+            out[d] = __float2bfloat16(x);
+        else
+            *at = x;
     }
 }
 
@@ -1428,6 +1466,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                 // (what O is held against, as a power of two over the sum's)
                 const float over = kE4m3 ? m_out - kShift - m : 0.0f;
                 const float inv = l > 0.0f ? (kE4m3 ? exp2_fast(within(over)) : 1.0f) / l : (l == 0.0f ? 0.0f : NAN);
+                float odd_out = 0.0f;   // bf16: NaN once an output's product was NaN or an infinity
                 __nv_bfloat16* const out = a.out + static_cast<long long>(it.row0 + t_row) * a.out_token_stride + static_cast<long long>(head) * a.out_head_stride;
 #pragma unroll 1
                 for (int d = 0; d < D; d += 16) {
@@ -1444,6 +1483,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                                 o[j] = __float_as_uint(fmaf(__uint_as_float(o[j]), f_mine, __uint_as_float(other[j]) * f_other));
                         }
                         if (half == 1) continue;
+                    }
+                    if (!kE4m3) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) odd_out = fmaf(__uint_as_float(o[j]), 0.0f, odd_out);
                     }
                     if (kE4m3 && whole && uniform(over < kLeast)) {
 #pragma unroll
@@ -1465,8 +1508,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, kE4m3>::kCtas))
                     }
                     __syncwarp();   // TMEM is read by whole warps
                 }
-                if (*s_odd != 0 && live && half == 0)
+                if (*s_odd != 0 && live && half == 0 && !(whole && l == 0.0f))
                     add_odd<D, kE4m3>(a, table, whole ? out : nullptr, part + row * 4, key_lo, key_hi, odd_from, it.ctx, from, hk, seen);
+                if constexpr (!kE4m3) {
+                    const bool mine = odd_out != 0.0f && live && half == 0;
+                    if (uniform(mine && l == l))
+                        settle_odd<D>(a, table, whole ? out : nullptr, part + row * 4, key_lo, key_hi, it.ctx, from, hk, seen, mine && l == l, whole && l == 0.0f);
+                }
                 if (live && half == 0 && whole && a.lse)
                     a.lse[static_cast<long long>(it.row0 + t_row) * a.n_heads + head] = l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l));
                 if (live && half == 0 && !whole) reinterpret_cast<float4*>(part + kRowsTile * D)[row] = make_float4(m, l, kE4m3 ? m_out - kShift : m, 0.0f);
@@ -1530,7 +1578,9 @@ __global__ void __launch_bounds__(256) tree_attention_join_kernel(const TreeArgs
     for (int i = 0; i < parts; ++i) {
         const float4 q = reinterpret_cast<const float4*>(part(i) + kRowsTile * D)[row];
         const float4 x = reinterpret_cast<const float4*>(part(i))[col4 * kRowsTile + row];
-        const float f = exp2_fast(q.z - m_out);
+        // (never 0: an infinity that the row sees is one whatever its part's weight.  What that adds of a finite O is less than
+        // the exponential's own flush takes away.)
+        const float f = fmaxf(exp2_fast(q.z - m_out), 0x1p-149f);
         l = fmaf(q.y, exp2_fast(q.x - m), l);
         o.x = fmaf(x.x, f, o.x);
         o.y = fmaf(x.y, f, o.y);
@@ -1539,6 +1589,7 @@ __global__ void __launch_bounds__(256) tree_attention_join_kernel(const TreeArgs
     }
     if (row >= h.rows) return;
     const float inv = l > 0.0f ? exp2_fast(within(m_out - m)) / l : (l == 0.0f ? 0.0f : NAN), rest = rest_of(m_out - m);
+    if (l == 0.0f) o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // no score above -infinity, whatever the values
     const int group = a.n_heads / a.n_kv_heads, t = (h.first_row + row) / group, head = h.hk * group + (h.first_row + row) - t * group;
     const long long token = a.row_start[h.b] + t;
     *reinterpret_cast<uint2*>(a.out + token * a.out_token_stride + head * a.out_head_stride + 4 * col4) =
