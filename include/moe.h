@@ -696,13 +696,15 @@ moe_status_t moe_beam_workspace_init(void* ws_dev, size_t ws_bytes, void* stream
  * the n largest of each sequence, in order: out_scores [seqs, n], parents [seqs, n] (w) and tokens [seqs, n] (v).
  * Each total is formed in fp64 of an fp32 sum of exponentials and rounded once: candidates of different
  * rows that lie closer than that sum's error (at most 2^-17, and 2^-24 more for every 64 of the
- * vocabulary; as a rule below 1e-6) may change places.  Ties, those between equal rows with equal scores among them, go to the lower beam, then
- * to the larger logit, then to the lower token.  logits as in moe_token_logprobs.
+ * vocabulary; as a rule below 1e-6) may change places.  Ties, those between equal rows with equal
+ * scores among them, go to the lower beam, then to the larger logit, then to the lower token.
+ * logits as in moe_token_logprobs.
  * scores_dev [seqs, beams] fp32: -inf for a beam that is not alive; a masked logit is
  * -inf too, so a finished beam is a row of -inf but for one token.  Totals of -inf are
  * no candidates; places past the last one hold -inf, -1, -1.  A row with NaN or +inf, or a NaN
  * score, gives none and records MOE_ERR_NONFINITE.  1 <= n <= MOE_MAX_TOP, beams <=
- * MOE_MAX_BEAMS.  status: the workspace's. */
+ * MOE_MAX_BEAMS: as many continuations as beams up to 32 of them, two a beam up to 16; of 33 to
+ * 64 beams a selection goes on with 32 at most.  status: the workspace's. */
 moe_status_t moe_beam_select(int32_t seqs, int32_t beams, int32_t vocab, uint32_t type, const void* logits_dev,
                              int64_t row_stride, const float* scores_dev, int32_t n, float* out_scores_dev,
                              int32_t* parents_dev, int32_t* tokens_dev, void* ws_dev, size_t ws_bytes, void* stream);
@@ -759,7 +761,8 @@ typedef struct {
 
 /* s = x + residual, rounded to the rows' type; y = s * (mean of s^2 + eps)^(-1/2) * weight in
  * fp32, rounded once to y and, as moe_quantize_fp8 does, to codes = e4m3(y / scale), scale =
- * max|y| / 448 (1 for a row of zeros).  Any finite s has a norm (squares that overflow are
+ * max|y| / 448 (1 for a row of zeros).  The codes are for products of the caller's own: this library's e4m3
+ * experts take bf16 rows (y) and quantise the rows of their slots themselves.  Any finite s has a norm (squares that overflow are
  * scaled).  A row with a NaN or an infinity is NaN, its scale too, and records MOE_ERR_NONFINITE. */
 moe_status_t moe_rms_norm(const moe_rms_norm_t* a, int32_t* status_dev, void* stream);
 

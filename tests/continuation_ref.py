@@ -32,7 +32,7 @@ def norm_grad(s, weight, dy, dsum, eps):
     e_dot = (2 * NORM + (32 + 5 + 32) * U32) * np.abs(g * u).mean(-1, keepdims=True)
     e_dx = r * ((NORM + 4 * U32) * (np.abs(g) + 2 * np.abs(u * dot)) + np.abs(u) * e_dot) + 2 * U32 * np.abs(add)
     size = np.abs(dy * u).sum(0)
-    # a block adds its rows in a row, the blocks' sums are added by 16 warps: never more roundings than rows and 64
+    # a block adds its rows in a row, the blocks' sums are added by 32 warps: never more roundings than rows and 64
     return dx, (dy * u).sum(0), e_dx + 1e-38, (NORM + U32 * (rows + 64)) * size + 1e-38
 
 

@@ -14,9 +14,12 @@
 // r is computed again from s in the gradient: s is read anyway.
 //
 // Measured on rows in memory (the copy rate is 6.7 TB/s): 16384 x 4096 bf16 with a
-// residual 79 us, at the copy rate; its gradient with fp32 dy 114 us, 0.88 of it, the
-// weights' sum being 6 us of that.  64 rows: 4 us, a launch and one chain of loads.  Rows
-// of 1407 fp32 are taken value by value: the gradient of 5001 23 us, 0.54.
+// residual 79 us, at the copy rate; its gradient with fp32 dy 113 us, 0.89 of it, the
+// weights' sum being 5 us of that.  64 rows: 4 us, a launch and one chain of loads.  Rows
+// of 1407 fp32 are taken value by value: the gradient of 5001 21.6 us, 0.58.  The gradient of
+// 67 million bf16 values (fp32 dy, dsum) in rows of 512 / 1000 / 2048 / 5120 / 8192 / 16384:
+// 0.86 / 0.74 / 0.79 / 0.56 / 0.71 / 0.80 of the copy rate; of 33 million fp32 ones in rows of
+// 512 to 4096 0.9, of 8192 0.83.
 //
 // Squares are summed in fp32.  A row whose sum is not finite is looked at again,
 // scaled by a power of two: values up to the type's largest have a norm.
@@ -30,7 +33,7 @@
 namespace moe {
 namespace {
 
-// (Blocks an SM, 5001 x 1407 fp32: 4 / 5 / 6 25.4 / 23.4 / 27.6 us; three fit of the rows of 4096 bf16, 114 us, 126 with two.)
+// (Blocks an SM, 5001 x 1407 fp32 with dsum: 4 / 5 / 6 27.6 / 25.2 / 29.2 us; three fit of the rows of 4096 bf16, 113 us, 126 with two.)
 constexpr int kGradBlocksPerSm = 5, kGradBlocks = kGradBlocksPerSm * 152;   // most blocks of the gradient, each with a row of the workspace
 
 // A piece as it lies in memory: N values (16 bytes of the rows' type) or one, unpacked where they are used.
@@ -316,8 +319,9 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256) rms_norm_kernel(const N
 
 // ---------------------------------------------------------------- gradient
 
-// Blocks an SM that the gradient's registers are held to.
-// (80 registers for pieces of eight bf16 values, of which a lane sums as many weights' gradients, 64 for four of fp32).
+// Blocks an SM that the gradient's registers are held to: 80 for pieces of eight bf16 values, of which a lane sums as many
+// weights' gradients, 64 for four of fp32.  Measured for rows of 4096 bf16 and of 1407 fp32; elsewhere what follows from the
+// same registers, at the cost of spills (rows of 8 to 2048 bf16, 56 to 152 bytes) or, from 4104 bf16 values on, of one block alone.
 template <class T, bool kVec, int W, int P>
 constexpr int grad_blocks()
 {
@@ -345,8 +349,8 @@ __global__ void __launch_bounds__(W >= 8 ? 32 * W : 256, (grad_blocks<T, kVec, W
 #pragma unroll
         for (int i = 0; i < N; ++i) dw[p][i] = 0.0f;
     int turn = 0;
-    // Rows of single bf16 values ask for the next row before they work on this one: 9000 x 1500 52 us, 68 without, 5001 x 1407
-    // of fp32, whose blocks hide more of each other's waits, 29 us and 23.
+    // Rows of single bf16 values ask for the next row before they work on this one: 9000 x 1500 with dsum 52 us, 95 without (3000 x
+    // 3001 41 and 36); 5001 x 1407 of fp32, whose blocks hide more of each other's waits, 37.6 us and 25.2.
     constexpr bool kAhead = !kVec && sizeof(T) == 2;
     Raw<T, kVec, N> next_s[P], next_d[P];
     Raw<D, kVec, N> next_g[P];

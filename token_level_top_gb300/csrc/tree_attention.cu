@@ -34,8 +34,10 @@
 // roles' loops together are more than the first level of the cache holds, so loops
 // are rolled and rare ways are out of line).  Items of at most 64 rows therefore have
 // their rows twice in the tile of 128, each copy with half of the tile's keys, joined
-// at the end: 4 x 65536 e4m3 226 -> 190 us, D = 64 bf16 127 -> 115 us; 128 sequences of up
-// to 4096, 64 heads on 8, e4m3: 242 us, 0.35 of the copy rate.
+// at the end: 4 x 65536 with 16 drafted, 32 heads on 8, e4m3 226 -> 190 us, of 64 bf16 values
+// a head 128 -> 116 us (0.69 of the copy rate); 128 sequences of up to 4096, 64 heads on 8,
+// e4m3: 242 us, 0.35 of the copy rate.  Of more rows the chain is paid for each tile: 61
+// drafted, 64 heads on 8, 4 x 65536: 539 us, 0.39 of its floor, of 64 values a head 390, 0.27.
 //
 // Work is dealt out as in attention.cu: all (sequence, key head, row tile) items in
 // order, each its number of key tiles and a gap long, cut into equal runs for the

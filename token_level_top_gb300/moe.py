@@ -903,7 +903,7 @@ def beam_workspace(rows: int, n: int, device="cuda") -> torch.Tensor:
 
 
 def beam_select(ws, logits, scores, n: int):
-    """The n best continuations of each sequence over its beams and the vocabulary (moe_beam_select): logits
+    """The n best (32 at most) continuations of each sequence over its beams and the vocabulary (moe_beam_select): logits
     [seqs * beams, vocab] fp32 or bf16, scores [seqs, beams] fp32 (-inf: no live beam).  Returns dict(scores, parents,
     tokens), each [seqs, n], in order; past the last candidate -inf, -1, -1."""
     kind = LOGITS.get(logits.dtype)
@@ -990,7 +990,8 @@ def _norm_weight(weight, cols, dev):
 def rms_norm(x, weight=None, residual=None, eps=1e-6, y=True, e4m3=False, out=None, sum_out=None, status=None):
     """The root-mean-square norm of rows x (+ residual) [rows, cols] fp32 or bf16 (moe_rms_norm), times weight [cols] fp32 or
     bf16.  Returns a dict: sum (with a residual: x + residual in the rows' type), y (unless y is False) of the rows' type,
-    and with e4m3 codes (uint8) and scales [rows] fp32 as quantize_fp8 has them.  out, sum_out: where y and sum go; either may
+    and with e4m3 codes (uint8) and scales [rows] fp32 as quantize_fp8 has them (for products of the caller's own: the e4m3
+    experts take y).  out, sum_out: where y and sum go; either may
     be x or residual.  status: a status_word or workspace that records NaN and infinities."""
     dtype = x.dtype
     kind = LOGITS.get(dtype)
