@@ -50,7 +50,8 @@ __device__ __forceinline__ long long ordered(double x)
 constexpr long long kNoTotal = -0x7ff0000000000001LL;   // of -inf
 
 // A row's sum of e^(x - maximum), by threads that take every kSelectThreads-th value: the same bits for equal rows, wherever
-// they start.  For all threads of the block.  (Rare: loads of single values, 16 in flight a thread.)
+// they start.  For all threads of the block.  (Rare, so loads of single values, 16 in flight a thread: 64 x 8 rows of 131071
+// fp32, all of a sequence's equal, 386 us, all different 60, of 50257 bf16 84 and 23.)
 template <class T>
 __device__ __noinline__ float sum_by_index(const BeamArgs& a, long long row, float maximum, float* buf)
 {
